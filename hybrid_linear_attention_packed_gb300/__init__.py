@@ -10,11 +10,17 @@ from .spanla import (  # noqa: F401
     SpanLAError,
     ViewStateCache,
     load_library,
+    packed_positions,
+    rope_inv_freq,
     span_la_branches_from_state,
     span_la_check,
+    span_la_decay_branches_from_state,
+    span_la_decay_pass,
+    span_la_decay_step,
     span_la_pass,
     span_la_pass_noalloc,
     span_la_plan_prepare,
+    span_la_qk_norm_rope,
     span_la_softmax_branches_from_kv,
     span_la_softmax_pass,
 )

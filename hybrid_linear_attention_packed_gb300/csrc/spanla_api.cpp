@@ -23,6 +23,7 @@
 #include <cstring>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <queue>
 #include <string>
 #include <vector>
@@ -137,10 +138,12 @@ span_la_status device_state(DeviceState** out) {
 
 // ------------------------------------------------------------------ profiling
 constexpr int kKernelSplit = 0, kKernelChunk = 1, kKernelScan = 2, kKernelTile = 3,
-              kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6;
+              kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6, kKernelRecurState = 7,
+              kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11;
 const char* const kKernelNames[SPAN_LA_NUM_KERNELS] = {"split_f32", "chunk_state", "segmented_scan",
                                                        "tile_output", "span_state", "span_output",
-                                                       "softmax_attn"};
+                                                       "softmax_attn", "recur_state", "recur_scan",
+                                                       "recur_output", "decay_step", "qk_norm_rope"};
 
 std::atomic<int64_t> g_launches[SPAN_LA_NUM_KERNELS];
 std::atomic<bool> g_profiling{false};
@@ -374,6 +377,10 @@ Plan make_span_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu,
                     const int32_t* parent, int H, int num_sms, bool fused) {
   Plan plan;
   plan.span_mode = true;
+  // One launch without views: branches from kept states.  Term A is then the
+  // kept state, as with three launches; only their own earlier pieces come
+  // from phase 1.
+  const bool kept = fused && V == 0;
   const std::vector<BranchGroup> groups = group_branches(branch_cu, B, parent, &plan.bounds);
 
   // Requests in order: view p (when p < V) followed by the branch groups
@@ -511,7 +518,7 @@ Plan make_span_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu,
       }
       if (fused) {
         if (bk.kind == 0 && bk.ntiles > 0) vlast[static_cast<size_t>(bk.id) * H + bk.head] = bps.back().c;
-        if (bk.kind != 0) {
+        if (bk.kind != 0 && !kept) {
           const size_t vh = static_cast<size_t>(groups[bk.id].parent) * H + bk.head;
           for (size_t q = bp_off[bi]; q < bps.size(); ++q)
             if (bps[q].c != vlast[vh]) vall[vh] = 1;
@@ -571,11 +578,13 @@ Plan make_span_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu,
       w.stateA = -1;
       w.stateB = -1;
       int32_t init = 0;
-      if (!fused) {
+      if (!fused || kept) {
         // three launches: the parent's final state (scan output) and the
-        // piece's scanned prefix slot
+        // piece's scanned prefix slot (or, from kept states in one launch,
+        // its earlier pieces)
         if (parent >= 0) { w.stateA = parent; w.a_n = 1; }
-        if (nslots > 0 && k > 0) { w.stateB = slot0 + k; w.b_n = 1; }
+        if (kept && k > 0) { w.stateB = slot0; w.b_n = k; }
+        else if (nslots > 0 && k > 0) { w.stateB = slot0 + k; w.b_n = 1; }
         init = (w.a_n + w.b_n) > 0 ? kTileHasInit : 0;
       } else {
         // one launch: the parent's final state from this CTA (carry) or as
@@ -651,7 +660,7 @@ Plan make_span_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu,
         for (int32_t i = 0; i < n; ++i) {
           dst[i].head = h;
           // the parent's final state (three launches, or a carry) is not a slot
-          if (fused && dst[i].stateA >= 0) dst[i].stateA += h * S0;
+          if (fused && !kept && dst[i].stateA >= 0) dst[i].stateA += h * S0;
           if (dst[i].stateB >= 0) dst[i].stateB += h * S0;
         }
       }
@@ -794,6 +803,7 @@ struct DescBlock {
   bool fused = false;      // one-launch pass (span mode)
   int n_p1_ctas = 0;
   bool p1_evict_first = false;
+  int piece = 0;           // decayed pass by the recurrence: rows of a piece
   std::vector<int32_t> empty_views;
 };
 
@@ -1521,6 +1531,208 @@ span_la_status check_operands(const void* q, const void* k, const void* v, void*
   return SPAN_LA_OK;
 }
 
+// ------------------------------------------------------------------ decayed passes
+// Plan of a decayed pass by the recurrence: segments in pieces of `piece`
+// rows.  Every piece of a view, and every piece of a branch of several
+// pieces, has a state slot (the scan turns them into the states entering the
+// pieces); a branch's last piece needs no state of its own.
+struct RecurPlan {
+  std::vector<RecurUnit> state, out;
+  std::vector<RecurScan> scan;
+  int piece = 0;
+  int64_t slots = 0;
+};
+
+// Rows of a piece: enough pieces for kRecurUnitsPerSm units (a piece of one
+// head) on every SM, in whole chunks of 16 rows, between 64 (below it a
+// unit's 16 KiB of state outweigh its rows) and 256 (above it one unit's run
+// time shows at the end of the launch).
+constexpr int kRecurUnitsPerSm = 8;
+int recur_piece(int64_t row_heads, int num_sms) {
+  const int64_t want = row_heads / (static_cast<int64_t>(std::max(1, num_sms)) * kRecurUnitsPerSm);
+  return static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(64, (want + 15) / 16 * 16)));
+}
+
+RecurPlan make_recur_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu, int32_t B,
+                          const int32_t* parent, int H, int num_sms) {
+  RecurPlan plan;
+  int64_t rows = 0;
+  if (V > 0) rows += view_cu[V] - view_cu[0];
+  if (B > 0) rows += branch_cu[B] - branch_cu[0];
+  plan.piece = recur_piece(rows * H, num_sms);
+  auto add = [&](int64_t start, int64_t len, int view, int par) {
+    const int64_t n = (len + plan.piece - 1) / plan.piece;
+    if (n == 0 && view < 0) return;
+    const bool slots = view >= 0 || n > 1;
+    const int32_t slot0 = static_cast<int32_t>(plan.slots);
+    for (int64_t c = 0; c < n; ++c) {
+      RecurUnit u{};
+      u.row0 = static_cast<int32_t>(start + c * plan.piece);
+      u.len = static_cast<int32_t>(std::min<int64_t>(plan.piece, len - c * plan.piece));
+      u.parent = par;
+      u.before = static_cast<int32_t>(c * plan.piece);
+      u.slot = slots ? static_cast<int32_t>(slot0 + c) : -1;
+      if (slots && (view >= 0 || c + 1 < n)) plan.state.push_back(u);
+      if (c == 0) u.slot = -1;
+      plan.out.push_back(u);
+    }
+    if (slots) {
+      plan.scan.push_back({slot0, static_cast<int32_t>(n), view,
+                           n > 0 ? static_cast<int32_t>(len - (n - 1) * plan.piece) : 0});
+      plan.slots += n;
+    }
+  };
+  for (int32_t s = 0; s < V; ++s) add(view_cu[s], view_cu[s + 1] - view_cu[s], s, -1);
+  for (int32_t b = 0; b < B; ++b) add(branch_cu[b], branch_cu[b + 1] - branch_cu[b], -1, parent[b]);
+  return plan;
+}
+
+DescBlock make_recur_desc(const RecurPlan& plan, int H) {
+  DescBlock d;
+  d.off_a = put(d.host, plan.state);
+  d.off_b = put(d.host, plan.out);
+  d.off_scan = put(d.host, plan.scan);
+  d.n_chunks = static_cast<int>(plan.state.size());
+  d.n_tiles = static_cast<int>(plan.out.size());
+  d.n_scan = static_cast<int>(plan.scan.size());
+  d.n_out_tiles = plan.out.size();
+  d.state_slots = plan.slots * H;
+  d.piece = plan.piece;
+  return d;
+}
+
+// The launches of a decayed pass by the recurrence over descriptors on the device.
+span_la_status enqueue_recur(const DescBlock& desc, const uint8_t* block, float* states, const void* q,
+                             const void* k, const void* v, const span_la_dims& dims, const float* log_decay,
+                             const float* stateA, float* final_out, void* out, cudaStream_t stream) {
+  RecurArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.state_units = reinterpret_cast<const RecurUnit*>(block + desc.off_a);
+  a.out_units = reinterpret_cast<const RecurUnit*>(block + desc.off_b);
+  a.scan = reinterpret_cast<const RecurScan*>(block + desc.off_scan);
+  a.n_state = desc.n_chunks;
+  a.n_out = desc.n_tiles;
+  a.n_scan = desc.n_scan;
+  a.H = dims.num_heads;
+  a.piece = desc.piece;
+  a.f32 = dims.dtype == SPAN_LA_F32;
+  a.log_decay = log_decay;
+  a.stateA = stateA;
+  a.ws = states;
+  a.final_out = final_out;
+  a.out = out;
+  cudaError_t e = cudaSuccess;
+  if (a.n_state > 0) e = counted_launch(kKernelRecurState, stream, [&] { return launch_recur_state(a, stream); });
+  if (e == cudaSuccess && a.n_scan > 0)
+    e = counted_launch(kKernelRecurScan, stream, [&] { return launch_recur_scan(a, stream); });
+  if (e == cudaSuccess && a.n_out > 0)
+    e = counted_launch(kKernelRecurOutput, stream, [&] { return launch_recur_output(a, stream); });
+  return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "decayed pass launch");
+}
+
+// Descriptors (cached, or in the call's workspace while the stream is being
+// captured), workspace and launches of a decayed pass (kept NULL) or of
+// branches from kept states (final_out NULL).
+template <typename BuildDesc>
+span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc, const void* q, const void* k,
+                         const void* v, const span_la_dims& dims, const float* log_decay, const float* kept,
+                         float* final_out, void* out, cudaStream_t stream, DeviceState* dev, int device) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  const bool use_cache = cap == cudaStreamCaptureStatusNone;
+  std::unique_lock<std::mutex> cache_lock(g_cache_mu, std::defer_lock);
+  DescBlock local;
+  const DescBlock* desc = nullptr;
+  const uint8_t* block = nullptr;
+  CacheEntry* entry = nullptr;
+  span_la_status st = SPAN_LA_OK;
+  if (use_cache) {
+    cache_lock.lock();
+    st = cached_block(key, device, stream, build_desc, &desc, &block, &entry);
+    if (st != SPAN_LA_OK) return st;
+  } else {
+    local = build_desc();
+    desc = &local;
+  }
+  if (desc->n_out_tiles == 0 && desc->n_scan == 0 && desc->empty_views.empty()) return SPAN_LA_OK;
+  // Workspace: the descriptors when they are not cached, the state slots.
+  const size_t slots = static_cast<size_t>(desc->state_slots);
+  const size_t off_states = use_cache ? 0 : align256(desc->host.size());
+  const size_t total = std::max<size_t>(off_states + slots * kStateFloats * sizeof(float), 256);
+  uint8_t* ws = nullptr;
+  if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", total);
+  e = cudaMallocAsync(reinterpret_cast<void**>(&ws), total, stream);
+  if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", total, cudaGetErrorString(e));
+  if (!use_cache) {
+    e = upload_descriptors(ws, std::move(local.host), true, stream);
+    if (e != cudaSuccess) st = cuda_fail(e, "cudaMemcpyAsync(descriptors)");
+    block = ws;
+  }
+  float* states = reinterpret_cast<float*>(ws + off_states);
+  if (st == SPAN_LA_OK)
+    st = enqueue_recur(*desc, block, states, q, k, v, dims, log_decay, kept != nullptr ? kept : final_out, final_out, out,
+                       stream);
+  st = finish_read(entry, stream, st);
+  const cudaError_t ef = cudaFreeAsync(ws, stream);
+  if (st == SPAN_LA_OK && ef != cudaSuccess) st = cuda_fail(ef, "cudaFreeAsync");
+  return st;
+}
+
+// The descriptors of a decayed pass: bf16 passes share span_output's one-launch plans.
+DescBlock make_decay_desc(const int32_t* view_cu, int32_t V, const int32_t* branch_cu, int32_t B, const int32_t* parent,
+                          const span_la_dims& dims, int num_sms) {
+  const int H = dims.num_heads;
+  return make_recur_desc(make_recur_plan(view_cu, V, branch_cu, B, parent, H, num_sms), H);
+}
+
+span_la_status check_log_decay(const float* log_decay) {
+  if (log_decay == nullptr || (reinterpret_cast<uintptr_t>(log_decay) & 3u) != 0)
+    return fail(SPAN_LA_ERR_INVALID, "log_decay must be a non-NULL 4-byte aligned pointer");
+  return SPAN_LA_OK;
+}
+
+// Heads and rows that the decayed and token kernels' one-dimensional grids hold.
+span_la_status check_grid(int64_t units, int H) {
+  if (H > 65535) return fail(SPAN_LA_ERR_INVALID, "num_heads %d > 65535", H);
+  if (units * H > INT32_MAX)
+    return fail(SPAN_LA_ERR_INVALID, "%lld pieces of %d heads are more than one launch takes", (long long)units, H);
+  return SPAN_LA_OK;
+}
+
+// A body that may allocate on the host, as a C entry: an allocation failure
+// becomes a status.
+template <typename Fn>
+span_la_status guarded(Fn&& fn) {
+  try {
+    g_detail.clear();
+    return fn();
+  } catch (const std::bad_alloc&) {
+    return fail(SPAN_LA_ERR_NOMEM, "out of host memory");
+  } catch (const std::exception& ex) {
+    return fail(SPAN_LA_ERR_INVALID, "%s", ex.what());
+  }
+}
+
+// The elements of a [rows] x [width] array with a row stride (bytes).
+struct Rows {
+  uintptr_t at;
+  int64_t stride, width, rows;
+  uintptr_t end() const { return at + static_cast<uintptr_t>((rows - 1) * stride + width); }
+};
+
+// True when no element of `a` is one of `b`: apart in memory, or different
+// columns of rows of the same stride.
+bool apart(const Rows& a, const Rows& b) {
+  if (a.width == 0 || b.width == 0 || a.end() <= b.at || b.end() <= a.at) return true;
+  if (a.stride != b.stride) return false;
+  const int64_t s = a.stride;
+  const int64_t d = static_cast<int64_t>(b.at >= a.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s);
+  return d >= a.width && d + b.width <= s;
+}
+
 }  // namespace
 
 namespace spanla {
@@ -1973,6 +2185,193 @@ span_la_status span_la_selftest_wait_timeout(int32_t limit_us, cudaStream_t stre
   cudaError_t e = launch_wait_timeout_probe(static_cast<unsigned>(limit_us), dev->err, stream);
   if (e != cudaSuccess) return cuda_fail(e, "probe launch");
   return SPAN_LA_OK;
+}
+
+span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, span_la_dims dims,
+                                  const float* log_decay, const int32_t* view_cu_seqlens, int32_t num_views,
+                                  const int32_t* branch_cu_seqlens, int32_t num_branches,
+                                  const int32_t* branch_parent, void* out, float* view_state_out,
+                                  cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    span_la_status st = check_dims(dims);
+    if (st != SPAN_LA_OK) return st;
+    std::vector<Segment> segs;
+    if ((st = check_cu(view_cu_seqlens, num_views, dims.total_rows, "view_cu_seqlens", &segs, true)) != SPAN_LA_OK) return st;
+    if ((st = check_cu(branch_cu_seqlens, num_branches, dims.total_rows, "branch_cu_seqlens", &segs, false)) != SPAN_LA_OK) return st;
+    if ((st = check_overlap(segs)) != SPAN_LA_OK) return st;
+    if ((st = check_parents(branch_parent, num_branches, num_views)) != SPAN_LA_OK) return st;
+    if (!segs.empty() && (st = check_operands(q, k, v, out, dims)) != SPAN_LA_OK) return st;
+    if (num_views > 0 && (view_state_out == nullptr || !aligned16(view_state_out)))
+      return fail(SPAN_LA_ERR_INVALID, "view_state_out must be a non-NULL 16-byte aligned pointer");
+    if (num_views == 0 && num_branches == 0) return SPAN_LA_OK;
+    if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
+    // (pieces of 64 rows at least, and 4 scan CTAs a segment)
+    if ((st = check_grid(dims.total_rows / 64 + 4 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
+    int device = 0;
+    cudaGetDevice(&device);
+    const std::vector<int32_t> key = plan_key(device, dims.dtype, dims.num_heads, 5, dev->num_sms, view_cu_seqlens,
+                                              num_views, branch_cu_seqlens, num_branches, branch_parent);
+    auto build = [&] {
+      return make_decay_desc(view_cu_seqlens, num_views, branch_cu_seqlens, num_branches, branch_parent, dims, dev->num_sms);
+    };
+    return run_decay(key, build, q, k, v, dims, log_decay, nullptr, view_state_out, out, stream, dev, device);
+  });
+}
+
+span_la_status span_la_decay_branches_from_state(const float* cached_state, int32_t num_states, const void* q,
+                                                 const void* k, const void* v, span_la_dims dims,
+                                                 const float* log_decay, const int32_t* branch_cu_seqlens,
+                                                 int32_t num_branches, const int32_t* branch_parent, void* out,
+                                                 cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    span_la_status st = check_dims(dims);
+    if (st != SPAN_LA_OK) return st;
+    if (num_states < 0) return fail(SPAN_LA_ERR_INVALID, "num_states %d < 0", num_states);
+    std::vector<Segment> segs;
+    if ((st = check_cu(branch_cu_seqlens, num_branches, dims.total_rows, "branch_cu_seqlens", &segs, false)) != SPAN_LA_OK) return st;
+    if ((st = check_overlap(segs)) != SPAN_LA_OK) return st;
+    if ((st = check_parents(branch_parent, num_branches, num_states)) != SPAN_LA_OK) return st;
+    if (!segs.empty() && (st = check_operands(q, k, v, out, dims)) != SPAN_LA_OK) return st;
+    if (num_branches > 0 && (cached_state == nullptr || !aligned16(cached_state)))
+      return fail(SPAN_LA_ERR_INVALID, "cached_state must be a non-NULL 16-byte aligned pointer");
+    if (segs.empty()) return SPAN_LA_OK;
+    if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
+    if ((st = check_grid(dims.total_rows / 64 + 4 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
+    int device = 0;
+    cudaGetDevice(&device);
+    const std::vector<int32_t> key = plan_key(device, dims.dtype, dims.num_heads, 6, dev->num_sms, nullptr, 0,
+                                              branch_cu_seqlens, num_branches, branch_parent);
+    auto build = [&] {
+      return make_decay_desc(nullptr, 0, branch_cu_seqlens, num_branches, branch_parent, dims, dev->num_sms);
+    };
+    return run_decay(key, build, q, k, v, dims, log_decay, cached_state, nullptr, out, stream, dev, device);
+  });
+}
+
+span_la_status span_la_decay_step(const void* q, const void* k, const void* v, span_la_dims dims,
+                                  const float* log_decay, float* states, int32_t num_states,
+                                  const int32_t* state_index, void* out, cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    span_la_status st = check_dims(dims);
+    if (st != SPAN_LA_OK) return st;
+    const int64_t n = dims.total_rows;
+    if (num_states < 0) return fail(SPAN_LA_ERR_INVALID, "num_states %d < 0", num_states);
+    if (state_index == nullptr && n > num_states)
+      return fail(SPAN_LA_ERR_INVALID, "%lld rows without state_index need as many states, got %d", (long long)n, num_states);
+    if (n == 0) return SPAN_LA_OK;
+    if ((st = check_operands(q, k, v, out, dims)) != SPAN_LA_OK) return st;
+    if (num_states > 0 && (states == nullptr || !aligned16(states)))
+      return fail(SPAN_LA_ERR_INVALID, "states must be a non-NULL 16-byte aligned pointer");
+    if (log_decay != nullptr && (st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
+    if ((st = check_grid(1, dims.num_heads)) != SPAN_LA_OK) return st;
+    if (state_index != nullptr) {
+      // Two rows of one state would race: every state at most once.
+      std::vector<int32_t> seen;
+      seen.reserve(static_cast<size_t>(n));
+      for (int64_t t = 0; t < n; ++t) {
+        const int32_t i = state_index[t];
+        if (i < -1 || i >= num_states)
+          return fail(SPAN_LA_ERR_INVALID, "state_index[%lld] = %d not in [-1, %d)", (long long)t, i, num_states);
+        if (i >= 0) seen.push_back(i);
+      }
+      std::sort(seen.begin(), seen.end());
+      const auto twice = std::adjacent_find(seen.begin(), seen.end());
+      if (twice != seen.end()) return fail(SPAN_LA_ERR_INVALID, "state_index has state %d twice", *twice);
+    }
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
+    StepArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.n = n;
+    a.H = dims.num_heads;
+    a.f32 = dims.dtype == SPAN_LA_F32;
+    a.log_decay = log_decay;
+    a.states = states;
+    a.index = state_index;
+    a.out = out;
+    const cudaError_t e = counted_launch(kKernelDecayStep, stream, [&] { return launch_decay_step(a, stream); });
+    return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "decay step launch");
+  });
+}
+
+span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_t rows, int32_t dtype,
+                                    int32_t weight_dtype, float eps, const double* inv_freq, int32_t rotary_dim,
+                                    int32_t interleaved, const int32_t* positions, cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    if (dtype != SPAN_LA_BF16 && dtype != SPAN_LA_F32) return fail(SPAN_LA_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
+    if (weight_dtype != SPAN_LA_BF16 && weight_dtype != SPAN_LA_F32)
+      return fail(SPAN_LA_ERR_UNSUPPORTED, "weight_dtype %d not supported", weight_dtype);
+    if (rows < 0 || rows > INT32_MAX) return fail(SPAN_LA_ERR_INVALID, "rows %lld out of range", (long long)rows);
+    if (rotary_dim < 0 || rotary_dim > kHeadDim || rotary_dim % 16 != 0)
+      return fail(SPAN_LA_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16 in [0, 64]", rotary_dim);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SPAN_LA_ERR_INVALID, "eps must be finite and >= 0");
+    if (rotary_dim > 0 && inv_freq == nullptr) return fail(SPAN_LA_ERR_INVALID, "inv_freq is NULL");
+    RopeArgs a{};
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+      if (!std::isfinite(inv_freq[i])) return fail(SPAN_LA_ERR_INVALID, "inv_freq[%d] is not finite", i);
+      const double turns = inv_freq[i] / 6.283185307179586;
+      const double part = turns - std::floor(turns);   // in [0, 1]: 1 when the fraction rounds up
+      a.freq[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0;
+    }
+    const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4;
+    const int64_t wsz = weight_dtype == SPAN_LA_BF16 ? 2 : 4;
+    Rows in[2], out[2];
+    const span_la_qk_side* sides[2] = {&q, &k};
+    RopeArgs::Side* to[2] = {&a.q, &a.k};
+    for (int i = 0; i < 2; ++i) {
+      const span_la_qk_side& x = *sides[i];
+      const char* name = i == 0 ? "q" : "k";
+      if (x.num_heads < 0 || x.num_heads > 65535) return fail(SPAN_LA_ERR_INVALID, "%s: num_heads %d not in [0, 65535]", name, x.num_heads);
+      const int64_t width = static_cast<int64_t>(x.num_heads) * kHeadDim;
+      if (x.num_heads > 0 && rows > 0) {
+        if (x.in == nullptr || x.out == nullptr || !aligned16(x.in) || !aligned16(x.out))
+          return fail(SPAN_LA_ERR_INVALID, "%s: in and out must be non-NULL and 16-byte aligned", name);
+        if (x.in_row_stride < width || x.out_row_stride < width || x.in_row_stride > INT32_MAX || x.out_row_stride > INT32_MAX ||
+            (x.in_row_stride * esz) % 16 != 0 || (x.out_row_stride * esz) % 16 != 0)
+          return fail(SPAN_LA_ERR_INVALID, "%s: row strides must be at least num_heads * 64 elements, below 2^31, and a "
+                      "multiple of 16 bytes", name);
+        if (x.weight != nullptr && (reinterpret_cast<uintptr_t>(x.weight) & static_cast<uintptr_t>(wsz - 1)) != 0)
+          return fail(SPAN_LA_ERR_INVALID, "%s: weight must be aligned to its type", name);
+      }
+      in[i] = {reinterpret_cast<uintptr_t>(x.in), x.in_row_stride * esz, width * esz, rows};
+      out[i] = {reinterpret_cast<uintptr_t>(x.out), x.out_row_stride * esz, width * esz, rows};
+      to[i]->in = x.in;
+      to[i]->out = x.out;
+      to[i]->weight = x.weight;
+      to[i]->in_stride = x.in_row_stride;
+      to[i]->out_stride = x.out_row_stride;
+      to[i]->heads = x.num_heads;
+      to[i]->w_stride = x.weight_per_head ? kHeadDim : 0;
+    }
+    if (rows == 0 || (q.num_heads == 0 && k.num_heads == 0)) return SPAN_LA_OK;
+    for (int i = 0; i < 2; ++i) {
+      const bool in_place = in[i].at == out[i].at && in[i].stride == out[i].stride;
+      if (!in_place && !apart(in[i], out[i]))
+        return fail(SPAN_LA_ERR_INVALID, "%s: out overlaps in without being the same array", i == 0 ? "q" : "k");
+      if (!apart(out[i], in[1 - i])) return fail(SPAN_LA_ERR_INVALID, "%s's out overlaps %s's in", i == 0 ? "q" : "k", i == 0 ? "k" : "q");
+    }
+    if (!apart(out[0], out[1])) return fail(SPAN_LA_ERR_INVALID, "q's out overlaps k's out");
+    if (positions == nullptr || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+      return fail(SPAN_LA_ERR_INVALID, "positions must be a non-NULL 4-byte aligned pointer");
+    DeviceState* dev = nullptr;
+    span_la_status st = device_state(&dev);
+    if (st != SPAN_LA_OK) return st;
+    a.rows = rows;
+    a.positions = positions;
+    a.eps = eps;
+    a.rotary = rotary_dim;
+    a.weight_f32 = weight_dtype == SPAN_LA_F32;
+    const cudaError_t e = counted_launch(kKernelNormRope, stream, [&] {
+      return launch_qk_norm_rope(a, dtype == SPAN_LA_F32, interleaved != 0, stream);
+    });
+    return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "q/k norm and rotation launch");
+  });
 }
 
 }  // extern "C"

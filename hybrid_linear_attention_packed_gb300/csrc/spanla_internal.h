@@ -255,6 +255,84 @@ cudaError_t launch_tile_output(bool split, const CUtensorMap* tm_q, const CUtens
                                const uint8_t* bounds, const float* stateA, const float* stateB,
                                void* out, int H, unsigned* err, cudaStream_t stream, bool pdl);
 
+// Decayed passes by the recurrence (CUDA cores).  Every segment (view or
+// branch) is cut into pieces of `piece` rows (the last one shorter).
+struct RecurUnit {
+  int32_t row0;     // first row of the piece
+  int32_t len;      // rows, >= 1
+  int32_t parent;   // output: index of the state the segment starts from, or -1 (zero)
+  int32_t slot;     // output: slot of the scanned prefix, or -1 (first piece); state: the slot to write
+  int32_t before;   // output: rows of the segment before the piece
+  int32_t pad[3];
+};
+static_assert(sizeof(RecurUnit) == 32, "RecurUnit layout");
+
+// The slots of one segment (every head), in order: slot s of head h is state
+// (slot0 + s) * H + h of the workspace.
+struct RecurScan {
+  int32_t slot0;
+  int32_t nslots;     // pieces (0: an empty view)
+  int32_t final_idx;  // view whose final state is the total, or -1 (a branch: its last piece has no state)
+  int32_t last_len;   // rows of the last piece
+};
+
+struct RecurArgs {
+  const void* q = nullptr;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  const RecurUnit* state_units = nullptr;
+  const RecurUnit* out_units = nullptr;
+  const RecurScan* scan = nullptr;
+  int64_t n_state = 0, n_out = 0, n_scan = 0;
+  int H = 0;
+  int piece = 0;
+  bool f32 = false;
+  const float* log_decay = nullptr;
+  const float* stateA = nullptr;   // [n][H][64][64]: states that segments start from
+  float* ws = nullptr;             // slots
+  float* final_out = nullptr;
+  void* out = nullptr;
+};
+cudaError_t launch_recur_state(const RecurArgs& a, cudaStream_t stream);
+cudaError_t launch_recur_scan(const RecurArgs& a, cudaStream_t stream);
+cudaError_t launch_recur_output(const RecurArgs& a, cudaStream_t stream);
+
+// One new row for each of n sequences (k_token.cu): row t updates state
+// index[t] (row t itself without indices; a negative index skips the row).
+constexpr int kStepFewSlots = 64;
+constexpr int kStepMostSlots = 1000;   // indices of one launch: its parameters stay within 4 KB
+struct StepArgs {
+  const void* q = nullptr;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  int64_t n = 0;
+  int H = 0;
+  bool f32 = false;
+  const float* log_decay = nullptr;   // NULL: no decay
+  float* states = nullptr;
+  const int32_t* index = nullptr;     // host
+  void* out = nullptr;
+};
+cudaError_t launch_decay_step(const StepArgs& a, cudaStream_t stream);
+
+// RMS norm of each head and position rotation of queries and keys (k_token.cu).
+struct RopeArgs {
+  struct Side {
+    const void* in;
+    void* out;
+    const void* weight;   // [64] (w_stride 0) or [heads][64] (w_stride 64), or NULL
+    int64_t in_stride, out_stride;   // elements from row to row
+    int32_t heads, w_stride;
+  } q, k;
+  int64_t rows;
+  const int32_t* positions;
+  float eps;
+  int32_t rotary;      // rotated dimensions, a multiple of 16
+  int32_t weight_f32;
+  uint64_t freq[kHeadDim / 2];   // turns per position as a 64-bit binary fraction
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool f32, bool interleaved, cudaStream_t stream);
+
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
 
 // Fixed workspace of span_la_pass_noalloc (a file-scope device array).

@@ -35,8 +35,9 @@ EXPORTED = ("span_la_pass", "span_la_branches_from_state", "span_la_check",
             "span_la_cache_stats", "span_la_softmax_pass", "span_la_softmax_branches_from_kv",
             "span_la_fault_inject", "span_la_softmax_plan_stats",
             "span_la_selftest_wait_timeout_noalloc", "span_la_pass_variant",
-            "span_la_plan_prepare")
-NUM_KERNELS = 7
+            "span_la_plan_prepare", "span_la_decay_pass", "span_la_decay_branches_from_state",
+            "span_la_decay_step", "span_la_qk_norm_rope")
+NUM_KERNELS = 12
 
 
 class SpanLAError(RuntimeError):
@@ -48,6 +49,12 @@ class SpanLAError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("total_rows", ctypes.c_int64), ("num_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class QkSide(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("in_row_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+                ("num_heads", ctypes.c_int32), ("weight_per_head", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -121,6 +128,17 @@ def load_library(path: Optional[str] = None):
                                                          vp, vp, vp, Dims, i32p, ctypes.c_int32, i32p,
                                                          ctypes.c_float, vp, vp, vp]
         lib.span_la_softmax_branches_from_kv.restype = ctypes.c_int
+        lib.span_la_decay_pass.argtypes = [vp, vp, vp, Dims, vp, i32p, ctypes.c_int32, i32p,
+                                           ctypes.c_int32, i32p, vp, vp, vp]
+        lib.span_la_decay_pass.restype = ctypes.c_int
+        lib.span_la_decay_branches_from_state.argtypes = [vp, ctypes.c_int32, vp, vp, vp, Dims, vp, i32p,
+                                                          ctypes.c_int32, i32p, vp, vp]
+        lib.span_la_decay_branches_from_state.restype = ctypes.c_int
+        lib.span_la_decay_step.argtypes = [vp, vp, vp, Dims, vp, vp, ctypes.c_int32, i32p, vp, vp]
+        lib.span_la_decay_step.restype = ctypes.c_int
+        lib.span_la_qk_norm_rope.argtypes = [QkSide, QkSide, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                             ctypes.c_float, vp, ctypes.c_int32, ctypes.c_int32, vp, vp]
+        lib.span_la_qk_norm_rope.restype = ctypes.c_int
         lib.span_la_cache_create.argtypes = [ctypes.c_int32, ctypes.c_int32,
                                              ctypes.POINTER(ctypes.c_void_p)]
         lib.span_la_cache_create.restype = ctypes.c_int
@@ -365,6 +383,213 @@ def span_la_softmax_branches_from_kv(view_k: torch.Tensor, view_v: torch.Tensor,
         lse.data_ptr() if lse is not None else None, _stream_handle(stream))
     _raise(lib, st, "span_la_softmax_branches_from_kv")
     return out
+
+
+def _on_current_device(**tensors) -> None:
+    """The library runs on the current device: its tensors have to be there."""
+    dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s must be on the current CUDA device (%d), got %s" % (name, dev, t.device))
+
+
+def _decay_args(log_decay, q, k, v, out, optional: bool = False) -> torch.Tensor:
+    """Checks log_decay and out of a decayed call; returns out (allocated when None)."""
+    if log_decay is None:
+        if not optional:
+            raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
+    elif (log_decay.dtype != torch.float32 or not log_decay.is_cuda or not log_decay.is_contiguous()
+          or log_decay.shape != (q.shape[1],)):
+        raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out must be a contiguous CUDA tensor like q")
+    _on_current_device(q=q, k=k, v=v, log_decay=log_decay, out=out)
+    return out
+
+
+def span_la_decay_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                       view_cu_seqlens: Sequence[int], branch_cu_seqlens: Optional[Sequence[int]],
+                       branch_parent: Optional[Sequence[int]], out: Optional[torch.Tensor] = None,
+                       view_state_out: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One packed pass of linear attention with a decay for each head
+    (``span_la_decay_pass`` in ``include/spanla.h``): ``log_decay`` is fp32
+    CUDA [H], the rest as for :func:`span_la_pass`.
+
+    Returns ``(out [T,H,64], view_state_out [V,H,64,64] fp32)``.
+    """
+    lib = load_library()
+    dims = _dims_of(q, k, v)
+    vcu, bcu, par = _i32(view_cu_seqlens), _i32(branch_cu_seqlens), _i32(branch_parent)
+    V = max(len(vcu) - 1, 0)
+    B = max(len(bcu) - 1, 0)
+    if par.size != B:
+        raise ValueError("one parent per branch")
+    out = _decay_args(log_decay, q, k, v, out)
+    H = q.shape[1]
+    if view_state_out is None:
+        view_state_out = torch.empty((V, H, 64, 64), dtype=torch.float32, device=q.device)
+    elif (view_state_out.dtype != torch.float32 or not view_state_out.is_contiguous()
+          or not view_state_out.is_cuda or view_state_out.numel() < V * H * 4096):
+        raise ValueError("view_state_out must be a contiguous fp32 CUDA tensor [V, H, 64, 64]")
+    else:
+        _on_current_device(view_state_out=view_state_out)
+    st = lib.span_la_decay_pass(q.data_ptr(), k.data_ptr(), v.data_ptr(), dims, log_decay.data_ptr(), _iptr(vcu), V,
+                                _iptr(bcu), B, _iptr(par), out.data_ptr(), view_state_out.data_ptr(),
+                                _stream_handle(stream))
+    _raise(lib, st, "span_la_decay_pass")
+    return out, view_state_out
+
+
+def span_la_decay_branches_from_state(cached_state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                      log_decay: torch.Tensor, branch_cu_seqlens: Sequence[int],
+                                      branch_parent: Sequence[int], out: Optional[torch.Tensor] = None,
+                                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Branches of a decayed pass from kept view states
+    (``span_la_decay_branches_from_state``)."""
+    lib = load_library()
+    dims = _dims_of(q, k, v)
+    bcu, par = _i32(branch_cu_seqlens), _i32(branch_parent)
+    B = max(len(bcu) - 1, 0)
+    if par.size != B:
+        raise ValueError("one parent per branch")
+    if (cached_state.dtype != torch.float32 or not cached_state.is_contiguous()
+            or not cached_state.is_cuda or cached_state.dim() != 4
+            or tuple(cached_state.shape[1:]) != (q.shape[1], 64, 64)):
+        raise ValueError("cached_state must be contiguous fp32 CUDA [P, H, 64, 64]")
+    out = _decay_args(log_decay, q, k, v, out)
+    _on_current_device(cached_state=cached_state)
+    st = lib.span_la_decay_branches_from_state(cached_state.data_ptr(), cached_state.shape[0], q.data_ptr(),
+                                               k.data_ptr(), v.data_ptr(), dims, log_decay.data_ptr(), _iptr(bcu), B,
+                                               _iptr(par), out.data_ptr(), _stream_handle(stream))
+    _raise(lib, st, "span_la_decay_branches_from_state")
+    return out
+
+
+def span_la_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, states: torch.Tensor,
+                       log_decay: Optional[torch.Tensor] = None, state_index: Optional[Sequence[int]] = None,
+                       out: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One new token of each of n sequences (``span_la_decay_step``): q, k, v
+    are [n, H, 64]; ``states`` (fp32 CUDA [P, H, 64, 64]) is updated in place.
+    ``state_index`` (host, n entries) names each row's state, -1 for a row to
+    skip; without it row t uses state t.  Without ``log_decay`` nothing decays.
+    Returns the outputs [n, H, 64]."""
+    lib = load_library()
+    dims = _dims_of(q, k, v)
+    if (states.dtype != torch.float32 or not states.is_contiguous() or not states.is_cuda or states.dim() != 4
+            or states.shape[1:] != (q.shape[1], 64, 64)):
+        raise ValueError("states must be contiguous fp32 CUDA [P, H, 64, 64]")
+    out = _decay_args(log_decay, q, k, v, out, optional=True)
+    _on_current_device(states=states)
+    index = None
+    if state_index is not None:
+        keep = _i32(state_index)
+        if keep.size != q.shape[0]:
+            raise ValueError("one state index per row")
+        index = _iptr(keep)
+    st = lib.span_la_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), dims,
+                                log_decay.data_ptr() if log_decay is not None else None, states.data_ptr(),
+                                states.shape[0], index, out.data_ptr(), _stream_handle(stream))
+    _raise(lib, st, "span_la_decay_step")
+    return out
+
+
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0) -> np.ndarray:
+    """The usual frequencies base^(-2 i / rotary_dim), i < rotary_dim / 2, for
+    :func:`span_la_qk_norm_rope` (float64, host)."""
+    return float(base) ** (-2.0 * np.arange(rotary_dim // 2, dtype=np.float64) / rotary_dim)
+
+
+def packed_positions(view_cu_seqlens: Sequence[int], branch_cu_seqlens: Optional[Sequence[int]],
+                     branch_parent: Optional[Sequence[int]], total_rows: int) -> np.ndarray:
+    """Positions of a packed pass's rows (host int32 [total_rows]) for
+    :func:`span_la_qk_norm_rope`: a view's rows count from 0, a branch's go on
+    from its parent view's length, and rows in no segment get -1 (skipped)."""
+    vcu, bcu, par = _i32(view_cu_seqlens), _i32(branch_cu_seqlens), _i32(branch_parent)
+    pos = np.full(int(total_rows), -1, dtype=np.int32)
+    for s in range(max(len(vcu) - 1, 0)):
+        pos[vcu[s]:vcu[s + 1]] = np.arange(vcu[s + 1] - vcu[s], dtype=np.int32)
+    for b in range(max(len(bcu) - 1, 0)):
+        p = int(par[b])
+        pos[bcu[b]:bcu[b + 1]] = np.arange(bcu[b + 1] - bcu[b], dtype=np.int32) + (vcu[p + 1] - vcu[p])
+    return pos
+
+
+def _qk_side(name: str, x: torch.Tensor, weight: Optional[torch.Tensor], out: Optional[torch.Tensor]):
+    """The C struct of one side of span_la_qk_norm_rope, and its output."""
+    if x.dim() != 3 or x.shape[2] != 64 or not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor [T, H, 64], got %s" % (name, tuple(x.shape)))
+    T, H, _ = x.shape
+    if out is None:
+        out = torch.empty((T, H, 64), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_cuda:
+        raise ValueError("%s_out must be a CUDA tensor of %s's shape and type" % (name, name))
+    strides = []
+    for what, t in ((name, x), (name + "_out", out)):
+        s0, s1, s2 = t.stride()
+        if T > 0 and H > 0 and (s2 != 1 or (H > 1 and s1 != 64)):
+            raise ValueError("%s: the heads of a row must lie next to each other" % what)
+        strides.append(s0 if T > 1 else H * 64)
+    per_head = 0
+    if weight is not None:
+        per_head = int(weight.dim() == 2)
+        if not weight.is_cuda or not weight.is_contiguous() or tuple(weight.shape) not in ((64,), (H, 64)):
+            raise ValueError("%s_weight must be contiguous CUDA [64] or [H, 64]" % name)
+    side = QkSide(x.data_ptr(), out.data_ptr(), weight.data_ptr() if weight is not None else None, strides[0], strides[1],
+                  H, per_head)
+    return side, out
+
+
+def span_la_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq,
+                         q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                         eps: float = 1e-6, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                         k_out: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every head of q [T, Hq, 64] and k [T, Hk, 64], then the
+    rotation by ``positions`` (CUDA int32 [T]; negative: the row is skipped)
+    (``span_la_qk_norm_rope``).
+
+    ``inv_freq`` holds rotary_dim / 2 host values in radians per position
+    (:func:`rope_inv_freq`; None or empty: norm only).  q and k may be strided
+    parts of a fused projection's rows; weights are [64] or [H, 64].  Returns
+    (q_out, k_out), allocated contiguous when not given; an output may be its
+    own input."""
+    lib = load_library()
+    if q.dtype == torch.bfloat16:
+        dt = SPAN_LA_BF16
+    elif q.dtype == torch.float32:
+        dt = SPAN_LA_F32
+    else:
+        raise ValueError("dtype %s not supported (bf16 or fp32)" % q.dtype)
+    if k.dtype != q.dtype or k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must share dtype and rows")
+    wdt = dt
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError("weight dtype %s not supported (bf16 or fp32)" % w.dtype)
+            wdt = SPAN_LA_BF16 if w.dtype == torch.bfloat16 else SPAN_LA_F32
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must share dtype")
+    if (positions.dtype != torch.int32 or not positions.is_cuda or not positions.is_contiguous()
+            or positions.shape != (q.shape[0],)):
+        raise ValueError("positions must be contiguous int32 CUDA [T]")
+    freq = None
+    if inv_freq is not None:
+        if isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda:
+            raise ValueError("inv_freq holds host values")
+        freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
+    rotary = 2 * (freq.size if freq is not None else 0)
+    qs, q_out = _qk_side("q", q, q_weight, q_out)
+    ks, k_out = _qk_side("k", k, k_weight, k_out)
+    _on_current_device(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    st = lib.span_la_qk_norm_rope(qs, ks, q.shape[0], dt, wdt, float(eps), freq.ctypes.data if rotary else None, rotary,
+                                  1 if interleaved else 0, positions.data_ptr(), _stream_handle(stream))
+    _raise(lib, st, "span_la_qk_norm_rope")
+    return q_out, k_out
 
 
 def _keys(keys) -> np.ndarray:

@@ -370,14 +370,16 @@ span_la_status span_la_plan_stats(const int32_t *view_cu_seqlens, int32_t num_vi
  * Kernel profiling (tracing hook).  Kernels are numbered
  *   0 split_f32, 1 chunk_state, 3 tile_output (fp32 inputs),
  *   2 segmented_scan (both), 4 span_state, 5 span_output (bf16 inputs),
- *   6 softmax_attn (span_la_softmax_pass).
+ *   6 softmax_attn (span_la_softmax_pass), 7 recur_state, 8 recur_scan,
+ *   9 recur_output (decayed passes),
+ *   10 decay_step, 11 qk_norm_rope.
  * Launches of every kernel are always counted.  While profiling is enabled,
  * every launch is also bracketed by two CUDA events recorded on the call's
  * stream (one device only); span_la_profile_read() waits for the pending
  * events and adds their elapsed times up.  Enabling adds two event records per
  * launch and nothing else to the work on the stream.
  */
-#define SPAN_LA_NUM_KERNELS 7
+#define SPAN_LA_NUM_KERNELS 12
 
 /* Turn event timing on (non-zero) or off. */
 span_la_status span_la_profile_enable(int32_t enable);
@@ -446,6 +448,111 @@ span_la_status span_la_softmax_branches_from_kv(const void *view_k, const void *
                                                 int32_t num_branches, const int32_t *branch_parent,
                                                 float scale, void *out, float *lse_out,
                                                 cudaStream_t stream);
+
+/*
+ * Linear attention with a decay for each head, over the same packed rows:
+ *
+ *     S_t = a_h S_{t-1} + k_t v_t^T        o_t = S_t^T q_t,   a_h = exp(log_decay[h])
+ *
+ * (span_la_pass is the case a_h = 1.)  Unrolled from a start state S0 before
+ * row t0:  o_t = sum_{t0 <= j <= t} a^(t-j) (q_t . k_j) v_j + a^(t-t0+1) S0^T q_t.
+ *
+ * span_la_decay_pass -- one packed pass: views from S = 0, branches from their
+ * parent view's final state, metadata, layouts, precision and errors as for
+ * span_la_pass ("Serving 0.88M TPS from Two RTXs and Mac Minis", section "The
+ * Workload": branches attend to the view, not to each other).
+ *   log_decay        device fp32 [H]: the natural logarithm of each head's
+ *                    decay, normally <= 0; -infinity is a decay of 0 (o_t
+ *                    sees row t only).  Read when the stream reaches the call
+ *   out              must not overlap q, k or v
+ *   other arguments  as for span_la_pass
+ * With fp32 inputs every product and sum is fp32.  With bf16 inputs the
+ * factors a^n are applied in fp32 and the state is kept to fp32 accuracy; the
+ * masked scores and the state enter their products with v and q rounded to
+ * bf16.
+ */
+span_la_status span_la_decay_pass(const void *q, const void *k, const void *v,
+                                  span_la_dims dims, const float *log_decay,
+                                  const int32_t *view_cu_seqlens, int32_t num_views,
+                                  const int32_t *branch_cu_seqlens, int32_t num_branches,
+                                  const int32_t *branch_parent,
+                                  void *out, float *view_state_out,
+                                  cudaStream_t stream);
+
+/*
+ * span_la_decay_branches_from_state -- branches of span_la_decay_pass only,
+ * each from a kept view state (as span_la_branches_from_state: shards of a
+ * long request, section "Long Requests").
+ *   cached_state     device fp32 [num_states][H][64][64]
+ *   branch_parent    host int32 [num_branches], each in [0, num_states)
+ */
+span_la_status span_la_decay_branches_from_state(const float *cached_state, int32_t num_states,
+                                                 const void *q, const void *k, const void *v,
+                                                 span_la_dims dims, const float *log_decay,
+                                                 const int32_t *branch_cu_seqlens,
+                                                 int32_t num_branches,
+                                                 const int32_t *branch_parent,
+                                                 void *out, cudaStream_t stream);
+
+/*
+ * span_la_decay_step -- the recurrence for one new row of each of
+ * dims.total_rows sequences: row t updates a state in place and gets its
+ * output, so that a sequence whose prompt span_la_decay_pass (or
+ * span_la_pass) ran goes on token by token from its view_state_out.
+ *   q, k, v, out     device [n][H][64], n = dims.total_rows
+ *   log_decay        as for span_la_decay_pass, or NULL: no decay (the next
+ *                    token of span_la_pass)
+ *   states           device fp32 [num_states][H][64][64], updated in place
+ *   state_index      HOST int32 [n]: the state of each row, in [-1, num_states);
+ *                    a row of -1 (padding) is skipped, its out left as it was;
+ *                    no state may be named twice.  NULL: row t uses state t
+ *                    (n <= num_states).  Read during the call only, and kept
+ *                    by a recorded call (CUDA graph capture)
+ * Sums and states are fp32; out is rounded to the input type.  No workspace.
+ */
+span_la_status span_la_decay_step(const void *q, const void *k, const void *v,
+                                  span_la_dims dims, const float *log_decay,
+                                  float *states, int32_t num_states,
+                                  const int32_t *state_index,
+                                  void *out, cudaStream_t stream);
+
+/* One side (queries or keys) of span_la_qk_norm_rope: heads of 64 elements
+ * next to each other in a row, rows at a stride (elements; a multiple of 16
+ * bytes), so that q and k may be parts of a fused projection's rows. */
+typedef struct {
+    const void *in;          /* device, 16-byte aligned */
+    void *out;               /* device, 16-byte aligned; may be `in` (same stride) */
+    const void *weight;      /* device [64], or [num_heads][64], or NULL (ones) */
+    int64_t in_row_stride;
+    int64_t out_row_stride;
+    int32_t num_heads;       /* 0: nothing on this side */
+    int32_t weight_per_head; /* nonzero: weight is [num_heads][64] */
+} span_la_qk_side;
+
+/*
+ * span_la_qk_norm_rope -- what a layer does to its queries and keys before the
+ * passes: the RMS norm of every head, then the rotation by its position,
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight
+ *     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin),  angle = position * inv_freq[i]
+ *
+ * for the first rotary_dim of the 64 dimensions; pair i is dimensions
+ * (i, i + rotary_dim / 2), or (2i, 2i + 1) when `interleaved` is nonzero.  In
+ * fp32, angles to 2^-32 of a turn at any position; rounded once, at the end.
+ *   rows, dtype      rows of both sides and the type of their in and out
+ *   weight_dtype     type of the weights (span_la_dtype)
+ *   inv_freq         HOST double [rotary_dim / 2], radians per position
+ *   rotary_dim       0 (norm only), 16, 32, 48 or 64
+ *   positions        device int32 [rows]; a row whose position is negative is
+ *                    neither read nor written
+ * The outputs must not overlap each other or the other side's input.  With
+ * eps = 0 a head of zeros gives NaN, as the formula does.
+ */
+span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_t rows,
+                                    int32_t dtype, int32_t weight_dtype, float eps,
+                                    const double *inv_freq, int32_t rotary_dim,
+                                    int32_t interleaved, const int32_t *positions,
+                                    cudaStream_t stream);
 
 /*
  * View-state cache ("Serving 0.88M TPS from Two RTXs and Mac Minis", section
