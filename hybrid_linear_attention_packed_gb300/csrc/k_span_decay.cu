@@ -1,0 +1,979 @@
+// Decayed linear attention over a packed pass, bf16 inputs: one cooperative
+// launch for the piece states, their decayed sums, and the output of every
+// row.  With a = exp(log_decay[h]) and S the state entering a tile of up to
+// 128 rows (row i of the tile, its segment starting at row s(i) of it):
+//
+//     o_i = sum_{s(i) <= j <= i} a^(i-j) (q_i . k_j) v_j  +  a^(i-s(i)+1) S^T q_i
+//     S  <- a^n S + sum_j a^(n-1-j) k_j v_j^T                       (n rows)
+//
+// The work is cut as span_output's is (k_span_output.cu): one run of tiles
+// per SM from a host-built list; a piece is the part of a segment-head inside
+// a run; first every CTA sums K^T V over its own pieces whose state another
+// CTA needs (phase 1), then a CTA that needs such states waits for a
+// grid-wide counter and sums them, here by Horner's rule, piece by piece:
+// S <- a^rows S + piece.  Where the decay enters:
+//
+//   scores   in fp32, as P leaves tensor memory to become the bf16 operand of
+//            P V: a row's factors fall by a from each column to the one
+//            before (running products of a^4, at most eight factors deep,
+//            from a power at the block's last column); in the 32 x 32 blocks on
+//            the diagonal of a head with a < 1/16, where those would start above
+//            1 by more than fp32 holds, by 2^((i-j) log2 a) for each element.
+//   Q S      a row factor, which no rounding to bf16 should see: Q S has its own
+//            accumulator, and the output warps add a^(i-s(i)+1) times it to P V.
+//   K^T V    by scaling V: V' = a^(n-1-j) v_j, fp32, as a sum of three bf16
+//            numbers (24 bits: exactly the fp32 product), each with its own
+//            product with K.  The state is kept to fp32 accuracy that way; V'
+//            rounded to bf16 once would leave it 2e-3 off, twice 3e-6.
+//            (A factor on the tensor memory side is not possible: the rows j are
+//            the summed dimension.)
+//
+// Against span_output the V' tile takes a load stage's place in shared memory
+// (three stages instead of four), and Q S's accumulator the second K^T V
+// region's in tensor memory.
+//
+// 19 warps:
+//   warp 0      producer: K, V tiles of phase 1, then Q, K, V tiles, by TMA.
+//   warp 1      front issuer: phase 1, K^T V'; then per tile P = Q K^T and,
+//               unless the tile ends its piece (or when it ends a view-head), dS = K^T V'.
+//   warp 2      O issuer: P V, then Q S.
+//   warps 3-10  scaling and conversion: V' of the tile (16 bytes of V at a
+//               time; rows past the tile become zero, and so do V's
+//               infinities and NaNs for P V, see add_nonfinite), then P, two warps per
+//               TMEM lane quarter, one per 64-column half.
+//   warps 11-18 state and output: the running state in registers (fp32, 16
+//               columns of one state row per thread), S staged in bf16, O stored.
+#include "decay_math.cuh"
+#include "span_tiles.cuh"
+#include "spanla_internal.h"
+#include "tc_ptx.cuh"
+
+namespace spanla {
+namespace {
+
+constexpr int kThreads = 32 * (3 + 8 + 8);
+constexpr int kGroupThreads = 32 * 8;                      // state and output
+constexpr int kConvWarps = 8;                              // scaling and conversion
+constexpr int kConvThreads = 32 * kConvWarps;
+constexpr int kStateWarp0 = 3 + kConvWarps;                // first state/output warp
+constexpr int kStages = 3;
+constexpr int kSetupLoads = kFirstLoads < kStages ? kFirstLoads : kStages;   // loads on fresh stages
+constexpr int kParts = 3;                                  // bf16 parts of V'
+constexpr uint32_t kRowTileBytes = kTileRows * 128;        // 128 rows x 128 B
+constexpr uint32_t kStageBytes = 3 * kRowTileBytes;        // Q K V
+constexpr uint32_t kStateTileBytes = kHeadDim * 128;       // 64 rows x 128 B (bf16)
+// An S operand: S in bf16 in its first 8 KB; O of two lane quarters on its way
+// out in the second 8 KB (quarters 0, 1 in operand 0; 2, 3 in operand 1).
+constexpr uint32_t kSOpBytes = 2 * kStateTileBytes;
+constexpr uint32_t kOQuarterBytes = kOutStoreRows * 128;
+static_assert(2 * kOQuarterBytes == kStateTileBytes, "two quarters of O staging per S operand");
+constexpr int kCoordSlots = 64;
+constexpr int kP1Slots = 32;
+constexpr int kSegSlots = 4;   // tiles whose segment starts are kept for the output warps
+constexpr int kBadSlots = 8;   // tiles whose marks are (made before P(i): five tiles could be open)
+// log2 a of a steep head: below it a^-31, the factor of a diagonal block's
+// last column in its first row (a masked one), could pass the fp32 range.
+constexpr float kSteepLog2 = -4.f;
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns: P buffers (128 each), O buffers (64 each), dS, Q S (64 each;
+// both hold piece states in phase 1).
+constexpr uint32_t kColP0 = 0, kColP1 = 128, kColO0 = 256, kColO1 = 320, kColD = 384, kColQS = 448;
+constexpr uint32_t kNamedStateBar = 1;
+
+struct DecaySmem {
+  static constexpr uint32_t kStage0 = 0;
+  static constexpr uint32_t kQ = 0, kK = kRowTileBytes, kV = 2 * kRowTileBytes;
+  static constexpr uint32_t kS = kStages * kStageBytes;
+  static constexpr uint32_t kVs = kS + 2 * kSOpBytes;              // V' parts
+  static constexpr uint32_t kBar = kVs + kParts * kRowTileBytes;
+  // Barriers; the pairs are used by alternate tiles (or phase-1 pieces).
+  // Empty takes two arrivals per use (both issuers read a tile's stage; the
+  // front issuer arrives twice on a phase-1 stage), OReady two (the MMAs'
+  // completion and the issuing thread, behind which the segment starts that
+  // the conversion warps wrote are visible).
+  static constexpr int kFull = 0, kEmpty = kStages, kPReady = 2 * kStages, kPDone = kPReady + 2, kOReady = kPReady + 4,
+                       kOFree = kPReady + 6, kSSmem = kPReady + 8, kP1Ready = kPReady + 10, kP1Free = kPReady + 12,
+                       kPFree = kPReady + 14, kDReady = kPReady + 16, kDFree = kPReady + 17, kVReady = kPReady + 18,
+                       kVFree = kPReady + 19, kP1Done = kPReady + 20, kNumBars = kPReady + 21;
+  static constexpr uint32_t kTmemSlot = kBar + 8 * kNumBars;
+  static constexpr uint32_t kCoord = (kTmemSlot + 4 + 15) & ~15u;
+  static constexpr uint32_t kP1 = kCoord + 8 * kCoordSlots;
+  static constexpr uint32_t kSeg = kP1 + sizeof(SpanDesc) * kP1Slots;   // first row of each row's segment
+  static constexpr uint32_t kBad = kSeg + kSegSlots * kTileRows;        // 1 + the tile whose V held an inf or NaN
+  static constexpr uint32_t kBytes = kBad + 4 * kBadSlots;
+  static constexpr uint32_t kRequest = kBytes + 1024;
+};
+static_assert(DecaySmem::kRequest <= 227 * 1024, "shared memory budget");
+
+struct DecayParams {
+  const CtaHead* heads;
+  const WorkTile* work;
+  const uint8_t* bounds;
+  const float* log_decay;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const float* stateA;
+  float* ws;
+  float2* ws_factor;      // a^rows of each slot's piece, as a Factor
+  float* final_out;
+  __nv_bfloat16* out;
+  unsigned* err;
+  const SpanDesc* p1;
+  unsigned* counter;
+  int a_rows;
+  int H;
+  int n_p1_ctas;
+};
+
+// True when one of two bf16 is infinite or NaN (its exponent bits all set).
+__device__ __forceinline__ bool nonfinite2(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ bool nonfinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool nonfinite_hi(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
+
+// (out of line: a few calls a piece)
+__device__ __noinline__ Factor factor_of(float ld, float n) { return decay_factor(ld, n); }
+
+// A tile's P V ran without the infinite and NaN values of V (they stand as 0
+// in shared memory: 0 times one of them, in a masked place, would be NaN).
+// Their terms a^(i-j) (q_i . k_j) v_jc, for the rows that see them: added to
+// 16 columns of row i = `row` of the tile.
+__device__ __noinline__ void add_nonfinite(float* y, const DecayParams& prm, int64_t row0, int row, int seg_start, int head,
+                                           int col, float l2) {
+  const int64_t stride = static_cast<int64_t>(prm.H) * kHeadDim;
+  const int64_t at = row0 * stride + static_cast<int64_t>(head) * kHeadDim;
+  for (int j = seg_start; j <= row; ++j) {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(prm.v + at + j * stride + col);
+    bool any = false;
+    for (int c = 0; c < 8; ++c) any |= nonfinite2(v[c]);
+    if (!any) continue;
+    float score = 0.f;
+    for (int e = 0; e < kHeadDim; ++e)
+      score = fmaf(__bfloat162float(prm.q[at + row * stride + e]), __bfloat162float(prm.k[at + j * stride + e]), score);
+    score *= decay_pow(l2, static_cast<float>(row - j));
+    for (int c = 0; c < 8; ++c) {
+      if (nonfinite_lo(v[c])) y[2 * c] += score * __uint_as_float(v[c] << 16);
+      if (nonfinite_hi(v[c])) y[2 * c + 1] += score * __uint_as_float(v[c] & 0xffff0000u);
+    }
+  }
+}
+
+// Two fp32 numbers (24 bits) as sums of three bf16 each (8 bits), packed:
+// cut off 16 bits, then the rest's, exactly.
+__device__ __forceinline__ void split3(uint64_t x, uint32_t (&part)[kParts]) {
+  const uint64_t minus = f32x2(-1.f, -1.f);
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    float lo, hi;
+    f32x2_split(x, lo, hi);
+    part[p] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    if (p + 1 < kParts)
+      x = fma_f32x2(f32x2(__uint_as_float(__float_as_uint(lo) & 0xffff0000u), __uint_as_float(__float_as_uint(hi) & 0xffff0000u)),
+                    minus, x);
+  }
+}
+
+// Eight values of V with an infinity or a NaN among them: its parts of V'
+// once more, without remainders of those (inf - inf), and zeros for them in V.
+__device__ __noinline__ void repair_piece(uint8_t* src, uint8_t* dst, float f, bool scale, bool clear) {
+  uint32_t* v = reinterpret_cast<uint32_t*>(src);
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t keep = (nonfinite_lo(v[e]) ? 0u : 0xffffu) | (nonfinite_hi(v[e]) ? 0u : 0xffff0000u);
+    if (scale) {
+      uint32_t part[kParts];
+      split3(mul_f32x2(f32x2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)), f32x2(f, f)), part);
+      for (int p = 0; p < kParts; ++p)
+        reinterpret_cast<uint32_t*>(dst + p * kRowTileBytes)[e] = p == 0 ? part[p] : part[p] & keep;
+    }
+    if (clear) v[e] &= keep;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                  const __grid_constant__ DecayParams prm) {
+  using L = DecaySmem;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int H = prm.H;
+  unsigned* err = prm.err;
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  auto bar = [&](int slot) { return base + L::kBar + 8u * slot; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+
+  const int4* hd = reinterpret_cast<const int4*>(prm.heads + blockIdx.x);
+  const int4 h0 = __ldg(hd), h1 = __ldg(hd + 1);
+  const int i_begin = h0.x, n = h0.y, p1_begin = h0.z, n_p1 = h0.w;
+  const int n1 = h1.x;                                   // phase-1 tiles
+  const int n_first = min(h1.y, kSetupLoads);            // loads issued during the set-up
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(L::kFull + s), 1);
+      mbar_init(bar(L::kEmpty + s), 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(L::kPReady + b), 1);
+      mbar_init(bar(L::kPDone + b), kConvThreads);
+      mbar_init(bar(L::kOReady + b), 2);
+      mbar_init(bar(L::kPFree + b), 1);
+      mbar_init(bar(L::kOFree + b), kGroupThreads);
+      mbar_init(bar(L::kSSmem + b), kGroupThreads);
+      mbar_init(bar(L::kP1Ready + b), 1);
+      mbar_init(bar(L::kP1Free + b), kGroupThreads);
+    }
+    mbar_init(bar(L::kDReady), 1);
+    mbar_init(bar(L::kDFree), kGroupThreads);
+    mbar_init(bar(L::kVReady), kConvThreads);
+    mbar_init(bar(L::kVFree), 1);
+    mbar_init(bar(L::kP1Done), kGroupThreads);
+    for (int s = 0; s < kBadSlots; ++s) reinterpret_cast<int*>(smem + L::kBad)[s] = 0;
+    fence_mbar_init();
+    const int4 f0 = __ldg(hd + 2), f1 = __ldg(hd + 3);
+    const int fr[2 * kFirstLoads] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+    for (int u = 0; u < kSetupLoads; ++u) {
+      if (u < n_first) {
+        const uint32_t st = base + L::kStage0 + u * kStageBytes;
+        mbar_arrive_expect_tx(bar(L::kFull + u), u < n1 ? 2 * kRowTileBytes : kStageBytes);
+        if (u >= n1) tma_load_3d(st + L::kQ, &tm_q, bar(L::kFull + u), 0, fr[2 * u], fr[2 * u + 1]);
+        tma_load_3d(st + L::kK, &tm_k, bar(L::kFull + u), 0, fr[2 * u], fr[2 * u + 1]);
+        tma_load_3d(st + L::kV, &tm_v, bar(L::kFull + u), 0, fr[2 * u], fr[2 * u + 1]);
+      }
+    }
+    tma_prefetch_desc(&tm_o);
+  }
+
+  const WorkTile* list = prm.work + i_begin;
+  const SpanDesc* p1 = prm.p1 + p1_begin;
+  int2* coord = reinterpret_cast<int2*>(smem + L::kCoord);
+  SpanDesc* p1s = reinterpret_cast<SpanDesc*>(smem + L::kP1);
+  if (warp == 2) {   // idle until the set-up completes: stages what the producer and phase 1 read
+    int2 c_lo = make_int2(0, 0), c_hi = make_int2(0, 0);
+    if (lane < n) c_lo = make_int2(list[lane].row0, list[lane].head);
+    if (lane + 32 < n && lane + 32 < kCoordSlots) c_hi = make_int2(list[lane + 32].row0, list[lane + 32].head);
+    for (int j = lane; j < n_p1 && j < kP1Slots; j += 32) p1s[j] = p1[j];
+    if (lane < n) coord[lane] = c_lo;
+    if (lane + 32 < n && lane + 32 < kCoordSlots) coord[lane + 32] = c_hi;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  auto p1_of = [&](int j) { return j < kP1Slots ? p1s[j] : p1[j]; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      bool ok = true;
+      int u = 0;   // load index: phase-1 tiles, then the run's tiles
+      for (int j = 0; j < n_p1 && ok; ++j) {
+        const SpanDesc sd = p1_of(j);
+        for (int r = 0; r < sd.len && ok; r += kTileRows, ++u) {
+          if (u < n_first) continue;   // issued during the set-up
+          const int s = u % kStages;
+          if (!wait_or_flag(bar(L::kEmpty + s), ((u / kStages) & 1) ^ 1, err, kErrTimeoutMma)) { ok = false; break; }
+          const uint32_t st = base + L::kStage0 + s * kStageBytes;
+          mbar_arrive_expect_tx(bar(L::kFull + s), 2 * kRowTileBytes);
+          tma_load_3d(st + L::kK, &tm_k, bar(L::kFull + s), 0, sd.row0 + r, sd.head);
+          tma_load_3d(st + L::kV, &tm_v, bar(L::kFull + s), 0, sd.row0 + r, sd.head);
+        }
+      }
+      for (int i = 0; i < n && ok; ++i, ++u) {
+        if (u < n_first) continue;
+        const int2 rc = i < kCoordSlots ? coord[i] : make_int2(list[i].row0, list[i].head);
+        const int s = u % kStages;
+        if (!wait_or_flag(bar(L::kEmpty + s), ((u / kStages) & 1) ^ 1, err, kErrTimeoutMma)) { ok = false; break; }
+        const uint32_t st = base + L::kStage0 + s * kStageBytes;
+        mbar_arrive_expect_tx(bar(L::kFull + s), kStageBytes);
+        tma_load_3d(st + L::kQ, &tm_q, bar(L::kFull + s), 0, rc.x, rc.y);
+        tma_load_3d(st + L::kK, &tm_k, bar(L::kFull + s), 0, rc.x, rc.y);
+        tma_load_3d(st + L::kV, &tm_v, bar(L::kFull + s), 0, rc.x, rc.y);
+      }
+      // Wait (bounded) for the last loads to land before the CTA can exit.
+      for (int w = (u > kStages ? u - kStages : 0); w < u; ++w)
+        mbar_wait_bounded(bar(L::kFull + w % kStages), (w / kStages) & 1, ok ? kWaitLimitNs : 1000000ull);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ front issuer
+    constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t id_kv = idesc_bf16_f32(128, 64, 1, 1);
+    bool ok = true;
+    int u = 0;
+    // Zero K (and V) rows past `rows` in a stage: they may hold anything, even
+    // NaN, or rows of another segment.
+    auto zero_tail = [&](uint32_t st, int rows, bool v_too) {
+      if (rows >= kTileRows) return;
+      uint8_t* krow = smem + (st + L::kK - base);
+      uint8_t* vrow = smem + (st + L::kV - base);
+      for (int q = rows * 8 + lane; q < kTileRows * 8; q += 32) {
+        *reinterpret_cast<uint4*>(krow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+        if (v_too) *reinterpret_cast<uint4*>(vrow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    };
+    // D = [K | K]^T V', the parts of V' smallest first.  (Both 64-wide M
+    // atoms read the K tile: leading byte offset 0; TMEM lanes 64..127 get a
+    // second copy of rows 0..63.)
+    auto mma_state = [&](uint32_t st, uint32_t col) {
+      const uint64_t dk = smem_desc_sw128(st + L::kK, 0, 1024);
+      const uint64_t dv = smem_desc_sw128(base + L::kVs, kRowTileBytes, 1024);
+#pragma unroll
+      for (int p = kParts - 1; p >= 0; --p)
+#pragma unroll
+        for (int kk = 0; kk < kTileRows / 16; ++kk)   // (addresses in units of 16 bytes)
+          mma_bf16(tmem + col, dk + kk * (2048 / 16), dv + p * (kRowTileBytes / 16) + kk * (2048 / 16), id_kv,
+                   (p < kParts - 1 || kk > 0) ? 1u : 0u);
+    };
+    // Phase 1: K^T V' of each tile of the pieces.
+    for (int j = 0; j < n_p1 && ok; ++j) {
+      const SpanDesc sd = p1_of(j);
+      for (int r = 0; r < sd.len; r += kTileRows, ++u) {
+        const int s = u % kStages, b = u & 1;
+        ok = wait_or_flag(bar(L::kFull + s), (u / kStages) & 1, err, kErrTimeoutTma);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t st = base + L::kStage0 + s * kStageBytes;
+        zero_tail(st, sd.len - r, false);
+        ok = wait_or_flag(bar(L::kVReady), u & 1, err, kErrTimeoutMma);
+        if (ok && u >= 2) ok = wait_or_flag(bar(L::kP1Free + b), ((u - 2) >> 1) & 1, err, kErrTimeoutMma);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          mma_state(st, b ? kColQS : kColD);
+          mma_commit(bar(L::kP1Ready + b));
+          mma_commit(bar(L::kVFree));
+          mma_commit(bar(L::kEmpty + s));
+          mma_commit(bar(L::kEmpty + s));
+        }
+        __syncwarp();
+      }
+    }
+    // The regions take the run's tiles once phase 1 has been read out.
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && n_p1 > 0) ok = wait_or_flag(bar(L::kP1Done), 0, err, kErrTimeoutMma);
+    ok = __all_sync(0xffffffffu, ok);
+    TileHead nxt = (ok && n > 0) ? load_head(list) : TileHead{};
+    for (int i = 0; i < n && ok; ++i, ++u) {
+      const TileHead r = nxt;
+      if (i + 1 < n) nxt = load_head(list + i + 1);
+      const int s = u % kStages, b = i & 1;
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + s), (u / kStages) & 1, err, kErrTimeoutTma)))
+        break;
+      const uint32_t st = base + L::kStage0 + s * kStageBytes;
+      zero_tail(st, r.nrows, true);
+      __syncwarp();
+      // P buffer b is free once P V of tile i-2 has completed.
+      bool ok2 = true;
+      if (i >= 2) ok2 = wait_or_flag(bar(L::kPFree + b), ((i - 2) >> 1) & 1, err, kErrTimeoutMma);
+      if (!__all_sync(0xffffffffu, ok2)) break;
+      tc_fence_after_sync();
+      if (lane == 0) {
+        const uint32_t colP = b ? kColP1 : kColP0;
+        for (int kk = 0; kk < kHeadDim / 16; ++kk)
+          mma_bf16(tmem + colP, smem_desc_sw128(st + L::kQ + kk * 32, 16, 1024),
+                   smem_desc_sw128(st + L::kK + kk * 32, 16, 1024), id_qk, kk > 0);
+        mma_commit(bar(L::kPReady + b));
+      }
+      __syncwarp();
+      // V'(i) is staged, and dS(i-1) has been read.
+      ok2 = wait_or_flag(bar(L::kVReady), u & 1, err, kErrTimeoutMma);
+      if (ok2 && i >= 1) ok2 = wait_or_flag(bar(L::kDFree), (i - 1) & 1, err, kErrTimeoutMma);
+      if (!__all_sync(0xffffffffu, ok2)) break;
+      tc_fence_after_sync();
+      if (lane == 0) {
+        if (!(r.flags & kTileLast) || (r.flags & kTileFinalOut)) mma_state(st, kColD);
+        mma_commit(bar(L::kDReady));
+        mma_commit(bar(L::kVFree));
+        mma_commit(bar(L::kEmpty + s));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O issuer
+    constexpr uint32_t id_n64_b_mn = idesc_bf16_f32(128, 64, 0, 1);
+    TileHead nxt = n > 0 ? load_head(list) : TileHead{};
+    for (int i = 0; i < n; ++i) {
+      const TileHead r = nxt;
+      if (i + 1 < n) nxt = load_head(list + i + 1);
+      const int u = n1 + i;
+      const int s = u % kStages, b = i & 1;
+      const uint32_t st = base + L::kStage0 + s * kStageBytes;
+      const bool has_state = !(r.flags & kTileFirst) || (r.flags & kTileHasInit);
+      const uint32_t colO = b ? kColO1 : kColO0;
+      // P(i) is bf16 in TMEM: O(i) = P(i) V(i).  (O(i-2) was read out before
+      // Q S of tile i-1 was issued.)
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kPDone + b), (i >> 1) & 1, err, kErrTimeoutMma))) break;
+      tc_fence_after_sync();
+      if (lane == 0) {
+        const uint32_t colP = b ? kColP1 : kColP0;
+        // keys 0..63 of P in columns 0..31, keys 64..127 in columns 64..95
+        for (int kk = 0; kk < kTileRows / 16; ++kk)
+          mma_bf16_tmem_a(tmem + colO, tmem + colP + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
+                          smem_desc_sw128(st + L::kV + kk * 2048, kRowTileBytes, 1024),
+                          id_n64_b_mn, kk > 0 ? 1u : 0u);
+        mma_commit(bar(L::kPFree + b));
+      }
+      __syncwarp();
+      // S(i) staged, and Q S of tile i-1 (and O(i-1)) read out: Q S.
+      bool ok = wait_or_flag(bar(L::kSSmem + b), (i >> 1) & 1, err, kErrTimeoutMma);
+      if (ok && i >= 1) ok = wait_or_flag(bar(L::kOFree + (b ^ 1)), ((i - 1) >> 1) & 1, err, kErrTimeoutMma);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      if (lane == 0) {
+        if (has_state) {
+          const uint32_t sop = base + L::kS + b * kSOpBytes;
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            mma_bf16(tmem + kColQS, smem_desc_sw128(st + L::kQ + kk * 32, 16, 1024),
+                     smem_desc_sw128(sop + kk * 2048, kStateTileBytes, 1024), id_n64_b_mn, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(L::kOReady + b));
+        mma_commit(bar(L::kEmpty + s));
+        mbar_arrive(bar(L::kOReady + b));
+      }
+      __syncwarp();
+    }
+  } else if (warp < 3 + kConvWarps) {
+    // ------------------------------------------------------------ scaling and conversion
+    const int ct = tid - 3 * 32;
+    const int quarter = warp & 3;                 // TMEM lane quarter of this warp
+    const int half = (warp - 3) >> 2;             // 64-column half of P this warp converts
+    const int row = quarter * 32 + lane;          // tile row = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    // V' of a tile (`scale`): row r of `rows` times a^(last - r), zero past
+    // them.  For a tile of the run (tile >= 0) the infinite and NaN values
+    // of V then become 0 and the tile is marked (see add_nonfinite).
+    auto prepare_v = [&](int s, int rows, int last, float l2, bool scale, int tile) {
+      uint8_t* src = smem + L::kStage0 + s * kStageBytes + L::kV + ct * 16;
+      uint8_t* dst = smem + L::kVs + ct * 16;
+      uint32_t bad = 0;
+#pragma unroll 2
+      for (int w = 0; w < kTileRows * 8 / kConvThreads; ++w) {
+        const int r = (ct >> 3) + (kConvThreads / 8) * w;   // 16-byte piece ct + 256 w is of row r whatever the swizzle
+        const uint32_t at = kConvThreads * 16 * w;
+        const uint4 x4 = r < rows ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+        bad |= (nonfinite2(x[0]) | nonfinite2(x[1]) | nonfinite2(x[2]) | nonfinite2(x[3])) << w;
+        if (scale) {
+          // (rows past the tile: 0 times 1)
+          const float f = decay_pow_fast(l2, static_cast<float>(max(last - r, 0)));
+          uint4 part[kParts];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b2[kParts];
+            split3(mul_f32x2(f32x2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)), f32x2(f, f)), b2);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) reinterpret_cast<uint32_t*>(&part[p])[e] = b2[p];
+          }
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) *reinterpret_cast<uint4*>(dst + p * kRowTileBytes + at) = part[p];
+        }
+      }
+      if (bad != 0) {
+        for (int w = 0; w < kTileRows * 8 / kConvThreads; ++w)
+          if ((bad >> w) & 1)
+            repair_piece(src + kConvThreads * 16 * w, dst + kConvThreads * 16 * w,
+                         decay_pow_fast(l2, static_cast<float>(last - (ct >> 3) - (kConvThreads / 8) * w)), scale, tile >= 0);
+        if (tile >= 0) reinterpret_cast<int*>(smem + L::kBad)[tile % kBadSlots] = tile + 1;
+      }
+      fence_proxy_async_smem();
+    };
+    // Stage u's V is in shared memory and the V' buffer is free.
+    auto v_ready = [&](int u) -> bool {
+      bool ok = wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma);
+      if (ok && u >= 1) ok = wait_or_flag(bar(L::kVFree), (u - 1) & 1, err, kErrTimeoutMma);
+      return __all_sync(0xffffffffu, ok);
+    };
+    bool ok = true;
+    int u = 0;
+    for (int j = 0; j < n_p1 && ok; ++j) {
+      const SpanDesc sd = p1_of(j);
+      const float l2 = decay_log2(load_log_decay(prm.log_decay, sd.head));
+      for (int r = 0; r < sd.len; r += kTileRows, ++u) {
+        ok = v_ready(u);
+        if (!ok) break;
+        prepare_v(u % kStages, sd.len - r, min(sd.len - r, kTileRows) - 1, l2, true, -1);
+        mbar_arrive(bar(L::kVReady));
+      }
+    }
+    TileMask nxt = n > 0 ? load_mask(list) : TileMask{};
+    TileHead nxt_head = n > 0 ? load_head(list) : TileHead{};
+    for (int i = 0; i < n && ok; ++i, ++u) {
+      const TileMask r = nxt;
+      const int flags = nxt_head.flags;
+      const float l2 = decay_log2(load_log_decay(prm.log_decay, nxt_head.head));
+      if (i + 1 < n) {
+        nxt = load_mask(list + i + 1);
+        nxt_head = load_head(list + i + 1);
+      }
+      const int b = i & 1;
+      if (!v_ready(u)) break;
+      prepare_v(u % kStages, r.nrows, r.nrows - 1, l2, !(flags & kTileLast) || (flags & kTileFinalOut), i);
+      mbar_arrive(bar(L::kVReady));
+
+      int seg_start = 0;
+      if (r.nbound > 1) {
+        const int nb = r.nbound < kInlineBounds ? r.nbound : kInlineBounds;
+        for (int q = 1; q < nb; ++q) {
+          const int sb = inline_bound(r.inl, q);
+          if (sb <= row) seg_start = sb;
+        }
+        for (int q = kInlineBounds; q < r.nbound; ++q) {
+          const int sb = prm.bounds[r.bound0 + q];
+          if (sb <= row) seg_start = sb;
+        }
+      }
+      const int hi_col = row < r.nrows ? row : -1;   // last kept column of this row
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kPReady + b), (i >> 1) & 1, err, kErrTimeoutMma)))
+        break;
+      tc_fence_after_sync();
+      // The output warps read it once O(i) is ready.  The slot's last reader,
+      // O(i-4), is behind: P(i) was issued after P V of tile i-2 completed, and
+      // that was issued after Q S of tile i-3, which waits for O(i-4).
+      if (half == 0) smem[L::kSeg + (i % kSegSlots) * kTileRows + row] = static_cast<uint8_t>(seg_start);
+      const uint32_t colP = (b ? kColP1 : kColP0) + half * 64;
+      // Two 32-column chunks in turn; chunk q's bf16 pairs go to columns
+      // 16q .. 16q + 15 of the half, over scores already read.
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c0 = half * 64 + 32 * q;
+        uint32_t pk[16];
+        if (__all_sync(0xffffffffu, c0 > hi_col || c0 + 31 < seg_start)) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = 0u;
+        } else {
+          uint32_t r0[32];
+          tmem_ld_32cols(tmem + lane_base + colP + 32 * q, r0);
+          tmem_ld_wait();
+          // Kept columns of this row: c0 + lo .. c0 + hi.
+          const int lo = seg_start - c0, hi = hi_col - c0;
+          const bool all_kept = __all_sync(0xffffffffu, lo <= 0 && hi >= 31);
+          if (c0 == quarter * 32 && l2 < kSteepLog2) {
+            // On the diagonal of a steep head: each factor by itself.
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              r0[c] = __float_as_uint(__uint_as_float(r0[c]) * decay_pow_fast(l2, static_cast<float>(max(row - c0 - c, 0))));
+          } else {
+            // a^(row - column), from the last column down, two pairs at a time.
+            const float step = decay_pow_fast(l2, 4.f);
+            const uint64_t step2 = f32x2(step, step);
+            uint64_t w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              w[e] = f32x2(decay_pow_fast(l2, static_cast<float>(row - (c0 + 28 + 2 * e))),
+                           decay_pow_fast(l2, static_cast<float>(row - (c0 + 29 + 2 * e))));
+#pragma unroll
+            for (int c = 28; c >= 0; c -= 4)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x0, x1;
+                f32x2_split(mul_f32x2(f32x2(__uint_as_float(r0[c + 2 * e]), __uint_as_float(r0[c + 2 * e + 1])), w[e]), x0, x1);
+                r0[c + 2 * e] = __float_as_uint(x0);
+                r0[c + 2 * e + 1] = __float_as_uint(x1);
+                w[e] = mul_f32x2(w[e], step2);
+              }
+          }
+          if (!all_kept) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c < lo || c > hi) r0[c] = 0u;
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(__uint_as_float(r0[2 * c]), __uint_as_float(r0[2 * c + 1]));
+        }
+        tmem_st_16cols(tmem + lane_base + colP + 16 * q, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(bar(L::kPDone + b));
+    }
+  } else {
+    // ------------------------------------------------------------ state and output
+    const int quarter = warp & 3;                 // TMEM lane quarter of this warp
+    const int pi = (warp - kStateWarp0) >> 2;     // which of the quarter's two warps
+    const int row = quarter * 32 + lane;          // tile row = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    // State work: lanes 0..63 and their copy in lanes 64..127 hold state rows
+    // d = row & 63; the lower copy handles columns 0..31, the upper 32..63,
+    // and the quarter's two warps take 16 of those each.
+    const int d = row & 63, sh = row >> 6;
+    const int col0 = 32 * sh + 16 * pi;
+    const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
+    bool ok = true;
+
+    // log2 a and a^128 of the head of the tiles at hand.
+    int cur_head = -1;
+    float l2 = 0.f, ld = 0.f;
+    Factor f_tile{1.f, 0.f};
+    auto set_head = [&](int head) {
+      if (head == cur_head) return;
+      cur_head = head;
+      ld = load_log_decay(prm.log_decay, head);
+      l2 = decay_log2(ld);
+      f_tile = factor_of(ld, static_cast<float>(kTileRows));
+    };
+
+    // Phase 1: S <- a^n S + K^T V' over the tiles of each piece (as the run's
+    // tiles do: tile by tile the fp32 sums are rounded to nearest, which the
+    // tensor core's long sums are not), into its slot with its decay; then this
+    // CTA counts itself in the grid-wide counter.
+    float s_run[16];
+    {
+      int u = 0;
+      for (int j = 0; j < n_p1 && ok; ++j) {
+        const SpanDesc sd = p1_of(j);
+        set_head(sd.head);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
+        for (int r = 0; r < sd.len; r += kTileRows, ++u) {
+          const int b = u & 1;
+          ok = __all_sync(0xffffffffu, wait_or_flag(bar(L::kP1Ready + b), (u >> 1) & 1, err, kErrTimeoutMma));
+          if (!ok) break;
+          tc_fence_after_sync();
+          uint32_t r0[16];
+          tmem_ld_16cols(tmem + lane_base + (b ? kColQS : kColD) + col0, r0);
+          tmem_ld_wait();
+          tc_fence_before_sync();
+          mbar_arrive(bar(L::kP1Free + b));
+          const Factor f = sd.len - r >= kTileRows ? f_tile : factor_of(ld, static_cast<float>(sd.len - r));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s_run[e] = f.step(s_run[e], __uint_as_float(r0[e]));
+        }
+        if (!ok) break;
+        store_slice(prm.ws + static_cast<int64_t>(sd.slot) * kStateFloats + slice, s_run);
+        if (tid == kStateWarp0 * 32) {
+          const Factor f = factor_of(ld, static_cast<float>(sd.len));
+          prm.ws_factor[sd.slot] = make_float2(f.hi, f.lo);
+        }
+      }
+    }
+    if (n_p1 > 0) {
+      mbar_arrive(bar(L::kP1Done));
+      __threadfence();
+      named_barrier_sync(kNamedStateBar, kGroupThreads);
+      if (tid == kStateWarp0 * 32) atomicAdd(prm.counter, 1u);
+    }
+    // Wait (bounded) until every phase-1 CTA has counted itself, once, before
+    // the first read of another CTA's slots.
+    bool synced = prm.n_p1_ctas == 0;
+    auto grid_sync = [&]() {
+      if (synced) return;
+      synced = true;
+      if (tid == kStateWarp0 * 32) {
+        const unsigned long long t0 = global_timer_ns();
+        while (ld_acquire_gpu(prm.counter) < static_cast<unsigned>(prm.n_p1_ctas)) {
+          if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrTimeoutMma);
+            break;
+          }
+          __nanosleep(64);
+        }
+      }
+      named_barrier_sync(kNamedStateBar, kGroupThreads);
+    };
+
+    // The running state (row d, columns col0 ..) in fp32.  tag_run names the
+    // start state it holds while it is one, tag_op the one each S operand
+    // holds; -1: none (see k_span_output.cu).
+    int64_t tag_run = -1, tag_op0 = -1, tag_op1 = -1;
+    auto carry_tag = [&](int view, int head) -> int64_t {
+      return (static_cast<int64_t>(1) << 62) | (static_cast<int64_t>(view) << 16) | head;
+    };
+    auto start_tag = [&](const TileState& r) -> int64_t {
+      if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
+      if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
+      return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
+             ((static_cast<int64_t>(r.stateB) + 1) << 16) ^ (static_cast<int64_t>(r.b_n) << 10) ^
+             static_cast<int64_t>(r.head);
+    };
+    // Term A (a kept state, or the parent view-head's pieces) and term B (the
+    // segment's earlier pieces), in order, by Horner's rule into s_run:
+    // S <- a^rows S + piece.  Two states in flight; through S operand t & 1
+    // (coalesced reads, XOR-swizzled on the half-row) into the threads' slices.
+    auto sum_start = [&](int t, const TileState& r) {
+      const int g = tid - kStateWarp0 * 32;
+      const int na = r.a_n, total = r.a_n + r.b_n;
+      const bool kept = prm.a_rows > 1 || prm.final_out == nullptr;   // term A is a kept state
+      const float* pa =
+          na > 0 ? prm.stateA + (static_cast<int64_t>(r.stateA) * prm.a_rows + (kept ? r.head : 0)) * kStateFloats : nullptr;
+      const float* pb = r.b_n > 0 ? prm.ws + static_cast<int64_t>(r.stateB) * kStateFloats : nullptr;
+      auto src = [&](int k) -> const float4* {
+        return reinterpret_cast<const float4*>(k < na ? pa + static_cast<int64_t>(k) * kStateFloats
+                                                      : pb + static_cast<int64_t>(k - na) * kStateFloats) + g;
+      };
+      auto factor = [&](int k) -> Factor {
+        if (k == 0) return Factor{0.f, 0.f};   // nothing before it
+        const float2 f = __ldcg(prm.ws_factor + (k < na ? r.stateA + k : r.stateB + k - na));
+        return Factor{f.x, f.y};
+      };
+      float4 acc[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add4 = [](float4& x, const Factor f, const float4 y) {
+        x.x = f.step(x.x, y.x); x.y = f.step(x.y, y.y); x.z = f.step(x.z, y.z); x.w = f.step(x.w, y.w);
+      };
+      for (int k = 0; k < total; k += 2) {
+        const bool two = k + 1 < total;
+        const float4* p0 = src(k);
+        const float4* p1 = src(two ? k + 1 : k);
+        float4 x[4], y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = __ldcg(p0 + kGroupThreads * c);
+        const Factor f0 = factor(k);
+        if (two) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[c] = __ldcg(p1 + kGroupThreads * c);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) add4(acc[c], f0, x[c]);
+        if (two) {
+          const Factor f1 = factor(k + 1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) add4(acc[c], f1, y[c]);
+        }
+      }
+      float4* buf = reinterpret_cast<float4*>(smem + L::kS + (t & 1) * kSOpBytes);
+      if (t & 1) tag_op1 = -1; else tag_op0 = -1;
+      // The buffer holds two warps' O staging: their TMA stores must have read it.
+      if (lane == 0) bulk_wait_read_all();
+      named_barrier_sync(kNamedStateBar, kGroupThreads);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int f = g + kGroupThreads * c, hr = f >> 3;
+        buf[hr * 8 + ((f & 7) ^ ((hr >> 1) & 7))] = acc[c];
+      }
+      named_barrier_sync(kNamedStateBar, kGroupThreads);
+      const int hr = 2 * d + sh;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v4 = buf[hr * 8 + ((4 * pi + c) ^ ((hr >> 1) & 7))];
+        s_run[4 * c] = v4.x; s_run[4 * c + 1] = v4.y; s_run[4 * c + 2] = v4.z; s_run[4 * c + 3] = v4.w;
+      }
+      named_barrier_sync(kNamedStateBar, kGroupThreads);
+    };
+    // The running state becomes the start state of the piece starting at `r`.
+    auto start_piece = [&](int t, const TileState& r) {
+      if (!(r.flags & kTileHasInit)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
+        tag_run = -1;
+        return;
+      }
+      const int64_t tag = start_tag(r);
+      if (tag == tag_run) return;
+      tag_run = tag;
+      if (r.flags & kTileCarry) {
+        // (a long branch ran in between: this thread's own slice, as it wrote it)
+        const float4* p4 = reinterpret_cast<const float4*>(
+            prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 v4 = __ldcg(p4 + c);
+          s_run[4 * c] = v4.x; s_run[4 * c + 1] = v4.y; s_run[4 * c + 2] = v4.z; s_run[4 * c + 3] = v4.w;
+        }
+        return;
+      }
+      grid_sync();
+      sum_start(t, r);
+    };
+
+    // S(t) -> S operand t & 1, unless it holds that start state already.  The
+    // operand was last read by Q S of tile t-2, whose completion o_work(t-2) saw.
+    auto stage = [&](int t, const TileState& r) {
+      const int64_t tag = start_tag(r);
+      const bool uses = !(r.flags & kTileFirst) || (r.flags & kTileHasInit);
+      const int64_t held = (t & 1) ? tag_op1 : tag_op0;
+      if (uses && !(tag >= 0 && tag == held)) {
+        stage_state_slice(smem + L::kS + (t & 1) * kSOpBytes, d, col0, s_run);
+        if (t & 1) tag_op1 = tag; else tag_op0 = tag;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(L::kSSmem + (t & 1)));
+    };
+
+    // O(i) = P V + a^(i-s(i)+1) Q S -> global (rows of the tile only), through
+    // this warp's O staging when its 32 rows all lie in the tile (one TMA
+    // store), else row by row.
+    bool o_pending = false;   // this warp's last TMA store may still read its staging
+    auto o_work = [&](int i, const TileState& r, bool live) -> bool {
+      const int b = i & 1;
+      if (!live || !__all_sync(0xffffffffu, wait_or_flag(bar(L::kOReady + b), (i >> 1) & 1, err, kErrTimeoutMma)))
+        return false;
+      tc_fence_after_sync();
+      const uint32_t colO = b ? kColO1 : kColO0;
+      const bool whole = (quarter + 1) * 32 <= r.nrows;
+      const bool has_state = !(r.flags & kTileFirst) || (r.flags & kTileHasInit);
+      uint8_t* ob = smem + L::kS + (quarter >> 1) * kSOpBytes + kStateTileBytes + (quarter & 1) * kOQuarterBytes +
+                    pi * (kOQuarterBytes / 2);
+      if (whole && o_pending) {
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+      }
+      uint4* dst = reinterpret_cast<uint4*>(
+          prm.out + ((static_cast<int64_t>(r.row0) + row) * H + r.head) * kHeadDim + 32 * pi);
+      const bool store = row < r.nrows;
+      const int seg_start = smem[L::kSeg + (i % kSegSlots) * kTileRows + row];
+      const bool bad = reinterpret_cast<const int*>(smem + L::kBad)[i % kBadSlots] == i + 1;
+      const float f = decay_pow_fast(l2, static_cast<float>(row - seg_start + 1));
+      uint32_t pk[16];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t r0[16];
+        tmem_ld_16cols(tmem + lane_base + colO + 32 * pi + 16 * hf, r0);
+        if (has_state) {
+          uint32_t r1[16];
+          tmem_ld_16cols(tmem + lane_base + kColQS + 32 * pi + 16 * hf, r1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r0[e] = __float_as_uint(fmaf(f, __uint_as_float(r1[e]), __uint_as_float(r0[e])));
+        } else {
+          tmem_ld_wait();
+        }
+        if (bad) {
+          float y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(r0[e]);
+          if (store) add_nonfinite(y, prm, r.row0, row, seg_start, r.head, 32 * pi + 16 * hf, l2);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r0[e] = __float_as_uint(y[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          pk[8 * hf + e] = pack_bf16x2(__uint_as_float(r0[2 * e]), __uint_as_float(r0[2 * e + 1]));
+      }
+      tc_fence_before_sync();
+      mbar_arrive(bar(L::kOFree + b));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v4 = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        if (whole)
+          *reinterpret_cast<uint4*>(ob + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v4;
+        else if (store)
+          dst[c] = v4;
+      }
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tm_o, smem_addr(ob), 32 * pi, r.row0 + quarter * 32, r.head);
+          bulk_commit_group();
+        }
+        o_pending = true;
+      }
+      return true;
+    };
+
+    // S <- a^n S + dS of tile i; at the last tile of a view-head that is the
+    // view's final state: write it out.  (Without `live`, or when the wait
+    // runs out, nothing is read or written, but the tags change as they would
+    // have: they decide which named barriers the group reaches.)
+    auto take_ds = [&](int i, const TileState& r, bool live) -> bool {
+      const bool good =
+          live && __all_sync(0xffffffffu, wait_or_flag(bar(L::kDReady), i & 1, err, kErrTimeoutMma));
+      if (good) tc_fence_after_sync();
+      if (!(r.flags & kTileLast) || (r.flags & kTileFinalOut)) {
+        if (good) {
+          const Factor f = r.nrows == kTileRows ? f_tile : factor_of(ld, static_cast<float>(r.nrows));
+          uint32_t r0[16];
+          tmem_ld_16cols(tmem + lane_base + kColD + col0, r0);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s_run[e] = f.step(s_run[e], __uint_as_float(r0[e]));
+        }
+        tag_run = -1;
+      }
+      if (good) {
+        tc_fence_before_sync();
+        mbar_arrive(bar(L::kDFree));
+      }
+      if (r.flags & kTileFinalOut) {
+        if (good)
+          store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
+        tag_run = carry_tag(r.final_idx, r.head);
+      }
+      return good;
+    };
+
+    // The group's named barriers (in the start-state sum and the grid-wide
+    // wait) are reached by all warps alike: where they fall depends on the
+    // tiles and the start-state tags only.  A warp whose bounded wait ran out
+    // goes on through the loop without waiting, reading or writing results.
+    if (n > 0) {
+      TileState cur = load_state(list);
+      TileState nxt = n > 1 ? load_state(list + 1) : TileState{};
+      start_piece(0, cur);
+      stage(0, cur);
+      for (int i = 0; i < n; ++i) {
+        set_head(cur.head);
+        // S(i+1) first: the O issuer needs it right after P V of tile i+1.
+        if (i + 1 < n || (cur.flags & kTileFinalOut)) ok = take_ds(i, cur, ok);
+        if (i + 1 < n) {
+          if (cur.flags & kTileLast) start_piece(i + 1, nxt);
+          stage(i + 1, nxt);
+        }
+        ok = o_work(i, cur, ok);
+        cur = nxt;
+        if (i + 2 < n) nxt = load_state(list + i + 2);
+      }
+    }
+    if (lane == 0) bulk_wait_all();   // the last O stores have completed
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace
+
+cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                              const CUtensorMap& tm_o, const SpanDecayArgs& a, cudaStream_t stream) {
+  if (a.grid <= 0) return cudaSuccess;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = set_smem_limit_once(span_decay_kernel, DecaySmem::kRequest, done);
+  if (e != cudaSuccess) return e;
+  DecayParams p{};
+  p.heads = a.heads;
+  p.work = a.work;
+  p.bounds = a.bounds;
+  p.log_decay = a.log_decay;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k = static_cast<const __nv_bfloat16*>(a.k);
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.stateA = a.stateA;
+  p.ws = a.ws;
+  p.ws_factor = a.ws_factor;
+  p.final_out = a.final_out;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.err = a.err;
+  p.p1 = a.p1;
+  p.counter = a.counter;
+  p.a_rows = a.a_rows;
+  p.H = a.H;
+  p.n_p1_ctas = a.n_p1_ctas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = DecaySmem::kRequest;
+  cfg.stream = stream;
+  // CTAs wait on one another when some have phase-1 pieces: then all of them
+  // must be resident at once.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.n_p1_ctas > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, span_decay_kernel, tm_q, tm_k, tm_v, tm_o, p);
+}
+
+}  // namespace spanla

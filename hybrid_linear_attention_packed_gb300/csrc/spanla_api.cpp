@@ -139,11 +139,13 @@ span_la_status device_state(DeviceState** out) {
 // ------------------------------------------------------------------ profiling
 constexpr int kKernelSplit = 0, kKernelChunk = 1, kKernelScan = 2, kKernelTile = 3,
               kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6, kKernelRecurState = 7,
-              kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11;
+              kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11,
+              kKernelSpanDecay = 12;
 const char* const kKernelNames[SPAN_LA_NUM_KERNELS] = {"split_f32", "chunk_state", "segmented_scan",
                                                        "tile_output", "span_state", "span_output",
                                                        "softmax_attn", "recur_state", "recur_scan",
-                                                       "recur_output", "decay_step", "qk_norm_rope"};
+                                                       "recur_output", "decay_step", "qk_norm_rope",
+                                                       "span_decay"};
 
 std::atomic<int64_t> g_launches[SPAN_LA_NUM_KERNELS];
 std::atomic<bool> g_profiling{false};
@@ -1632,6 +1634,50 @@ span_la_status enqueue_recur(const DescBlock& desc, const uint8_t* block, float*
   return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "decayed pass launch");
 }
 
+// The one launch of a decayed bf16 pass.  stateA: kept states (final_out
+// NULL), else term A are workspace slots.
+span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, float* states, float2* factors,
+                                  unsigned* counter, const void* q, const void* k, const void* v,
+                                  const span_la_dims& dims, const float* log_decay, const float* kept,
+                                  float* final_out, void* out, unsigned* err, cudaStream_t stream) {
+  const int H = dims.num_heads;
+  cudaError_t e = cudaSuccess;
+  for (size_t j = 0; j < desc.empty_views.size() && e == cudaSuccess; ++j)
+    e = cudaMemsetAsync(final_out + static_cast<int64_t>(desc.empty_views[j]) * H * kStateFloats, 0,
+                        static_cast<size_t>(H) * kStateFloats * sizeof(float), stream);
+  if (e == cudaSuccess && desc.n_p1_ctas > 0) e = cudaMemsetAsync(counter, 0, sizeof(unsigned), stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(pass counter)");
+  if (desc.n_out_tiles == 0) return SPAN_LA_OK;
+  CUtensorMap tm_q{}, tm_k{}, tm_v{}, tm_o{};
+  span_la_status st = encode_map(&tm_q, q, dims.total_rows, H, kTileBoxRows, 1);
+  if (st == SPAN_LA_OK) st = encode_map(&tm_k, k, dims.total_rows, H, kTileBoxRows, 1);
+  if (st == SPAN_LA_OK) st = encode_map(&tm_v, v, dims.total_rows, H, kTileBoxRows, 1);
+  if (st == SPAN_LA_OK) st = encode_map(&tm_o, out, dims.total_rows, H, kOutStoreRows, 1, 32);
+  if (st != SPAN_LA_OK) return st;
+  SpanDecayArgs a;
+  a.heads = reinterpret_cast<const CtaHead*>(block + desc.off_h);
+  a.work = reinterpret_cast<const WorkTile*>(block + desc.off_b);
+  a.grid = desc.grid;
+  a.bounds = block + desc.off_bounds;
+  a.log_decay = log_decay;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.stateA = kept != nullptr ? kept : states;
+  a.a_rows = kept != nullptr ? H : 1;
+  a.ws = states;
+  a.ws_factor = factors;
+  a.final_out = final_out;
+  a.out = out;
+  a.H = H;
+  a.err = err;
+  a.p1 = reinterpret_cast<const SpanDesc*>(block + desc.off_a);
+  a.counter = counter;
+  a.n_p1_ctas = desc.n_p1_ctas;
+  e = counted_launch(kKernelSpanDecay, stream, [&] { return launch_span_decay(tm_q, tm_k, tm_v, tm_o, a, stream); });
+  return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "decayed pass launch");
+}
+
 // Descriptors (cached, or in the call's workspace while the stream is being
 // captured), workspace and launches of a decayed pass (kept NULL) or of
 // branches from kept states (final_out NULL).
@@ -1658,10 +1704,13 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
     desc = &local;
   }
   if (desc->n_out_tiles == 0 && desc->n_scan == 0 && desc->empty_views.empty()) return SPAN_LA_OK;
-  // Workspace: the descriptors when they are not cached, the state slots.
+  // Workspace: the descriptors when they are not cached, the state slots,
+  // their pieces' decays and the counter (bf16).
   const size_t slots = static_cast<size_t>(desc->state_slots);
   const size_t off_states = use_cache ? 0 : align256(desc->host.size());
-  const size_t total = std::max<size_t>(off_states + slots * kStateFloats * sizeof(float), 256);
+  const size_t off_factors = off_states + slots * kStateFloats * sizeof(float);
+  const size_t off_counter = off_factors + align256(slots * sizeof(float2));
+  const size_t total = off_counter + 256;
   uint8_t* ws = nullptr;
   if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", total);
   e = cudaMallocAsync(reinterpret_cast<void**>(&ws), total, stream);
@@ -1673,8 +1722,12 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
   }
   float* states = reinterpret_cast<float*>(ws + off_states);
   if (st == SPAN_LA_OK)
-    st = enqueue_recur(*desc, block, states, q, k, v, dims, log_decay, kept != nullptr ? kept : final_out, final_out, out,
-                       stream);
+    st = dims.dtype == SPAN_LA_BF16
+             ? enqueue_span_decay(*desc, block, states, reinterpret_cast<float2*>(ws + off_factors),
+                                  reinterpret_cast<unsigned*>(ws + off_counter), q, k, v, dims, log_decay, kept,
+                                  final_out, out, dev->err, stream)
+             : enqueue_recur(*desc, block, states, q, k, v, dims, log_decay, kept != nullptr ? kept : final_out,
+                             final_out, out, stream);
   st = finish_read(entry, stream, st);
   const cudaError_t ef = cudaFreeAsync(ws, stream);
   if (st == SPAN_LA_OK && ef != cudaSuccess) st = cuda_fail(ef, "cudaFreeAsync");
@@ -1685,6 +1738,8 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
 DescBlock make_decay_desc(const int32_t* view_cu, int32_t V, const int32_t* branch_cu, int32_t B, const int32_t* parent,
                           const span_la_dims& dims, int num_sms) {
   const int H = dims.num_heads;
+  if (dims.dtype == SPAN_LA_BF16)
+    return make_desc(make_span_plan(view_cu, V, branch_cu, B, parent, H, num_sms, true), H);
   return make_recur_desc(make_recur_plan(view_cu, V, branch_cu, B, parent, H, num_sms), H);
 }
 
@@ -2211,8 +2266,13 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
     cudaGetDevice(&device);
-    const std::vector<int32_t> key = plan_key(device, dims.dtype, dims.num_heads, 5, dev->num_sms, view_cu_seqlens,
-                                              num_views, branch_cu_seqlens, num_branches, branch_parent);
+    // (bf16: the key of span_la_pass's one-launch plan, which is the same plan)
+    const std::vector<int32_t> key =
+        dims.dtype == SPAN_LA_BF16
+            ? pass_key(device, dims, dev->num_sms, true, view_cu_seqlens, num_views, branch_cu_seqlens, num_branches,
+                       branch_parent)
+            : plan_key(device, dims.dtype, dims.num_heads, 5, dev->num_sms, view_cu_seqlens, num_views,
+                       branch_cu_seqlens, num_branches, branch_parent);
     auto build = [&] {
       return make_decay_desc(view_cu_seqlens, num_views, branch_cu_seqlens, num_branches, branch_parent, dims, dev->num_sms);
     };

@@ -255,6 +255,32 @@ cudaError_t launch_tile_output(bool split, const CUtensorMap* tm_q, const CUtens
                                const uint8_t* bounds, const float* stateA, const float* stateB,
                                void* out, int H, unsigned* err, cudaStream_t stream, bool pdl);
 
+// Decayed passes of bf16 inputs (k_span_decay.cu): the one-launch structure
+// of span_output, from a plan of the same kind.
+struct SpanDecayArgs {
+  const CtaHead* heads = nullptr;
+  const WorkTile* work = nullptr;
+  int grid = 0;
+  const uint8_t* bounds = nullptr;
+  const float* log_decay = nullptr;
+  const void* q = nullptr;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  const float* stateA = nullptr;   // term A: kept states [n][H][64][64] (a_rows = H, final_out NULL), or the slots
+  int a_rows = 1;
+  float* ws = nullptr;             // slots
+  float2* ws_factor = nullptr;     // one per slot
+  float* final_out = nullptr;
+  void* out = nullptr;
+  int H = 0;
+  unsigned* err = nullptr;
+  const SpanDesc* p1 = nullptr;
+  unsigned* counter = nullptr;
+  int n_p1_ctas = 0;
+};
+cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                              const CUtensorMap& tm_o, const SpanDecayArgs& a, cudaStream_t stream);
+
 // Decayed passes by the recurrence (CUDA cores).  Every segment (view or
 // branch) is cut into pieces of `piece` rows (the last one shorter).
 struct RecurUnit {

@@ -37,7 +37,7 @@ EXPORTED = ("span_la_pass", "span_la_branches_from_state", "span_la_check",
             "span_la_selftest_wait_timeout_noalloc", "span_la_pass_variant",
             "span_la_plan_prepare", "span_la_decay_pass", "span_la_decay_branches_from_state",
             "span_la_decay_step", "span_la_qk_norm_rope")
-NUM_KERNELS = 12
+NUM_KERNELS = 13
 
 
 class SpanLAError(RuntimeError):

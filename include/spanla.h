@@ -371,7 +371,7 @@ span_la_status span_la_plan_stats(const int32_t *view_cu_seqlens, int32_t num_vi
  *   0 split_f32, 1 chunk_state, 3 tile_output (fp32 inputs),
  *   2 segmented_scan (both), 4 span_state, 5 span_output (bf16 inputs),
  *   6 softmax_attn (span_la_softmax_pass), 7 recur_state, 8 recur_scan,
- *   9 recur_output (decayed passes),
+ *   9 recur_output (decayed passes, fp32), 12 span_decay (bf16),
  *   10 decay_step, 11 qk_norm_rope.
  * Launches of every kernel are always counted.  While profiling is enabled,
  * every launch is also bracketed by two CUDA events recorded on the call's
@@ -379,7 +379,7 @@ span_la_status span_la_plan_stats(const int32_t *view_cu_seqlens, int32_t num_vi
  * events and adds their elapsed times up.  Enabling adds two event records per
  * launch and nothing else to the work on the stream.
  */
-#define SPAN_LA_NUM_KERNELS 12
+#define SPAN_LA_NUM_KERNELS 13
 
 /* Turn event timing on (non-zero) or off. */
 span_la_status span_la_profile_enable(int32_t enable);
