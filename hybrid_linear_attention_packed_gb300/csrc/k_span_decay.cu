@@ -18,7 +18,7 @@
 //            before (running products of a^4, at most eight factors deep,
 //            from a power at the block's last column); in the 32 x 32 blocks on
 //            the diagonal of a head with a < 1/16, where those would start above
-//            1 by more than fp32 holds, by 2^((i-j) log2 a) for each element.
+//            1 by more than fp32 holds, products of a from the diagonal down.
 //   Q S      a row factor, which no rounding to bf16 should see: Q S has its own
 //            accumulator, and the output warps add a^(i-s(i)+1) times it to P V.
 //   K^T V    by scaling V: V' = a^(n-1-j) v_j, fp32, as a sum of three bf16
@@ -100,7 +100,8 @@ struct DecaySmem {
   static constexpr uint32_t kP1 = kCoord + 8 * kCoordSlots;
   static constexpr uint32_t kSeg = kP1 + sizeof(SpanDesc) * kP1Slots;   // first row of each row's segment
   static constexpr uint32_t kBad = kSeg + kSegSlots * kTileRows;        // 1 + the tile whose V held an inf or NaN
-  static constexpr uint32_t kBytes = kBad + 4 * kBadSlots;
+  static constexpr uint32_t kDecay = kBad + 4 * kBadSlots;              // a head's decay, one per state warp
+  static constexpr uint32_t kBytes = kDecay + 16 * (kGroupThreads / 32);
   static constexpr uint32_t kRequest = kBytes + 1024;
 };
 static_assert(DecaySmem::kRequest <= 227 * 1024, "shared memory budget");
@@ -137,23 +138,29 @@ __device__ __noinline__ Factor factor_of(float ld, float n) { return decay_facto
 // A tile's P V ran without the infinite and NaN values of V (they stand as 0
 // in shared memory: 0 times one of them, in a masked place, would be NaN).
 // Their terms a^(i-j) (q_i . k_j) v_jc, for the rows that see them: added to
-// 16 columns of row i = `row` of the tile.
-__device__ __noinline__ void add_nonfinite(float* y, const DecayParams& prm, int64_t row0, int row, int seg_start, int head,
-                                           int col, float l2) {
+// 32 columns of row i = `row` of the tile where the output has them already
+// (whatever it holds there, one such term makes it infinite or NaN).
+__device__ __noinline__ void add_nonfinite(const DecayParams& prm, int64_t row0, int row, int seg_start, int head, int col,
+                                           float l2) {
   const int64_t stride = static_cast<int64_t>(prm.H) * kHeadDim;
   const int64_t at = row0 * stride + static_cast<int64_t>(head) * kHeadDim;
+  uint32_t* out = reinterpret_cast<uint32_t*>(prm.out + at + row * stride + col);
   for (int j = seg_start; j <= row; ++j) {
     const uint32_t* v = reinterpret_cast<const uint32_t*>(prm.v + at + j * stride + col);
     bool any = false;
-    for (int c = 0; c < 8; ++c) any |= nonfinite2(v[c]);
+    for (int c = 0; c < 16; ++c) any |= nonfinite2(v[c]);
     if (!any) continue;
     float score = 0.f;
     for (int e = 0; e < kHeadDim; ++e)
       score = fmaf(__bfloat162float(prm.q[at + row * stride + e]), __bfloat162float(prm.k[at + j * stride + e]), score);
     score *= decay_pow(l2, static_cast<float>(row - j));
-    for (int c = 0; c < 8; ++c) {
-      if (nonfinite_lo(v[c])) y[2 * c] += score * __uint_as_float(v[c] << 16);
-      if (nonfinite_hi(v[c])) y[2 * c + 1] += score * __uint_as_float(v[c] & 0xffff0000u);
+    for (int c = 0; c < 16; ++c) {
+      if (!nonfinite2(v[c])) continue;
+      const uint32_t o = __ldcg(out + c);
+      float lo = __uint_as_float(o << 16), hi = __uint_as_float(o & 0xffff0000u);
+      if (nonfinite_lo(v[c])) lo += score * __uint_as_float(v[c] << 16);
+      if (nonfinite_hi(v[c])) hi += score * __uint_as_float(v[c] & 0xffff0000u);
+      out[c] = pack_bf16x2(lo, hi);
     }
   }
 }
@@ -233,6 +240,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mbar_init(bar(L::kVFree), 1);
     mbar_init(bar(L::kP1Done), kGroupThreads);
     for (int s = 0; s < kBadSlots; ++s) reinterpret_cast<int*>(smem + L::kBad)[s] = 0;
+    for (int w = 0; w < kGroupThreads / 32; ++w) reinterpret_cast<float4*>(smem + L::kDecay)[w].w = __int_as_float(-1);
     fence_mbar_init();
     const int4 f0 = __ldg(hd + 2), f1 = __ldg(hd + 3);
     const int fr[2 * kFirstLoads] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
@@ -558,10 +566,14 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const int lo = seg_start - c0, hi = hi_col - c0;
           const bool all_kept = __all_sync(0xffffffffu, lo <= 0 && hi >= 31);
           if (c0 == quarter * 32 && l2 < kSteepLog2) {
-            // On the diagonal of a steep head: each factor by itself.
+            // On the diagonal of a steep head: from the row's own column down.
+            const float a1 = decay_pow_fast(l2, 1.f);
+            float w = 1.f;
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              r0[c] = __float_as_uint(__uint_as_float(r0[c]) * decay_pow_fast(l2, static_cast<float>(max(row - c0 - c, 0))));
+            for (int c = 31; c >= 0; --c) {
+              w = c < lane ? w * a1 : 1.f;
+              r0[c] = __float_as_uint(__uint_as_float(r0[c]) * w);
+            }
           } else {
             // a^(row - column), from the last column down, two pairs at a time.
             const float step = decay_pow_fast(l2, 4.f);
@@ -610,16 +622,28 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
     bool ok = true;
 
-    // log2 a and a^128 of the head of the tiles at hand.
-    int cur_head = -1;
-    float l2 = 0.f, ld = 0.f;
-    Factor f_tile{1.f, 0.f};
-    auto set_head = [&](int head) {
-      if (head == cur_head) return;
-      cur_head = head;
-      ld = load_log_decay(prm.log_decay, head);
-      l2 = decay_log2(ld);
-      f_tile = factor_of(ld, static_cast<float>(kTileRows));
+    // (log2 a, a^128 as a Factor, the head) of the tiles at hand, kept in
+    // shared memory by each warp for itself: registers are short here.
+    float4* decay_of = reinterpret_cast<float4*>(smem + L::kDecay) + (warp - kStateWarp0);
+    auto head_decay = [&](int head) -> float4 {
+      float4 x = *decay_of;
+      if (__float_as_int(x.w) != head) {
+        const float ld = load_log_decay(prm.log_decay, head);
+        const Factor f = factor_of(ld, static_cast<float>(kTileRows));
+        x = make_float4(decay_log2(ld), f.hi, f.lo, __int_as_float(head));
+        __syncwarp();
+        if (lane == 0) *decay_of = x;
+        __syncwarp();
+      }
+      return x;
+    };
+    // a^n of a tile of n rows.
+    auto tile_factor = [&](int head, int rows) -> Factor {
+      if (rows >= kTileRows) {
+        const float4 x = head_decay(head);
+        return Factor{x.y, x.z};
+      }
+      return factor_of(load_log_decay(prm.log_decay, head), static_cast<float>(rows));
     };
 
     // Phase 1: S <- a^n S + K^T V' over the tiles of each piece (as the run's
@@ -631,7 +655,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       int u = 0;
       for (int j = 0; j < n_p1 && ok; ++j) {
         const SpanDesc sd = p1_of(j);
-        set_head(sd.head);
 #pragma unroll
         for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
         for (int r = 0; r < sd.len; r += kTileRows, ++u) {
@@ -644,14 +667,14 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           tmem_ld_wait();
           tc_fence_before_sync();
           mbar_arrive(bar(L::kP1Free + b));
-          const Factor f = sd.len - r >= kTileRows ? f_tile : factor_of(ld, static_cast<float>(sd.len - r));
+          const Factor f = tile_factor(sd.head, sd.len - r);
 #pragma unroll
           for (int e = 0; e < 16; ++e) s_run[e] = f.step(s_run[e], __uint_as_float(r0[e]));
         }
         if (!ok) break;
         store_slice(prm.ws + static_cast<int64_t>(sd.slot) * kStateFloats + slice, s_run);
         if (tid == kStateWarp0 * 32) {
-          const Factor f = factor_of(ld, static_cast<float>(sd.len));
+          const Factor f = factor_of(load_log_decay(prm.log_decay, sd.head), static_cast<float>(sd.len));
           prm.ws_factor[sd.slot] = make_float2(f.hi, f.lo);
         }
       }
@@ -823,6 +846,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const bool store = row < r.nrows;
       const int seg_start = smem[L::kSeg + (i % kSegSlots) * kTileRows + row];
       const bool bad = reinterpret_cast<const int*>(smem + L::kBad)[i % kBadSlots] == i + 1;
+      const float l2 = head_decay(r.head).x;
       const float f = decay_pow_fast(l2, static_cast<float>(row - seg_start + 1));
       uint32_t pk[16];
 #pragma unroll
@@ -837,14 +861,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int e = 0; e < 16; ++e) r0[e] = __float_as_uint(fmaf(f, __uint_as_float(r1[e]), __uint_as_float(r0[e])));
         } else {
           tmem_ld_wait();
-        }
-        if (bad) {
-          float y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(r0[e]);
-          if (store) add_nonfinite(y, prm, r.row0, row, seg_start, r.head, 32 * pi + 16 * hf, l2);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) r0[e] = __float_as_uint(y[e]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -869,6 +885,11 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         o_pending = true;
       }
+      if (bad) {
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+        if (store) add_nonfinite(prm, r.row0, row, seg_start, r.head, 32 * pi, l2);
+      }
       return true;
     };
 
@@ -882,7 +903,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (good) tc_fence_after_sync();
       if (!(r.flags & kTileLast) || (r.flags & kTileFinalOut)) {
         if (good) {
-          const Factor f = r.nrows == kTileRows ? f_tile : factor_of(ld, static_cast<float>(r.nrows));
+          const Factor f = tile_factor(r.head, r.nrows);
           uint32_t r0[16];
           tmem_ld_16cols(tmem + lane_base + kColD + col0, r0);
           tmem_ld_wait();
@@ -913,7 +934,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       start_piece(0, cur);
       stage(0, cur);
       for (int i = 0; i < n; ++i) {
-        set_head(cur.head);
         // S(i+1) first: the O issuer needs it right after P V of tile i+1.
         if (i + 1 < n || (cur.flags & kTileFinalOut)) ok = take_ds(i, cur, ok);
         if (i + 1 < n) {
