@@ -1,4 +1,5 @@
-"""Build ``libspanla.so`` in-tree with nvcc for sm_103a.
+"""Build ``libspanla.so`` in-tree with nvcc for sm_103a, and the binding's
+extension module ``_fastcall.so`` (csrc/py) with the host compiler.
 
 Each translation unit compiles in parallel into ``_build/``; the objects are
 linked into ``hybrid_linear_attention_packed_gb300/libspanla.so`` against the
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspanla.so")
+EXT_SRC = os.path.join(CSRC, "py", "fastcall.cpp")
+EXT = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -42,10 +45,28 @@ def _headers():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in _sources() + _headers() + [__file__])
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    return any(os.path.getmtime(p) > t for p in _sources() + _headers() + [EXT_SRC, __file__])
+
+
+def _compile_ext() -> str:
+    """The binding's extension module, against the headers of the torch that is installed."""
+    import sysconfig
+
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = EXT + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", os.path.join(tdir, "include"), "-I", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda_home, "include"), EXT_SRC, "-o", tmp,
+           "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed on %s:\n%s%s" % (cmd[0], EXT_SRC, r.stdout, r.stderr))
+    return tmp
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -67,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(compile_one, _sources()))
+        ext_tmp = ext.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [
         "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
@@ -75,6 +98,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    os.replace(ext_tmp, EXT)
     return LIB
 
 

@@ -2377,7 +2377,7 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
       if (!std::isfinite(inv_freq[i])) return fail(SPAN_LA_ERR_INVALID, "inv_freq[%d] is not finite", i);
       const double turns = inv_freq[i] / 6.283185307179586;
       const double part = turns - std::floor(turns);   // in [0, 1]: 1 when the fraction rounds up
-      a.freq[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0;
+      a.freq[i] = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
     }
     const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4;
     const int64_t wsz = weight_dtype == SPAN_LA_BF16 ? 2 : 4;

@@ -59,6 +59,7 @@ class QkSide(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_fast = None   # csrc/py/fastcall.cpp bound to _lib: the usual calls without the interpreter's share
 
 
 def load_library(path: Optional[str] = None):
@@ -155,7 +156,17 @@ def load_library(path: Optional[str] = None):
         lib.span_la_cache_stats.restype = ctypes.c_int
         if path is None:
             _lib = lib
+            _bind_fast(lib)
         return lib
+
+
+def _bind_fast(lib) -> None:
+    global _fast
+    from . import _fastcall
+    _fastcall.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+                     for f in (lib.span_la_decay_pass, lib.span_la_decay_branches_from_state, lib.span_la_decay_step,
+                               lib.span_la_qk_norm_rope)])
+    _fast = _fastcall
 
 
 def _raise(lib, status: int, where: str):
@@ -385,28 +396,46 @@ def span_la_softmax_branches_from_kv(view_k: torch.Tensor, view_v: torch.Tensor,
     return out
 
 
-def _on_current_device(**tensors) -> None:
+def _current_device() -> int:
+    return _raw_device() if _raw_device is not None else torch.cuda.current_device()
+
+
+def _on_device(dev: int, name: str, t: torch.Tensor) -> None:
     """The library runs on the current device: its tensors have to be there."""
-    dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError("%s must be on the current CUDA device (%d), got %s" % (name, dev, t.device))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device (%d), got %s" % (name, dev, t.device))
 
 
-def _decay_args(log_decay, q, k, v, out, optional: bool = False) -> torch.Tensor:
-    """Checks log_decay and out of a decayed call; returns out (allocated when None)."""
-    if log_decay is None:
-        if not optional:
+def _decay_args(q, k, v, log_decay, out) -> Tuple[Dims, torch.Tensor, int]:
+    """What the decayed calls check alike: q, k, v (as _dims_of), log_decay (may be None here) and out (allocated when
+    None).  Returns the dims, out and the current device.  The usual case costs one look at each attribute."""
+    dims = _dims_of(q, k, v)
+    dev = _current_device()
+    if q.get_device() != dev or k.get_device() != dev or v.get_device() != dev:
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _on_device(dev, name, t)
+    if log_decay is not None:
+        sh = log_decay.shape
+        if (log_decay.dtype != torch.float32 or not log_decay.is_contiguous() or len(sh) != 1 or sh[0] != dims.num_heads
+                or not log_decay.is_cuda):
             raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
-    elif (log_decay.dtype != torch.float32 or not log_decay.is_cuda or not log_decay.is_contiguous()
-          or log_decay.shape != (q.shape[1],)):
-        raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
+        _on_device(dev, "log_decay", log_decay)
     if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
+        return dims, torch.empty_like(q), dev
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
-    _on_current_device(q=q, k=k, v=v, log_decay=log_decay, out=out)
-    return out
+    _on_device(dev, "out", out)
+    return dims, out, dev
+
+
+def _check_states(name: str, x: torch.Tensor, H: int, dev: int) -> int:
+    """x as contiguous fp32 CUDA [n, H, 64, 64] on the current device; returns n."""
+    sh = x.shape
+    if (len(sh) != 4 or sh[1] != H or sh[2] != 64 or sh[3] != 64 or x.dtype != torch.float32 or not x.is_contiguous()
+            or not x.is_cuda):
+        raise ValueError("%s must be contiguous fp32 CUDA [n, H, 64, 64]" % name)
+    _on_device(dev, name, x)
+    return sh[0]
 
 
 def span_la_decay_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -420,22 +449,27 @@ def span_la_decay_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
 
     Returns ``(out [T,H,64], view_state_out [V,H,64,64] fp32)``.
     """
-    lib = load_library()
-    dims = _dims_of(q, k, v)
+    if _fast is not None:   # (None: an argument that the code below takes or refuses)
+        r = _fast.decay_pass(q, k, v, log_decay, view_cu_seqlens, branch_cu_seqlens, branch_parent, out, view_state_out,
+                             stream)
+        if r is not None:
+            if type(r) is int:
+                _raise(_lib, r, "span_la_decay_pass")
+            return r
+    lib = _lib or load_library()
+    if log_decay is None:
+        raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
+    dims, out, dev = _decay_args(q, k, v, log_decay, out)
     vcu, bcu, par = _i32(view_cu_seqlens), _i32(branch_cu_seqlens), _i32(branch_parent)
     V = max(len(vcu) - 1, 0)
     B = max(len(bcu) - 1, 0)
     if par.size != B:
         raise ValueError("one parent per branch")
-    out = _decay_args(log_decay, q, k, v, out)
-    H = q.shape[1]
+    H = dims.num_heads
     if view_state_out is None:
         view_state_out = torch.empty((V, H, 64, 64), dtype=torch.float32, device=q.device)
-    elif (view_state_out.dtype != torch.float32 or not view_state_out.is_contiguous()
-          or not view_state_out.is_cuda or view_state_out.numel() < V * H * 4096):
-        raise ValueError("view_state_out must be a contiguous fp32 CUDA tensor [V, H, 64, 64]")
-    else:
-        _on_current_device(view_state_out=view_state_out)
+    elif _check_states("view_state_out", view_state_out, H, dev) < V:
+        raise ValueError("view_state_out must hold %d states" % V)
     st = lib.span_la_decay_pass(q.data_ptr(), k.data_ptr(), v.data_ptr(), dims, log_decay.data_ptr(), _iptr(vcu), V,
                                 _iptr(bcu), B, _iptr(par), out.data_ptr(), view_state_out.data_ptr(),
                                 _stream_handle(stream))
@@ -449,19 +483,22 @@ def span_la_decay_branches_from_state(cached_state: torch.Tensor, q: torch.Tenso
                                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Branches of a decayed pass from kept view states
     (``span_la_decay_branches_from_state``)."""
-    lib = load_library()
-    dims = _dims_of(q, k, v)
+    if _fast is not None:
+        r = _fast.decay_fork(cached_state, q, k, v, log_decay, branch_cu_seqlens, branch_parent, out, stream)
+        if r is not None:
+            if type(r) is int:
+                _raise(_lib, r, "span_la_decay_branches_from_state")
+            return r
+    lib = _lib or load_library()
+    if log_decay is None:
+        raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
+    dims, out, dev = _decay_args(q, k, v, log_decay, out)
+    n = _check_states("cached_state", cached_state, dims.num_heads, dev)
     bcu, par = _i32(branch_cu_seqlens), _i32(branch_parent)
     B = max(len(bcu) - 1, 0)
     if par.size != B:
         raise ValueError("one parent per branch")
-    if (cached_state.dtype != torch.float32 or not cached_state.is_contiguous()
-            or not cached_state.is_cuda or cached_state.dim() != 4
-            or tuple(cached_state.shape[1:]) != (q.shape[1], 64, 64)):
-        raise ValueError("cached_state must be contiguous fp32 CUDA [P, H, 64, 64]")
-    out = _decay_args(log_decay, q, k, v, out)
-    _on_current_device(cached_state=cached_state)
-    st = lib.span_la_decay_branches_from_state(cached_state.data_ptr(), cached_state.shape[0], q.data_ptr(),
+    st = lib.span_la_decay_branches_from_state(cached_state.data_ptr(), n, q.data_ptr(),
                                                k.data_ptr(), v.data_ptr(), dims, log_decay.data_ptr(), _iptr(bcu), B,
                                                _iptr(par), out.data_ptr(), _stream_handle(stream))
     _raise(lib, st, "span_la_decay_branches_from_state")
@@ -477,22 +514,24 @@ def span_la_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, states
     ``state_index`` (host, n entries) names each row's state, -1 for a row to
     skip; without it row t uses state t.  Without ``log_decay`` nothing decays.
     Returns the outputs [n, H, 64]."""
-    lib = load_library()
-    dims = _dims_of(q, k, v)
-    if (states.dtype != torch.float32 or not states.is_contiguous() or not states.is_cuda or states.dim() != 4
-            or states.shape[1:] != (q.shape[1], 64, 64)):
-        raise ValueError("states must be contiguous fp32 CUDA [P, H, 64, 64]")
-    out = _decay_args(log_decay, q, k, v, out, optional=True)
-    _on_current_device(states=states)
+    if _fast is not None:
+        r = _fast.decay_step(q, k, v, states, log_decay, state_index, out, stream)
+        if r is not None:
+            if type(r) is int:
+                _raise(_lib, r, "span_la_decay_step")
+            return r
+    lib = _lib or load_library()
+    dims, out, dev = _decay_args(q, k, v, log_decay, out)
+    n = _check_states("states", states, dims.num_heads, dev)
     index = None
     if state_index is not None:
         keep = _i32(state_index)
-        if keep.size != q.shape[0]:
+        if keep.size != dims.total_rows:
             raise ValueError("one state index per row")
         index = _iptr(keep)
     st = lib.span_la_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), dims,
-                                log_decay.data_ptr() if log_decay is not None else None, states.data_ptr(),
-                                states.shape[0], index, out.data_ptr(), _stream_handle(stream))
+                                None if log_decay is None else log_decay.data_ptr(), states.data_ptr(), n, index,
+                                out.data_ptr(), _stream_handle(stream))
     _raise(lib, st, "span_la_decay_step")
     return out
 
@@ -518,29 +557,46 @@ def packed_positions(view_cu_seqlens: Sequence[int], branch_cu_seqlens: Optional
     return pos
 
 
-def _qk_side(name: str, x: torch.Tensor, weight: Optional[torch.Tensor], out: Optional[torch.Tensor]):
+def _row_stride(name: str, x: torch.Tensor, T: int, H: int) -> int:
+    """The row stride of [T, H, 64] whose heads lie next to each other in a row."""
+    s0, s1, s2 = x.stride()
+    if (s2 != 1 or (s1 != 64 and H > 1)) and T > 0 and H > 0:
+        raise ValueError("%s: the heads of a row must lie next to each other" % name)
+    return s0 if T > 1 else H * 64
+
+
+def _qk_side(name: str, x: torch.Tensor, T: int, weight: Optional[torch.Tensor], out: Optional[torch.Tensor],
+             dev: int) -> Tuple[QkSide, torch.Tensor]:
     """The C struct of one side of span_la_qk_norm_rope, and its output."""
-    if x.dim() != 3 or x.shape[2] != 64 or not x.is_cuda:
-        raise ValueError("%s must be a CUDA tensor [T, H, 64], got %s" % (name, tuple(x.shape)))
-    T, H, _ = x.shape
+    sh = x.shape
+    if len(sh) != 3 or sh[2] != 64 or not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor [T, H, 64], got %s" % (name, tuple(sh)))
+    _on_device(dev, name, x)
+    H = sh[1]
     if out is None:
-        out = torch.empty((T, H, 64), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_cuda:
-        raise ValueError("%s_out must be a CUDA tensor of %s's shape and type" % (name, name))
-    strides = []
-    for what, t in ((name, x), (name + "_out", out)):
-        s0, s1, s2 = t.stride()
-        if T > 0 and H > 0 and (s2 != 1 or (H > 1 and s1 != 64)):
-            raise ValueError("%s: the heads of a row must lie next to each other" % what)
-        strides.append(s0 if T > 1 else H * 64)
-    per_head = 0
+        if x.is_contiguous():
+            out = torch.empty_like(x)
+        else:
+            out = torch.empty((T, H, 64), dtype=x.dtype, device=x.device)
+        out_stride = H * 64
+    else:
+        if out.shape != sh or out.dtype != x.dtype or not out.is_cuda:
+            raise ValueError("%s_out must be a CUDA tensor of %s's shape and type" % (name, name))
+        _on_device(dev, name + "_out", out)
+        out_stride = _row_stride(name + "_out", out, T, H)
+    per_head, wp = 0, None
     if weight is not None:
-        per_head = int(weight.dim() == 2)
-        if not weight.is_cuda or not weight.is_contiguous() or tuple(weight.shape) not in ((64,), (H, 64)):
+        wsh = weight.shape
+        per_head = len(wsh) - 1
+        if (not weight.is_cuda or not weight.is_contiguous() or wsh[-1] != 64 or per_head not in (0, 1)
+                or (per_head and wsh[0] != H)):
             raise ValueError("%s_weight must be contiguous CUDA [64] or [H, 64]" % name)
-    side = QkSide(x.data_ptr(), out.data_ptr(), weight.data_ptr() if weight is not None else None, strides[0], strides[1],
-                  H, per_head)
-    return side, out
+        _on_device(dev, name + "_weight", weight)
+        wp = weight.data_ptr()
+    return QkSide(x.data_ptr(), out.data_ptr(), wp, _row_stride(name, x, T, H), out_stride, H, per_head), out
+
+
+_DTYPES = {torch.bfloat16: SPAN_LA_BF16, torch.float32: SPAN_LA_F32}
 
 
 def span_la_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq,
@@ -557,37 +613,47 @@ def span_la_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tens
     parts of a fused projection's rows; weights are [64] or [H, 64].  Returns
     (q_out, k_out), allocated contiguous when not given; an output may be its
     own input."""
-    lib = load_library()
-    if q.dtype == torch.bfloat16:
-        dt = SPAN_LA_BF16
-    elif q.dtype == torch.float32:
-        dt = SPAN_LA_F32
-    else:
+    if _fast is not None:
+        r = _fast.qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out, stream)
+        if r is not None:
+            if type(r) is int:
+                _raise(_lib, r, "span_la_qk_norm_rope")
+            return r
+    lib = _lib or load_library()
+    dt = _DTYPES.get(q.dtype)
+    if dt is None:
         raise ValueError("dtype %s not supported (bf16 or fp32)" % q.dtype)
-    if k.dtype != q.dtype or k.shape[0] != q.shape[0]:
+    T = q.shape[0]
+    if k.dtype != q.dtype or k.shape[0] != T:
         raise ValueError("q and k must share dtype and rows")
+    if not q.is_cuda or not k.is_cuda:
+        raise ValueError("q and k must be CUDA tensors")
     wdt = dt
-    for w in (q_weight, k_weight):
-        if w is not None:
-            if w.dtype not in (torch.bfloat16, torch.float32):
-                raise ValueError("weight dtype %s not supported (bf16 or fp32)" % w.dtype)
-            wdt = SPAN_LA_BF16 if w.dtype == torch.bfloat16 else SPAN_LA_F32
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must share dtype")
-    if (positions.dtype != torch.int32 or not positions.is_cuda or not positions.is_contiguous()
-            or positions.shape != (q.shape[0],)):
+    if q_weight is not None or k_weight is not None:
+        wt = (k_weight if q_weight is None else q_weight).dtype
+        if wt not in _DTYPES:
+            raise ValueError("weight dtype %s not supported (bf16 or fp32)" % wt)
+        if k_weight is not None and k_weight.dtype != wt:
+            raise ValueError("q_weight and k_weight must share dtype")
+        wdt = _DTYPES[wt]
+    dev = _current_device()
+    qs, q_out = _qk_side("q", q, T, q_weight, q_out, dev)
+    ks, k_out = _qk_side("k", k, T, k_weight, k_out, dev)
+    psh = positions.shape
+    if (positions.dtype != torch.int32 or not positions.is_contiguous() or len(psh) != 1 or psh[0] != T
+            or not positions.is_cuda):
         raise ValueError("positions must be contiguous int32 CUDA [T]")
-    freq = None
+    _on_device(dev, "positions", positions)
+    freq, rotary = None, 0
     if inv_freq is not None:
         if isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda:
             raise ValueError("inv_freq holds host values")
-        freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
-    rotary = 2 * (freq.size if freq is not None else 0)
-    qs, q_out = _qk_side("q", q, q_weight, q_out)
-    ks, k_out = _qk_side("k", k, k_weight, k_out)
-    _on_current_device(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
-    st = lib.span_la_qk_norm_rope(qs, ks, q.shape[0], dt, wdt, float(eps), freq.ctypes.data if rotary else None, rotary,
-                                  1 if interleaved else 0, positions.data_ptr(), _stream_handle(stream))
+        keep = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        rotary = 2 * keep.size
+        if rotary:
+            freq = keep.ctypes.data
+    st = lib.span_la_qk_norm_rope(qs, ks, T, dt, wdt, eps, freq, rotary, 1 if interleaved else 0, positions.data_ptr(),
+                                  _stream_handle(stream))
     _raise(lib, st, "span_la_qk_norm_rope")
     return q_out, k_out
 
