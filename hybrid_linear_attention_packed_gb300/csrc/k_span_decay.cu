@@ -6,13 +6,25 @@
 //     o_i = sum_{s(i) <= j <= i} a^(i-j) (q_i . k_j) v_j  +  a^(i-s(i)+1) S^T q_i
 //     S  <- a^n S + sum_j a^(n-1-j) k_j v_j^T                       (n rows)
 //
-// The work is cut as span_output's is (k_span_output.cu): one run of tiles
-// per SM from a host-built list; a piece is the part of a segment-head inside
-// a run; first every CTA sums K^T V over its own pieces whose state another
-// CTA needs (phase 1), then a CTA that needs such states waits for a
-// grid-wide counter and sums them, here by Horner's rule, piece by piece:
-// S <- a^rows S + piece.  Where the decay enters:
+// The work is cut as span_output's is (k_span_output.cu): one run of tiles per
+// SM from a host-built list; a piece is the part of a segment-head (a view, or
+// a branch longer than a tile) inside a run.  Two phases:
 //
+//   1. Every CTA runs over K and V of its pieces and keeps the pieces' own
+//      states, S <- a^n S + K^T V' from S = 0 with V' = a^(n-1-j) v_j: the state
+//      before each tile goes to a table (16 KiB a tile and head), the one
+//      after the piece to a slot that other CTAs read.
+//   2. After a grid-wide counter a CTA sums the slots that a piece's start
+//      state needs by Horner's rule, S <- a^rows S + piece, and runs the tiles:
+//      the state entering tile t of a piece is a^(128 t) (start) + (table).
+//
+// So K^T V, with its scaled operand, is not in the second phase's chain, which
+// is bound by the latency of its hand-offs.  Keeping it there (the first
+// phase then only for pieces that others need, the running state carried from
+// tile to tile as span_output does) took 5,300 cycles a tile and 198 us for a
+// pass of four requests.
+//
+// Where the decay enters:
 //   scores   in fp32, as P leaves tensor memory to become the bf16 operand of
 //            P V: a row's factors fall by a from each column to the one
 //            before (running products of a^4, at most eight factors deep,
@@ -21,28 +33,23 @@
 //            1 by more than fp32 holds, products of a from the diagonal down.
 //   Q S      a row factor, which no rounding to bf16 should see: Q S has its own
 //            accumulator, and the output warps add a^(i-s(i)+1) times it to P V.
-//   K^T V    by scaling V: V' = a^(n-1-j) v_j, fp32, as a sum of three bf16
-//            numbers (24 bits: exactly the fp32 product), each with its own
-//            product with K.  The state is kept to fp32 accuracy that way; V'
-//            rounded to bf16 once would leave it 2e-3 off, twice 3e-6.
-//            (A factor on the tensor memory side is not possible: the rows j are
-//            the summed dimension.)
-//
-// Against span_output the V' tile takes a load stage's place in shared memory
-// (three stages instead of four), and Q S's accumulator the second K^T V
-// region's in tensor memory.
+//   K^T V    by scaling V, fp32, as a sum of three bf16 numbers (24 bits: exactly
+//            the fp32 product), side by side as one operand of 192 columns.  The
+//            state is kept to fp32 accuracy that way; V' rounded to bf16 once
+//            would leave it 2e-3 off, twice 3e-6.  (A factor on the tensor
+//            memory side is not possible: the rows j are the summed dimension.)
 //
 // 19 warps:
-//   warp 0      producer: K, V tiles of phase 1, then Q, K, V tiles, by TMA.
-//   warp 1      front issuer: phase 1, K^T V'; then per tile P = Q K^T and,
-//               unless the tile ends its piece (or when it ends a view-head), dS = K^T V'.
+//   warp 0      producer: K, V tiles of phase 1, then Q, K, V tiles and table
+//               entries, by TMA and bulk copies.
+//   warp 1      front issuer: phase 1, K^T V'; then per tile P = Q K^T.
 //   warp 2      O issuer: P V, then Q S.
-//   warps 3-10  scaling and conversion: V' of the tile (16 bytes of V at a
-//               time; rows past the tile become zero, and so do V's
-//               infinities and NaNs for P V, see add_nonfinite), then P, two warps per
-//               TMEM lane quarter, one per 64-column half.
-//   warps 11-18 state and output: the running state in registers (fp32, 16
-//               columns of one state row per thread), S staged in bf16, O stored.
+//   warps 3-10  phase 1: V' (16 bytes of V at a time; rows past the tile become
+//               zero).  Then P, two warps per TMEM lane quarter, one per
+//               64-column half; V's rows past the tile, infinities and NaNs
+//               become zero first (see add_nonfinite).
+//   warps 11-18 states and output: 16 columns of one state row per thread.
+//               Phase 1: the piece states.  Then S staged in bf16, O stored.
 #include "decay_math.cuh"
 #include "span_tiles.cuh"
 #include "spanla_internal.h"
@@ -67,48 +74,54 @@ constexpr uint32_t kStateTileBytes = kHeadDim * 128;       // 64 rows x 128 B (b
 constexpr uint32_t kSOpBytes = 2 * kStateTileBytes;
 constexpr uint32_t kOQuarterBytes = kOutStoreRows * 128;
 static_assert(2 * kOQuarterBytes == kStateTileBytes, "two quarters of O staging per S operand");
-constexpr int kCoordSlots = 64;
-constexpr int kP1Slots = 32;
+constexpr int kP1Slots = 16;
 constexpr int kSegSlots = 4;   // tiles whose segment starts are kept for the output warps
 constexpr int kBadSlots = 8;   // tiles whose marks are (made before P(i): five tiles could be open)
 // log2 a of a steep head: below it a^-31, the factor of a diagonal block's
 // last column in its first row (a masked one), could pass the fp32 range.
 constexpr float kSteepLog2 = -4.f;
 constexpr uint32_t kTmemCols = 512;
-// TMEM columns: P buffers (128 each), O buffers (64 each), dS, Q S (64 each;
-// both hold piece states in phase 1).
-constexpr uint32_t kColP0 = 0, kColP1 = 128, kColO0 = 256, kColO1 = 320, kColD = 384, kColQS = 448;
+// TMEM columns: P buffers (128 each), O and Q S buffers (64 each); in phase 1
+// two K^T V' buffers of 192.
+constexpr uint32_t kColP0 = 0, kColP1 = 128, kColO0 = 256, kColO1 = 320, kColQS0 = 384, kColQS1 = 448;
+constexpr uint32_t kColsState = kParts * kHeadDim, kColD0 = 0, kColD1 = kColsState;
+static_assert(2 * kColsState <= kTmemCols, "two K^T V' buffers");
 constexpr uint32_t kNamedStateBar = 1;
 
 struct DecaySmem {
   static constexpr uint32_t kStage0 = 0;
-  static constexpr uint32_t kQ = 0, kK = kRowTileBytes, kV = 2 * kRowTileBytes;
+  static constexpr uint32_t kK = 0, kV = kRowTileBytes, kQ = 2 * kRowTileBytes;
   static constexpr uint32_t kS = kStages * kStageBytes;
-  static constexpr uint32_t kVs = kS + 2 * kSOpBytes;              // V' parts
-  static constexpr uint32_t kBar = kVs + kParts * kRowTileBytes;
-  // Barriers; the pairs are used by alternate tiles (or phase-1 pieces).
-  // Empty takes two arrivals per use (both issuers read a tile's stage; the
-  // front issuer arrives twice on a phase-1 stage), OReady two (the MMAs'
-  // completion and the issuing thread, behind which the segment starts that
-  // the conversion warps wrote are visible).
+  // The stages' table entries (phase 2).  In phase 1, which uses neither
+  // those nor the S operands and Q, two V' buffers: buffer 0 here, buffer 1 in
+  // the last stage's Q and the S operands, which lie together.
+  static constexpr uint32_t kTable = kS + 2 * kSOpBytes;
+  static constexpr uint32_t kVs0 = kTable, kVs1 = kS - kRowTileBytes;
+  static_assert(kStages * kStateFloats * 4 == kParts * kRowTileBytes && 2 * kSOpBytes == (kParts - 1) * kRowTileBytes,
+                "the V' buffers' places");
+  static_assert(kQ + kRowTileBytes == kStageBytes, "the last stage's Q ends where the S operands begin");
+  static constexpr uint32_t kBar = kTable + kStages * kStateFloats * 4;
+  // Barriers; the pairs are used by alternate tiles.  Empty takes two
+  // arrivals per use (both issuers read a tile's stage; the front issuer
+  // arrives twice on a phase-1 stage), OReady two (the MMAs' completion and
+  // the issuing thread, behind which the segment starts that the conversion
+  // warps wrote are visible).
   static constexpr int kFull = 0, kEmpty = kStages, kPReady = 2 * kStages, kPDone = kPReady + 2, kOReady = kPReady + 4,
                        kOFree = kPReady + 6, kSSmem = kPReady + 8, kP1Ready = kPReady + 10, kP1Free = kPReady + 12,
-                       kPFree = kPReady + 14, kDReady = kPReady + 16, kDFree = kPReady + 17, kVReady = kPReady + 18,
-                       kVFree = kPReady + 19, kP1Done = kPReady + 20, kNumBars = kPReady + 21;
+                       kPFree = kPReady + 14, kVReady = kPReady + 16, kVFree = kPReady + 18, kP1Done = kPReady + 20,
+                       kNumBars = kPReady + 21;
   static constexpr uint32_t kTmemSlot = kBar + 8 * kNumBars;
-  static constexpr uint32_t kCoord = (kTmemSlot + 4 + 15) & ~15u;
-  static constexpr uint32_t kP1 = kCoord + 8 * kCoordSlots;
-  static constexpr uint32_t kSeg = kP1 + sizeof(SpanDesc) * kP1Slots;   // first row of each row's segment
+  static constexpr uint32_t kP1 = (kTmemSlot + 4 + 15) & ~15u;
+  static constexpr uint32_t kSeg = kP1 + sizeof(DecayPiece) * kP1Slots;   // first row of each row's segment
   static constexpr uint32_t kBad = kSeg + kSegSlots * kTileRows;        // 1 + the tile whose V held an inf or NaN
-  static constexpr uint32_t kDecay = kBad + 4 * kBadSlots;              // a head's decay, one per state warp
-  static constexpr uint32_t kBytes = kDecay + 16 * (kGroupThreads / 32);
+  static constexpr uint32_t kBytes = kBad + 4 * kBadSlots;
   static constexpr uint32_t kRequest = kBytes + 1024;
 };
 static_assert(DecaySmem::kRequest <= 227 * 1024, "shared memory budget");
 
 struct DecayParams {
   const CtaHead* heads;
-  const WorkTile* work;
+  const DecayTile* work;
   const uint8_t* bounds;
   const float* log_decay;
   const __nv_bfloat16* q;
@@ -116,16 +129,38 @@ struct DecayParams {
   const __nv_bfloat16* v;
   const float* stateA;
   float* ws;
+  float* table;           // states before the tiles of the pieces (thread-major, see table_at)
   float2* ws_factor;      // a^rows of each slot's piece, as a Factor
   float* final_out;
   __nv_bfloat16* out;
   unsigned* err;
-  const SpanDesc* p1;
+  const DecayPiece* p1;
   unsigned* counter;
   int a_rows;
   int H;
   int n_p1_ctas;
 };
+
+// The parts of a tile record each role reads.
+struct Start {   // rows and flags, the start state, the final state and the table's entries
+  int32_t row0, nrows, head, flags, stateA, stateB, a_n, b_n, final_idx, slot;
+};
+__device__ __forceinline__ Start load_start(const DecayTile* p) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(p));
+  const int4 b = __ldg(reinterpret_cast<const int4*>(p) + 1);
+  const int2 c = __ldg(reinterpret_cast<const int2*>(p) + 4);
+  return Start{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y};
+}
+struct Mask {    // rows and segment starts (conversion)
+  int32_t nrows, head, flags, bound0;
+  uint4 inl;
+  __device__ __forceinline__ int nbound() const { return flags >> kDecayBoundShift; }
+};
+__device__ __forceinline__ Mask load_mask4(const DecayTile* p) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(p));
+  const uint4 d = __ldg(reinterpret_cast<const uint4*>(p) + 3);
+  return Mask{a.y, a.z, a.w, __ldg(&p->bound0), d};
+}
 
 // True when one of two bf16 is infinite or NaN (its exponent bits all set).
 __device__ __forceinline__ bool nonfinite2(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
@@ -181,19 +216,21 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t (&part)[kParts]) {
 }
 
 // Eight values of V with an infinity or a NaN among them: its parts of V'
-// once more, without remainders of those (inf - inf), and zeros for them in V.
-__device__ __noinline__ void repair_piece(uint8_t* src, uint8_t* dst, float f, bool scale, bool clear) {
-  uint32_t* v = reinterpret_cast<uint32_t*>(src);
+// once more, without remainders of those (inf - inf).
+__device__ __noinline__ void repair_piece(const uint8_t* src, uint8_t* dst, float f) {
+  const uint32_t* v = reinterpret_cast<const uint32_t*>(src);
   for (int e = 0; e < 4; ++e) {
     const uint32_t keep = (nonfinite_lo(v[e]) ? 0u : 0xffffu) | (nonfinite_hi(v[e]) ? 0u : 0xffff0000u);
-    if (scale) {
-      uint32_t part[kParts];
-      split3(mul_f32x2(f32x2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)), f32x2(f, f)), part);
-      for (int p = 0; p < kParts; ++p)
-        reinterpret_cast<uint32_t*>(dst + p * kRowTileBytes)[e] = p == 0 ? part[p] : part[p] & keep;
-    }
-    if (clear) v[e] &= keep;
+    uint32_t part[kParts];
+    split3(mul_f32x2(f32x2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)), f32x2(f, f)), part);
+    for (int p = 0; p < kParts; ++p)
+      reinterpret_cast<uint32_t*>(dst + p * kRowTileBytes)[e] = p == 0 ? part[p] : part[p] & keep;
   }
+}
+// ... and zeros in their place.
+__device__ __noinline__ void clear_nonfinite(uint8_t* src) {
+  uint32_t* v = reinterpret_cast<uint32_t*>(src);
+  for (int e = 0; e < 4; ++e) v[e] &= (nonfinite_lo(v[e]) ? 0u : 0xffffu) | (nonfinite_hi(v[e]) ? 0u : 0xffff0000u);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -218,7 +255,9 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   const int4 h0 = __ldg(hd), h1 = __ldg(hd + 1);
   const int i_begin = h0.x, n = h0.y, p1_begin = h0.z, n_p1 = h0.w;
   const int n1 = h1.x;                                   // phase-1 tiles
-  const int n_first = min(h1.y, kSetupLoads);            // loads issued during the set-up
+  const bool counted = h1.z != 0;                        // others wait for this CTA's slots
+  // Loads issued during the set-up: phase 1's, or else the run's.
+  const int n_first = min(n1 > 0 ? n1 : h1.y, kSetupLoads);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(L::kFull + s), 1);
@@ -233,20 +272,17 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(bar(L::kSSmem + b), kGroupThreads);
       mbar_init(bar(L::kP1Ready + b), 1);
       mbar_init(bar(L::kP1Free + b), kGroupThreads);
+      mbar_init(bar(L::kVReady + b), kConvThreads);
+      mbar_init(bar(L::kVFree + b), 1);
     }
-    mbar_init(bar(L::kDReady), 1);
-    mbar_init(bar(L::kDFree), kGroupThreads);
-    mbar_init(bar(L::kVReady), kConvThreads);
-    mbar_init(bar(L::kVFree), 1);
     mbar_init(bar(L::kP1Done), kGroupThreads);
     for (int s = 0; s < kBadSlots; ++s) reinterpret_cast<int*>(smem + L::kBad)[s] = 0;
-    for (int w = 0; w < kGroupThreads / 32; ++w) reinterpret_cast<float4*>(smem + L::kDecay)[w].w = __int_as_float(-1);
     fence_mbar_init();
     const int4 f0 = __ldg(hd + 2), f1 = __ldg(hd + 3);
     const int fr[2 * kFirstLoads] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
     for (int u = 0; u < kSetupLoads; ++u) {
-      if (u < n_first) {
+      if (u < n_first) {   // (phase-1 tiles, or a run's when there are none)
         const uint32_t st = base + L::kStage0 + u * kStageBytes;
         mbar_arrive_expect_tx(bar(L::kFull + u), u < n1 ? 2 * kRowTileBytes : kStageBytes);
         if (u >= n1) tma_load_3d(st + L::kQ, &tm_q, bar(L::kFull + u), 0, fr[2 * u], fr[2 * u + 1]);
@@ -257,17 +293,11 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     tma_prefetch_desc(&tm_o);
   }
 
-  const WorkTile* list = prm.work + i_begin;
-  const SpanDesc* p1 = prm.p1 + p1_begin;
-  int2* coord = reinterpret_cast<int2*>(smem + L::kCoord);
-  SpanDesc* p1s = reinterpret_cast<SpanDesc*>(smem + L::kP1);
-  if (warp == 2) {   // idle until the set-up completes: stages what the producer and phase 1 read
-    int2 c_lo = make_int2(0, 0), c_hi = make_int2(0, 0);
-    if (lane < n) c_lo = make_int2(list[lane].row0, list[lane].head);
-    if (lane + 32 < n && lane + 32 < kCoordSlots) c_hi = make_int2(list[lane + 32].row0, list[lane + 32].head);
+  const DecayTile* list = prm.work + i_begin;
+  const DecayPiece* p1 = prm.p1 + p1_begin;
+  DecayPiece* p1s = reinterpret_cast<DecayPiece*>(smem + L::kP1);
+  if (warp == 2) {   // idle until the set-up completes: stages the phase-1 pieces
     for (int j = lane; j < n_p1 && j < kP1Slots; j += 32) p1s[j] = p1[j];
-    if (lane < n) coord[lane] = c_lo;
-    if (lane + 32 < n && lane + 32 < kCoordSlots) coord[lane + 32] = c_hi;
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
@@ -285,7 +315,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       bool ok = true;
       int u = 0;   // load index: phase-1 tiles, then the run's tiles
       for (int j = 0; j < n_p1 && ok; ++j) {
-        const SpanDesc sd = p1_of(j);
+        const DecayPiece sd = p1_of(j);
         for (int r = 0; r < sd.len && ok; r += kTileRows, ++u) {
           if (u < n_first) continue;   // issued during the set-up
           const int s = u % kStages;
@@ -296,16 +326,37 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           tma_load_3d(st + L::kV, &tm_v, bar(L::kFull + s), 0, sd.row0 + r, sd.head);
         }
       }
+      bool p1_over = n_p1 == 0;   // phase 1's V' buffers are free and its table is written
+      auto wait_p1 = [&]() {
+        if (!p1_over) ok = wait_or_flag(bar(L::kP1Done), 0, err, kErrTimeoutMma);
+        p1_over = true;
+      };
+      int t = 0;   // tile of its piece
+      int4 nxt = n > 0 ? __ldg(reinterpret_cast<const int4*>(list)) : int4{};   // row0, nrows, head, flags
+      int nxt_table0 = n > 0 ? __ldg(&list->table0) : 0;
       for (int i = 0; i < n && ok; ++i, ++u) {
+        const int4 h = nxt;
+        const int table0 = nxt_table0;
+        if (i + 1 < n) {
+          nxt = __ldg(reinterpret_cast<const int4*>(list + i + 1));
+          nxt_table0 = __ldg(&list[i + 1].table0);
+        }
+        t = (h.w & kTileFirst) ? 0 : t + 1;
         if (u < n_first) continue;
-        const int2 rc = i < kCoordSlots ? coord[i] : make_int2(list[i].row0, list[i].head);
         const int s = u % kStages;
         if (!wait_or_flag(bar(L::kEmpty + s), ((u / kStages) & 1) ^ 1, err, kErrTimeoutMma)) { ok = false; break; }
         const uint32_t st = base + L::kStage0 + s * kStageBytes;
-        mbar_arrive_expect_tx(bar(L::kFull + s), kStageBytes);
-        tma_load_3d(st + L::kQ, &tm_q, bar(L::kFull + s), 0, rc.x, rc.y);
-        tma_load_3d(st + L::kK, &tm_k, bar(L::kFull + s), 0, rc.x, rc.y);
-        tma_load_3d(st + L::kV, &tm_v, bar(L::kFull + s), 0, rc.x, rc.y);
+        mbar_arrive_expect_tx(bar(L::kFull + s), kStageBytes + (t > 0 ? kStateFloats * 4 : 0));
+        tma_load_3d(st + L::kK, &tm_k, bar(L::kFull + s), 0, h.x, h.z);
+        tma_load_3d(st + L::kV, &tm_v, bar(L::kFull + s), 0, h.x, h.z);
+        if (s == kStages - 1) wait_p1();
+        tma_load_3d(st + L::kQ, &tm_q, bar(L::kFull + s), 0, h.x, h.z);
+        if (t > 0) {
+          wait_p1();
+          bulk_copy_g2s(base + L::kTable + s * (kStateFloats * 4),
+                        prm.table + (static_cast<int64_t>(table0) + t - 1) * kStateFloats, kStateFloats * 4,
+                        bar(L::kFull + s));
+        }
       }
       // Wait (bounded) for the last loads to land before the CTA can exit.
       for (int w = (u > kStages ? u - kStages : 0); w < u; ++w)
@@ -314,94 +365,64 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   } else if (warp == 1) {
     // ------------------------------------------------------------ front issuer
     constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0);
-    constexpr uint32_t id_kv = idesc_bf16_f32(128, 64, 1, 1);
+    constexpr uint32_t id_kv = idesc_bf16_f32(128, kColsState, 1, 1);
     bool ok = true;
     int u = 0;
-    // Zero K (and V) rows past `rows` in a stage: they may hold anything, even
-    // NaN, or rows of another segment.
-    auto zero_tail = [&](uint32_t st, int rows, bool v_too) {
-      if (rows >= kTileRows) return;
-      uint8_t* krow = smem + (st + L::kK - base);
-      uint8_t* vrow = smem + (st + L::kV - base);
-      for (int q = rows * 8 + lane; q < kTileRows * 8; q += 32) {
-        *reinterpret_cast<uint4*>(krow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
-        if (v_too) *reinterpret_cast<uint4*>(vrow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-    };
-    // D = [K | K]^T V', the parts of V' smallest first.  (Both 64-wide M
-    // atoms read the K tile: leading byte offset 0; TMEM lanes 64..127 get a
-    // second copy of rows 0..63.)
-    auto mma_state = [&](uint32_t st, uint32_t col) {
-      const uint64_t dk = smem_desc_sw128(st + L::kK, 0, 1024);
-      const uint64_t dv = smem_desc_sw128(base + L::kVs, kRowTileBytes, 1024);
-#pragma unroll
-      for (int p = kParts - 1; p >= 0; --p)
-#pragma unroll
-        for (int kk = 0; kk < kTileRows / 16; ++kk)   // (addresses in units of 16 bytes)
-          mma_bf16(tmem + col, dk + kk * (2048 / 16), dv + p * (kRowTileBytes / 16) + kk * (2048 / 16), id_kv,
-                   (p < kParts - 1 || kk > 0) ? 1u : 0u);
-    };
-    // Phase 1: K^T V' of each tile of the pieces.
+    // Phase 1: [K | K]^T [V'_0 V'_1 V'_2] of each tile of the pieces.  (Both
+    // 64-wide M atoms read the K tile: leading byte offset 0; TMEM lanes
+    // 64..127 get a second copy of rows 0..63.)
     for (int j = 0; j < n_p1 && ok; ++j) {
-      const SpanDesc sd = p1_of(j);
+      const DecayPiece sd = p1_of(j);
       for (int r = 0; r < sd.len; r += kTileRows, ++u) {
         const int s = u % kStages, b = u & 1;
         ok = wait_or_flag(bar(L::kFull + s), (u / kStages) & 1, err, kErrTimeoutTma);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t st = base + L::kStage0 + s * kStageBytes;
-        zero_tail(st, sd.len - r, false);
-        ok = wait_or_flag(bar(L::kVReady), u & 1, err, kErrTimeoutMma);
+        if (sd.len - r < kTileRows) {
+          // K rows past the piece may hold anything, even NaN: zeros.
+          uint8_t* krow = smem + (st + L::kK - base);
+          for (int q = (sd.len - r) * 8 + lane; q < kTileRows * 8; q += 32)
+            *reinterpret_cast<uint4*>(krow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
+        ok = wait_or_flag(bar(L::kVReady + b), (u >> 1) & 1, err, kErrTimeoutMma);
         if (ok && u >= 2) ok = wait_or_flag(bar(L::kP1Free + b), ((u - 2) >> 1) & 1, err, kErrTimeoutMma);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          mma_state(st, b ? kColQS : kColD);
+          const uint64_t dk = smem_desc_sw128(st + L::kK, 0, 1024);
+          const uint64_t dv = smem_desc_sw128(base + (b ? L::kVs1 : L::kVs0), kRowTileBytes, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kTileRows / 16; ++kk)   // (addresses in units of 16 bytes)
+            mma_bf16(tmem + (b ? kColD1 : kColD0), dk + kk * (2048 / 16), dv + kk * (2048 / 16), id_kv, kk > 0 ? 1u : 0u);
           mma_commit(bar(L::kP1Ready + b));
-          mma_commit(bar(L::kVFree));
+          mma_commit(bar(L::kVFree + b));
           mma_commit(bar(L::kEmpty + s));
           mma_commit(bar(L::kEmpty + s));
         }
         __syncwarp();
       }
     }
-    // The regions take the run's tiles once phase 1 has been read out.
+    // The run's tiles take the columns once phase 1 has been read out.
     ok = __all_sync(0xffffffffu, ok);
     if (ok && n_p1 > 0) ok = wait_or_flag(bar(L::kP1Done), 0, err, kErrTimeoutMma);
     ok = __all_sync(0xffffffffu, ok);
-    TileHead nxt = (ok && n > 0) ? load_head(list) : TileHead{};
     for (int i = 0; i < n && ok; ++i, ++u) {
-      const TileHead r = nxt;
-      if (i + 1 < n) nxt = load_head(list + i + 1);
       const int s = u % kStages, b = i & 1;
-      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + s), (u / kStages) & 1, err, kErrTimeoutTma)))
-        break;
-      const uint32_t st = base + L::kStage0 + s * kStageBytes;
-      zero_tail(st, r.nrows, true);
-      __syncwarp();
+      ok = wait_or_flag(bar(L::kFull + s), (u / kStages) & 1, err, kErrTimeoutTma);
       // P buffer b is free once P V of tile i-2 has completed.
-      bool ok2 = true;
-      if (i >= 2) ok2 = wait_or_flag(bar(L::kPFree + b), ((i - 2) >> 1) & 1, err, kErrTimeoutMma);
-      if (!__all_sync(0xffffffffu, ok2)) break;
+      if (ok && i >= 2) ok = wait_or_flag(bar(L::kPFree + b), ((i - 2) >> 1) & 1, err, kErrTimeoutMma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       tc_fence_after_sync();
       if (lane == 0) {
-        const uint32_t colP = b ? kColP1 : kColP0;
+        const uint32_t st = base + L::kStage0 + s * kStageBytes;
+        const uint64_t dq = smem_desc_sw128(st + L::kQ, 16, 1024), dk = smem_desc_sw128(st + L::kK, 16, 1024);
+#pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          mma_bf16(tmem + colP, smem_desc_sw128(st + L::kQ + kk * 32, 16, 1024),
-                   smem_desc_sw128(st + L::kK + kk * 32, 16, 1024), id_qk, kk > 0);
+          mma_bf16(tmem + (b ? kColP1 : kColP0), dq + kk * 2, dk + kk * 2, id_qk, kk > 0 ? 1u : 0u);
         mma_commit(bar(L::kPReady + b));
-      }
-      __syncwarp();
-      // V'(i) is staged, and dS(i-1) has been read.
-      ok2 = wait_or_flag(bar(L::kVReady), u & 1, err, kErrTimeoutMma);
-      if (ok2 && i >= 1) ok2 = wait_or_flag(bar(L::kDFree), (i - 1) & 1, err, kErrTimeoutMma);
-      if (!__all_sync(0xffffffffu, ok2)) break;
-      tc_fence_after_sync();
-      if (lane == 0) {
-        if (!(r.flags & kTileLast) || (r.flags & kTileFinalOut)) mma_state(st, kColD);
-        mma_commit(bar(L::kDReady));
-        mma_commit(bar(L::kVFree));
         mma_commit(bar(L::kEmpty + s));
       }
       __syncwarp();
@@ -409,40 +430,39 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   } else if (warp == 2) {
     // ------------------------------------------------------------ O issuer
     constexpr uint32_t id_n64_b_mn = idesc_bf16_f32(128, 64, 0, 1);
-    TileHead nxt = n > 0 ? load_head(list) : TileHead{};
+    int flags = n > 0 ? __ldg(&list->flags) : 0;
     for (int i = 0; i < n; ++i) {
-      const TileHead r = nxt;
-      if (i + 1 < n) nxt = load_head(list + i + 1);
+      const bool has_state = !(flags & kTileFirst) || (flags & kTileHasInit);
+      if (i + 1 < n) flags = __ldg(&list[i + 1].flags);
       const int u = n1 + i;
       const int s = u % kStages, b = i & 1;
       const uint32_t st = base + L::kStage0 + s * kStageBytes;
-      const bool has_state = !(r.flags & kTileFirst) || (r.flags & kTileHasInit);
-      const uint32_t colO = b ? kColO1 : kColO0;
-      // P(i) is bf16 in TMEM: O(i) = P(i) V(i).  (O(i-2) was read out before
-      // Q S of tile i-1 was issued.)
-      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kPDone + b), (i >> 1) & 1, err, kErrTimeoutMma))) break;
-      tc_fence_after_sync();
-      if (lane == 0) {
-        const uint32_t colP = b ? kColP1 : kColP0;
-        // keys 0..63 of P in columns 0..31, keys 64..127 in columns 64..95
-        for (int kk = 0; kk < kTileRows / 16; ++kk)
-          mma_bf16_tmem_a(tmem + colO, tmem + colP + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
-                          smem_desc_sw128(st + L::kV + kk * 2048, kRowTileBytes, 1024),
-                          id_n64_b_mn, kk > 0 ? 1u : 0u);
-        mma_commit(bar(L::kPFree + b));
-      }
-      __syncwarp();
-      // S(i) staged, and Q S of tile i-1 (and O(i-1)) read out: Q S.
-      bool ok = wait_or_flag(bar(L::kSSmem + b), (i >> 1) & 1, err, kErrTimeoutMma);
-      if (ok && i >= 1) ok = wait_or_flag(bar(L::kOFree + (b ^ 1)), ((i - 1) >> 1) & 1, err, kErrTimeoutMma);
+      // P(i) is bf16 in TMEM, and O(i-2) and its Q S have been read: P V.
+      bool ok = wait_or_flag(bar(L::kPDone + b), (i >> 1) & 1, err, kErrTimeoutMma);
+      if (ok && i >= 2) ok = wait_or_flag(bar(L::kOFree + b), ((i - 2) >> 1) & 1, err, kErrTimeoutMma);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after_sync();
       if (lane == 0) {
+        const uint32_t colP = tmem + (b ? kColP1 : kColP0);
+        const uint64_t dv = smem_desc_sw128(st + L::kV, kRowTileBytes, 1024);
+        // keys 0..63 of P in columns 0..31, keys 64..127 in columns 64..95
+#pragma unroll
+        for (int kk = 0; kk < kTileRows / 16; ++kk)
+          mma_bf16_tmem_a(tmem + (b ? kColO1 : kColO0), colP + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
+                          dv + kk * (2048 / 16), id_n64_b_mn, kk > 0 ? 1u : 0u);
+        mma_commit(bar(L::kPFree + b));
+      }
+      __syncwarp();
+      // S(i) staged: Q S.
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kSSmem + b), (i >> 1) & 1, err, kErrTimeoutMma))) break;
+      tc_fence_after_sync();
+      if (lane == 0) {
         if (has_state) {
-          const uint32_t sop = base + L::kS + b * kSOpBytes;
+          const uint64_t dq = smem_desc_sw128(st + L::kQ, 16, 1024);
+          const uint64_t ds = smem_desc_sw128(base + L::kS + b * kSOpBytes, kStateTileBytes, 1024);
+#pragma unroll
           for (int kk = 0; kk < kHeadDim / 16; ++kk)
-            mma_bf16(tmem + kColQS, smem_desc_sw128(st + L::kQ + kk * 32, 16, 1024),
-                     smem_desc_sw128(sop + kk * 2048, kStateTileBytes, 1024), id_n64_b_mn, kk > 0 ? 1u : 0u);
+            mma_bf16(tmem + (b ? kColQS1 : kColQS0), dq + kk * 2, ds + kk * (2048 / 16), id_n64_b_mn, kk > 0 ? 1u : 0u);
         }
         mma_commit(bar(L::kOReady + b));
         mma_commit(bar(L::kEmpty + s));
@@ -457,23 +477,32 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int half = (warp - 3) >> 2;             // 64-column half of P this warp converts
     const int row = quarter * 32 + lane;          // tile row = TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    // V' of a tile (`scale`): row r of `rows` times a^(last - r), zero past
-    // them.  For a tile of the run (tile >= 0) the infinite and NaN values
-    // of V then become 0 and the tile is marked (see add_nonfinite).
-    auto prepare_v = [&](int s, int rows, int last, float l2, bool scale, int tile) {
-      uint8_t* src = smem + L::kStage0 + s * kStageBytes + L::kV + ct * 16;
-      uint8_t* dst = smem + L::kVs + ct * 16;
-      uint32_t bad = 0;
+    const uint32_t my16 = L::kV + ct * 16;   // this thread's 16-byte pieces of a V tile: every 4 KB from here
+    constexpr int kPieces = kTileRows * 8 / kConvThreads;
+    constexpr uint32_t kPieceStep = kConvThreads * 16;
+    auto piece_row = [&](int w) { return (ct >> 3) + (kConvThreads / 8) * w; };   // (whatever the swizzle)
+    bool ok = true;
+    int u = 0;
+    // Phase 1: V' of each tile: row r times a^(rows - 1 - r), zero past them.
+    for (int j = 0; j < n_p1 && ok; ++j) {
+      const DecayPiece sd = p1_of(j);
+      const float l2 = decay_log2(load_log_decay(prm.log_decay, sd.head));
+      for (int r0 = 0; r0 < sd.len; r0 += kTileRows, ++u) {
+        const int rows = min(sd.len - r0, kTileRows);
+        ok = wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma);
+        if (ok && u >= 2) ok = wait_or_flag(bar(L::kVFree + (u & 1)), ((u - 2) >> 1) & 1, err, kErrTimeoutMma);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* src = smem + L::kStage0 + (u % kStages) * kStageBytes + my16;
+        uint8_t* dst = smem + ((u & 1) ? L::kVs1 : L::kVs0) + ct * 16;
+        uint32_t bad = 0;
 #pragma unroll 2
-      for (int w = 0; w < kTileRows * 8 / kConvThreads; ++w) {
-        const int r = (ct >> 3) + (kConvThreads / 8) * w;   // 16-byte piece ct + 256 w is of row r whatever the swizzle
-        const uint32_t at = kConvThreads * 16 * w;
-        const uint4 x4 = r < rows ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-        bad |= (nonfinite2(x[0]) | nonfinite2(x[1]) | nonfinite2(x[2]) | nonfinite2(x[3])) << w;
-        if (scale) {
-          // (rows past the tile: 0 times 1)
-          const float f = decay_pow_fast(l2, static_cast<float>(max(last - r, 0)));
+        for (int w = 0; w < kPieces; ++w) {
+          const int r = piece_row(w);
+          const uint4 x4 = r < rows ? *reinterpret_cast<const uint4*>(src + kPieceStep * w) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+          bad |= (nonfinite2(x[0]) | nonfinite2(x[1]) | nonfinite2(x[2]) | nonfinite2(x[3])) << w;
+          const float f = decay_pow_fast(l2, static_cast<float>(max(rows - 1 - r, 0)));
           uint4 part[kParts];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -483,59 +512,63 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int p = 0; p < kParts; ++p) reinterpret_cast<uint32_t*>(&part[p])[e] = b2[p];
           }
 #pragma unroll
-          for (int p = 0; p < kParts; ++p) *reinterpret_cast<uint4*>(dst + p * kRowTileBytes + at) = part[p];
+          for (int p = 0; p < kParts; ++p)
+            *reinterpret_cast<uint4*>(dst + p * kRowTileBytes + kPieceStep * w) = part[p];
         }
-      }
-      if (bad != 0) {
-        for (int w = 0; w < kTileRows * 8 / kConvThreads; ++w)
-          if ((bad >> w) & 1)
-            repair_piece(src + kConvThreads * 16 * w, dst + kConvThreads * 16 * w,
-                         decay_pow_fast(l2, static_cast<float>(last - (ct >> 3) - (kConvThreads / 8) * w)), scale, tile >= 0);
-        if (tile >= 0) reinterpret_cast<int*>(smem + L::kBad)[tile % kBadSlots] = tile + 1;
-      }
-      fence_proxy_async_smem();
-    };
-    // Stage u's V is in shared memory and the V' buffer is free.
-    auto v_ready = [&](int u) -> bool {
-      bool ok = wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma);
-      if (ok && u >= 1) ok = wait_or_flag(bar(L::kVFree), (u - 1) & 1, err, kErrTimeoutMma);
-      return __all_sync(0xffffffffu, ok);
-    };
-    bool ok = true;
-    int u = 0;
-    for (int j = 0; j < n_p1 && ok; ++j) {
-      const SpanDesc sd = p1_of(j);
-      const float l2 = decay_log2(load_log_decay(prm.log_decay, sd.head));
-      for (int r = 0; r < sd.len; r += kTileRows, ++u) {
-        ok = v_ready(u);
-        if (!ok) break;
-        prepare_v(u % kStages, sd.len - r, min(sd.len - r, kTileRows) - 1, l2, true, -1);
-        mbar_arrive(bar(L::kVReady));
+        if (bad != 0) {
+          for (int w = 0; w < kPieces; ++w)
+            if ((bad >> w) & 1)
+              repair_piece(src + kPieceStep * w, dst + kPieceStep * w,
+                           decay_pow_fast(l2, static_cast<float>(rows - 1 - piece_row(w))));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::kVReady + (u & 1)));
       }
     }
-    TileMask nxt = n > 0 ? load_mask(list) : TileMask{};
-    TileHead nxt_head = n > 0 ? load_head(list) : TileHead{};
+    Mask nxt = n > 0 ? load_mask4(list) : Mask{};
+    float nxt_l2 = n > 0 ? decay_log2(load_log_decay(prm.log_decay, nxt.head)) : 0.f;
     for (int i = 0; i < n && ok; ++i, ++u) {
-      const TileMask r = nxt;
-      const int flags = nxt_head.flags;
-      const float l2 = decay_log2(load_log_decay(prm.log_decay, nxt_head.head));
+      const Mask r = nxt;
+      const float l2 = nxt_l2;
       if (i + 1 < n) {
-        nxt = load_mask(list + i + 1);
-        nxt_head = load_head(list + i + 1);
+        nxt = load_mask4(list + i + 1);
+        nxt_l2 = decay_log2(load_log_decay(prm.log_decay, nxt.head));
       }
       const int b = i & 1;
-      if (!v_ready(u)) break;
-      prepare_v(u % kStages, r.nrows, r.nrows - 1, l2, !(flags & kTileLast) || (flags & kTileFinalOut), i);
-      mbar_arrive(bar(L::kVReady));
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma))) break;
+      // V's rows past the tile, its infinities and NaNs become zero (0 times
+      // one of those, in a masked place, would be NaN); the latter mark the tile.
+      {
+        uint8_t* src = smem + L::kStage0 + (u % kStages) * kStageBytes + my16;
+        uint32_t bad = 0;
+        uint4 x[kPieces];
+#pragma unroll
+        for (int w = 0; w < kPieces; ++w) x[w] = *reinterpret_cast<const uint4*>(src + kPieceStep * w);
+#pragma unroll
+        for (int w = 0; w < kPieces; ++w)
+          bad |= (nonfinite2(x[w].x) | nonfinite2(x[w].y) | nonfinite2(x[w].z) | nonfinite2(x[w].w)) << w;
+        if (bad != 0 || r.nrows < kTileRows) {
+          for (int w = 0; w < kPieces; ++w) {
+            if (piece_row(w) >= r.nrows) {
+              *reinterpret_cast<uint4*>(src + kPieceStep * w) = make_uint4(0u, 0u, 0u, 0u);
+            } else if ((bad >> w) & 1) {
+              clear_nonfinite(src + kPieceStep * w);
+              reinterpret_cast<int*>(smem + L::kBad)[i % kBadSlots] = i + 1;
+            }
+          }
+          fence_proxy_async_smem();
+        }
+      }
 
       int seg_start = 0;
-      if (r.nbound > 1) {
-        const int nb = r.nbound < kInlineBounds ? r.nbound : kInlineBounds;
+      const int nbound = r.nbound();
+      if (nbound > 1) {
+        const int nb = nbound < kInlineBounds ? nbound : kInlineBounds;
         for (int q = 1; q < nb; ++q) {
           const int sb = inline_bound(r.inl, q);
           if (sb <= row) seg_start = sb;
         }
-        for (int q = kInlineBounds; q < r.nbound; ++q) {
+        for (int q = kInlineBounds; q < nbound; ++q) {
           const int sb = prm.bounds[r.bound0 + q];
           if (sb <= row) seg_start = sb;
         }
@@ -621,69 +654,67 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int col0 = 32 * sh + 16 * pi;
     const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
     bool ok = true;
+    // The table holds a state as this group's threads hold it: float4 c of
+    // thread g at c * 256 + g, so that each writes and reads whole lines.
+    const int g = tid - kStateWarp0 * 32;
+    auto table_at = [&](int64_t entry) { return reinterpret_cast<float4*>(prm.table + entry * kStateFloats) + g; };
 
-    // (log2 a, a^128 as a Factor, the head) of the tiles at hand, kept in
-    // shared memory by each warp for itself: registers are short here.
-    float4* decay_of = reinterpret_cast<float4*>(smem + L::kDecay) + (warp - kStateWarp0);
-    auto head_decay = [&](int head) -> float4 {
-      float4 x = *decay_of;
-      if (__float_as_int(x.w) != head) {
-        const float ld = load_log_decay(prm.log_decay, head);
-        const Factor f = factor_of(ld, static_cast<float>(kTileRows));
-        x = make_float4(decay_log2(ld), f.hi, f.lo, __int_as_float(head));
-        __syncwarp();
-        if (lane == 0) *decay_of = x;
-        __syncwarp();
-      }
-      return x;
-    };
-    // a^n of a tile of n rows.
-    auto tile_factor = [&](int head, int rows) -> Factor {
-      if (rows >= kTileRows) {
-        const float4 x = head_decay(head);
-        return Factor{x.y, x.z};
-      }
-      return factor_of(load_log_decay(prm.log_decay, head), static_cast<float>(rows));
-    };
-
-    // Phase 1: S <- a^n S + K^T V' over the tiles of each piece (as the run's
-    // tiles do: tile by tile the fp32 sums are rounded to nearest, which the
-    // tensor core's long sums are not), into its slot with its decay; then this
-    // CTA counts itself in the grid-wide counter.
-    float s_run[16];
-    {
+    // Phase 1: S <- a^n S + K^T V' over the tiles of each piece.  (Tile by
+    // tile, in fp32 rounded to nearest, which the tensor core's long sums are
+    // not.)  Then this CTA counts itself in the grid-wide counter.
+    if (n_p1 > 0) {
       int u = 0;
       for (int j = 0; j < n_p1 && ok; ++j) {
-        const SpanDesc sd = p1_of(j);
+        const DecayPiece sd = p1_of(j);
+        const float ld = load_log_decay(prm.log_decay, sd.head);
+        const Factor f_tile = factor_of(ld, static_cast<float>(kTileRows));
+        float s[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
-        for (int r = 0; r < sd.len; r += kTileRows, ++u) {
+        for (int e = 0; e < 16; ++e) s[e] = 0.f;
+        int t = 0;
+        for (int r = 0; r < sd.len; r += kTileRows, ++u, ++t) {
           const int b = u & 1;
           ok = __all_sync(0xffffffffu, wait_or_flag(bar(L::kP1Ready + b), (u >> 1) & 1, err, kErrTimeoutMma));
           if (!ok) break;
           tc_fence_after_sync();
-          uint32_t r0[16];
-          tmem_ld_16cols(tmem + lane_base + (b ? kColQS : kColD) + col0, r0);
+          // the parts' products, smallest first
+          const uint32_t at = tmem + lane_base + (b ? kColD1 : kColD0) + col0;
+          uint32_t x[16], y[16];
+          tmem_ld_16cols(at + 2 * kHeadDim, x);
+          tmem_ld_16cols(at + kHeadDim, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
+          tmem_ld_16cols(at, y);
           tmem_ld_wait();
           tc_fence_before_sync();
           mbar_arrive(bar(L::kP1Free + b));
-          const Factor f = tile_factor(sd.head, sd.len - r);
+          const Factor f = sd.len - r >= kTileRows ? f_tile : factor_of(ld, static_cast<float>(sd.len - r));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s_run[e] = f.step(s_run[e], __uint_as_float(r0[e]));
+          for (int e = 0; e < 16; ++e) s[e] = f.step(s[e], __uint_as_float(x[e]) + __uint_as_float(y[e]));
+          if (t < sd.n_table) {
+            float4* p = table_at(static_cast<int64_t>(sd.table0) + t);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[kGroupThreads * c] = make_float4(s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
+          }
         }
         if (!ok) break;
-        store_slice(prm.ws + static_cast<int64_t>(sd.slot) * kStateFloats + slice, s_run);
-        if (tid == kStateWarp0 * 32) {
-          const Factor f = factor_of(load_log_decay(prm.log_decay, sd.head), static_cast<float>(sd.len));
-          prm.ws_factor[sd.slot] = make_float2(f.hi, f.lo);
+        if (sd.slot >= 0) {
+          store_slice(prm.ws + static_cast<int64_t>(sd.slot) * kStateFloats + slice, s);
+          if (g == 0) {
+            const Factor f = factor_of(ld, static_cast<float>(sd.len));
+            prm.ws_factor[sd.slot] = make_float2(f.hi, f.lo);
+          }
         }
       }
-    }
-    if (n_p1 > 0) {
+      // (the producer reads the table by bulk copies)
+      asm volatile("fence.proxy.async;" ::: "memory");
       mbar_arrive(bar(L::kP1Done));
-      __threadfence();
-      named_barrier_sync(kNamedStateBar, kGroupThreads);
-      if (tid == kStateWarp0 * 32) atomicAdd(prm.counter, 1u);
+      if (counted) {
+        __threadfence();
+        named_barrier_sync(kNamedStateBar, kGroupThreads);
+        if (g == 0) atomicAdd(prm.counter, 1u);
+      }
     }
     // Wait (bounded) until every phase-1 CTA has counted itself, once, before
     // the first read of another CTA's slots.
@@ -704,14 +735,15 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       named_barrier_sync(kNamedStateBar, kGroupThreads);
     };
 
-    // The running state (row d, columns col0 ..) in fp32.  tag_run names the
-    // start state it holds while it is one, tag_op the one each S operand
-    // holds; -1: none (see k_span_output.cu).
+    // The start state of the piece at hand (row d, columns col0 ..), fp32.
+    // tag_run names it, tag_op the start state each S operand holds; -1: none
+    // (see k_span_output.cu).
+    float s_run[16];
     int64_t tag_run = -1, tag_op0 = -1, tag_op1 = -1;
     auto carry_tag = [&](int view, int head) -> int64_t {
       return (static_cast<int64_t>(1) << 62) | (static_cast<int64_t>(view) << 16) | head;
     };
-    auto start_tag = [&](const TileState& r) -> int64_t {
+    auto start_tag = [&](const Start& r) -> int64_t {
       if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
       if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
       return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
@@ -722,8 +754,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // segment's earlier pieces), in order, by Horner's rule into s_run:
     // S <- a^rows S + piece.  Two states in flight; through S operand t & 1
     // (coalesced reads, XOR-swizzled on the half-row) into the threads' slices.
-    auto sum_start = [&](int t, const TileState& r) {
-      const int g = tid - kStateWarp0 * 32;
+    auto sum_start = [&](int t, const Start& r) {
       const int na = r.a_n, total = r.a_n + r.b_n;
       const bool kept = prm.a_rows > 1 || prm.final_out == nullptr;   // term A is a kept state
       const float* pa =
@@ -784,7 +815,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       named_barrier_sync(kNamedStateBar, kGroupThreads);
     };
     // The running state becomes the start state of the piece starting at `r`.
-    auto start_piece = [&](int t, const TileState& r) {
+    auto start_piece = [&](int t, const Start& r) {
       if (!(r.flags & kTileHasInit)) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
@@ -809,25 +840,48 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       sum_start(t, r);
     };
 
-    // S(t) -> S operand t & 1, unless it holds that start state already.  The
-    // operand was last read by Q S of tile t-2, whose completion o_work(t-2) saw.
-    auto stage = [&](int t, const TileState& r) {
-      const int64_t tag = start_tag(r);
-      const bool uses = !(r.flags & kTileFirst) || (r.flags & kTileHasInit);
-      const int64_t held = (t & 1) ? tag_op1 : tag_op0;
-      if (uses && !(tag >= 0 && tag == held)) {
-        stage_state_slice(smem + L::kS + (t & 1) * kSOpBytes, d, col0, s_run);
-        if (t & 1) tag_op1 = tag; else tag_op0 = tag;
+    // S(t) -> S operand t & 1, unless it holds that start state already: the
+    // start state for a piece's first tile, else a^rows times it plus the
+    // table's entry in the tile's stage, `rows` rows into the piece.  The
+    // operand was last read by Q S of tile t-2, whose completion o_work(t-2)
+    // saw.  (The stage is released behind Q S, so behind this.)
+    auto stage = [&](int t, const Start& r, float l2, int rows, bool live) -> bool {
+      uint8_t* op = smem + L::kS + (t & 1) * kSOpBytes;
+      if (r.flags & kTileFirst) {
+        const int64_t tag = start_tag(r);
+        const int64_t held = (t & 1) ? tag_op1 : tag_op0;
+        if ((r.flags & kTileHasInit) && !(tag >= 0 && tag == held)) {
+          stage_state_slice(op, d, col0, s_run);
+          if (t & 1) tag_op1 = tag; else tag_op0 = tag;
+        }
+      } else {
+        if (t & 1) tag_op1 = -1; else tag_op0 = -1;
+        const int u = n1 + t;
+        if (live) live = __all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma));
+        if (!live) return false;
+        const float f = decay_pow_fast(l2, static_cast<float>(rows));
+        const float4* x = reinterpret_cast<const float4*>(smem + L::kTable + (u % kStages) * (kStateFloats * 4)) + g;
+        float y[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 xc = x[kGroupThreads * c];
+          y[4 * c] = fmaf(f, s_run[4 * c], xc.x);
+          y[4 * c + 1] = fmaf(f, s_run[4 * c + 1], xc.y);
+          y[4 * c + 2] = fmaf(f, s_run[4 * c + 2], xc.z);
+          y[4 * c + 3] = fmaf(f, s_run[4 * c + 3], xc.w);
+        }
+        stage_state_slice(op, d, col0, y);
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(L::kSSmem + (t & 1)));
+      return live;
     };
 
     // O(i) = P V + a^(i-s(i)+1) Q S -> global (rows of the tile only), through
     // this warp's O staging when its 32 rows all lie in the tile (one TMA
     // store), else row by row.
     bool o_pending = false;   // this warp's last TMA store may still read its staging
-    auto o_work = [&](int i, const TileState& r, bool live) -> bool {
+    auto o_work = [&](int i, const Start& r, float l2, bool live) -> bool {
       const int b = i & 1;
       if (!live || !__all_sync(0xffffffffu, wait_or_flag(bar(L::kOReady + b), (i >> 1) & 1, err, kErrTimeoutMma)))
         return false;
@@ -846,7 +900,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const bool store = row < r.nrows;
       const int seg_start = smem[L::kSeg + (i % kSegSlots) * kTileRows + row];
       const bool bad = reinterpret_cast<const int*>(smem + L::kBad)[i % kBadSlots] == i + 1;
-      const float l2 = head_decay(r.head).x;
       const float f = decay_pow_fast(l2, static_cast<float>(row - seg_start + 1));
       uint32_t pk[16];
 #pragma unroll
@@ -855,7 +908,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tmem_ld_16cols(tmem + lane_base + colO + 32 * pi + 16 * hf, r0);
         if (has_state) {
           uint32_t r1[16];
-          tmem_ld_16cols(tmem + lane_base + kColQS + 32 * pi + 16 * hf, r1);
+          tmem_ld_16cols(tmem + lane_base + (b ? kColQS1 : kColQS0) + 32 * pi + 16 * hf, r1);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) r0[e] = __float_as_uint(fmaf(f, __uint_as_float(r1[e]), __uint_as_float(r0[e])));
@@ -893,56 +946,53 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       return true;
     };
 
-    // S <- a^n S + dS of tile i; at the last tile of a view-head that is the
-    // view's final state: write it out.  (Without `live`, or when the wait
-    // runs out, nothing is read or written, but the tags change as they would
-    // have: they decide which named barriers the group reaches.)
-    auto take_ds = [&](int i, const TileState& r, bool live) -> bool {
-      const bool good =
-          live && __all_sync(0xffffffffu, wait_or_flag(bar(L::kDReady), i & 1, err, kErrTimeoutMma));
-      if (good) tc_fence_after_sync();
-      if (!(r.flags & kTileLast) || (r.flags & kTileFinalOut)) {
-        if (good) {
-          const Factor f = tile_factor(r.head, r.nrows);
-          uint32_t r0[16];
-          tmem_ld_16cols(tmem + lane_base + kColD + col0, r0);
-          tmem_ld_wait();
+    // A view-head's final state: its last piece's start state decayed over the
+    // piece, plus the piece's own state.
+    auto final_state = [&](const Start& r, int rows) {
+      const float4* p = reinterpret_cast<const float4*>(prm.ws + static_cast<int64_t>(r.slot) * kStateFloats + slice);
+      const Factor f = factor_of(load_log_decay(prm.log_decay, r.head), static_cast<float>(rows));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s_run[e] = f.step(s_run[e], __uint_as_float(r0[e]));
-        }
-        tag_run = -1;
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = __ldcg(p + c);   // (this thread's own, as it wrote it)
+        s_run[4 * c] = f.step(s_run[4 * c], x.x);
+        s_run[4 * c + 1] = f.step(s_run[4 * c + 1], x.y);
+        s_run[4 * c + 2] = f.step(s_run[4 * c + 2], x.z);
+        s_run[4 * c + 3] = f.step(s_run[4 * c + 3], x.w);
       }
-      if (good) {
-        tc_fence_before_sync();
-        mbar_arrive(bar(L::kDFree));
-      }
-      if (r.flags & kTileFinalOut) {
-        if (good)
-          store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
-        tag_run = carry_tag(r.final_idx, r.head);
-      }
-      return good;
+      store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
+      tag_run = carry_tag(r.final_idx, r.head);
     };
 
     // The group's named barriers (in the start-state sum and the grid-wide
     // wait) are reached by all warps alike: where they fall depends on the
     // tiles and the start-state tags only.  A warp whose bounded wait ran out
-    // goes on through the loop without waiting, reading or writing results.
+    // goes on through the loop without waiting or storing outputs.
     if (n > 0) {
-      TileState cur = load_state(list);
-      TileState nxt = n > 1 ? load_state(list + 1) : TileState{};
+      Start cur = load_start(list);
+      Start nxt = n > 1 ? load_start(list + 1) : Start{};
+      float l2 = decay_log2(load_log_decay(prm.log_decay, cur.head));
+      int rows = 0;               // rows of the piece before the tile to stage
       start_piece(0, cur);
-      stage(0, cur);
+      ok = stage(0, cur, l2, 0, ok);
       for (int i = 0; i < n; ++i) {
-        // S(i+1) first: the O issuer needs it right after P V of tile i+1.
-        if (i + 1 < n || (cur.flags & kTileFinalOut)) ok = take_ds(i, cur, ok);
+        float l2_next = l2;
         if (i + 1 < n) {
-          if (cur.flags & kTileLast) start_piece(i + 1, nxt);
-          stage(i + 1, nxt);
+          // S(i+1) first: the O issuer needs it right after P V of tile i+1.
+          rows += cur.nrows;
+          if (cur.flags & kTileFinalOut) final_state(cur, rows);
+          if (cur.flags & kTileLast) {
+            l2_next = decay_log2(load_log_decay(prm.log_decay, nxt.head));
+            rows = 0;
+            start_piece(i + 1, nxt);
+          }
+          ok = stage(i + 1, nxt, l2_next, rows, ok);
+        } else if (cur.flags & kTileFinalOut) {
+          final_state(cur, rows + cur.nrows);
         }
-        ok = o_work(i, cur, ok);
+        ok = o_work(i, cur, l2, ok);
         cur = nxt;
-        if (i + 2 < n) nxt = load_state(list + i + 2);
+        l2 = l2_next;
+        if (i + 2 < n) nxt = load_start(list + i + 2);
       }
     }
     if (lane == 0) bulk_wait_all();   // the last O stores have completed
@@ -972,6 +1022,7 @@ cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, 
   p.v = static_cast<const __nv_bfloat16*>(a.v);
   p.stateA = a.stateA;
   p.ws = a.ws;
+  p.table = a.table;
   p.ws_factor = a.ws_factor;
   p.final_out = a.final_out;
   p.out = static_cast<__nv_bfloat16*>(a.out);

@@ -806,6 +806,7 @@ struct DescBlock {
   int n_p1_ctas = 0;
   bool p1_evict_first = false;
   int piece = 0;           // decayed pass by the recurrence: rows of a piece
+  int64_t table_states = 0;   // decayed bf16 pass: entries of the table of tile states
   std::vector<int32_t> empty_views;
 };
 
@@ -1636,8 +1637,8 @@ span_la_status enqueue_recur(const DescBlock& desc, const uint8_t* block, float*
 
 // The one launch of a decayed bf16 pass.  stateA: kept states (final_out
 // NULL), else term A are workspace slots.
-span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, float* states, float2* factors,
-                                  unsigned* counter, const void* q, const void* k, const void* v,
+span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, float* states, float* table,
+                                  float2* factors, unsigned* counter, const void* q, const void* k, const void* v,
                                   const span_la_dims& dims, const float* log_decay, const float* kept,
                                   float* final_out, void* out, unsigned* err, cudaStream_t stream) {
   const int H = dims.num_heads;
@@ -1656,7 +1657,7 @@ span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, f
   if (st != SPAN_LA_OK) return st;
   SpanDecayArgs a;
   a.heads = reinterpret_cast<const CtaHead*>(block + desc.off_h);
-  a.work = reinterpret_cast<const WorkTile*>(block + desc.off_b);
+  a.work = reinterpret_cast<const DecayTile*>(block + desc.off_b);
   a.grid = desc.grid;
   a.bounds = block + desc.off_bounds;
   a.log_decay = log_decay;
@@ -1666,12 +1667,13 @@ span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, f
   a.stateA = kept != nullptr ? kept : states;
   a.a_rows = kept != nullptr ? H : 1;
   a.ws = states;
+  a.table = table;
   a.ws_factor = factors;
   a.final_out = final_out;
   a.out = out;
   a.H = H;
   a.err = err;
-  a.p1 = reinterpret_cast<const SpanDesc*>(block + desc.off_a);
+  a.p1 = reinterpret_cast<const DecayPiece*>(block + desc.off_a);
   a.counter = counter;
   a.n_p1_ctas = desc.n_p1_ctas;
   e = counted_launch(kKernelSpanDecay, stream, [&] { return launch_span_decay(tm_q, tm_k, tm_v, tm_o, a, stream); });
@@ -1704,11 +1706,12 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
     desc = &local;
   }
   if (desc->n_out_tiles == 0 && desc->n_scan == 0 && desc->empty_views.empty()) return SPAN_LA_OK;
-  // Workspace: the descriptors when they are not cached, the state slots,
-  // their pieces' decays and the counter (bf16).
+  // Workspace: the descriptors when they are not cached, the state slots and,
+  // for bf16, the table of tile states, the slots' decays and the counter.
   const size_t slots = static_cast<size_t>(desc->state_slots);
   const size_t off_states = use_cache ? 0 : align256(desc->host.size());
-  const size_t off_factors = off_states + slots * kStateFloats * sizeof(float);
+  const size_t off_table = off_states + slots * kStateFloats * sizeof(float);
+  const size_t off_factors = off_table + static_cast<size_t>(desc->table_states) * kStateFloats * sizeof(float);
   const size_t off_counter = off_factors + align256(slots * sizeof(float2));
   const size_t total = off_counter + 256;
   uint8_t* ws = nullptr;
@@ -1723,7 +1726,8 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
   float* states = reinterpret_cast<float*>(ws + off_states);
   if (st == SPAN_LA_OK)
     st = dims.dtype == SPAN_LA_BF16
-             ? enqueue_span_decay(*desc, block, states, reinterpret_cast<float2*>(ws + off_factors),
+             ? enqueue_span_decay(*desc, block, states, reinterpret_cast<float*>(ws + off_table),
+                                  reinterpret_cast<float2*>(ws + off_factors),
                                   reinterpret_cast<unsigned*>(ws + off_counter), q, k, v, dims, log_decay, kept,
                                   final_out, out, dev->err, stream)
              : enqueue_recur(*desc, block, states, q, k, v, dims, log_decay, kept != nullptr ? kept : final_out,
@@ -1734,12 +1738,94 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
   return st;
 }
 
-// The descriptors of a decayed pass: bf16 passes share span_output's one-launch plans.
+// The descriptors of a decayed bf16 pass from a one-launch plan: the tiles of
+// each CTA's run, and the pieces among them whose own states phase 1 computes,
+// namely those of several tiles (the states between them), those that
+// other CTAs sum (the plan's spans), and the ones that end a view.
+DescBlock make_span_decay_desc(const Plan& plan) {
+  DescBlock d;
+  d.grid = plan.out_grid();
+  std::vector<DecayTile> tiles(plan.work.size());
+  std::vector<DecayPiece> pieces;
+  std::vector<CtaHead> heads(static_cast<size_t>(d.grid));
+  int64_t slots = static_cast<int64_t>(plan.spans.size());
+  for (int c = 0; c < d.grid; ++c) {
+    CtaHead& h = heads[c];
+    h = CtaHead{};
+    h.i_begin = plan.cta_begin[c];
+    h.n = plan.cta_begin[c + 1] - plan.cta_begin[c];
+    h.p1_begin = static_cast<int32_t>(pieces.size());
+    int32_t span = plan.span_begin.empty() ? 0 : plan.span_begin[c];
+    const int32_t span_end = plan.span_begin.empty() ? 0 : plan.span_begin[c + 1];
+    h.pad[0] = span_end > span;
+    for (int32_t i = h.i_begin; i < h.i_begin + h.n;) {
+      int32_t e = i;   // the piece's last tile
+      while (!(plan.work[e].flags & kTileLast)) ++e;
+      const WorkTile& w0 = plan.work[i];
+      const WorkTile& w1 = plan.work[e];
+      // (the plan lists a CTA's spans in the order of its tiles)
+      const bool span_of = span < span_end && plan.spans[span].row0 == w0.row0 && plan.spans[span].head == w0.head;
+      DecayPiece p{};
+      p.row0 = w0.row0;
+      p.head = w0.head;
+      p.slot = span_of ? plan.spans[span].slot : (w1.flags & kTileFinalOut) ? static_cast<int32_t>(slots++) : -1;
+      p.n_table = e - i;
+      p.table0 = static_cast<int32_t>(d.table_states);
+      p.len = (p.slot >= 0 ? w1.row0 + w1.nrows : w1.row0) - w0.row0;
+      span += span_of;
+      d.table_states += p.n_table;
+      if (p.len > 0 && (p.slot >= 0 || p.n_table > 0)) {
+        pieces.push_back(p);
+        for (int32_t r = 0; r < p.len; r += kTileRows, ++h.n1)
+          if (h.n_first < kFirstLoads) {
+            h.first[2 * h.n_first] = p.row0 + r;
+            h.first[2 * h.n_first + 1] = p.head;
+            ++h.n_first;
+          }
+      }
+      for (; i <= e; ++i) {
+        const WorkTile& w = plan.work[i];
+        DecayTile& t = tiles[i];
+        t.row0 = w.row0;
+        t.nrows = w.nrows;
+        t.head = w.head;
+        t.flags = w.flags | (w.nbound << kDecayBoundShift);
+        t.stateA = w.stateA;
+        t.stateB = w.stateB;
+        t.a_n = w.a_n;
+        t.b_n = w.b_n;
+        t.final_idx = w.final_idx;
+        t.slot = p.slot;
+        t.table0 = p.table0;
+        t.bound0 = w.bound0;
+        std::memcpy(t.inl, w.inl, sizeof(t.inl));
+      }
+    }
+    h.n_p1 = static_cast<int32_t>(pieces.size()) - h.p1_begin;
+    for (int32_t i = 0; i < h.n && h.n_first < kFirstLoads; ++i, ++h.n_first) {
+      h.first[2 * h.n_first] = plan.work[h.i_begin + i].row0;
+      h.first[2 * h.n_first + 1] = plan.work[h.i_begin + i].head;
+    }
+  }
+  d.off_bounds = put(d.host, plan.bounds);
+  d.off_a = put(d.host, pieces);
+  d.off_b = put(d.host, tiles);
+  d.off_h = put(d.host, heads);
+  d.state_slots = slots;
+  d.n_out_tiles = tiles.size();
+  d.block_bytes = d.host.size();
+  d.fused = true;
+  d.n_p1_ctas = plan.n_p1_ctas;
+  d.empty_views = plan.empty_views;
+  return d;
+}
+
+// The descriptors of a decayed pass.
 DescBlock make_decay_desc(const int32_t* view_cu, int32_t V, const int32_t* branch_cu, int32_t B, const int32_t* parent,
                           const span_la_dims& dims, int num_sms) {
   const int H = dims.num_heads;
   if (dims.dtype == SPAN_LA_BF16)
-    return make_desc(make_span_plan(view_cu, V, branch_cu, B, parent, H, num_sms, true), H);
+    return make_span_decay_desc(make_span_plan(view_cu, V, branch_cu, B, parent, H, num_sms, true));
   return make_recur_desc(make_recur_plan(view_cu, V, branch_cu, B, parent, H, num_sms), H);
 }
 
@@ -2266,13 +2352,8 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
     cudaGetDevice(&device);
-    // (bf16: the key of span_la_pass's one-launch plan, which is the same plan)
-    const std::vector<int32_t> key =
-        dims.dtype == SPAN_LA_BF16
-            ? pass_key(device, dims, dev->num_sms, true, view_cu_seqlens, num_views, branch_cu_seqlens, num_branches,
-                       branch_parent)
-            : plan_key(device, dims.dtype, dims.num_heads, 5, dev->num_sms, view_cu_seqlens, num_views,
-                       branch_cu_seqlens, num_branches, branch_parent);
+    const std::vector<int32_t> key = plan_key(device, dims.dtype, dims.num_heads, 5, dev->num_sms, view_cu_seqlens,
+                                              num_views, branch_cu_seqlens, num_branches, branch_parent);
     auto build = [&] {
       return make_decay_desc(view_cu_seqlens, num_views, branch_cu_seqlens, num_branches, branch_parent, dims, dev->num_sms);
     };

@@ -257,9 +257,32 @@ cudaError_t launch_tile_output(bool split, const CUtensorMap* tm_q, const CUtens
 
 // Decayed passes of bf16 inputs (k_span_decay.cu): the one-launch structure
 // of span_output, from a plan of the same kind.
+//
+// A piece whose own states phase 1 computes: after its t-th tile of 128 rows
+// the state goes to entry table0 + t of the table (t < n_table), after all
+// `len` rows to `slot` (or nowhere: -1).
+struct DecayPiece {
+  int32_t row0, len, head, slot;
+  int32_t table0, n_table;
+  int32_t pad[2];
+};
+static_assert(sizeof(DecayPiece) == 32, "DecayPiece layout");
+
+// One tile of a CTA's run: as WorkTile (flags, start-state recipe, segment
+// starts), and `table0`, the table entry of the state before the piece's
+// second tile, and `slot` of the piece's own state (kTileFinalOut).
+constexpr int kDecayBoundShift = 8;   // the number of segment starts stands above the flags
+struct DecayTile {
+  int32_t row0, nrows, head, flags;
+  int32_t stateA, stateB, a_n, b_n;
+  int32_t final_idx, slot, table0, bound0;
+  uint8_t inl[kInlineBounds];
+};
+static_assert(sizeof(DecayTile) == 64, "DecayTile layout");
+
 struct SpanDecayArgs {
-  const CtaHead* heads = nullptr;
-  const WorkTile* work = nullptr;
+  const CtaHead* heads = nullptr;   // (pad[0]: others wait for the CTA's slots)
+  const DecayTile* work = nullptr;
   int grid = 0;
   const uint8_t* bounds = nullptr;
   const float* log_decay = nullptr;
@@ -269,12 +292,13 @@ struct SpanDecayArgs {
   const float* stateA = nullptr;   // term A: kept states [n][H][64][64] (a_rows = H, final_out NULL), or the slots
   int a_rows = 1;
   float* ws = nullptr;             // slots
+  float* table = nullptr;
   float2* ws_factor = nullptr;     // one per slot
   float* final_out = nullptr;
   void* out = nullptr;
   int H = 0;
   unsigned* err = nullptr;
-  const SpanDesc* p1 = nullptr;
+  const DecayPiece* p1 = nullptr;
   unsigned* counter = nullptr;
   int n_p1_ctas = 0;
 };

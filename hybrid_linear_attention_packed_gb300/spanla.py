@@ -162,7 +162,10 @@ def load_library(path: Optional[str] = None):
 
 def _bind_fast(lib) -> None:
     global _fast
-    from . import _fastcall
+    try:
+        from . import _fastcall
+    except ImportError:   # not built: the same calls by way of ctypes
+        return
     _fastcall.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                      for f in (lib.span_la_decay_pass, lib.span_la_decay_branches_from_state, lib.span_la_decay_step,
                                lib.span_la_qk_norm_rope)])
