@@ -14,7 +14,7 @@
 //      states, S <- a^n S + K^T V' from S = 0 with V' = a^(n-1-j) v_j: the state
 //      before each tile goes to a table (16 KiB a tile and head), the one
 //      after the piece to a slot that other CTAs read.
-//   2. After a grid-wide counter a CTA sums the slots that a piece's start
+//   2. Once every CTA has counted itself a CTA sums the slots that a piece's start
 //      state needs by Horner's rule, S <- a^rows S + piece, and runs the tiles:
 //      the state entering tile t of a piece is a^(128 t) (start) + (table).
 //
@@ -136,6 +136,7 @@ struct DecayParams {
   unsigned* err;
   const DecayPiece* p1;
   unsigned* counter;
+  unsigned target;
   int a_rows;
   int H;
   int n_p1_ctas;
@@ -661,7 +662,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
     // Phase 1: S <- a^n S + K^T V' over the tiles of each piece.  (Tile by
     // tile, in fp32 rounded to nearest, which the tensor core's long sums are
-    // not.)  Then this CTA counts itself in the grid-wide counter.
+    // not.)  Then this CTA counts itself.
     if (n_p1 > 0) {
       int u = 0;
       for (int j = 0; j < n_p1 && ok; ++j) {
@@ -716,15 +717,15 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (g == 0) atomicAdd(prm.counter, 1u);
       }
     }
-    // Wait (bounded) until every phase-1 CTA has counted itself, once, before
-    // the first read of another CTA's slots.
+    // Wait (bounded) until every CTA whose slots others read has counted
+    // itself, once, before the first read of such a slot.
     bool synced = prm.n_p1_ctas == 0;
     auto grid_sync = [&]() {
       if (synced) return;
       synced = true;
-      if (tid == kStateWarp0 * 32) {
+      if (g == 0) {
         const unsigned long long t0 = global_timer_ns();
-        while (ld_acquire_gpu(prm.counter) < static_cast<unsigned>(prm.n_p1_ctas)) {
+        while (ld_acquire_gpu(prm.counter) != prm.target) {
           if (global_timer_ns() - t0 > kWaitLimitNs) {
             atomicOr(err, kErrTimeoutMma);
             break;
@@ -1029,6 +1030,7 @@ cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, 
   p.err = a.err;
   p.p1 = a.p1;
   p.counter = a.counter;
+  p.target = a.target;
   p.a_rows = a.a_rows;
   p.H = a.H;
   p.n_p1_ctas = a.n_p1_ctas;

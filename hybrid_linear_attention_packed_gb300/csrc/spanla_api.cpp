@@ -807,6 +807,7 @@ struct DescBlock {
   bool p1_evict_first = false;
   int piece = 0;           // decayed pass by the recurrence: rows of a piece
   int64_t table_states = 0;   // decayed bf16 pass: entries of the table of tile states
+  size_t kept_ws = 0;      // workspace kept with the cached block (decayed passes)
   std::vector<int32_t> empty_views;
 };
 
@@ -983,6 +984,7 @@ struct CacheEntry {
   cudaEvent_t uploaded = nullptr;
   cudaStream_t upload_stream = nullptr;
   std::vector<std::pair<cudaStream_t, cudaEvent_t>> readers;   // last read per stream
+  unsigned passes = 0;          // decayed passes that counted in the kept workspace
   bool sync_on_evict = false;   // a read could not be recorded: synchronise before freeing
   uint64_t last_use = 0;
 };
@@ -1130,13 +1132,15 @@ span_la_status cached_block(const std::vector<int32_t>& key, int device, cudaStr
   en.device = device;
   en.key = key;
   en.desc = build();
-  const size_t bytes = std::max<size_t>(en.desc.host.size(), 256);
+  const size_t bytes = std::max<size_t>(align256(en.desc.host.size()) + en.desc.kept_ws, 256);
   if (injected_alloc_failure())
     return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(descriptors, %zu): injected failure", bytes);
   cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&en.d_block), bytes, stream);
   if (e != cudaSuccess)
     return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(descriptors, %zu): %s", bytes, cudaGetErrorString(e));
   e = upload_pinned(en.d_block, en.desc.host, device, stream);
+  if (e == cudaSuccess && en.desc.kept_ws > 0)   // (a kept workspace ends in its counter)
+    e = cudaMemsetAsync(en.d_block + align256(en.desc.host.size()) + en.desc.kept_ws - 256, 0, 256, stream);
   if (e == cudaSuccess) e = take_cache_event(device, &en.uploaded);
   if (e == cudaSuccess) e = cudaEventRecord(en.uploaded, stream);
   if (e != cudaSuccess) {
@@ -1638,7 +1642,7 @@ span_la_status enqueue_recur(const DescBlock& desc, const uint8_t* block, float*
 // The one launch of a decayed bf16 pass.  stateA: kept states (final_out
 // NULL), else term A are workspace slots.
 span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, float* states, float* table,
-                                  float2* factors, unsigned* counter, const void* q, const void* k, const void* v,
+                                  float2* factors, unsigned* counter, unsigned target, const void* q, const void* k, const void* v,
                                   const span_la_dims& dims, const float* log_decay, const float* kept,
                                   float* final_out, void* out, unsigned* err, cudaStream_t stream) {
   const int H = dims.num_heads;
@@ -1646,8 +1650,7 @@ span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, f
   for (size_t j = 0; j < desc.empty_views.size() && e == cudaSuccess; ++j)
     e = cudaMemsetAsync(final_out + static_cast<int64_t>(desc.empty_views[j]) * H * kStateFloats, 0,
                         static_cast<size_t>(H) * kStateFloats * sizeof(float), stream);
-  if (e == cudaSuccess && desc.n_p1_ctas > 0) e = cudaMemsetAsync(counter, 0, sizeof(unsigned), stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(pass counter)");
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(empty views)");
   if (desc.n_out_tiles == 0) return SPAN_LA_OK;
   CUtensorMap tm_q{}, tm_k{}, tm_v{}, tm_o{};
   span_la_status st = encode_map(&tm_q, q, dims.total_rows, H, kTileBoxRows, 1);
@@ -1675,10 +1678,28 @@ span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, f
   a.err = err;
   a.p1 = reinterpret_cast<const DecayPiece*>(block + desc.off_a);
   a.counter = counter;
+  a.target = target;
   a.n_p1_ctas = desc.n_p1_ctas;
   e = counted_launch(kKernelSpanDecay, stream, [&] { return launch_span_decay(tm_q, tm_k, tm_v, tm_o, a, stream); });
   return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "decayed pass launch");
 }
+
+// Workspace of a decayed pass: the state slots and, for bf16, the table of
+// tile states, the slots' decays and the phase-1 counter.
+struct DecayWorkspace {
+  size_t table = 0, factors = 0, counter = 0, bytes = 0;
+  explicit DecayWorkspace(const DescBlock& d) {
+    table = static_cast<size_t>(d.state_slots) * kStateFloats * sizeof(float);
+    factors = table + static_cast<size_t>(d.table_states) * kStateFloats * sizeof(float);
+    counter = factors + align256(static_cast<size_t>(d.state_slots) * sizeof(float2));
+    bytes = counter + (d.n_p1_ctas > 0 ? 256 : 0);
+  }
+};
+
+// A workspace of up to this size stays with its plan in the cache: a call's
+// own stream-ordered allocation and release cost the stream about 2 us, of 35
+// for a pass over one request (20 MB).  Larger ones are not worth holding on to.
+constexpr size_t kKeptWorkspaceBytes = size_t(64) << 20;
 
 // Descriptors (cached, or in the call's workspace while the stream is being
 // captured), workspace and launches of a decayed pass (kept NULL) or of
@@ -1699,42 +1720,67 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
   span_la_status st = SPAN_LA_OK;
   if (use_cache) {
     cache_lock.lock();
-    st = cached_block(key, device, stream, build_desc, &desc, &block, &entry);
+    st = cached_block(key, device, stream, [&] {
+      DescBlock d = build_desc();
+      const size_t bytes = DecayWorkspace(d).bytes;
+      d.kept_ws = bytes <= kKeptWorkspaceBytes ? bytes : 0;   // (at least the 256 bytes of a counter, or nothing)
+      return d;
+    }, &desc, &block, &entry);
     if (st != SPAN_LA_OK) return st;
   } else {
     local = build_desc();
     desc = &local;
   }
   if (desc->n_out_tiles == 0 && desc->n_scan == 0 && desc->empty_views.empty()) return SPAN_LA_OK;
-  // Workspace: the descriptors when they are not cached, the state slots and,
-  // for bf16, the table of tile states, the slots' decays and the counter.
-  const size_t slots = static_cast<size_t>(desc->state_slots);
-  const size_t off_states = use_cache ? 0 : align256(desc->host.size());
-  const size_t off_table = off_states + slots * kStateFloats * sizeof(float);
-  const size_t off_factors = off_table + static_cast<size_t>(desc->table_states) * kStateFloats * sizeof(float);
-  const size_t off_counter = off_factors + align256(slots * sizeof(float2));
-  const size_t total = off_counter + 256;
+  const DecayWorkspace at(*desc);
   uint8_t* ws = nullptr;
-  if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", total);
-  e = cudaMallocAsync(reinterpret_cast<void**>(&ws), total, stream);
-  if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", total, cudaGetErrorString(e));
-  if (!use_cache) {
-    e = upload_descriptors(ws, std::move(local.host), true, stream);
-    if (e != cudaSuccess) st = cuda_fail(e, "cudaMemcpyAsync(descriptors)");
-    block = ws;
+  uint8_t* own = nullptr;   // allocated by this call
+  if (use_cache && desc->kept_ws >= at.bytes) {
+    // The plan's workspace: behind the calls that used it, on whatever streams.
+    ws = const_cast<uint8_t*>(block) + align256(desc->host.size());
+    for (const auto& r : entry->readers)
+      if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, r.second, 0);
+    if (e == cudaSuccess && entry->sync_on_evict) e = cudaDeviceSynchronize();   // (a use that could not be recorded)
+    if (e != cudaSuccess) return cuda_fail(e, "waiting for the plan's workspace");
+  } else {
+    const size_t desc_bytes = use_cache ? 0 : align256(desc->host.size());
+    const size_t total = std::max<size_t>(desc_bytes + at.bytes, 256);
+    if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", total);
+    e = cudaMallocAsync(reinterpret_cast<void**>(&own), total, stream);
+    if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", total, cudaGetErrorString(e));
+    ws = own + desc_bytes;
+    if (!use_cache) {
+      e = upload_descriptors(own, std::move(local.host), true, stream);
+      if (e != cudaSuccess) st = cuda_fail(e, "cudaMemcpyAsync(descriptors)");
+      block = own;
+    }
   }
-  float* states = reinterpret_cast<float*>(ws + off_states);
+  float* states = reinterpret_cast<float*>(ws);
+  // The counter starts at 0 in a workspace of the call's own; in a kept one it
+  // goes on from call to call.
+  unsigned* counter = reinterpret_cast<unsigned*>(ws + at.counter);
+  unsigned target = static_cast<unsigned>(desc->n_p1_ctas);
+  if (st == SPAN_LA_OK && desc->n_p1_ctas > 0) {
+    if (own != nullptr) {
+      e = cudaMemsetAsync(counter, 0, sizeof(unsigned), stream);
+      if (e != cudaSuccess) st = cuda_fail(e, "cudaMemsetAsync(pass counter)");
+    } else {
+      target *= ++entry->passes;   // (modulo 2^32, as the counter)
+    }
+  }
   if (st == SPAN_LA_OK)
     st = dims.dtype == SPAN_LA_BF16
-             ? enqueue_span_decay(*desc, block, states, reinterpret_cast<float*>(ws + off_table),
-                                  reinterpret_cast<float2*>(ws + off_factors),
-                                  reinterpret_cast<unsigned*>(ws + off_counter), q, k, v, dims, log_decay, kept,
-                                  final_out, out, dev->err, stream)
+             ? enqueue_span_decay(*desc, block, states, reinterpret_cast<float*>(ws + at.table),
+                                  reinterpret_cast<float2*>(ws + at.factors), counter, target, q, k, v, dims, log_decay,
+                                  kept, final_out, out, dev->err, stream)
              : enqueue_recur(*desc, block, states, q, k, v, dims, log_decay, kept != nullptr ? kept : final_out,
                              final_out, out, stream);
+  if (st != SPAN_LA_OK && own == nullptr && desc->n_p1_ctas > 0) --entry->passes;   // (nothing counted)
   st = finish_read(entry, stream, st);
-  const cudaError_t ef = cudaFreeAsync(ws, stream);
-  if (st == SPAN_LA_OK && ef != cudaSuccess) st = cuda_fail(ef, "cudaFreeAsync");
+  if (own != nullptr) {
+    const cudaError_t ef = cudaFreeAsync(own, stream);
+    if (st == SPAN_LA_OK && ef != cudaSuccess) st = cuda_fail(ef, "cudaFreeAsync");
+  }
   return st;
 }
 

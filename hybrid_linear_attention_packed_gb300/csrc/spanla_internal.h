@@ -300,7 +300,8 @@ struct SpanDecayArgs {
   unsigned* err = nullptr;
   const DecayPiece* p1 = nullptr;
   unsigned* counter = nullptr;
-  int n_p1_ctas = 0;
+  unsigned target = 0;             // the counter once every CTA whose slots others read has counted itself
+  int n_p1_ctas = 0;               // those CTAs
 };
 cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               const CUtensorMap& tm_o, const SpanDecayArgs& a, cudaStream_t stream);
