@@ -1,4 +1,4 @@
-// Decayed linear attention by the recurrence itself, on CUDA cores:
+// Decayed linear attention for fp32 inputs, on CUDA cores:
 //
 //     S_t = a S_{t-1} + k_t v_t^T        o_t = S_t^T q_t        (a = exp(log_decay[h]))
 //
@@ -6,21 +6,25 @@
 // launches: the local state of every piece that a later piece or a branch
 // needs, a scan that turns those into the state entering each piece (and each
 // view's final state), and the output of every piece from its start state.
+// Every product and sum is fp32.
 //
-// The recurrence needs 3 * 4096 operations a row and head for the output
-// (k_i v_j, a S + that, q_i S) and 2 * 4096 for a piece state, all in fp32:
-// results are exact to fp32 roundings.  It is bound by the fp32 pipe, not by
-// memory (1 KB a row and head in fp32).
+// Rows come in chunks of 12.  A piece state adds a^(n-1-r) k_r v_r^T to a^n S
+// over a chunk of n rows: 4096 multiply-adds a row and head.  An output chunk
+// keeps S_r / a^(r+1) instead of S_r, so that the update is one multiply-add
+// for each element, k_r / a^(r+1) times v_r, and the output another, a^(r+1)
+// times at the end: 8192 a row and head, where the recurrence as written takes
+// 12288.  A head with a < e^-2, for which a^-12 could leave the fp32 range,
+// takes it as written.
+//
+// Bound by the fp32 pipe, not by memory (1 KB a row and head).
 //
 // One CTA of 64 threads per (piece, head): thread (rg, cg) holds the 8 x 8
 // block of S at rows 8 rg, columns 8 cg in registers, so that a row costs it
-// 8 values of q and of k and 8 of v from shared memory for 192 operations.
-// Partial outputs are added over the 8 row groups: 4 inside a warp by
-// shuffles (each lane keeps 2 columns), 2 across the warps through shared
-// memory.  Rows come in chunks of 16 by 16-byte asynchronous copies, one
-// chunk ahead.
-#include <cuda_bf16.h>
-
+// 8 values each of q, k and v from shared memory for 128 multiply-adds, two
+// columns at a time (f32x2).  Partial outputs are added over the 8 row groups:
+// 4 inside a warp by shuffles (each lane keeps 2 columns), 2 across the warps
+// through shared memory.  Rows come by 16-byte asynchronous copies, one chunk
+// ahead.
 #include "decay_math.cuh"
 #include "spanla_internal.h"
 #include "tc_ptx.cuh"
@@ -29,30 +33,19 @@ namespace spanla {
 namespace {
 
 constexpr int kThreads = 64;
-constexpr int kRows = 16;    // rows of a chunk
+constexpr float kSteepLogDecay = -2.f;
+constexpr int kRows = 12;    // rows of a chunk: eight CTAs' buffers fill the shared memory
 
-template <typename T>
-struct Row8;   // 8 consecutive values of a row in shared memory, as fp32
-template <>
-struct Row8<float> {
-  static __device__ __forceinline__ void get(const float* p, float* x) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-};
-template <>
-struct Row8<__nv_bfloat16> {
-  static __device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-};
+// 8 consecutive values as four pairs.
+__device__ __forceinline__ void get_pairs(const float* p, uint64_t (&x)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+__device__ __forceinline__ void get8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -63,44 +56,36 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void store_out(float* p, float a, float b) {
-  *reinterpret_cast<float2*>(p) = make_float2(a, b);
-}
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float a, float b) {
-  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
-}
-
-template <typename T, bool kOut>
+template <bool kOut>
 struct Smem {
-  T row[2][kOut ? 3 : 2][kRows][kHeadDim];   // K, V (and Q) of two chunks
+  float row[2][kOut ? 3 : 2][kRows][kHeadDim];            // K, V (and Q) of two chunks
   float part[kOut ? 2 : 1][kOut ? kRows : 1][kHeadDim];   // a warp's partial outputs
 };
 
-template <typename T, bool kOut>
-__global__ void __launch_bounds__(kThreads)
-recur_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+template <bool kOut>
+__global__ void __launch_bounds__(kThreads, kRecurUnitsPerSm)
+recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
              const RecurUnit* __restrict__ units, int H, const float* __restrict__ log_decay,
-             const float* __restrict__ stateA, float* __restrict__ ws, T* __restrict__ out) {
-  __shared__ __align__(16) Smem<T, kOut> sm;
+             const float* __restrict__ stateA, float* __restrict__ ws, float* __restrict__ out) {
+  __shared__ __align__(16) Smem<kOut> sm;
+  griddep_launch_dependents();   // (the next launch waits for this one's end before it reads)
   const int h = blockIdx.x % H;
   const RecurUnit u = units[blockIdx.x / H];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rg = tid >> 3, cg = tid & 7;
   const float ld = load_log_decay(log_decay, h);
-  // a is rounded, which a state that remembers 1 / (1 - a) rows would collect
-  // that often: every chunk's end makes up for its rows.
-  const Factor f1 = decay_factor(ld, 1.f);
-  const float a = f1.hi;
-  const float eps = f1.lo != 0.f ? f1.lo / f1.hi : 0.f;
+  const float l2 = decay_log2(ld);
+  const Factor f_chunk = decay_factor(ld, static_cast<float>(kRows));   // a^n of a whole chunk
+  const bool steep = kOut && ld < kSteepLogDecay;
+  const float a1 = decay_pow(l2, 1.f);
 
   const int64_t stride = static_cast<int64_t>(H) * kHeadDim;
   const int64_t base = static_cast<int64_t>(u.row0) * stride + static_cast<int64_t>(h) * kHeadDim;
-  constexpr int kVec = 16 / sizeof(T);              // values of one copy
-  constexpr int kPerRow = kHeadDim / kVec;
+  constexpr int kPerRow = kHeadDim / 4;             // 16-byte copies of a row
   auto load = [&](int r0, int b) {
     const int n = min(kRows, u.len - r0);
     for (int c = tid; c < n * kPerRow; c += kThreads) {
-      const int r = c / kPerRow, x = (c % kPerRow) * kVec;
+      const int r = c / kPerRow, x = (c % kPerRow) * 4;
       const int64_t at = base + (r0 + r) * stride + x;
       cp_async16(smem_addr(&sm.row[b][0][r][x]), k + at);
       cp_async16(smem_addr(&sm.row[b][1][r][x]), v + at);
@@ -110,37 +95,47 @@ recur_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restri
   load(0, 0);
   cp_async_commit();
 
-  float S[8][8];
+  uint64_t S[8][4];   // 8 rows, four pairs of columns
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) S[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) S[i][j] = 0;
   if (kOut) {
+    griddep_wait();   // start states from the scan
     // Start state: the scanned prefix of the segment's earlier rows, plus the
     // parent view's final state decayed over them.
     const int64_t slice = static_cast<int64_t>(8 * rg) * kHeadDim + 8 * cg;
     if (u.parent >= 0) {
-      const float f = decay_pow(decay_log2(ld), static_cast<float>(u.before));
+      const float f = decay_pow(l2, static_cast<float>(u.before));
+      const uint64_t f2 = f32x2(f, f);
       const float* p = stateA + (static_cast<int64_t>(u.parent) * H + h) * kStateFloats + slice;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        Row8<float>::get(p + i * kHeadDim, S[i]);
+        get_pairs(p + i * kHeadDim, S[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) S[i][j] *= f;
+        for (int j = 0; j < 4; ++j) S[i][j] = mul_f32x2(S[i][j], f2);
       }
     }
     if (u.slot >= 0) {
+      const uint64_t one = f32x2(1.f, 1.f);
       const float* p = ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + slice;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float x[8];
-        Row8<float>::get(p + i * kHeadDim, x);
+        uint64_t x[4];
+        get_pairs(p + i * kHeadDim, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) S[i][j] += x[j];
+        for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(S[i][j], one, x[j]);
       }
     }
   }
 
+  auto decay_state = [&](const Factor f) {
+    const uint64_t hi = f32x2(f.hi, f.hi), lo = f32x2(f.lo, f.lo);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(hi, S[i][j], mul_f32x2(lo, S[i][j]));
+  };
   int b = 0;
   for (int r0 = 0; r0 < u.len; r0 += kRows, b ^= 1) {
     const int n = min(kRows, u.len - r0);
@@ -148,23 +143,43 @@ recur_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restri
     cp_async_commit();
     cp_async_wait<1>();
     __syncthreads();
+    const Factor fn = n == kRows ? f_chunk : decay_factor(ld, static_cast<float>(n));
+    if (!kOut) decay_state(fn);
     for (int r = 0; r < n; ++r) {
-      float kr[8], vr[8];
-      Row8<T>::get(&sm.row[b][0][r][8 * rg], kr);
-      Row8<T>::get(&sm.row[b][1][r][8 * cg], vr);
+      float kr[8];
+      uint64_t vr[4];
+      get8(&sm.row[b][0][r][8 * rg], kr);
+      get_pairs(&sm.row[b][1][r][8 * cg], vr);
+      if (steep) {
+        const uint64_t a2 = f32x2(a1, a1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t k2 = f32x2(kr[i], kr[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) S[i][j] = fmaf(a, S[i][j], kr[i] * vr[j]);
+          for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(a2, S[i][j], mul_f32x2(k2, vr[j]));
+        }
+      } else {
+        const float w = decay_pow(l2, static_cast<float>(kOut ? -(r + 1) : n - 1 - r));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float kw = kr[i] * w;
+          const uint64_t k2 = f32x2(kw, kw);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(k2, vr[j], S[i][j]);
+        }
+      }
       if (kOut) {
         float qr[8], o[8];
-        Row8<T>::get(&sm.row[b][kOut ? 2 : 0][r][8 * rg], qr);
+        get8(&sm.row[b][kOut ? 2 : 0][r][8 * rg], qr);
+        uint64_t o2[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = qr[0] * S[0][j];
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t q2 = f32x2(qr[i], qr[i]);
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
+          for (int j = 0; j < 4; ++j) o2[j] = i == 0 ? mul_f32x2(q2, S[i][j]) : fma_f32x2(q2, S[i][j], o2[j]);
+        }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = fmaf(qr[i], S[i][j], o[j]);
+        for (int j = 0; j < 4; ++j) f32x2_split(o2[j], o[2 * j], o[2 * j + 1]);
         // Add over the warp's 4 row groups (lane bits 3 and 4), each step
         // keeping half of the columns.
         const bool up4 = lane & 16, up3 = lane & 8;
@@ -179,21 +194,20 @@ recur_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restri
           const float give = up3 ? x[j] : x[2 + j];
           y[j] = (up3 ? x[2 + j] : x[j]) + __shfl_xor_sync(0xffffffffu, give, 8);
         }
+        const float w = steep ? 1.f : decay_pow(l2, static_cast<float>(r + 1));
         *reinterpret_cast<float2*>(&sm.part[kOut ? warp : 0][kOut ? r : 0][8 * cg + (up4 ? 4 : 0) + (up3 ? 2 : 0)]) =
-            make_float2(y[0], y[1]);
+            make_float2(y[0] * w, y[1] * w);
       }
     }
-    const float back = eps * static_cast<float>(n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) S[i][j] = fmaf(back, S[i][j], S[i][j]);
+    if (kOut && !steep) decay_state(fn);
     __syncthreads();
     if (kOut) {
-      for (int c = tid; c < n * (kHeadDim / 2); c += kThreads) {
-        const int r = c / (kHeadDim / 2), x = 2 * (c % (kHeadDim / 2));
-        store_out(out + base + (r0 + r) * stride + x, sm.part[0][kOut ? r : 0][x] + sm.part[kOut ? 1 : 0][kOut ? r : 0][x],
-                  sm.part[0][kOut ? r : 0][x + 1] + sm.part[kOut ? 1 : 0][kOut ? r : 0][x + 1]);
+      for (int c = tid; c < n * (kHeadDim / 4); c += kThreads) {
+        const int r = c / (kHeadDim / 4), x = 4 * (c % (kHeadDim / 4));
+        const float4 p0 = *reinterpret_cast<const float4*>(&sm.part[0][kOut ? r : 0][x]);
+        const float4 p1 = *reinterpret_cast<const float4*>(&sm.part[kOut ? 1 : 0][kOut ? r : 0][x]);
+        *reinterpret_cast<float4*>(out + base + (r0 + r) * stride + x) =
+            make_float4(p0.x + p1.x, p0.y + p1.y, p0.z + p1.z, p0.w + p1.w);
       }
       // (The next chunk's partial outputs are written behind its barrier.)
     }
@@ -202,8 +216,8 @@ recur_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restri
     float* p = ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + static_cast<int64_t>(8 * rg) * kHeadDim + 8 * cg;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      *reinterpret_cast<float4*>(p + i * kHeadDim) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
-      *reinterpret_cast<float4*>(p + i * kHeadDim + 4) = make_float4(S[i][4], S[i][5], S[i][6], S[i][7]);
+      *reinterpret_cast<ulonglong2*>(p + i * kHeadDim) = make_ulonglong2(S[i][0], S[i][1]);
+      *reinterpret_cast<ulonglong2*>(p + i * kHeadDim + 4) = make_ulonglong2(S[i][2], S[i][3]);
     }
   }
 }
@@ -219,6 +233,8 @@ constexpr int kAhead = 8;
 __global__ void __launch_bounds__(kScanThreads)
 recur_scan_kernel(const RecurScan* __restrict__ scan, int H, int piece, const float* __restrict__ log_decay,
                   float* __restrict__ ws, float* __restrict__ final_out) {
+  griddep_launch_dependents();
+  griddep_wait();   // piece states
   const int part = blockIdx.x % kScanParts;
   const int64_t rest = blockIdx.x / kScanParts;
   const int h = static_cast<int>(rest % H);
@@ -253,39 +269,40 @@ recur_scan_kernel(const RecurScan* __restrict__ scan, int H, int piece, const fl
     *reinterpret_cast<float4*>(final_out + (static_cast<int64_t>(sd.final_idx) * H + h) * kStateFloats + off) = run;
 }
 
-template <typename T>
-cudaError_t recur_state(const RecurArgs& a, cudaStream_t stream) {
-  recur_kernel<T, false><<<static_cast<unsigned>(a.n_state * a.H), kThreads, 0, stream>>>(
-      nullptr, static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.state_units, a.H, a.log_decay, nullptr, a.ws,
-      nullptr);
-  return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t recur_output(const RecurArgs& a, cudaStream_t stream) {
-  recur_kernel<T, true><<<static_cast<unsigned>(a.n_out * a.H), kThreads, 0, stream>>>(
-      static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.out_units, a.H, a.log_decay,
-      a.stateA, a.ws, static_cast<T*>(a.out));
-  return cudaGetLastError();
+// A launch whose set-up may overlap the end of the kernel before it (`after`:
+// there is one in this call).
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), int64_t grid, int threads, bool after, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
 cudaError_t launch_recur_state(const RecurArgs& a, cudaStream_t stream) {
   if (a.n_state <= 0) return cudaSuccess;
-  return a.f32 ? recur_state<float>(a, stream) : recur_state<__nv_bfloat16>(a, stream);
+  return launch(recur_kernel<false>, a.n_state * a.H, kThreads, false, stream, static_cast<const float*>(nullptr), a.k,
+                a.v, a.state_units, a.H, a.log_decay, static_cast<const float*>(nullptr), a.ws, static_cast<float*>(nullptr));
 }
 
 cudaError_t launch_recur_scan(const RecurArgs& a, cudaStream_t stream) {
   if (a.n_scan <= 0) return cudaSuccess;
-  recur_scan_kernel<<<static_cast<unsigned>(a.n_scan * a.H * kScanParts), kScanThreads, 0, stream>>>(
-      a.scan, a.H, a.piece, a.log_decay, a.ws, a.final_out);
-  return cudaGetLastError();
+  return launch(recur_scan_kernel, a.n_scan * a.H * kScanParts, kScanThreads, a.n_state > 0, stream, a.scan, a.H, a.piece,
+                a.log_decay, a.ws, a.final_out);
 }
 
 cudaError_t launch_recur_output(const RecurArgs& a, cudaStream_t stream) {
   if (a.n_out <= 0) return cudaSuccess;
-  return a.f32 ? recur_output<float>(a, stream) : recur_output<__nv_bfloat16>(a, stream);
+  return launch(recur_kernel<true>, a.n_out * a.H, kThreads, a.n_scan > 0, stream, a.q, a.k, a.v, a.out_units, a.H,
+                a.log_decay, a.stateA, a.ws, a.out);
 }
 
 }  // namespace spanla

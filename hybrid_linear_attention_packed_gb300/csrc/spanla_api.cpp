@@ -1550,23 +1550,31 @@ struct RecurPlan {
   int64_t slots = 0;
 };
 
-// Rows of a piece: enough pieces for kRecurUnitsPerSm units (a piece of one
-// head) on every SM, in whole chunks of 16 rows, between 64 (below it a
-// unit's 16 KiB of state outweigh its rows) and 256 (above it one unit's run
-// time shows at the end of the launch).
-constexpr int kRecurUnitsPerSm = 8;
-int recur_piece(int64_t row_heads, int num_sms) {
-  const int64_t want = row_heads / (static_cast<int64_t>(std::max(1, num_sms)) * kRecurUnitsPerSm);
-  return static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(64, (want + 15) / 16 * 16)));
+// Rows of a piece, in whole chunks of 16: so many that the pieces of every
+// head, with the branches, fill the units that the SMs run at once (every unit
+// then starts at once; a second round of a few would double the time), but
+// at least a 64th of the longest segment (the scan walks a segment's pieces in
+// turn), and at most 256 (the end of a launch waits for the last piece).
+int recur_piece(int64_t rows, int64_t longest, int64_t segments, int H, int num_sms) {
+  const int64_t units = static_cast<int64_t>(std::max(1, num_sms)) * kRecurUnitsPerSm;
+  const int64_t free_units = std::max(units - segments * H, units / 2);   // (a segment's last piece is a part one)
+  const int64_t want = std::max((rows * H + free_units - 1) / free_units, (longest + 63) / 64);
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(256, (longest + 63) / 64 / 16 * 16 + 16),
+                                            std::max<int64_t>(16, (want + 15) / 16 * 16)));
 }
 
 RecurPlan make_recur_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu, int32_t B,
                           const int32_t* parent, int H, int num_sms) {
   RecurPlan plan;
-  int64_t rows = 0;
-  if (V > 0) rows += view_cu[V] - view_cu[0];
-  if (B > 0) rows += branch_cu[B] - branch_cu[0];
-  plan.piece = recur_piece(rows * H, num_sms);
+  int64_t rows = 0, longest = 0, segments = 0;
+  for (const auto& cu : {std::make_pair(view_cu, V), std::make_pair(branch_cu, B)})
+    for (int32_t s = 0; s < cu.second; ++s) {
+      const int64_t len = cu.first[s + 1] - cu.first[s];
+      rows += len;
+      longest = std::max(longest, len);
+      segments += len > 0;
+    }
+  plan.piece = recur_piece(rows, longest, segments, H, num_sms);
   auto add = [&](int64_t start, int64_t len, int view, int par) {
     const int64_t n = (len + plan.piece - 1) / plan.piece;
     if (n == 0 && view < 0) return;
@@ -1613,9 +1621,9 @@ span_la_status enqueue_recur(const DescBlock& desc, const uint8_t* block, float*
                              const void* k, const void* v, const span_la_dims& dims, const float* log_decay,
                              const float* stateA, float* final_out, void* out, cudaStream_t stream) {
   RecurArgs a;
-  a.q = q;
-  a.k = k;
-  a.v = v;
+  a.q = static_cast<const float*>(q);
+  a.k = static_cast<const float*>(k);
+  a.v = static_cast<const float*>(v);
   a.state_units = reinterpret_cast<const RecurUnit*>(block + desc.off_a);
   a.out_units = reinterpret_cast<const RecurUnit*>(block + desc.off_b);
   a.scan = reinterpret_cast<const RecurScan*>(block + desc.off_scan);
@@ -1624,12 +1632,11 @@ span_la_status enqueue_recur(const DescBlock& desc, const uint8_t* block, float*
   a.n_scan = desc.n_scan;
   a.H = dims.num_heads;
   a.piece = desc.piece;
-  a.f32 = dims.dtype == SPAN_LA_F32;
   a.log_decay = log_decay;
   a.stateA = stateA;
   a.ws = states;
   a.final_out = final_out;
-  a.out = out;
+  a.out = static_cast<float*>(out);
   cudaError_t e = cudaSuccess;
   if (a.n_state > 0) e = counted_launch(kKernelRecurState, stream, [&] { return launch_recur_state(a, stream); });
   if (e == cudaSuccess && a.n_scan > 0)
@@ -2392,8 +2399,8 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
       return fail(SPAN_LA_ERR_INVALID, "view_state_out must be a non-NULL 16-byte aligned pointer");
     if (num_views == 0 && num_branches == 0) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
-    // (pieces of 64 rows at least, and 4 scan CTAs a segment)
-    if ((st = check_grid(dims.total_rows / 64 + 4 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    // (pieces of 16 rows at least, and 4 scan CTAs a segment)
+    if ((st = check_grid(dims.total_rows / 16 + 4 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2425,7 +2432,7 @@ span_la_status span_la_decay_branches_from_state(const float* cached_state, int3
       return fail(SPAN_LA_ERR_INVALID, "cached_state must be a non-NULL 16-byte aligned pointer");
     if (segs.empty()) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
-    if ((st = check_grid(dims.total_rows / 64 + 4 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    if ((st = check_grid(dims.total_rows / 16 + 4 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;

@@ -306,7 +306,7 @@ struct SpanDecayArgs {
 cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               const CUtensorMap& tm_o, const SpanDecayArgs& a, cudaStream_t stream);
 
-// Decayed passes by the recurrence (CUDA cores).  Every segment (view or
+// Decayed passes of fp32 inputs, by the recurrence (k_decay_recur.cu, CUDA cores).  Every segment (view or
 // branch) is cut into pieces of `piece` rows (the last one shorter).
 struct RecurUnit {
   int32_t row0;     // first row of the piece
@@ -327,22 +327,23 @@ struct RecurScan {
   int32_t last_len;   // rows of the last piece
 };
 
+constexpr int kRecurUnitsPerSm = 8;   // pieces of one head that run on an SM at once
+
 struct RecurArgs {
-  const void* q = nullptr;
-  const void* k = nullptr;
-  const void* v = nullptr;
+  const float* q = nullptr;
+  const float* k = nullptr;
+  const float* v = nullptr;
   const RecurUnit* state_units = nullptr;
   const RecurUnit* out_units = nullptr;
   const RecurScan* scan = nullptr;
   int64_t n_state = 0, n_out = 0, n_scan = 0;
   int H = 0;
   int piece = 0;
-  bool f32 = false;
   const float* log_decay = nullptr;
   const float* stateA = nullptr;   // [n][H][64][64]: states that segments start from
   float* ws = nullptr;             // slots
   float* final_out = nullptr;
-  void* out = nullptr;
+  float* out = nullptr;
 };
 cudaError_t launch_recur_state(const RecurArgs& a, cudaStream_t stream);
 cudaError_t launch_recur_scan(const RecurArgs& a, cudaStream_t stream);
