@@ -21,7 +21,7 @@
 // One CTA of 64 threads per (piece, head): thread (rg, cg) holds the 8 x 8
 // block of S at rows 8 rg, columns 8 cg in registers, so that a row costs it
 // 8 values each of q, k and v from shared memory for 128 multiply-adds, two
-// columns at a time (f32x2).  Partial outputs are added over the 8 row groups:
+// rows of S at a time (f32x2).  Partial outputs are added over the 8 row groups:
 // 4 inside a warp by shuffles (each lane keeps 2 columns), 2 across the warps
 // through shared memory.  Rows come by 16-byte asynchronous copies, one chunk
 // ahead.
@@ -60,6 +60,7 @@ template <bool kOut>
 struct Smem {
   float row[2][kOut ? 3 : 2][kRows][kHeadDim];            // K, V (and Q) of two chunks
   float part[kOut ? 2 : 1][kOut ? kRows : 1][kHeadDim];   // a warp's partial outputs
+  float up[kRows + 1], down[kRows + 1];                   // a^m and a^-m
 };
 
 template <bool kOut>
@@ -78,6 +79,10 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
   const Factor f_chunk = decay_factor(ld, static_cast<float>(kRows));   // a^n of a whole chunk
   const bool steep = kOut && ld < kSteepLogDecay;
   const float a1 = decay_pow(l2, 1.f);
+  if (tid <= kRows) {   // (read behind the first chunk's barrier)
+    sm.up[tid] = decay_pow(l2, static_cast<float>(tid));
+    sm.down[tid] = decay_pow(l2, -static_cast<float>(tid));
+  }
 
   const int64_t stride = static_cast<int64_t>(H) * kHeadDim;
   const int64_t base = static_cast<int64_t>(u.row0) * stride + static_cast<int64_t>(h) * kHeadDim;
@@ -95,46 +100,38 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
   load(0, 0);
   cp_async_commit();
 
-  uint64_t S[8][4];   // 8 rows, four pairs of columns
+  uint64_t S[4][8];   // four pairs of rows, 8 columns
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) S[i][j] = 0;
+    for (int j = 0; j < 8; ++j) S[i][j] = 0;
   if (kOut) {
     griddep_wait();   // start states from the scan
     // Start state: the scanned prefix of the segment's earlier rows, plus the
     // parent view's final state decayed over them.
     const int64_t slice = static_cast<int64_t>(8 * rg) * kHeadDim + 8 * cg;
-    if (u.parent >= 0) {
-      const float f = decay_pow(l2, static_cast<float>(u.before));
+    auto add = [&](const float* p, float f) {
       const uint64_t f2 = f32x2(f, f);
-      const float* p = stateA + (static_cast<int64_t>(u.parent) * H + h) * kStateFloats + slice;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        get_pairs(p + i * kHeadDim, S[i]);
+      for (int i = 0; i < 4; ++i) {
+        float x[8], y[8];
+        get8(p + 2 * i * kHeadDim, x);
+        get8(p + (2 * i + 1) * kHeadDim, y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] = mul_f32x2(S[i][j], f2);
+        for (int j = 0; j < 8; ++j) S[i][j] = fma_f32x2(f32x2(x[j], y[j]), f2, S[i][j]);
       }
-    }
-    if (u.slot >= 0) {
-      const uint64_t one = f32x2(1.f, 1.f);
-      const float* p = ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + slice;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint64_t x[4];
-        get_pairs(p + i * kHeadDim, x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(S[i][j], one, x[j]);
-      }
-    }
+    };
+    if (u.parent >= 0)
+      add(stateA + (static_cast<int64_t>(u.parent) * H + h) * kStateFloats + slice, decay_pow(l2, static_cast<float>(u.before)));
+    if (u.slot >= 0) add(ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + slice, 1.f);
   }
 
   auto decay_state = [&](const Factor f) {
     const uint64_t hi = f32x2(f.hi, f.hi), lo = f32x2(f.lo, f.lo);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(hi, S[i][j], mul_f32x2(lo, S[i][j]));
+      for (int j = 0; j < 8; ++j) S[i][j] = fma_f32x2(hi, S[i][j], mul_f32x2(lo, S[i][j]));
   };
   int b = 0;
   for (int r0 = 0; r0 < u.len; r0 += kRows, b ^= 1) {
@@ -146,40 +143,43 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
     const Factor fn = n == kRows ? f_chunk : decay_factor(ld, static_cast<float>(n));
     if (!kOut) decay_state(fn);
     for (int r = 0; r < n; ++r) {
-      float kr[8];
-      uint64_t vr[4];
-      get8(&sm.row[b][0][r][8 * rg], kr);
-      get_pairs(&sm.row[b][1][r][8 * cg], vr);
+      uint64_t kr[4];
+      float vr[8];
+      get_pairs(&sm.row[b][0][r][8 * rg], kr);
+      get8(&sm.row[b][1][r][8 * cg], vr);
       if (steep) {
         const uint64_t a2 = f32x2(a1, a1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t k2 = f32x2(kr[i], kr[i]);
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t v2 = f32x2(vr[j], vr[j]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(a2, S[i][j], mul_f32x2(k2, vr[j]));
+          for (int i = 0; i < 4; ++i) S[i][j] = fma_f32x2(a2, S[i][j], mul_f32x2(kr[i], v2));
         }
       } else {
-        const float w = decay_pow(l2, static_cast<float>(kOut ? -(r + 1) : n - 1 - r));
+        const float w = kOut ? sm.down[r + 1] : sm.up[n - 1 - r];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float kw = kr[i] * w;
-          const uint64_t k2 = f32x2(kw, kw);
+        for (int i = 0; i < 4; ++i) kr[i] = mul_f32x2(kr[i], f32x2(w, w));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) S[i][j] = fma_f32x2(k2, vr[j], S[i][j]);
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t v2 = f32x2(vr[j], vr[j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[i][j] = fma_f32x2(kr[i], v2, S[i][j]);
         }
       }
       if (kOut) {
-        float qr[8], o[8];
-        get8(&sm.row[b][kOut ? 2 : 0][r][8 * rg], qr);
-        uint64_t o2[4];
+        uint64_t qr[4], o2[8];
+        get_pairs(&sm.row[b][kOut ? 2 : 0][r][8 * rg], qr);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t q2 = f32x2(qr[i], qr[i]);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o2[j] = i == 0 ? mul_f32x2(q2, S[i][j]) : fma_f32x2(q2, S[i][j], o2[j]);
+          for (int j = 0; j < 8; ++j) o2[j] = i == 0 ? mul_f32x2(qr[0], S[0][j]) : fma_f32x2(qr[i], S[i][j], o2[j]);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float lo, hi;
+          f32x2_split(o2[j], lo, hi);
+          o[j] = lo + hi;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f32x2_split(o2[j], o[2 * j], o[2 * j + 1]);
         // Add over the warp's 4 row groups (lane bits 3 and 4), each step
         // keeping half of the columns.
         const bool up4 = lane & 16, up3 = lane & 8;
@@ -194,7 +194,7 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
           const float give = up3 ? x[j] : x[2 + j];
           y[j] = (up3 ? x[2 + j] : x[j]) + __shfl_xor_sync(0xffffffffu, give, 8);
         }
-        const float w = steep ? 1.f : decay_pow(l2, static_cast<float>(r + 1));
+        const float w = steep ? 1.f : sm.up[r + 1];
         *reinterpret_cast<float2*>(&sm.part[kOut ? warp : 0][kOut ? r : 0][8 * cg + (up4 ? 4 : 0) + (up3 ? 2 : 0)]) =
             make_float2(y[0] * w, y[1] * w);
       }
@@ -215,58 +215,60 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
   if (!kOut) {
     float* p = ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + static_cast<int64_t>(8 * rg) * kHeadDim + 8 * cg;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      *reinterpret_cast<ulonglong2*>(p + i * kHeadDim) = make_ulonglong2(S[i][0], S[i][1]);
-      *reinterpret_cast<ulonglong2*>(p + i * kHeadDim + 4) = make_ulonglong2(S[i][2], S[i][3]);
+    for (int i = 0; i < 4; ++i) {
+      float x[8], y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f32x2_split(S[i][j], x[j], y[j]);
+      float* p0 = p + 2 * i * kHeadDim;
+      float* p1 = p0 + kHeadDim;
+      *reinterpret_cast<float4*>(p0) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(p0 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<float4*>(p1) = make_float4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<float4*>(p1 + 4) = make_float4(y[4], y[5], y[6], y[7]);
     }
   }
 }
 
 // The piece states of each segment-head, in order, become the states entering
 // the pieces (in place), and their total the view's final state:
-// run <- a^len run + piece.  256 threads take one float4 of a quarter of a
-// state each, 8 slots of loads ahead.
+// run <- a^len run + piece.  One element a thread, so that a pass of few
+// segments still has a state's 4096 chains times its heads in flight, 16 slots
+// of loads ahead.  (A float4 a thread, 8 slots ahead: 25 us where this takes
+// SCAN_US, for 58 slots of 16 heads.)
 constexpr int kScanThreads = 256;
-constexpr int kScanParts = kStateFloats / (4 * kScanThreads);
-constexpr int kAhead = 8;
+constexpr int kScanParts = kStateFloats / kScanThreads;
+constexpr int kAhead = 16;
 
 __global__ void __launch_bounds__(kScanThreads)
 recur_scan_kernel(const RecurScan* __restrict__ scan, int H, int piece, const float* __restrict__ log_decay,
                   float* __restrict__ ws, float* __restrict__ final_out) {
   griddep_launch_dependents();
-  griddep_wait();   // piece states
   const int part = blockIdx.x % kScanParts;
   const int64_t rest = blockIdx.x / kScanParts;
   const int h = static_cast<int>(rest % H);
   const RecurScan sd = scan[rest / H];
-  const int off = (part * kScanThreads + threadIdx.x) * 4;
+  const int off = part * kScanThreads + threadIdx.x;
   const float ld = load_log_decay(log_decay, h);
   const Factor f = decay_factor(ld, static_cast<float>(piece));
   const Factor f_last = decay_factor(ld, static_cast<float>(sd.last_len));
   float* p = ws + (static_cast<int64_t>(sd.slot0) * H + h) * kStateFloats + off;
   const int64_t stride = static_cast<int64_t>(H) * kStateFloats;
   const int n_read = sd.final_idx >= 0 ? sd.nslots : sd.nslots - 1;   // a branch's last piece has no state of its own
-  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  griddep_wait();   // piece states
+  float run = 0.f;
   for (int c0 = 0; c0 < sd.nslots; c0 += kAhead) {
-    float4 x[kAhead];
+    float x[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (c0 + j < n_read) x[j] = *reinterpret_cast<const float4*>(p + (c0 + j) * stride);
+      if (c0 + j < n_read) x[j] = __ldcg(p + (c0 + j) * stride);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int c = c0 + j;
-      if (c < sd.nslots) *reinterpret_cast<float4*>(p + c * stride) = run;
-      if (c < n_read) {
-        const Factor g = c + 1 < sd.nslots ? f : f_last;
-        run.x = g.step(run.x, x[j].x);
-        run.y = g.step(run.y, x[j].y);
-        run.z = g.step(run.z, x[j].z);
-        run.w = g.step(run.w, x[j].w);
-      }
+      if (c < sd.nslots) __stcg(p + c * stride, run);
+      if (c < n_read) run = (c + 1 < sd.nslots ? f : f_last).step(run, x[j]);
     }
   }
-  if (sd.final_idx >= 0)
-    *reinterpret_cast<float4*>(final_out + (static_cast<int64_t>(sd.final_idx) * H + h) * kStateFloats + off) = run;
+  if (sd.final_idx >= 0) final_out[(static_cast<int64_t>(sd.final_idx) * H + h) * kStateFloats + off] = run;
 }
 
 // A launch whose set-up may overlap the end of the kernel before it (`after`:

@@ -2399,8 +2399,8 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
       return fail(SPAN_LA_ERR_INVALID, "view_state_out must be a non-NULL 16-byte aligned pointer");
     if (num_views == 0 && num_branches == 0) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
-    // (pieces of 16 rows at least, and 4 scan CTAs a segment)
-    if ((st = check_grid(dims.total_rows / 16 + 4 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    // (pieces of 16 rows at least, and 16 scan CTAs a segment)
+    if ((st = check_grid(dims.total_rows / 16 + 16 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2432,7 +2432,7 @@ span_la_status span_la_decay_branches_from_state(const float* cached_state, int3
       return fail(SPAN_LA_ERR_INVALID, "cached_state must be a non-NULL 16-byte aligned pointer");
     if (segs.empty()) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
-    if ((st = check_grid(dims.total_rows / 16 + 4 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    if ((st = check_grid(dims.total_rows / 16 + 16 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
