@@ -112,52 +112,84 @@ cudaError_t step_chunk(const StepArgs& a, int64_t t0, int64_t n, cudaStream_t st
 
 // ------------------------------------------------------------------ norm and rotation
 // One warp per row.  A lane holds 16 bytes of a head (kVec values; kLanes
-// lanes a head), so a warp step covers 256 (bf16) or 128 (fp32) values, all
-// its loads in flight before the first is used.
+// lanes a head), so a warp step covers 4 (bf16) or 2 (fp32) heads; two steps
+// of each side are in flight.
 //
 // The angle of position p and frequency f (in turns, f / 2 pi) is p f mod 1.
 // f is held as a 64-bit binary fraction F, so that the low 64 bits of p F are
 // the angle exactly, whatever the position; its top 32 bits go to
 // sincospi.  The row's angles are computed once, one per lane, for all heads.
+//
+// (y_a, y_b) = r (w_a x_a, w_b x_b) rotated by (c, s): each lane keeps its
+// dimensions' own factors c w and their partners' -+ s w, so that an element
+// costs two products and a multiply-add besides the sum of squares, two
+// elements at a time (f32x2).  Where the partner is:
+//   kWhole  pairs (i, i + 32): a lane loads 8 bytes of each half of the head,
+//           so that pairs meet in it
+//   kPart   pairs (i, i + r/2) of r < 64 rotated dimensions: 16 bytes a lane,
+//           partners from another lane by shuffles
+//   kNext   pairs (2 i, 2 i + 1): 16 bytes a lane
+enum RopePairs { kWhole, kPart, kNext };
 constexpr int kRopeWarps = 4;
+// CTAs on an SM: 32 warps of 64 registers, with two steps of each side in
+// flight.  For 7,829 rows of 16 + 16 heads (bf16) 16.6 us; 18.4 us with four
+// steps, or with 24 warps.  A warp that runs on to further rows, loading the
+// next one's first steps ahead, took 24 us.
+constexpr int kRopeCtas = 8;
 
 template <typename T>
-struct Lane16;   // 16 bytes of a row
+struct Lane16;   // 16 bytes of a row as pairs of fp32
 template <>
 struct Lane16<float> {
   static constexpr int kVec = 4;
-  static __device__ __forceinline__ void unpack(const uint4& a, float* x) {
-    x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+  static __device__ __forceinline__ void unpack(const uint4& a, uint64_t (&x)[2]) {
+    x[0] = f32x2(__uint_as_float(a.x), __uint_as_float(a.y));
+    x[1] = f32x2(__uint_as_float(a.z), __uint_as_float(a.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  static __device__ __forceinline__ uint4 pack(const uint64_t (&x)[2]) {
+    float a, b, c, d;
+    f32x2_split(x[0], a, b);
+    f32x2_split(x[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
 };
 template <>
 struct Lane16<__nv_bfloat16> {
   static constexpr int kVec = 8;
-  static __device__ __forceinline__ void unpack(const uint4& a, float* x) {
+  static __device__ __forceinline__ void unpack(const uint4& a, uint64_t (&x)[4]) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  static __device__ __forceinline__ uint4 pack(const uint64_t (&x)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f32x2_split(x[i], lo, hi);
+      w[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
-template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(32 * kRopeWarps)
+// Two neighbouring weights (of an even index).
+__device__ __forceinline__ float2 load_weights(const void* p, bool f32, int at) {
+  if (p == nullptr) return make_float2(1.f, 1.f);
+  if (f32) return __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + at));
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + at));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <typename T, RopePairs kPairs>
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas)
 qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane16<T>;
-  constexpr int kVec = L::kVec;
+  constexpr int kVec = L::kVec, kHalfVec = kVec / 2;
   constexpr int kLanes = kHeadDim / kVec;      // lanes a head
   constexpr int kHeads = 32 / kLanes;          // heads a warp step
-  constexpr int kSteps = 4;                    // steps in flight
-  __shared__ float2 table[kRopeWarps][32];     // cos, sin of the row's angles
+  constexpr int kSteps = 2;                    // steps in flight, of each side
+  __shared__ float2 table[kRopeWarps][kHeadDim / 2];   // cos, sin of the row's angles
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
   if (t >= a.rows) return;                     // (warps do not wait for one another)
@@ -165,20 +197,25 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   if (pos < 0) return;                         // a row in no sequence
   const int half = a.rotary >> 1;
   const int l = lane % kLanes, sub = lane / kLanes;
-  const int q_steps = (a.q.heads + kHeads - 1) / kHeads, k_steps = (a.k.heads + kHeads - 1) / kHeads;
-  const int steps = q_steps + k_steps;
+  // This lane's values: kVec of them from d0 on, or (kWhole) kHalfVec from d0
+  // and from d0 + 32 on.
+  const int d0 = kPairs == kWhole ? l * kHalfVec : l * kVec;
 
-  uint4 raw[kSteps];
-  auto load = [&](int s, uint4& x) {
-    const bool is_q = s < q_steps;
-    const RopeArgs::Side& side = is_q ? a.q : a.k;
-    const int head = (is_q ? s : s - q_steps) * kHeads + sub;
-    x = make_uint4(0u, 0u, 0u, 0u);
-    if (s < steps && head < side.heads)
-      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(side.in) + t * side.in_stride + head * kHeadDim + l * kVec);
+  auto load = [&](const T* row, int heads, int step) -> uint4 {
+    const int head = step * kHeads + sub;
+    if (head >= heads) return make_uint4(0u, 0u, 0u, 0u);
+    const T* p = row + head * kHeadDim + d0;
+    if (kPairs != kWhole) return *reinterpret_cast<const uint4*>(p);
+    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + kHeadDim / 2);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
   };
+  const T* row_q = static_cast<const T*>(a.q.in) + t * a.q.in_stride;
+  const T* row_k = static_cast<const T*>(a.k.in) + t * a.k.in_stride;
+  uint4 raw_q[kSteps], raw_k[kSteps];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) load(i, raw[i]);
+  for (int i = 0; i < kSteps; ++i) raw_q[i] = load(row_q, a.q.heads, i);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) raw_k[i] = load(row_k, a.k.heads, i);
 
   if (lane < half) {
     const uint64_t turn = a.freq[lane] * static_cast<uint64_t>(pos);
@@ -188,68 +225,103 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     table[warp][lane] = make_float2(c, s);
   }
   __syncwarp();
-  // This lane's angles: kVec / 2 neighbouring pairs, or kVec dimensions of
-  // one half of the rotated part.
-  const int d0 = l * kVec;
-  const bool rotated = d0 < a.rotary;
-  const bool upper = d0 >= half;
-  const int partner = lane + (rotated ? (upper ? -(half / kVec) : half / kVec) : 0);
-  float c[kVec], s[kVec];
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) {
-    const int f = kInterleaved ? (d0 + e) >> 1 : (upper ? d0 - half : d0) + e;
-    const float2 cs = rotated ? table[warp][f] : make_float2(1.f, 0.f);
-    c[e] = cs.x;
-    s[e] = kInterleaved ? cs.y : (upper ? cs.y : -cs.y);
-  }
+  const bool rotated = kPairs == kWhole || d0 < a.rotary;
+  const bool upper = kPairs == kPart && d0 >= half;
+  // kPart: the lane with the partners, and their first dimension.
+  const int away = kPairs == kPart && rotated ? (upper ? -half : half) : 0;
+  const int partner = lane + away / kVec;
 
-  for (int s0 = 0; s0 < steps; s0 += kSteps) {
+  auto run_side = [&](const RopeArgs::Side& side, const T* row, uint4 (&raw)[kSteps]) {
+    uint64_t own[kHalfVec], other[kHalfVec];   // by pairs of values
+    auto factors = [&](int w0) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int st = s0 + i;
-      if (st >= steps) break;
-      const bool is_q = st < q_steps;
-      const RopeArgs::Side& side = is_q ? a.q : a.k;
-      const int head = (is_q ? st : st - q_steps) * kHeads + sub;
-      float x[kVec];
-      L::unpack(raw[i], x);
-      load(st + kSteps, raw[i]);
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int m = kLanes / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      const float r = 1.f / sqrtf(ss * (1.f / kHeadDim) + a.eps);
-      const int wo = (head < side.heads ? head : 0) * side.w_stride + d0;
-      if (side.weight == nullptr) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[e] *= r;
-      } else if (a.weight_f32) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[e] *= r * __ldg(static_cast<const float*>(side.weight) + wo + e);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          x[e] *= r * __bfloat162float(static_cast<const __nv_bfloat16*>(side.weight)[wo + e]);
-      }
-      float y[kVec];
-      if (kInterleaved) {
-#pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          y[e] = x[e] * c[e] - x[e + 1] * s[e];
-          y[e + 1] = x[e + 1] * c[e] + x[e] * s[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float other = __shfl_sync(0xffffffffu, x[e], partner);
-          y[e] = rotated ? fmaf(other, s[e], x[e] * c[e]) : x[e];
+      for (int e = 0; e < kVec; e += 2) {
+        if (kPairs == kNext) {
+          const float2 w = load_weights(side.weight, a.weight_f32, w0 + d0 + e);
+          const float2 cs = rotated ? table[warp][(d0 + e) >> 1] : make_float2(1.f, 0.f);
+          own[e / 2] = f32x2(cs.x * w.x, cs.x * w.y);
+          other[e / 2] = f32x2(-cs.y * w.y, cs.y * w.x);
+        } else {
+          const bool second = kPairs == kWhole ? e >= kHalfVec : upper;
+          const int d = kPairs == kWhole ? d0 + e % kHalfVec + (second ? kHeadDim / 2 : 0) : d0 + e;
+          const int pd = kPairs == kWhole ? (second ? d - kHeadDim / 2 : d + kHeadDim / 2) : d + away;
+          const float2 w = load_weights(side.weight, a.weight_f32, w0 + d), pw = load_weights(side.weight, a.weight_f32, w0 + pd);
+          const int f = second ? pd : d;
+          const float2 cs0 = rotated ? table[warp][f] : make_float2(1.f, 0.f);
+          const float2 cs1 = rotated ? table[warp][f + 1] : make_float2(1.f, 0.f);
+          own[e / 2] = f32x2(cs0.x * w.x, cs1.x * w.y);
+          other[e / 2] = second ? f32x2(cs0.y * pw.x, cs1.y * pw.y) : f32x2(-cs0.y * pw.x, -cs1.y * pw.y);
         }
       }
-      if (head < side.heads)
-        *reinterpret_cast<uint4*>(static_cast<T*>(side.out) + t * side.out_stride + head * kHeadDim + d0) = L::pack(y);
+    };
+    if (side.w_stride == 0) factors(0);
+    T* out = static_cast<T*>(side.out) + t * side.out_stride;
+    const int heads = side.heads;
+    const int steps = (heads + kHeads - 1) / kHeads;
+    for (int s0 = 0; s0 < steps; s0 += kSteps) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        if (s0 + i >= steps) break;
+        const int head = (s0 + i) * kHeads + sub;
+        if (side.w_stride != 0) factors((head < heads ? head : 0) * side.w_stride);
+        const uint4 mine = raw[i];
+        raw[i] = load(row, heads, s0 + i + kSteps);
+        uint64_t x[kHalfVec], z[kHalfVec];
+        L::unpack(mine, x);
+        if (kPairs == kPart) {
+          const uint4 theirs = make_uint4(__shfl_sync(0xffffffffu, mine.x, partner), __shfl_sync(0xffffffffu, mine.y, partner),
+                                          __shfl_sync(0xffffffffu, mine.z, partner), __shfl_sync(0xffffffffu, mine.w, partner));
+          L::unpack(theirs, z);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kHalfVec; ++e) {
+            if (kPairs == kWhole) {
+              z[e] = x[(e + kHalfVec / 2) % kHalfVec];
+            } else {
+              float lo, hi;
+              f32x2_split(x[e], lo, hi);
+              z[e] = f32x2(hi, lo);
+            }
+          }
+        }
+        uint64_t ss2 = mul_f32x2(x[0], x[0]);
+#pragma unroll
+        for (int e = 1; e < kHalfVec; ++e) ss2 = fma_f32x2(x[e], x[e], ss2);
+        float ss, hi;
+        f32x2_split(ss2, ss, hi);
+        ss += hi;
+#pragma unroll
+        for (int m = kLanes / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float r = rsqrtf(fmaf(ss, 1.f / kHeadDim, a.eps));
+        const uint64_t r2 = f32x2(r, r);
+#pragma unroll
+        for (int e = 0; e < kHalfVec; ++e) {
+          uint64_t y = mul_f32x2(x[e], own[e]);
+          if (rotated) y = fma_f32x2(z[e], other[e], y);   // (a partner's infinity stays out of dimensions that have none)
+          x[e] = mul_f32x2(y, r2);
+        }
+        if (head < heads) {
+          const uint4 y = L::pack(x);
+          T* p = out + head * kHeadDim + d0;
+          if (kPairs == kWhole) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(y.x, y.y);
+            *reinterpret_cast<uint2*>(p + kHeadDim / 2) = make_uint2(y.z, y.w);
+          } else {
+            *reinterpret_cast<uint4*>(p) = y;
+          }
+        }
+      }
     }
-  }
+  };
+  run_side(a.q, row_q, raw_q);
+  run_side(a.k, row_k, raw_k);
+}
+
+template <typename T>
+void run_rope(const RopeArgs& a, bool interleaved, unsigned grid, cudaStream_t stream) {
+  if (interleaved) qk_norm_rope_kernel<T, kNext><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
+  else if (a.rotary == kHeadDim) qk_norm_rope_kernel<T, kWhole><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
+  else qk_norm_rope_kernel<T, kPart><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -279,13 +351,8 @@ cudaError_t launch_decay_step(const StepArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool f32, bool interleaved, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((a.rows + kRopeWarps - 1) / kRopeWarps);
-  if (f32) {
-    if (interleaved) qk_norm_rope_kernel<float, true><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
-    else qk_norm_rope_kernel<float, false><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
-  } else {
-    if (interleaved) qk_norm_rope_kernel<__nv_bfloat16, true><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
-    else qk_norm_rope_kernel<__nv_bfloat16, false><<<grid, 32 * kRopeWarps, 0, stream>>>(a);
-  }
+  if (f32) run_rope<float>(a, interleaved, grid, stream);
+  else run_rope<__nv_bfloat16>(a, interleaved, grid, stream);
   return cudaGetLastError();
 }
 

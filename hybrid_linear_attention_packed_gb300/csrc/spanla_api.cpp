@@ -2514,7 +2514,6 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
       a.freq[i] = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
     }
     const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4;
-    const int64_t wsz = weight_dtype == SPAN_LA_BF16 ? 2 : 4;
     Rows in[2], out[2];
     const span_la_qk_side* sides[2] = {&q, &k};
     RopeArgs::Side* to[2] = {&a.q, &a.k};
@@ -2530,8 +2529,8 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
             (x.in_row_stride * esz) % 16 != 0 || (x.out_row_stride * esz) % 16 != 0)
           return fail(SPAN_LA_ERR_INVALID, "%s: row strides must be at least num_heads * 64 elements, below 2^31, and a "
                       "multiple of 16 bytes", name);
-        if (x.weight != nullptr && (reinterpret_cast<uintptr_t>(x.weight) & static_cast<uintptr_t>(wsz - 1)) != 0)
-          return fail(SPAN_LA_ERR_INVALID, "%s: weight must be aligned to its type", name);
+        if (x.weight != nullptr && !aligned16(x.weight))
+          return fail(SPAN_LA_ERR_INVALID, "%s: weight must be 16-byte aligned", name);
       }
       in[i] = {reinterpret_cast<uintptr_t>(x.in), x.in_row_stride * esz, width * esz, rows};
       out[i] = {reinterpret_cast<uintptr_t>(x.out), x.out_row_stride * esz, width * esz, rows};

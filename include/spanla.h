@@ -522,7 +522,7 @@ span_la_status span_la_decay_step(const void *q, const void *k, const void *v,
 typedef struct {
     const void *in;          /* device, 16-byte aligned */
     void *out;               /* device, 16-byte aligned; may be `in` (same stride) */
-    const void *weight;      /* device [64], or [num_heads][64], or NULL (ones) */
+    const void *weight;      /* device [64], or [num_heads][64], 16-byte aligned, or NULL (ones) */
     int64_t in_row_stride;
     int64_t out_row_stride;
     int32_t num_heads;       /* 0: nothing on this side */
