@@ -46,10 +46,11 @@
 //   warp 2      O issuer: P V, then Q S.
 //   warps 3-10  phase 1: V' (16 bytes of V at a time; rows past the tile become
 //               zero).  Then P, two warps per TMEM lane quarter, one per
-//               64-column half; V's rows past the tile, infinities and NaNs
-//               become zero first (see add_nonfinite).
-//   warps 11-18 states and output: 16 columns of one state row per thread.
-//               Phase 1: the piece states.  Then S staged in bf16, O stored.
+//               64-column half (V's rows past the tile, infinities and NaNs
+//               become zero first, see add_nonfinite), and S, staged in bf16
+//               while P V runs.
+//   warps 11-18 phase 1: the piece states, 16 columns of one state row per
+//               thread.  Then O, 32 columns of one row per thread.
 #include "decay_math.cuh"
 #include "span_tiles.cuh"
 #include "spanla_internal.h"
@@ -137,7 +138,6 @@ struct DecayParams {
   const DecayPiece* p1;
   unsigned* counter;
   unsigned target;
-  int a_rows;
   int H;
   int n_p1_ctas;
 };
@@ -151,6 +151,11 @@ __device__ __forceinline__ Start load_start(const DecayTile* p) {
   const int4 b = __ldg(reinterpret_cast<const int4*>(p) + 1);
   const int2 c = __ldg(reinterpret_cast<const int2*>(p) + 4);
   return Start{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y};
+}
+struct Out { int32_t row0, nrows, head, flags; };   // (output)
+__device__ __forceinline__ Out load_out(const DecayTile* p) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(p));
+  return Out{a.x, a.y, a.z, a.w};
 }
 struct Mask {    // rows and segment starts (conversion)
   int32_t nrows, head, flags, bound0;
@@ -270,7 +275,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(bar(L::kOReady + b), 2);
       mbar_init(bar(L::kPFree + b), 1);
       mbar_init(bar(L::kOFree + b), kGroupThreads);
-      mbar_init(bar(L::kSSmem + b), kGroupThreads);
+      mbar_init(bar(L::kSSmem + b), kConvThreads);
       mbar_init(bar(L::kP1Ready + b), 1);
       mbar_init(bar(L::kP1Free + b), kGroupThreads);
       mbar_init(bar(L::kVReady + b), kConvThreads);
@@ -526,6 +531,141 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         mbar_arrive(bar(L::kVReady + (u & 1)));
       }
     }
+
+    // Phase 2.  Each thread holds 16 columns of one row of the start state of
+    // the piece at hand, in the places the output warps have theirs in phase 1:
+    // lanes 0..63 and 64..127 of tensor memory are rows d = row & 63, the lower
+    // for columns 0..31, the upper for 32..63, and the quarter's two warps take
+    // 16 of those each.
+    const int d = row & 63, sh = row >> 6;
+    const int col0 = 32 * sh + 16 * half;
+    const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
+    // tag_run names the start state in s_run, tag_op the one each S operand
+    // holds; -1: none (see k_span_output.cu).
+    float s_run[16];
+    int64_t tag_run = -1, tag_op0 = -1, tag_op1 = -1;
+    auto carry_tag = [&](int view, int head) -> int64_t {
+      return (static_cast<int64_t>(1) << 62) | (static_cast<int64_t>(view) << 16) | head;
+    };
+    auto start_tag = [&](const Start& r) -> int64_t {
+      if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
+      if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
+      return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
+             ((static_cast<int64_t>(r.stateB) + 1) << 16) ^ (static_cast<int64_t>(r.b_n) << 10) ^
+             static_cast<int64_t>(r.head);
+    };
+    // Wait (bounded), once, for this CTA's phase 1 to have been written out.
+    bool p1_over = n_p1 == 0;
+    auto wait_p1 = [&](bool live) -> bool {
+      if (p1_over) return live;
+      p1_over = true;
+      return live && __all_sync(0xffffffffu, wait_or_flag(bar(L::kP1Done), 0, err, kErrTimeoutMma));
+    };
+    // Wait (bounded) until every CTA whose slots others read has counted
+    // itself, once, before the first read of such a slot.  (Each warp for
+    // itself: a warp whose waits ran out has left the loop.)
+    bool synced = prm.n_p1_ctas == 0;
+    auto grid_sync = [&]() {
+      if (synced) return;
+      synced = true;
+      if (lane == 0) {
+        const unsigned long long t0 = global_timer_ns();
+        while (ld_acquire_gpu(prm.counter) != prm.target) {
+          if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrTimeoutMma);
+            break;
+          }
+          __nanosleep(64);
+        }
+      }
+      __syncwarp();
+    };
+    // This thread's slice of a state in the usual layout.
+    auto load_row = [&](const float* p) {
+      const float4* p4 = reinterpret_cast<const float4*>(p + slice);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = __ldcg(p4 + c);
+        s_run[4 * c] = x.x; s_run[4 * c + 1] = x.y; s_run[4 * c + 2] = x.z; s_run[4 * c + 3] = x.w;
+      }
+    };
+    // s_run <- a^rows s_run + slot k.
+    auto add_slot = [&](int k) {
+      const float2 f2 = __ldcg(prm.ws_factor + k);
+      const Factor f{f2.x, f2.y};
+      const float4* p = reinterpret_cast<const float4*>(prm.ws + static_cast<int64_t>(k) * kStateFloats) + ct;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = __ldcg(p + kConvThreads * c);
+        s_run[4 * c] = f.step(s_run[4 * c], x.x);
+        s_run[4 * c + 1] = f.step(s_run[4 * c + 1], x.y);
+        s_run[4 * c + 2] = f.step(s_run[4 * c + 2], x.z);
+        s_run[4 * c + 3] = f.step(s_run[4 * c + 3], x.w);
+      }
+    };
+    // s_run becomes the start state of the piece of tile `r`: zero, the final
+    // state this CTA computed (carry), the one it holds already, or term A (a
+    // kept state, or the parent view-head's pieces) and term B (the segment's
+    // earlier pieces) by Horner's rule.
+    auto start_piece = [&](const Start& r) {
+      const int64_t tag = start_tag(r);
+      if (tag >= 0 && tag == tag_run) return;
+      tag_run = tag;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
+      if (tag < 0) return;
+      if (r.flags & kTileCarry) {   // (a long branch ran in between: as this thread wrote it)
+        load_row(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats);
+        return;
+      }
+      const bool kept = prm.final_out == nullptr;
+      if (r.b_n > 0 || !kept) grid_sync();
+      if (kept) load_row(prm.stateA + (static_cast<int64_t>(r.stateA) * H + r.head) * kStateFloats);
+      else
+#pragma unroll 2
+        for (int k = 0; k < r.a_n; ++k) add_slot(r.stateA + k);
+#pragma unroll 2
+      for (int k = 0; k < r.b_n; ++k) add_slot(r.stateB + k);
+    };
+    // A view-head's final state: its last piece's start state decayed over the
+    // piece, plus the piece's own state.
+    auto final_state = [&](const Start& r) {
+      add_slot(r.slot);
+      store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
+      tag_run = carry_tag(r.final_idx, r.head);
+    };
+    // S(i) -> S operand i & 1, unless it holds that start state already: the
+    // start state for a piece's first tile, else a^rows times it plus the
+    // table's entry in the tile's stage, `rows` rows into the piece.
+    auto stage = [&](int i, int u, const Start& r, float l2, int rows) {
+      uint8_t* op = smem + L::kS + (i & 1) * kSOpBytes;
+      if (r.flags & kTileFirst) {
+        const int64_t tag = start_tag(r);
+        const int64_t held = (i & 1) ? tag_op1 : tag_op0;
+        if (tag >= 0 && tag != held) {
+          stage_state_slice(op, d, col0, s_run);
+          if (i & 1) tag_op1 = tag; else tag_op0 = tag;
+        }
+      } else {
+        if (i & 1) tag_op1 = -1; else tag_op0 = -1;
+        const float f = decay_pow_fast(l2, static_cast<float>(rows));
+        const float4* x = reinterpret_cast<const float4*>(smem + L::kTable + (u % kStages) * (kStateFloats * 4)) + ct;
+        float y[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 xc = x[kConvThreads * c];
+          y[4 * c] = fmaf(f, s_run[4 * c], xc.x);
+          y[4 * c + 1] = fmaf(f, s_run[4 * c + 1], xc.y);
+          y[4 * c + 2] = fmaf(f, s_run[4 * c + 2], xc.z);
+          y[4 * c + 3] = fmaf(f, s_run[4 * c + 3], xc.w);
+        }
+        stage_state_slice(op, d, col0, y);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(L::kSSmem + (i & 1)));
+    };
+
+    int rows_before = 0;   // rows of the piece before the tile
     Mask nxt = n > 0 ? load_mask4(list) : Mask{};
     float nxt_l2 = n > 0 ? decay_log2(load_log_decay(prm.log_decay, nxt.head)) : 0.f;
     for (int i = 0; i < n && ok; ++i, ++u) {
@@ -641,6 +781,21 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(bar(L::kPDone + b));
+
+      // S(i).  (The record's rest is in the L1: the mask came from it.)
+      const Start w = load_start(list + i);
+      ok = wait_p1(ok);
+      if (w.flags & kTileFirst) {
+        rows_before = 0;
+        start_piece(w);
+      }
+      // The operand was last read by Q S of tile i-2.
+      if (ok && i >= 2) ok = wait_or_flag(bar(L::kOReady + b), ((i - 2) >> 1) & 1, err, kErrTimeoutMma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      stage(i, u, w, l2, rows_before);
+      rows_before += w.nrows;
+      if (w.flags & kTileFinalOut) final_state(w);
     }
   } else {
     // ------------------------------------------------------------ state and output
@@ -653,10 +808,10 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // and the quarter's two warps take 16 of those each.
     const int d = row & 63, sh = row >> 6;
     const int col0 = 32 * sh + 16 * pi;
-    const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
     bool ok = true;
-    // The table holds a state as this group's threads hold it: float4 c of
-    // thread g at c * 256 + g, so that each writes and reads whole lines.
+    // The table and the slots hold a state as this group's threads hold it, and
+    // the conversion warps' that read it: float4 c of thread g at c * 256 + g,
+    // so that each writes and reads whole lines.
     const int g = tid - kStateWarp0 * 32;
     auto table_at = [&](int64_t entry) { return reinterpret_cast<float4*>(prm.table + entry * kStateFloats) + g; };
 
@@ -701,191 +856,32 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         if (!ok) break;
         if (sd.slot >= 0) {
-          store_slice(prm.ws + static_cast<int64_t>(sd.slot) * kStateFloats + slice, s);
+          float4* p = reinterpret_cast<float4*>(prm.ws + static_cast<int64_t>(sd.slot) * kStateFloats) + g;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) p[kGroupThreads * c] = make_float4(s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
           if (g == 0) {
             const Factor f = factor_of(ld, static_cast<float>(sd.len));
             prm.ws_factor[sd.slot] = make_float2(f.hi, f.lo);
           }
         }
       }
-      // (the producer reads the table by bulk copies)
+      // (the producer reads the table by bulk copies, the conversion warps of
+      // this and other CTAs the slots)
       asm volatile("fence.proxy.async;" ::: "memory");
+      __threadfence();
       mbar_arrive(bar(L::kP1Done));
       if (counted) {
-        __threadfence();
         named_barrier_sync(kNamedStateBar, kGroupThreads);
         if (g == 0) atomicAdd(prm.counter, 1u);
       }
     }
-    // Wait (bounded) until every CTA whose slots others read has counted
-    // itself, once, before the first read of such a slot.
-    bool synced = prm.n_p1_ctas == 0;
-    auto grid_sync = [&]() {
-      if (synced) return;
-      synced = true;
-      if (g == 0) {
-        const unsigned long long t0 = global_timer_ns();
-        while (ld_acquire_gpu(prm.counter) != prm.target) {
-          if (global_timer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, kErrTimeoutMma);
-            break;
-          }
-          __nanosleep(64);
-        }
-      }
-      named_barrier_sync(kNamedStateBar, kGroupThreads);
-    };
-
-    // The start state of the piece at hand (row d, columns col0 ..), fp32.
-    // tag_run names it, tag_op the start state each S operand holds; -1: none
-    // (see k_span_output.cu).
-    float s_run[16];
-    int64_t tag_run = -1, tag_op0 = -1, tag_op1 = -1;
-    auto carry_tag = [&](int view, int head) -> int64_t {
-      return (static_cast<int64_t>(1) << 62) | (static_cast<int64_t>(view) << 16) | head;
-    };
-    auto start_tag = [&](const Start& r) -> int64_t {
-      if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
-      if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
-      return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
-             ((static_cast<int64_t>(r.stateB) + 1) << 16) ^ (static_cast<int64_t>(r.b_n) << 10) ^
-             static_cast<int64_t>(r.head);
-    };
-    // Term A (a kept state, or the parent view-head's pieces) and term B (the
-    // segment's earlier pieces), in order, by Horner's rule into s_run:
-    // S <- a^rows S + piece.  Two states in flight; through S operand t & 1
-    // (coalesced reads, XOR-swizzled on the half-row) into the threads' slices.
-    auto sum_start = [&](int t, const Start& r) {
-      const int na = r.a_n, total = r.a_n + r.b_n;
-      const bool kept = prm.a_rows > 1 || prm.final_out == nullptr;   // term A is a kept state
-      const float* pa =
-          na > 0 ? prm.stateA + (static_cast<int64_t>(r.stateA) * prm.a_rows + (kept ? r.head : 0)) * kStateFloats : nullptr;
-      const float* pb = r.b_n > 0 ? prm.ws + static_cast<int64_t>(r.stateB) * kStateFloats : nullptr;
-      auto src = [&](int k) -> const float4* {
-        return reinterpret_cast<const float4*>(k < na ? pa + static_cast<int64_t>(k) * kStateFloats
-                                                      : pb + static_cast<int64_t>(k - na) * kStateFloats) + g;
-      };
-      auto factor = [&](int k) -> Factor {
-        if (k == 0) return Factor{0.f, 0.f};   // nothing before it
-        const float2 f = __ldcg(prm.ws_factor + (k < na ? r.stateA + k : r.stateB + k - na));
-        return Factor{f.x, f.y};
-      };
-      float4 acc[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add4 = [](float4& x, const Factor f, const float4 y) {
-        x.x = f.step(x.x, y.x); x.y = f.step(x.y, y.y); x.z = f.step(x.z, y.z); x.w = f.step(x.w, y.w);
-      };
-      for (int k = 0; k < total; k += 2) {
-        const bool two = k + 1 < total;
-        const float4* p0 = src(k);
-        const float4* p1 = src(two ? k + 1 : k);
-        float4 x[4], y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = __ldcg(p0 + kGroupThreads * c);
-        const Factor f0 = factor(k);
-        if (two) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) y[c] = __ldcg(p1 + kGroupThreads * c);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) add4(acc[c], f0, x[c]);
-        if (two) {
-          const Factor f1 = factor(k + 1);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) add4(acc[c], f1, y[c]);
-        }
-      }
-      float4* buf = reinterpret_cast<float4*>(smem + L::kS + (t & 1) * kSOpBytes);
-      if (t & 1) tag_op1 = -1; else tag_op0 = -1;
-      // The buffer holds two warps' O staging: their TMA stores must have read it.
-      if (lane == 0) bulk_wait_read_all();
-      named_barrier_sync(kNamedStateBar, kGroupThreads);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int f = g + kGroupThreads * c, hr = f >> 3;
-        buf[hr * 8 + ((f & 7) ^ ((hr >> 1) & 7))] = acc[c];
-      }
-      named_barrier_sync(kNamedStateBar, kGroupThreads);
-      const int hr = 2 * d + sh;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 v4 = buf[hr * 8 + ((4 * pi + c) ^ ((hr >> 1) & 7))];
-        s_run[4 * c] = v4.x; s_run[4 * c + 1] = v4.y; s_run[4 * c + 2] = v4.z; s_run[4 * c + 3] = v4.w;
-      }
-      named_barrier_sync(kNamedStateBar, kGroupThreads);
-    };
-    // The running state becomes the start state of the piece starting at `r`.
-    auto start_piece = [&](int t, const Start& r) {
-      if (!(r.flags & kTileHasInit)) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
-        tag_run = -1;
-        return;
-      }
-      const int64_t tag = start_tag(r);
-      if (tag == tag_run) return;
-      tag_run = tag;
-      if (r.flags & kTileCarry) {
-        // (a long branch ran in between: this thread's own slice, as it wrote it)
-        const float4* p4 = reinterpret_cast<const float4*>(
-            prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 v4 = __ldcg(p4 + c);
-          s_run[4 * c] = v4.x; s_run[4 * c + 1] = v4.y; s_run[4 * c + 2] = v4.z; s_run[4 * c + 3] = v4.w;
-        }
-        return;
-      }
-      grid_sync();
-      sum_start(t, r);
-    };
-
-    // S(t) -> S operand t & 1, unless it holds that start state already: the
-    // start state for a piece's first tile, else a^rows times it plus the
-    // table's entry in the tile's stage, `rows` rows into the piece.  The
-    // operand was last read by Q S of tile t-2, whose completion o_work(t-2)
-    // saw.  (The stage is released behind Q S, so behind this.)
-    auto stage = [&](int t, const Start& r, float l2, int rows, bool live) -> bool {
-      uint8_t* op = smem + L::kS + (t & 1) * kSOpBytes;
-      if (r.flags & kTileFirst) {
-        const int64_t tag = start_tag(r);
-        const int64_t held = (t & 1) ? tag_op1 : tag_op0;
-        if ((r.flags & kTileHasInit) && !(tag >= 0 && tag == held)) {
-          stage_state_slice(op, d, col0, s_run);
-          if (t & 1) tag_op1 = tag; else tag_op0 = tag;
-        }
-      } else {
-        if (t & 1) tag_op1 = -1; else tag_op0 = -1;
-        const int u = n1 + t;
-        if (live) live = __all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma));
-        if (!live) return false;
-        const float f = decay_pow_fast(l2, static_cast<float>(rows));
-        const float4* x = reinterpret_cast<const float4*>(smem + L::kTable + (u % kStages) * (kStateFloats * 4)) + g;
-        float y[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 xc = x[kGroupThreads * c];
-          y[4 * c] = fmaf(f, s_run[4 * c], xc.x);
-          y[4 * c + 1] = fmaf(f, s_run[4 * c + 1], xc.y);
-          y[4 * c + 2] = fmaf(f, s_run[4 * c + 2], xc.z);
-          y[4 * c + 3] = fmaf(f, s_run[4 * c + 3], xc.w);
-        }
-        stage_state_slice(op, d, col0, y);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(L::kSSmem + (t & 1)));
-      return live;
-    };
-
     // O(i) = P V + a^(i-s(i)+1) Q S -> global (rows of the tile only), through
     // this warp's O staging when its 32 rows all lie in the tile (one TMA
     // store), else row by row.
     bool o_pending = false;   // this warp's last TMA store may still read its staging
-    auto o_work = [&](int i, const Start& r, float l2, bool live) -> bool {
+    auto o_work = [&](int i, const Out& r, float l2) -> bool {
       const int b = i & 1;
-      if (!live || !__all_sync(0xffffffffu, wait_or_flag(bar(L::kOReady + b), (i >> 1) & 1, err, kErrTimeoutMma)))
-        return false;
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kOReady + b), (i >> 1) & 1, err, kErrTimeoutMma))) return false;
       tc_fence_after_sync();
       const uint32_t colO = b ? kColO1 : kColO0;
       const bool whole = (quarter + 1) * 32 <= r.nrows;
@@ -947,54 +943,16 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       return true;
     };
 
-    // A view-head's final state: its last piece's start state decayed over the
-    // piece, plus the piece's own state.
-    auto final_state = [&](const Start& r, int rows) {
-      const float4* p = reinterpret_cast<const float4*>(prm.ws + static_cast<int64_t>(r.slot) * kStateFloats + slice);
-      const Factor f = factor_of(load_log_decay(prm.log_decay, r.head), static_cast<float>(rows));
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 x = __ldcg(p + c);   // (this thread's own, as it wrote it)
-        s_run[4 * c] = f.step(s_run[4 * c], x.x);
-        s_run[4 * c + 1] = f.step(s_run[4 * c + 1], x.y);
-        s_run[4 * c + 2] = f.step(s_run[4 * c + 2], x.z);
-        s_run[4 * c + 3] = f.step(s_run[4 * c + 3], x.w);
+    Out nxt = n > 0 ? load_out(list) : Out{};
+    float nxt_l2 = n > 0 ? decay_log2(load_log_decay(prm.log_decay, nxt.head)) : 0.f;
+    for (int i = 0; i < n && ok; ++i) {
+      const Out cur = nxt;
+      const float l2 = nxt_l2;
+      if (i + 1 < n) {
+        nxt = load_out(list + i + 1);
+        nxt_l2 = decay_log2(load_log_decay(prm.log_decay, nxt.head));
       }
-      store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
-      tag_run = carry_tag(r.final_idx, r.head);
-    };
-
-    // The group's named barriers (in the start-state sum and the grid-wide
-    // wait) are reached by all warps alike: where they fall depends on the
-    // tiles and the start-state tags only.  A warp whose bounded wait ran out
-    // goes on through the loop without waiting or storing outputs.
-    if (n > 0) {
-      Start cur = load_start(list);
-      Start nxt = n > 1 ? load_start(list + 1) : Start{};
-      float l2 = decay_log2(load_log_decay(prm.log_decay, cur.head));
-      int rows = 0;               // rows of the piece before the tile to stage
-      start_piece(0, cur);
-      ok = stage(0, cur, l2, 0, ok);
-      for (int i = 0; i < n; ++i) {
-        float l2_next = l2;
-        if (i + 1 < n) {
-          // S(i+1) first: the O issuer needs it right after P V of tile i+1.
-          rows += cur.nrows;
-          if (cur.flags & kTileFinalOut) final_state(cur, rows);
-          if (cur.flags & kTileLast) {
-            l2_next = decay_log2(load_log_decay(prm.log_decay, nxt.head));
-            rows = 0;
-            start_piece(i + 1, nxt);
-          }
-          ok = stage(i + 1, nxt, l2_next, rows, ok);
-        } else if (cur.flags & kTileFinalOut) {
-          final_state(cur, rows + cur.nrows);
-        }
-        ok = o_work(i, cur, l2, ok);
-        cur = nxt;
-        l2 = l2_next;
-        if (i + 2 < n) nxt = load_start(list + i + 2);
-      }
+      ok = o_work(i, cur, l2);
     }
     if (lane == 0) bulk_wait_all();   // the last O stores have completed
   }
@@ -1031,7 +989,6 @@ cudaError_t launch_span_decay(const CUtensorMap& tm_q, const CUtensorMap& tm_k, 
   p.p1 = a.p1;
   p.counter = a.counter;
   p.target = a.target;
-  p.a_rows = a.a_rows;
   p.H = a.H;
   p.n_p1_ctas = a.n_p1_ctas;
   cudaLaunchConfig_t cfg = {};

@@ -1674,8 +1674,7 @@ span_la_status enqueue_span_decay(const DescBlock& desc, const uint8_t* block, f
   a.q = q;
   a.k = k;
   a.v = v;
-  a.stateA = kept != nullptr ? kept : states;
-  a.a_rows = kept != nullptr ? H : 1;
+  a.stateA = kept;
   a.ws = states;
   a.table = table;
   a.ws_factor = factors;

@@ -289,8 +289,7 @@ struct SpanDecayArgs {
   const void* q = nullptr;
   const void* k = nullptr;
   const void* v = nullptr;
-  const float* stateA = nullptr;   // term A: kept states [n][H][64][64] (a_rows = H, final_out NULL), or the slots
-  int a_rows = 1;
+  const float* stateA = nullptr;   // kept states [n][H][64][64] (final_out NULL): term A; else term A are slots
   float* ws = nullptr;             // slots
   float* table = nullptr;
   float2* ws_factor = nullptr;     // one per slot
