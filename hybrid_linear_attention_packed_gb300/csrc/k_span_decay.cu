@@ -46,11 +46,11 @@
 //   warp 2      O issuer: P V, then Q S.
 //   warps 3-10  phase 1: V' (16 bytes of V at a time; rows past the tile become
 //               zero).  Then P, two warps per TMEM lane quarter, one per
-//               64-column half (V's rows past the tile, infinities and NaNs
-//               become zero first, see add_nonfinite), and S, staged in bf16
-//               while P V runs.
+//               64-column half; V's rows past the tile, infinities and NaNs
+//               become zero first (see add_nonfinite).
 //   warps 11-18 phase 1: the piece states, 16 columns of one state row per
-//               thread.  Then O, 32 columns of one row per thread.
+//               thread.  Then S, staged in bf16, and O, 32 columns of one row
+//               per thread.
 #include "decay_math.cuh"
 #include "span_tiles.cuh"
 #include "spanla_internal.h"
@@ -151,11 +151,6 @@ __device__ __forceinline__ Start load_start(const DecayTile* p) {
   const int4 b = __ldg(reinterpret_cast<const int4*>(p) + 1);
   const int2 c = __ldg(reinterpret_cast<const int2*>(p) + 4);
   return Start{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y};
-}
-struct Out { int32_t row0, nrows, head, flags; };   // (output)
-__device__ __forceinline__ Out load_out(const DecayTile* p) {
-  const int4 a = __ldg(reinterpret_cast<const int4*>(p));
-  return Out{a.x, a.y, a.z, a.w};
 }
 struct Mask {    // rows and segment starts (conversion)
   int32_t nrows, head, flags, bound0;
@@ -275,7 +270,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(bar(L::kOReady + b), 2);
       mbar_init(bar(L::kPFree + b), 1);
       mbar_init(bar(L::kOFree + b), kGroupThreads);
-      mbar_init(bar(L::kSSmem + b), kConvThreads);
+      mbar_init(bar(L::kSSmem + b), kGroupThreads);
       mbar_init(bar(L::kP1Ready + b), 1);
       mbar_init(bar(L::kP1Free + b), kGroupThreads);
       mbar_init(bar(L::kVReady + b), kConvThreads);
@@ -531,141 +526,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         mbar_arrive(bar(L::kVReady + (u & 1)));
       }
     }
-
-    // Phase 2.  Each thread holds 16 columns of one row of the start state of
-    // the piece at hand, in the places the output warps have theirs in phase 1:
-    // lanes 0..63 and 64..127 of tensor memory are rows d = row & 63, the lower
-    // for columns 0..31, the upper for 32..63, and the quarter's two warps take
-    // 16 of those each.
-    const int d = row & 63, sh = row >> 6;
-    const int col0 = 32 * sh + 16 * half;
-    const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
-    // tag_run names the start state in s_run, tag_op the one each S operand
-    // holds; -1: none (see k_span_output.cu).
-    float s_run[16];
-    int64_t tag_run = -1, tag_op0 = -1, tag_op1 = -1;
-    auto carry_tag = [&](int view, int head) -> int64_t {
-      return (static_cast<int64_t>(1) << 62) | (static_cast<int64_t>(view) << 16) | head;
-    };
-    auto start_tag = [&](const Start& r) -> int64_t {
-      if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
-      if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
-      return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
-             ((static_cast<int64_t>(r.stateB) + 1) << 16) ^ (static_cast<int64_t>(r.b_n) << 10) ^
-             static_cast<int64_t>(r.head);
-    };
-    // Wait (bounded), once, for this CTA's phase 1 to have been written out.
-    bool p1_over = n_p1 == 0;
-    auto wait_p1 = [&](bool live) -> bool {
-      if (p1_over) return live;
-      p1_over = true;
-      return live && __all_sync(0xffffffffu, wait_or_flag(bar(L::kP1Done), 0, err, kErrTimeoutMma));
-    };
-    // Wait (bounded) until every CTA whose slots others read has counted
-    // itself, once, before the first read of such a slot.  (Each warp for
-    // itself: a warp whose waits ran out has left the loop.)
-    bool synced = prm.n_p1_ctas == 0;
-    auto grid_sync = [&]() {
-      if (synced) return;
-      synced = true;
-      if (lane == 0) {
-        const unsigned long long t0 = global_timer_ns();
-        while (ld_acquire_gpu(prm.counter) != prm.target) {
-          if (global_timer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, kErrTimeoutMma);
-            break;
-          }
-          __nanosleep(64);
-        }
-      }
-      __syncwarp();
-    };
-    // This thread's slice of a state in the usual layout.
-    auto load_row = [&](const float* p) {
-      const float4* p4 = reinterpret_cast<const float4*>(p + slice);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 x = __ldcg(p4 + c);
-        s_run[4 * c] = x.x; s_run[4 * c + 1] = x.y; s_run[4 * c + 2] = x.z; s_run[4 * c + 3] = x.w;
-      }
-    };
-    // s_run <- a^rows s_run + slot k.
-    auto add_slot = [&](int k) {
-      const float2 f2 = __ldcg(prm.ws_factor + k);
-      const Factor f{f2.x, f2.y};
-      const float4* p = reinterpret_cast<const float4*>(prm.ws + static_cast<int64_t>(k) * kStateFloats) + ct;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 x = __ldcg(p + kConvThreads * c);
-        s_run[4 * c] = f.step(s_run[4 * c], x.x);
-        s_run[4 * c + 1] = f.step(s_run[4 * c + 1], x.y);
-        s_run[4 * c + 2] = f.step(s_run[4 * c + 2], x.z);
-        s_run[4 * c + 3] = f.step(s_run[4 * c + 3], x.w);
-      }
-    };
-    // s_run becomes the start state of the piece of tile `r`: zero, the final
-    // state this CTA computed (carry), the one it holds already, or term A (a
-    // kept state, or the parent view-head's pieces) and term B (the segment's
-    // earlier pieces) by Horner's rule.
-    auto start_piece = [&](const Start& r) {
-      const int64_t tag = start_tag(r);
-      if (tag >= 0 && tag == tag_run) return;
-      tag_run = tag;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
-      if (tag < 0) return;
-      if (r.flags & kTileCarry) {   // (a long branch ran in between: as this thread wrote it)
-        load_row(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats);
-        return;
-      }
-      const bool kept = prm.final_out == nullptr;
-      if (r.b_n > 0 || !kept) grid_sync();
-      if (kept) load_row(prm.stateA + (static_cast<int64_t>(r.stateA) * H + r.head) * kStateFloats);
-      else
-#pragma unroll 2
-        for (int k = 0; k < r.a_n; ++k) add_slot(r.stateA + k);
-#pragma unroll 2
-      for (int k = 0; k < r.b_n; ++k) add_slot(r.stateB + k);
-    };
-    // A view-head's final state: its last piece's start state decayed over the
-    // piece, plus the piece's own state.
-    auto final_state = [&](const Start& r) {
-      add_slot(r.slot);
-      store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
-      tag_run = carry_tag(r.final_idx, r.head);
-    };
-    // S(i) -> S operand i & 1, unless it holds that start state already: the
-    // start state for a piece's first tile, else a^rows times it plus the
-    // table's entry in the tile's stage, `rows` rows into the piece.
-    auto stage = [&](int i, int u, const Start& r, float l2, int rows) {
-      uint8_t* op = smem + L::kS + (i & 1) * kSOpBytes;
-      if (r.flags & kTileFirst) {
-        const int64_t tag = start_tag(r);
-        const int64_t held = (i & 1) ? tag_op1 : tag_op0;
-        if (tag >= 0 && tag != held) {
-          stage_state_slice(op, d, col0, s_run);
-          if (i & 1) tag_op1 = tag; else tag_op0 = tag;
-        }
-      } else {
-        if (i & 1) tag_op1 = -1; else tag_op0 = -1;
-        const float f = decay_pow_fast(l2, static_cast<float>(rows));
-        const float4* x = reinterpret_cast<const float4*>(smem + L::kTable + (u % kStages) * (kStateFloats * 4)) + ct;
-        float y[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 xc = x[kConvThreads * c];
-          y[4 * c] = fmaf(f, s_run[4 * c], xc.x);
-          y[4 * c + 1] = fmaf(f, s_run[4 * c + 1], xc.y);
-          y[4 * c + 2] = fmaf(f, s_run[4 * c + 2], xc.z);
-          y[4 * c + 3] = fmaf(f, s_run[4 * c + 3], xc.w);
-        }
-        stage_state_slice(op, d, col0, y);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(L::kSSmem + (i & 1)));
-    };
-
-    int rows_before = 0;   // rows of the piece before the tile
     Mask nxt = n > 0 ? load_mask4(list) : Mask{};
     float nxt_l2 = n > 0 ? decay_log2(load_log_decay(prm.log_decay, nxt.head)) : 0.f;
     for (int i = 0; i < n && ok; ++i, ++u) {
@@ -781,21 +641,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(bar(L::kPDone + b));
-
-      // S(i).  (The record's rest is in the L1: the mask came from it.)
-      const Start w = load_start(list + i);
-      ok = wait_p1(ok);
-      if (w.flags & kTileFirst) {
-        rows_before = 0;
-        start_piece(w);
-      }
-      // The operand was last read by Q S of tile i-2.
-      if (ok && i >= 2) ok = wait_or_flag(bar(L::kOReady + b), ((i - 2) >> 1) & 1, err, kErrTimeoutMma);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      stage(i, u, w, l2, rows_before);
-      rows_before += w.nrows;
-      if (w.flags & kTileFinalOut) final_state(w);
     }
   } else {
     // ------------------------------------------------------------ state and output
@@ -809,9 +654,9 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int d = row & 63, sh = row >> 6;
     const int col0 = 32 * sh + 16 * pi;
     bool ok = true;
-    // The table and the slots hold a state as this group's threads hold it, and
-    // the conversion warps' that read it: float4 c of thread g at c * 256 + g,
-    // so that each writes and reads whole lines.
+    // The table and the slots hold a state as this group's threads hold it:
+    // float4 c of thread g at c * 256 + g, so that each writes and reads whole
+    // lines.
     const int g = tid - kStateWarp0 * 32;
     auto table_at = [&](int64_t entry) { return reinterpret_cast<float4*>(prm.table + entry * kStateFloats) + g; };
 
@@ -865,21 +710,144 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
         }
       }
-      // (the producer reads the table by bulk copies, the conversion warps of
-      // this and other CTAs the slots)
+      // (the producer reads the table by bulk copies, other CTAs the slots)
       asm volatile("fence.proxy.async;" ::: "memory");
       __threadfence();
       mbar_arrive(bar(L::kP1Done));
-      if (counted) {
-        named_barrier_sync(kNamedStateBar, kGroupThreads);
-        if (g == 0) atomicAdd(prm.counter, 1u);
-      }
+      named_barrier_sync(kNamedStateBar, kGroupThreads);   // (also for the slots' decays, which one thread writes)
+      if (counted && g == 0) atomicAdd(prm.counter, 1u);
     }
+    // Phase 2.  s_run is the start state of the piece at hand (row d, columns
+    // col0 ..).  tag_run names it, tag_op the start state each S operand holds;
+    // -1: none (see k_span_output.cu).
+    const int64_t slice = static_cast<int64_t>(d) * kHeadDim + col0;
+    float s_run[16];
+    int64_t tag_run = -1, tag_op0 = -1, tag_op1 = -1;
+    auto carry_tag = [&](int view, int head) -> int64_t {
+      return (static_cast<int64_t>(1) << 62) | (static_cast<int64_t>(view) << 16) | head;
+    };
+    auto start_tag = [&](const Start& r) -> int64_t {
+      if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
+      if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
+      return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
+             ((static_cast<int64_t>(r.stateB) + 1) << 16) ^ (static_cast<int64_t>(r.b_n) << 10) ^
+             static_cast<int64_t>(r.head);
+    };
+    // Wait (bounded) until every CTA whose slots others read has counted
+    // itself, once, before the first read of such a slot.  (Each warp for
+    // itself: a warp whose waits ran out has left the loop.)
+    bool synced = prm.n_p1_ctas == 0;
+    auto grid_sync = [&]() {
+      if (synced) return;
+      synced = true;
+      if (lane == 0) {
+        const unsigned long long t0 = global_timer_ns();
+        while (ld_acquire_gpu(prm.counter) != prm.target) {
+          if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrTimeoutMma);
+            break;
+          }
+          __nanosleep(64);
+        }
+      }
+      __syncwarp();
+    };
+    // This thread's slice of a state in the usual layout.
+    auto load_row = [&](const float* p) {
+      const float4* p4 = reinterpret_cast<const float4*>(p + slice);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = __ldcg(p4 + c);
+        s_run[4 * c] = x.x; s_run[4 * c + 1] = x.y; s_run[4 * c + 2] = x.z; s_run[4 * c + 3] = x.w;
+      }
+    };
+    // s_run <- a^rows s_run + slot k.
+    auto add_slot = [&](int k) {
+      const float2 f2 = __ldcg(prm.ws_factor + k);
+      const Factor f{f2.x, f2.y};
+      const float4* p = reinterpret_cast<const float4*>(prm.ws + static_cast<int64_t>(k) * kStateFloats) + g;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = __ldcg(p + kGroupThreads * c);
+        s_run[4 * c] = f.step(s_run[4 * c], x.x);
+        s_run[4 * c + 1] = f.step(s_run[4 * c + 1], x.y);
+        s_run[4 * c + 2] = f.step(s_run[4 * c + 2], x.z);
+        s_run[4 * c + 3] = f.step(s_run[4 * c + 3], x.w);
+      }
+    };
+    // s_run becomes the start state of the piece of tile `r`: zero, the final
+    // state this CTA computed (carry), the one it holds already, or term A (a
+    // kept state, or the parent view-head's pieces) and term B (the segment's
+    // earlier pieces) by Horner's rule.
+    auto start_piece = [&](const Start& r) {
+      const int64_t tag = start_tag(r);
+      if (tag >= 0 && tag == tag_run) return;
+      tag_run = tag;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s_run[e] = 0.f;
+      if (tag < 0) return;
+      if (r.flags & kTileCarry) {   // (a long branch ran in between: as this thread wrote it)
+        load_row(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats);
+        return;
+      }
+      const bool kept = prm.final_out == nullptr;
+      if (r.b_n > 0 || !kept) grid_sync();
+      if (kept) load_row(prm.stateA + (static_cast<int64_t>(r.stateA) * H + r.head) * kStateFloats);
+      else
+#pragma unroll 2
+        for (int k = 0; k < r.a_n; ++k) add_slot(r.stateA + k);
+#pragma unroll 2
+      for (int k = 0; k < r.b_n; ++k) add_slot(r.stateB + k);
+    };
+    // A view-head's final state: its last piece's start state decayed over the
+    // piece, plus the piece's own state.
+    auto final_state = [&](const Start& r) {
+      add_slot(r.slot);
+      store_slice(prm.final_out + (static_cast<int64_t>(r.final_idx) * H + r.head) * kStateFloats + slice, s_run);
+      tag_run = carry_tag(r.final_idx, r.head);
+    };
+    // S(i) -> S operand i & 1, unless it holds that start state already: the
+    // start state for a piece's first tile, else a^rows times it plus the
+    // table's entry in the tile's stage, `rows` rows into the piece.  The
+    // operand was last read by Q S of tile i-2, whose completion o_work(i-2)
+    // saw.  (The stage is released behind Q S, so behind this.)
+    auto stage = [&](int i, const Start& r, float l2, int rows) -> bool {
+      uint8_t* op = smem + L::kS + (i & 1) * kSOpBytes;
+      if (r.flags & kTileFirst) {
+        const int64_t tag = start_tag(r);
+        const int64_t held = (i & 1) ? tag_op1 : tag_op0;
+        if (tag >= 0 && tag != held) {
+          stage_state_slice(op, d, col0, s_run);
+          if (i & 1) tag_op1 = tag; else tag_op0 = tag;
+        }
+      } else {
+        if (i & 1) tag_op1 = -1; else tag_op0 = -1;
+        const int u = n1 + i;
+        if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma)))
+          return false;
+        const float f = decay_pow_fast(l2, static_cast<float>(rows));
+        const float4* x = reinterpret_cast<const float4*>(smem + L::kTable + (u % kStages) * (kStateFloats * 4)) + g;
+        float y[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 xc = x[kGroupThreads * c];
+          y[4 * c] = fmaf(f, s_run[4 * c], xc.x);
+          y[4 * c + 1] = fmaf(f, s_run[4 * c + 1], xc.y);
+          y[4 * c + 2] = fmaf(f, s_run[4 * c + 2], xc.z);
+          y[4 * c + 3] = fmaf(f, s_run[4 * c + 3], xc.w);
+        }
+        stage_state_slice(op, d, col0, y);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(L::kSSmem + (i & 1)));
+      return true;
+    };
+
     // O(i) = P V + a^(i-s(i)+1) Q S -> global (rows of the tile only), through
     // this warp's O staging when its 32 rows all lie in the tile (one TMA
     // store), else row by row.
     bool o_pending = false;   // this warp's last TMA store may still read its staging
-    auto o_work = [&](int i, const Out& r, float l2) -> bool {
+    auto o_work = [&](int i, const Start& r, float l2) -> bool {
       const int b = i & 1;
       if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kOReady + b), (i >> 1) & 1, err, kErrTimeoutMma))) return false;
       tc_fence_after_sync();
@@ -943,16 +911,33 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       return true;
     };
 
-    Out nxt = n > 0 ? load_out(list) : Out{};
-    float nxt_l2 = n > 0 ? decay_log2(load_log_decay(prm.log_decay, nxt.head)) : 0.f;
-    for (int i = 0; i < n && ok; ++i) {
-      const Out cur = nxt;
-      const float l2 = nxt_l2;
-      if (i + 1 < n) {
-        nxt = load_out(list + i + 1);
-        nxt_l2 = decay_log2(load_log_decay(prm.log_decay, nxt.head));
+    // (A warp whose bounded wait ran out leaves the loop: no barrier in it waits
+    // for warps.)
+    if (n > 0 && ok) {
+      Start cur = load_start(list);
+      Start nxt = n > 1 ? load_start(list + 1) : Start{};
+      float l2 = decay_log2(load_log_decay(prm.log_decay, cur.head));
+      int rows = 0;   // rows of the piece before the tile to stage
+      start_piece(cur);
+      ok = stage(0, cur, l2, 0);
+      for (int i = 0; i < n && ok; ++i) {
+        float l2_next = l2;
+        if (cur.flags & kTileFinalOut) final_state(cur);
+        if (i + 1 < n) {
+          // S(i+1) first: the O issuer needs it right after P V of tile i+1.
+          rows += cur.nrows;
+          if (cur.flags & kTileLast) {
+            if (nxt.head != cur.head) l2_next = decay_log2(load_log_decay(prm.log_decay, nxt.head));
+            rows = 0;
+            start_piece(nxt);
+          }
+          if (!stage(i + 1, nxt, l2_next, rows)) break;
+        }
+        ok = o_work(i, cur, l2);
+        cur = nxt;
+        l2 = l2_next;
+        if (i + 2 < n) nxt = load_start(list + i + 2);
       }
-      ok = o_work(i, cur, l2);
     }
     if (lane == 0) bulk_wait_all();   // the last O stores have completed
   }
