@@ -1926,6 +1926,16 @@ bool apart(const Rows& a, const Rows& b) {
   return d >= a.width && d + b.width <= s;
 }
 
+// out of a decayed call, none of whose elements is one of q's, k's or v's.
+span_la_status check_out(const void* q, const void* k, const void* v, const void* out, const span_la_dims& dims) {
+  const int64_t width = static_cast<int64_t>(dims.num_heads) * kHeadDim * (dims.dtype == SPAN_LA_BF16 ? 2 : 4);
+  const Rows o{reinterpret_cast<uintptr_t>(out), width, width, dims.total_rows};
+  for (const void* x : {q, k, v})
+    if (!apart(Rows{reinterpret_cast<uintptr_t>(x), width, width, dims.total_rows}, o))
+      return fail(SPAN_LA_ERR_INVALID, "out overlaps q, k or v");
+  return SPAN_LA_OK;
+}
+
 }  // namespace
 
 namespace spanla {
@@ -2400,6 +2410,7 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     // (pieces of 16 rows at least, and 16 scan CTAs a segment)
     if ((st = check_grid(dims.total_rows / 16 + 16 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    if (!segs.empty() && (st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2432,6 +2443,7 @@ span_la_status span_la_decay_branches_from_state(const float* cached_state, int3
     if (segs.empty()) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     if ((st = check_grid(dims.total_rows / 16 + 16 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
+    if ((st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2461,6 +2473,7 @@ span_la_status span_la_decay_step(const void* q, const void* k, const void* v, s
       return fail(SPAN_LA_ERR_INVALID, "states must be a non-NULL 16-byte aligned pointer");
     if (log_decay != nullptr && (st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     if ((st = check_grid(1, dims.num_heads)) != SPAN_LA_OK) return st;
+    if ((st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
     if (state_index != nullptr) {
       // Two rows of one state would race: every state at most once.
       std::vector<int32_t> seen;

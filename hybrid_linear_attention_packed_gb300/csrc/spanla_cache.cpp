@@ -18,6 +18,7 @@
 #include <cstdio>
 #include <cstdarg>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
 #include <unordered_map>
@@ -148,6 +149,55 @@ span_la_status refuse_capture(cudaStream_t stream) {
   return SPAN_LA_OK;
 }
 
+// Branches from cached states: `run` makes the call, given each branch's slot.
+template <typename Run>
+span_la_status cache_branches(span_la_view_cache* cache, const uint64_t* parent_keys, const span_la_dims& dims,
+                              int32_t num_branches, cudaStream_t stream, Run&& run) {
+  if (cache == nullptr) return cache_fail(SPAN_LA_ERR_INVALID, "cache is NULL");
+  if (dims.num_heads != cache->heads)
+    return cache_fail(SPAN_LA_ERR_INVALID, "num_heads %d differs from the cache's %d", dims.num_heads,
+                      cache->heads);
+  if (num_branches < 0 || (num_branches > 0 && parent_keys == nullptr))
+    return cache_fail(SPAN_LA_ERR_INVALID, "bad parent key array");
+  span_la_status cst = check_device(cache);
+  if (cst == SPAN_LA_OK) cst = refuse_capture(stream);
+  if (cst != SPAN_LA_OK) return cst;
+  std::vector<int32_t> slots(num_branches);
+  {
+    std::lock_guard<std::mutex> lock(cache->mu);
+    for (int32_t b = 0; b < num_branches; ++b) {
+      auto it = cache->slot_of.find(parent_keys[b]);
+      if (it == cache->slot_of.end()) {
+        cache->misses += 1;
+        return cache_fail(SPAN_LA_ERR_INVALID, "parent key of branch %d is not cached", b);
+      }
+      slots[b] = it->second;
+    }
+    // Only a call that will run counts as a use of its entries.
+    for (int32_t b = 0; b < num_branches; ++b) {
+      cache->last_use[slots[b]] = ++cache->clock;
+      cache->hits += 1;
+    }
+    // Wait for the puts of these states (a no-op on the put's own stream),
+    // enqueue, then record the reads, all under the lock so that no put of
+    // another thread can reuse these slots in between.
+    std::vector<int32_t> distinct(slots);
+    std::sort(distinct.begin(), distinct.end());
+    distinct.erase(std::unique(distinct.begin(), distinct.end()), distinct.end());
+    for (int32_t slot : distinct) {
+      cudaError_t e = cudaStreamWaitEvent(stream, cache->written[slot], 0);
+      if (e != cudaSuccess) return cache_fail(SPAN_LA_ERR_CUDA, "cudaStreamWaitEvent: %s", cudaGetErrorString(e));
+    }
+    span_la_status st = run(slots.data());
+    if (st != SPAN_LA_OK) return st;
+    for (int32_t slot : distinct) {
+      cudaError_t e = note_read(cache, slot, stream);
+      if (e != cudaSuccess) return cache_fail(SPAN_LA_ERR_CUDA, "cudaEventRecord: %s", cudaGetErrorString(e));
+    }
+    return SPAN_LA_OK;
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -268,50 +318,23 @@ span_la_status span_la_cache_branches(span_la_view_cache* cache, const uint64_t*
                                       const void* q, const void* k, const void* v, span_la_dims dims,
                                       const int32_t* branch_cu_seqlens, int32_t num_branches, void* out,
                                       cudaStream_t stream) {
-  if (cache == nullptr) return cache_fail(SPAN_LA_ERR_INVALID, "cache is NULL");
-  if (dims.num_heads != cache->heads)
-    return cache_fail(SPAN_LA_ERR_INVALID, "num_heads %d differs from the cache's %d", dims.num_heads,
-                      cache->heads);
-  if (num_branches < 0 || (num_branches > 0 && parent_keys == nullptr))
-    return cache_fail(SPAN_LA_ERR_INVALID, "bad parent key array");
-  span_la_status cst = check_device(cache);
-  if (cst == SPAN_LA_OK) cst = refuse_capture(stream);
-  if (cst != SPAN_LA_OK) return cst;
-  std::vector<int32_t> slots(num_branches);
-  {
-    std::lock_guard<std::mutex> lock(cache->mu);
-    for (int32_t b = 0; b < num_branches; ++b) {
-      auto it = cache->slot_of.find(parent_keys[b]);
-      if (it == cache->slot_of.end()) {
-        cache->misses += 1;
-        return cache_fail(SPAN_LA_ERR_INVALID, "parent key of branch %d is not cached", b);
-      }
-      slots[b] = it->second;
-    }
-    // Only a call that will run counts as a use of its entries.
-    for (int32_t b = 0; b < num_branches; ++b) {
-      cache->last_use[slots[b]] = ++cache->clock;
-      cache->hits += 1;
-    }
-    // Wait for the puts of these states (a no-op on the put's own stream),
-    // enqueue, then record the reads, all under the lock so that no put of
-    // another thread can reuse these slots in between.
-    std::vector<int32_t> distinct(slots);
-    std::sort(distinct.begin(), distinct.end());
-    distinct.erase(std::unique(distinct.begin(), distinct.end()), distinct.end());
-    for (int32_t slot : distinct) {
-      cudaError_t e = cudaStreamWaitEvent(stream, cache->written[slot], 0);
-      if (e != cudaSuccess) return cache_fail(SPAN_LA_ERR_CUDA, "cudaStreamWaitEvent: %s", cudaGetErrorString(e));
-    }
-    span_la_status st = span_la_branches_from_state(cache->pool, cache->capacity, q, k, v, dims,
-                                                    branch_cu_seqlens, num_branches, slots.data(), out,
-                                                    stream);
-    if (st != SPAN_LA_OK) return st;
-    for (int32_t slot : distinct) {
-      cudaError_t e = note_read(cache, slot, stream);
-      if (e != cudaSuccess) return cache_fail(SPAN_LA_ERR_CUDA, "cudaEventRecord: %s", cudaGetErrorString(e));
-    }
-    return SPAN_LA_OK;
+  return cache_branches(cache, parent_keys, dims, num_branches, stream, [&](const int32_t* slots) {
+    return span_la_branches_from_state(cache->pool, cache->capacity, q, k, v, dims, branch_cu_seqlens, num_branches,
+                                       slots, out, stream);
+  });
+}
+
+span_la_status span_la_cache_decay_branches(span_la_view_cache* cache, const uint64_t* parent_keys,
+                                            const void* q, const void* k, const void* v, span_la_dims dims,
+                                            const float* log_decay, const int32_t* branch_cu_seqlens,
+                                            int32_t num_branches, void* out, cudaStream_t stream) {
+  try {
+    return cache_branches(cache, parent_keys, dims, num_branches, stream, [&](const int32_t* slots) {
+      return span_la_decay_branches_from_state(cache->pool, cache->capacity, q, k, v, dims, log_decay, branch_cu_seqlens,
+                                               num_branches, slots, out, stream);
+    });
+  } catch (const std::exception& e) {
+    return cache_fail(SPAN_LA_ERR_NOMEM, "out of host memory: %s", e.what());
   }
 }
 

@@ -36,7 +36,7 @@ EXPORTED = ("span_la_pass", "span_la_branches_from_state", "span_la_check",
             "span_la_fault_inject", "span_la_softmax_plan_stats",
             "span_la_selftest_wait_timeout_noalloc", "span_la_pass_variant",
             "span_la_plan_prepare", "span_la_decay_pass", "span_la_decay_branches_from_state",
-            "span_la_decay_step", "span_la_qk_norm_rope")
+            "span_la_decay_step", "span_la_qk_norm_rope", "span_la_cache_decay_branches")
 NUM_KERNELS = 13
 
 
@@ -152,6 +152,8 @@ def load_library(path: Optional[str] = None):
         lib.span_la_cache_branches.argtypes = [vp, vp, vp, vp, vp, Dims, i32p, ctypes.c_int32,
                                                vp, vp]
         lib.span_la_cache_branches.restype = ctypes.c_int
+        lib.span_la_cache_decay_branches.argtypes = [vp, vp, vp, vp, vp, Dims, vp, i32p, ctypes.c_int32, vp, vp]
+        lib.span_la_cache_decay_branches.restype = ctypes.c_int
         lib.span_la_cache_stats.argtypes = [vp, ctypes.POINTER(ctypes.c_int64)]
         lib.span_la_cache_stats.restype = ctypes.c_int
         if path is None:
@@ -727,14 +729,23 @@ class ViewStateCache:
 
     def branches(self, parent_keys, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                  branch_cu_seqlens: Sequence[int], out: Optional[torch.Tensor] = None,
-                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-        """Branch b forks from the state cached under parent_keys[b]."""
+                 stream: Optional[torch.cuda.Stream] = None,
+                 log_decay: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Branch b forks from the state cached under parent_keys[b]; with
+        ``log_decay`` (fp32 CUDA [H]) as a branch of a decayed pass."""
         dims = _dims_of(q, k, v)
         bcu = _i32(branch_cu_seqlens)
         B = max(len(bcu) - 1, 0)
         ks = _keys(parent_keys)
         if ks.size != B:
             raise ValueError("one parent key per branch")
+        if log_decay is not None:
+            dims, out, _ = _decay_args(q, k, v, log_decay, out)
+            _raise(self._lib, self._lib.span_la_cache_decay_branches(
+                self._live(), ks.ctypes.data if ks.size else None, q.data_ptr(), k.data_ptr(), v.data_ptr(), dims,
+                log_decay.data_ptr(), _iptr(bcu), B, out.data_ptr(), _stream_handle(stream)),
+                "span_la_cache_decay_branches")
+            return out
         if out is None:
             out = torch.empty_like(q)
         if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:

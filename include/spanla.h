@@ -466,6 +466,10 @@ span_la_status span_la_softmax_branches_from_kv(const void *view_k, const void *
  *                    sees row t only).  Read when the stream reaches the call
  *   out              must not overlap q, k or v
  *   other arguments  as for span_la_pass
+ *   plan             kept in the plan cache with, up to 64 MB, the call's
+ *                    workspace (calls of one plan on several streams then run
+ *                    one after the other); span_la_plan_prepare does not
+ *                    prepare it
  * With fp32 inputs every product and sum is fp32.  With bf16 inputs the
  * factors a^n are applied in fp32 and the state is kept to fp32 accuracy; the
  * masked scores and the state enter their products with v and q rounded to
@@ -499,7 +503,8 @@ span_la_status span_la_decay_branches_from_state(const float *cached_state, int3
  * dims.total_rows sequences: row t updates a state in place and gets its
  * output, so that a sequence whose prompt span_la_decay_pass (or
  * span_la_pass) ran goes on token by token from its view_state_out.
- *   q, k, v, out     device [n][H][64], n = dims.total_rows
+ *   q, k, v, out     device [n][H][64], n = dims.total_rows; out must not
+ *                    overlap the others
  *   log_decay        as for span_la_decay_pass, or NULL: no decay (the next
  *                    token of span_la_pass)
  *   states           device fp32 [num_states][H][64][64], updated in place
@@ -612,6 +617,18 @@ span_la_status span_la_cache_branches(span_la_view_cache *cache, const uint64_t 
                                       const void *q, const void *k, const void *v,
                                       span_la_dims dims, const int32_t *branch_cu_seqlens,
                                       int32_t num_branches, void *out, cudaStream_t stream);
+
+/*
+ * As span_la_cache_branches, with a decay for each head
+ * (span_la_decay_branches_from_state): the cached states are then those of
+ * span_la_decay_pass.  A cache holds states of either kind; the caller's keys
+ * keep them apart.
+ */
+span_la_status span_la_cache_decay_branches(span_la_view_cache *cache, const uint64_t *parent_keys,
+                                            const void *q, const void *k, const void *v,
+                                            span_la_dims dims, const float *log_decay,
+                                            const int32_t *branch_cu_seqlens,
+                                            int32_t num_branches, void *out, cudaStream_t stream);
 
 /* stats[0..5] = entries, capacity, hits, misses, evictions, puts (counts of
  * keys; a hit or a miss is one key looked up by contains or by a branch call). */

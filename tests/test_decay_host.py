@@ -23,7 +23,10 @@ def _i32(a):
     return a, (a.ctypes.data if a.size else None)
 
 
-def _pass(lib, vcu=(0, 50), bcu=(50, 60), par=(0,), T=100, H=2, D=64, dtype=0, q=FAKE, out=FAKE, state=FAKE, ld=FAKE):
+OUT = FAKE * 16
+
+
+def _pass(lib, vcu=(0, 50), bcu=(50, 60), par=(0,), T=100, H=2, D=64, dtype=0, q=FAKE, out=OUT, state=FAKE, ld=FAKE):
     (va, vp), (ba, bp), (pa, pp) = _i32(vcu), _i32(bcu), _i32(par)
     st = lib.span_la_decay_pass(q, q, q, spanla.Dims(T, H, D, dtype), ld, vp, max(len(va) - 1, 0), bp,
                                 max(len(ba) - 1, 0), pp, out, state, None)
@@ -44,6 +47,8 @@ def _pass(lib, vcu=(0, 50), bcu=(50, 60), par=(0,), T=100, H=2, D=64, dtype=0, q
     (dict(q=None), INVALID, "non-NULL"),
     (dict(q=FAKE + 8), INVALID, "aligned"),
     (dict(out=None), INVALID, "non-NULL"),
+    (dict(out=FAKE), INVALID, "out overlaps"),
+    (dict(out=FAKE + 100 * 2 * 64 * 2 - 16), INVALID, "out overlaps"),
     (dict(state=None), INVALID, "view_state_out"),
     (dict(state=FAKE + 4), INVALID, "view_state_out"),
     (dict(ld=None), INVALID, "log_decay"),
@@ -64,9 +69,9 @@ def test_nothing_to_do_needs_no_device(lib):
     assert lib.span_la_decay_step(None, None, None, spanla.Dims(0, 2, 64, 0), None, None, 0, None, None, None) == 0
 
 
-def _fork(lib, bcu=(0, 10), par=(0,), n=1, kept=FAKE, ld=FAKE, q=FAKE):
+def _fork(lib, bcu=(0, 10), par=(0,), n=1, kept=FAKE, ld=FAKE, q=FAKE, out=OUT):
     (ba, bp), (pa, pp) = _i32(bcu), _i32(par)
-    st = lib.span_la_decay_branches_from_state(kept, n, q, q, q, spanla.Dims(10, 2, 64, 0), ld, bp, len(ba) - 1, pp, FAKE,
+    st = lib.span_la_decay_branches_from_state(kept, n, q, q, q, spanla.Dims(10, 2, 64, 0), ld, bp, len(ba) - 1, pp, out,
                                                None)
     return st, lib.span_la_last_error_detail().decode()
 
@@ -74,14 +79,14 @@ def _fork(lib, bcu=(0, 10), par=(0,), n=1, kept=FAKE, ld=FAKE, q=FAKE):
 @pytest.mark.parametrize("kw,what", [
     (dict(bcu=(0, 11)), "non-decreasing"), (dict(par=(1,)), "branch_parent"), (dict(n=-1), "num_states"),
     (dict(kept=None), "cached_state"), (dict(kept=FAKE + 8), "cached_state"), (dict(ld=None), "log_decay"),
-    (dict(q=None), "non-NULL"),
+    (dict(q=None), "non-NULL"), (dict(out=FAKE + 64), "out overlaps"),
 ])
 def test_fork_refuses(lib, kw, what):
     st, detail = _fork(lib, **kw)
     assert st == INVALID and what in detail
 
 
-def _step(lib, n=3, H=2, D=64, dtype=0, q=FAKE, ld=FAKE, states=FAKE, num=8, index=(0, 5, 7), out=FAKE):
+def _step(lib, n=3, H=2, D=64, dtype=0, q=FAKE, ld=FAKE, states=FAKE, num=8, index=(0, 5, 7), out=OUT):
     (ia, ip) = _i32(index if index is not None else [])
     st = lib.span_la_decay_step(q, q, q, spanla.Dims(n, H, D, dtype), ld, states, num, ip, out, None)
     return st, lib.span_la_last_error_detail().decode()
@@ -98,6 +103,7 @@ def _step(lib, n=3, H=2, D=64, dtype=0, q=FAKE, ld=FAKE, states=FAKE, num=8, ind
     (dict(states=FAKE + 4), INVALID, "states"),
     (dict(q=None), INVALID, "non-NULL"),
     (dict(out=FAKE + 2), INVALID, "aligned"),
+    (dict(out=FAKE), INVALID, "out overlaps"),
     (dict(ld=FAKE + 1), INVALID, "log_decay"),
     (dict(D=32), UNSUPPORTED, "head_dim"),
     (dict(dtype=9), UNSUPPORTED, "dtype"),

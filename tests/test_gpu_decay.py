@@ -21,7 +21,7 @@ import numpy as np
 import pytest
 import torch
 
-from hybrid_linear_attention_packed_gb300 import (SpanLAError, packed_positions, rope_inv_freq, span_la_check,
+from hybrid_linear_attention_packed_gb300 import (SpanLAError, ViewStateCache, packed_positions, rope_inv_freq, span_la_check,
                                                   span_la_decay_branches_from_state, span_la_decay_pass, span_la_decay_step,
                                                   span_la_pass, span_la_qk_norm_rope, spanla, workloads)
 from oracle.decay_oracle import oracle_decay_pass, oracle_norm_rope
@@ -273,6 +273,96 @@ def test_graph_replays_and_eager_calls_between(cuda_device, dtype):
             ref, ref_s = span_la_decay_pass(*b, ld, *args)
             span_la_check()
             assert torch.equal(res[0], ref) and torch.equal(res[1], ref_s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_plan_on_many_streams_at_once(cuda_device, dtype):
+    """Passes of one plan (which share its kept workspace) on eleven streams that nothing orders, each with inputs of its
+    own, three rounds: more streams than the plan records readers for."""
+    w = workloads.make_pass([1500, 700], [30] * 5 + [300], [0, 1, 0, 1, 1, 0], H=8, dtype=dtype, seed=21)
+    ld = torch.from_numpy(_decays(8, "slopes")).to(cuda_device)
+    q, k, v = _put(w, cuda_device)
+    n = 11
+    vs = [v * (1.0 + i) for i in range(n)]
+    refs = [span_la_decay_pass(q, k, x, ld, w.view_cu, w.branch_cu, w.branch_parent) for x in vs]
+    outs = [(torch.empty_like(q), torch.empty_like(refs[0][1])) for _ in range(n)]
+    streams = [torch.cuda.Stream(cuda_device) for _ in range(n)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in range(n):
+            span_la_decay_pass(q, k, vs[i], ld, w.view_cu, w.branch_cu, w.branch_parent, out=outs[i][0],
+                               view_state_out=outs[i][1], stream=streams[i])
+    torch.cuda.synchronize()
+    span_la_check()
+    for (o, s), (ro, rs) in zip(outs, refs):
+        assert torch.equal(o, ro) and torch.equal(s, rs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_plans_are_evicted_in_stream_order(cuda_device, dtype):
+    """Forty layouts twice over, past the sixteen that the plan cache holds, on two streams without a synchronisation."""
+    layouts = [([200 + 37 * i, 64], [20, 150 + i], [0, 1]) for i in range(40)]
+    ws = [workloads.make_pass(*lay, H=2, dtype=dtype, seed=30 + i) for i, lay in enumerate(layouts)]
+    ld = torch.from_numpy(_decays(2, "slopes")).to(cuda_device)
+    ins = [_put(w, cuda_device) for w in ws]
+    streams = [torch.cuda.Stream(cuda_device) for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[torch.empty_like(x[0]) for x in ins] for _ in range(2)]
+    states = [[torch.empty(2, 2, 64, 64, device=cuda_device) for _ in ins] for _ in range(2)]
+    for rep in range(2):
+        for i, w in enumerate(ws):
+            span_la_decay_pass(*ins[i], ld, w.view_cu, w.branch_cu, w.branch_parent, out=got[rep][i],
+                               view_state_out=states[rep][i], stream=streams[(i + rep) % 2])
+    torch.cuda.synchronize()
+    span_la_check()
+    for i, w in enumerate(ws):
+        assert torch.equal(got[0][i], got[1][i]) and torch.equal(states[0][i], states[1][i])
+        if i % 8 == 0:
+            _check(w, _decays(2, "slopes"), got[0][i], states[0][i])
+
+
+def test_branches_by_key_from_the_view_state_cache(cuda_device):
+    w = workloads.make_pass([300, 900], [30, 7, 200, 64], [0, 1, 1, 0], H=4, dtype="bf16", seed=22)
+    ld = torch.from_numpy(_decays(4, "slopes")).to(cuda_device)
+    q, k, v = _put(w, cuda_device)
+    _, states = span_la_decay_pass(q, k, v, ld, w.view_cu, None, None)
+    keys = np.array([5, 2 ** 63 + 9], dtype=np.uint64)
+    with ViewStateCache(4, 3) as cache:
+        cache.put(keys, states)
+        got = cache.branches(keys[w.branch_parent], q, k, v, w.branch_cu, log_decay=ld)
+        ref = span_la_decay_branches_from_state(states, q, k, v, ld, w.branch_cu, w.branch_parent)
+        span_la_check()
+        lo = int(w.branch_cu[0])
+        assert torch.equal(got[lo:], ref[lo:])
+        with pytest.raises(SpanLAError, match="not cached"):
+            cache.branches([5, 6, 5, 5], q, k, v, w.branch_cu, log_decay=ld)
+        with pytest.raises(ValueError, match="log_decay"):
+            cache.branches(keys[w.branch_parent], q, k, v, w.branch_cu, log_decay=ld[:2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_masked_infinities_and_nans_stay_masked(cuda_device, dtype):
+    """Rows after, and siblings beside: an infinite or NaN value (or key) of one row changes no earlier row and no
+    other branch's bits; the rows that see it are not finite."""
+    w = workloads.make_pass([200], [20, 30, 40], [0, 0, 0], H=2, dtype=dtype, seed=23)
+    ld = np.float32([-0.01, -3.0])
+    clean, _ = _run(w, ld, cuda_device)
+    b1, b2 = int(w.branch_cu[1]), int(w.branch_cu[2])
+    w.v[b1 + 10, 0, 7] = float("inf")
+    w.v[b1 + 12, 1, :] = float("nan")
+    w.k[b1 + 15, 0, :] = float("nan")
+    w.v[150, 0, 3] = float("-inf")
+    out, state = _run(w, ld, cuda_device)
+    assert torch.equal(out[:150], clean[:150]) and torch.equal(out[150:, 1][:50], clean[150:, 1][:50])
+    rest = [c for c in range(64) if c != 3]
+    assert torch.equal(out[:b1, 0][:, rest], clean[:b1, 0][:, rest])        # the view and the first branch: column 3 only
+    assert torch.equal(out[b2:, 0][:, rest], clean[b2:, 0][:, rest]) and torch.equal(out[b2:, 1], clean[b2:, 1])
+    assert torch.equal(out[b1:b1 + 10, 0][:, rest], clean[b1:b1 + 10, 0][:, rest])
+    assert torch.equal(out[b1:b1 + 12, 1], clean[b1:b1 + 12, 1]) and torch.isnan(out[b1 + 12, 1]).all()
+    # the rows that see them: infinite by the unrolled sum, NaN by the recurrence, whose state then holds infinities of
+    # both signs (k_i times one) that the output adds
+    assert not torch.isfinite(out[150, 0, 3]) and not torch.isfinite(out[b1 + 10, 0, 7])
+    assert not torch.isfinite(state[0, 0, :, 3]).any() and torch.isfinite(state[0, 0][:, rest]).all()
 
 
 def test_allocation_failure_is_reported_and_nothing_written(cuda_device):
