@@ -234,7 +234,7 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
 // run <- a^len run + piece.  One element a thread, so that a pass of few
 // segments still has a state's 4096 chains times its heads in flight, 16 slots
 // of loads ahead.  (A float4 a thread, 8 slots ahead: 25 us where this takes
-// SCAN_US, for 58 slots of 16 heads.)
+// 10, for 58 slots of 16 heads.)
 constexpr int kScanThreads = 256;
 constexpr int kScanParts = kStateFloats / kScanThreads;
 constexpr int kAhead = 16;

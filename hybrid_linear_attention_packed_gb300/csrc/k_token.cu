@@ -327,9 +327,9 @@ void run_rope(const RopeArgs& a, bool interleaved, unsigned grid, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_decay_step(const StepArgs& a, cudaStream_t stream) {
-  // The indices ride in the launch's parameters (up to 4 KB), so that the
-  // host array is read during the call only and nothing is copied; a longer
-  // batch takes a launch per kStepMostSlots rows.
+  // The indices ride in the launch's parameters, so that the host array is
+  // read during the call only and nothing is copied; a longer batch takes a
+  // launch per kStepMostSlots rows.
   for (int64_t t0 = 0; t0 < a.n;) {
     const int64_t most = a.index != nullptr ? kStepMostSlots : (INT64_C(1) << 30) / a.H;
     const int64_t n = a.n - t0 < most ? a.n - t0 : most;
@@ -339,6 +339,9 @@ cudaError_t launch_decay_step(const StepArgs& a, cudaStream_t stream) {
     } else if (n <= kStepFewSlots) {
       e = a.f32 ? step_chunk<float, kStepFewSlots>(a, t0, n, stream)
                 : step_chunk<__nv_bfloat16, kStepFewSlots>(a, t0, n, stream);
+    } else if (n <= kStepManySlots) {
+      e = a.f32 ? step_chunk<float, kStepManySlots>(a, t0, n, stream)
+                : step_chunk<__nv_bfloat16, kStepManySlots>(a, t0, n, stream);
     } else {
       e = a.f32 ? step_chunk<float, kStepMostSlots>(a, t0, n, stream)
                 : step_chunk<__nv_bfloat16, kStepMostSlots>(a, t0, n, stream);

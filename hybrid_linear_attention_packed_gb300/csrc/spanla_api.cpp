@@ -2475,14 +2475,22 @@ span_la_status span_la_decay_step(const void* q, const void* k, const void* v, s
     if ((st = check_grid(1, dims.num_heads)) != SPAN_LA_OK) return st;
     if ((st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
     if (state_index != nullptr) {
-      // Two rows of one state would race: every state at most once.
+      // Two rows of one state would race: every state at most once.  (A bit for
+      // each of a small pool's states, else by sorting.)
+      constexpr int32_t kBits = 4096;
+      uint64_t bits[kBits / 64] = {};
       std::vector<int32_t> seen;
-      seen.reserve(static_cast<size_t>(n));
       for (int64_t t = 0; t < n; ++t) {
         const int32_t i = state_index[t];
         if (i < -1 || i >= num_states)
           return fail(SPAN_LA_ERR_INVALID, "state_index[%lld] = %d not in [-1, %d)", (long long)t, i, num_states);
-        if (i >= 0) seen.push_back(i);
+        if (i < 0) continue;
+        if (num_states > kBits) {
+          seen.push_back(i);
+        } else {
+          if ((bits[i >> 6] >> (i & 63)) & 1) return fail(SPAN_LA_ERR_INVALID, "state_index has state %d twice", i);
+          bits[i >> 6] |= uint64_t(1) << (i & 63);
+        }
       }
       std::sort(seen.begin(), seen.end());
       const auto twice = std::adjacent_find(seen.begin(), seen.end());

@@ -95,6 +95,7 @@ def _step(lib, n=3, H=2, D=64, dtype=0, q=FAKE, ld=FAKE, states=FAKE, num=8, ind
 @pytest.mark.parametrize("kw,status,what", [
     (dict(index=(0, 5, 5)), INVALID, "twice"),
     (dict(index=(7, -1, 7)), INVALID, "twice"),
+    (dict(index=(9000, 3, 9000), num=10000), INVALID, "twice"),
     (dict(index=(0, 8, 1)), INVALID, "state_index[1]"),
     (dict(index=(0, 1, -2)), INVALID, "state_index[2]"),
     (dict(index=None, num=2), INVALID, "as many states"),

@@ -46,7 +46,7 @@ def _check(q, k, v, ld, before, index, out, states, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,H,pool", [(1, 1, 1), (3, 5, 7), (64, 2, 64), (65, 3, 90), (130, 16, 131), (1001, 1, 1100),
-                                      (2003, 1, 2003)])
+                                      (2003, 1, 2003), (4099, 1, 4100)])
 def test_step_with_indices(cuda_device, n, H, pool, dtype):
     q, k, v, states, ld = _draw(n, H, pool, dtype, cuda_device)
     index = np.random.default_rng(n).permutation(pool)[:n].astype(np.int32)
