@@ -629,9 +629,10 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
               }
           }
           if (!all_kept) {
+            const uint32_t kept = (hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u) & (lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c < lo || c > hi) r0[c] = 0u;
+              if (!(kept & (1u << c))) r0[c] = 0u;
           }
 #pragma unroll
           for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(__uint_as_float(r0[2 * c]), __uint_as_float(r0[2 * c + 1]));
