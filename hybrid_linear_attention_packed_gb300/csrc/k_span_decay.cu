@@ -497,7 +497,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         uint8_t* src = smem + L::kStage0 + (u % kStages) * kStageBytes + my16;
         uint8_t* dst = smem + ((u & 1) ? L::kVs1 : L::kVs0) + ct * 16;
         uint32_t bad = 0;
-#pragma unroll 2
+#pragma unroll 4
         for (int w = 0; w < kPieces; ++w) {
           const int r = piece_row(w);
           const uint4 x4 = r < rows ? *reinterpret_cast<const uint4*>(src + kPieceStep * w) : make_uint4(0u, 0u, 0u, 0u);
@@ -585,7 +585,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const uint32_t colP = (b ? kColP1 : kColP0) + half * 64;
       // Two 32-column chunks in turn; chunk q's bf16 pairs go to columns
       // 16q .. 16q + 15 of the half, over scores already read.
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         const int c0 = half * 64 + 32 * q;
         uint32_t pk[16];
