@@ -193,6 +193,43 @@ def test_fork_from_kept_states(cuda_device, dtype):
     _check(w, ld, out, None, kept=_f64(kept))
 
 
+@pytest.mark.parametrize("tiles", range(126, 134))
+def test_a_branch_behind_a_branch_of_many_pieces(cuda_device, tiles):
+    """One head and one kept state: a branch over some 64 SMs, and another whose first tile follows its last one on an SM.
+    The first rows of the second come from the kept state, not from the first branch's."""
+    w = workloads.make_pass([], [128 * tiles, 128 * (304 - tiles)], [0, 0], H=1, dtype="bf16", seed=17)
+    kept = torch.randn(1, 1, 64, 64, generator=torch.Generator().manual_seed(2))
+    ld = np.asarray([-1e-3], dtype=np.float32)
+    q, k, v = _put(w, cuda_device)
+    out = span_la_decay_branches_from_state(kept.to(cuda_device), q, k, v, torch.from_numpy(ld).to(cuda_device), w.branch_cu,
+                                            w.branch_parent)
+    span_la_check()
+    lo = int(w.branch_cu[1])
+    ref, _ = oracle_decay_pass(*(_f64(x[lo:lo + 128]) for x in (q, k, v)), ld, [], [0, 128], [0], _f64(kept))
+    got = _f64(out[lo:lo + 128])
+    assert np.linalg.norm(got - ref) <= 5e-3 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("decay", [True])
+def test_branches_behind_a_branch_of_many_pieces_in_a_pass(cuda_device, decay):
+    """As above behind a view of one tile, with the first branch over some 128 SMs, decayed and not."""
+    ld = np.asarray([-1e-3 if decay else 0.0], dtype=np.float32)
+    for tiles in range(250, 264):
+        w = workloads.make_pass([128], [128 * tiles, 128 * (303 - tiles)], [0, 0], H=1, dtype="bf16", seed=18)
+        q, k, v = _put(w, cuda_device)
+        args = (w.view_cu, w.branch_cu, w.branch_parent)
+        if decay:
+            out, _ = span_la_decay_pass(q, k, v, torch.from_numpy(ld).to(cuda_device), *args)
+        else:
+            out, _ = span_la_pass(q, k, v, *args)
+        span_la_check()
+        lo = int(w.branch_cu[1])
+        both = [np.concatenate([_f64(x[:128]), _f64(x[lo:lo + 128])]) for x in (q, k, v)]
+        ref, _ = oracle_decay_pass(*both, ld, [0, 128], [128, 256], [0])
+        got = _f64(out[lo:lo + 128])
+        assert np.linalg.norm(got - ref[128:]) <= 5e-3 * np.linalg.norm(ref[128:]), tiles
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_shards_from_a_pass_agree_with_its_branches(cuda_device, dtype):
     w = workloads.make_pass([1000], [40, 7, 90, 128, 33, 300, 64, 5], [0] * 8, H=3, dtype=dtype, seed=13)
