@@ -548,9 +548,8 @@ span_output_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto start_tag = [&](const TileState& r) -> int64_t {
       if (!(r.flags & kTileFirst) || !(r.flags & kTileHasInit)) return -1;
       if (r.flags & kTileCarry) return carry_tag(r.final_idx, r.head);
-      return ((static_cast<int64_t>(r.stateA) + 1) << 40) ^ ((static_cast<int64_t>(r.a_n)) << 34) ^
-             ((static_cast<int64_t>(r.stateB) + 1) << 16) ^ (static_cast<int64_t>(r.b_n) << 10) ^
-             static_cast<int64_t>(r.head);
+      if (r.b_n > 0) return static_cast<int64_t>(1) << 61;   // (only the first piece of a CTA's run has earlier ones)
+      return (static_cast<int64_t>(r.stateA) << 16) | r.head;   // (a_n goes by stateA)
     };
     // Sum, in order, of the states of term A (a_n states a_rows heads apart)
     // and term B (b_n workspace slots) into s_run.  The group reads each

@@ -210,7 +210,7 @@ def test_a_branch_behind_a_branch_of_many_pieces(cuda_device, tiles):
     assert np.linalg.norm(got - ref) <= 5e-3 * np.linalg.norm(ref)
 
 
-@pytest.mark.parametrize("decay", [True])
+@pytest.mark.parametrize("decay", [True, False])
 def test_branches_behind_a_branch_of_many_pieces_in_a_pass(cuda_device, decay):
     """As above behind a view of one tile, with the first branch over some 128 SMs, decayed and not."""
     ld = np.asarray([-1e-3 if decay else 0.0], dtype=np.float32)
