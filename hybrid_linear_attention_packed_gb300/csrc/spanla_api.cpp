@@ -1926,13 +1926,21 @@ bool apart(const Rows& a, const Rows& b) {
   return d >= a.width && d + b.width <= s;
 }
 
-// out of a decayed call, none of whose elements is one of q's, k's or v's.
-span_la_status check_out(const void* q, const void* k, const void* v, const void* out, const span_la_dims& dims) {
+// What a decayed call writes overlaps nothing else of it: out none of q, k and
+// v, and `num_states` states at `states` neither those (when they are
+// written) nor out.
+span_la_status check_out(const void* q, const void* k, const void* v, const void* out, const span_la_dims& dims,
+                         const char* name, const float* states, int64_t num_states, bool states_written) {
   const int64_t width = static_cast<int64_t>(dims.num_heads) * kHeadDim * (dims.dtype == SPAN_LA_BF16 ? 2 : 4);
-  const Rows o{reinterpret_cast<uintptr_t>(out), width, width, dims.total_rows};
+  auto rows = [&](const void* x) { return Rows{reinterpret_cast<uintptr_t>(x), width, width, dims.total_rows}; };
+  const int64_t state_width = num_states > 0 ? static_cast<int64_t>(dims.num_heads) * kStateFloats * sizeof(float) : 0;
+  const Rows s{reinterpret_cast<uintptr_t>(states), state_width, state_width, num_states};
   for (const void* x : {q, k, v})
-    if (!apart(Rows{reinterpret_cast<uintptr_t>(x), width, width, dims.total_rows}, o))
-      return fail(SPAN_LA_ERR_INVALID, "out overlaps q, k or v");
+    if (!apart(rows(x), rows(out))) return fail(SPAN_LA_ERR_INVALID, "out overlaps q, k or v");
+  if (!apart(rows(out), s)) return fail(SPAN_LA_ERR_INVALID, "%s overlaps out", name);
+  if (states_written)
+    for (const void* x : {q, k, v})
+      if (!apart(rows(x), s)) return fail(SPAN_LA_ERR_INVALID, "%s overlaps q, k or v", name);
   return SPAN_LA_OK;
 }
 
@@ -2410,7 +2418,7 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     // (pieces of 16 rows at least, and 16 scan CTAs a segment)
     if ((st = check_grid(dims.total_rows / 16 + 16 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
-    if (!segs.empty() && (st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
+    if (!segs.empty() && (st = check_out(q, k, v, out, dims, "view_state_out", view_state_out, num_views, true)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2443,7 +2451,7 @@ span_la_status span_la_decay_branches_from_state(const float* cached_state, int3
     if (segs.empty()) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     if ((st = check_grid(dims.total_rows / 16 + 16 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
-    if ((st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
+    if ((st = check_out(q, k, v, out, dims, "cached_state", cached_state, num_states, false)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2473,7 +2481,6 @@ span_la_status span_la_decay_step(const void* q, const void* k, const void* v, s
       return fail(SPAN_LA_ERR_INVALID, "states must be a non-NULL 16-byte aligned pointer");
     if (log_decay != nullptr && (st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     if ((st = check_grid(1, dims.num_heads)) != SPAN_LA_OK) return st;
-    if ((st = check_out(q, k, v, out, dims)) != SPAN_LA_OK) return st;
     if (state_index != nullptr) {
       // Two rows of one state would race: every state at most once.  (A bit for
       // each of a small pool's states, else by sorting.)
@@ -2496,6 +2503,7 @@ span_la_status span_la_decay_step(const void* q, const void* k, const void* v, s
       const auto twice = std::adjacent_find(seen.begin(), seen.end());
       if (twice != seen.end()) return fail(SPAN_LA_ERR_INVALID, "state_index has state %d twice", *twice);
     }
+    if ((st = check_out(q, k, v, out, dims, "states", states, num_states, true)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     StepArgs a;

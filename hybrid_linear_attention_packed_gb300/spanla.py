@@ -553,10 +553,16 @@ def packed_positions(view_cu_seqlens: Sequence[int], branch_cu_seqlens: Optional
     :func:`span_la_qk_norm_rope`: a view's rows count from 0, a branch's go on
     from its parent view's length, and rows in no segment get -1 (skipped)."""
     vcu, bcu, par = _i32(view_cu_seqlens), _i32(branch_cu_seqlens), _i32(branch_parent)
+    V, B = max(len(vcu) - 1, 0), max(len(bcu) - 1, 0)
+    if par.size != B or (B and not (0 <= par.min() and par.max() < V)):
+        raise ValueError("one parent per branch, in [0, %d)" % V)
+    for cu in (vcu, bcu):
+        if cu.size and (cu[0] < 0 or cu[-1] > total_rows or (np.diff(cu) < 0).any()):
+            raise ValueError("row offsets must be non-decreasing in [0, total_rows]")
     pos = np.full(int(total_rows), -1, dtype=np.int32)
-    for s in range(max(len(vcu) - 1, 0)):
+    for s in range(V):
         pos[vcu[s]:vcu[s + 1]] = np.arange(vcu[s + 1] - vcu[s], dtype=np.int32)
-    for b in range(max(len(bcu) - 1, 0)):
+    for b in range(B):
         p = int(par[b])
         pos[bcu[b]:bcu[b + 1]] = np.arange(bcu[b + 1] - bcu[b], dtype=np.int32) + (vcu[p + 1] - vcu[p])
     return pos

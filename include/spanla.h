@@ -462,15 +462,17 @@ span_la_status span_la_softmax_branches_from_kv(const void *view_k, const void *
  * span_la_pass ("Serving 0.88M TPS from Two RTXs and Mac Minis", section "The
  * Workload": branches attend to the view, not to each other).
  *   log_decay        device fp32 [H]: the natural logarithm of each head's
- *                    decay, normally <= 0; -infinity is a decay of 0 (o_t
- *                    sees row t only).  Read when the stream reaches the call
+ *                    decay, normally <= 0 (at most 2); -infinity is a decay
+ *                    of 0 (o_t sees row t only).  Read when the stream reaches the call
  *   out              must not overlap q, k or v
+ *   view_state_out   must not overlap q, k, v or out
  *   other arguments  as for span_la_pass
  *   plan             kept in the plan cache with, up to 64 MB, the call's
  *                    workspace (calls of one plan on several streams then run
  *                    one after the other); span_la_plan_prepare does not
  *                    prepare it
- * With fp32 inputs every product and sum is fp32.  With bf16 inputs the
+ * With fp32 inputs every product and sum is fp32; the output's states are held
+ * times up to e^24 inside, so their elements have to stay below 1e28.  With bf16 inputs the
  * factors a^n are applied in fp32 and the state is kept to fp32 accuracy; the
  * masked scores and the state enter their products with v and q rounded to
  * bf16.
@@ -487,7 +489,7 @@ span_la_status span_la_decay_pass(const void *q, const void *k, const void *v,
  * span_la_decay_branches_from_state -- branches of span_la_decay_pass only,
  * each from a kept view state (as span_la_branches_from_state: shards of a
  * long request, section "Long Requests").
- *   cached_state     device fp32 [num_states][H][64][64]
+ *   cached_state     device fp32 [num_states][H][64][64], apart from out
  *   branch_parent    host int32 [num_branches], each in [0, num_states)
  */
 span_la_status span_la_decay_branches_from_state(const float *cached_state, int32_t num_states,
@@ -507,7 +509,8 @@ span_la_status span_la_decay_branches_from_state(const float *cached_state, int3
  *                    overlap the others
  *   log_decay        as for span_la_decay_pass, or NULL: no decay (the next
  *                    token of span_la_pass)
- *   states           device fp32 [num_states][H][64][64], updated in place
+ *   states           device fp32 [num_states][H][64][64], updated in place;
+ *                    apart from q, k, v and out
  *   state_index      HOST int32 [n]: the state of each row, in [-1, num_states);
  *                    a row of -1 (padding) is skipped, its out left as it was;
  *                    no state may be named twice.  NULL: row t uses state t

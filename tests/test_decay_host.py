@@ -172,3 +172,30 @@ def test_binding_refuses_cpu_tensors_and_shapes(lib):
         spanla.span_la_qk_norm_rope(x, x, torch.zeros(4, dtype=torch.int32), None)
     with pytest.raises(ValueError, match="dtype"):
         spanla.span_la_qk_norm_rope(x.half(), x.half(), torch.zeros(4, dtype=torch.int32), None)
+
+
+def test_states_that_overlap_other_arguments(lib):
+    st, detail = _pass(lib, state=OUT + 64)
+    assert st == INVALID and "view_state_out overlaps out" in detail
+    st, detail = _pass(lib, state=FAKE + 16)
+    assert st == INVALID and "view_state_out overlaps q, k or v" in detail
+    st, detail = _fork(lib, kept=OUT - 16)
+    assert st == INVALID and "cached_state overlaps out" in detail
+    st, detail = _step(lib, states=OUT)
+    assert st == INVALID and "states overlaps out" in detail
+    st, detail = _step(lib, states=FAKE)
+    assert st == INVALID and "states overlaps q, k or v" in detail
+
+
+@pytest.mark.parametrize("args", [
+    ([0, 4], [4, 6], [1], 8), ([0, 4], [4, 6], [-1], 8), ([0, 4], [4, 6], [], 8), ([0, 4], None, [0], 8),
+    ([0, 4], [4, 9], [0], 8), ([-1, 4], None, None, 8), ([0, 4, 3], None, None, 8), (None, [0, 2], [0], 8),
+])
+def test_packed_positions_refuses(args):
+    with pytest.raises(ValueError):
+        spanla.packed_positions(*args)
+
+
+def test_packed_positions():
+    pos = spanla.packed_positions([1, 4, 4], [4, 6, 6, 7], [0, 0, 1], 9)
+    assert pos.dtype == np.int32 and pos.tolist() == [-1, 0, 1, 2, 3, 4, 0, -1, -1]
