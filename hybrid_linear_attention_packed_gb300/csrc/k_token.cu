@@ -14,7 +14,9 @@ namespace {
 // One CTA of 128 threads per (token, head): S <- a S + k v^T, o = S^T q.
 // Thread (ir, jg) holds rows ir + 8 u (u = 0..7), columns 4 jg .. 4 jg + 3, so
 // that all 16 KiB of the state are in flight at once and every warp load or
-// store covers two whole rows.
+// store covers two whole rows.  Bound by the state's way in and out, 32 KiB a
+// token and head: 1,024 tokens of 16 heads take 82.6 us (bf16), 6.6 TB/s; one
+// token takes a launch, 2 us.
 constexpr int kStepThreads = 128;
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -113,7 +115,9 @@ cudaError_t step_chunk(const StepArgs& a, int64_t t0, int64_t n, cudaStream_t st
 // ------------------------------------------------------------------ norm and rotation
 // One warp per row.  A lane holds 16 bytes of a head (kVec values; kLanes
 // lanes a head), so a warp step covers 4 (bf16) or 2 (fp32) heads; two steps
-// of each side are in flight.
+// of each side are in flight.  Bound by memory: 43,758 rows of 16 + 16 heads in
+// fp32 take 110.6 us (6.5 TB/s); 7,829 rows in bf16, 1.6 warps for every one that
+// fits, 16.5 us cold (3.9 TB/s, issue slots 54 % busy).
 //
 // The angle of position p and frequency f (in turns, f / 2 pi) is p f mod 1.
 // f is held as a 64-bit binary fraction F, so that the low 64 bits of p F are
