@@ -8,26 +8,29 @@
 // view's final state), and the output of every piece from its start state.
 // Every product and sum is fp32.
 //
-// Rows come in chunks of 12.  A piece state adds a^(n-1-r) k_r v_r^T to a^n S
+// Rows come in chunks of 16.  A piece state adds a^(n-1-r) k_r v_r^T to a^n S
 // over a chunk of n rows: 4096 multiply-adds a row and head.  An output chunk
 // keeps S_r / a^(r+1) instead of S_r, so that the update is one multiply-add
 // for each element, k_r / a^(r+1) times v_r, and the output another, a^(r+1)
 // times at the end: 8192 a row and head, where the recurrence as written takes
-// 12288.  A head with a < e^-2, for which a^-12 could leave the fp32 range,
+// 12288.  A head with a < e^-1.5, for which a^-16 could leave the fp32 range,
 // takes it as written.
 //
-// Bound by the fp32 pipe, not by memory (1 KB a row and head): 7,796 rows of 16
-// heads take 111 us (35 us the piece states, 12 the scan, 75 the outputs, their
-// ends overlapped), the fp32 pipe 45 % busy and the issue slots 50 % with the 16
-// warps that the registers of the states leave room for.
+// One warp per (piece, head): thread (rg, cg) holds rows 16 rg .. and columns
+// 4 cg .. and 32 + 4 cg .. of S, 16 x 8, in registers, so that a row costs it 16
+// values each of k and q and 8 of v from shared memory for 256 multiply-adds, two
+// rows of S at a time (f32x2).  Partial outputs are added over the 4 row groups
+// by shuffles (each lane keeps 2 columns).  Rows come by 16-byte asynchronous
+// copies, one chunk ahead, and k and v of a row from shared memory while the row
+// before it is multiplied.
 //
-// One CTA of 64 threads per (piece, head): thread (rg, cg) holds the 8 x 8
-// block of S at rows 8 rg, columns 8 cg in registers, so that a row costs it
-// 8 values each of q, k and v from shared memory for 128 multiply-adds, two
-// rows of S at a time (f32x2).  Partial outputs are added over the 8 row groups:
-// 4 inside a warp by shuffles (each lane keeps 2 columns), 2 across the warps
-// through shared memory.  Rows come by 16-byte asynchronous copies, one chunk
-// ahead.
+// Bound by the fp32 pipe, not by memory (1 KB a row and head): 7,796 rows of 16
+// heads take 90 us (30 us the piece states, 13 the scan, 60 the outputs, their
+// ends overlapped), the pipe 52 % busy with the 8 warps that the registers
+// of the states leave room for.  With 8 x 8 blocks, two warps a piece and 16 on an
+// SM, the loads and sums around the multiply-adds took a third more
+// instructions: 111 us, 99 with this block at the same pieces.  Outputs
+// interleaved with the update (102), two rows unrolled (106): slower.
 #include "decay_math.cuh"
 #include "spanla_internal.h"
 #include "tc_ptx.cuh"
@@ -35,17 +38,22 @@
 namespace spanla {
 namespace {
 
-constexpr int kThreads = 64;
-constexpr float kSteepLogDecay = -2.f;
-constexpr int kRows = 12;    // rows of a chunk: eight CTAs' buffers fill the shared memory
+constexpr int kThreads = 32;
+constexpr int kPairs = 8;      // pairs of rows of S a thread holds
+constexpr float kSteepLogDecay = -1.5f;
+constexpr int kRows = 16;    // rows of a chunk: eight CTAs' buffers fill the shared memory
 
-// 8 consecutive values as four pairs.
-__device__ __forceinline__ void get_pairs(const float* p, uint64_t (&x)[4]) {
-  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+// 16 consecutive values as eight pairs.
+__device__ __forceinline__ void get_pairs(const float* p, uint64_t (&x)[kPairs]) {
+#pragma unroll
+  for (int i = 0; i < kPairs; i += 2) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
+    x[i] = a.x; x[i + 1] = a.y;
+  }
 }
+// Columns 4 cg .. 4 cg + 3 of a row and the same of its second half.
 __device__ __forceinline__ void get8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + kHeadDim / 2);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
@@ -62,7 +70,6 @@ __device__ __forceinline__ void cp_async_wait() {
 template <bool kOut>
 struct Smem {
   float row[2][kOut ? 3 : 2][kRows][kHeadDim];            // K, V (and Q) of two chunks
-  float part[kOut ? 2 : 1][kOut ? kRows : 1][kHeadDim];   // a warp's partial outputs
   float up[kRows + 1], down[kRows + 1];                   // a^m and a^-m
 };
 
@@ -75,7 +82,7 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
   griddep_launch_dependents();   // (the next launch waits for this one's end before it reads)
   const int h = blockIdx.x % H;
   const RecurUnit u = units[blockIdx.x / H];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int rg = tid >> 3, cg = tid & 7;
   const float ld = load_log_decay(log_decay, h);
   const float l2 = decay_log2(ld);
@@ -103,20 +110,20 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
   load(0, 0);
   cp_async_commit();
 
-  uint64_t S[4][8];   // four pairs of rows, 8 columns
+  uint64_t S[kPairs][8];   // pairs of rows, 8 columns
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kPairs; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) S[i][j] = 0;
   if (kOut) {
     griddep_wait();   // start states from the scan
     // Start state: the scanned prefix of the segment's earlier rows, plus the
     // parent view's final state decayed over them.
-    const int64_t slice = static_cast<int64_t>(8 * rg) * kHeadDim + 8 * cg;
+    const int64_t slice = static_cast<int64_t>(2 * kPairs * rg) * kHeadDim + 4 * cg;
     auto add = [&](const float* p, float f) {
       const uint64_t f2 = f32x2(f, f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kPairs; ++i) {
         float x[8], y[8];
         get8(p + 2 * i * kHeadDim, x);
         get8(p + (2 * i + 1) * kHeadDim, y);
@@ -132,7 +139,7 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
   auto decay_state = [&](const Factor f) {
     const uint64_t hi = f32x2(f.hi, f.hi), lo = f32x2(f.lo, f.lo);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kPairs; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) S[i][j] = fma_f32x2(hi, S[i][j], mul_f32x2(lo, S[i][j]));
   };
@@ -142,38 +149,43 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
     if (r0 + kRows < u.len) load(r0 + kRows, b ^ 1);
     cp_async_commit();
     cp_async_wait<1>();
-    __syncthreads();
+    __syncwarp();
     const Factor fn = n == kRows ? f_chunk : decay_factor(ld, static_cast<float>(n));
     if (!kOut) decay_state(fn);
+    uint64_t kr[kPairs];
+    float vr[8], w;
+    auto fetch = [&](int r) {
+      get_pairs(&sm.row[b][0][r][2 * kPairs * rg], kr);
+      get8(&sm.row[b][1][r][4 * cg], vr);
+      w = kOut ? sm.down[r + 1] : sm.up[max(n - 1 - r, 0)];
+    };
+    fetch(0);
     for (int r = 0; r < n; ++r) {
-      uint64_t kr[4];
-      float vr[8];
-      get_pairs(&sm.row[b][0][r][8 * rg], kr);
-      get8(&sm.row[b][1][r][8 * cg], vr);
+      uint64_t qr[kPairs];
+      if (kOut) get_pairs(&sm.row[b][kOut ? 2 : 0][r][2 * kPairs * rg], qr);
       if (steep) {
         const uint64_t a2 = f32x2(a1, a1);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint64_t v2 = f32x2(vr[j], vr[j]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[i][j] = fma_f32x2(a2, S[i][j], mul_f32x2(kr[i], v2));
+          for (int i = 0; i < kPairs; ++i) S[i][j] = fma_f32x2(a2, S[i][j], mul_f32x2(kr[i], v2));
         }
       } else {
-        const float w = kOut ? sm.down[r + 1] : sm.up[n - 1 - r];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kr[i] = mul_f32x2(kr[i], f32x2(w, w));
+        for (int i = 0; i < kPairs; ++i) kr[i] = mul_f32x2(kr[i], f32x2(w, w));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint64_t v2 = f32x2(vr[j], vr[j]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[i][j] = fma_f32x2(kr[i], v2, S[i][j]);
+          for (int i = 0; i < kPairs; ++i) S[i][j] = fma_f32x2(kr[i], v2, S[i][j]);
         }
       }
+      fetch(min(r + 1, kRows - 1));
       if (kOut) {
-        uint64_t qr[4], o2[8];
-        get_pairs(&sm.row[b][kOut ? 2 : 0][r][8 * rg], qr);
+        uint64_t o2[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kPairs; ++i)
 #pragma unroll
           for (int j = 0; j < 8; ++j) o2[j] = i == 0 ? mul_f32x2(qr[0], S[0][j]) : fma_f32x2(qr[i], S[i][j], o2[j]);
         float o[8];
@@ -183,9 +195,9 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
           f32x2_split(o2[j], lo, hi);
           o[j] = lo + hi;
         }
-        // Add over the warp's 4 row groups (lane bits 3 and 4), each step
-        // keeping half of the columns.
-        const bool up4 = lane & 16, up3 = lane & 8;
+        // Add over the 4 row groups (lane bits 3 and 4), each step keeping half
+        // of the columns.
+        const bool up4 = tid & 16, up3 = tid & 8;
         float x[4], y[2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -197,37 +209,27 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
           const float give = up3 ? x[j] : x[2 + j];
           y[j] = (up3 ? x[2 + j] : x[j]) + __shfl_xor_sync(0xffffffffu, give, 8);
         }
-        const float w = steep ? 1.f : sm.up[r + 1];
-        *reinterpret_cast<float2*>(&sm.part[kOut ? warp : 0][kOut ? r : 0][8 * cg + (up4 ? 4 : 0) + (up3 ? 2 : 0)]) =
-            make_float2(y[0] * w, y[1] * w);
+        const float f = steep ? 1.f : sm.up[r + 1];
+        *reinterpret_cast<float2*>(out + base + (r0 + r) * stride + 4 * cg + (up4 ? kHeadDim / 2 : 0) + (up3 ? 2 : 0)) =
+            make_float2(y[0] * f, y[1] * f);
       }
     }
     if (kOut && !steep) decay_state(fn);
-    __syncthreads();
-    if (kOut) {
-      for (int c = tid; c < n * (kHeadDim / 4); c += kThreads) {
-        const int r = c / (kHeadDim / 4), x = 4 * (c % (kHeadDim / 4));
-        const float4 p0 = *reinterpret_cast<const float4*>(&sm.part[0][kOut ? r : 0][x]);
-        const float4 p1 = *reinterpret_cast<const float4*>(&sm.part[kOut ? 1 : 0][kOut ? r : 0][x]);
-        *reinterpret_cast<float4*>(out + base + (r0 + r) * stride + x) =
-            make_float4(p0.x + p1.x, p0.y + p1.y, p0.z + p1.z, p0.w + p1.w);
-      }
-      // (The next chunk's partial outputs are written behind its barrier.)
-    }
+    __syncwarp();
   }
   if (!kOut) {
-    float* p = ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + static_cast<int64_t>(8 * rg) * kHeadDim + 8 * cg;
+    float* p = ws + (static_cast<int64_t>(u.slot) * H + h) * kStateFloats + static_cast<int64_t>(2 * kPairs * rg) * kHeadDim + 4 * cg;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       float x[8], y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f32x2_split(S[i][j], x[j], y[j]);
       float* p0 = p + 2 * i * kHeadDim;
       float* p1 = p0 + kHeadDim;
       *reinterpret_cast<float4*>(p0) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(p0 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<float4*>(p0 + kHeadDim / 2) = make_float4(x[4], x[5], x[6], x[7]);
       *reinterpret_cast<float4*>(p1) = make_float4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<float4*>(p1 + 4) = make_float4(y[4], y[5], y[6], y[7]);
+      *reinterpret_cast<float4*>(p1 + kHeadDim / 2) = make_float4(y[4], y[5], y[6], y[7]);
     }
   }
 }

@@ -1550,42 +1550,52 @@ struct RecurPlan {
   int64_t slots = 0;
 };
 
-// Rows of a piece, in whole chunks of 16: so many that the pieces of every
-// head, with the branches, fill the units that the SMs run at once (every unit
-// then starts at once; a second round of a few would double the time), but
-// at least a 64th of the longest segment (the scan walks a segment's pieces in
-// turn), and at most 256 (the end of a launch waits for the last piece).
-int recur_piece(int64_t rows, int64_t longest, int64_t segments, int H, int num_sms) {
+// Rows of a piece, in whole chunks of 16: so many that the pieces fill the
+// units that the SMs run at once; but no fewer than the square root of a tenth of
+// the longest segment (the scan takes some 0.05 us a slot, a piece 0.5 us a row),
+// and no more than 256 (the end of a launch waits for the last piece).  Branches
+// alone, of up to 128 rows, are not cut: they take one launch then (64 of them
+// 59 us, 78 in pieces of 64 rows).  Measured: 7,400 rows of 16 heads in pieces
+// of 80, 96, 112, 128, 160 rows 100, 112, 90, 100, 121 us (this rule: 112); of 8
+// heads in 48, 64, 80, 128 rows 70, 57, 68, 84 (64); of one in 16, 32, 48,
+// 128 rows 37, 35, 40, 80 (32); 18,000 rows of 16 heads in 128, 192, 256, 320 rows
+// 197, 213, 195, 229 (256).
+int recur_piece(int64_t rows, int64_t longest, bool branches_only, int H, int num_sms) {
+  constexpr int64_t kChunk = 16, kUncut = 128, kMost = 256;
+  if (branches_only && longest <= kUncut) return kUncut;
   const int64_t units = static_cast<int64_t>(std::max(1, num_sms)) * kRecurUnitsPerSm;
-  const int64_t free_units = std::max(units - segments * H, units / 2);   // (a segment's last piece is a part one)
-  const int64_t want = std::max((rows * H + free_units - 1) / free_units, (longest + 63) / 64);
-  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(256, (longest + 63) / 64 / 16 * 16 + 16),
-                                            std::max<int64_t>(16, (want + 15) / 16 * 16)));
+  int64_t least = kChunk;
+  while (10 * least * least < longest) least += kChunk;
+  const int64_t fill = (rows * H + units - 1) / units;
+  return static_cast<int>(std::max(least, std::min(kMost, (fill + kChunk - 1) / kChunk * kChunk)));
 }
 
 RecurPlan make_recur_plan(const int32_t* view_cu, int32_t V, const int32_t* branch_cu, int32_t B,
                           const int32_t* parent, int H, int num_sms) {
   RecurPlan plan;
-  int64_t rows = 0, longest = 0, segments = 0;
+  int64_t rows = 0, longest = 0;
   for (const auto& cu : {std::make_pair(view_cu, V), std::make_pair(branch_cu, B)})
     for (int32_t s = 0; s < cu.second; ++s) {
       const int64_t len = cu.first[s + 1] - cu.first[s];
       rows += len;
       longest = std::max(longest, len);
-      segments += len > 0;
     }
-  plan.piece = recur_piece(rows, longest, segments, H, num_sms);
+  plan.piece = recur_piece(rows, longest, V == 0, H, num_sms);
   auto add = [&](int64_t start, int64_t len, int view, int par) {
-    const int64_t n = (len + plan.piece - 1) / plan.piece;
+    // A branch of little more than a piece stays whole, without a state.  (16
+    // branches of 100 rows, 32 heads, in pieces of 96: 128 us cut, 79 whole.)
+    const bool whole = view < 0 && 2 * len <= 3 * plan.piece;
+    const int64_t step = whole ? std::max<int64_t>(len, 1) : plan.piece;
+    const int64_t n = (len + step - 1) / step;
     if (n == 0 && view < 0) return;
     const bool slots = view >= 0 || n > 1;
     const int32_t slot0 = static_cast<int32_t>(plan.slots);
     for (int64_t c = 0; c < n; ++c) {
       RecurUnit u{};
-      u.row0 = static_cast<int32_t>(start + c * plan.piece);
-      u.len = static_cast<int32_t>(std::min<int64_t>(plan.piece, len - c * plan.piece));
+      u.row0 = static_cast<int32_t>(start + c * step);
+      u.len = static_cast<int32_t>(std::min<int64_t>(step, len - c * step));
       u.parent = par;
-      u.before = static_cast<int32_t>(c * plan.piece);
+      u.before = static_cast<int32_t>(c * step);
       u.slot = slots ? static_cast<int32_t>(slot0 + c) : -1;
       if (slots && (view >= 0 || c + 1 < n)) plan.state.push_back(u);
       if (c == 0) u.slot = -1;
