@@ -1905,17 +1905,22 @@ span_la_status check_grid(int64_t units, int H) {
   return SPAN_LA_OK;
 }
 
-// A body that may allocate on the host, as a C entry: an allocation failure
-// becomes a status.
+// A body that may allocate on the host, as a C entry: nothing that it throws
+// gets out, an allocation failure becomes a status (without its text when there
+// is no room for that either).
 template <typename Fn>
 span_la_status guarded(Fn&& fn) {
   try {
-    g_detail.clear();
-    return fn();
-  } catch (const std::bad_alloc&) {
-    return fail(SPAN_LA_ERR_NOMEM, "out of host memory");
-  } catch (const std::exception& ex) {
-    return fail(SPAN_LA_ERR_INVALID, "%s", ex.what());
+    try {
+      g_detail.clear();
+      return fn();
+    } catch (const std::bad_alloc&) {
+      return fail(SPAN_LA_ERR_NOMEM, "out of host memory");
+    } catch (const std::exception& ex) {
+      return fail(SPAN_LA_ERR_INVALID, "%s", ex.what());
+    }
+  } catch (...) {
+    return SPAN_LA_ERR_NOMEM;
   }
 }
 

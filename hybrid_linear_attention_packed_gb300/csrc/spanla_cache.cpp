@@ -333,8 +333,8 @@ span_la_status span_la_cache_decay_branches(span_la_view_cache* cache, const uin
       return span_la_decay_branches_from_state(cache->pool, cache->capacity, q, k, v, dims, log_decay, branch_cu_seqlens,
                                                num_branches, slots, out, stream);
     });
-  } catch (const std::exception& e) {
-    return cache_fail(SPAN_LA_ERR_NOMEM, "out of host memory: %s", e.what());
+  } catch (const std::exception&) {
+    return SPAN_LA_ERR_NOMEM;
   }
 }
 
