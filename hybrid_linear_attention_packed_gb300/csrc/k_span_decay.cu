@@ -30,9 +30,13 @@
 // cold).  Large passes are bound by DRAM: K and V are read once for each phase
 // and the table is written and read, 679 MB for four requests where the call's
 // own inputs and outputs are 359 MB, at 5.8 TB/s (85 % of what a copy reaches);
-// the chains would take about as long, 1.1 us a tile in phase 1 and 1.6 in
-// phase 2.  Small ones are bound by latency: launch, one tile through phase 1,
-// the grid-wide counter, one tile through phase 2.
+// the chains would take about as long, 1.0 us a tile in phase 1 and 1.6 in
+// phase 2.  Phase 1 is bound by shared memory: 176 KB go in and out a tile (K and
+// V, V read and written three times as wide, the operands read), 1,400 cycles
+// of the 1,850 that its products take one behind the other; the output warps'
+// help with V' (16 warps instead of 8) changed nothing.  Small passes are bound by
+// latency: launch, their tiles through phase 1, the grid-wide counter, their tiles
+// through phase 2.
 //
 // The runs are cut to equal numbers of tiles, whatever they are: with the tiles
 // that have a phase-1 part weighted 2 : 1 against packed branches, sixteen requests
