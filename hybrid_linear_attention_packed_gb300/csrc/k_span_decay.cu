@@ -22,11 +22,11 @@
 // is bound by the latency of its hand-offs.  Keeping it there (the first
 // phase then only for pieces that others need, the running state carried from
 // tile to tile as span_output does) took 5,300 cycles a tile and 198 us for a
-// pass of four requests, against 121.
+// pass of four requests, against 120.
 //
 // Measured, 16 heads: 7,796 rows (a view of 7,400 and 8 branches) 26.7 us with
-// the inputs in L2 and 28.8 us cold; 43,684 rows of four requests 121 us;
-// 208,830 rows of sixteen 515 us; 64 branches from a kept state 14.4 us (16.4
+// the inputs in L2 and 28.8 us cold; 43,684 rows of four requests 120 us;
+// 208,830 rows of sixteen 509 us; 64 branches from a kept state 14.4 us (16.4
 // cold).  Large passes are bound by DRAM: K and V are read once for each phase
 // and the table is written and read, 679 MB for four requests where the call's
 // own inputs and outputs are 359 MB, at 5.8 TB/s (85 % of what a copy reaches);
@@ -545,14 +545,15 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
     }
     Mask nxt = n > 0 ? load_mask4(list) : Mask{};
-    float nxt_l2 = n > 0 ? decay_log2(load_log_decay(prm.log_decay, nxt.head)) : 0.f;
+    int head = -1;
+    float l2 = 0.f;
     for (int i = 0; i < n && ok; ++i, ++u) {
       const Mask r = nxt;
-      const float l2 = nxt_l2;
-      if (i + 1 < n) {
-        nxt = load_mask4(list + i + 1);
-        nxt_l2 = decay_log2(load_log_decay(prm.log_decay, nxt.head));
+      if (r.head != head) {   // (a load whose address is itself on its way would hold up every tile)
+        head = r.head;
+        l2 = decay_log2(load_log_decay(prm.log_decay, head));
       }
+      if (i + 1 < n) nxt = load_mask4(list + i + 1);
       const int b = i & 1;
       if (!__all_sync(0xffffffffu, wait_or_flag(bar(L::kFull + u % kStages), (u / kStages) & 1, err, kErrTimeoutTma))) break;
       // V's rows past the tile, its infinities and NaNs become zero (0 times
