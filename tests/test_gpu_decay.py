@@ -16,6 +16,7 @@ o_t, and n the rows the sum runs over.
 * states are fp32 in both: |error| <= (2 n + 128) 2^-24 A_S.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -494,3 +495,38 @@ def test_a_layer_from_projection_to_next_tokens(cuda_device, dtype):
         assert torch.linalg.norm(a - b) <= (2e-5 if dtype == "f32" else 1e-2) * torch.linalg.norm(b)
     span_la_check()
     assert torch.linalg.norm(states.double() - final.double()) <= 1e-5 * torch.linalg.norm(final.double())
+
+
+def test_calls_from_several_host_threads(cuda_device):
+    """Four host threads, each on a stream of its own, with plans that they share: the results of one call after another."""
+    ws = [workloads.make_pass([900, 300], [60, 5, 200], [0, 1, 0], H=3, dtype=d, seed=31) for d in ("bf16", "f32")]
+    ws += [workloads.make_pass([2000], [40] * 6, [0] * 6, H=4, dtype=d, seed=32) for d in ("bf16", "f32")]
+    args = []
+    for w in ws:
+        q, k, v = (x.to(cuda_device) for x in (w.q, w.k, w.v))
+        args.append((q, k, v, torch.from_numpy(_decays(q.shape[1], "slopes")).to(cuda_device), w.view_cu, w.branch_cu,
+                     w.branch_parent))
+    want = [span_la_decay_pass(*a) for a in args]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(t):
+        try:
+            torch.cuda.set_device(cuda_device)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for i in range(40):
+                    j = (i + t) % len(args)
+                    out, state = span_la_decay_pass(*args[j])
+                    if not (torch.equal(out, want[j][0]) and torch.equal(state, want[j][1])):
+                        wrong.append((t, i, j))
+        except Exception as e:   # noqa: BLE001 (a thread's exception would be lost)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    span_la_check()
+    assert wrong == []
