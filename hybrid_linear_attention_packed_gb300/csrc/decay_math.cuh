@@ -9,6 +9,7 @@
 // expm1 while it is near 1.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 
 namespace spanla {
@@ -34,20 +35,26 @@ __device__ __forceinline__ float decay_pow_fast(float l2, float n) {
   return y;
 }
 
-// a^n as hi + lo (lo = 0 below 1/2, where nothing is remembered for long).
+// a^n as hi + lo, lo of hi's sign and 0 only with it, so that an infinite state
+// stays infinite (hi s and lo s agree; with lo = 0, or of the other sign, their
+// sum would be NaN).  Where a^n is hi, lo is too small to be seen beside it.
 struct Factor {
   float hi, lo;
   // a^n s + x, with one rounding of a^n in effect.
   __device__ __forceinline__ float step(float s, float x) const { return fmaf(hi, s, fmaf(lo, s, x)); }
 };
 
+constexpr Factor kNoDecay = {1.f, FLT_MIN};
+
 __device__ __forceinline__ Factor decay_factor(float ld, float n) {
   const float m1 = expm1f(ld * n);   // a^n - 1
   if (m1 > -0.5f) {
-    const float hi = 1.f + m1;
-    return {hi, m1 - (hi - 1.f)};    // (both differences exact for hi in [1/2, 2])
+    const float hi = __fadd_rd(1.f, m1);
+    return {hi, fmaxf(m1 - (hi - 1.f), FLT_MIN)};   // (both differences exact for hi in [1/2, 2])
   }
-  return {expf(ld * n), 0.f};
+  // Below 1/2, where nothing is remembered for long, hi alone.
+  const float hi = expf(ld * n);
+  return {hi, hi > 0.f ? fmaxf(hi * 0x1p-40f, 0x1p-149f) : 0.f};
 }
 
 }  // namespace spanla

@@ -66,7 +66,7 @@ decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __r
     sk[tid] = to_float(k[row + tid]);
   }
   const float4 x = load4(v + row + 4 * jg);
-  const Factor g = log_decay != nullptr ? decay_factor(load_log_decay(log_decay, h), 1.f) : Factor{1.f, 0.f};
+  const Factor g = log_decay != nullptr ? decay_factor(load_log_decay(log_decay, h), 1.f) : kNoDecay;
   __syncthreads();
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
