@@ -234,19 +234,32 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t (&part)[kParts]) {
   }
 }
 
-// Eight values of V with an infinity or a NaN among them: its parts of V'
-// once more, without remainders of those (inf - inf).
-__device__ __noinline__ void repair_piece(const uint8_t* src, uint8_t* dst, float f) {
-  const uint32_t* v = reinterpret_cast<const uint32_t*>(src);
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t keep = (nonfinite_lo(v[e]) ? 0u : 0xffffu) | (nonfinite_hi(v[e]) ? 0u : 0xffff0000u);
-    uint32_t part[kParts];
-    split3(mul_f32x2(f32x2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)), f32x2(f, f)), part);
-    for (int p = 0; p < kParts; ++p)
-      reinterpret_cast<uint32_t*>(dst + p * kRowTileBytes)[e] = p == 0 ? part[p] : part[p] & keep;
+// The infinite and NaN ones among 16 products sum_j a^(rows-1-j) k_jd v_jc (c
+// from col on), once more from the definition: an infinity in K or V met parts of
+// V' that are 0 or a remainder of itself, and made NaN where the sum is infinite.
+__device__ __noinline__ void redo_products(const DecayParams& prm, int64_t row0, int rows, int head, int d, int col, float l2,
+                                           float* x) {
+  const int64_t stride = static_cast<int64_t>(prm.H) * kHeadDim;
+  const int64_t at = row0 * stride + static_cast<int64_t>(head) * kHeadDim;
+  float sum[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) sum[c] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < rows; ++j) {
+    const float f = decay_pow(l2, static_cast<float>(rows - 1 - j)) * __bfloat162float(prm.k[at + j * stride + d]);
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(prm.v + at + j * stride + col);
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const uint32_t w = v[c / 2];
+      sum[c] = fmaf(f, __uint_as_float(w << 16), sum[c]);
+      sum[c + 1] = fmaf(f, __uint_as_float(w & 0xffff0000u), sum[c + 1]);
+    }
   }
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (!isfinite(x[c])) x[c] = sum[c];
 }
-// ... and zeros in their place.
+// Zeros in place of the infinite and NaN ones of eight values of V.
 __device__ __noinline__ void clear_nonfinite(uint8_t* src) {
   uint32_t* v = reinterpret_cast<uint32_t*>(src);
   for (int e = 0; e < 4; ++e) v[e] &= (nonfinite_lo(v[e]) ? 0u : 0xffffu) | (nonfinite_hi(v[e]) ? 0u : 0xffff0000u);
@@ -514,13 +527,11 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (!ok) break;
         uint8_t* src = smem + L::kStage0 + (u % kStages) * kStageBytes + my16;
         uint8_t* dst = smem + ((u & 1) ? L::kVs1 : L::kVs0) + ct * 16;
-        uint32_t bad = 0;
 #pragma unroll 4
         for (int w = 0; w < kPieces; ++w) {
           const int r = piece_row(w);
           const uint4 x4 = r < rows ? *reinterpret_cast<const uint4*>(src + kPieceStep * w) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-          bad |= (nonfinite2(x[0]) | nonfinite2(x[1]) | nonfinite2(x[2]) | nonfinite2(x[3])) << w;
           const float f = decay_pow_fast(l2, static_cast<float>(max(rows - 1 - r, 0)));
           uint4 part[kParts];
 #pragma unroll
@@ -533,12 +544,6 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
           for (int p = 0; p < kParts; ++p)
             *reinterpret_cast<uint4*>(dst + p * kRowTileBytes + kPieceStep * w) = part[p];
-        }
-        if (bad != 0) {
-          for (int w = 0; w < kPieces; ++w)
-            if ((bad >> w) & 1)
-              repair_piece(src + kPieceStep * w, dst + kPieceStep * w,
-                           decay_pow_fast(l2, static_cast<float>(rows - 1 - piece_row(w))));
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(L::kVReady + (u & 1)));
@@ -710,9 +715,23 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           tmem_ld_wait();
           tc_fence_before_sync();
           mbar_arrive(bar(L::kP1Free + b));
+          float bad = 0.f;   // NaN if a product is infinite or NaN
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
+            bad = fmaf(__uint_as_float(x[e]), 0.f, bad);
+          }
+          if (bad != 0.f) {
+            float z[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[e] = __uint_as_float(x[e]);
+            redo_products(prm, sd.row0 + r, min(sd.len - r, kTileRows), sd.head, d, col0, decay_log2(ld), z);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(z[e]);
+          }
           const Factor f = sd.len - r >= kTileRows ? f_tile : factor_of(ld, static_cast<float>(sd.len - r));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[e] = f.step(s[e], __uint_as_float(x[e]) + __uint_as_float(y[e]));
+          for (int e = 0; e < 16; ++e) s[e] = f.step(s[e], __uint_as_float(x[e]));
           if (t < sd.n_table) {
             float4* p = table_at(static_cast<int64_t>(sd.table0) + t);
 #pragma unroll

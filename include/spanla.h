@@ -456,7 +456,7 @@ span_la_status span_la_softmax_branches_from_kv(const void *view_k, const void *
  *
  * (span_la_pass is the case a_h = 1.)  Unrolled from a start state S0 before
  * row t0:  o_t = sum_{t0 <= j <= t} a^(t-j) (q_t . k_j) v_j + a^(t-t0+1) S0^T q_t.
- * An infinite value or state gives what these say, an infinity or (0 times one,
+ * An infinite key, value or state gives what these say, an infinity or (0 times one,
  * two of opposite signs) a NaN, in the rows and states that see it and no others;
  * the terms of one row are added by the first form or by the second.  A factor
  * a^n below the range of fp32 counts as 0.

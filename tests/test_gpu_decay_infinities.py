@@ -92,3 +92,16 @@ def test_infinite_values_over_tiles_and_pieces(cuda_device, layout, dtype):
     w.v[int(w.view_cu[-1]) - 100, :, 1] = INF            # (in the last view, or the only one)
     w.v[int(w.branch_cu[1]) - 4, :, 20] = -INF           # (in the first branch)
     _compare(w, ld, cuda_device)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", sorted(LAYOUTS))
+def test_infinite_keys_over_tiles_and_pieces(cuda_device, layout, dtype):
+    """k_ti = inf: row i of the state, with v's signs; where v is 0, inf times 0."""
+    w, ld = _workload(layout, dtype, 42)
+    w.v = w.v.abs() + 0.1
+    w.v[:, :, 40] *= -1
+    w.k[5, :, 2] = INF
+    w.v[5, :, 11] = 0
+    w.k[int(w.view_cu[1]) - 1, 0, 17] = INF              # (in the first view's last row, whose factor is 1)
+    _compare(w, ld, cuda_device)
