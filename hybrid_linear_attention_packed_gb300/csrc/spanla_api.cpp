@@ -1751,7 +1751,9 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
   const DecayWorkspace at(*desc);
   uint8_t* ws = nullptr;
   uint8_t* own = nullptr;   // allocated by this call
-  if (use_cache && desc->kept_ws >= at.bytes) {
+  if (use_cache && at.bytes == 0) {
+    // No workspace (branches of one tile): nothing to wait for.
+  } else if (use_cache && desc->kept_ws >= at.bytes) {
     // The plan's workspace: behind the calls that used it, on whatever streams.
     ws = const_cast<uint8_t*>(block) + align256(desc->host.size());
     for (const auto& r : entry->readers)
