@@ -975,6 +975,9 @@ cudaError_t upload_pinned(void* dst, const std::vector<uint8_t>& bytes, int devi
 // into a graph bypass the cache.
 constexpr int kCacheEntries = 16;
 constexpr size_t kMaxReaders = 8;
+// Workspaces that decayed passes keep with their plans (kKeptWorkspaceBytes
+// each at most): this much in all, whatever metadata comes.
+constexpr size_t kKeptTotalBytes = size_t(256) << 20;
 
 struct CacheEntry {
   int device = -1;
@@ -1116,22 +1119,30 @@ span_la_status cached_block(const std::vector<int32_t>& key, int device, cudaStr
       return SPAN_LA_OK;
     }
   }
-  int on_device = 0;
-  size_t victim = g_cache.size();
-  for (size_t i = 0; i < g_cache.size(); ++i) {
-    if (g_cache[i].device != device) continue;
-    ++on_device;
-    if (victim == g_cache.size() || g_cache[i].last_use < g_cache[victim].last_use) victim = i;
-  }
-  if (on_device >= kCacheEntries) {
-    cudaError_t e = release_entry(g_cache[victim], stream);
-    if (e != cudaSuccess) return cuda_fail(e, "plan cache eviction");
-    g_cache.erase(g_cache.begin() + victim);
-  }
   CacheEntry en;
   en.device = device;
   en.key = key;
   en.desc = build();
+  // The least recently used block goes when there are as many as the cache
+  // holds, and of those with a workspace while theirs come to too much.
+  while (true) {
+    int on_device = 0;
+    size_t kept = en.desc.kept_ws;
+    size_t victim = g_cache.size(), kept_victim = g_cache.size();
+    for (size_t i = 0; i < g_cache.size(); ++i) {
+      if (g_cache[i].device != device) continue;
+      ++on_device;
+      if (victim == g_cache.size() || g_cache[i].last_use < g_cache[victim].last_use) victim = i;
+      if (g_cache[i].desc.kept_ws == 0) continue;
+      kept += g_cache[i].desc.kept_ws;
+      if (kept_victim == g_cache.size() || g_cache[i].last_use < g_cache[kept_victim].last_use) kept_victim = i;
+    }
+    if (kept > kKeptTotalBytes && kept_victim < g_cache.size()) victim = kept_victim;
+    else if (on_device < kCacheEntries) break;
+    cudaError_t e = release_entry(g_cache[victim], stream);
+    if (e != cudaSuccess) return cuda_fail(e, "plan cache eviction");
+    g_cache.erase(g_cache.begin() + victim);
+  }
   const size_t bytes = std::max<size_t>(align256(en.desc.host.size()) + en.desc.kept_ws, 256);
   if (injected_alloc_failure())
     return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(descriptors, %zu): injected failure", bytes);
