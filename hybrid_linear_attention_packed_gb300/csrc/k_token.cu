@@ -121,8 +121,11 @@ cudaError_t step_chunk(const StepArgs& a, int64_t t0, int64_t n, cudaStream_t st
 //
 // The angle of position p and frequency f (in turns, f / 2 pi) is p f mod 1.
 // f is held as a 64-bit binary fraction F, so that the low 64 bits of p F are
-// the angle exactly, whatever the position; its top 32 bits go to
-// sincospi.  The row's angles are computed once, one per lane, for all heads.
+// the angle to p times F's own error (2^-63 at most), below 2^-32 of a turn at any
+// position; its top 32 bits count.  What is left of it beside the nearest quarter
+// turn goes to sincospi, as fp32: 24 bits of at most an eighth of a turn, to
+// 2^-28.  (The whole angle as fp32 was off by 2^-26.)  The row's angles are
+// computed once, one per lane, for all heads.
 //
 // (y_a, y_b) = r (w_a x_a, w_b x_b) rotated by (c, s): each lane keeps its
 // dimensions' own factors c w and their partners' -+ s w, so that an element
@@ -223,9 +226,20 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
 
   if (lane < half) {
     const uint64_t turn = a.freq[lane] * static_cast<uint64_t>(pos);
-    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;   // half turns: 2^-31
+    const uint32_t angle = static_cast<uint32_t>(turn >> 32);
+    const uint32_t quarters = (angle + 0x20000000u) >> 30;
+    const float x = static_cast<float>(static_cast<int32_t>(angle - (quarters << 30))) * 0x1p-31f;   // half turns
     float c, s;
     sincospif(x, &s, &c);
+    if (quarters & 1) {   // a quarter turn further: (c, s) -> (-s, c)
+      const float c0 = c;
+      c = -s;
+      s = c0;
+    }
+    if (quarters & 2) {
+      c = -c;
+      s = -s;
+    }
     table[warp][lane] = make_float2(c, s);
   }
   __syncwarp();

@@ -1937,6 +1937,26 @@ span_la_status guarded(Fn&& fn) {
   }
 }
 
+// x modulo 1 as a 64-bit binary fraction, to half its last bit.
+uint64_t binary_fraction(double x) {
+  double r = x - std::nearbyint(x);   // (exact)
+  if (r >= 0.5) r -= 1.0;
+  if (r < -0.5) r += 1.0;
+  return static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(r * 18446744073709551616.0)));
+}
+
+// radians / (2 pi) modulo 1 as a 64-bit binary fraction F, off by 1.5 units for
+// frequencies below 2^45: position times F, modulo 2^64, is the angle at any
+// position to 2^-32 of a turn.  1 / (2 pi) is a sum of two doubles, its product
+// with the first another one.  (The volatile keeps a compiler from putting the
+// unrounded product in place of the rounded one.)
+uint64_t turn_fraction(double radians) {
+  constexpr double k0 = 0x1.45f306dc9c883p-3, k1 = -0x1.6b01ec5417056p-57;
+  volatile double rounded = radians * k0;
+  const double p0 = rounded;
+  return binary_fraction(p0) + binary_fraction(std::fma(radians, k0, -p0)) + binary_fraction(radians * k1);
+}
+
 // The elements of a [rows] x [width] array with a row stride (bytes).
 struct Rows {
   uintptr_t at;
@@ -2565,9 +2585,7 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
     RopeArgs a{};
     for (int i = 0; i < rotary_dim / 2; ++i) {
       if (!std::isfinite(inv_freq[i])) return fail(SPAN_LA_ERR_INVALID, "inv_freq[%d] is not finite", i);
-      const double turns = inv_freq[i] / 6.283185307179586;
-      const double part = turns - std::floor(turns);   // in [0, 1]: 1 when the fraction rounds up
-      a.freq[i] = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
+      a.freq[i] = turn_fraction(inv_freq[i]);
     }
     const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4;
     Rows in[2], out[2];

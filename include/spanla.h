@@ -552,10 +552,10 @@ typedef struct {
  *
  * for the first rotary_dim of the 64 dimensions; pair i is dimensions
  * (i, i + rotary_dim / 2), or (2i, 2i + 1) when `interleaved` is nonzero.  In
- * fp32, angles to 2^-32 of a turn at any position; rounded once, at the end.
+ * fp32, angles to 2^-27 of a turn at any position; rounded once, at the end.
  *   rows, dtype      rows of both sides and the type of their in and out
  *   weight_dtype     type of the weights (span_la_dtype)
- *   inv_freq         HOST double [rotary_dim / 2], radians per position
+ *   inv_freq         HOST double [rotary_dim / 2], radians per position (below 2^45)
  *   rotary_dim       0 (norm only), 16, 32, 48 or 64
  *   positions        device int32 [rows]; a row whose position is negative is
  *                    neither read nor written
