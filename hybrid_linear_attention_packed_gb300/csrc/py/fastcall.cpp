@@ -16,9 +16,11 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 
 #include "spanla.h"
 
@@ -142,13 +144,14 @@ struct Common {   // q, k, v, log_decay (NULL where allowed) on the current devi
   }
 };
 
-// C++ exceptions (an allocation that fails) become Python's.
+// C++ exceptions become Python's, each the one that torch makes of it (an
+// allocation that fails torch.OutOfMemoryError).
 template <typename Fn>
 PyObject* guarded(Fn&& fn) {
   try {
     return fn();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
