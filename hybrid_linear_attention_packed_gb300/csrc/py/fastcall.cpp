@@ -6,14 +6,17 @@
 //   * returns its result when everything is as it should be and the library
 //     accepted the call;
 //   * returns None, having done nothing, when any argument is not the usual
-//     one: spanla.py then checks them one by one and names the problem, or
-//     makes the call itself;
+//     one, or torch is in a mode in which allocations are more than that:
+//     spanla.py then checks them one by one and names the problem, or makes the
+//     call itself;
 //   * returns the library's status (an int) when the library refused.
 // The library is reached through the addresses that bind() is given, so that
 // it is the one that spanla.py loaded.
 #include <Python.h>
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -31,7 +34,8 @@ decltype(&span_la_decay_branches_from_state) g_fork = nullptr;
 decltype(&span_la_decay_step) g_step = nullptr;
 decltype(&span_la_qk_norm_rope) g_rope = nullptr;
 
-// (without the dispatcher: about 1 us less for a call that returns two tensors)
+// (without the dispatcher: about 1 us less for a call that returns two tensors;
+// see usual_mode)
 at::Tensor new_tensor(at::IntArrayRef size, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
@@ -144,11 +148,16 @@ struct Common {   // q, k, v, log_decay (NULL where allowed) on the current devi
   }
 };
 
+// False where new tensors have to go through the dispatcher: a dispatch mode is to
+// see them, or deterministic algorithms are asked for, which fill them.
+bool usual_mode() { return !c10::impl::dispatch_mode_enabled() && !at::globalContext().deterministicAlgorithms(); }
+
 // C++ exceptions become Python's, each the one that torch makes of it (an
 // allocation that fails torch.OutOfMemoryError).
 template <typename Fn>
 PyObject* guarded(Fn&& fn) {
   try {
+    if (!usual_mode()) Py_RETURN_NONE;
     return fn();
   } catch (...) {
     torch::translate_exception_to_python(std::current_exception());

@@ -1,8 +1,9 @@
 """The binding's extension module makes the same calls as ctypes: the same
-bits, the same errors."""
+bits, the same errors, the same allocations."""
 import numpy as np
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from hybrid_linear_attention_packed_gb300 import (rope_inv_freq, span_la_check, span_la_decay_branches_from_state,
                                                   span_la_decay_pass, span_la_decay_step, span_la_qk_norm_rope, spanla)
@@ -62,3 +63,41 @@ def test_out_of_memory_has_its_own_type(cuda_device, name, fast, monkeypatch):
         torch.cuda.set_per_process_memory_fraction(1.0, cuda_device)
     call()
     span_la_check()
+
+
+def _leave_ones(like):
+    x = torch.ones_like(like)
+    torch.cuda.synchronize()
+    del x
+
+
+def test_new_outputs_are_filled_where_torch_fills_them(cuda_device):
+    """torch.use_deterministic_algorithms fills memory that nothing wrote: NaN in the skipped rows of a step."""
+    q = torch.randn(6, 2, 64, device=cuda_device)
+    pool = torch.randn(2, 2, 64, 64, device=cuda_device)
+    index = np.array([-1, 1, -1, -1, 0, -1], dtype=np.int32)
+    _leave_ones(q)
+    torch.use_deterministic_algorithms(True)
+    try:
+        out = span_la_decay_step(q, q, q, pool, None, index)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    span_la_check()
+    assert torch.isnan(out[torch.from_numpy(index < 0).to(cuda_device)]).all()
+    assert torch.isfinite(out[[1, 4]]).all()
+
+
+@pytest.mark.parametrize("name", ["pass", "fork", "step", "rope"])
+def test_a_dispatch_mode_sees_the_outputs(cuda_device, name):
+    class Seen(TorchDispatchMode):
+        names = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.names.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    call = _calls(cuda_device)[name]
+    with Seen() as seen:
+        call()
+    span_la_check()
+    assert any("empty" in n for n in seen.names)
