@@ -4,7 +4,10 @@ extension module ``_fastcall.so`` (csrc/py) with the host compiler.
 Each translation unit compiles in parallel into ``_build/``; the objects are
 linked into ``hybrid_linear_attention_packed_gb300/libspanla.so`` against the
 shared CUDA runtime (the one PyTorch also loads).  Rebuilds only when a source
-or header is newer than the library.
+or header is newer than the library.  The extension module is optional (the
+binding makes its calls by ctypes without it): where it cannot be compiled, a
+warning says so and the library is built all the same.  It is rebuilt for
+another PyTorch or Python, too.
 """
 from __future__ import annotations
 
@@ -14,6 +17,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,24 +49,47 @@ def _headers():
             + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
+def _newer(product: str, sources) -> bool:
+    if not os.path.exists(product):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return any(os.path.getmtime(p) > t for p in _sources() + _headers() + [EXT_SRC, __file__])
+    t = os.path.getmtime(product)
+    return any(os.path.getmtime(p) > t for p in sources)
+
+
+def _stale() -> bool:
+    return _newer(LIB, _sources() + _headers() + [__file__])
+
+
+def _ext_abi() -> str:
+    """What the extension module is compiled against: torch and the interpreter."""
+    import torch
+    return "%s %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
+def _ext_stamp() -> str:
+    return os.path.join(BUILD, os.path.basename(EXT) + ".abi")
+
+
+def _ext_stale() -> bool:
+    if _newer(EXT, [EXT_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return True
+    try:
+        with open(_ext_stamp()) as f:
+            return f.read() != _ext_abi()
+    except (OSError, ImportError):
+        return True
 
 
 def _compile_ext() -> str:
     """The binding's extension module, against the headers of the torch that is installed."""
-    import sysconfig
-
     import torch
     tdir = os.path.dirname(torch.__file__)
     cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = EXT + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
            "-I", os.path.join(tdir, "include"), "-I", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda_home, "include"), EXT_SRC, "-o", tmp,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda_home, "include"),
+           "-DSPANLA_TORCH_VERSION=\"%s\"" % torch.__version__, EXT_SRC, "-o", tmp,
            "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -69,17 +97,32 @@ def _compile_ext() -> str:
     return tmp
 
 
+def _install_ext(pending) -> None:
+    """Put the compiled module in its place, or warn that there is none (an older one could hold structures of
+    another header: it goes)."""
+    try:
+        tmp = pending.result()
+    except Exception as e:   # noqa: BLE001 (no compiler, no headers, ...)
+        if os.path.exists(EXT):
+            os.remove(EXT)
+        warnings.warn("the extension module was not built, its calls go by ctypes: %s" % e)
+        return
+    os.replace(tmp, EXT)
+    with open(_ext_stamp(), "w") as f:
+        f.write(_ext_abi())
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link the library; returns its path."""
-    if not force and not _stale():
+    """Compile and link the library and the extension module where stale; returns the library's path."""
+    stale, ext_stale = force or _stale(), force or _ext_stale()
+    if not stale and not ext_stale:
         return LIB
-    nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
     def compile_one(src: str):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc] + ARCH + COMMON + extra + ["-c", src, "-o", obj]
+        cmd = [_nvcc()] + ARCH + COMMON + extra + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
@@ -88,17 +131,18 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        ext = ex.submit(_compile_ext)
-        objs = list(ex.map(compile_one, _sources()))
-        ext_tmp = ext.result()
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [
-        "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB)
-    os.replace(ext_tmp, EXT)
+        ext = ex.submit(_compile_ext) if ext_stale else None
+        if stale:
+            objs = list(ex.map(compile_one, _sources()))
+            tmp = LIB + ".tmp.%d" % os.getpid()
+            cmd = [_nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [
+                "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
+            os.replace(tmp, LIB)
+        if ext is not None:
+            _install_ext(ext)
     return LIB
 
 

@@ -168,6 +168,8 @@ def _bind_fast(lib) -> None:
         from . import _fastcall
     except ImportError:   # not built: the same calls by way of ctypes
         return
+    if getattr(_fastcall, "torch_version", None) != str(torch.__version__):   # built for another one
+        return
     _fastcall.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                      for f in (lib.span_la_decay_pass, lib.span_la_decay_branches_from_state, lib.span_la_decay_step,
                                lib.span_la_qk_norm_rope)])
