@@ -56,11 +56,16 @@ def test_out_of_memory_has_its_own_type(cuda_device, name, fast, monkeypatch):
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     torch.cuda.set_per_process_memory_fraction(1e-6, cuda_device)
+    held = []
     try:
+        with pytest.raises(torch.OutOfMemoryError):      # (what earlier tests left free in the allocator's blocks)
+            while True:
+                held.append(torch.empty(40_000, 16, 64, dtype=torch.bfloat16, device=cuda_device))
         with pytest.raises(torch.OutOfMemoryError):
             call()
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0, cuda_device)
+        held.clear()
     call()
     span_la_check()
 
