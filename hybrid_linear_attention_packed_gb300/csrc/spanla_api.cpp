@@ -1965,20 +1965,20 @@ struct Rows {
 };
 
 // True when no element of `a` is one of `b`: apart in memory, or different
-// columns of rows of the same stride.
+// columns of rows of the same stride (a single row has any stride).
 bool apart(const Rows& a, const Rows& b) {
   if (a.width == 0 || b.width == 0 || a.end() <= b.at || b.end() <= a.at) return true;
-  if (a.stride != b.stride) return false;
-  const int64_t s = a.stride;
+  if (a.stride != b.stride && a.rows > 1 && b.rows > 1) return false;
+  const int64_t s = a.rows > 1 ? a.stride : b.stride;
   const int64_t d = static_cast<int64_t>(b.at >= a.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s);
   return d >= a.width && d + b.width <= s;
 }
 
-// What a decayed call writes overlaps nothing else of it: out none of q, k and
-// v, and `num_states` states at `states` neither those (when they are
-// written) nor out.
-span_la_status check_out(const void* q, const void* k, const void* v, const void* out, const span_la_dims& dims,
-                         const char* name, const float* states, int64_t num_states, bool states_written) {
+// What a decayed call writes overlaps nothing else of it: out none of q, k, v
+// and log_decay (or NULL), and `num_states` states at `states` neither those (when
+// they are written) nor out.
+span_la_status check_out(const void* q, const void* k, const void* v, const void* out, const float* log_decay,
+                         const span_la_dims& dims, const char* name, const float* states, int64_t num_states, bool states_written) {
   const int64_t width = static_cast<int64_t>(dims.num_heads) * kHeadDim * (dims.dtype == SPAN_LA_BF16 ? 2 : 4);
   auto rows = [&](const void* x) { return Rows{reinterpret_cast<uintptr_t>(x), width, width, dims.total_rows}; };
   const int64_t state_width = num_states > 0 ? static_cast<int64_t>(dims.num_heads) * kStateFloats * sizeof(float) : 0;
@@ -1989,6 +1989,10 @@ span_la_status check_out(const void* q, const void* k, const void* v, const void
   if (states_written)
     for (const void* x : {q, k, v})
       if (!apart(rows(x), s)) return fail(SPAN_LA_ERR_INVALID, "%s overlaps q, k or v", name);
+  const int64_t decays = log_decay != nullptr ? dims.num_heads * static_cast<int64_t>(sizeof(float)) : 0;
+  const Rows ld{reinterpret_cast<uintptr_t>(log_decay), decays, decays, 1};
+  if (!apart(rows(out), ld)) return fail(SPAN_LA_ERR_INVALID, "out overlaps log_decay");
+  if (states_written && !apart(s, ld)) return fail(SPAN_LA_ERR_INVALID, "%s overlaps log_decay", name);
   return SPAN_LA_OK;
 }
 
@@ -2466,7 +2470,7 @@ span_la_status span_la_decay_pass(const void* q, const void* k, const void* v, s
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     // (pieces of 16 rows at least, and 16 scan CTAs a segment)
     if ((st = check_grid(dims.total_rows / 16 + 16 * (static_cast<int64_t>(num_views) + num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
-    if (!segs.empty() && (st = check_out(q, k, v, out, dims, "view_state_out", view_state_out, num_views, true)) != SPAN_LA_OK) return st;
+    if (!segs.empty() && (st = check_out(q, k, v, out, log_decay, dims, "view_state_out", view_state_out, num_views, true)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2499,7 +2503,7 @@ span_la_status span_la_decay_branches_from_state(const float* cached_state, int3
     if (segs.empty()) return SPAN_LA_OK;
     if ((st = check_log_decay(log_decay)) != SPAN_LA_OK) return st;
     if ((st = check_grid(dims.total_rows / 16 + 16 * static_cast<int64_t>(num_branches), dims.num_heads)) != SPAN_LA_OK) return st;
-    if ((st = check_out(q, k, v, out, dims, "cached_state", cached_state, num_states, false)) != SPAN_LA_OK) return st;
+    if ((st = check_out(q, k, v, out, log_decay, dims, "cached_state", cached_state, num_states, false)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     int device = 0;
@@ -2551,7 +2555,7 @@ span_la_status span_la_decay_step(const void* q, const void* k, const void* v, s
       const auto twice = std::adjacent_find(seen.begin(), seen.end());
       if (twice != seen.end()) return fail(SPAN_LA_ERR_INVALID, "state_index has state %d twice", *twice);
     }
-    if ((st = check_out(q, k, v, out, dims, "states", states, num_states, true)) != SPAN_LA_OK) return st;
+    if ((st = check_out(q, k, v, out, log_decay, dims, "states", states, num_states, true)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     StepArgs a;
@@ -2626,6 +2630,17 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
     if (!apart(out[0], out[1])) return fail(SPAN_LA_ERR_INVALID, "q's out overlaps k's out");
     if (positions == nullptr || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
       return fail(SPAN_LA_ERR_INVALID, "positions must be a non-NULL 4-byte aligned pointer");
+    const int64_t pos_bytes = rows * static_cast<int64_t>(sizeof(int32_t)), wsz = weight_dtype == SPAN_LA_BF16 ? 2 : 4;
+    for (int i = 0; i < 2; ++i) {
+      const char* name = i == 0 ? "q" : "k";
+      if (!apart(out[i], {reinterpret_cast<uintptr_t>(positions), pos_bytes, pos_bytes, 1}))
+        return fail(SPAN_LA_ERR_INVALID, "%s's out overlaps positions", name);
+      for (const span_la_qk_side* x : sides) {
+        const int64_t bytes = x->weight == nullptr ? 0 : (x->weight_per_head ? x->num_heads : 1) * kHeadDim * wsz;
+        if (!apart(out[i], {reinterpret_cast<uintptr_t>(x->weight), bytes, bytes, 1}))
+          return fail(SPAN_LA_ERR_INVALID, "%s's out overlaps a weight", name);
+      }
+    }
     DeviceState* dev = nullptr;
     span_la_status st = device_state(&dev);
     if (st != SPAN_LA_OK) return st;

@@ -468,8 +468,8 @@ span_la_status span_la_softmax_branches_from_kv(const void *view_k, const void *
  *   log_decay        device fp32 [H]: the natural logarithm of each head's
  *                    decay, normally <= 0 (at most 2); -infinity is a decay
  *                    of 0 (o_t sees row t only).  Read when the stream reaches the call
- *   out              must not overlap q, k or v
- *   view_state_out   must not overlap q, k, v or out
+ *   out              must not overlap q, k, v or log_decay
+ *   view_state_out   must not overlap q, k, v, log_decay or out
  *   other arguments  as for span_la_pass
  *   plan             kept in the plan cache with, up to 64 MB, the call's
  *                    workspace (calls of one plan on several streams then run
@@ -516,7 +516,7 @@ span_la_status span_la_decay_branches_from_state(const float *cached_state, int3
  *   log_decay        as for span_la_decay_pass, or NULL: no decay (the next
  *                    token of span_la_pass)
  *   states           device fp32 [num_states][H][64][64], updated in place;
- *                    apart from q, k, v and out
+ *                    apart from q, k, v, log_decay and out
  *   state_index      HOST int32 [n]: the state of each row, in [-1, num_states);
  *                    a row of -1 (padding) is skipped, its out left as it was;
  *                    no state may be named twice.  NULL: row t uses state t
@@ -559,7 +559,8 @@ typedef struct {
  *   rotary_dim       0 (norm only), 16, 32, 48 or 64
  *   positions        device int32 [rows]; a row whose position is negative is
  *                    neither read nor written
- * The outputs must not overlap each other or the other side's input.  With
+ * The outputs must not overlap each other, the other side's input, the weights or
+ * the positions.  With
  * eps = 0 a head of zeros gives NaN, as the formula does.
  */
 span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_t rows,
