@@ -188,7 +188,10 @@ def _i32(a) -> np.ndarray:
         return a
     if isinstance(a, torch.Tensor):
         a = a.detach().cpu().numpy()
-    return np.ascontiguousarray(np.asarray(a, dtype=np.int64).reshape(-1).astype(np.int32))
+    a = np.asarray(a)
+    if a.size and not (a.min() >= -2 ** 31 and a.max() < 2 ** 31):
+        raise ValueError("offsets and indices must fit 32 bits")
+    return np.ascontiguousarray(a.reshape(-1).astype(np.int32))
 
 
 def _iptr(a: np.ndarray):
@@ -559,7 +562,7 @@ def packed_positions(view_cu_seqlens: Sequence[int], branch_cu_seqlens: Optional
     if par.size != B or (B and not (0 <= par.min() and par.max() < V)):
         raise ValueError("one parent per branch, in [0, %d)" % V)
     for cu in (vcu, bcu):
-        if cu.size and (cu[0] < 0 or cu[-1] > total_rows or (np.diff(cu) < 0).any()):
+        if cu.size and (cu[0] < 0 or cu[-1] > total_rows or (cu[1:] < cu[:-1]).any()):
             raise ValueError("row offsets must be non-decreasing in [0, total_rows]")
     pos = np.full(int(total_rows), -1, dtype=np.int32)
     for s in range(V):

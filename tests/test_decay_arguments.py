@@ -1,6 +1,6 @@
 """Arguments of the decayed calls and the q/k norm and rotation that have to be
 refused on the host (CPU): outputs over the small arrays that a kernel reads
-while it writes them."""
+while it writes them, and offsets that do not fit 32 bits."""
 import numpy as np
 import pytest
 
@@ -60,3 +60,25 @@ def test_norm_rope_refuses_outputs_over_what_it_reads(lib, weight, pos, what):
     f = np.ones(32)
     st = lib.span_la_qk_norm_rope(q, k, 10, 0, 0, 1e-6, f.ctypes.data, 64, 0, int(pos), None)
     assert what in _detail(lib, st)
+
+
+@pytest.mark.parametrize("bad", [[0, 2 ** 32], [0, 2 ** 31], [-2 ** 31 - 1, 4], np.array([0, 2 ** 32 + 4]),
+                                 np.array([0, 2 ** 64 - 1], dtype=np.uint64), [0, 2 ** 70]])
+def test_offsets_that_do_not_fit_32_bits_are_refused(lib, bad):
+    """(Cut to 32 bits, 2^32 would be 0 and 2^32 + 4 would be 4.)"""
+    with pytest.raises(ValueError, match="32 bits"):
+        spanla.packed_positions(bad, None, None, 8)
+    with pytest.raises(ValueError, match="32 bits"):
+        spanla.plan_stats(bad, None, None, 1)
+
+
+def test_offsets_that_fit_are_taken_as_before(lib):
+    for cu in ([0, 4], np.array([0, 4], dtype=np.uint8), (0, 4), np.array([[0], [4]]), np.array([0.0, 4.0])):
+        assert spanla.packed_positions(cu, None, None, 5).tolist() == [0, 1, 2, 3, -1]
+    assert spanla._i32([]).size == 0 and spanla._i32([-2 ** 31, 2 ** 31 - 1]).tolist() == [-2 ** 31, 2 ** 31 - 1]
+
+
+@pytest.mark.parametrize("cu", [[2 ** 31 - 1, -5], [3, 2 ** 31 - 1, -2 ** 31 + 1, 4]])
+def test_offsets_whose_differences_wrap_are_refused(cu):
+    with pytest.raises(ValueError, match="non-decreasing"):
+        spanla.packed_positions(cu, None, None, 8)
