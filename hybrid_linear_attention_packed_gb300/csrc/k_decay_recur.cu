@@ -57,6 +57,13 @@ __device__ __forceinline__ void get8(const float* p, float (&x)[8]) {
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
+// The same of a state in global memory, from L2: the launch before wrote it, and
+// this one may have started during it, so that it is not read-only data.
+__device__ __forceinline__ void get8_state(const float* p, float (&x)[8]) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p + kHeadDim / 2));
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -77,7 +84,7 @@ template <bool kOut>
 __global__ void __launch_bounds__(kThreads, kRecurUnitsPerSm)
 recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
              const RecurUnit* __restrict__ units, int H, const float* __restrict__ log_decay,
-             const float* __restrict__ stateA, float* __restrict__ ws, float* __restrict__ out) {
+             const float* stateA, float* ws, float* __restrict__ out) {
   __shared__ __align__(16) Smem<kOut> sm;
   griddep_launch_dependents();   // (the next launch waits for this one's end before it reads)
   const int h = blockIdx.x % H;
@@ -125,8 +132,8 @@ recur_kernel(const float* __restrict__ q, const float* __restrict__ k, const flo
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         float x[8], y[8];
-        get8(p + 2 * i * kHeadDim, x);
-        get8(p + (2 * i + 1) * kHeadDim, y);
+        get8_state(p + 2 * i * kHeadDim, x);
+        get8_state(p + (2 * i + 1) * kHeadDim, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) S[i][j] = fma_f32x2(f32x2(x[j], y[j]), f2, S[i][j]);
       }
