@@ -63,7 +63,7 @@ tile_output_kernel(const __grid_constant__ CUtensorMap tm_q0, const __grid_const
                    const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_k1,
                    const __grid_constant__ CUtensorMap tm_v0, const __grid_constant__ CUtensorMap tm_v1,
                    const TileDesc* __restrict__ tiles, const uint8_t* __restrict__ bounds,
-                   const float* __restrict__ stateA, const float* __restrict__ stateB,
+                   const float* stateA, const float* stateB,
                    void* __restrict__ out, int H, unsigned* __restrict__ err) {
   using L = TileSmem<SPLIT>;
   extern __shared__ uint8_t smem_raw[];
@@ -118,7 +118,9 @@ tile_output_kernel(const __grid_constant__ CUtensorMap tm_q0, const __grid_const
   }
 
   // Start state S0 = stateA[a] + stateB[b] -> bf16 high / low parts, stored
-  // MN-major ([d rows][64 e], 128-byte swizzle) as the B operand of Q S0.
+  // MN-major ([d rows][64 e], 128-byte swizzle) as the B operand of Q S0.  (Not
+  // read-only data: the scan that writes them may still run when this launch
+  // starts.)
   const bool has_state = (td.stateA >= 0) || (td.stateB >= 0);
   if (has_state) {
     const int d = tid >> 1;
@@ -132,7 +134,7 @@ tile_output_kernel(const __grid_constant__ CUtensorMap tm_q0, const __grid_const
           stateA + static_cast<int64_t>(td.stateA) * H * kStateFloats + row_off);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float4 x = a[c];
+        const float4 x = __ldca(a + c);
         s[4 * c] += x.x; s[4 * c + 1] += x.y; s[4 * c + 2] += x.z; s[4 * c + 3] += x.w;
       }
     }
@@ -141,7 +143,7 @@ tile_output_kernel(const __grid_constant__ CUtensorMap tm_q0, const __grid_const
           stateB + static_cast<int64_t>(td.stateB) * H * kStateFloats + row_off);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float4 x = b[c];
+        const float4 x = __ldca(b + c);
         s[4 * c] += x.x; s[4 * c + 1] += x.y; s[4 * c + 2] += x.z; s[4 * c + 3] += x.w;
       }
     }
