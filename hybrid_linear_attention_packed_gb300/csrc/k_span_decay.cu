@@ -416,6 +416,7 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int q = (sd.len - r) * 8 + lane; q < kTileRows * 8; q += 32)
             *reinterpret_cast<uint4*>(krow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
+          __syncwarp();   // (lane 0 issues the product)
         }
         ok = wait_or_flag(bar(L::kVReady + b), (u >> 1) & 1, err, kErrTimeoutMma);
         if (ok && u >= 2) ok = wait_or_flag(bar(L::kP1Free + b), ((u - 2) >> 1) & 1, err, kErrTimeoutMma);
@@ -603,8 +604,9 @@ span_decay_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         break;
       tc_fence_after_sync();
       // The output warps read it once O(i) is ready.  The slot's last reader,
-      // O(i-4), is behind: P(i) was issued after P V of tile i-2 completed, and
-      // that was issued after Q S of tile i-3, which waits for O(i-4).
+      // O(i-4), is behind: P(i) was issued after P V of tile i-2 completed, which
+      // was issued once O(i-4)'s accumulators had been read (kOFree), behind the
+      // read of the slot.
       if (half == 0) smem[L::kSeg + (i % kSegSlots) * kTileRows + row] = static_cast<uint8_t>(seg_start);
       const uint32_t colP = (b ? kColP1 : kColP0) + half * 64;
       // Two 32-column chunks in turn; chunk q's bf16 pairs go to columns
