@@ -969,7 +969,7 @@ cudaError_t upload_pinned(void* dst, const std::vector<uint8_t>& bytes, int devi
 // allocation uploaded on the calling stream; a call on another stream first
 // waits for that upload.  At most kCacheEntries blocks are kept per device.
 // Every call that reads a block records an event on its stream afterwards
-// (one event per stream, at most kMaxReaders streams per block), so that
+// (one event per stream, by its id, at most kMaxReaders streams per block), so that
 // evicting a block frees it in stream order behind its last reads, without
 // synchronising the host.  Calls made while their stream is being captured
 // into a graph bypass the cache.
@@ -985,8 +985,8 @@ struct CacheEntry {
   DescBlock desc;
   uint8_t* d_block = nullptr;
   cudaEvent_t uploaded = nullptr;
-  cudaStream_t upload_stream = nullptr;
-  std::vector<std::pair<cudaStream_t, cudaEvent_t>> readers;   // last read per stream
+  uint64_t upload_stream = 0;   // (stream_id)
+  std::vector<std::pair<uint64_t, cudaEvent_t>> readers;   // last read per stream
   unsigned passes = 0;          // decayed passes that counted in the kept workspace
   bool sync_on_evict = false;   // a read could not be recorded: synchronise before freeing
   uint64_t last_use = 0;
@@ -1015,13 +1015,14 @@ void give_cache_event(int device, cudaEvent_t ev) {
 // block.  A new stream beyond kMaxReaders takes over the oldest reader: it
 // first waits for that reader's event, so its own event covers both.
 cudaError_t note_reader(CacheEntry& en, cudaStream_t stream) {
+  const uint64_t id = stream_id(stream);
   for (auto& r : en.readers)
-    if (r.first == stream) return cudaEventRecord(r.second, stream);
+    if (r.first == id) return cudaEventRecord(r.second, stream);
   if (en.readers.size() >= kMaxReaders) {
     auto& oldest = en.readers.front();
     cudaError_t e = cudaStreamWaitEvent(stream, oldest.second, 0);
     if (e != cudaSuccess) return e;
-    oldest.first = stream;
+    oldest.first = id;
     e = cudaEventRecord(oldest.second, stream);
     std::rotate(en.readers.begin(), en.readers.begin() + 1, en.readers.end());
     return e;
@@ -1034,7 +1035,7 @@ cudaError_t note_reader(CacheEntry& en, cudaStream_t stream) {
     give_cache_event(en.device, ev);
     return e;
   }
-  en.readers.emplace_back(stream, ev);
+  en.readers.emplace_back(id, ev);
   return cudaSuccess;
 }
 
@@ -1046,9 +1047,10 @@ cudaError_t release_entry(CacheEntry& en, cudaStream_t stream) {
     e = cudaDeviceSynchronize();
   } else {
     // work already on `stream` is ordered before the free without a wait
-    if (en.upload_stream != stream) e = cudaStreamWaitEvent(stream, en.uploaded, 0);
+    const uint64_t id = stream_id(stream);
+    if (en.upload_stream != id) e = cudaStreamWaitEvent(stream, en.uploaded, 0);
     for (const auto& r : en.readers)
-      if (e == cudaSuccess && r.first != stream) e = cudaStreamWaitEvent(stream, r.second, 0);
+      if (e == cudaSuccess && r.first != id) e = cudaStreamWaitEvent(stream, r.second, 0);
   }
   if (e == cudaSuccess) e = cudaFreeAsync(en.d_block, stream);
   if (e != cudaSuccess) return e;
@@ -1108,7 +1110,7 @@ span_la_status cached_block(const std::vector<int32_t>& key, int device, cudaStr
                             CacheEntry** entry) {
   for (CacheEntry& en : g_cache) {
     if (en.device == device && en.key == key) {
-      if (en.upload_stream != stream) {
+      if (en.upload_stream != stream_id(stream)) {
         cudaError_t e = cudaStreamWaitEvent(stream, en.uploaded, 0);
         if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent(descriptor upload)");
       }
@@ -1159,7 +1161,7 @@ span_la_status cached_block(const std::vector<int32_t>& key, int device, cudaStr
     cudaFreeAsync(en.d_block, stream);
     return cuda_fail(e, "descriptor upload");
   }
-  en.upload_stream = stream;
+  en.upload_stream = stream_id(stream);
   en.last_use = ++g_cache_clock;
   g_cache.push_back(std::move(en));
   *desc = &g_cache.back().desc;
@@ -1767,8 +1769,9 @@ span_la_status run_decay(const std::vector<int32_t>& key, BuildDesc&& build_desc
   } else if (use_cache && desc->kept_ws >= at.bytes) {
     // The plan's workspace: behind the calls that used it, on whatever streams.
     ws = const_cast<uint8_t*>(block) + align256(desc->host.size());
+    const uint64_t id = stream_id(stream);
     for (const auto& r : entry->readers)
-      if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, r.second, 0);
+      if (e == cudaSuccess && r.first != id) e = cudaStreamWaitEvent(stream, r.second, 0);
     if (e == cudaSuccess && entry->sync_on_evict) e = cudaDeviceSynchronize();   // (a use that could not be recorded)
     if (e != cudaSuccess) return cuda_fail(e, "waiting for the plan's workspace");
   } else {

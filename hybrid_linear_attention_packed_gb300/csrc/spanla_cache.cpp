@@ -32,7 +32,7 @@
 
 struct span_la_view_cache {
   struct Reader {
-    cudaStream_t stream;
+    uint64_t stream;      // (spanla::stream_id)
     cudaEvent_t done;     // recorded after that stream's last branch call on the slot
   };
   int device = 0;
@@ -107,9 +107,10 @@ cudaError_t order_before_write(span_la_view_cache* c, int32_t slot, cudaStream_t
 
 // Record on `stream` that it has enqueued a read of `slot`.
 cudaError_t note_read(span_la_view_cache* c, int32_t slot, cudaStream_t stream) {
+  const uint64_t id = spanla::stream_id(stream);
   for (auto& r : c->readers[slot])
-    if (r.stream == stream) return cudaEventRecord(r.done, stream);
-  span_la_view_cache::Reader r{stream, nullptr};
+    if (r.stream == id) return cudaEventRecord(r.done, stream);
+  span_la_view_cache::Reader r{id, nullptr};
   cudaError_t e = new_event(c, &r.done);
   if (e == cudaSuccess) e = cudaEventRecord(r.done, stream);
   if (e == cudaSuccess) c->readers[slot].push_back(r);

@@ -255,6 +255,16 @@ cudaError_t launch_tile_output(bool split, const CUtensorMap* tm_q, const CUtens
                                const uint8_t* bounds, const float* stateA, const float* stateB,
                                void* out, int H, unsigned* err, cudaStream_t stream, bool pdl);
 
+// What a stream is, whatever its handle: a handle may come back for a new
+// stream once its own is destroyed (with work still on its way), and the
+// per-thread default stream has one handle for every thread's.  (A stream whose id
+// cannot be had is like no other.)
+inline uint64_t stream_id(cudaStream_t stream) {
+  static std::atomic<uint64_t> none{UINT64_MAX};
+  unsigned long long id = 0;
+  return cudaStreamGetId(stream, &id) == cudaSuccess ? id : none.fetch_sub(1, std::memory_order_relaxed);
+}
+
 // Decayed passes of bf16 inputs (k_span_decay.cu): the one-launch structure
 // of span_output, from a plan of the same kind.
 //

@@ -54,7 +54,8 @@
  *   behind the calls that read it.  The cached plans, their events and the
  *   pinned staging buffers belong to the device's primary context and live
  *   until the process exits: do not call the library on a device after a
- *   cudaDeviceReset of that device.
+ *   cudaDeviceReset of that device.  Calls on the per-thread default stream
+ *   (cudaStreamPerThread) are untested.
  * Graphs.  The pass, branch and softmax calls may be recorded while `stream`
  *   is being captured into a CUDA graph: the recorded work replays on the
  *   buffers of the recorded call (their current contents), with its own
