@@ -25,7 +25,7 @@
 // before it is multiplied.
 //
 // Bound by the fp32 pipe, not by memory (1 KB a row and head): 7,796 rows of 16
-// heads take 90 us (30 us the piece states, 13 the scan, 60 the outputs, their
+// heads take 91 us (30 us the piece states, 13 the scan, 60 the outputs, their
 // ends overlapped), the pipe 52 % busy with the 8 warps that the registers
 // of the states leave room for.  With 8 x 8 blocks, two warps a piece and 16 on an
 // SM, the loads and sums around the multiply-adds took a third more

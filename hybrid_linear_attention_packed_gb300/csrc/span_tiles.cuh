@@ -1,7 +1,8 @@
-// Device pieces that the span kernels (k_span_output.cu, k_span_decay.cu)
-// share: the parts of a tile record each role reads, state slices to global
-// memory and to the shared-memory S operand, and waits that flag their
-// timeouts.
+// Device pieces of the span kernels.  k_span_output.cu and k_span_decay.cu
+// share waits that flag their timeouts, inline segment starts, state slices to
+// global memory and to the shared-memory S operand, and the counter's load; the
+// parts of a WorkTile that each role reads are k_span_output.cu's
+// (k_span_decay.cu's DecayTile has its own).
 #pragma once
 
 #include "spanla_internal.h"
