@@ -1121,30 +1121,28 @@ span_la_status cached_block(const std::vector<int32_t>& key, int device, cudaStr
       return SPAN_LA_OK;
     }
   }
-  CacheEntry en;
-  en.device = device;
-  en.key = key;
-  en.desc = build();
-  // The least recently used block goes when there are as many as the cache
-  // holds, and of those with a workspace while theirs come to too much.
-  while (true) {
-    int on_device = 0;
-    size_t kept = en.desc.kept_ws;
-    size_t victim = g_cache.size(), kept_victim = g_cache.size();
-    for (size_t i = 0; i < g_cache.size(); ++i) {
-      if (g_cache[i].device != device) continue;
-      ++on_device;
-      if (victim == g_cache.size() || g_cache[i].last_use < g_cache[victim].last_use) victim = i;
-      if (g_cache[i].desc.kept_ws == 0) continue;
-      kept += g_cache[i].desc.kept_ws;
-      if (kept_victim == g_cache.size() || g_cache[i].last_use < g_cache[kept_victim].last_use) kept_victim = i;
-    }
-    if (kept > kKeptTotalBytes && kept_victim < g_cache.size()) victim = kept_victim;
-    else if (on_device < kCacheEntries) break;
+  int on_device = 0;
+  size_t victim = g_cache.size();
+  for (size_t i = 0; i < g_cache.size(); ++i) {
+    if (g_cache[i].device != device) continue;
+    ++on_device;
+    if (victim == g_cache.size() || g_cache[i].last_use < g_cache[victim].last_use) victim = i;
+  }
+  if (on_device >= kCacheEntries) {
     cudaError_t e = release_entry(g_cache[victim], stream);
     if (e != cudaSuccess) return cuda_fail(e, "plan cache eviction");
     g_cache.erase(g_cache.begin() + victim);
   }
+  CacheEntry en;
+  en.device = device;
+  en.key = key;
+  en.desc = build();
+  // Past the bound a plan goes without a workspace of its own: its calls then
+  // allocate one each, which costs them less than the loss of another plan.
+  size_t kept = en.desc.kept_ws;
+  for (const CacheEntry& other : g_cache)
+    if (other.device == device) kept += other.desc.kept_ws;
+  if (kept > kKeptTotalBytes) en.desc.kept_ws = 0;
   const size_t bytes = std::max<size_t>(align256(en.desc.host.size()) + en.desc.kept_ws, 256);
   if (injected_alloc_failure())
     return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(descriptors, %zu): injected failure", bytes);

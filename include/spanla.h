@@ -474,10 +474,9 @@ span_la_status span_la_softmax_branches_from_kv(const void *view_k, const void *
  *   other arguments  as for span_la_pass
  *   plan             kept in the plan cache with, up to 64 MB, the call's
  *                    workspace (calls of one plan on several streams then run
- *                    one after the other); at most 256 MB of workspaces on a
- *                    device, those of the least recently used plans released
- *                    with their plans; span_la_plan_prepare does not prepare
- *                    it
+ *                    one after the other), and 256 MB of workspaces on a
+ *                    device in all, past which a plan's calls allocate theirs;
+ *                    span_la_plan_prepare does not prepare it
  * With fp32 inputs every product and sum is fp32; the output's states are held
  * times up to e^24 inside, so their elements have to stay below 1e28.  With bf16 inputs the
  * factors a^n are applied in fp32 and the state is kept to fp32 accuracy; the
