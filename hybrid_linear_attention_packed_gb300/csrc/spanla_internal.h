@@ -258,7 +258,8 @@ cudaError_t launch_tile_output(bool split, const CUtensorMap* tm_q, const CUtens
 // What a stream is, whatever its handle: a handle may come back for a new
 // stream once its own is destroyed (with work still on its way), and the
 // per-thread default stream has one handle for every thread's.  (A stream whose id
-// cannot be had is like no other.)
+// cannot be had is like no other.  Not for a stream that is being captured: the
+// question would end its capture.)
 inline uint64_t stream_id(cudaStream_t stream) {
   static std::atomic<uint64_t> none{UINT64_MAX};
   unsigned long long id = 0;
