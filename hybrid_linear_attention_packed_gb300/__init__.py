@@ -9,6 +9,7 @@ and :mod:`.workloads` the seeded synthetic inputs.
 from .spanla import (  # noqa: F401
     SpanLAError,
     ViewStateCache,
+    kv_pages,
     load_library,
     packed_positions,
     rope_inv_freq,
@@ -17,10 +18,13 @@ from .spanla import (  # noqa: F401
     span_la_decay_branches_from_state,
     span_la_decay_pass,
     span_la_decay_step,
+    span_la_kv_read,
+    span_la_kv_write,
     span_la_pass,
     span_la_pass_noalloc,
     span_la_plan_prepare,
     span_la_qk_norm_rope,
     span_la_softmax_branches_from_kv,
+    span_la_softmax_paged,
     span_la_softmax_pass,
 )

@@ -1,0 +1,194 @@
+// Packed rows of keys and values into the paged cache, quantised on the way,
+// and back.  Both are bound by memory.
+//
+// A row and head of e4m3 pages is held as y = x / 2^e rounded to e4m3 with the
+// least e >= -126 at which its largest finite magnitude is at most 448 2^e.  (A
+// floating-point grid is as fine at any scale, so a power of two loses nothing
+// to the exact quotient, and y 2^e is a bf16 number: reading back rounds
+// nothing.)  e is at most 119: beyond 448 2^119 = 1.75 2^127 magnitudes come out as
+// that, as the next value of the grid is not an fp32 number.  Infinite and NaN
+// elements are held as NaN.
+//
+// A CTA of 8 warps takes 32 packed rows; each warp one head of K or V of them at
+// a time, 8 lanes a row (16 bytes of bf16 a lane), 4 rows at once, all 32 in
+// flight.  Consecutive rows of one head are neighbours in a page, and the 32
+// powers of two go out as one store.
+#include "paged.cuh"
+
+namespace spanla {
+namespace {
+
+constexpr int kRows = 32, kWarps = 8, kSteps = kRows / 4;
+
+struct Places {            // of a CTA's rows: element offset of head 0 in the pages (-1: none), byte offset in the scales
+  int64_t at[kRows], scale_at[kRows];
+};
+
+__device__ __forceinline__ void find_places(const KvArgs& a, Places& pl) {
+  if (threadIdx.x < kRows) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x;
+    int64_t at = -1, scale_at = 0;
+    const int s = t < a.rows ? seq_of_row(a, t) : -1;
+    if (s >= 0) {
+      bool bad = false;
+      const SeqRows r = seq_rows(a, s, &bad);
+      const int64_t pos = r.len - (r.n - (t - r.row0));   // (negative: the sequence is shorter than its packed rows)
+      if (t >= r.row0 && t - r.row0 < r.n && pos >= 0) {
+        const int32_t page = page_of(a, s, static_cast<int32_t>(pos));
+        if (page < 0) {
+          atomicOr(a.err, kErrPage);
+        } else {
+          const int32_t in = static_cast<int32_t>(pos) & (a.page_rows - 1);
+          at = page * a.page_stride + in * a.row_stride;
+          scale_at = page * a.scale_page_stride + in;
+        }
+      }
+    }
+    pl.at[threadIdx.x] = at;
+    pl.scale_at[threadIdx.x] = scale_at;
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_sequences(a);
+  __syncthreads();
+}
+
+// 8 elements.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// Blocks (row block, heads of K and V by 8): the units u = blockIdx.y * 8 + warp are K of head u / 2 (u even) or V.
+template <typename T, bool kE4m3>
+__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows in) {
+  __shared__ Places pl;
+  find_places(a, pl);
+  const int lane = threadIdx.x & 31, unit = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  if (unit >= 2 * a.heads) return;
+  const int head = unit >> 1, sub = lane & 7;
+  const bool is_v = unit & 1;
+  const T* src = static_cast<const T*>(is_v ? in.v : in.k) + head * kHeadDim + sub * 8;
+  const int64_t stride = is_v ? in.v_row_stride : in.k_row_stride;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  float x[kSteps][8];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (pl.at[r] >= 0) load8(src + (t0 + r) * stride, x[i]);
+  }
+  uint32_t code = 0;   // row `lane`'s power of two
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    const int64_t at = pl.at[r] + head * a.head_stride + sub * 8;
+    if (kE4m3) {
+      uint32_t top = 0;   // magnitudes as bits order like numbers
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (finite(x[i][c])) top = max(top, __float_as_uint(x[i][c]) & 0x7fffffffu);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      // top = m 2^E, 1 <= m < 2: at most 448 2^e = 1.75 2^(8 + e) from e = E - 8 on, or E - 7 where m > 1.75.
+      const int e = min(119, max(-126, static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0)));
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const uint32_t mine = __shfl_sync(0xffffffffu, static_cast<uint32_t>(e + 127), (lane & 3) * 8);
+      if ((lane >> 2) == i) code = mine;
+      if (pl.at[r] >= 0) {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float y0 = finite(x[i][2 * c]) ? x[i][2 * c] * inv : NAN;
+          const float y1 = finite(x[i][2 * c + 1]) ? x[i][2 * c + 1] * inv : NAN;
+          w[c] = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v : a.k) + at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      }
+    } else if (pl.at[r] >= 0) {
+      store8(static_cast<__nv_bfloat16*>(is_v ? a.v : a.k) + at, x[i]);
+    }
+  }
+  if (kE4m3 && pl.at[lane] >= 0)
+    (is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride] = static_cast<uint8_t>(code);
+}
+
+template <typename T, bool kE4m3>
+__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows to) {
+  __shared__ Places pl;
+  find_places(a, pl);
+  const int lane = threadIdx.x & 31, unit = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  if (unit >= 2 * a.heads) return;
+  const int head = unit >> 1, sub = lane & 7;
+  const bool is_v = unit & 1;
+  T* dst = static_cast<T*>(is_v ? to.v : to.k) + head * kHeadDim + sub * 8;
+  const int64_t stride = is_v ? to.v_row_stride : to.k_row_stride;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  float x[kSteps][8];
+  if (kE4m3) {
+    uint2 raw[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (pl.at[r] >= 0)
+        raw[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8));
+    }
+    const float scale =
+        pl.at[lane] >= 0 ? scale_of((is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const float e = __shfl_sync(0xffffffffu, scale, 4 * i + (lane >> 3));
+      const uint32_t w[2] = {raw[i].x, raw[i].y};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 y = from_e4m3x2((w[c >> 1] >> (16 * (c & 1))) & 0xffffu);
+        x[i][2 * c] = y.x * e, x[i][2 * c + 1] = y.y * e;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (pl.at[r] >= 0) load8(static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8, x[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (pl.at[r] >= 0) store8(dst + (t0 + r) * stride, x[i]);
+  }
+}
+
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((a.rows + kRows - 1) / kRows), (2 * a.heads + kWarps - 1) / kWarps);
+  kernel<<<grid, kWarps * 32, 0, stream>>>(a, x);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream) {
+  if (f32) return launch(e4m3 ? kv_write_kernel<float, true> : kv_write_kernel<float, false>, a, x, stream);
+  return launch(e4m3 ? kv_write_kernel<__nv_bfloat16, true> : kv_write_kernel<__nv_bfloat16, false>, a, x, stream);
+}
+
+cudaError_t launch_kv_read(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream) {
+  if (f32) return launch(e4m3 ? kv_read_kernel<float, true> : kv_read_kernel<float, false>, a, x, stream);
+  return launch(e4m3 ? kv_read_kernel<__nv_bfloat16, true> : kv_read_kernel<__nv_bfloat16, false>, a, x, stream);
+}
+
+}  // namespace spanla

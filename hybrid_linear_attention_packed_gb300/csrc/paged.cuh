@@ -1,0 +1,124 @@
+// The paged cache of keys and values on the device: where a sequence's rows
+// stand, and e4m3 rows with a power of two each.
+//
+// Page tables, lengths and row offsets are device memory that a host check
+// cannot see, so each kernel checks what it reads of them: a sequence whose
+// offsets or length are out of range is skipped, a page out of range is not
+// touched, and either sets a bit of the device error word (span_la_check).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "spanla_internal.h"
+#include "tc_ptx.cuh"
+
+namespace spanla {
+
+// A sequence's part of a call: packed rows [row0, row0 + n), whose last one is
+// row len - 1 of the sequence.  n = 0 where there is nothing to do (or it is
+// out of range: then *bad is set).
+struct SeqRows {
+  int64_t row0;
+  int32_t n, len;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const KvArgs& a, int s, bool* bad) {
+  const int64_t b = a.row_cu != nullptr ? a.row_cu[s] : s;
+  const int64_t e = a.row_cu != nullptr ? a.row_cu[s + 1] : s + 1;
+  const int32_t len = a.seq_len[s];
+  const bool wrong = b < 0 || e < b || e > a.rows || e - b > a.max_rows || len < 0 || len > a.capacity;
+  if (wrong) *bad = true;
+  return {b, wrong ? 0 : static_cast<int32_t>(e - b), wrong ? 0 : len};
+}
+
+// The sequence whose rows hold packed row t, or -1.
+__device__ __forceinline__ int seq_of_row(const KvArgs& a, int64_t t) {
+  if (a.row_cu == nullptr) return t < a.seqs ? static_cast<int>(t) : -1;
+  int lo = 0, hi = a.seqs + 1;   // the first offset above t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.row_cu[mid] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo >= 1 && lo <= a.seqs ? lo - 1 : -1;
+}
+
+// The page of row `pos` (0 <= pos < len) of sequence s, or -1 (out of range).
+__device__ __forceinline__ int32_t page_of(const KvArgs& a, int s, int32_t pos) {
+  const int32_t p = a.table[s * a.table_stride + (pos >> a.page_shift)];
+  return p >= 0 && p < a.pages ? p : -1;
+}
+
+// Every sequence's offsets and length, by the threads of one CTA.
+__device__ __forceinline__ void check_sequences(const KvArgs& a) {
+  bool bad = false;
+  for (int s = threadIdx.x; s < a.seqs; s += blockDim.x) seq_rows(a, s, &bad);
+  if (bad) atomicOr(a.err, kErrSequence);
+}
+
+// 2^(code - 127); 255 is NaN.
+__device__ __forceinline__ float scale_of(uint32_t code) {
+  return __uint_as_float(code == 0 ? 0x00400000u : code == 255 ? 0x7fffffffu : code << 23);
+}
+
+// Two e4m3 values (the low byte first) as fp32; exact.
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// Row elements 2 * lane, 2 * lane + 1 of row `pos` of the cache, given its page.
+template <bool kE4m3>
+__device__ __forceinline__ float2 cached_pair(const KvArgs& a, const void* base, const uint8_t* scale, int32_t page, int32_t pos,
+                                              int head, int lane) {
+  const int32_t r = pos & (a.page_rows - 1);
+  const int64_t at = page * a.page_stride + head * a.head_stride + r * a.row_stride + 2 * lane;
+  if (kE4m3) {
+    const float2 x = from_e4m3x2(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(base) + at));
+    const float e = scale_of(scale[page * a.scale_page_stride + head * a.scale_head_stride + r]);
+    return make_float2(x.x * e, x.y * e);
+  }
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(static_cast<const __nv_bfloat16*>(base) + at));
+}
+
+// Softmax attention of one packed row t and query head by one warp, in fp32
+// throughout: the row of sequence s that sees its first `seen` rows.  The other
+// kernels send a row here whose products came out infinite or NaN: they multiply
+// rows that the row does not see by 0, this does not touch them.
+template <bool kE4m3>
+__device__ __noinline__ void attend_row(const KvArgs& a, const PagedAttn& p, int s, int64_t t, int head, int32_t seen) {
+  const int lane = threadIdx.x & 31, kvh = head / p.group;
+  const float2 q = __bfloat1622float2(
+      *reinterpret_cast<const __nv_bfloat162*>(p.q + t * p.q_row_stride + head * kHeadDim + 2 * lane));
+  float m = -INFINITY, l = 0.f;
+  float2 o = make_float2(0.f, 0.f);
+  bool bad = false;
+  for (int32_t j = 0; j < seen; ++j) {
+    const int32_t page = page_of(a, s, j);
+    if (page < 0) {
+      bad = true;
+      continue;
+    }
+    const float2 k = cached_pair<kE4m3>(a, a.k, a.k_scale, page, j, kvh, lane);
+    float x = q.x * k.x + q.y * k.y;
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    x *= p.scale;
+    if (x == -INFINITY) continue;   // weight 0
+    const float2 v = cached_pair<kE4m3>(a, a.v, a.v_scale, page, j, kvh, lane);
+    const float m_new = x > m || x != x ? x : m;
+    const float old = m == m_new ? 1.f : m == -INFINITY ? 0.f : expf(m - m_new), w = expf(x - m_new);
+    l = l * old + w;
+    o.x = (old == 0.f ? 0.f : o.x * old) + w * v.x;
+    o.y = (old == 0.f ? 0.f : o.y * old) + w * v.y;
+    m = m_new;
+  }
+  if (bad && lane == 0) atomicOr(a.err, kErrPage);
+  const bool none = l == 0.f;
+  const int64_t at = t * p.heads + head;
+  *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + 2 * lane) = none ? 0u : pack_bf16x2(o.x / l, o.y / l);
+  if (p.lse != nullptr && lane == 0) p.lse[at] = none ? -INFINITY : m + logf(l);
+}
+
+}  // namespace spanla

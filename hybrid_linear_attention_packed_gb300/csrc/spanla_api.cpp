@@ -140,12 +140,12 @@ span_la_status device_state(DeviceState** out) {
 constexpr int kKernelSplit = 0, kKernelChunk = 1, kKernelScan = 2, kKernelTile = 3,
               kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6, kKernelRecurState = 7,
               kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11,
-              kKernelSpanDecay = 12;
+              kKernelSpanDecay = 12, kKernelKvWrite = 13, kKernelKvRead = 14, kKernelPagedRows = 15;
 const char* const kKernelNames[SPAN_LA_NUM_KERNELS] = {"split_f32", "chunk_state", "segmented_scan",
                                                        "tile_output", "span_state", "span_output",
                                                        "softmax_attn", "recur_state", "recur_scan",
                                                        "recur_output", "decay_step", "qk_norm_rope",
-                                                       "span_decay"};
+                                                       "span_decay", "kv_write", "kv_read", "paged_rows"};
 
 std::atomic<int64_t> g_launches[SPAN_LA_NUM_KERNELS];
 std::atomic<bool> g_profiling{false};
@@ -1997,6 +1997,162 @@ span_la_status check_out(const void* q, const void* k, const void* v, const void
   return SPAN_LA_OK;
 }
 
+// ------------------------------------------------------------------ paged cache
+// The bytes that something of a call lies in.
+struct Bytes {
+  uintptr_t lo, hi;
+  const char* name;
+};
+
+Bytes bytes_at(const void* p, int64_t n, const char* name) {
+  return {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(p != nullptr ? n : 0), name};
+}
+
+// Refuses a call one of whose written ranges meets another range of it.
+span_la_status check_apart(const std::vector<Bytes>& written, const std::vector<Bytes>& read) {
+  auto meet = [](const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; };
+  for (size_t i = 0; i < written.size(); ++i) {
+    for (size_t j = i + 1; j < written.size(); ++j)
+      if (meet(written[i], written[j])) return fail(SPAN_LA_ERR_INVALID, "%s overlaps %s", written[i].name, written[j].name);
+    for (const Bytes& r : read)
+      if (meet(written[i], r)) return fail(SPAN_LA_ERR_INVALID, "%s overlaps %s", written[i].name, r.name);
+  }
+  return SPAN_LA_OK;
+}
+
+// One axis of a strided array.
+struct Axis {
+  int64_t stride, size;
+};
+
+// Rows of `width` along three axes: true where no two of them share an element.  (Axes are put in the order of
+// their strides; each then has to step over all that the ones before it span.)
+bool rows_apart(Axis (&axes)[3], int64_t width) {
+  std::sort(axes, axes + 3, [](const Axis& a, const Axis& b) { return a.size > 1 && (b.size <= 1 || a.stride < b.stride); });
+  int64_t span = width;
+  for (const Axis& a : axes) {
+    if (a.size <= 1) continue;
+    if (a.stride < span) return false;
+    span = (a.size - 1) * a.stride + span;
+  }
+  return true;
+}
+
+// True where a row of one such array meets a row of a second one with the same axes (sorted by rows_apart), d
+// elements behind.
+bool rows_meet(const Axis (&axes)[3], int64_t width, int64_t d, int level = 2) {
+  while (level >= 0 && axes[level].size <= 1) --level;
+  if (level < 0) return d > -width && d < width;
+  const Axis& a = axes[level];
+  const int64_t q = d / a.stride;
+  for (int64_t n = q - 1; n <= q + 1; ++n)
+    if (n > -a.size && n < a.size && rows_meet(axes, width, d - n * a.stride, level - 1)) return true;
+  return false;
+}
+
+// What every call on a paged cache checks of it, and its kernels' arguments; `written`: its pages are.
+span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t max_rows, bool written, KvArgs* a,
+                              std::vector<Bytes>* pages, std::vector<Bytes>* metadata) {
+  if (c == nullptr) return fail(SPAN_LA_ERR_INVALID, "cache is NULL");
+  if (c->dtype != SPAN_LA_BF16 && c->dtype != SPAN_LA_E4M3)
+    return fail(SPAN_LA_ERR_UNSUPPORTED, "cache dtype %d not supported", c->dtype);
+  if (c->page_rows < 16 || c->page_rows > 256 || (c->page_rows & (c->page_rows - 1)) != 0)
+    return fail(SPAN_LA_ERR_UNSUPPORTED, "page_rows %d is not 16, 32, 64, 128 or 256", c->page_rows);
+  if (c->num_heads < 1 || c->num_heads > 65535) return fail(SPAN_LA_ERR_INVALID, "num_heads %d not in [1, 65535]", c->num_heads);
+  if (c->num_pages < 1) return fail(SPAN_LA_ERR_INVALID, "num_pages %d < 1", c->num_pages);
+  if (rows < 0 || rows > INT32_MAX) return fail(SPAN_LA_ERR_INVALID, "rows %lld out of range", (long long)rows);
+  if (c->num_seqs < 0) return fail(SPAN_LA_ERR_INVALID, "num_seqs %d < 0", c->num_seqs);
+  if (c->row_cu == nullptr && rows != c->num_seqs)
+    return fail(SPAN_LA_ERR_INVALID, "%lld rows without row_cu need as many sequences, got %d", (long long)rows, c->num_seqs);
+  const bool e4m3 = c->dtype == SPAN_LA_E4M3;
+  const int64_t esz = e4m3 ? 1 : 2;
+  if (c->k == nullptr || c->v == nullptr || !aligned16(c->k) || !aligned16(c->v))
+    return fail(SPAN_LA_ERR_INVALID, "k and v pages must be non-NULL and 16-byte aligned");
+  constexpr int64_t kMost = int64_t(1) << 39;   // elements that an axis spans (the tensor maps' limit; no overflow below)
+  auto behind = [](const void* x, const void* y) {
+    return static_cast<int64_t>(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x));
+  };
+  Axis axes[3] = {{c->page_stride, c->num_pages}, {c->head_stride, c->num_heads}, {c->row_stride, c->page_rows}};
+  for (Axis& x : axes) {
+    if (x.size > 1 && (x.stride < kHeadDim || x.stride > kMost / x.size || (x.stride * esz) % 16 != 0))
+      return fail(SPAN_LA_ERR_INVALID, "page, head and row strides must be at least 64 elements and multiples of 16 bytes");
+  }
+  const int64_t extent = ((c->num_pages - 1) * (c->num_pages > 1 ? c->page_stride : 0) +
+                          (c->num_heads - 1) * (c->num_heads > 1 ? c->head_stride : 0) + (c->page_rows - 1) * c->row_stride + kHeadDim) * esz;
+  if (!rows_apart(axes, kHeadDim)) return fail(SPAN_LA_ERR_INVALID, "rows of the pages overlap with these strides");
+  int64_t scale_extent = 0;
+  if (e4m3) {
+    if (c->k_scale == nullptr || c->v_scale == nullptr || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+      return fail(SPAN_LA_ERR_INVALID, "E4M3 pages need k_scale and v_scale, 16-byte aligned");
+    Axis sc[3] = {{c->scale_page_stride, c->num_pages}, {c->scale_head_stride, c->num_heads}, {0, 1}};
+    for (const Axis& x : sc)
+      if (x.size > 1 && (x.stride < c->page_rows || x.stride > kMost / x.size || x.stride % 16 != 0))
+        return fail(SPAN_LA_ERR_INVALID, "scale strides must be at least page_rows and multiples of 16");
+    scale_extent = (c->num_pages - 1) * (c->num_pages > 1 ? c->scale_page_stride : 0) +
+                   (c->num_heads - 1) * (c->num_heads > 1 ? c->scale_head_stride : 0) + c->page_rows;
+    if (!rows_apart(sc, c->page_rows)) return fail(SPAN_LA_ERR_INVALID, "rows of the scales overlap with these strides");
+    if (written && rows_meet(sc, c->page_rows, behind(c->k_scale, c->v_scale)))
+      return fail(SPAN_LA_ERR_INVALID, "k_scale overlaps v_scale");
+  }
+  // (pages of K and V may be interleaved: what meets is looked for row by row)
+  if (written && rows_meet(axes, kHeadDim, behind(c->k, c->v) / esz))
+    return fail(SPAN_LA_ERR_INVALID, "k pages overlap v pages");
+  if (c->table_width < 0 || static_cast<int64_t>(c->table_width) * c->page_rows > INT32_MAX)
+    return fail(SPAN_LA_ERR_INVALID, "table_width %d pages of %d rows are too many", c->table_width, c->page_rows);
+  if (c->num_seqs > 0) {
+    auto word = [](const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (c->table_width > 0 && !word(c->page_table)) return fail(SPAN_LA_ERR_INVALID, "page_table must be non-NULL and 4-byte aligned");
+    if (c->num_seqs > 1 && c->table_stride < c->table_width)
+      return fail(SPAN_LA_ERR_INVALID, "table_stride %lld < table_width %d", (long long)c->table_stride, c->table_width);
+    if (!word(c->seq_len)) return fail(SPAN_LA_ERR_INVALID, "seq_len must be non-NULL and 4-byte aligned");
+    if (c->row_cu != nullptr && !word(c->row_cu)) return fail(SPAN_LA_ERR_INVALID, "row_cu must be 4-byte aligned");
+  }
+  const int64_t table_bytes = c->num_seqs > 0 ? ((c->num_seqs - 1) * (c->num_seqs > 1 ? c->table_stride : 0) + c->table_width) * 4 : 0;
+  *pages = {bytes_at(c->k, extent, "k pages"), bytes_at(c->v, extent, "v pages")};
+  if (e4m3) {
+    pages->push_back(bytes_at(c->k_scale, scale_extent, "k_scale"));
+    pages->push_back(bytes_at(c->v_scale, scale_extent, "v_scale"));
+  }
+  *metadata = {bytes_at(c->page_table, table_bytes, "page_table"), bytes_at(c->seq_len, c->num_seqs * int64_t(4), "seq_len"),
+               bytes_at(c->row_cu, (c->num_seqs + int64_t(1)) * 4, "row_cu")};
+  a->k = c->k;
+  a->v = c->v;
+  a->k_scale = c->k_scale;
+  a->v_scale = c->v_scale;
+  a->table = c->page_table;
+  a->seq_len = c->seq_len;
+  a->row_cu = c->row_cu;
+  a->page_stride = c->num_pages > 1 ? c->page_stride : kHeadDim;
+  a->head_stride = c->num_heads > 1 ? c->head_stride : kHeadDim;
+  a->row_stride = c->row_stride;
+  a->scale_page_stride = c->num_pages > 1 ? c->scale_page_stride : 0;
+  a->scale_head_stride = c->num_heads > 1 ? c->scale_head_stride : 0;
+  a->table_stride = c->table_stride;
+  a->capacity = static_cast<int64_t>(c->table_width) * c->page_rows;
+  a->rows = rows;
+  a->max_rows = max_rows;
+  a->pages = c->num_pages;
+  a->page_rows = c->page_rows;
+  a->page_shift = 0;
+  while ((1 << a->page_shift) < c->page_rows) ++a->page_shift;
+  a->heads = c->num_heads;
+  a->seqs = c->num_seqs;
+  return SPAN_LA_OK;
+}
+
+// Rows of `heads` heads of a packed array (q, k or v), `stride` elements apart.
+span_la_status check_rows(const char* name, const void* p, int64_t stride, int64_t rows, int64_t heads, int64_t esz) {
+  if (p == nullptr || !aligned16(p)) return fail(SPAN_LA_ERR_INVALID, "%s must be non-NULL and 16-byte aligned", name);
+  if (rows > 1 && (stride < heads * kHeadDim || stride > INT32_MAX || (stride * esz) % 16 != 0))
+    return fail(SPAN_LA_ERR_INVALID, "%s: the row stride must be at least num_heads * 64 elements, below 2^31, and a multiple "
+                "of 16 bytes", name);
+  return SPAN_LA_OK;
+}
+
+int64_t rows_bytes(int64_t stride, int64_t rows, int64_t heads, int64_t esz) {
+  return rows > 0 ? ((rows - 1) * stride + heads * kHeadDim) * esz : 0;
+}
+
 }  // namespace
 
 namespace spanla {
@@ -2205,6 +2361,11 @@ span_la_status span_la_check(cudaStream_t stream) {
       if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(clear no-allocation error word)");
     }
   }
+  constexpr unsigned kPaged = kErrSequence | kErrPage;
+  if ((word & kPaged) != 0 && (word & ~kPaged) == 0 && na_word == 0)
+    return fail(SPAN_LA_ERR_INVALID, "paged cache: %s%s%s out of range (error word 0x%x)",
+                word & kErrSequence ? "a sequence's row offsets or length" : "", word == kPaged ? ", and " : "",
+                word & kErrPage ? "a page" : "", word);
   if (word != 0 || na_word != 0)
     return fail(SPAN_LA_ERR_TIMEOUT, "a bounded device wait ran out (error word 0x%x, no-allocation path 0x%x)",
                 word, na_word);
@@ -2654,6 +2815,103 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
       return launch_qk_norm_rope(a, dtype == SPAN_LA_F32, interleaved != 0, stream);
     });
     return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "q/k norm and rotation launch");
+  });
+}
+
+span_la_status span_la_kv_write(const void* k, const void* v, int64_t k_row_stride, int64_t v_row_stride, int64_t rows,
+                                int32_t dtype, const span_la_kv_cache* cache, cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    if (dtype != SPAN_LA_BF16 && dtype != SPAN_LA_F32) return fail(SPAN_LA_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
+    KvArgs a{};
+    std::vector<Bytes> pages, metadata;
+    span_la_status st = check_kv_cache(cache, rows, rows, true, &a, &pages, &metadata);
+    if (st != SPAN_LA_OK) return st;
+    if (rows == 0 || a.seqs == 0) return SPAN_LA_OK;
+    const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4;
+    if ((st = check_rows("k", k, k_row_stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
+    if ((st = check_rows("v", v, v_row_stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
+    metadata.push_back(bytes_at(k, rows_bytes(k_row_stride, rows, a.heads, esz), "k"));
+    metadata.push_back(bytes_at(v, rows_bytes(v_row_stride, rows, a.heads, esz), "v"));
+    // (k and v pages, and their scales, may lie in between each other: check_kv_cache has looked)
+    for (const Bytes& x : pages)
+      if ((st = check_apart({x}, metadata)) != SPAN_LA_OK) return st;
+    if (pages.size() == 4)
+      for (int i = 0; i < 2; ++i)
+        if ((st = check_apart({pages[i]}, {pages[2], pages[3]})) != SPAN_LA_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
+    a.err = dev->err;
+    const KvRows x{const_cast<void*>(k), const_cast<void*>(v), k_row_stride, v_row_stride};
+    const cudaError_t e = counted_launch(kKernelKvWrite, stream, [&] {
+      return launch_kv_write(a, x, cache->dtype == SPAN_LA_E4M3, dtype == SPAN_LA_F32, stream);
+    });
+    return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "cache write launch");
+  });
+}
+
+span_la_status span_la_kv_read(const span_la_kv_cache* cache, int64_t rows, int32_t dtype, void* k_out, void* v_out,
+                               cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    if (dtype != SPAN_LA_BF16 && dtype != SPAN_LA_F32) return fail(SPAN_LA_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
+    KvArgs a{};
+    std::vector<Bytes> pages, metadata;
+    span_la_status st = check_kv_cache(cache, rows, rows, false, &a, &pages, &metadata);
+    if (st != SPAN_LA_OK) return st;
+    if (rows == 0 || a.seqs == 0) return SPAN_LA_OK;
+    const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4, stride = static_cast<int64_t>(a.heads) * kHeadDim;
+    if ((st = check_rows("k_out", k_out, stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
+    if ((st = check_rows("v_out", v_out, stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
+    metadata.insert(metadata.end(), pages.begin(), pages.end());
+    st = check_apart({bytes_at(k_out, rows * stride * esz, "k_out"), bytes_at(v_out, rows * stride * esz, "v_out")}, metadata);
+    if (st != SPAN_LA_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
+    a.err = dev->err;
+    const KvRows x{k_out, v_out, stride, stride};
+    const cudaError_t e = counted_launch(kKernelKvRead, stream, [&] {
+      return launch_kv_read(a, x, cache->dtype == SPAN_LA_E4M3, dtype == SPAN_LA_F32, stream);
+    });
+    return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "cache read launch");
+  });
+}
+
+span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_t rows, int32_t num_q_heads,
+                                     const span_la_kv_cache* cache, int32_t max_rows, float scale, void* out,
+                                     float* lse_out, cudaStream_t stream) {
+  return guarded([&]() -> span_la_status {
+    if (max_rows < 0) return fail(SPAN_LA_ERR_INVALID, "max_rows %d < 0", max_rows);
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(SPAN_LA_ERR_INVALID, "scale must be finite and >= 0");
+    KvArgs a{};
+    std::vector<Bytes> pages, metadata;
+    span_la_status st = check_kv_cache(cache, rows, max_rows == 0 ? rows : max_rows, false, &a, &pages, &metadata);
+    if (st != SPAN_LA_OK) return st;
+    if (num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % a.heads != 0 || num_q_heads / a.heads > 128)
+      return fail(SPAN_LA_ERR_INVALID, "num_q_heads %d is not a multiple of %d heads, at most 128 times it", num_q_heads, a.heads);
+    if (rows == 0 || a.seqs == 0) return SPAN_LA_OK;
+    const int64_t width = static_cast<int64_t>(num_q_heads) * kHeadDim;
+    if ((st = check_rows("q", q, q_row_stride, rows, num_q_heads, 2)) != SPAN_LA_OK) return st;
+    if ((st = check_rows("out", out, width, rows, num_q_heads, 2)) != SPAN_LA_OK) return st;
+    if (lse_out != nullptr && (reinterpret_cast<uintptr_t>(lse_out) & 3u) != 0)
+      return fail(SPAN_LA_ERR_INVALID, "lse_out must be 4-byte aligned");
+    metadata.insert(metadata.end(), pages.begin(), pages.end());
+    metadata.push_back(bytes_at(q, rows_bytes(q_row_stride, rows, num_q_heads, 2), "q"));
+    st = check_apart({bytes_at(out, rows * width * 2, "out"), bytes_at(lse_out, rows * num_q_heads * int64_t(4), "lse_out")}, metadata);
+    if (st != SPAN_LA_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
+    a.err = dev->err;
+    PagedAttn p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse_out;
+    p.q_row_stride = q_row_stride;
+    p.heads = num_q_heads;
+    p.group = num_q_heads / a.heads;
+    p.scale = scale == 0.f ? 0.125f : scale;
+    const cudaError_t e = counted_launch(kKernelPagedRows, stream, [&] {
+      return launch_paged_rows(a, p, cache->dtype == SPAN_LA_E4M3, stream);
+    });
+    return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "paged attention launch");
   });
 }
 

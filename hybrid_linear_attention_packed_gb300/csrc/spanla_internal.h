@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <vector>
 
@@ -397,6 +398,53 @@ struct RopeArgs {
   uint64_t freq[kHeadDim / 2];   // turns per position as a 64-bit binary fraction
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool f32, bool interleaved, cudaStream_t stream);
+
+// Device error word bits of the paged cache (tc_ptx.cuh has the others).
+constexpr unsigned kErrSequence = 8u;   // a sequence's offsets or length out of range
+constexpr unsigned kErrPage = 16u;      // a page out of range
+
+// The softmax layer's paged cache of keys and values: pages [pages][heads]
+// [page_rows][64] of bf16, or of e4m3 with a power of two (its exponent + 127)
+// for every row and head.  Row j of sequence s stands in page
+// table[s * table_stride + (j >> page_shift)].
+struct KvArgs {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const int32_t* table;
+  const int32_t* seq_len;
+  const int32_t* row_cu;      // NULL: sequence s has packed row s alone
+  int64_t page_stride, head_stride, row_stride;   // elements
+  int64_t scale_page_stride, scale_head_stride;   // bytes
+  int64_t table_stride;
+  int64_t capacity;           // rows that a row of the table has room for
+  int64_t rows;               // packed rows of the call
+  int64_t max_rows;           // most rows of a sequence
+  int32_t pages, page_rows, page_shift, heads, seqs;
+  unsigned* err;
+};
+
+// Packed rows into the cache, and back (k_kv_pages.cu).
+struct KvRows {
+  void* k;
+  void* v;
+  int64_t k_row_stride, v_row_stride;   // elements
+};
+cudaError_t launch_kv_write(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream);
+
+// Softmax attention of packed rows over the cache (k_paged_attn.cu).
+struct PagedAttn {
+  const __nv_bfloat16* q;     // rows of `heads` heads, q_row_stride elements apart
+  __nv_bfloat16* out;         // [rows][heads][64]
+  float* lse;                 // [rows][heads] or NULL
+  int64_t q_row_stride;
+  int32_t heads;              // query heads; head h reads key head h / group
+  int32_t group;
+  float scale;
+};
+cudaError_t launch_paged_rows(const KvArgs& a, const PagedAttn& p, bool e4m3, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
 

@@ -22,6 +22,7 @@ LIB_PATH = os.environ.get("SPANLA_LIB", os.path.join(_PKG, "libspanla.so"))
 
 SPAN_LA_BF16 = 0
 SPAN_LA_F32 = 1
+SPAN_LA_E4M3 = 2
 
 STATUS = {0: "SPAN_LA_OK", 1: "SPAN_LA_ERR_INVALID", 2: "SPAN_LA_ERR_UNSUPPORTED",
           3: "SPAN_LA_ERR_CUDA", 4: "SPAN_LA_ERR_NOMEM", 5: "SPAN_LA_ERR_TIMEOUT"}
@@ -36,8 +37,9 @@ EXPORTED = ("span_la_pass", "span_la_branches_from_state", "span_la_check",
             "span_la_fault_inject", "span_la_softmax_plan_stats",
             "span_la_selftest_wait_timeout_noalloc", "span_la_pass_variant",
             "span_la_plan_prepare", "span_la_decay_pass", "span_la_decay_branches_from_state",
-            "span_la_decay_step", "span_la_qk_norm_rope", "span_la_cache_decay_branches")
-NUM_KERNELS = 13
+            "span_la_decay_step", "span_la_qk_norm_rope", "span_la_cache_decay_branches",
+            "span_la_kv_write", "span_la_kv_read", "span_la_softmax_paged")
+NUM_KERNELS = 16
 
 
 class SpanLAError(RuntimeError):
@@ -55,6 +57,16 @@ class QkSide(ctypes.Structure):
     _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("in_row_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
                 ("num_heads", ctypes.c_int32), ("weight_per_head", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_rows", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("row_cu", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -140,6 +152,14 @@ def load_library(path: Optional[str] = None):
         lib.span_la_qk_norm_rope.argtypes = [QkSide, QkSide, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                              ctypes.c_float, vp, ctypes.c_int32, ctypes.c_int32, vp, vp]
         lib.span_la_qk_norm_rope.restype = ctypes.c_int
+        cachep = ctypes.POINTER(KvCache)
+        lib.span_la_kv_write.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, cachep, vp]
+        lib.span_la_kv_write.restype = ctypes.c_int
+        lib.span_la_kv_read.argtypes = [cachep, ctypes.c_int64, ctypes.c_int32, vp, vp, vp]
+        lib.span_la_kv_read.restype = ctypes.c_int
+        lib.span_la_softmax_paged.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, cachep, ctypes.c_int32,
+                                              ctypes.c_float, vp, vp, vp]
+        lib.span_la_softmax_paged.restype = ctypes.c_int
         lib.span_la_cache_create.argtypes = [ctypes.c_int32, ctypes.c_int32,
                                              ctypes.POINTER(ctypes.c_void_p)]
         lib.span_la_cache_create.restype = ctypes.c_int
@@ -672,6 +692,173 @@ def span_la_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tens
                                   _stream_handle(stream))
     _raise(lib, st, "span_la_qk_norm_rope")
     return q_out, k_out
+
+
+def kv_pages(num_pages: int, num_heads: int, page_rows: int, dtype: torch.dtype = torch.bfloat16, device=None):
+    """Zeroed pages of a paged cache: ``(k_pages, v_pages, k_scale, v_scale)``,
+    the pages [num_pages, num_heads, page_rows, 64] of ``dtype`` (bf16 or
+    float8_e4m3fn), the scales uint8 [num_pages, num_heads, page_rows] or None."""
+    if dtype not in _PAGE_DTYPES:
+        raise ValueError("page dtype %s not supported (bf16 or float8_e4m3fn)" % dtype)
+    dev = torch.device("cuda") if device is None else device
+    shape = (int(num_pages), int(num_heads), int(page_rows))
+    if dtype == torch.bfloat16:
+        return tuple(torch.zeros(shape + (64,), dtype=dtype, device=dev) for _ in range(2)) + (None, None)
+    pages = tuple(torch.zeros(shape + (64,), dtype=torch.uint8, device=dev).view(dtype) for _ in range(2))
+    return pages + tuple(torch.full(shape, 127, dtype=torch.uint8, device=dev) for _ in range(2))
+
+
+_PAGE_DTYPES = {torch.bfloat16: SPAN_LA_BF16, torch.float8_e4m3fn: SPAN_LA_E4M3}
+
+
+def _i32_on(dev: int, name: str, x: torch.Tensor, shape) -> int:
+    """The address of a contiguous int32 CUDA tensor of a shape."""
+    if x.dtype != torch.int32 or not x.is_cuda or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError("%s must be contiguous int32 CUDA [%s]" % (name, ", ".join(str(n) for n in shape)))
+    _on_device(dev, name, x)
+    return x.data_ptr()
+
+
+def _kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor,
+              row_cu: Optional[torch.Tensor], k_scale: Optional[torch.Tensor], v_scale: Optional[torch.Tensor]) -> Tuple[KvCache, int]:
+    """The C struct of a paged cache, and the current device."""
+    sh, st = k_pages.shape, k_pages.stride()
+    for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if x.dim() != 4 or x.shape[3] != 64 or not x.is_cuda:
+            raise ValueError("%s must be a CUDA tensor [num_pages, num_heads, page_rows, 64], got %s" % (name, tuple(x.shape)))
+        if x.stride(3) != 1:
+            raise ValueError("%s: the 64 elements of a row must lie next to each other" % name)
+    dev = _current_device()
+    _on_device(dev, "k_pages", k_pages)
+    _on_device(dev, "v_pages", v_pages)
+    if v_pages.shape != sh or v_pages.dtype != k_pages.dtype or v_pages.stride() != st:
+        raise ValueError("k_pages and v_pages must share shape, dtype and strides")
+    dt = _PAGE_DTYPES.get(k_pages.dtype)
+    if dt is None:
+        raise ValueError("page dtype %s not supported (bf16 or float8_e4m3fn)" % k_pages.dtype)
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_cuda or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 CUDA [num_seqs, width], the entries of a row next to each other")
+    _on_device(dev, "page_table", page_table)
+    S, width = page_table.shape
+    c = KvCache(k_pages.data_ptr(), v_pages.data_ptr(), None, None, st[0], st[1], st[2], 0, 0, sh[0], sh[2], sh[1], dt, S, width,
+                page_table.stride(0) if S > 1 else width, page_table.data_ptr(), _i32_on(dev, "seq_len", seq_len, (S,)),
+                None if row_cu is None else _i32_on(dev, "row_cu", row_cu, (S + 1,)))
+    if dt == SPAN_LA_E4M3:
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (x is None or x.dtype != torch.uint8 or not x.is_cuda or tuple(x.shape) != tuple(sh[:3])
+                    or x.stride(2) != 1 or x.stride() != k_scale.stride()):
+                raise ValueError("%s must be uint8 CUDA [num_pages, num_heads, page_rows], the bytes of a page and head next to "
+                                 "each other, k_scale and v_scale of the same strides" % name)
+            _on_device(dev, name, x)
+        c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        c.scale_page_stride, c.scale_head_stride = k_scale.stride(0), k_scale.stride(1)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("bf16 pages have no scales")
+    return c, dev
+
+
+def _packed(name: str, x: torch.Tensor, H: Optional[int], dev: int) -> int:
+    """x as rows [T, H, 64] on the device; returns its row stride."""
+    if x.dim() != 3 or x.shape[2] != 64 or not x.is_cuda or (H is not None and x.shape[1] != H):
+        raise ValueError("%s must be a CUDA tensor [T, %s, 64], got %s" % (name, "H" if H is None else H, tuple(x.shape)))
+    _on_device(dev, name, x)
+    return _row_stride(name, x, x.shape[0], x.shape[1])
+
+
+def span_la_kv_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                     seq_len: torch.Tensor, row_cu: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """New rows k, v [T, H, 64] (bf16 or fp32; parts of a fused projection's rows
+    will do) into their places in the paged cache (``span_la_kv_write``).
+
+    ``k_pages``, ``v_pages``: [num_pages, H, page_rows, 64] bf16, or float8_e4m3fn
+    with uint8 scales [num_pages, H, page_rows] (:func:`kv_pages`).  On the device,
+    int32: ``page_table`` [S, width], ``seq_len`` [S] (rows in the cache after the
+    call) and ``row_cu`` [S + 1]: packed rows row_cu[s] .. row_cu[s + 1] are the
+    last ones of sequence s (None: one row of each sequence)."""
+    lib = _lib or load_library()
+    c, dev = _kv_cache(k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale)
+    dt = _DTYPES.get(k.dtype)
+    if dt is None:
+        raise ValueError("dtype %s not supported (bf16 or fp32)" % k.dtype)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must share shape and dtype")
+    ks, vs = _packed("k", k, c.num_heads, dev), _packed("v", v, c.num_heads, dev)
+    _raise(lib, lib.span_la_kv_write(k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0], dt, c, _stream_handle(stream)),
+           "span_la_kv_write")
+
+
+def span_la_kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor,
+                    row_cu: Optional[torch.Tensor], total_rows: Optional[int] = None, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                    k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The packed rows out of the cache (``span_la_kv_read``; the cache as for
+    :func:`span_la_kv_write`): k and v [T, H, 64] of ``dtype`` (bf16 or fp32), T =
+    ``total_rows`` (default: the given outputs' rows, or one a sequence).  With a
+    kept view's length in row_cu and seq_len, they are the view_k and view_v of
+    :func:`span_la_softmax_branches_from_kv`."""
+    lib = _lib or load_library()
+    c, dev = _kv_cache(k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale)
+    if total_rows is None:
+        given = k_out if k_out is not None else v_out
+        if given is None and row_cu is not None:
+            raise ValueError("total_rows, or an output, says how many rows there are")
+        total_rows = c.num_seqs if given is None else given.shape[0]
+    outs = []
+    for name, x in (("k_out", k_out), ("v_out", v_out)):
+        if x is None:
+            x = torch.empty((int(total_rows), c.num_heads, 64), dtype=dtype, device=k_pages.device)
+        elif (tuple(x.shape) != (int(total_rows), c.num_heads, 64) or x.dtype != dtype or not x.is_cuda or not x.is_contiguous()):
+            raise ValueError("%s must be a contiguous CUDA tensor [%d, %d, 64] of %s" % (name, total_rows, c.num_heads, dtype))
+        else:
+            _on_device(dev, name, x)
+        outs.append(x)
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("dtype %s not supported (bf16 or fp32)" % dtype)
+    _raise(lib, lib.span_la_kv_read(c, int(total_rows), dt, outs[0].data_ptr(), outs[1].data_ptr(), _stream_handle(stream)),
+           "span_la_kv_read")
+    return outs[0], outs[1]
+
+
+def span_la_softmax_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                          seq_len: torch.Tensor, row_cu: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                          v_scale: Optional[torch.Tensor] = None, max_rows: Optional[int] = None, scale: float = 0.0,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Softmax attention of q [T, Hq, 64] (bf16; parts of a fused projection's
+    rows will do) over the paged cache (``span_la_softmax_paged``; the cache as for
+    :func:`span_la_kv_write`, which has written the rows' own keys and values
+    before): row i of a sequence sees the sequence's rows up to itself, query head
+    h the key head h // (Hq // H).  ``max_rows``: the most packed rows of a sequence
+    where it is known (1 without ``row_cu``).  ``lse`` (fp32 [T, Hq], optional)
+    receives the natural-log normaliser.  Returns [T, Hq, 64]."""
+    lib = _lib or load_library()
+    c, dev = _kv_cache(k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale)
+    qs = _packed("q", q, None, dev)
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bf16, got %s" % q.dtype)
+    T, H = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((T, H, 64), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out must be a contiguous CUDA tensor like q")
+    else:
+        _on_device(dev, "out", out)
+    if lse is not None:
+        if lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda or tuple(lse.shape) != (T, H):
+            raise ValueError("lse must be contiguous fp32 CUDA [T, H]")
+        _on_device(dev, "lse", lse)
+    if max_rows is None:
+        max_rows = 1 if row_cu is None else 0
+    elif max_rows < 1:
+        raise ValueError("max_rows must be at least 1")
+    _raise(lib, lib.span_la_softmax_paged(q.data_ptr(), qs, T, H, c, int(max_rows), float(scale), out.data_ptr(),
+                                          lse.data_ptr() if lse is not None else None, _stream_handle(stream)),
+           "span_la_softmax_paged")
+    return out
 
 
 def _keys(keys) -> np.ndarray:

@@ -89,7 +89,8 @@ extern "C" {
 
 typedef enum {
     SPAN_LA_BF16 = 0,
-    SPAN_LA_F32 = 1
+    SPAN_LA_F32 = 1,
+    SPAN_LA_E4M3 = 2    /* pages of a span_la_kv_cache only */
 } span_la_dtype;
 
 typedef enum {
@@ -259,7 +260,9 @@ span_la_status span_la_pass_noalloc(const void *q, const void *k, const void *v,
  * error words of the current device: the library's main word and, where
  * span_la_pass_noalloc has run on the device, that path's own word.  Returns
  * SPAN_LA_ERR_CUDA if the stream reports a CUDA error, SPAN_LA_ERR_TIMEOUT if
- * a kernel's bounded wait ran out, SPAN_LA_OK otherwise.  Allocates nothing.
+ * a kernel's bounded wait ran out, SPAN_LA_ERR_INVALID if a kernel found
+ * offsets, a length or a page of a paged cache (device memory) out of range,
+ * SPAN_LA_OK otherwise.  Allocates nothing.
  */
 span_la_status span_la_check(cudaStream_t stream);
 
@@ -373,14 +376,15 @@ span_la_status span_la_plan_stats(const int32_t *view_cu_seqlens, int32_t num_vi
  *   2 segmented_scan (both), 4 span_state, 5 span_output (bf16 inputs),
  *   6 softmax_attn (span_la_softmax_pass), 7 recur_state, 8 recur_scan,
  *   9 recur_output (decayed passes, fp32), 12 span_decay (bf16),
- *   10 decay_step, 11 qk_norm_rope.
+ *   10 decay_step, 11 qk_norm_rope, 13 kv_write, 14 kv_read, 15 paged_rows
+ *   (paged cache).
  * Launches of every kernel are always counted.  While profiling is enabled,
  * every launch is also bracketed by two CUDA events recorded on the call's
  * stream (one device only); span_la_profile_read() waits for the pending
  * events and adds their elapsed times up.  Enabling adds two event records per
  * launch and nothing else to the work on the stream.
  */
-#define SPAN_LA_NUM_KERNELS 13
+#define SPAN_LA_NUM_KERNELS 16
 
 /* Turn event timing on (non-zero) or off. */
 span_la_status span_la_profile_enable(int32_t enable);
@@ -568,6 +572,108 @@ span_la_status span_la_qk_norm_rope(span_la_qk_side q, span_la_qk_side k, int64_
                                     const double *inv_freq, int32_t rotary_dim,
                                     int32_t interleaved, const int32_t *positions,
                                     cudaStream_t stream);
+
+/*
+ * The softmax layer's paged cache of keys and values ("Serving 0.88M TPS from
+ * Two RTXs and Mac Minis", section "Long Requests": the softmax layers' K and V
+ * are the other half of what is kept of a view; section "Serving many users" of
+ * the third page: pages of a cache, chunks of prompts, single tokens).
+ *
+ * Pages [num_pages][num_heads][page_rows][64] of keys and as many of values;
+ * row j of sequence s is row j % page_rows of page page_table[s][j / page_rows].
+ * bf16 pages hold the values.  E4M3 pages hold y, rounded to nearest even, with
+ * one byte b for every row and head: the value is y 2^(b - 127), b the least of
+ * 1 .. 246 at which the row's largest finite magnitude is at most 448 2^(b - 127)
+ * (magnitudes past 448 2^119 = 1.75 2^127 come out as that; a byte of 255 stands
+ * for NaN); infinite and NaN elements are held as NaN.
+ *
+ * A call's packed rows row_cu[s] .. row_cu[s + 1] are the last ones of sequence
+ * s, which has seq_len[s] rows in the cache after them: packed row
+ * row_cu[s] + i is row seq_len[s] - (row_cu[s + 1] - row_cu[s]) + i of the
+ * sequence.  (So a step's span_la_kv_write and span_la_softmax_paged take the
+ * same metadata.)  Row i = -1 and before, where a sequence is shorter than its
+ * packed rows, does not exist: it is not written or read back, and sees nothing.
+ *
+ * The metadata is device memory, read when the stream reaches the call: a
+ * recorded call (CUDA graph) replays on its current contents.  The kernels check
+ * it: a sequence with offsets out of order or of [0, rows], more packed rows than
+ * max_rows, or a length outside [0, table_width * page_rows] is skipped, and so
+ * are the rows of a page outside [0, num_pages); span_la_check then reports
+ * SPAN_LA_ERR_INVALID.  Entries of page_table past a sequence's last row are not
+ * read.  Packed rows of no sequence are left as they were.
+ */
+typedef struct {
+    void *k;                    /* device, 16-byte aligned */
+    void *v;
+    uint8_t *k_scale;           /* E4M3: device [num_pages][num_heads][page_rows], 16-byte */
+    uint8_t *v_scale;           /* aligned, rows next to each other; else not looked at */
+    int64_t page_stride;        /* of k and v, in elements: multiples of 16 bytes, with which */
+    int64_t head_stride;        /* no two rows of 64 overlap, in any order (pages of K and V */
+    int64_t row_stride;         /* may be interleaved, heads be inside of rows) */
+    int64_t scale_page_stride;  /* of k_scale and v_scale, in bytes: multiples of 16 */
+    int64_t scale_head_stride;
+    int32_t num_pages;
+    int32_t page_rows;          /* 16, 32, 64, 128 or 256 */
+    int32_t num_heads;
+    int32_t dtype;              /* SPAN_LA_BF16 or SPAN_LA_E4M3 */
+    int32_t num_seqs;
+    int32_t table_width;        /* entries in a row of page_table */
+    int64_t table_stride;       /* from row to row of page_table, >= table_width */
+    const int32_t *page_table;  /* device [num_seqs][table_width] */
+    const int32_t *seq_len;     /* device [num_seqs] */
+    const int32_t *row_cu;      /* device [num_seqs + 1], or NULL: one row a sequence, packed row s of sequence s */
+} span_la_kv_cache;
+
+/*
+ * span_la_kv_write -- packed rows of keys and values into their places in the
+ * cache, quantised on the way where its pages are E4M3.
+ *   k, v             device [rows][num_heads][64], dtype (SPAN_LA_BF16 or
+ *                    SPAN_LA_F32), 16-byte aligned; rows k_row_stride and
+ *                    v_row_stride elements apart (multiples of 16 bytes: parts
+ *                    of a fused projection's rows)
+ *   cache            a row of a page that two packed rows name gets either's
+ *                    values; pages and scales overlap nothing else of the call
+ * fp32 rows into bf16 pages are rounded to nearest even.
+ */
+span_la_status span_la_kv_write(const void *k, const void *v, int64_t k_row_stride, int64_t v_row_stride,
+                                int64_t rows, int32_t dtype, const span_la_kv_cache *cache, cudaStream_t stream);
+
+/*
+ * span_la_kv_read -- the packed rows out of the cache: for a whole kept view
+ * row_cu holds the views' lengths summed up, and k_out and v_out are what
+ * span_la_softmax_branches_from_kv takes as view_k and view_v.
+ *   k_out, v_out     device [rows][num_heads][64], dtype (SPAN_LA_BF16 or
+ *                    SPAN_LA_F32), 16-byte aligned, contiguous
+ * Exact: both page types hold numbers of bf16 (below 2^-126 not all of e4m3's).
+ */
+span_la_status span_la_kv_read(const span_la_kv_cache *cache, int64_t rows, int32_t dtype, void *k_out, void *v_out,
+                               cudaStream_t stream);
+
+/*
+ * span_la_softmax_paged -- softmax attention of packed rows over the cache:
+ * for packed row t = row i of its sequence, and query head h with its key head
+ * g = h / (num_q_heads / num_heads),
+ *
+ *   o_t = sum_{j <= i} softmax_j(scale * q_t . k_j) v_j,   lse_t = ln sum_{j <= i} exp(scale * q_t . k_j).
+ *
+ * The next token of each sequence, some drafted tokens, chunks of prompts, or
+ * any mixture; keys and values of the packed rows themselves have been written
+ * before (span_la_kv_write).
+ *   q                device bf16 [rows][num_q_heads][64], 16-byte aligned, rows
+ *                    q_row_stride elements apart (a multiple of 16 bytes)
+ *   num_q_heads      a multiple of the cache's num_heads, at most 128 times it
+ *   max_rows         the most packed rows of a sequence, or 0: not known (a small
+ *                    one saves the launch for long chunks)
+ *   scale            > 0, or 0 for 1/sqrt(64)
+ *   out              device bf16 [rows][num_q_heads][64], 16-byte aligned
+ *   lse_out          device fp32 [rows][num_q_heads] or NULL
+ * A row that sees nothing (or nothing but scores of -infinity) gets o = 0 and
+ * lse = -infinity.  What a row does not see does not reach it, whatever it holds.
+ * Scores, sums and o are fp32; out is rounded to bf16.  Deterministic.
+ */
+span_la_status span_la_softmax_paged(const void *q, int64_t q_row_stride, int64_t rows, int32_t num_q_heads,
+                                     const span_la_kv_cache *cache, int32_t max_rows, float scale,
+                                     void *out, float *lse_out, cudaStream_t stream);
 
 /*
  * View-state cache ("Serving 0.88M TPS from Two RTXs and Mac Minis", section

@@ -1,0 +1,335 @@
+"""Softmax attention over the paged cache against the float64 form."""
+import numpy as np
+import pytest
+import torch
+
+from hybrid_linear_attention_packed_gb300 import (SpanLAError, kv_pages, packed_positions, rope_inv_freq, span_la_check,
+                                                  span_la_kv_read, span_la_kv_write, span_la_qk_norm_rope,
+                                                  span_la_softmax_branches_from_kv, span_la_softmax_paged,
+                                                  span_la_softmax_pass)
+from oracle import paged_oracle as po
+from paged_helpers import BF16, E4M3, U16, check_attention, f64, i32, make_pages, make_table
+
+pytestmark = pytest.mark.gpu
+
+# What the weights are rounded to: to bf16, half a step (where they are held more exactly, so much the better).
+WEIGHTS = U16
+
+
+def _setup(lens, rows, G, H, R, cache, dev, seed=0, layout="plain", v_size=1.0, q_size=1.0, width=None):
+    """A cache whose rows of sequences hold numbers and all others NaN, and the queries."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    table, P = make_table(lens, R, 2, seed, width)
+    c = make_pages(P, H, R, cache, dev, layout, fill=0xFF)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1])
+    k = torch.randn(T, H, 64, generator=g, device=dev)
+    v = torch.randn(T, H, 64, generator=g, device=dev) * v_size
+    v = v * torch.exp2(torch.randint(-4, 5, (T, H, 1), generator=g, device=dev).float())    # rows of different sizes
+    if T:
+        span_la_kv_write(k, v, c[0], c[1], i32(table, dev), i32(lens, dev), i32(cu, dev), c[2], c[3])
+    n = int(sum(rows))
+    q = (torch.randn(n, G * H, 64, generator=g, device=dev) * q_size).to(BF16)
+    return q, c, table, np.concatenate([[0], np.cumsum(rows)])
+
+
+def _run(q, c, table, lens, cu, dev, **kw):
+    out = torch.full_like(q, float("nan"), memory_format=torch.contiguous_format)
+    lse = torch.full(q.shape[:2], float("nan"), device=dev)
+    span_la_softmax_paged(q, c[0], c[1], i32(table, dev), i32(lens, dev), i32(cu, dev), c[2], c[3], out=out, lse=lse, **kw)
+    span_la_check()
+    return out, lse
+
+
+CASES = [
+    # lens, rows, G, H, R
+    ([1], [1], 1, 1, 16),
+    ([1, 2, 15, 16, 17, 31, 32, 33], [1] * 8, 1, 3, 16),
+    ([63, 64, 65, 127, 128, 129, 255, 257], [1] * 8, 4, 2, 32),
+    ([700, 3, 1300], [1, 1, 1], 8, 2, 128),
+    ([900, 40], [1, 1], 16, 1, 64),
+    ([300, 77, 5], [4, 3, 2], 4, 2, 16),
+    ([300, 77], [5, 16], 1, 5, 256),
+    ([1000, 900], [2, 2], 3, 2, 64),
+    ([257, 130], [17, 20], 1, 2, 32),
+    ([129, 128, 127], [129, 128, 127], 1, 2, 64),
+    ([400, 300, 1], [33, 300, 1], 2, 2, 16),
+    ([513], [260], 3, 2, 128),
+    ([700, 513], [100, 513], 5, 1, 32),
+    ([300], [40], 32, 1, 64),
+    ([260, 5], [9, 5], 128, 1, 16),
+    ([900, 20, 450, 64, 1], [300, 1, 2, 64, 1], 1, 4, 64),
+    ([2000], [1], 1, 16, 16),
+    ([5000], [600], 1, 2, 256),
+]
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(cuda_device, case, cache):
+    lens, rows, G, H, R = CASES[case]
+    q, c, table, cu = _setup(lens, rows, G, H, R, cache, cuda_device, seed=case)
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("layout", ["interleaved", "rows"])
+@pytest.mark.parametrize("rows", [[1, 1], [3, 90]])
+def test_other_layouts_and_strided_queries(cuda_device, layout, cache, rows):
+    lens = [333, 150]
+    q, c, table, cu = _setup(lens, rows, 2, 3, 32, cache, cuda_device, seed=3, layout=layout)
+    fused = torch.cat([q.reshape(len(q), -1), q.reshape(len(q), -1)[:, :128]], 1)
+    strided = fused[:, :6 * 64].view(len(q), 6, 64)
+    big = torch.full((2, 40), 1 << 30, dtype=torch.int32, device=cuda_device)         # a part of a wider table
+    big[:, 5:5 + table.shape[1]] = i32(table, cuda_device)
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    again = span_la_softmax_paged(strided, c[0], c[1], big[:, 5:5 + table.shape[1]], i32(lens, cuda_device), i32(cu, cuda_device),
+                                  c[2], c[3])
+    span_la_check()
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 4, 70])
+@pytest.mark.parametrize("scale,q_size", [(1.0, 2.0), (0.01, 1.0), (0.3, 8.0), (1e-20, 1e18)])
+def test_scales(cuda_device, rows, scale, q_size, cache):
+    """Flat and peaked weights, large scores, queries of any size."""
+    lens = [500, 70]
+    q, c, table, cu = _setup(lens, [rows, rows], 2, 2, 64, cache, cuda_device, seed=7, q_size=q_size)
+    out, lse = _run(q, c, table, lens, cu, cuda_device, scale=scale)
+    check_attention(q, out, lse, c, table, lens, cu, scale, WEIGHTS)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 3, 40])
+@pytest.mark.parametrize("big,small", [(2.0 ** 60, 2.0 ** -60), (2.0 ** 100, 1.0), (1.0, 2.0 ** -100)])
+def test_values_of_far_sizes(cuda_device, rows, big, small, cache):
+    """Rows of V whose sizes are far apart, the large ones with almost no weight or with most of it; rows of zeros."""
+    lens = [200, 90]
+    q, c, table, cu = _setup(lens, [rows, rows], 2, 2, 32, cache, cuda_device, seed=8)
+    g = torch.Generator(device=cuda_device).manual_seed(1)
+    T = sum(lens)
+    k = torch.randn(T, 2, 64, generator=g, device=cuda_device)
+    v = torch.randn(T, 2, 64, generator=g, device=cuda_device) * small
+    v[7::31] *= big / small
+    v[5::13] = 0
+    k[7::62] = -4 * q[0, 0].float()          # hardly seen
+    k[38::62] = 0.4 * q[0, 0].float()
+    all_cu = np.concatenate([[0], np.cumsum(lens)])
+    span_la_kv_write(k, v, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), i32(all_cu, cuda_device), c[2], c[3])
+    out, lse = _run(q, c, table, lens, cu, cuda_device, scale=1.0)
+    check_attention(q, out, lse, c, table, lens, cu, 1.0, WEIGHTS)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows,G", [(1, 1), (4, 2), (30, 4), (200, 1)])
+def test_rows_that_see_nothing(cuda_device, rows, G, cache):
+    """Sequences shorter than their packed rows, empty ones, sequences of no packed rows."""
+    lens, n = [0, rows // 2, 40, 1, rows - 1, 300], [rows, rows, 0, rows, rows, rows]
+    q, c, table, cu = _setup(lens, n, G, 2, 16, cache, cuda_device, seed=9)
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    assert (out[:rows] == 0).all() and torch.isneginf(lse[:rows]).all()
+
+
+@pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan"), 3.3e38])
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows,G", [(2, 1), (4, 4), (40, 2), (300, 1)])
+def test_what_a_row_does_not_see_does_not_reach_it(cuda_device, rows, G, cache, what):
+    """The last row of every sequence holds infinities or NaN: only the last packed row sees it."""
+    lens = [rows + 5, 310, rows]
+    q, c, table, cu = _setup(lens, [rows] * 3, G, 2, 32, cache, cuda_device, seed=11)
+    before = [L - 1 for L in lens]
+    clean, _ = _run(q, c, table, lens, cu, cuda_device)
+    for x, dims in ((0, [3, 60]), (1, [0, 17, 63])):
+        new = torch.randn(3, 2, 64, device=cuda_device)
+        new[:, :, dims] = what
+        pair = (new, torch.zeros_like(new)) if x == 0 else (torch.zeros_like(new), new)
+        span_la_kv_write(pair[0], pair[1], c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), None, c[2], c[3])
+        out, lse = _run(q, c, table, lens, cu, cuda_device)
+        keep = np.concatenate([np.arange(cu[s], cu[s + 1] - 1) for s in range(3)])
+        if x == 0:                                       # keys that are not seen change no bit
+            assert torch.equal(out[keep], clean[keep])
+        ref_cu = np.concatenate([[0], np.cumsum([rows - 1] * 3)])
+        check_attention(q[keep], out[keep], lse[keep], c, table, before, ref_cu, 0.125, WEIGHTS)
+        seen = f64(out[cu[1] + rows - 1])
+        if x == 1 and not (cache == E4M3 and np.isfinite(what)):
+            finite = np.ones(64, dtype=bool)
+            finite[dims] = False
+            if not np.isfinite(what):
+                assert not np.isfinite(seen[:, dims]).any()
+            assert np.isfinite(seen[:, finite]).all()
+
+
+def test_other_rows_of_the_call_are_left(cuda_device):
+    """Packed rows of no sequence, and sequences of more rows than max_rows (reported)."""
+    lens = [50, 60, 70]
+    q, c, table, _ = _setup(lens, [10, 2, 2], 1, 2, 16, BF16, cuda_device)
+    q = torch.cat([q, q])
+    cu = [2, 12, 14, 16]
+    out, _ = _run(q, c, table, lens, cu, cuda_device)
+    check_attention(q, out, None, c, table, lens, cu, 0.125, WEIGHTS)
+    assert torch.isnan(out[:2]).all() and torch.isnan(out[16:]).all()
+    out.fill_(float("nan"))
+    span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), i32(cu, cuda_device), max_rows=4, out=out)
+    with pytest.raises(SpanLAError, match="out of range"):
+        span_la_check()
+    check_attention(q, out, None, c, table, lens, cu, 0.125, WEIGHTS, max_rows=4)
+    assert torch.isnan(out[2:12]).all()
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_pages_out_of_range_are_not_seen_and_reported(cuda_device, rows):
+    lens = [100, 200, 300]
+    q, c, table, cu = _setup(lens, [rows] * 3, 2, 2, 16, BF16, cuda_device, seed=5)
+    bad = table.copy()
+    bad[1, 2], bad[2, 0] = 1 << 30, -1
+    lens_bad = np.array(lens)
+    out = torch.full_like(q, float("nan"))
+    span_la_softmax_paged(q, c[0], c[1], i32(bad, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), out=out)
+    with pytest.raises(SpanLAError, match="a page out of range"):
+        span_la_check()
+    check_attention(q[:rows], out[:rows], None, c, table, lens[:1], cu[:2], 0.125, WEIGHTS)
+    assert torch.isfinite(out.float()).all()
+    lens_bad[1] = -5
+    out.fill_(float("nan"))
+    span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), out=out)
+    with pytest.raises(SpanLAError, match="offsets or length"):
+        span_la_check()
+    assert torch.isnan(out[rows:2 * rows]).all()
+    keep = np.concatenate([np.arange(rows), np.arange(2 * rows, 3 * rows)])
+    check_attention(q[keep], out[keep], None, c, table[[0, 2]], [100, 300], [0, rows, 2 * rows], 0.125, WEIGHTS)
+
+
+@pytest.mark.parametrize("rows", [1, 4, 100])
+def test_same_bits_again_and_on_another_stream(cuda_device, rows):
+    lens = [1500, 30, 700, 64]
+    q, c, table, cu = _setup(lens, [min(rows, n) for n in lens], 2, 4, 64, E4M3, cuda_device, seed=4)
+    ref, lse = _run(q, c, table, lens, cu, cuda_device)
+    args = [c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), i32(cu, cuda_device), c[2], c[3]]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(cuda_device) for _ in range(3)]
+    outs = []
+    for i in range(12):                                # calls in flight side by side
+        s = streams[i % 3]
+        o = torch.empty_like(q)
+        span_la_softmax_paged(q, *args, out=o, stream=s)
+        outs.append(o)
+    torch.cuda.synchronize()
+    span_la_check()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
+def test_more_sequences_than_one_launch_takes(cuda_device):
+    S = 2500
+    rng = np.random.default_rng(0)
+    lens = rng.integers(1, 40, S)
+    q, c, table, cu = _setup(list(lens), [1] * S, 1, 1, 16, BF16, cuda_device, seed=6)
+    out, lse = _run(q, c, table, lens, cu, cuda_device, max_rows=1)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    single = span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device))
+    span_la_check()
+    assert torch.equal(single, out)
+
+
+def test_generation_step_by_step_in_a_graph(cuda_device):
+    """A prompt in chunks, then tokens: norm and rotation, cache write, attention, recorded once for the tokens and
+    replayed with growing lengths.  Equals the softmax layer over whole sequences, to its own bound."""
+    dev, H, R, S, prompt, steps = cuda_device, 4, 16, 3, 50, 20
+    g = torch.Generator(device=dev).manual_seed(2)
+    L = prompt + steps
+    proj = torch.randn(S, L, 3 * H * 64, generator=g, device=dev).to(BF16)
+    freq = rope_inv_freq(64)
+    pos = torch.arange(L, device=dev, dtype=torch.int32)
+    table, P = make_table([L] * S, R, 0, 3)
+    c = make_pages(P, H, R, BF16, dev)
+    dt = i32(table, dev)
+
+    def layer(rows, where, lens, cu, max_rows):
+        n = rows.shape[0]
+        q, k, v = (rows[:, i * H * 64:(i + 1) * H * 64].view(n, H, 64) for i in range(3))
+        q, k = span_la_qk_norm_rope(q, k, where, freq)
+        span_la_kv_write(k, v, c[0], c[1], dt, lens, cu)
+        return span_la_softmax_paged(q, c[0], c[1], dt, lens, cu, max_rows=max_rows)
+
+    got = torch.empty(S, L, H, 64, dtype=BF16, device=dev)
+    for a, b in ((0, 33), (33, prompt)):                # chunks
+        cu = i32(np.arange(S + 1) * (b - a), dev)
+        o = layer(proj[:, a:b].reshape(S * (b - a), -1), pos[a:b].repeat(S), i32([b] * S, dev), cu, b - a)
+        got[:, a:b] = o.view(S, b - a, H, 64)
+    rows, where, lens = proj[:, prompt].clone(), pos[prompt:prompt + 1].repeat(S), i32([prompt + 1] * S, dev)
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        o = layer(rows, where, lens, None, None)
+    for t in range(prompt, L):
+        rows.copy_(proj[:, t]), where.fill_(t), lens.fill_(t + 1)
+        graph.replay()
+        got[:, t] = o
+    torch.cuda.synchronize()
+    span_la_check()
+    flat = proj.reshape(S * L, -1)
+    q, k, v = (flat[:, i * H * 64:(i + 1) * H * 64].view(S * L, H, 64) for i in range(3))
+    vcu = (np.arange(S + 1) * L).astype(np.int32)
+    q, k = span_la_qk_norm_rope(q, k, torch.from_numpy(packed_positions(vcu, None, None, S * L)).to(dev), freq)
+    whole = span_la_softmax_pass(q, k, v.contiguous(), vcu, [], [])
+    span_la_check()
+    for s in range(S):
+        ref, _, mass, _ = po.attend(f64(q[s * L:(s + 1) * L]), f64(k[s * L:(s + 1) * L]), f64(v[s * L:(s + 1) * L]), 0.125)
+        tol = 1.01 * U16 * np.abs(ref) + (WEIGHTS + 2.0 ** -12) * mass       # as check_attention, its small terms in one
+        assert np.all(np.abs(f64(got[s]) - ref) <= tol)
+        assert np.all(np.abs(f64(got[s]) - f64(whole[s * L:(s + 1) * L])) <= 2 * tol)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+def test_branches_over_a_view_read_back(cuda_device, cache):
+    """A view's keys and values kept in the cache, read back for the branches that are scored over it."""
+    dev, H, view, blens = cuda_device, 3, 300, [20, 1, 64, 130]
+    g = torch.Generator(device=dev).manual_seed(3)
+    k, v = (torch.randn(view, H, 64, generator=g, device=dev).to(BF16) for _ in range(2))
+    bcu = np.concatenate([[0], np.cumsum(blens)]).astype(np.int32)
+    q, bk, bv = (torch.randn(int(bcu[-1]), H, 64, generator=g, device=dev).to(BF16) for _ in range(3))
+    table, P = make_table([view], 64, 1, 0)
+    c = make_pages(P, H, 64, cache, dev)
+    args = [i32(table, dev), i32([view], dev), i32([0, view], dev)]
+    span_la_kv_write(k, v, c[0], c[1], *args, c[2], c[3])
+    vk, vv = span_la_kv_read(c[0], c[1], *args, view, c[2], c[3])
+    if cache == BF16:
+        assert torch.equal(vk, k) and torch.equal(vv, v)
+    out = span_la_softmax_branches_from_kv(vk, vv, [0, view], q, bk, bv, bcu, [0] * 4)
+    span_la_check()
+    for b in range(4):
+        rows = slice(int(bcu[b]), int(bcu[b + 1]))
+        K, V = np.concatenate([f64(vk), f64(bk[rows])]), np.concatenate([f64(vv), f64(bv[rows])])
+        ref, _, mass, _ = po.attend(f64(q[rows]), K, V, 0.125)
+        assert np.all(np.abs(f64(out[rows]) - ref) <= 1.01 * U16 * np.abs(ref) + (WEIGHTS + 2.0 ** -12) * mass)
+    # The same branches with their own rows in the cache, in pages of their own behind a copy of the view's last one.
+    n = -(-(view + max(blens)) // 64)
+    kp, vp, ks, vs = kv_pages(4 * n, H, 64, cache, dev)
+    tb = i32(np.arange(4 * n).reshape(4, n), dev)
+    lens = i32([view + b for b in blens], dev)
+    full = [torch.cat([torch.cat([x, y[int(bcu[b]):int(bcu[b + 1])]]) for b in range(4)]) for x, y in ((k, bk), (v, bv))]
+    span_la_kv_write(full[0], full[1], kp, vp, tb, lens, i32(np.concatenate([[0], np.cumsum([view + b for b in blens])]), dev), ks, vs)
+    paged = span_la_softmax_paged(q, kp, vp, tb, lens, i32(bcu, dev), ks, vs)
+    span_la_check()
+    check_attention(q, paged, None, (kp, vp, ks, vs), tb.cpu().numpy(), [view + b for b in blens], bcu, 0.125, WEIGHTS)
+
+
+def test_pages_past_two_to_the_32(cuda_device):
+    P, H, R = 23000, 32, 128
+    kp, vp, ks, vs = kv_pages(P, H, R, E4M3, cuda_device)
+    lens = [257]
+    table = np.array([[P - 1, 11, P - 2]])
+    k, v = (torch.randn(257, H, 64, device=cuda_device) for _ in range(2))
+    span_la_kv_write(k, v, kp, vp, i32(table, cuda_device), i32(lens, cuda_device), i32([0, 257], cuda_device), ks, vs)
+    small = [torch.stack([x[int(p)] for p in table[0]]) for x in (kp.view(torch.uint8), vp.view(torch.uint8), ks, vs)]
+    small = (small[0].view(E4M3), small[1].view(E4M3), small[2], small[3])
+    for rows in (1, 40):
+        q = torch.randn(rows, H, 64, device=cuda_device).to(BF16)
+        out, lse = _run(q, (kp, vp, ks, vs), table, lens, [0, rows], cuda_device)
+        check_attention(q, out, lse, small, np.arange(3)[None], lens, [0, rows], 0.125, WEIGHTS)
+    del kp, vp, ks, vs
+    torch.cuda.empty_cache()
