@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) paged_rows_kernel(const __grid
   bool bad = false;
   const SeqRows r = seq_rows(a, s, &bad);
   const int64_t i = t - r.row0;
-  if (i < 0 || i >= r.n) return;
+  if (i < 0 || i >= r.n || static_cast<int64_t>(r.n) * p.group <= kStepHeads) return;
   const int32_t seen = max(0, static_cast<int32_t>(r.len - r.n + i + 1));
   const int head = blockIdx.y * kRowWarps + (threadIdx.x >> 5);
   if (head < p.heads) attend_row<kE4m3>(a, p, s, t, head, seen);

@@ -140,12 +140,14 @@ span_la_status device_state(DeviceState** out) {
 constexpr int kKernelSplit = 0, kKernelChunk = 1, kKernelScan = 2, kKernelTile = 3,
               kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6, kKernelRecurState = 7,
               kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11,
-              kKernelSpanDecay = 12, kKernelKvWrite = 13, kKernelKvRead = 14, kKernelPagedRows = 15;
+              kKernelSpanDecay = 12, kKernelKvWrite = 13, kKernelKvRead = 14, kKernelPagedRows = 15, kKernelPagedStep = 16,
+              kKernelPagedJoin = 17;
 const char* const kKernelNames[SPAN_LA_NUM_KERNELS] = {"split_f32", "chunk_state", "segmented_scan",
                                                        "tile_output", "span_state", "span_output",
                                                        "softmax_attn", "recur_state", "recur_scan",
                                                        "recur_output", "decay_step", "qk_norm_rope",
-                                                       "span_decay", "kv_write", "kv_read", "paged_rows"};
+                                                       "span_decay", "kv_write", "kv_read", "paged_rows",
+                                                       "paged_step", "paged_join"};
 
 std::atomic<int64_t> g_launches[SPAN_LA_NUM_KERNELS];
 std::atomic<bool> g_profiling{false};
@@ -2140,6 +2142,54 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
   return SPAN_LA_OK;
 }
 
+// Boxes of `rows` rows of one page and head, out of pages [pages][heads][page_rows][64].
+span_la_status encode_pages(CUtensorMap* map, const void* base, const KvArgs& a, bool e4m3, int rows) {
+  const cuuint64_t esz = e4m3 ? 1 : 2;
+  const cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(a.page_rows), static_cast<cuuint64_t>(a.heads),
+                              static_cast<cuuint64_t>(a.pages)};
+  const cuuint64_t strides[3] = {a.row_stride * esz, a.head_stride * esz, a.page_stride * esz};
+  const cuuint32_t box[4] = {kHeadDim, static_cast<cuuint32_t>(std::min(rows, a.page_rows)), 1, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+                              dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              e4m3 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPAN_LA_ERR_CUDA, "cuTensorMapEncodeTiled of pages failed (%d)", (int)r);
+  return SPAN_LA_OK;
+}
+
+// The launches of span_la_softmax_paged: sequences of few row heads and those of many each go to their kernel (they
+// tell them apart by the row offsets, which are in device memory).
+span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num_sms, cudaStream_t stream) {
+  span_la_status st = SPAN_LA_OK;
+  cudaError_t e = cudaSuccess;
+  if (p.group <= kStepHeads) {
+    CUtensorMap tm_k, tm_v;
+    if ((st = encode_pages(&tm_k, a.k, a, e4m3, kStepUnit)) != SPAN_LA_OK) return st;
+    if ((st = encode_pages(&tm_v, a.v, a, e4m3, kStepUnit)) != SPAN_LA_OK) return st;
+    const int64_t units = std::max<int64_t>(1, (a.capacity + kStepUnit - 1) / kStepUnit);   // of a sequence and head, at most
+    const int grid = paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), e4m3, num_sms);
+    float* ws = nullptr;
+    if (grid > 1) {
+      const size_t bytes = static_cast<size_t>(grid) * kStepWsFloats * sizeof(float);
+      if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", bytes);
+      e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, stream);
+      if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", bytes, cudaGetErrorString(e));
+    }
+    for (int s0 = 0; s0 < a.seqs && e == cudaSuccess; s0 += kStepSeqs) {
+      const int ns = std::min(kStepSeqs, a.seqs - s0);
+      e = counted_launch(kKernelPagedStep, stream, [&] { return launch_paged_step(tm_k, tm_v, a, p, s0, ns, grid, e4m3, ws, stream); });
+      if (e == cudaSuccess && grid > 1)
+        e = counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, grid, e4m3, ws, stream); });
+    }
+    const cudaError_t ef = ws != nullptr ? cudaFreeAsync(ws, stream) : cudaSuccess;
+    if (e == cudaSuccess) e = ef;
+  }
+  if (e == cudaSuccess && a.max_rows * p.group > kStepHeads)
+    e = counted_launch(kKernelPagedRows, stream, [&] { return launch_paged_rows(a, p, e4m3, stream); });
+  return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "paged attention launch");
+}
+
 // Rows of `heads` heads of a packed array (q, k or v), `stride` elements apart.
 span_la_status check_rows(const char* name, const void* p, int64_t stride, int64_t rows, int64_t heads, int64_t esz) {
   if (p == nullptr || !aligned16(p)) return fail(SPAN_LA_ERR_INVALID, "%s must be non-NULL and 16-byte aligned", name);
@@ -2908,10 +2958,7 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     p.heads = num_q_heads;
     p.group = num_q_heads / a.heads;
     p.scale = scale == 0.f ? 0.125f : scale;
-    const cudaError_t e = counted_launch(kKernelPagedRows, stream, [&] {
-      return launch_paged_rows(a, p, cache->dtype == SPAN_LA_E4M3, stream);
-    });
-    return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "paged attention launch");
+    return run_paged(a, p, cache->dtype == SPAN_LA_E4M3, dev->num_sms, stream);
   });
 }
 

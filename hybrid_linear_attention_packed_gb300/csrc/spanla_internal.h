@@ -444,6 +444,21 @@ struct PagedAttn {
   int32_t group;
   float scale;
 };
+// Sequences of at most kStepHeads packed row heads (rows * group) of a key head (k_paged_step.cu), at most kStepSeqs in
+// a launch: [s0, s0 + ns).  `ws`: kStepWsFloats for each of the `grid` CTAs; the join kernel, with the same grid, follows
+// where there is more than one.
+constexpr int kStepHeads = 16, kStepSeqs = 1024, kStepUnit = 32;
+constexpr int kStepWsFloats = 2432;
+struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begins in the CTA and goes on in the next ones
+  int32_t parts;                // CTAs with some of it, or 0
+  int32_t s, h, n, len, row0;
+  int32_t pad[2];
+};
+int paged_step_grid(int64_t most_units, bool e4m3, int num_sms);
+cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
+                              int grid, bool e4m3, float* ws, cudaStream_t stream);
+cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
+
 cudaError_t launch_paged_rows(const KvArgs& a, const PagedAttn& p, bool e4m3, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
