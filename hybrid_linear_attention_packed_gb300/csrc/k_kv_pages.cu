@@ -13,23 +13,48 @@
 // a time, 8 lanes a row (16 bytes of bf16 a lane), 4 rows at once, all 32 in
 // flight.  Consecutive rows of one head are neighbours in a page, and the 32
 // powers of two go out as one store.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace spanla {
 namespace {
 
 constexpr int kRows = 32, kWarps = 8, kSteps = kRows / 4;
+constexpr int64_t kBlocks = 608;   // four for each of 152 SMs
 
 struct Places {            // of a CTA's rows: element offset of head 0 in the pages (-1: none), byte offset in the scales
   int64_t at[kRows], scale_at[kRows];
 };
 
+// The sequence of a row near row t0 of a warp's 32 rows: all lanes look for t0's together (32 offsets at a time), then
+// each goes on to its own, which mostly is the same.
+__device__ __forceinline__ int find_seq(const KvArgs& a, int64_t t0) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = t0 + lane;
+  if (a.row_cu == nullptr) return t < a.seqs ? static_cast<int>(t) : -1;
+  int lo = 0, n = a.seqs + 1;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const int upto = __popc(__ballot_sync(0xffffffffu, at < lo + n && a.row_cu[min(at, a.seqs)] <= t0));
+    const int from = max(upto - 1, 0) * step;
+    n = min(step, n - from);
+    lo += from;
+  }
+  for (int i = 0; i < 4; ++i) {
+    if (lo >= a.seqs) return -1;
+    if (a.row_cu[lo + 1] > t) return lo;   // (a.row_cu[lo] > t: the caller sees that)
+    ++lo;
+  }
+  return seq_of_row(a, t);
+}
+
 __device__ __forceinline__ void find_places(const KvArgs& a, Places& pl) {
   if (threadIdx.x < kRows) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows, t = t0 + threadIdx.x;
     int64_t at = -1, scale_at = 0;
-    const int s = t < a.rows ? seq_of_row(a, t) : -1;
-    if (s >= 0) {
+    const int s = find_seq(a, t0);
+    if (s >= 0 && t < a.rows) {
       bool bad = false;
       const SeqRows r = seq_rows(a, s, &bad);
       const int64_t pos = r.len - (r.n - (t - r.row0));   // (negative: the sequence is shorter than its packed rows)
@@ -51,130 +76,170 @@ __device__ __forceinline__ void find_places(const KvArgs& a, Places& pl) {
   __syncthreads();
 }
 
-// 8 elements.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 8 elements as they lie in memory, and as fp32.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void store(float* p) const { reinterpret_cast<float4*>(p)[0] = a, reinterpret_cast<float4*>(p)[1] = b; }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) { a = make_float4(x[0], x[1], x[2], x[3]), b = make_float4(x[4], x[5], x[6], x[7]); }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+};
+// One type into another: rounded once, the same type as it is.
+template <typename To, typename From>
+__device__ __forceinline__ void convert(const Eight<From>& x, Eight<To>& y) {
+  float f[8];
+  x.get(f);
+  y.set(f);
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+template <typename T>
+__device__ __forceinline__ void convert(const Eight<T>& x, Eight<T>& y) {
+  y = x;
 }
 
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// Blocks (row block, heads of K and V by 8): the units u = blockIdx.y * 8 + warp are K of head u / 2 (u even) or V.
+// Units u: K of head u / 2 (u even) or V; a CTA's warps take every so manieth one.
 template <typename T, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows in) {
   __shared__ Places pl;
   find_places(a, pl);
-  const int lane = threadIdx.x & 31, unit = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (unit >= 2 * a.heads) return;
-  const int head = unit >> 1, sub = lane & 7;
-  const bool is_v = unit & 1;
-  const T* src = static_cast<const T*>(is_v ? in.v : in.k) + head * kHeadDim + sub * 8;
-  const int64_t stride = is_v ? in.v_row_stride : in.k_row_stride;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  float x[kSteps][8];
+  for (int unit = blockIdx.y * kWarps + (threadIdx.x >> 5); unit < 2 * a.heads; unit += gridDim.y * kWarps) {
+    const int head = unit >> 1;
+    const bool is_v = unit & 1;
+    const T* src = static_cast<const T*>(is_v ? in.v : in.k) + head * kHeadDim + sub * 8;
+    const int64_t stride = is_v ? in.v_row_stride : in.k_row_stride;
+    Eight<T> x[kSteps];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    if (pl.at[r] >= 0) load8(src + (t0 + r) * stride, x[i]);
-  }
-  uint32_t code = 0;   // row `lane`'s power of two
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    const int64_t at = pl.at[r] + head * a.head_stride + sub * 8;
-    if (kE4m3) {
-      uint32_t top = 0;   // magnitudes as bits order like numbers
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (finite(x[i][c])) top = max(top, __float_as_uint(x[i][c]) & 0x7fffffffu);
-#pragma unroll
-      for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-      // top = m 2^E, 1 <= m < 2: at most 448 2^e = 1.75 2^(8 + e) from e = E - 8 on, or E - 7 where m > 1.75.
-      const int e = min(119, max(-126, static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0)));
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      const uint32_t mine = __shfl_sync(0xffffffffu, static_cast<uint32_t>(e + 127), (lane & 3) * 8);
-      if ((lane >> 2) == i) code = mine;
-      if (pl.at[r] >= 0) {
-        uint32_t w[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float y0 = finite(x[i][2 * c]) ? x[i][2 * c] * inv : NAN;
-          const float y1 = finite(x[i][2 * c + 1]) ? x[i][2 * c + 1] * inv : NAN;
-          w[c] = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v : a.k) + at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-      }
-    } else if (pl.at[r] >= 0) {
-      store8(static_cast<__nv_bfloat16*>(is_v ? a.v : a.k) + at, x[i]);
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      x[i] = Eight<T>{};
+      if (pl.at[r] >= 0) x[i].load(src + (t0 + r) * stride);
     }
+    uint32_t code = 0;   // row `lane`'s power of two
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const int64_t at = pl.at[r] + head * a.head_stride + sub * 8;
+      if (kE4m3) {
+        float f[8];
+        x[i].get(f);
+        uint32_t top = 0;   // magnitudes as bits order like numbers
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (finite(f[c])) top = max(top, __float_as_uint(f[c]) & 0x7fffffffu);
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        // top = m 2^E, 1 <= m < 2: at most 448 2^e = 1.75 2^(8 + e) from e = E - 8 on, or E - 7 where m > 1.75.
+        const int e = min(119, max(-126, static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0)));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const uint32_t mine = __shfl_sync(0xffffffffu, static_cast<uint32_t>(e + 127), (lane & 3) * 8);
+        if ((lane >> 2) == i) code = mine;
+        if (pl.at[r] >= 0) {
+          uint32_t w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float y0 = finite(f[2 * c]) ? f[2 * c] * inv : NAN;
+            const float y1 = finite(f[2 * c + 1]) ? f[2 * c + 1] * inv : NAN;
+            w[c] = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v : a.k) + at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        }
+      } else if (pl.at[r] >= 0) {
+        Eight<__nv_bfloat16> y;
+        convert(x[i], y);
+        y.store(static_cast<__nv_bfloat16*>(is_v ? a.v : a.k) + at);
+      }
+    }
+    if (kE4m3 && pl.at[lane] >= 0)
+      (is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride] = static_cast<uint8_t>(code);
   }
-  if (kE4m3 && pl.at[lane] >= 0)
-    (is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride] = static_cast<uint8_t>(code);
 }
 
 template <typename T, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows to) {
   __shared__ Places pl;
   find_places(a, pl);
-  const int lane = threadIdx.x & 31, unit = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (unit >= 2 * a.heads) return;
-  const int head = unit >> 1, sub = lane & 7;
-  const bool is_v = unit & 1;
-  T* dst = static_cast<T*>(is_v ? to.v : to.k) + head * kHeadDim + sub * 8;
-  const int64_t stride = is_v ? to.v_row_stride : to.k_row_stride;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  float x[kSteps][8];
-  if (kE4m3) {
-    uint2 raw[kSteps];
+  for (int unit = blockIdx.y * kWarps + (threadIdx.x >> 5); unit < 2 * a.heads; unit += gridDim.y * kWarps) {
+    const int head = unit >> 1;
+    const bool is_v = unit & 1;
+    T* dst = static_cast<T*>(is_v ? to.v : to.k) + head * kHeadDim + sub * 8;
+    const int64_t stride = is_v ? to.v_row_stride : to.k_row_stride;
+    if (kE4m3) {
+      uint2 raw[kSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (pl.at[r] >= 0)
-        raw[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8));
-    }
-    const float scale =
-        pl.at[lane] >= 0 ? scale_of((is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride]) : 0.f;
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        raw[i] = make_uint2(0u, 0u);
+        if (pl.at[r] >= 0)
+          raw[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8));
+      }
+      const float scale =
+          pl.at[lane] >= 0 ? scale_of((is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride]) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const float e = __shfl_sync(0xffffffffu, scale, 4 * i + (lane >> 3));
-      const uint32_t w[2] = {raw[i].x, raw[i].y};
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const float e = __shfl_sync(0xffffffffu, scale, r);
+        const uint32_t w[2] = {raw[i].x, raw[i].y};
+        float f[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 y = from_e4m3x2((w[c >> 1] >> (16 * (c & 1))) & 0xffffu);
-        x[i][2 * c] = y.x * e, x[i][2 * c + 1] = y.y * e;
+        for (int c = 0; c < 4; ++c) {
+          const float2 y = from_e4m3x2((w[c >> 1] >> (16 * (c & 1))) & 0xffffu);
+          f[2 * c] = y.x * e, f[2 * c + 1] = y.y * e;
+        }
+        Eight<T> y;
+        y.set(f);
+        if (pl.at[r] >= 0) y.store(dst + (t0 + r) * stride);
+      }
+    } else {
+      Eight<__nv_bfloat16> x[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        if (pl.at[r] >= 0) x[i].load(static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        Eight<T> y;
+        convert(x[i], y);
+        if (pl.at[r] >= 0) y.store(dst + (t0 + r) * stride);
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (pl.at[r] >= 0) load8(static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8, x[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    if (pl.at[r] >= 0) store8(dst + (t0 + r) * stride, x[i]);
   }
 }
 
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((a.rows + kRows - 1) / kRows), (2 * a.heads + kWarps - 1) / kWarps);
+  // A CTA takes all heads of its rows where there are CTAs enough: finding the rows' places takes four reads one behind
+  // the other, as long as copying a few heads.
+  const int64_t blocks = (a.rows + kRows - 1) / kRows;
+  const int64_t split = std::min<int64_t>((2 * a.heads + kWarps - 1) / kWarps, std::max<int64_t>(1, (kBlocks + blocks - 1) / blocks));
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
   kernel<<<grid, kWarps * 32, 0, stream>>>(a, x);
   return cudaGetLastError();
 }

@@ -16,8 +16,8 @@
 // pages: q, K and V enter as fp16 (K and V exactly, q scaled by a power of two
 // for its row, then all but its least elements), the rows' powers of two go onto
 // the scores and the weights in fp32; the weights w_j = p_j 2^(e_j) have a running
-// maximum M of their own, so that fp16 holds them at up to 2^15 (2^-11 of each, and
-// 2^-40 of the largest).
+// maximum 2^M of their own and enter 2^15 times over it, so that fp16 holds them to
+// 2^-11 of each, or 2^-40 of the largest.
 //
 // A warp's first and last items may go on in other warps.  Those parts (m, M, l,
 // O) meet in shared memory for the warps of a CTA and then, for the items that go
@@ -45,7 +45,8 @@ struct Cfg {
   static constexpr uint32_t kStage = 2 * kHalf;
   static constexpr uint32_t kRing = kStages * kStage;          // of a warp
   static constexpr uint32_t kScales = kWarps * kRing;          // 2 x 32 bytes a stage
-  static constexpr uint32_t kHead = kScales + (kE4m3 ? kWarps * kStages * 2 * kUnit : 0);
+  static constexpr uint32_t kFactors = kScales + (kE4m3 ? kWarps * kStages * 2 * kUnit : 0);   // of a unit's rows, 8 bytes
+  static constexpr uint32_t kHead = kFactors + (kE4m3 ? kWarps * kUnit * 8 : 0);
   static constexpr uint32_t kSum = kHead + kWarps * kSlotFloats * 4;
   static constexpr uint32_t kLen = kSum + (kStepSeqs + 1) * 8;
   static constexpr uint32_t kRow0 = kLen + kStepSeqs * 4;
@@ -83,10 +84,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 values (low half of `two`) as fp16.
-__device__ __forceinline__ uint32_t half_of_e4m3x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// Four e4m3 values as two pairs of fp16.
+__device__ __forceinline__ void half2_of_e4m3(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(four));
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -115,9 +116,10 @@ __device__ __forceinline__ void store_pair(const PagedAttn& p, int64_t at, int d
   *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + d) = pack_bf16x2(x, y);
 }
 
-// The scores of a row head are relative to 2^m, its O to 2^M: o = O 2^(M - m) / l.
+// The weights of a row head are relative to 2^m, its O to 2^(M - 15) (bf16 pages: 2^m): o = O 2^(M - 15 - m) / l.
+template <bool kE4m3>
 __device__ __forceinline__ float out_factor(float m, float M, float l) {
-  return l == 0.f ? 0.f : (M == m ? 1.f : ex2(M - m)) / l;
+  return l == 0.f ? 0.f : (kE4m3 ? ex2(M - m - 15.f) : 1.f) / l;
 }
 __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l)); }
 
@@ -193,9 +195,9 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   // ---------------------------------------------------------------- this warp's units
   const int64_t nw = min(static_cast<int64_t>(gridDim.x) * kW, U);     // warps at work: each has a unit at least
   auto begin_of = [&](int64_t w) { return w >= nw ? U : U * w / nw; };
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kW + warp;
-  const int64_t lo = begin_of(gw), hi = begin_of(gw + 1);
-  const int64_t cta_lo = begin_of(static_cast<int64_t>(blockIdx.x) * kW), cta_hi = begin_of(static_cast<int64_t>(blockIdx.x + 1) * kW);
+  const int64_t edge = begin_of(static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));   // lane w: of the CTA's warp w
+  auto edge_of = [&](int w) { return __shfl_sync(0xffffffffu, edge, w); };
+  const int64_t lo = edge_of(warp), hi = edge_of(warp + 1), cta_lo = edge_of(0), cta_hi = edge_of(kW);
   auto locate = [&](int64_t x, At& at) {
     int l = 0, r = ns;   // the last sequence that starts at x or before
     while (r - l > 1) {
@@ -222,6 +224,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   const uint32_t ring = base + warp * C::kRing;
   uint8_t* ring_p = smem + warp * C::kRing;
   uint32_t* info = reinterpret_cast<uint32_t*>(smem + C::kInfo) + warp * kS;
+  float2* factors = reinterpret_cast<float2*>(smem + C::kFactors) + warp * kUnit;
   uint8_t* scales = smem + C::kScales + warp * kS * 2 * kUnit;
   float* head_slot = reinterpret_cast<float*>(smem + C::kHead) + warp * kSlotFloats;
   float* tail_slot = reinterpret_cast<float*>(ring_p);   // once the ring is done
@@ -390,7 +393,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(st + row * 64 + ((t ^ ((row >> 1) & 3)) << 4)) : "memory");
 #pragma unroll
-        for (int c = 0; c < 4; ++c) mma16816<true>(x[i], qa[c], half_of_e4m3x2(w[c] & 0xffffu), half_of_e4m3x2(w[c] >> 16));
+        for (int c = 0; c < 4; ++c) {
+          uint32_t b0, b1;
+          half2_of_e4m3(w[c], b0, b1);
+          mma16816<true>(x[i], qa[c], b0, b1);
+        }
       } else {
         const uint32_t row = i * 8 + (lane & 7);
 #pragma unroll
@@ -402,21 +409,29 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
       }
     }
+    if (kE4m3) {
+      // (what a row's powers of two do: the score's factor, the weight's logarithm)
+      const uint8_t* sc = scales + stage * 2 * kUnit + lane;
+      const uint32_t v = sc[kUnit];
+      factors[lane] = make_float2(scale_of(sc[0]), v == 255 ? NAN : static_cast<float>(static_cast<int>(v) - 127));
+      __syncwarp();
+    }
     const int f0 = kE4m3 ? (t & 1) + 4 * (t >> 1) : 2 * t, f1 = kE4m3 ? 3 - (t & 1) + 4 * (t >> 1) : 2 * t + 1;
-    float ev[4][2];   // e4m3: log2 of V's powers of two
+    // z: e4m3: the score with log2 of V's power of two, whose maximum is M + 15.
+    const bool two = n * p.group > 8;   // (else row heads g + 8 are none)
+    float z[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (kE4m3) {
-        const uint8_t* sc = scales + stage * 2 * kUnit + i * 8;
-        const float k0 = scale_of(sc[f0]), k1 = scale_of(sc[f1]);
-        x[i][0] = x[i][0] * qc[0] * k0, x[i][1] = x[i][1] * qc[0] * k1;
-        x[i][2] = x[i][2] * qc[1] * k0, x[i][3] = x[i][3] * qc[1] * k1;
-        const uint32_t v0 = sc[kUnit + f0], v1 = sc[kUnit + f1];
-        ev[i][0] = v0 == 255 ? NAN : static_cast<float>(static_cast<int>(v0) - 127);
-        ev[i][1] = v1 == 255 ? NAN : static_cast<float>(static_cast<int>(v1) - 127);
-      } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[i][c] *= c2;
+      for (int c = 0; c < 4; ++c) {
+        if (c >= 2 && !two) continue;
+        if (kE4m3) {
+          const float2 sc = factors[i * 8 + ((c & 1) ? f1 : f0)];
+          x[i][c] = x[i][c] * qc[c >> 1] * sc.x;
+          z[i][c] = x[i][c] + sc.y;
+        } else {
+          x[i][c] *= c2;
+        }
       }
     }
     if (!whole || j0 + kUnit > first_hidden) {
@@ -425,22 +440,19 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int in = i * 8 + ((c & 1) ? f1 : f0);
-          if (!((exist >> in) & 1u) || j0 + in >= seen[c >> 1]) x[i][c] = -INFINITY;
+          if (!((exist >> in) & 1u) || j0 + in >= seen[c >> 1]) x[i][c] = z[i][c] = -INFINITY;
         }
       }
     }
     // Running maxima.
-    float top[2], wtop[2];
+    float top[2] = {m[0], m[1]}, wtop[2] = {M[0], M[1]};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      top[i] = m[i], wtop[i] = M[i];
+      if (i == 1 && !two) continue;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         top[i] = fmaxf(top[i], fmaxf(x[k][2 * i], x[k][2 * i + 1]));
-        if (kE4m3) {
-          if (x[k][2 * i] != -INFINITY) wtop[i] = fmaxf(wtop[i], x[k][2 * i] + ev[k][0] - 15.f);
-          if (x[k][2 * i + 1] != -INFINITY) wtop[i] = fmaxf(wtop[i], x[k][2 * i + 1] + ev[k][1] - 15.f);
-        }
+        if (kE4m3) wtop[i] = fmaxf(wtop[i], fmaxf(z[k][2 * i], z[k][2 * i + 1]));
       }
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
@@ -465,7 +477,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
     // Weights and O.
     const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-    const float B0 = M[0] == -INFINITY ? 0.f : M[0], B1 = M[1] == -INFINITY ? 0.f : M[1];
+    const float B0 = (M[0] == -INFINITY ? 0.f : M[0]) - 15.f, B1 = (M[1] == -INFINITY ? 0.f : M[1]) - 15.f;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       uint32_t hi_p[4], lo_p[4];
@@ -475,9 +487,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         float w[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          w[c] = 0.f;
+          if (c >= 2 && !two) continue;
           const float pw = ex2(x[i][c] - (c < 2 ? b0 : b1));
           l[c >> 1] += pw;
-          w[c] = !kE4m3 ? pw : x[i][c] == -INFINITY ? 0.f : ex2(x[i][c] + ev[i][c & 1] - (c < 2 ? B0 : B1));
+          w[c] = kE4m3 ? ex2(z[i][c] - (c < 2 ? B0 : B1)) : pw;
         }
         if (kE4m3) {
           hi_p[2 * half] = half2_of(w[0], w[1]);
@@ -504,8 +518,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int j = 0; j < 4; ++j) {   // blocks 2 j, 2 j + 1: two bytes of each row
           const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
           const uint32_t y0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), y1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
-          mma16816<true>(o[2 * j], hi_p, half_of_e4m3x2(y0 & 0xffffu), half_of_e4m3x2(y1 & 0xffffu));
-          mma16816<true>(o[2 * j + 1], hi_p, half_of_e4m3x2(y0 >> 16), half_of_e4m3x2(y1 >> 16));
+          uint32_t b0[2], b1[2];
+          half2_of_e4m3(y0, b0[0], b0[1]);
+          half2_of_e4m3(y1, b1[0], b1[1]);
+          mma16816<true>(o[2 * j], hi_p, b0[0], b1[0]);
+          mma16816<true>(o[2 * j + 1], hi_p, b0[1], b1[1]);
         }
       } else {
         const uint32_t row = 16 * ks + (lane & 15);
@@ -542,7 +559,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = 0; i < 2; ++i) {
           const int row = g + 8 * i;
           if (row >= mh) continue;
-          const float f = out_factor(m[i], M[i], l[i]);
+          const float f = out_factor<kE4m3>(m[i], M[i], l[i]);
           const int64_t at = (s_row0[cons.s] + static_cast<int64_t>(row / p.group)) * p.heads + cons.h * p.group + row % p.group;
           float y[16];
 #pragma unroll
@@ -604,48 +621,54 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   ok = __syncthreads_and(ok);
 
   // ---------------------------------------------------------------- items over several warps of this CTA
-  // `cons` is the last item of the warp's units; its first one it finds again.
+  // `cons` is the last item of the warp's units; its first one it finds again.  The warps that have some of an item
+  // share its row heads.
   float* ws_part = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
   if (ok && lo < hi) {
     At first{};
     locate(lo, first);
-    const int64_t first_begin = lo - first.blk, first_end = first_begin + first.units;
-    const int64_t last_begin = (hi - 1) - cons.blk, last_end = last_begin + cons.units;
-    // This warp's first item began before it, and no later warp of the CTA has some of it: join what they have.
-    const bool joins = first_begin < lo && (first_end <= hi || hi == cta_hi);
-    // Its last item begins here and goes on in the next CTA.
-    const bool leaves = last_begin >= lo && last_end > hi && hi == cta_hi;
+    const bool same = first.s == cons.s && first.h == cons.h;
 #pragma unroll 1
-    for (int what = 0; what < 2; ++what) {
-      if (!(what == 0 ? joins : leaves)) continue;
+    for (int what = 0; what < (same ? 1 : 2); ++what) {
       const At& at = what == 0 ? first : cons;
-      const int64_t ib = what == 0 ? first_begin : last_begin, ie = what == 0 ? first_end : last_end;
-      int w0 = warp;   // the first warp of the CTA with some of the item
-      while (w0 > 0 && begin_of(gw - (warp - w0)) > ib) --w0;
+      const int64_t ib = what == 0 ? lo - first.blk : hi - 1 - cons.blk, ie = ib + at.units;
+      if (ib >= lo && ie <= hi) continue;
+      int w0 = warp, w1 = warp;   // the first and the last warp of the CTA with some of it
+      while (w0 > 0 && edge_of(w0) > ib) --w0;
+      while (w1 < kW - 1 && edge_of(w1 + 1) < min(ie, cta_hi)) ++w1;
+      const int parts = w1 - w0 + 1;
       const bool complete = ib >= cta_lo && ie <= cta_hi;
+      const bool w0_head = edge_of(w0) > ib;      // (the later ones have it in their head slots)
       const int n = s_count[at.s], mh = n * p.group;
       float* out_slot = ws_part + (ib < cta_lo ? 0 : kSlotFloats);
+      const float* mine = slot_of(w0 + min(lane, parts - 1), min(lane, parts - 1) > 0 || w0_head) + kM * kSlotStride;
       uint32_t which = 0;
-      for (int row = 0; row < mh; ++row) {
-        float jm = -INFINITY, jM = -INFINITY;
-        for (int w = w0; w <= warp; ++w) {
-          const float* sl = slot_of(w, begin_of(gw - warp + w) > ib);
-          jm = fmaxf(jm, sl[kM * kSlotStride + row]);
-          jM = fmaxf(jM, sl[kM * kSlotStride + kM + row]);
+      for (int row = warp - w0; row < mh; row += parts) {
+        const float pm = lane < parts ? mine[row] : -INFINITY, pM = lane < parts ? mine[kM + row] : -INFINITY;
+        float jm = pm, jM = pM;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) {
+          jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, d));
+          jM = fmaxf(jM, __shfl_xor_sync(0xffffffffu, jM, d));
         }
-        float jl = 0.f;
+        jm = __shfl_sync(0xffffffffu, jm, 0), jM = __shfl_sync(0xffffffffu, jM, 0);
+        const float f = rescale(pM, jM);
+        float jl = lane < parts ? mine[2 * kM + row] * rescale(pm, jm) : 0.f;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, d);
+        jl = __shfl_sync(0xffffffffu, jl, 0);
         float2 jo = make_float2(0.f, 0.f);
-        for (int w = w0; w <= warp; ++w) {
-          const float* sl = slot_of(w, begin_of(gw - warp + w) > ib);
-          const float2 part = *reinterpret_cast<const float2*>(sl + row * kSlotStride + 2 * lane);
-          const float f = rescale(sl[kM * kSlotStride + kM + row], jM);
-          jl += sl[kM * kSlotStride + 2 * kM + row] * rescale(sl[kM * kSlotStride + row], jm);
-          jo.x += f * part.x, jo.y += f * part.y;
+#pragma unroll 4
+        for (int w = 0; w < parts; ++w) {
+          const float2 part =
+              *reinterpret_cast<const float2*>(slot_of(w0 + w, w > 0 || w0_head) + row * kSlotStride + 2 * lane);
+          const float fw = __shfl_sync(0xffffffffu, f, w);
+          jo.x = fmaf(fw, part.x, jo.x), jo.y = fmaf(fw, part.y, jo.y);
         }
         if (complete) {
           const int64_t o_at = (s_row0[at.s] + static_cast<int64_t>(row / p.group)) * p.heads + at.h * p.group + row % p.group;
-          const float f = out_factor(jm, jM, jl);
-          const float y0 = jl == 0.f ? 0.f : jo.x * f, y1 = jl == 0.f ? 0.f : jo.y * f;
+          const float of = out_factor<kE4m3>(jm, jM, jl);
+          const float y0 = jl == 0.f ? 0.f : jo.x * of, y1 = jl == 0.f ? 0.f : jo.y * of;
           store_pair(p, o_at, 2 * lane, y0, y1);
           if (p.lse != nullptr && lane == 0) p.lse[o_at] = log_sum(jm, jl);
           if (__any_sync(0xffffffffu, (!(fabsf(y0) <= 3.4e38f) || !(fabsf(y1) <= 3.4e38f)) && jl == jl)) which |= 1u << row;
@@ -686,14 +709,16 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 // One CTA for each CTA of the step kernel: the item that begins in it and goes on, from the parts of this and the next
-// CTAs.  16 groups of 16 lanes: a group has a row head and every so manieth part.
-constexpr int kJoinThreads = 256;
+// CTAs.  16 groups of 16 lanes: first a group has a row head, its lanes the parts' maxima and sums; then a group has a
+// row head and every so manieth part, its lanes four elements of O each.
+constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16;
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
                                                                   const float* __restrict__ ws) {
   __shared__ float4 so[16][16];
-  __shared__ float sm[16][3];
+  __shared__ float factor[kM][kStepMaxGrid];
+  __shared__ float total[kM][3];
   __shared__ uint32_t wild;
   griddep_wait();
   const float* mine = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
@@ -701,33 +726,54 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   if (j.parts == 0) return;
   const int tid = threadIdx.x, grp = tid >> 4, sub = tid & 15;
   const int mh = j.n * p.group;
+  auto part_of = [&](int i) { return mine + static_cast<int64_t>(i) * kStepWsFloats + (i == 0 ? kSlotFloats : 0); };
+  if (tid == 0) wild = 0;
+  {
+    float pm[kJoinEach], pM[kJoinEach], pl[kJoinEach], m = -INFINITY, M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) {
+      const int i = sub + 16 * k;
+      const bool in = i < j.parts && grp < mh;
+      const float* st = part_of(in ? i : 0) + kM * kSlotStride + (in ? grp : 0);
+      pm[k] = in ? st[0] : -INFINITY, pM[k] = in ? st[kM] : -INFINITY, pl[k] = in ? st[2 * kM] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) m = fmaxf(m, pm[k]), M = fmaxf(M, pM[k]);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) {
+      l += pl[k] * rescale(pm[k], m);
+      if (sub + 16 * k < j.parts) factor[grp][sub + 16 * k] = rescale(pM[k], M);
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (sub == 0) total[grp][0] = m, total[grp][1] = M, total[grp][2] = l;
+  }
+  __syncthreads();
   int rows = 1;
   while (rows < mh) rows <<= 1;
   const int row = grp & (rows - 1), slices = 16 / rows;
-  if (tid == 0) wild = 0;
-  float m = -INFINITY, M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float pm, float pM, float pl, const float4 po) {
-    const float nm = fmaxf(m, pm), nM = fmaxf(M, pM);
-    l = l * rescale(m, nm) + pl * rescale(pm, nm);
-    const float f = rescale(M, nM), pf = rescale(pM, nM);
-    o.x = o.x * f + po.x * pf, o.y = o.y * f + po.y * pf, o.z = o.z * f + po.z * pf, o.w = o.w * f + po.w * pf;
-    m = nm, M = nM;
-  };
   if (row < mh) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = grp / rows; i < j.parts; i += slices) {
-      const float* sl = mine + static_cast<int64_t>(i) * kStepWsFloats + (i == 0 ? kSlotFloats : 0);
-      add(sl[kM * kSlotStride + row], sl[kM * kSlotStride + kM + row], sl[kM * kSlotStride + 2 * kM + row],
-          *reinterpret_cast<const float4*>(sl + row * kSlotStride + 4 * sub));
+      const float4 x = *reinterpret_cast<const float4*>(part_of(i) + row * kSlotStride + 4 * sub);
+      const float f = factor[row][i];
+      o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
     }
   }
   so[grp][sub] = o;
-  if (sub == 0) sm[grp][0] = m, sm[grp][1] = M, sm[grp][2] = l;
   __syncthreads();
   if (grp < rows && row < mh) {
-    for (int i = 1; i < slices; ++i) add(sm[grp + i * rows][0], sm[grp + i * rows][1], sm[grp + i * rows][2], so[grp + i * rows][sub]);
-    const float f = out_factor(m, M, l);
+    for (int i = 1; i < slices; ++i) {
+      const float4 x = so[grp + i * rows][sub];
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+    }
+    const float m = total[row][0], M = total[row][1], l = total[row][2], f = out_factor<kE4m3>(m, M, l);
     const int64_t at = (j.row0 + static_cast<int64_t>(row / p.group)) * p.heads + j.h * p.group + row % p.group;
     const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
     bool w = false;
@@ -759,7 +805,7 @@ static_assert(kStepWsFloats * 4 >= 2 * kSlotFloats * 4 + sizeof(StepJoin), "work
 
 int paged_step_grid(int64_t most_units, bool e4m3, int num_sms) {
   const int64_t w = e4m3 ? Cfg<true>::kWarps : Cfg<false>::kWarps;
-  return static_cast<int>(std::min<int64_t>(num_sms, (most_units + w - 1) / w));
+  return static_cast<int>(std::min<int64_t>(std::min(num_sms, kStepMaxGrid), (most_units + w - 1) / w));
 }
 
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,

@@ -1,5 +1,5 @@
-// The usual call of the decayed passes, the single-token step and the q/k norm
-// and rotation, from Python in about two microseconds: a decode step's kernel
+// The usual call of the decayed passes, the single-token step, the q/k norm
+// and rotation and the paged cache, from Python in about two microseconds: a decode step's kernel
 // takes less time than a dozen tensor attributes read through the
 // interpreter.  Each function here takes the arguments of its namesake in
 // spanla.py, already in order, and
@@ -33,6 +33,9 @@ decltype(&span_la_decay_pass) g_pass = nullptr;
 decltype(&span_la_decay_branches_from_state) g_fork = nullptr;
 decltype(&span_la_decay_step) g_step = nullptr;
 decltype(&span_la_qk_norm_rope) g_rope = nullptr;
+decltype(&span_la_kv_write) g_write = nullptr;
+decltype(&span_la_kv_read) g_read = nullptr;
+decltype(&span_la_softmax_paged) g_paged = nullptr;
 
 // (without the dispatcher: about 1 us less for a call that returns two tensors;
 // see usual_mode)
@@ -317,14 +320,168 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(addresses of span_la_decay_pass, .._branches_from_state, .._step, span_la_qk_norm_rope)
+// A paged cache: (k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale) into the library's struct.
+struct Cache {
+  span_la_kv_cache c{};
+  int dev = 0;
+  bool take(PyObject* ok, PyObject* ov, PyObject* ot, PyObject* ol, PyObject* oc, PyObject* oks, PyObject* ovs) {
+    const at::Tensor *k = tensor(ok), *v = tensor(ov), *table = tensor(ot), *len = tensor(ol);
+    if (!k || !v || !table || !len || !k->is_cuda() || k->dim() != 4) return false;
+    dev = c10::cuda::current_device();
+    const at::ScalarType type = k->scalar_type();
+    if (k->get_device() != dev || !v->is_cuda() || v->get_device() != dev || v->scalar_type() != type || v->sizes() != k->sizes() ||
+        v->strides() != k->strides() || k->size(3) != 64 || k->stride(3) != 1 || k->size(0) > INT32_MAX || k->size(1) > INT32_MAX ||
+        k->size(2) > INT32_MAX || (type != at::kBFloat16 && type != at::kFloat8_e4m3fn))
+      return false;
+    if (table->dim() != 2 || table->scalar_type() != at::kInt || !table->is_cuda() || table->get_device() != dev ||
+        (table->size(1) > 1 && table->stride(1) != 1) || table->size(0) > INT32_MAX || table->size(1) > INT32_MAX)
+      return false;
+    const int64_t S = table->size(0);
+    if (len->dim() != 1 || len->size(0) != S || !contiguous_on(*len, dev, at::kInt)) return false;
+    if (oc != Py_None) {
+      const at::Tensor* cu = tensor(oc);
+      if (!cu || cu->dim() != 1 || cu->size(0) != S + 1 || !contiguous_on(*cu, dev, at::kInt)) return false;
+      c.row_cu = static_cast<const int32_t*>(cu->data_ptr());
+    }
+    if (type == at::kFloat8_e4m3fn) {
+      const at::Tensor *ks = tensor(oks), *vs = tensor(ovs);
+      if (!ks || !vs || ks->dim() != 3 || ks->scalar_type() != at::kByte || vs->scalar_type() != at::kByte || !ks->is_cuda() ||
+          !vs->is_cuda() || ks->get_device() != dev || vs->get_device() != dev || ks->sizes() != k->sizes().slice(0, 3) ||
+          vs->sizes() != ks->sizes() || vs->strides() != ks->strides() || ks->stride(2) != 1)
+        return false;
+      c.k_scale = static_cast<uint8_t*>(ks->data_ptr());
+      c.v_scale = static_cast<uint8_t*>(vs->data_ptr());
+      c.scale_page_stride = ks->stride(0);
+      c.scale_head_stride = ks->stride(1);
+      c.dtype = SPAN_LA_E4M3;
+    } else {
+      if (oks != Py_None || ovs != Py_None) return false;
+      c.dtype = SPAN_LA_BF16;
+    }
+    c.k = k->data_ptr();
+    c.v = v->data_ptr();
+    c.page_stride = k->stride(0);
+    c.head_stride = k->stride(1);
+    c.row_stride = k->stride(2);
+    c.num_pages = static_cast<int32_t>(k->size(0));
+    c.num_heads = static_cast<int32_t>(k->size(1));
+    c.page_rows = static_cast<int32_t>(k->size(2));
+    c.num_seqs = static_cast<int32_t>(S);
+    c.table_width = static_cast<int32_t>(table->size(1));
+    c.table_stride = S > 1 ? table->stride(0) : table->size(1);
+    c.page_table = static_cast<const int32_t*>(table->data_ptr());
+    c.seq_len = static_cast<const int32_t*>(len->data_ptr());
+    return true;
+  }
+};
+
+// Rows [T, H, 64] whose heads lie next to each other in a row, and their stride.
+bool packed_rows(const at::Tensor& t, int dev, int64_t* stride) {
+  if (t.dim() != 3 || t.size(2) != 64 || !t.is_cuda() || t.get_device() != dev || t.size(0) < 1 || t.size(1) < 1 ||
+      t.size(1) > INT32_MAX || t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != 64))
+    return false;
+  *stride = t.size(0) > 1 ? t.stride(0) : t.size(1) * 64;
+  return true;
+}
+
+// (k, v, k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale, stream): True when it is done
+PyObject* py_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Cache c;
+    cudaStream_t stream;
+    int64_t ks, vs;
+    if (n != 10 || !c.take(a[2], a[3], a[4], a[5], a[6], a[7], a[8])) return none();
+    const at::Tensor *k = tensor(a[0]), *v = tensor(a[1]);
+    if (!k || !v || !packed_rows(*k, c.dev, &ks) || !packed_rows(*v, c.dev, &vs) || k->sizes() != v->sizes() ||
+        k->size(1) != c.c.num_heads || k->scalar_type() != v->scalar_type() || !stream_of(a[9], c.dev, &stream))
+      return none();
+    const at::ScalarType type = k->scalar_type();
+    if (type != at::kBFloat16 && type != at::kFloat) return none();
+    span_la_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_write(k->data_ptr(), v->data_ptr(), ks, vs, k->size(0), type == at::kBFloat16 ? SPAN_LA_BF16 : SPAN_LA_F32, &c.c, stream);
+    Py_END_ALLOW_THREADS
+    if (st != SPAN_LA_OK) return PyLong_FromLong(st);
+    Py_RETURN_TRUE;
+  });
+}
+
+// (k_pages, v_pages, page_table, seq_len, row_cu, total_rows, k_scale, v_scale, bf16, stream): new outputs
+PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Cache c;
+    cudaStream_t stream;
+    if (n != 10 || !PyLong_CheckExact(a[5]) || !PyBool_Check(a[8]) || !c.take(a[0], a[1], a[2], a[3], a[4], a[6], a[7]) ||
+        !stream_of(a[9], c.dev, &stream))
+      return none();
+    const int64_t T = PyLong_AsLongLong(a[5]);
+    if (T < 1 || T > INT32_MAX) {
+      PyErr_Clear();
+      return none();
+    }
+    const bool bf16 = a[8] == Py_True;
+    at::Tensor outs[2];
+    for (at::Tensor& x : outs) x = new_tensor({T, c.c.num_heads, 64}, bf16 ? at::kBFloat16 : at::kFloat, c.dev);
+    span_la_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_read(&c.c, T, bf16 ? SPAN_LA_BF16 : SPAN_LA_F32, outs[0].data_ptr(), outs[1].data_ptr(), stream);
+    Py_END_ALLOW_THREADS
+    if (st != SPAN_LA_OK) return PyLong_FromLong(st);
+    return Py_BuildValue("(NN)", wrap(outs[0]), wrap(outs[1]));
+  });
+}
+
+// (q, k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale, max_rows, scale, out, lse, stream)
+PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Cache c;
+    cudaStream_t stream;
+    int64_t qs;
+    if (n != 13 || !PyFloat_Check(a[9]) || !c.take(a[1], a[2], a[3], a[4], a[5], a[6], a[7])) return none();
+    const at::Tensor* q = tensor(a[0]);
+    if (!q || !packed_rows(*q, c.dev, &qs) || q->scalar_type() != at::kBFloat16 || !stream_of(a[12], c.dev, &stream)) return none();
+    int64_t max_rows = c.c.row_cu == nullptr ? 1 : 0;
+    if (a[8] != Py_None) {
+      if (!PyLong_CheckExact(a[8])) return none();
+      max_rows = PyLong_AsLongLong(a[8]);
+      if (max_rows < 1 || max_rows > INT32_MAX) {
+        PyErr_Clear();
+        return none();
+      }
+    }
+    at::Tensor out;
+    if (a[10] == Py_None) {
+      out = new_tensor(q->sizes(), at::kBFloat16, c.dev);
+    } else {
+      const at::Tensor* t = tensor(a[10]);
+      if (t == nullptr || !like(*t, *q, c.dev)) return none();
+      out = *t;
+    }
+    float* lse = nullptr;
+    if (a[11] != Py_None) {
+      const at::Tensor* t = tensor(a[11]);
+      if (t == nullptr || t->dim() != 2 || t->size(0) != q->size(0) || t->size(1) != q->size(1) || !contiguous_on(*t, c.dev, at::kFloat))
+        return none();
+      lse = static_cast<float*>(t->data_ptr());
+    }
+    span_la_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_paged(q->data_ptr(), qs, q->size(0), static_cast<int32_t>(q->size(1)), &c.c, static_cast<int32_t>(max_rows),
+                 static_cast<float>(PyFloat_AS_DOUBLE(a[9])), out.data_ptr(), lse, stream);
+    Py_END_ALLOW_THREADS
+    return st != SPAN_LA_OK ? PyLong_FromLong(st) : wrap(out);
+  });
+}
+
+// bind(addresses of span_la_decay_pass, .._branches_from_state, .._step, span_la_qk_norm_rope, span_la_kv_write, .._read,
+// span_la_softmax_paged)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
     return nullptr;
   }
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  void* p[7];
+  for (int i = 0; i < 7; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is NULL");
@@ -335,6 +492,9 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_fork = reinterpret_cast<decltype(g_fork)>(p[1]);
   g_step = reinterpret_cast<decltype(g_step)>(p[2]);
   g_rope = reinterpret_cast<decltype(g_rope)>(p[3]);
+  g_write = reinterpret_cast<decltype(g_write)>(p[4]);
+  g_read = reinterpret_cast<decltype(g_read)>(p[5]);
+  g_paged = reinterpret_cast<decltype(g_paged)>(p[6]);
   Py_RETURN_NONE;
 }
 
@@ -344,6 +504,9 @@ PyMethodDef kMethods[] = {
     {"decay_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_fork)), METH_FASTCALL, nullptr},
     {"decay_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_step)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_rope)), METH_FASTCALL, nullptr},
+    {"kv_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_write)), METH_FASTCALL, nullptr},
+    {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_read)), METH_FASTCALL, nullptr},
+    {"softmax_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_paged)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -2010,15 +2010,18 @@ Bytes bytes_at(const void* p, int64_t n, const char* name) {
   return {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(p != nullptr ? n : 0), name};
 }
 
-// Refuses a call one of whose written ranges meets another range of it.
-span_la_status check_apart(const std::vector<Bytes>& written, const std::vector<Bytes>& read) {
-  auto meet = [](const Bytes& a, const Bytes& b) { return a.lo < b.hi && b.lo < a.hi; };
-  for (size_t i = 0; i < written.size(); ++i) {
-    for (size_t j = i + 1; j < written.size(); ++j)
-      if (meet(written[i], written[j])) return fail(SPAN_LA_ERR_INVALID, "%s overlaps %s", written[i].name, written[j].name);
-    for (const Bytes& r : read)
-      if (meet(written[i], r)) return fail(SPAN_LA_ERR_INVALID, "%s overlaps %s", written[i].name, r.name);
-  }
+// Some of them (a call has at most a dozen).
+struct Ranges {
+  Bytes at[12];
+  int n = 0;
+  void add(const Bytes& b) { at[n++] = b; }
+};
+
+// Refuses a call if `written` meets one of `others`.
+span_la_status check_apart(const Bytes& written, const Ranges& others, int from = 0) {
+  for (int i = from; i < others.n; ++i)
+    if (written.lo < others.at[i].hi && others.at[i].lo < written.hi)
+      return fail(SPAN_LA_ERR_INVALID, "%s overlaps %s", written.name, others.at[i].name);
   return SPAN_LA_OK;
 }
 
@@ -2054,7 +2057,7 @@ bool rows_meet(const Axis (&axes)[3], int64_t width, int64_t d, int level = 2) {
 
 // What every call on a paged cache checks of it, and its kernels' arguments; `written`: its pages are.
 span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t max_rows, bool written, KvArgs* a,
-                              std::vector<Bytes>* pages, std::vector<Bytes>* metadata) {
+                              Ranges* pages, Ranges* metadata) {
   if (c == nullptr) return fail(SPAN_LA_ERR_INVALID, "cache is NULL");
   if (c->dtype != SPAN_LA_BF16 && c->dtype != SPAN_LA_E4M3)
     return fail(SPAN_LA_ERR_UNSUPPORTED, "cache dtype %d not supported", c->dtype);
@@ -2110,13 +2113,15 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
     if (c->row_cu != nullptr && !word(c->row_cu)) return fail(SPAN_LA_ERR_INVALID, "row_cu must be 4-byte aligned");
   }
   const int64_t table_bytes = c->num_seqs > 0 ? ((c->num_seqs - 1) * (c->num_seqs > 1 ? c->table_stride : 0) + c->table_width) * 4 : 0;
-  *pages = {bytes_at(c->k, extent, "k pages"), bytes_at(c->v, extent, "v pages")};
+  pages->add(bytes_at(c->k, extent, "k pages"));
+  pages->add(bytes_at(c->v, extent, "v pages"));
   if (e4m3) {
-    pages->push_back(bytes_at(c->k_scale, scale_extent, "k_scale"));
-    pages->push_back(bytes_at(c->v_scale, scale_extent, "v_scale"));
+    pages->add(bytes_at(c->k_scale, scale_extent, "k_scale"));
+    pages->add(bytes_at(c->v_scale, scale_extent, "v_scale"));
   }
-  *metadata = {bytes_at(c->page_table, table_bytes, "page_table"), bytes_at(c->seq_len, c->num_seqs * int64_t(4), "seq_len"),
-               bytes_at(c->row_cu, (c->num_seqs + int64_t(1)) * 4, "row_cu")};
+  metadata->add(bytes_at(c->page_table, table_bytes, "page_table"));
+  metadata->add(bytes_at(c->seq_len, c->num_seqs * int64_t(4), "seq_len"));
+  metadata->add(bytes_at(c->row_cu, (c->num_seqs + int64_t(1)) * 4, "row_cu"));
   a->k = c->k;
   a->v = c->v;
   a->k_scale = c->k_scale;
@@ -2873,21 +2878,20 @@ span_la_status span_la_kv_write(const void* k, const void* v, int64_t k_row_stri
   return guarded([&]() -> span_la_status {
     if (dtype != SPAN_LA_BF16 && dtype != SPAN_LA_F32) return fail(SPAN_LA_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
     KvArgs a{};
-    std::vector<Bytes> pages, metadata;
+    Ranges pages, metadata;
     span_la_status st = check_kv_cache(cache, rows, rows, true, &a, &pages, &metadata);
     if (st != SPAN_LA_OK) return st;
     if (rows == 0 || a.seqs == 0) return SPAN_LA_OK;
     const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4;
     if ((st = check_rows("k", k, k_row_stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
     if ((st = check_rows("v", v, v_row_stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
-    metadata.push_back(bytes_at(k, rows_bytes(k_row_stride, rows, a.heads, esz), "k"));
-    metadata.push_back(bytes_at(v, rows_bytes(v_row_stride, rows, a.heads, esz), "v"));
+    metadata.add(bytes_at(k, rows_bytes(k_row_stride, rows, a.heads, esz), "k"));
+    metadata.add(bytes_at(v, rows_bytes(v_row_stride, rows, a.heads, esz), "v"));
     // (k and v pages, and their scales, may lie in between each other: check_kv_cache has looked)
-    for (const Bytes& x : pages)
-      if ((st = check_apart({x}, metadata)) != SPAN_LA_OK) return st;
-    if (pages.size() == 4)
-      for (int i = 0; i < 2; ++i)
-        if ((st = check_apart({pages[i]}, {pages[2], pages[3]})) != SPAN_LA_OK) return st;
+    for (int i = 0; i < pages.n; ++i)
+      if ((st = check_apart(pages.at[i], metadata)) != SPAN_LA_OK) return st;
+    for (int i = 0; i < 2; ++i)
+      if ((st = check_apart(pages.at[i], pages, 2)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     a.err = dev->err;
@@ -2904,16 +2908,18 @@ span_la_status span_la_kv_read(const span_la_kv_cache* cache, int64_t rows, int3
   return guarded([&]() -> span_la_status {
     if (dtype != SPAN_LA_BF16 && dtype != SPAN_LA_F32) return fail(SPAN_LA_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
     KvArgs a{};
-    std::vector<Bytes> pages, metadata;
+    Ranges pages, metadata;
     span_la_status st = check_kv_cache(cache, rows, rows, false, &a, &pages, &metadata);
     if (st != SPAN_LA_OK) return st;
     if (rows == 0 || a.seqs == 0) return SPAN_LA_OK;
     const int64_t esz = dtype == SPAN_LA_BF16 ? 2 : 4, stride = static_cast<int64_t>(a.heads) * kHeadDim;
     if ((st = check_rows("k_out", k_out, stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
     if ((st = check_rows("v_out", v_out, stride, rows, a.heads, esz)) != SPAN_LA_OK) return st;
-    metadata.insert(metadata.end(), pages.begin(), pages.end());
-    st = check_apart({bytes_at(k_out, rows * stride * esz, "k_out"), bytes_at(v_out, rows * stride * esz, "v_out")}, metadata);
-    if (st != SPAN_LA_OK) return st;
+    const Bytes out_k = bytes_at(k_out, rows * stride * esz, "k_out"), out_v = bytes_at(v_out, rows * stride * esz, "v_out");
+    for (int i = 0; i < pages.n; ++i) metadata.add(pages.at[i]);
+    if ((st = check_apart(out_v, metadata)) != SPAN_LA_OK) return st;
+    metadata.add(out_v);
+    if ((st = check_apart(out_k, metadata)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     a.err = dev->err;
@@ -2932,7 +2938,7 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     if (max_rows < 0) return fail(SPAN_LA_ERR_INVALID, "max_rows %d < 0", max_rows);
     if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(SPAN_LA_ERR_INVALID, "scale must be finite and >= 0");
     KvArgs a{};
-    std::vector<Bytes> pages, metadata;
+    Ranges pages, metadata;
     span_la_status st = check_kv_cache(cache, rows, max_rows == 0 ? rows : max_rows, false, &a, &pages, &metadata);
     if (st != SPAN_LA_OK) return st;
     if (num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % a.heads != 0 || num_q_heads / a.heads > 128)
@@ -2943,10 +2949,12 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     if ((st = check_rows("out", out, width, rows, num_q_heads, 2)) != SPAN_LA_OK) return st;
     if (lse_out != nullptr && (reinterpret_cast<uintptr_t>(lse_out) & 3u) != 0)
       return fail(SPAN_LA_ERR_INVALID, "lse_out must be 4-byte aligned");
-    metadata.insert(metadata.end(), pages.begin(), pages.end());
-    metadata.push_back(bytes_at(q, rows_bytes(q_row_stride, rows, num_q_heads, 2), "q"));
-    st = check_apart({bytes_at(out, rows * width * 2, "out"), bytes_at(lse_out, rows * num_q_heads * int64_t(4), "lse_out")}, metadata);
-    if (st != SPAN_LA_OK) return st;
+    const Bytes out_lse = bytes_at(lse_out, rows * num_q_heads * int64_t(4), "lse_out");
+    for (int i = 0; i < pages.n; ++i) metadata.add(pages.at[i]);
+    metadata.add(bytes_at(q, rows_bytes(q_row_stride, rows, num_q_heads, 2), "q"));
+    if ((st = check_apart(out_lse, metadata)) != SPAN_LA_OK) return st;
+    metadata.add(out_lse);
+    if ((st = check_apart(bytes_at(out, rows * width * 2, "out"), metadata)) != SPAN_LA_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     a.err = dev->err;

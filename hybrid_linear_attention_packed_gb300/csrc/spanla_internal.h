@@ -448,7 +448,7 @@ struct PagedAttn {
 // a launch: [s0, s0 + ns).  `ws`: kStepWsFloats for each of the `grid` CTAs; the join kernel, with the same grid, follows
 // where there is more than one.
 constexpr int kStepHeads = 16, kStepSeqs = 1024, kStepUnit = 32;
-constexpr int kStepWsFloats = 2432;
+constexpr int kStepWsFloats = 2432, kStepMaxGrid = 160;
 struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begins in the CTA and goes on in the next ones
   int32_t parts;                // CTAs with some of it, or 0
   int32_t s, h, n, len, row0;

@@ -192,7 +192,7 @@ def _bind_fast(lib) -> None:
         return
     _fastcall.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                      for f in (lib.span_la_decay_pass, lib.span_la_decay_branches_from_state, lib.span_la_decay_step,
-                               lib.span_la_qk_norm_rope)])
+                               lib.span_la_qk_norm_rope, lib.span_la_kv_write, lib.span_la_kv_read, lib.span_la_softmax_paged)])
     _fast = _fastcall
 
 
@@ -777,6 +777,12 @@ def span_la_kv_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
     int32: ``page_table`` [S, width], ``seq_len`` [S] (rows in the cache after the
     call) and ``row_cu`` [S + 1]: packed rows row_cu[s] .. row_cu[s + 1] are the
     last ones of sequence s (None: one row of each sequence)."""
+    if _fast is not None:
+        r = _fast.kv_write(k, v, k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale, stream)
+        if r is not None:
+            if r is not True:
+                _raise(_lib, r, "span_la_kv_write")
+            return
     lib = _lib or load_library()
     c, dev = _kv_cache(k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale)
     dt = _DTYPES.get(k.dtype)
@@ -799,6 +805,12 @@ def span_la_kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: to
     ``total_rows`` (default: the given outputs' rows, or one a sequence).  With a
     kept view's length in row_cu and seq_len, they are the view_k and view_v of
     :func:`span_la_softmax_branches_from_kv`."""
+    if _fast is not None and k_out is None and v_out is None and dtype in _DTYPES:
+        r = _fast.kv_read(k_pages, v_pages, page_table, seq_len, row_cu, total_rows, k_scale, v_scale, dtype is torch.bfloat16, stream)
+        if r is not None:
+            if type(r) is int:
+                _raise(_lib, r, "span_la_kv_read")
+            return r
     lib = _lib or load_library()
     c, dev = _kv_cache(k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale)
     if total_rows is None:
@@ -835,6 +847,12 @@ def span_la_softmax_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
     h the key head h // (Hq // H).  ``max_rows``: the most packed rows of a sequence
     where it is known (1 without ``row_cu``).  ``lse`` (fp32 [T, Hq], optional)
     receives the natural-log normaliser.  Returns [T, Hq, 64]."""
+    if _fast is not None:
+        r = _fast.softmax_paged(q, k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale, max_rows, scale, out, lse, stream)
+        if r is not None:
+            if type(r) is int:
+                _raise(_lib, r, "span_la_softmax_paged")
+            return r
     lib = _lib or load_library()
     c, dev = _kv_cache(k_pages, v_pages, page_table, seq_len, row_cu, k_scale, v_scale)
     qs = _packed("q", q, None, dev)
