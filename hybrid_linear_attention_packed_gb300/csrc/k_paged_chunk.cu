@@ -1,0 +1,775 @@
+// Softmax attention of chunks of new rows (more than 16 row heads of a sequence
+// and key head) over the paged cache, on the tensor cores (tcgen05).
+//
+// An item is up to two tiles of 128 row heads of one sequence and key head: rows
+// r of the sequence and the `group` query heads of the key head, as row head
+// r * group + g, so that grouped heads share the cached rows as consecutive rows
+// do.  Per block of 128 cached rows, each tile has
+//
+//     S = Q K^T                 (M128 N128 K64, fp32 in tensor memory)
+//     P = 2^(scale' (S - m))    (bf16, in tensor memory columns of its own)
+//     O += P V                  (M128 N64 K128, A = P, in tensor memory over the item's blocks)
+//
+// with a reference maximum m, raised (and O scaled) only when a row's maximum
+// exceeds it by a factor of 2^8 of its weights.  Every row head belongs to one
+// thread, which takes its 128 scores into registers at once: the next S is on its
+// way while the exponentials are computed, and the other tile's work fills what
+// is left.  (Columns of a tile: S 128, P 64, O 64; two tiles are all 512.)
+//
+// The blocks of all items are numbered through, and every CTA (one an SM) gets
+// the same number of consecutive ones, whatever the lengths, which are device
+// memory.  An item that goes over several CTAs leaves its parts (m, l, O) in the
+// workspace for the join kernel, which starts behind this one.
+//
+// 12 warps, 16 for e4m3 pages:
+//   0      loads, by TMA: Q of each item, K and V of each block, page by page
+//   1, 2   issue the products of tile 0 and of tile 1
+//   3      bf16 pages: zeroes V rows that do not exist (0 times what lies there may be NaN)
+//   4-7    softmax of tile 0, a thread a row head; 8-11 of tile 1
+//   12-15  e4m3 pages: K and V as they were loaded into bf16 tiles, a thread a row, times its power of two (exact)
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace spanla {
+namespace {
+
+constexpr uint32_t kTileBytes = kTileRows * 128;      // 128 rows of 64 bf16
+constexpr uint32_t kStageBytes = 2 * kTileBytes;      // K, V
+constexpr uint32_t kRawBytes = 2 * kTileRows * 64;    // of e4m3
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColP = 128, kColO = 192, kTileCols = 256;
+constexpr int kPartFloats = kChunkPartFloats;         // of a tile: O [128][64], then m and l of 128 row heads
+
+template <bool kE4m3>
+struct Cfg {
+  static constexpr int kThreads = kE4m3 ? 512 : 384;
+  static constexpr int kStages = kE4m3 ? 3 : 4;
+  static constexpr int kRaw = kE4m3 ? 2 : 0;
+  // Registers of a thread, by warps of four: they add up to what the block is launched with.
+  static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
+  static constexpr int kRegsFew = 56, kRegsConvert = 88, kRegsSoftmax = kE4m3 ? 184 : 224;
+  static_assert((kRegsFew + 2 * kRegsSoftmax + (kE4m3 ? kRegsConvert : 0)) * 128 <= kRegsLaunch * kThreads, "registers");
+  static constexpr uint32_t kQ = 0;                                   // [2 buffers][2 tiles]
+  static constexpr uint32_t kStage0 = 4 * kTileBytes;
+  static constexpr uint32_t kRaw0 = kStage0 + kStages * kStageBytes;
+  static constexpr uint32_t kScale0 = kRaw0 + kRaw * kRawBytes;       // [raw stage][K, V][128]
+  static constexpr uint32_t kSum = kScale0 + kRaw * 2 * kTileRows;
+  static constexpr uint32_t kLen = kSum + (kStepSeqs + 1) * 8;
+  static constexpr uint32_t kRow0 = kLen + kStepSeqs * 4;
+  static constexpr uint32_t kCount = kRow0 + kStepSeqs * 4;
+  static constexpr uint32_t kScan = kCount + kStepSeqs * 4;
+  static constexpr uint32_t kBar = kScan + 16 * 8;
+  // barriers
+  static constexpr int kFull = 0, kReady = kFull + (kE4m3 ? kRaw : kStages), kEmpty = kReady + kStages, kRawEmpty = kEmpty + kStages,
+                       kQFull = kRawEmpty + kRaw, kQFree = kQFull + 2, kSReady = kQFree + 2, kSFree = kSReady + 2, kPReady = kSFree + 2,
+                       kPvDone = kPReady + 2, kNumBars = kPvDone + 2;
+  static constexpr uint32_t kInfo = kBar + 8 * kNumBars;              // pages of a block that are there: bit i, rows 16 i ..
+  static constexpr uint32_t kTmemSlot = kInfo + 4 * (kStages + kRaw);
+  static constexpr uint32_t kBytes = kTmemSlot + 16;
+  static constexpr uint32_t kRequest = kBytes + 1024;
+  static_assert(kRequest <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ bool wait_or_flag(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
+  if (mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
+  atomicOr(err, code);
+  return false;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Rows of a sequence in an item (both tiles), and blocks of 128 cached rows of item b of a sequence of n new rows: as
+// many as its last row sees.
+__device__ __forceinline__ int32_t blocks_of(int32_t len, int32_t n, int32_t b, int32_t rows) {
+  return max(1, (len - n + min(n, (b + 1) * rows) + kTileRows - 1) >> 7);
+}
+
+// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's steps).
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    if (a >= m) sum += n * (n - 1) / 2 * (a / m), a %= m;
+    if (b >= m) sum += n * (b / m), b %= m;
+    const int64_t last = a * n + b;
+    if (last < m) break;
+    n = last / m;
+    b = last % m;
+    const int64_t x = m;
+    m = a, a = x;
+  }
+  return sum;
+}
+
+// Blocks of the items before item b (b up to their number).
+__device__ __forceinline__ int64_t blocks_before(int32_t len, int32_t n, int32_t b, int32_t rows) {
+  const int32_t items = (n + rows - 1) / rows, full = min(b, items - 1), first = len - n;   // full: items of `rows` rows
+  const int32_t one = min(full, max(0, kTileRows - first) / rows);                          // those of one block
+  int64_t sum = one + floor_sum(full - one, kTileRows, rows, static_cast<int64_t>(first) + static_cast<int64_t>(one + 1) * rows + kTileRows - 1);
+  if (b == items) sum += blocks_of(len, n, items - 1, rows);
+  return sum;
+}
+
+// A run of blocks [j0, j1) of one item.
+struct Run {
+  int s, h;
+  int32_t b, j0, j1, blocks;
+};
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, float* __restrict__ ws) {
+  using C = Cfg<kE4m3>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int64_t* sum = reinterpret_cast<int64_t*>(smem + C::kSum);
+  int32_t* s_len = reinterpret_cast<int32_t*>(smem + C::kLen);
+  int32_t* s_row0 = reinterpret_cast<int32_t*>(smem + C::kRow0);
+  int32_t* s_n = reinterpret_cast<int32_t*>(smem + C::kCount);
+  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(smem + C::kInfo);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
+  auto bar = [&](int slot) { return base + C::kBar + 8u * slot; };
+  const int32_t tile_rows = kTileRows / p.group, item_rows = 2 * tile_rows;
+
+  if (tid == 0) {
+    for (int i = 0; i < (kE4m3 ? C::kRaw : C::kStages); ++i) mbar_init(bar(C::kFull + i), 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bar(C::kReady + i), kE4m3 ? 128 : 1);
+      mbar_init(bar(C::kEmpty + i), 2);
+    }
+    for (int i = 0; i < C::kRaw; ++i) mbar_init(bar(C::kRawEmpty + i), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kQFull + i), 1);
+      mbar_init(bar(C::kQFree + i), 2);
+      mbar_init(bar(C::kSReady + i), 1);
+      mbar_init(bar(C::kSFree + i), 128);
+      mbar_init(bar(C::kPReady + i), 128);
+      mbar_init(bar(C::kPvDone + i), 1);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  // ---------------------------------------------------------------- the sequences' running sums of blocks
+  {
+    const int per = (ns + C::kThreads - 1) / C::kThreads, b = min(ns, tid * per), e = min(ns, b + per);
+    bool bad = false;
+    int64_t mine = 0;
+    for (int s = b; s < e; ++s) {
+      const SeqRows r = seq_rows(a, s0 + s, &bad);
+      const bool here = static_cast<int64_t>(r.n) * p.group > kStepHeads;
+      s_len[s] = r.len;
+      s_row0[s] = static_cast<int32_t>(r.row0);
+      s_n[s] = here ? r.n : 0;
+      sum[s] = mine;
+      mine += here ? blocks_before(r.len, r.n, (r.n + item_rows - 1) / item_rows, item_rows) * a.heads : 0;
+    }
+    if (bad) atomicOr(a.err, kErrSequence);
+    int64_t upto = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kScan);
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    for (int s = b; s < e; ++s) sum[s] += before;
+    if (tid == C::kThreads - 1) sum[ns] = before + mine;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+  }
+  const uint32_t tmem = *tmem_slot;
+  const int64_t U = sum[ns];
+  const int64_t nw = min(static_cast<int64_t>(gridDim.x), U);       // CTAs at work: each has a block at least
+  const int64_t lo = blockIdx.x < nw ? U * blockIdx.x / nw : U, hi = blockIdx.x + 1 < nw ? U * (blockIdx.x + 1) / nw : U;
+  // The run of blocks that unit `lo` begins (every warp finds it for itself).
+  Run first{};
+  if (lo < hi) {
+    int l = 0, r = ns;   // the last sequence that starts at lo or before
+    while (r - l > 1) {
+      const int mid = (l + r) >> 1;
+      if (sum[mid] <= lo) l = mid;
+      else r = mid;
+    }
+    first.s = l;
+    const int32_t len = s_len[l], n = s_n[l], items = (n + item_rows - 1) / item_rows;
+    const int64_t a_head = (sum[l + 1] - sum[l]) / a.heads, in = lo - sum[l];
+    first.h = static_cast<int>(in / a_head);
+    const int64_t rest = in - first.h * a_head;
+    int32_t at = 0, count = items;   // the last item that starts at `rest` or before, 32 at a time
+    while (count > 1) {
+      const int32_t step = (count + 31) / 32, mine = at + lane * step;
+      const int upto = __popc(__ballot_sync(0xffffffffu, mine < at + count && blocks_before(len, n, mine, item_rows) <= rest));
+      const int32_t from = max(upto - 1, 0) * step;
+      count = min(step, count - from);
+      at += from;
+    }
+    first.b = at;
+    first.blocks = blocks_of(len, n, at, item_rows);
+    first.j0 = static_cast<int32_t>(rest - blocks_before(len, n, at, item_rows));
+    first.j1 = static_cast<int32_t>(min(static_cast<int64_t>(first.blocks), first.j0 + (hi - lo)));
+  }
+  auto next_run = [&](Run& r, int64_t& left) {
+    left -= r.j1 - r.j0;
+    if (left <= 0) return;
+    if ((r.b + 1) * static_cast<int64_t>(item_rows) < s_n[r.s]) {
+      ++r.b;
+    } else {
+      r.b = 0;
+      if (++r.h == a.heads) {
+        r.h = 0;
+        do ++r.s;
+        while (sum[r.s + 1] == sum[r.s]);
+      }
+    }
+    r.blocks = blocks_of(s_len[r.s], s_n[r.s], r.b, item_rows);
+    r.j0 = 0;
+    r.j1 = static_cast<int32_t>(min(static_cast<int64_t>(r.blocks), left));
+  };
+  // Rows of tile x of a run's item.
+  auto rows_of = [&](const Run& r, int x) { return max(0, min(tile_rows, s_n[r.s] - r.b * item_rows - x * tile_rows)); };
+
+  Run r = first;
+  int64_t left = hi - lo;
+  if (warp < 4) {
+    regs_dec<C::kRegsFew>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ loads
+      constexpr int kRing = kE4m3 ? C::kRaw : C::kStages;
+      bool ok = true;
+      int g = 0, item = 0;
+      const int32_t box = min(a.page_rows, kTileRows), copies = kTileRows / box;   // copies: pages of a block, at most 8
+      for (; left > 0 && ok; next_run(r, left), ++item) {
+        const int qb = item & 1;
+        const int32_t len = s_len[r.s], n_pages = (len + a.page_rows - 1) >> a.page_shift;
+        if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kQFree + qb), ((item >> 1) & 1) ^ 1, a.err, kErrTimeoutMma))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const int tiles = rows_of(r, 1) > 0 ? 2 : 1;
+          mbar_arrive_expect_tx(bar(C::kQFull + qb), tiles * tile_rows * p.group * 128);
+          for (int x = 0; x < tiles; ++x)
+            tma_load_3d(base + C::kQ + (2 * qb + x) * kTileBytes, &tm_q, bar(C::kQFull + qb), 0, r.h * p.group,
+                        s_row0[r.s] + r.b * item_rows + x * tile_rows);
+        }
+        int win0 = -64;
+        int32_t win = -1;   // lane i: page win0 + i of the sequence
+        for (int32_t j = r.j0; j < r.j1 && ok; ++j, ++g) {
+          const int st = g % kRing;
+          if (!__all_sync(0xffffffffu, wait_or_flag(bar((kE4m3 ? C::kRawEmpty : C::kEmpty) + st), ((g / kRing) & 1) ^ 1, a.err, kErrTimeoutMma))) {
+            ok = false;
+            break;
+          }
+          const int32_t page0 = (j * kTileRows) >> a.page_shift;
+          if (page0 < win0 || page0 + copies > win0 + 32) {
+            win0 = page0;
+            win = page0 + lane < n_pages ? a.table[(s0 + r.s) * a.table_stride + page0 + lane] : 0;
+            if (win < 0 || win >= a.pages) {
+              atomicOr(a.err, kErrPage);
+              win = -1;
+            }
+          }
+          const int32_t page = __shfl_sync(0xffffffffu, win, (page0 - win0 + lane) & 31);
+          const bool mine = lane < copies && page0 + lane < n_pages && page >= 0;
+          const uint32_t which = __ballot_sync(0xffffffffu, mine);
+          if (lane == 0) {
+            uint32_t there = 0;   // 16 rows a bit
+            for (int c = 0; c < copies; ++c)
+              if ((which >> c) & 1u) there |= ((1u << (box / 16)) - 1u) << (c * (box / 16));
+            info[st] = there;
+            const uint32_t bytes = __popc(which) * box * (kE4m3 ? 130u : 256u);
+            if (bytes != 0) mbar_arrive_expect_tx(bar(C::kFull + st), bytes);
+            else mbar_arrive(bar(C::kFull + st));
+          }
+          __syncwarp();
+          if (mine) {
+            const int32_t row = (j * kTileRows) & (a.page_rows - 1);   // (0 but in pages of 256 rows)
+            const uint32_t to = kE4m3 ? base + C::kRaw0 + st * kRawBytes : base + C::kStage0 + st * kStageBytes;
+            constexpr uint32_t kRow = kE4m3 ? 64 : 128;
+            tma_load_4d(to + lane * box * kRow, &tm_k, bar(C::kFull + st), 0, row, r.h, page);
+            tma_load_4d(to + kTileRows * kRow + lane * box * kRow, &tm_v, bar(C::kFull + st), 0, row, r.h, page);
+            if (kE4m3) {
+              const int64_t from = page * a.scale_page_stride + r.h * a.scale_head_stride + row;
+              const uint32_t sc = base + C::kScale0 + st * 2 * kTileRows + lane * box;
+              bulk_copy_g2s(sc, a.k_scale + from, box, bar(C::kFull + st));
+              bulk_copy_g2s(sc + kTileRows, a.v_scale + from, box, bar(C::kFull + st));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // Wait (bounded) for the loads in flight before the CTA can exit.
+      for (int u = max(0, g - kRing); u < g; ++u)
+        mbar_wait_bounded(bar(C::kFull + u % kRing), (u / kRing) & 1, ok ? kWaitLimitNs : 1000000ull);
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ V rows that do not exist; the join kernel's record
+      bool ok = true;
+      int g = 0;
+      ChunkJoin join{};
+      for (; left > 0 && ok; next_run(r, left)) {
+        const int32_t len = s_len[r.s];
+        if (!kE4m3) {
+          for (int32_t j = r.j0; j < r.j1; ++j, ++g) {
+            const int st = g % C::kStages;
+            if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kFull + st), (g / C::kStages) & 1, a.err, kErrTimeoutTma))) {
+              ok = false;
+              break;
+            }
+            const uint32_t there = info[st];
+            const int32_t rows = len - j * kTileRows;
+            if (rows < kTileRows || there != 0xffu) {
+              uint8_t* v = smem + C::kStage0 + st * kStageBytes + kTileBytes;
+              for (int i = lane; i < kTileRows * 8; i += 32)
+                if ((i >> 3) >= rows || !((there >> (i >> 7)) & 1u)) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kReady + st));
+          }
+        }
+        if (r.j0 == 0 && r.j1 < r.blocks) {
+          const int64_t end = hi + (r.blocks - r.j1);   // of the item's units
+          join.parts = static_cast<int32_t>((end * nw - 1) / U) - static_cast<int32_t>(blockIdx.x) + 1;
+          join.s = s0 + r.s;
+          join.h = r.h;
+          join.first = r.b * item_rows;
+          join.n = s_n[r.s];
+          join.len = len;
+          join.row0 = s_row0[r.s];
+        }
+      }
+      if (lane == 0 && gridDim.x > 1) {
+        if (!ok) join.parts = 0;
+        *reinterpret_cast<ChunkJoin*>(ws + blockIdx.x * kChunkWsFloats + 4 * kPartFloats) = join;
+      }
+    } else {
+      // ------------------------------------------------------------ products of tile x
+      const int x = warp - 1;
+      constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0), id_pv = idesc_bf16_f32(128, 64, 0, 1);
+      const uint32_t ts = tmem + x * kTileCols;
+      const int k_ready = kE4m3 ? C::kReady : C::kFull;
+      bool ok = true, pv_first = false;
+      int g = 0, gx = 0, item = 0, pv_stage = -1, pv_use = 0;   // pv_*: the block whose P V is still to be issued
+      auto issue_pv = [&]() -> bool {
+        if (pv_stage < 0) return true;
+        bool w = wait_or_flag(bar(C::kReady + pv_stage), pv_use & 1, a.err, kErrTimeoutTma);
+        if (w) w = wait_or_flag(bar(C::kPReady + x), (gx - 1) & 1, a.err, kErrTimeoutMma);
+        if (!__all_sync(0xffffffffu, w)) return false;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t v = base + C::kStage0 + pv_stage * kStageBytes + kTileBytes;
+          for (int kk = 0; kk < kTileRows / 16; ++kk)
+            mma_bf16_tmem_a(ts + kColO, ts + kColP + kk * 8, smem_desc_sw128(v + kk * 2048, kTileBytes, 1024), id_pv,
+                            (!pv_first || kk > 0) ? 1u : 0u);
+          mma_commit(bar(C::kPvDone + x));
+          mma_commit(bar(C::kEmpty + pv_stage));
+        }
+        __syncwarp();
+        pv_stage = -1;
+        return true;
+      };
+      for (; left > 0 && ok; next_run(r, left), ++item) {
+        const int qb = item & 1;
+        const bool here = rows_of(r, x) > 0;
+        if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kQFull + qb), (item >> 1) & 1, a.err, kErrTimeoutTma))) ok = false;
+        if (ok && !here) {
+          ok = issue_pv();
+          if (ok && lane == 0) mbar_arrive(bar(C::kQFree + qb));
+        }
+        const uint32_t q = base + C::kQ + (2 * qb + x) * kTileBytes;
+        for (int32_t j = r.j0; j < r.j1 && ok; ++j, ++g) {
+          const int st = g % C::kStages;
+          bool w = wait_or_flag(bar(k_ready + st), (g / C::kStages) & 1, a.err, kErrTimeoutTma);
+          if (here && w && gx > 0) w = wait_or_flag(bar(C::kSFree + x), (gx - 1) & 1, a.err, kErrTimeoutMma);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          if (!here) {
+            if (lane == 0) mbar_arrive(bar(C::kEmpty + st));
+            continue;
+          }
+          tc_fence_after_sync();
+          if (lane == 0) {
+            const uint32_t k = base + C::kStage0 + st * kStageBytes;
+            for (int kk = 0; kk < kHeadDim / 16; ++kk)
+              mma_bf16(ts, smem_desc_sw128(q + kk * 32, 16, 1024), smem_desc_sw128(k + kk * 32, 16, 1024), id_qk, kk > 0 ? 1u : 0u);
+            mma_commit(bar(C::kSReady + x));
+            if (j == r.j1 - 1) mma_commit(bar(C::kQFree + qb));
+          }
+          __syncwarp();
+          if (!issue_pv()) {
+            ok = false;
+            break;
+          }
+          pv_stage = st, pv_use = g / C::kStages, pv_first = j == r.j0;
+          ++gx;
+        }
+      }
+      if (ok) issue_pv();
+    }
+  } else if (warp < 12) {
+    // -------------------------------------------------------------- softmax of tile x
+    regs_inc<C::kRegsSoftmax>();
+    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t ts = tmem + x * kTileCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float c2 = p.scale * 1.4426950408889634f;
+    const float raise_margin = fminf(8.f / c2, 1e37f);
+    const int my_row = row / p.group, my_head = row % p.group;
+    bool ok = true;
+    int g = 0, gx = 0;
+    for (; left > 0 && ok; next_run(r, left)) {
+      const int32_t rows = rows_of(r, x);
+      if (rows == 0) {
+        g += r.j1 - r.j0;
+        continue;
+      }
+      const bool live = my_row < rows;
+      const int32_t len = s_len[r.s], n = s_n[r.s], in_seq = r.b * item_rows + x * tile_rows + my_row;
+      const int32_t seen = live ? max(0, len - n + in_seq + 1) : INT32_MAX;   // (who is no row head has nothing to mask)
+      float m_ref = -INFINITY, l = 0.f;
+      for (int32_t j = r.j0; j < r.j1; ++j, ++g, ++gx) {
+        const int st = g % C::kStages;
+        bool w = wait_or_flag(bar(C::kSReady + x), gx & 1, a.err, kErrTimeoutMma);
+        // (for `info`, long complete)
+        if (w) w = wait_or_flag(bar((kE4m3 ? C::kReady : C::kFull) + st), (g / C::kStages) & 1, a.err, kErrTimeoutTma);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        const uint32_t there = info[kE4m3 ? C::kRaw + st : st];
+        tc_fence_after_sync();
+        float sc[128];
+        {
+          uint32_t(&sr)[128] = reinterpret_cast<uint32_t(&)[128]>(sc);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32cols(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
+          tmem_ld_wait();
+        }
+        tc_fence_before_sync();
+        mbar_arrive(bar(C::kSFree + x));
+        const int32_t hi_col = seen - j * kTileRows;      // columns before it are seen
+        if (!__all_sync(0xffffffffu, hi_col >= kTileRows && there == 0xffu)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= hi_col || !((there >> (c / 16)) & 1u)) sc[c] = -INFINITY;
+        }
+        float mx0 = fmaxf(sc[0], sc[1]), mx1 = fmaxf(sc[2], sc[3]);
+#pragma unroll
+        for (int c = 4; c < 128; c += 4) {
+          mx0 = max3(mx0, sc[c], sc[c + 1]);
+          mx1 = max3(mx1, sc[c + 2], sc[c + 3]);
+        }
+        const float mx = fmaxf(mx0, mx1);
+        if (j == r.j0) {
+          m_ref = mx;   // (O starts with this block)
+        } else if (__any_sync(0xffffffffu, mx > m_ref + raise_margin)) {
+          if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kPvDone + x), (gx - 1) & 1, a.err, kErrTimeoutMma))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const float m_new = fmaxf(m_ref, mx);
+          const float f = m_new == m_ref ? 1.f : ex2((m_ref - m_new) * c2);   // 0 where m_ref = -inf
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t o[16];
+            tmem_ld_16cols(ts + kColO + 16 * h, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st_16cols(ts + kColO + 16 * h, o);
+          }
+          l = m_ref == -INFINITY ? 0.f : l * f;
+          m_ref = m_new;
+        }
+        const float neg = -(m_ref == -INFINITY ? 0.f : m_ref) * c2;
+        const uint64_t cc = f32x2(c2, c2), nn = f32x2(neg, neg);
+        uint64_t acc[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float y0, y1;
+            f32x2_split(fma_f32x2(f32x2(sc[32 * h + 2 * c], sc[32 * h + 2 * c + 1]), cc, nn), y0, y1);
+            y0 = ex2(y0), y1 = ex2(y1);
+            acc[c & 1] = add_f32x2(acc[c & 1], f32x2(y0, y1));
+            pk[c] = pack_bf16x2(y0, y1);
+          }
+          if (h == 0 && gx > 0) {   // P's last reader
+            if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kPvDone + x), (gx - 1) & 1, a.err, kErrTimeoutMma))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+          }
+          tmem_st_16cols(ts + kColP + 16 * h, pk);
+        }
+        if (!ok) break;
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(bar(C::kPReady + x));
+        float a0, a1, b0, b1;
+        f32x2_split(acc[0], a0, a1);
+        f32x2_split(acc[1], b0, b1);
+        l += (a0 + b0) + (a1 + b1);
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------ the end of the item, or of this CTA's part
+      if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kPvDone + x), (gx - 1) & 1, a.err, kErrTimeoutMma))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c2;
+      const bool complete = r.j0 == 0 && r.j1 == r.blocks;
+      const int64_t at = (s_row0[r.s] + static_cast<int64_t>(in_seq)) * p.heads + r.h * p.group + my_head;
+      float* part = ws + blockIdx.x * kChunkWsFloats + (2 * (r.j0 > 0 ? 0 : 1) + x) * kPartFloats;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool wild = false;
+      uint32_t o[2][32];
+      tmem_ld_32cols(ts + kColO, o[0]);
+      tmem_ld_32cols(ts + kColO + 32, o[1]);
+      tmem_ld_wait();
+      tc_fence_before_sync();
+      if (live && complete) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const float y0 = __uint_as_float(o[c >> 2][8 * (c & 3) + 2 * d]) * inv, y1 = __uint_as_float(o[c >> 2][8 * (c & 3) + 2 * d + 1]) * inv;
+            wild |= !(fabsf(y0) <= 3.4e38f) || !(fabsf(y1) <= 3.4e38f);
+            pk[d] = l == 0.f ? 0u : pack_bf16x2(y0, y1);
+          }
+          dst[c] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m2, 0.6931471805599453f, logf(l));
+      } else if (live) {
+        float4* dst = reinterpret_cast<float4*>(part + row * kHeadDim);
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          dst[c] = make_float4(__uint_as_float(o[c >> 3][4 * (c & 7)]), __uint_as_float(o[c >> 3][4 * (c & 7) + 1]),
+                               __uint_as_float(o[c >> 3][4 * (c & 7) + 2]), __uint_as_float(o[c >> 3][4 * (c & 7) + 3]));
+        part[kTileRows * kHeadDim + row] = m2;
+        part[kTileRows * kHeadDim + kTileRows + row] = l;
+      }
+      // Rows whose O came out infinite or NaN though the sum of weights is finite: once more from the cache, without
+      // the rows that they do not see.
+      uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
+      while (which != 0) {
+        const int i = __ffs(which) - 1;
+        which &= which - 1;
+        const int rr = quarter * 32 + i, in = r.b * item_rows + x * tile_rows + rr / p.group;
+        attend_row<kE4m3>(a, p, s0 + r.s, s_row0[r.s] + static_cast<int64_t>(in), r.h * p.group + rr % p.group, max(0, len - n + in + 1));
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- e4m3 rows into bf16 tiles
+    regs_dec<C::kRegsConvert>();
+    if (kE4m3) {
+      const int row = tid - 384;
+      bool ok = true;
+      int g = 0;
+      for (; left > 0 && ok; next_run(r, left)) {
+        const int32_t len = s_len[r.s];
+        for (int32_t j = r.j0; j < r.j1; ++j, ++g) {
+          const int rs = g % max(1, C::kRaw), st = g % C::kStages;
+          bool w = wait_or_flag(bar(C::kFull + rs), (g / max(1, C::kRaw)) & 1, a.err, kErrTimeoutTma);
+          if (w) w = wait_or_flag(bar(C::kEmpty + st), ((g / C::kStages) & 1) ^ 1, a.err, kErrTimeoutMma);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          const uint32_t there = info[rs];
+          const bool exists = j * kTileRows + row < len && ((there >> (row / 16)) & 1u);
+          if (row == 0) info[C::kRaw + st] = there;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t* from = smem + C::kRaw0 + rs * kRawBytes + kv * kTileRows * 64 + row * 64;
+            uint8_t* to = smem + C::kStage0 + st * kStageBytes + kv * kTileBytes + row * 128;
+            const float e = scale_of(smem[C::kScale0 + (rs * 2 + kv) * kTileRows + row]);
+            const uint64_t ee = f32x2(e, e);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 y = *reinterpret_cast<const uint4*>(from + ((c ^ ((row >> 1) & 3)) << 4));
+              const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+              uint32_t out[8];
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                const float2 v = from_e4m3x2((in[d >> 1] >> (16 * (d & 1))) & 0xffffu);
+                float v0, v1;
+                f32x2_split(mul_f32x2(f32x2(v.x, v.y), ee), v0, v1);
+                out[d] = exists ? pack_bf16x2(v0, v1) : 0u;
+              }
+              *reinterpret_cast<uint4*>(to + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+              *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(C::kRawEmpty + rs));
+          mbar_arrive(bar(C::kReady + st));
+        }
+      }
+    }
+  }
+
+  griddep_launch_dependents();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// CTA (c, y): 16 row heads (y & 7) of tile y >> 3 of the item that begins in CTA c of the chunk kernel and goes on, from
+// the parts of it and the next CTAs.  A group of 16 lanes has a row head: first its lanes the parts' maxima and sums,
+// then four elements of O each.
+constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16;
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
+                                                                  const float* __restrict__ ws) {
+  __shared__ float factor[16][kStepMaxGrid];
+  griddep_wait();
+  const float* mine = ws + blockIdx.x * kChunkWsFloats;
+  const ChunkJoin j = *reinterpret_cast<const ChunkJoin*>(mine + 4 * kPartFloats);
+  const int x = blockIdx.y >> 3, grp = threadIdx.x >> 4, sub = threadIdx.x & 15, row = (blockIdx.y & 7) * 16 + grp;
+  const int32_t tile_rows = kTileRows / p.group, in = j.first + x * tile_rows + row / p.group;
+  const bool live = j.parts > 0 && row / p.group < tile_rows && in < j.n;
+  if (!__syncthreads_or(live)) return;
+  auto part_of = [&](int i) { return mine + i * kChunkWsFloats + (2 * (i == 0 ? 1 : 0) + x) * kPartFloats; };
+  float pm[kJoinEach], pl[kJoinEach], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinEach; ++k) {
+    const int i = sub + 16 * k;
+    const bool has = live && i < j.parts;
+    const float* st = part_of(has ? i : 0) + kTileRows * kHeadDim + row;
+    pm[k] = has ? st[0] : -INFINITY, pl[k] = has ? st[kTileRows] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kJoinEach; ++k) m = fmaxf(m, pm[k]);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+  for (int k = 0; k < kJoinEach; ++k) {
+    const float f = pm[k] == m ? 1.f : pm[k] == -INFINITY ? 0.f : ex2(pm[k] - m);
+    l += pl[k] * f;
+    if (sub + 16 * k < j.parts) factor[grp][sub + 16 * k] = f;
+  }
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  __syncwarp();
+  bool wild = false;
+  const int head = j.h * p.group + row % p.group;
+  if (live) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < j.parts; ++i) {
+      const float4 y = *reinterpret_cast<const float4*>(part_of(i) + row * kHeadDim + 4 * sub);
+      const float f = factor[grp][i];
+      o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = (j.row0 + static_cast<int64_t>(in)) * p.heads + head;
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    wild = !(fabsf(o.x) <= 3.4e38f) || !(fabsf(o.y) <= 3.4e38f) || !(fabsf(o.z) <= 3.4e38f) || !(fabsf(o.w) <= 3.4e38f);
+    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * sub) =
+        l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    if (p.lse != nullptr && sub == 0) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+  }
+  const uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
+  __syncwarp();
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {   // the warp's two row heads
+    if (((which >> (16 * half)) & 0xffffu) == 0) continue;
+    const int rr = __shfl_sync(0xffffffffu, row, 16 * half), at = j.first + x * tile_rows + rr / p.group;
+    attend_row<kE4m3>(a, p, j.s, j.row0 + static_cast<int64_t>(at), j.h * p.group + rr % p.group, max(0, j.len - j.n + at + 1));
+  }
+}
+
+template <bool kE4m3>
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0,
+                   int ns, int grid, float* ws, cudaStream_t stream) {
+  using C = Cfg<kE4m3>;
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {   // the warps' shares of registers have to be those of the launch
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, paged_chunk_kernel<kE4m3>);
+    if (e != cudaSuccess) return e;
+    regs.store(attr.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3>, C::kRequest, done);
+  if (e != cudaSuccess) return e;
+  paged_chunk_kernel<kE4m3><<<grid, C::kThreads, C::kRequest, stream>>>(tm_q, tm_k, tm_v, a, p, s0, ns, ws);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream) {
+  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream) : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
+}
+
+cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 16);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return e4m3 ? cudaLaunchKernelEx(&cfg, chunk_join_kernel<true>, a, p, ws) : cudaLaunchKernelEx(&cfg, chunk_join_kernel<false>, a, p, ws);
+}
+
+}  // namespace spanla

@@ -140,14 +140,14 @@ span_la_status device_state(DeviceState** out) {
 constexpr int kKernelSplit = 0, kKernelChunk = 1, kKernelScan = 2, kKernelTile = 3,
               kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6, kKernelRecurState = 7,
               kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11,
-              kKernelSpanDecay = 12, kKernelKvWrite = 13, kKernelKvRead = 14, kKernelPagedRows = 15, kKernelPagedStep = 16,
-              kKernelPagedJoin = 17;
+              kKernelSpanDecay = 12, kKernelKvWrite = 13, kKernelKvRead = 14, kKernelPagedStep = 15, kKernelPagedJoin = 16,
+              kKernelPagedChunk = 17, kKernelChunkJoin = 18;
 const char* const kKernelNames[SPAN_LA_NUM_KERNELS] = {"split_f32", "chunk_state", "segmented_scan",
                                                        "tile_output", "span_state", "span_output",
                                                        "softmax_attn", "recur_state", "recur_scan",
                                                        "recur_output", "decay_step", "qk_norm_rope",
-                                                       "span_decay", "kv_write", "kv_read", "paged_rows",
-                                                       "paged_step", "paged_join"};
+                                                       "span_decay", "kv_write", "kv_read", "paged_step",
+                                                       "paged_join", "paged_chunk", "chunk_join"};
 
 std::atomic<int64_t> g_launches[SPAN_LA_NUM_KERNELS];
 std::atomic<bool> g_profiling{false};
@@ -2163,35 +2163,68 @@ span_la_status encode_pages(CUtensorMap* map, const void* base, const KvArgs& a,
   return SPAN_LA_OK;
 }
 
+// Boxes of the row heads of one tile and key head out of q: `group` heads of 128 / group rows.
+span_la_status encode_tile(CUtensorMap* map, const KvArgs& a, const PagedAttn& p) {
+  const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(p.heads), static_cast<cuuint64_t>(a.rows)};
+  const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.rows > 1 ? p.q_row_stride : p.heads * int64_t(kHeadDim)) * 2};
+  const cuuint32_t box[3] = {kHeadDim, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(kTileRows / p.group)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides, box, estride,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPAN_LA_ERR_CUDA, "cuTensorMapEncodeTiled of q failed (%d)", (int)r);
+  return SPAN_LA_OK;
+}
+
 // The launches of span_la_softmax_paged: sequences of few row heads and those of many each go to their kernel (they
 // tell them apart by the row offsets, which are in device memory).
 span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num_sms, cudaStream_t stream) {
   span_la_status st = SPAN_LA_OK;
+  CUtensorMap tm_q, tm_k, tm_v;
+  const bool step = p.group <= kStepHeads, chunk = a.max_rows * p.group > kStepHeads;
+  const int64_t units = std::max<int64_t>(1, (a.capacity + kStepUnit - 1) / kStepUnit);   // of a sequence and head, at most
+  const int step_grid = step ? paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), e4m3, num_sms) : 0;
+  const int chunk_grid = chunk ? std::min(num_sms, kStepMaxGrid) : 0;
+  const size_t bytes = std::max(static_cast<size_t>(step_grid > 1 ? step_grid : 0) * kStepWsFloats,
+                                static_cast<size_t>(chunk_grid > 1 ? chunk_grid : 0) * kChunkWsFloats) * sizeof(float);
+  float* ws = nullptr;
   cudaError_t e = cudaSuccess;
-  if (p.group <= kStepHeads) {
-    CUtensorMap tm_k, tm_v;
-    if ((st = encode_pages(&tm_k, a.k, a, e4m3, kStepUnit)) != SPAN_LA_OK) return st;
-    if ((st = encode_pages(&tm_v, a.v, a, e4m3, kStepUnit)) != SPAN_LA_OK) return st;
-    const int64_t units = std::max<int64_t>(1, (a.capacity + kStepUnit - 1) / kStepUnit);   // of a sequence and head, at most
-    const int grid = paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), e4m3, num_sms);
-    float* ws = nullptr;
-    if (grid > 1) {
-      const size_t bytes = static_cast<size_t>(grid) * kStepWsFloats * sizeof(float);
-      if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", bytes);
-      e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, stream);
-      if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", bytes, cudaGetErrorString(e));
-    }
-    for (int s0 = 0; s0 < a.seqs && e == cudaSuccess; s0 += kStepSeqs) {
-      const int ns = std::min(kStepSeqs, a.seqs - s0);
-      e = counted_launch(kKernelPagedStep, stream, [&] { return launch_paged_step(tm_k, tm_v, a, p, s0, ns, grid, e4m3, ws, stream); });
-      if (e == cudaSuccess && grid > 1)
-        e = counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, grid, e4m3, ws, stream); });
-    }
-    const cudaError_t ef = ws != nullptr ? cudaFreeAsync(ws, stream) : cudaSuccess;
-    if (e == cudaSuccess) e = ef;
+  if (bytes > 0) {
+    if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", bytes);
+    e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, stream);
+    if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", bytes, cudaGetErrorString(e));
   }
-  if (e == cudaSuccess && a.max_rows * p.group > kStepHeads)
-    e = counted_launch(kKernelPagedRows, stream, [&] { return launch_paged_rows(a, p, e4m3, stream); });
+  auto each = [&](auto&& launch) {   // at most kStepSeqs sequences a launch
+    for (int s0 = 0; s0 < a.seqs && e == cudaSuccess; s0 += kStepSeqs) e = launch(s0, std::min(kStepSeqs, a.seqs - s0));
+  };
+  if (step) {
+    st = encode_pages(&tm_k, a.k, a, e4m3, kStepUnit);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, kStepUnit);
+    if (st == SPAN_LA_OK)
+      each([&](int s0, int ns) {
+        cudaError_t x = counted_launch(kKernelPagedStep, stream,
+                                       [&] { return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, ws, stream); });
+        if (x == cudaSuccess && step_grid > 1)
+          x = counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, step_grid, e4m3, ws, stream); });
+        return x;
+      });
+  }
+  if (chunk && st == SPAN_LA_OK && e == cudaSuccess) {
+    st = encode_tile(&tm_q, a, p);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_k, a.k, a, e4m3, kTileRows);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, kTileRows);
+    if (st == SPAN_LA_OK)
+      each([&](int s0, int ns) {
+        cudaError_t x = counted_launch(kKernelPagedChunk, stream,
+                                       [&] { return launch_paged_chunk(tm_q, tm_k, tm_v, a, p, s0, ns, chunk_grid, e4m3, ws, stream); });
+        if (x == cudaSuccess && chunk_grid > 1)
+          x = counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(a, p, chunk_grid, e4m3, ws, stream); });
+        return x;
+      });
+  }
+  const cudaError_t ef = ws != nullptr ? cudaFreeAsync(ws, stream) : cudaSuccess;
+  if (e == cudaSuccess) e = ef;
+  if (st != SPAN_LA_OK) return st;
   return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "paged attention launch");
 }
 

@@ -434,7 +434,7 @@ struct KvRows {
 cudaError_t launch_kv_write(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream);
 
-// Softmax attention of packed rows over the cache (k_paged_attn.cu).
+// Softmax attention of packed rows over the cache.
 struct PagedAttn {
   const __nv_bfloat16* q;     // rows of `heads` heads, q_row_stride elements apart
   __nv_bfloat16* out;         // [rows][heads][64]
@@ -459,7 +459,17 @@ cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
                               int grid, bool e4m3, float* ws, cudaStream_t stream);
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
-cudaError_t launch_paged_rows(const KvArgs& a, const PagedAttn& p, bool e4m3, cudaStream_t stream);
+// Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles).
+constexpr int kChunkPartFloats = kTileRows * kHeadDim + 2 * kTileRows;
+constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8;
+struct alignas(16) ChunkJoin {
+  int32_t parts;
+  int32_t s, h, first, n, len, row0;   // first: the item's first row in the sequence's packed rows
+  int32_t pad;
+};
+cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream);
+cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
 
