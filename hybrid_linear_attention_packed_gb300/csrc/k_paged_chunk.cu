@@ -23,7 +23,7 @@
 //
 // 12 warps, 16 for e4m3 pages:
 //   0      loads, by TMA: Q of each item, K and V of each block, page by page
-//   1, 2   issue the products of tile 0 and of tile 1
+//   1, 2   issue the products, S and P V
 //   3      bf16 pages: zeroes V rows that do not exist (0 times what lies there may be NaN)
 //   4-7    softmax of tile 0, a thread a row head; 8-11 of tile 1
 //   12-15  e4m3 pages: K and V as they were loaded into bf16 tiles, a thread a row, times its power of two (exact)
@@ -48,7 +48,7 @@ struct Cfg {
   static constexpr int kRaw = kE4m3 ? 2 : 0;
   // Registers of a thread, by warps of four: they add up to what the block is launched with.
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
-  static constexpr int kRegsFew = 56, kRegsConvert = 88, kRegsSoftmax = kE4m3 ? 184 : 224;
+  static constexpr int kRegsFew = kE4m3 ? 72 : 88, kRegsConvert = 88, kRegsSoftmax = kE4m3 ? 176 : 208;
   static_assert((kRegsFew + 2 * kRegsSoftmax + (kE4m3 ? kRegsConvert : 0)) * 128 <= kRegsLaunch * kThreads, "registers");
   static constexpr uint32_t kQ = 0;                                   // [2 buffers][2 tiles]
   static constexpr uint32_t kStage0 = 4 * kTileBytes;
@@ -65,7 +65,8 @@ struct Cfg {
                        kQFull = kRawEmpty + kRaw, kQFree = kQFull + 2, kSReady = kQFree + 2, kSFree = kSReady + 2, kPReady = kSFree + 2,
                        kPvDone = kPReady + 2, kNumBars = kPvDone + 2;
   static constexpr uint32_t kInfo = kBar + 8 * kNumBars;              // pages of a block that are there: bit i, rows 16 i ..
-  static constexpr uint32_t kTmemSlot = kInfo + 4 * (kStages + kRaw);
+  static constexpr uint32_t kMissing = kInfo + 4 * (kStages + kRaw);
+  static constexpr uint32_t kTmemSlot = kMissing + 4;
   static constexpr uint32_t kBytes = kTmemSlot + 16;
   static constexpr uint32_t kRequest = kBytes + 1024;
   static_assert(kRequest <= 227 * 1024, "shared memory budget");
@@ -162,6 +163,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   int32_t* s_row0 = reinterpret_cast<int32_t*>(smem + C::kRow0);
   int32_t* s_n = reinterpret_cast<int32_t*>(smem + C::kCount);
   volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(smem + C::kInfo);
+  volatile uint32_t* some_missing = reinterpret_cast<volatile uint32_t*>(smem + C::kMissing);   // some block lacks pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
   auto bar = [&](int slot) { return base + C::kBar + 8u * slot; };
   const int32_t tile_rows = kTileRows / p.group, item_rows = 2 * tile_rows;
@@ -169,19 +171,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < (kE4m3 ? C::kRaw : C::kStages); ++i) mbar_init(bar(C::kFull + i), 1);
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(C::kReady + i), kE4m3 ? 128 : 1);
-      mbar_init(bar(C::kEmpty + i), 2);
+      mbar_init(bar(C::kReady + i), kE4m3 ? 4 : 1);
+      mbar_init(bar(C::kEmpty + i), 1);
     }
-    for (int i = 0; i < C::kRaw; ++i) mbar_init(bar(C::kRawEmpty + i), 128);
+    for (int i = 0; i < C::kRaw; ++i) mbar_init(bar(C::kRawEmpty + i), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kQFull + i), 1);
-      mbar_init(bar(C::kQFree + i), 2);
+      mbar_init(bar(C::kQFree + i), 1);
       mbar_init(bar(C::kSReady + i), 1);
       mbar_init(bar(C::kSFree + i), 128);
       mbar_init(bar(C::kPReady + i), 128);
       mbar_init(bar(C::kPvDone + i), 1);
     }
     fence_mbar_init();
+    *some_missing = 0;
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -190,6 +193,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  griddep_launch_dependents();   // (the join kernel's CTAs wait for this grid's end)
   // ---------------------------------------------------------------- the sequences' running sums of blocks
   {
     const int per = (ns + C::kThreads - 1) / C::kThreads, b = min(ns, tid * per), e = min(ns, b + per);
@@ -321,6 +325,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int c = 0; c < copies; ++c)
               if ((which >> c) & 1u) there |= ((1u << (box / 16)) - 1u) << (c * (box / 16));
             info[st] = there;
+            if (there != 0xffu) *some_missing = 1;
             const uint32_t bytes = __popc(which) * box * (kE4m3 ? 130u : 256u);
             if (bytes != 0) mbar_arrive_expect_tx(bar(C::kFull + st), bytes);
             else mbar_arrive(bar(C::kFull + st));
@@ -386,71 +391,68 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!ok) join.parts = 0;
         *reinterpret_cast<ChunkJoin*>(ws + blockIdx.x * kChunkWsFloats + 4 * kPartFloats) = join;
       }
-    } else {
-      // ------------------------------------------------------------ products of tile x
-      const int x = warp - 1;
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ products, issued by one lane: S by warp 1, P V by warp 2
+      // Apart, because the S that a softmax warp needs next may be issued as soon as it has taken the last one, while
+      // the P V in between waits for its exponentials: with both from one warp in turn, S came 650 cycles late.  (The
+      // loops are unrolled and the descriptors' low words counted up; built for each product, on a scheduler shared
+      // with busy warps, the issue took twice as long as the products.)
       constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0), id_pv = idesc_bf16_f32(128, 64, 0, 1);
-      const uint32_t ts = tmem + x * kTileCols;
-      const int k_ready = kE4m3 ? C::kReady : C::kFull;
-      bool ok = true, pv_first = false;
-      int g = 0, gx = 0, item = 0, pv_stage = -1, pv_use = 0;   // pv_*: the block whose P V is still to be issued
-      auto issue_pv = [&]() -> bool {
-        if (pv_stage < 0) return true;
-        bool w = wait_or_flag(bar(C::kReady + pv_stage), pv_use & 1, a.err, kErrTimeoutTma);
-        if (w) w = wait_or_flag(bar(C::kPReady + x), (gx - 1) & 1, a.err, kErrTimeoutMma);
-        if (!__all_sync(0xffffffffu, w)) return false;
-        tc_fence_after_sync();
-        if (lane == 0) {
-          const uint32_t v = base + C::kStage0 + pv_stage * kStageBytes + kTileBytes;
-          for (int kk = 0; kk < kTileRows / 16; ++kk)
-            mma_bf16_tmem_a(ts + kColO, ts + kColP + kk * 8, smem_desc_sw128(v + kk * 2048, kTileBytes, 1024), id_pv,
-                            (!pv_first || kk > 0) ? 1u : 0u);
-          mma_commit(bar(C::kPvDone + x));
-          mma_commit(bar(C::kEmpty + pv_stage));
+      bool ok = true;
+      int st = 0, item = 0;
+      uint32_t use = 0, gx[2] = {0, 0};      // use: of the ring, st: its stage; gx: blocks of each tile
+      if (warp == 1) {
+        const uint64_t d_q = smem_desc_sw128(base + C::kQ, 16, 1024), d_k = smem_desc_sw128(base + C::kStage0, 16, 1024);
+        const uint32_t b_k = bar(kE4m3 ? C::kReady : C::kFull);
+        for (; left > 0 && ok; next_run(r, left), ++item) {
+          const int qb = item & 1, tiles = rows_of(r, 1) > 0 ? 2 : 1;
+          ok = wait_or_flag(bar(C::kQFull + qb), (item >> 1) & 1, a.err, kErrTimeoutTma);
+          const uint64_t q = d_q + qb * (2 * kTileBytes >> 4);
+          for (int32_t j = r.j0; j < r.j1 && ok; ++j) {
+            ok = wait_or_flag(b_k + 8 * st, use & 1, a.err, kErrTimeoutTma);
+            const uint64_t k = d_k + st * (kStageBytes >> 4);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x >= tiles || !ok) break;
+              if (gx[x] > 0) ok = wait_or_flag(bar(C::kSFree + x), (gx[x] - 1) & 1, a.err, kErrTimeoutMma);
+              if (!ok) break;
+              tc_fence_after_sync();
+#pragma unroll
+              for (int kk = 0; kk < kHeadDim / 16; ++kk)
+                mma_bf16(tmem + x * kTileCols, q + x * (kTileBytes >> 4) + kk * 2, k + kk * 2, id_qk, kk > 0 ? 1u : 0u);
+              mma_commit(bar(C::kSReady + x));
+              ++gx[x];
+            }
+            if (ok && j == r.j1 - 1) mma_commit(bar(C::kQFree + qb));
+            if (++st == C::kStages) st = 0, ++use;
+          }
         }
-        __syncwarp();
-        pv_stage = -1;
-        return true;
-      };
-      for (; left > 0 && ok; next_run(r, left), ++item) {
-        const int qb = item & 1;
-        const bool here = rows_of(r, x) > 0;
-        if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kQFull + qb), (item >> 1) & 1, a.err, kErrTimeoutTma))) ok = false;
-        if (ok && !here) {
-          ok = issue_pv();
-          if (ok && lane == 0) mbar_arrive(bar(C::kQFree + qb));
-        }
-        const uint32_t q = base + C::kQ + (2 * qb + x) * kTileBytes;
-        for (int32_t j = r.j0; j < r.j1 && ok; ++j, ++g) {
-          const int st = g % C::kStages;
-          bool w = wait_or_flag(bar(k_ready + st), (g / C::kStages) & 1, a.err, kErrTimeoutTma);
-          if (here && w && gx > 0) w = wait_or_flag(bar(C::kSFree + x), (gx - 1) & 1, a.err, kErrTimeoutMma);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
+      } else {
+        const uint64_t d_v = smem_desc_sw128(base + C::kStage0 + kTileBytes, kTileBytes, 1024);
+        for (; left > 0 && ok; next_run(r, left)) {
+          const int tiles = rows_of(r, 1) > 0 ? 2 : 1;
+          for (int32_t j = r.j0; j < r.j1 && ok; ++j) {
+            ok = wait_or_flag(bar(C::kReady + st), use & 1, a.err, kErrTimeoutTma);
+            const uint64_t v = d_v + st * (kStageBytes >> 4);
+            const uint32_t more = j > r.j0 ? 1u : 0u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x >= tiles || !ok) break;
+              ok = wait_or_flag(bar(C::kPReady + x), gx[x] & 1, a.err, kErrTimeoutMma);
+              if (!ok) break;
+              tc_fence_after_sync();
+#pragma unroll
+              for (int kk = 0; kk < kTileRows / 16; ++kk)
+                mma_bf16_tmem_a(tmem + x * kTileCols + kColO, tmem + x * kTileCols + kColP + kk * 8, v + kk * (2048 >> 4), id_pv,
+                                kk > 0 ? 1u : more);
+              mma_commit(bar(C::kPvDone + x));
+              ++gx[x];
+            }
+            if (ok) mma_commit(bar(C::kEmpty + st));   // (S of the block is done: P came of it)
+            if (++st == C::kStages) st = 0, ++use;
           }
-          if (!here) {
-            if (lane == 0) mbar_arrive(bar(C::kEmpty + st));
-            continue;
-          }
-          tc_fence_after_sync();
-          if (lane == 0) {
-            const uint32_t k = base + C::kStage0 + st * kStageBytes;
-            for (int kk = 0; kk < kHeadDim / 16; ++kk)
-              mma_bf16(ts, smem_desc_sw128(q + kk * 32, 16, 1024), smem_desc_sw128(k + kk * 32, 16, 1024), id_qk, kk > 0 ? 1u : 0u);
-            mma_commit(bar(C::kSReady + x));
-            if (j == r.j1 - 1) mma_commit(bar(C::kQFree + qb));
-          }
-          __syncwarp();
-          if (!issue_pv()) {
-            ok = false;
-            break;
-          }
-          pv_stage = st, pv_use = g / C::kStages, pv_first = j == r.j0;
-          ++gx;
         }
       }
-      if (ok) issue_pv();
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------- softmax of tile x
@@ -474,14 +476,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       float m_ref = -INFINITY, l = 0.f;
       for (int32_t j = r.j0; j < r.j1; ++j, ++g, ++gx) {
         const int st = g % C::kStages;
-        bool w = wait_or_flag(bar(C::kSReady + x), gx & 1, a.err, kErrTimeoutMma);
-        // (for `info`, long complete)
-        if (w) w = wait_or_flag(bar((kE4m3 ? C::kReady : C::kFull) + st), (g / C::kStages) & 1, a.err, kErrTimeoutTma);
-        if (!__all_sync(0xffffffffu, w)) {
+        if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kSReady + x), gx & 1, a.err, kErrTimeoutMma))) {
           ok = false;
           break;
         }
-        const uint32_t there = info[kE4m3 ? C::kRaw + st : st];
+        uint32_t there = 0xffu;
+        if (__any_sync(0xffffffffu, *some_missing != 0)) {   // (set before the block's loads were issued)
+          if (!__all_sync(0xffffffffu, wait_or_flag(bar((kE4m3 ? C::kReady : C::kFull) + st), (g / C::kStages) & 1, a.err, kErrTimeoutTma))) {
+            ok = false;
+            break;
+          }
+          there = info[kE4m3 ? C::kRaw + st : st];
+        }
         tc_fence_after_sync();
         float sc[128];
         {
@@ -491,20 +497,19 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           tmem_ld_wait();
         }
         tc_fence_before_sync();
-        mbar_arrive(bar(C::kSFree + x));
+        mbar_arrive(bar(C::kSFree + x));   // (by every thread: a warp barrier and one arrival took longer)
         const int32_t hi_col = seen - j * kTileRows;      // columns before it are seen
         if (!__all_sync(0xffffffffu, hi_col >= kTileRows && there == 0xffu)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c >= hi_col || !((there >> (c / 16)) & 1u)) sc[c] = -INFINITY;
         }
-        float mx0 = fmaxf(sc[0], sc[1]), mx1 = fmaxf(sc[2], sc[3]);
+        float mx4[4];
 #pragma unroll
-        for (int c = 4; c < 128; c += 4) {
-          mx0 = max3(mx0, sc[c], sc[c + 1]);
-          mx1 = max3(mx1, sc[c + 2], sc[c + 3]);
-        }
-        const float mx = fmaxf(mx0, mx1);
+        for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(sc[2 * c], sc[2 * c + 1]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], sc[c], sc[c + 1]);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         if (j == r.j0) {
           m_ref = mx;   // (O starts with this block)
         } else if (__any_sync(0xffffffffu, mx > m_ref + raise_margin)) {
@@ -530,27 +535,24 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const float neg = -(m_ref == -INFINITY ? 0.f : m_ref) * c2;
         const uint64_t cc = f32x2(c2, c2), nn = f32x2(neg, neg);
         uint64_t acc[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+        uint32_t pk[2][32];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float y0, y1;
-            f32x2_split(fma_f32x2(f32x2(sc[32 * h + 2 * c], sc[32 * h + 2 * c + 1]), cc, nn), y0, y1);
-            y0 = ex2(y0), y1 = ex2(y1);
-            acc[c & 1] = add_f32x2(acc[c & 1], f32x2(y0, y1));
-            pk[c] = pack_bf16x2(y0, y1);
-          }
-          if (h == 0 && gx > 0) {   // P's last reader
-            if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kPvDone + x), (gx - 1) & 1, a.err, kErrTimeoutMma))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-          }
-          tmem_st_16cols(ts + kColP + 16 * h, pk);
+        for (int c = 0; c < 64; ++c) {
+          float y0, y1;
+          f32x2_split(fma_f32x2(f32x2(sc[2 * c], sc[2 * c + 1]), cc, nn), y0, y1);
+          y0 = ex2(y0), y1 = ex2(y1);
+          acc[c & 1] = add_f32x2(acc[c & 1], f32x2(y0, y1));
+          pk[c >> 5][c & 31] = pack_bf16x2(y0, y1);
         }
-        if (!ok) break;
+        if (gx > 0) {   // P's last reader
+          if (!__all_sync(0xffffffffu, wait_or_flag(bar(C::kPvDone + x), (gx - 1) & 1, a.err, kErrTimeoutMma))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+        }
+        tmem_st_32cols(ts + kColP, pk[0]);
+        tmem_st_32cols(ts + kColP + 32, pk[1]);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(bar(C::kPReady + x));
@@ -634,37 +636,54 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           for (int kv = 0; kv < 2; ++kv) {
             const uint8_t* from = smem + C::kRaw0 + rs * kRawBytes + kv * kTileRows * 64 + row * 64;
             uint8_t* to = smem + C::kStage0 + st * kStageBytes + kv * kTileBytes + row * 128;
+            if (!exists) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(to + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
             const float e = scale_of(smem[C::kScale0 + (rs * 2 + kv) * kTileRows + row]);
             const uint64_t ee = f32x2(e, e);
+            uint4 in[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) in[c] = *reinterpret_cast<const uint4*>(from + ((c ^ ((row >> 1) & 3)) << 4));
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 y = *reinterpret_cast<const uint4*>(from + ((c ^ ((row >> 1) & 3)) << 4));
-              const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+              const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
               uint32_t out[8];
 #pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                const float2 v = from_e4m3x2((in[d >> 1] >> (16 * (d & 1))) & 0xffffu);
-                float v0, v1;
-                f32x2_split(mul_f32x2(f32x2(v.x, v.y), ee), v0, v1);
-                out[d] = exists ? pack_bf16x2(v0, v1) : 0u;
+              for (int d = 0; d < 4; ++d) {
+                uint32_t h[2];
+                half2_of_e4m3(w[d], h[0], h[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                  float v0, v1;
+                  f32x2_split(mul_f32x2(f32x2(v.x, v.y), ee), v0, v1);
+                  out[2 * d + i] = pack_bf16x2(v0, v1);
+                }
               }
               *reinterpret_cast<uint4*>(to + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
               *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(bar(C::kRawEmpty + rs));
-          mbar_arrive(bar(C::kReady + st));
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::kRawEmpty + rs));
+            mbar_arrive(bar(C::kReady + st));
+          }
         }
       }
     }
   }
 
-  griddep_launch_dependents();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  // The launches before it in the call work on other sequences, so it need not have waited for them; but what comes
+  // behind the call waits for it alone.
+  griddep_wait();
 }
 
 // CTA (c, y): 16 row heads (y & 7) of tile y >> 3 of the item that begins in CTA c of the chunk kernel and goes on, from
@@ -687,17 +706,22 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   float pm[kJoinEach], pl[kJoinEach], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int k = 0; k < kJoinEach; ++k) {
+    if (16 * k >= j.parts) break;
     const int i = sub + 16 * k;
     const bool has = live && i < j.parts;
     const float* st = part_of(has ? i : 0) + kTileRows * kHeadDim + row;
     pm[k] = has ? st[0] : -INFINITY, pl[k] = has ? st[kTileRows] : 0.f;
   }
 #pragma unroll
-  for (int k = 0; k < kJoinEach; ++k) m = fmaxf(m, pm[k]);
+  for (int k = 0; k < kJoinEach; ++k) {
+    if (16 * k >= j.parts) break;
+    m = fmaxf(m, pm[k]);
+  }
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
 #pragma unroll
   for (int k = 0; k < kJoinEach; ++k) {
+    if (16 * k >= j.parts) break;
     const float f = pm[k] == m ? 1.f : pm[k] == -INFINITY ? 0.f : ex2(pm[k] - m);
     l += pl[k] * f;
     if (sub + 16 * k < j.parts) factor[grp][sub + 16 * k] = f;
@@ -735,7 +759,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
 
 template <bool kE4m3>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0,
-                   int ns, int grid, float* ws, cudaStream_t stream) {
+                   int ns, int grid, float* ws, bool behind, cudaStream_t stream) {
   using C = Cfg<kE4m3>;
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> regs{0};
@@ -748,15 +772,25 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
   const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  paged_chunk_kernel<kE4m3><<<grid, C::kThreads, C::kRequest, stream>>>(tm_q, tm_k, tm_v, a, p, s0, ns, ws);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kRequest;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<kE4m3>, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
-                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream) {
-  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream) : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, bool behind, cudaStream_t stream) {
+  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, behind, stream)
+              : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, behind, stream);
 }
 
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {

@@ -84,11 +84,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four e4m3 values as two pairs of fp16.
-__device__ __forceinline__ void half2_of_e4m3(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(four));
-}
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -162,6 +157,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  griddep_launch_dependents();   // (the next kernels of the call wait for this grid's end, or need not)
   // ---------------------------------------------------------------- the sequences' running sums of units
   {
     const int per = (ns + kW * 32 - 1) / (kW * 32), b = min(ns, tid * per), e = min(ns, b + per);
@@ -617,7 +613,6 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (!ok) {   // wait (a little) for the loads in flight before the CTA can leave
     for (int64_t u = done; u < issued; ++u) mbar_wait_bounded(bar(static_cast<int>((u - lo) % kS)), static_cast<uint32_t>((u - lo) / kS) & 1u, 1000000ull);
   }
-  griddep_launch_dependents();
   ok = __syncthreads_and(ok);
 
   // ---------------------------------------------------------------- items over several warps of this CTA
@@ -720,6 +715,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   __shared__ float factor[kM][kStepMaxGrid];
   __shared__ float total[kM][3];
   __shared__ uint32_t wild;
+  griddep_launch_dependents();
   griddep_wait();
   const float* mine = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
   const StepJoin j = *reinterpret_cast<const StepJoin*>(mine + 2 * kSlotFloats);

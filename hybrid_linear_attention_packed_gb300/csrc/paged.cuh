@@ -69,6 +69,11 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
   return __half22float2(__half2(h));
 }
 
+// Four e4m3 values as two pairs of fp16.
+__device__ __forceinline__ void half2_of_e4m3(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(four));
+}
 // Row elements 2 * lane, 2 * lane + 1 of row `pos` of the cache, given its page.
 template <bool kE4m3>
 __device__ __forceinline__ float2 cached_pair(const KvArgs& a, const void* base, const uint8_t* scale, int32_t page, int32_t pos,

@@ -2185,8 +2185,8 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   const int64_t units = std::max<int64_t>(1, (a.capacity + kStepUnit - 1) / kStepUnit);   // of a sequence and head, at most
   const int step_grid = step ? paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), e4m3, num_sms) : 0;
   const int chunk_grid = chunk ? std::min(num_sms, kStepMaxGrid) : 0;
-  const size_t bytes = std::max(static_cast<size_t>(step_grid > 1 ? step_grid : 0) * kStepWsFloats,
-                                static_cast<size_t>(chunk_grid > 1 ? chunk_grid : 0) * kChunkWsFloats) * sizeof(float);
+  const size_t step_ws = align256(static_cast<size_t>(step_grid > 1 ? step_grid : 0) * kStepWsFloats * sizeof(float));
+  const size_t bytes = step_ws + static_cast<size_t>(chunk_grid > 1 ? chunk_grid : 0) * kChunkWsFloats * sizeof(float);
   float* ws = nullptr;
   cudaError_t e = cudaSuccess;
   if (bytes > 0) {
@@ -2213,12 +2213,15 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     st = encode_tile(&tm_q, a, p);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_k, a.k, a, e4m3, kTileRows);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, kTileRows);
+    float* cws = bytes > 0 ? ws + step_ws / sizeof(float) : nullptr;
+    const bool behind = step && step_grid > 1;   // (the join kernel lets it start early)
     if (st == SPAN_LA_OK)
       each([&](int s0, int ns) {
-        cudaError_t x = counted_launch(kKernelPagedChunk, stream,
-                                       [&] { return launch_paged_chunk(tm_q, tm_k, tm_v, a, p, s0, ns, chunk_grid, e4m3, ws, stream); });
+        cudaError_t x = counted_launch(kKernelPagedChunk, stream, [&] {
+          return launch_paged_chunk(tm_q, tm_k, tm_v, a, p, s0, ns, chunk_grid, e4m3, cws, behind && s0 == 0, stream);
+        });
         if (x == cudaSuccess && chunk_grid > 1)
-          x = counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(a, p, chunk_grid, e4m3, ws, stream); });
+          x = counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(a, p, chunk_grid, e4m3, cws, stream); });
         return x;
       });
   }

@@ -460,6 +460,7 @@ cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
 // Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles).
+// `behind`: behind the step kernels of the same call, whose end it need not wait for.
 constexpr int kChunkPartFloats = kTileRows * kHeadDim + 2 * kTileRows;
 constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8;
 struct alignas(16) ChunkJoin {
@@ -468,7 +469,7 @@ struct alignas(16) ChunkJoin {
   int32_t pad;
 };
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
-                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream);
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, bool behind, cudaStream_t stream);
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
