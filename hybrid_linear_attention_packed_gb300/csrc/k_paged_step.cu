@@ -4,11 +4,12 @@
 //
 // Bound by memory: every cached row and head is read once, 256 bytes of bf16 or
 // 130 of e4m3, for 256 multiply-adds a row head.  So the cached rows are cut into
-// units of 32, numbered through all sequences, key heads and rows, and every warp
-// of the card gets the same number of consecutive units, whatever the lengths: a
-// warp finds its first unit by the sequences' running sums, and streams its units
-// through a ring of its own, filled by TMA (its lane 0), without waiting for other
-// warps.  The lengths are device memory: every CTA sums them up for itself.
+// units of 8 KB (32 rows of bf16, 64 of e4m3), numbered through all sequences, key
+// heads and rows, and every warp of the card gets the same number of consecutive
+// units, whatever the lengths: a warp finds its first unit by the sequences'
+// running sums, and streams its units through a ring of its own, filled by TMA (its
+// lane 0), without waiting for other warps.  The lengths are device memory: every
+// CTA sums them up for itself.
 //
 // A unit: S = Q K^T (m16n8k16, the row heads as M), running maximum m and sum l of
 // each row head in registers, O += P V.  bf16 pages: P enters as two bf16 parts
@@ -17,7 +18,8 @@
 // for its row, then all but its least elements), the rows' powers of two go onto
 // the scores and the weights in fp32; the weights w_j = p_j 2^(e_j) have a running
 // maximum 2^M of their own and enter 2^15 times over it, so that fp16 holds them to
-// 2^-11 of each, or 2^-40 of the largest.
+// 2^-11 of each, or 2^-40 of the largest.  Products that add to the same sums stand
+// apart in the code: one behind the other they would wait for each other.
 //
 // A warp's first and last items may go on in other warps.  Those parts (m, M, l,
 // O) meet in shared memory for the warps of a CTA and then, for the items that go
@@ -29,34 +31,38 @@
 namespace spanla {
 namespace {
 
-constexpr int kUnit = kStepUnit;          // cached rows
-constexpr int kM = kStepHeads;            // row heads
+constexpr int kM = kStepHeads;            // row heads of an item, at most
 constexpr int kSlotStride = 72;           // floats from row head to row head of a part (72: no bank conflicts)
 
-// A part of an item: [16][72] floats of O, then m, M, l of 16 row heads.
+// A part of an item: [kM][72] floats of O, then m, M, l of kM row heads.
 constexpr int kSlotFloats = kM * kSlotStride + 3 * kM;
 
-template <bool kE4m3>
+// kTwo: up to 16 row heads, as 8 and 8 (else up to 8, and the products' second half is empty).
+template <bool kE4m3, bool kTwo>
 struct Cfg {
-  static constexpr int kWarps = kE4m3 ? 12 : 8;
-  static constexpr int kStages = kE4m3 ? 3 : 2;
+  static constexpr int kUnit = kE4m3 ? 64 : 32;                // cached rows
+  static constexpr int kWarps = 8;
+  // Three units of bf16 in flight a warp where there is room: with few units a warp, their latencies are the call.
+  static constexpr int kStages = kE4m3 || kTwo ? 2 : 3;
+  static constexpr int kRows = kTwo ? 16 : 8;                  // row heads of a part in shared memory
+  static constexpr int kSlot = kRows * kSlotStride + 3 * kM;   // its floats
   static constexpr uint32_t kRow = kE4m3 ? 64 : 128;           // bytes
   static constexpr uint32_t kHalf = kUnit * kRow;              // K or V of a unit
   static constexpr uint32_t kStage = 2 * kHalf;
   static constexpr uint32_t kRing = kStages * kStage;          // of a warp
-  static constexpr uint32_t kScales = kWarps * kRing;          // 2 x 32 bytes a stage
+  static constexpr uint32_t kScales = kWarps * kRing;          // 2 x kUnit bytes a stage
   static constexpr uint32_t kFactors = kScales + (kE4m3 ? kWarps * kStages * 2 * kUnit : 0);   // of a unit's rows, 8 bytes
   static constexpr uint32_t kHead = kFactors + (kE4m3 ? kWarps * kUnit * 8 : 0);
-  static constexpr uint32_t kSum = kHead + kWarps * kSlotFloats * 4;
+  static constexpr uint32_t kSum = kHead + kWarps * kSlot * 4;
   static constexpr uint32_t kLen = kSum + (kStepSeqs + 1) * 8;
   static constexpr uint32_t kRow0 = kLen + kStepSeqs * 4;
   static constexpr uint32_t kCount = kRow0 + kStepSeqs * 4;
-  static constexpr uint32_t kInfo = kCount + kStepSeqs;
-  static constexpr uint32_t kScan = kInfo + kWarps * kStages * 4;
-  static constexpr uint32_t kBar = (kScan + kWarps * 8 + 7) / 8 * 8;
+  static constexpr uint32_t kInfo = kCount + kStepSeqs;        // 8 bytes a stage: the rows that are there
+  static constexpr uint32_t kScan = kInfo + kWarps * kStages * 8;
+  static constexpr uint32_t kBar = kScan + kWarps * 8;
   static constexpr uint32_t kBytes = kBar + kWarps * kStages * 8;
   static constexpr uint32_t kRequest = kBytes + 1024;
-  static_assert(kRequest <= 227 * 1024 && kRing >= kSlotFloats * 4, "shared memory budget");
+  static_assert(kRequest <= 227 * 1024 && kRing >= kSlot * 4 && kInfo % 8 == 0 && kSum % 16 == 0 && kHead % 16 == 0, "shared memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -77,10 +83,10 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
 template <bool kHalfFloat>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (kHalfFloat)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
@@ -104,9 +110,12 @@ struct At {
   int32_t blk, units;  // unit of the item, units of the item
 };
 
-__device__ __forceinline__ int32_t units_of(int32_t len) { return max(1, (len + kUnit - 1) / kUnit); }
+// a / b, quickly where both fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
 
-// Output of row head m of an item, elements d0 .. d0 + 1.
+// Output of a row head: elements d, d + 1.
 __device__ __forceinline__ void store_pair(const PagedAttn& p, int64_t at, int d, float x, float y) {
   *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + d) = pack_bf16x2(x, y);
 }
@@ -134,12 +143,12 @@ __device__ __forceinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, u
   }
 }
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(Cfg<kE4m3>::kWarps * 32, 1)
+template <bool kE4m3, bool kTwo>
+__global__ void __launch_bounds__(Cfg<kE4m3, kTwo>::kWarps * 32, 1)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvArgs a,
                   const __grid_constant__ PagedAttn p, int s0, int ns, float* __restrict__ ws) {
-  using C = Cfg<kE4m3>;
-  constexpr int kW = C::kWarps, kS = C::kStages;
+  using C = Cfg<kE4m3, kTwo>;
+  constexpr int kW = C::kWarps, kS = C::kStages, kUnit = C::kUnit, kN = kUnit / 8, kR = kTwo ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -150,12 +159,15 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   int32_t* s_row0 = reinterpret_cast<int32_t*>(smem + C::kRow0);
   uint8_t* s_count = smem + C::kCount;
   auto bar = [&](int stage) { return base + C::kBar + 8u * (warp * kS + stage); };
+  auto units_of = [](int32_t len) { return max(1, (len + kUnit - 1) / kUnit); };
 
   if (lane == 0) {
     for (int i = 0; i < kS; ++i) mbar_init(bar(i), 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    if (warp == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
   }
   griddep_launch_dependents();   // (the next kernels of the call wait for this grid's end, or need not)
   // ---------------------------------------------------------------- the sequences' running sums of units
@@ -178,7 +190,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += x;
     }
-    int64_t* scan = reinterpret_cast<int64_t*>(smem + (C::kScan + 7) / 8 * 8);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kScan);
     if (lane == 31) scan[warp] = upto;
     __syncthreads();
     int64_t before = upto - mine;
@@ -189,9 +201,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   }
   const int64_t U = sum[ns];
   // ---------------------------------------------------------------- this warp's units
-  const int64_t nw = min(static_cast<int64_t>(gridDim.x) * kW, U);     // warps at work: each has a unit at least
-  auto begin_of = [&](int64_t w) { return w >= nw ? U : U * w / nw; };
-  const int64_t edge = begin_of(static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));   // lane w: of the CTA's warp w
+  // nw warps are at work, each has a unit at least: the first `more` have each + 1 of them, the others `each`.
+  const int64_t nw = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * kW, U));
+  const int64_t each = quotient(U, nw), more = U - each * nw;
+  const int64_t edge_w = min(nw, static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));
+  const int64_t edge = each * edge_w + min(edge_w, more);         // lane w: the first unit of the CTA's warp w
   auto edge_of = [&](int w) { return __shfl_sync(0xffffffffu, edge, w); };
   const int64_t lo = edge_of(warp), hi = edge_of(warp + 1), cta_lo = edge_of(0), cta_hi = edge_of(kW);
   auto locate = [&](int64_t x, At& at) {
@@ -204,7 +218,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     at.s = l;
     at.units = units_of(s_len[l]);
     const int64_t in = x - sum[l];
-    at.h = static_cast<int>(in / at.units);
+    at.h = static_cast<int>(quotient(in, at.units));
     at.blk = static_cast<int32_t>(in - static_cast<int64_t>(at.h) * at.units);
   };
   auto advance = [&](At& at) {
@@ -219,24 +233,27 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
   const uint32_t ring = base + warp * C::kRing;
   uint8_t* ring_p = smem + warp * C::kRing;
-  uint32_t* info = reinterpret_cast<uint32_t*>(smem + C::kInfo) + warp * kS;
+  uint64_t* info = reinterpret_cast<uint64_t*>(smem + C::kInfo) + warp * kS;
   float2* factors = reinterpret_cast<float2*>(smem + C::kFactors) + warp * kUnit;
   uint8_t* scales = smem + C::kScales + warp * kS * 2 * kUnit;
-  float* head_slot = reinterpret_cast<float*>(smem + C::kHead) + warp * kSlotFloats;
-  float* tail_slot = reinterpret_cast<float*>(ring_p);   // once the ring is done
+  // A part that began in an earlier warp stands in the head slot, one that goes on in later ones in the ring, which is
+  // done by then.
   auto slot_of = [&](int w, bool head) {
-    return head ? reinterpret_cast<float*>(smem + C::kHead) + w * kSlotFloats : reinterpret_cast<float*>(smem + w * C::kRing);
+    return head ? reinterpret_cast<float*>(smem + C::kHead) + w * C::kSlot : reinterpret_cast<float*>(smem + w * C::kRing);
   };
+  constexpr int kStats = C::kRows * kSlotStride;   // in a slot in shared memory: m, M and l behind O
 
   // ---------------------------------------------------------------- loads
+  constexpr uint64_t kAll = kUnit == 64 ? ~0ull : (1ull << (kUnit & 63)) - 1ull;
   const uint64_t policy = l2_evict_first_policy();
+  const int32_t box = min(a.page_rows, kUnit), copies = kUnit / box;   // copies: pages of a unit, at most 4
   int win_s = -1, win0 = 0;
   int32_t win = -1;        // lane i: page win0 + i of sequence win_s
   auto issue = [&](const At& at, int stage) {
     const int32_t len = s_len[at.s];
     const int32_t n_pages = (len + a.page_rows - 1) >> a.page_shift;
-    const int32_t first = (at.blk * kUnit) >> a.page_shift;       // (16-row pages: first and first + 1, first even)
-    if (at.s != win_s || first < win0 || first >= win0 + 32) {
+    const int32_t first = (at.blk * kUnit) >> a.page_shift;
+    if (at.s != win_s || first < win0 || first + copies > win0 + 32) {
       win_s = at.s;
       win0 = first;
       win = first + lane < n_pages ? a.table[(s0 + at.s) * a.table_stride + first + lane] : 0;
@@ -245,31 +262,32 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         win = -1;
       }
     }
-    const bool two = a.page_rows < kUnit;
-    const int32_t p0 = __shfl_sync(0xffffffffu, win, first - win0), p1 = __shfl_sync(0xffffffffu, win, (first - win0 + 1) & 31);
-    const bool has0 = first < n_pages && p0 >= 0, has1 = two ? first + 1 < n_pages && p1 >= 0 : has0;
+    const int32_t page = __shfl_sync(0xffffffffu, win, (first - win0 + lane) & 31);
+    const bool mine = lane < copies && first + lane < n_pages && page >= 0;
+    const uint32_t which = __ballot_sync(0xffffffffu, mine);
     if (lane == 0) {
-      info[stage] = (has0 ? 0xffffu : 0u) | (has1 ? 0xffff0000u : 0u);
-      const uint32_t st = ring + stage * C::kStage;
-      const int32_t rows = two ? 16 : kUnit;
-      const int copies = (has0 ? 1 : 0) + (two && has1 ? 1 : 0);
-      const uint32_t bytes = copies * rows * (2 * C::kRow + (kE4m3 ? 2 : 0));
-      if (bytes == 0) {
-        mbar_arrive(bar(stage));
-      } else {
-        mbar_arrive_expect_tx(bar(stage), bytes);
-        for (int c = 0; c < (two ? 2 : 1); ++c) {
-          if (!(c == 0 ? has0 : has1)) continue;
-          const int32_t page = c == 0 ? p0 : p1, row = two ? 0 : (at.blk * kUnit) & (a.page_rows - 1);
-          tma_load_4d(st + c * 16 * C::kRow, &tm_k, bar(stage), 0, row, at.h, page, policy);
-          tma_load_4d(st + C::kHalf + c * 16 * C::kRow, &tm_v, bar(stage), 0, row, at.h, page, policy);
-          if (kE4m3) {
-            const int64_t from = page * a.scale_page_stride + at.h * a.scale_head_stride + row;
-            const uint32_t to = smem_addr(scales) + stage * 2 * kUnit + c * 16;
-            bulk_copy_g2s(to, a.k_scale + from, rows, bar(stage));
-            bulk_copy_g2s(to + kUnit, a.v_scale + from, rows, bar(stage));
-          }
-        }
+      uint64_t there = kAll;
+      if (which != (1u << copies) - 1u) {
+        there = 0;
+        for (int c = 0; c < copies; ++c)
+          if ((which >> c) & 1u) there |= (box == 64 ? ~0ull : (1ull << box) - 1ull) << (c * box);
+      }
+      info[stage] = there;
+      const uint32_t bytes = __popc(which) * box * (2 * C::kRow + (kE4m3 ? 2 : 0));
+      if (bytes == 0) mbar_arrive(bar(stage));
+      else mbar_arrive_expect_tx(bar(stage), bytes);
+    }
+    __syncwarp();
+    if (mine) {
+      const int32_t row = (at.blk * kUnit) & (a.page_rows - 1);
+      const uint32_t st = ring + stage * C::kStage + lane * box * C::kRow;
+      tma_load_4d(st, &tm_k, bar(stage), 0, row, at.h, page, policy);
+      tma_load_4d(st + C::kHalf, &tm_v, bar(stage), 0, row, at.h, page, policy);
+      if (kE4m3) {
+        const int64_t from = page * a.scale_page_stride + at.h * a.scale_head_stride + row;
+        const uint32_t to = smem_addr(scales) + stage * 2 * kUnit + lane * box;
+        bulk_copy_g2s(to, a.k_scale + from, box, bar(stage));
+        bulk_copy_g2s(to + kUnit, a.v_scale + from, box, bar(stage));
       }
     }
     __syncwarp();
@@ -289,15 +307,16 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   // ---------------------------------------------------------------- units
   const float c2 = p.scale * 1.4426950408889634f;
   uint32_t qa[4][4];                  // Q fragments of the item
-  float qc[2] = {c2, c2};             // what turns a score of row g, g + 8 into powers of two
-  float o[8][4], m[2], M[2], l[2];
-  int32_t seen[2];                    // rows that row heads g, g + 8 see
+  float qc[kR];                       // what turns a score of row g, g + 8 into powers of two
+  float o[8][4], m[kR], M[kR], l[kR];
+  int32_t seen[kR];                   // rows that row heads g, g + 8 see
   int32_t first_hidden = 0;           // rows before it are seen by every row head
   bool ok = true, started_before = false;
   int64_t done = lo;
   bool new_item = true;
+  int stage = 0;
+  uint32_t phase = 0;
   while (done < hi) {
-    const int stage = static_cast<int>((done - lo) % kS);
     const int32_t len = s_len[cons.s];
     const int n = s_count[cons.s];
     if (new_item) {
@@ -305,6 +324,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int mh = n * p.group;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        if (i >= kR) {   // (rows 8 .. 15 of the products are none)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) qa[c][i] = qa[c][2 + i] = 0u;
+          continue;
+        }
         const int row = g + 8 * i, r = row / p.group;
         const bool live = row < mh;
         seen[i] = live ? len - n + r + 1 : 0;
@@ -340,6 +364,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
           qc[i] = c2 * (1.f / 16384.f) * __uint_as_float(static_cast<uint32_t>(e) << 23);
         } else {
+          qc[i] = c2;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * c + 2 * t) : 0u;
@@ -352,7 +377,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       new_item = false;
     }
-    if (!mbar_wait_bounded(bar(stage), static_cast<uint32_t>((done - lo) / kS) & 1u, kWaitLimitNs)) {
+    if (!mbar_wait_bounded(bar(stage), phase, kWaitLimitNs)) {
       atomicOr(a.err, kErrTimeoutTma);
       ok = false;
     }
@@ -363,141 +388,161 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t st = ring + stage * C::kStage;
     const uint32_t vt = st + C::kHalf;
     const int32_t j0 = cons.blk * kUnit;
-    const uint32_t pages_ok = info[stage];
     const int32_t left = len - j0;                              // rows of the unit that exist
-    const bool whole = left >= kUnit && pages_ok == 0xffffffffu;
-    uint32_t exist = pages_ok & (left >= kUnit ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u);
-    if (!whole && !((exist >> lane) & 1u)) {
+    const uint64_t exist = info[stage] & (left >= kUnit ? kAll : left <= 0 ? 0ull : (1ull << left) - 1ull);
+    const bool whole = exist == kAll;
+    if (!whole) {
       // What does not exist may hold anything; its weight is 0, and 0 times NaN is NaN.
-      uint4* row = reinterpret_cast<uint4*>(ring_p + stage * C::kStage + C::kHalf + lane * C::kRow);
+      for (int row = lane; row < kUnit; row += 32)
+        if (!((exist >> row) & 1ull)) {
+          uint4* v = reinterpret_cast<uint4*>(ring_p + stage * C::kStage + C::kHalf + row * C::kRow);
 #pragma unroll
-      for (int c = 0; c < static_cast<int>(C::kRow / 16); ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < static_cast<int>(C::kRow / 16); ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
       fence_proxy_async_smem();   // (the next load of this stage comes behind it)
+    }
+    if (kE4m3) {
+      // (what a row's powers of two do: the score's factor, the weight's logarithm)
+#pragma unroll
+      for (int k = 0; k < kUnit / 32; ++k) {
+        const uint8_t* sc = scales + stage * 2 * kUnit + lane + 32 * k;
+        const uint32_t v = sc[kUnit];
+        factors[lane + 32 * k] = make_float2(scale_of(sc[0]), v == 255 ? NAN : static_cast<float>(static_cast<int>(v) - 127));
+      }
     }
     __syncwarp();
 
     // S: x[i][0..1] of row head g, [2..3] of g + 8, cached rows col(i, 0), col(i, 1) of the unit.
-    float x[4][4];
+    float x[kN][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
-      if (kE4m3) {
-        // Column n of a block of 8 is cached row (n & 1 ? 3 - (t & 1) : t & 1) + 4 (t >> 1), t = n >> 1: with the
-        // 64-byte swizzle no two lanes' reads of K or V then meet in a bank.
-        const uint32_t row = i * 8 + ((g & 1) ? 3 - ((g >> 1) & 1) : (g >> 1) & 1) + 4 * (g >> 2);
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(st + row * 64 + ((t ^ ((row >> 1) & 3)) << 4)) : "memory");
+    for (int i = 0; i < kN; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+    // Column n of a block of 8 is (e4m3) cached row (n & 1 ? 3 - (t & 1) : t & 1) + 4 (t >> 1), t = n >> 1: with the
+    // 64-byte swizzle no two lanes' reads of K or V then meet in a bank.
+    const int f0 = kE4m3 ? (t & 1) + 4 * (t >> 1) : 2 * t, f1 = kE4m3 ? 3 - (t & 1) + 4 * (t >> 1) : 2 * t + 1;
+    if (kE4m3) {
+      const uint32_t in8 = ((g & 1) ? 3 - ((g >> 1) & 1) : (g >> 1) & 1) + 4 * (g >> 2);
+      const uint32_t at0 = st + in8 * 64 + ((t ^ ((in8 >> 1) & 3)) << 4);
+#pragma unroll
+      for (int half = 0; half < kN / 4; ++half) {
+        uint32_t w[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                       : "r"(at0 + (4 * half + i) * 512) : "memory");
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t b0, b1;
-          half2_of_e4m3(w[c], b0, b1);
-          mma16816<true>(x[i], qa[c], b0, b1);
-        }
-      } else {
-        const uint32_t row = i * 8 + (lane & 7);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t b[4];
-          ldsm4(st + row * 128 + (((4 * c + (lane >> 3)) ^ (lane & 7)) << 4), b);
-          mma16816<false>(x[i], qa[2 * c], b[0], b[1]);
-          mma16816<false>(x[i], qa[2 * c + 1], b[2], b[3]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            half2_of_e4m3(w[i][c], b0, b1);
+            mma16816<true>(x[4 * half + i], qa[c], b0, b1);
+          }
+        }
+      }
+    } else {
+      const uint32_t at0 = st + (lane & 7) * 128;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t b[kN][4];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) ldsm4(at0 + i * 1024 + (((4 * c + (lane >> 3)) ^ (lane & 7)) << 4), b[i]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) mma16816<false>(x[i], qa[2 * c + k], b[i][2 * k], b[i][2 * k + 1]);
         }
       }
     }
-    if (kE4m3) {
-      // (what a row's powers of two do: the score's factor, the weight's logarithm)
-      const uint8_t* sc = scales + stage * 2 * kUnit + lane;
-      const uint32_t v = sc[kUnit];
-      factors[lane] = make_float2(scale_of(sc[0]), v == 255 ? NAN : static_cast<float>(static_cast<int>(v) - 127));
-      __syncwarp();
-    }
-    const int f0 = kE4m3 ? (t & 1) + 4 * (t >> 1) : 2 * t, f1 = kE4m3 ? 3 - (t & 1) + 4 * (t >> 1) : 2 * t + 1;
-    // z: e4m3: the score with log2 of V's power of two, whose maximum is M + 15.
-    const bool two = n * p.group > 8;   // (else row heads g + 8 are none)
-    float z[4][4];
+    // z: e4m3: the score with log2 of V's power of two, whose maximum is M.
+    const bool two = kTwo && n * p.group > 8;   // (else row heads g + 8 are none)
+    float z[kN][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int r = 0; r < kR; ++r) {
+      if (r == 1 && !two) break;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= 2 && !two) continue;
-        if (kE4m3) {
-          const float2 sc = factors[i * 8 + ((c & 1) ? f1 : f0)];
-          x[i][c] = x[i][c] * qc[c >> 1] * sc.x;
-          z[i][c] = x[i][c] + sc.y;
-        } else {
-          x[i][c] *= c2;
+      for (int i = 0; i < kN; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          x[i][2 * r + c] *= qc[r];
+          if (kE4m3) {
+            const float2 sc = factors[i * 8 + (c ? f1 : f0)];
+            x[i][2 * r + c] *= sc.x;
+            z[i][2 * r + c] = x[i][2 * r + c] + sc.y;
+          }
         }
       }
     }
     if (!whole || j0 + kUnit > first_hidden) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int r = 0; r < kR; ++r) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int in = i * 8 + ((c & 1) ? f1 : f0);
-          if (!((exist >> in) & 1u) || j0 + in >= seen[c >> 1]) x[i][c] = z[i][c] = -INFINITY;
+        for (int i = 0; i < kN; ++i) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int in = i * 8 + (c ? f1 : f0);
+            if (!((exist >> in) & 1ull) || j0 + in >= seen[r]) x[i][2 * r + c] = z[i][2 * r + c] = -INFINITY;
+          }
         }
       }
     }
     // Running maxima.
-    float top[2] = {m[0], m[1]}, wtop[2] = {M[0], M[1]};
+    float top[kR], wtop[kR];
+    bool raised = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (i == 1 && !two) continue;
+    for (int r = 0; r < kR; ++r) {
+      top[r] = m[r], wtop[r] = M[r];
+      if (r == 1 && !two) break;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        top[i] = fmaxf(top[i], fmaxf(x[k][2 * i], x[k][2 * i + 1]));
-        if (kE4m3) wtop[i] = fmaxf(wtop[i], fmaxf(z[k][2 * i], z[k][2 * i + 1]));
+      for (int i = 0; i < kN; ++i) {
+        top[r] = fmaxf(top[r], fmaxf(x[i][2 * r], x[i][2 * r + 1]));
+        if (kE4m3) wtop[r] = fmaxf(wtop[r], fmaxf(z[i][2 * r], z[i][2 * r + 1]));
       }
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
-        if (kE4m3) wtop[i] = fmaxf(wtop[i], __shfl_xor_sync(0xffffffffu, wtop[i], d));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], d));
+        if (kE4m3) wtop[r] = fmaxf(wtop[r], __shfl_xor_sync(0xffffffffu, wtop[r], d));
       }
-      if (!kE4m3) wtop[i] = top[i];
+      if (!kE4m3) wtop[r] = top[r];
+      raised |= top[r] != m[r] || wtop[r] != M[r];
     }
-    if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1] || wtop[0] != M[0] || wtop[1] != M[1])) {
+    if (__any_sync(0xffffffffu, raised)) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] *= rescale(m[i], top[i]);
-        const float f = rescale(M[i], wtop[i]);
+      for (int r = 0; r < kR; ++r) {
+        l[r] *= rescale(m[r], top[r]);
+        const float f = rescale(M[r], wtop[r]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          o[j][2 * i] *= f;
-          o[j][2 * i + 1] *= f;
+          o[j][2 * r] *= f;
+          o[j][2 * r + 1] *= f;
         }
-        m[i] = top[i];
-        M[i] = wtop[i];
+        m[r] = top[r];
+        M[r] = wtop[r];
       }
     }
-    // Weights and O.
-    const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-    const float B0 = (M[0] == -INFINITY ? 0.f : M[0]) - 15.f, B1 = (M[1] == -INFINITY ? 0.f : M[1]) - 15.f;
+    // Weights and O, 16 cached rows at a time.
+    float bm[kR], bM[kR];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      uint32_t hi_p[4], lo_p[4];
+    for (int r = 0; r < kR; ++r) {
+      bm[r] = m[r] == -INFINITY ? 0.f : m[r];
+      bM[r] = (M[r] == -INFINITY ? 0.f : M[r]) - 15.f;
+    }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = 2 * ks + half;
-        float w[4];
+    for (int ks = 0; ks < kN / 2; ++ks) {
+      uint32_t hi_p[4] = {0u, 0u, 0u, 0u}, lo_p[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          w[c] = 0.f;
-          if (c >= 2 && !two) continue;
-          const float pw = ex2(x[i][c] - (c < 2 ? b0 : b1));
-          l[c >> 1] += pw;
-          w[c] = kE4m3 ? ex2(z[i][c] - (c < 2 ? B0 : B1)) : pw;
-        }
-        if (kE4m3) {
-          hi_p[2 * half] = half2_of(w[0], w[1]);
-          hi_p[2 * half + 1] = half2_of(w[2], w[3]);
-        } else {
+      for (int r = 0; r < kR; ++r) {
+        if (r == 1 && !two) break;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            hi_p[2 * half + r] = pack_bf16x2(w[2 * r], w[2 * r + 1]);
-            lo_p[2 * half + r] = pack_bf16x2(w[2 * r] - __uint_as_float(hi_p[2 * half + r] << 16),
-                                             w[2 * r + 1] - __uint_as_float(hi_p[2 * half + r] & 0xffff0000u));
+        for (int half = 0; half < 2; ++half) {
+          const int i = 2 * ks + half;
+          const float p0 = ex2(x[i][2 * r] - bm[r]), p1 = ex2(x[i][2 * r + 1] - bm[r]);
+          l[r] += p0 + p1;
+          if (kE4m3) {
+            hi_p[2 * half + r] = half2_of(ex2(z[i][2 * r] - bM[r]), ex2(z[i][2 * r + 1] - bM[r]));
+          } else {
+            const uint32_t h = pack_bf16x2(p0, p1);
+            hi_p[2 * half + r] = h;
+            lo_p[2 * half + r] = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
           }
         }
       }
@@ -506,31 +551,28 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         uint32_t v[4][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t row = 16 * ks + 8 * (k >> 1) + ((k & 1) ? f1 : f0);
+          const uint32_t in8 = (k & 1) ? f1 : f0;
           asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1])
-                       : "r"(vt + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8) : "memory");
+                       : "r"(vt + (16 * ks + 8 * (k >> 1) + in8) * 64 + (((g >> 1) ^ ((in8 >> 1) & 3)) << 4) + (g & 1) * 8) : "memory");
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // blocks 2 j, 2 j + 1: two bytes of each row
           const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-          const uint32_t y0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), y1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
           uint32_t b0[2], b1[2];
-          half2_of_e4m3(y0, b0[0], b0[1]);
-          half2_of_e4m3(y1, b1[0], b1[1]);
+          half2_of_e4m3(__byte_perm(v[0][j >> 1], v[1][j >> 1], sel), b0[0], b0[1]);
+          half2_of_e4m3(__byte_perm(v[2][j >> 1], v[3][j >> 1], sel), b1[0], b1[1]);
           mma16816<true>(o[2 * j], hi_p, b0[0], b1[0]);
           mma16816<true>(o[2 * j + 1], hi_p, b0[1], b1[1]);
         }
       } else {
-        const uint32_t row = 16 * ks + (lane & 15);
+        uint32_t b[4][4];
+        const uint32_t at0 = vt + (16 * ks + (lane & 15)) * 128;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t b[4];
-          ldsm4_trans(vt + row * 128 + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4), b);
-          mma16816<false>(o[2 * j], hi_p, b[0], b[1]);
-          mma16816<false>(o[2 * j], lo_p, b[0], b[1]);
-          mma16816<false>(o[2 * j + 1], hi_p, b[2], b[3]);
-          mma16816<false>(o[2 * j + 1], lo_p, b[2], b[3]);
-        }
+        for (int j = 0; j < 4; ++j) ldsm4_trans(at0 + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4), b[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mma16816<false>(o[j], hi_p, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mma16816<false>(o[j], lo_p, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
       }
     }
     __syncwarp();
@@ -540,69 +582,69 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       advance(prod);
       ++issued;
     }
+    if (++stage == kS) stage = 0, phase ^= 1u;
     const bool item_done = cons.blk == cons.units - 1;
     if (item_done || done == hi) {
       // ------------------------------------------------------------ the end of an item, or of this warp's part of it
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      for (int r = 0; r < kR; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       }
       const int mh = n * p.group;
       if (item_done && !started_before) {
-        bool wild[2] = {false, false};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = g + 8 * i;
-          if (row >= mh) continue;
-          const float f = out_factor<kE4m3>(m[i], M[i], l[i]);
-          const int64_t at = (s_row0[cons.s] + static_cast<int64_t>(row / p.group)) * p.heads + cons.h * p.group + row % p.group;
-          float y[16];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y[j] = l[i] == 0.f ? 0.f : o[j][2 * i] * f;
-            y[8 + j] = l[i] == 0.f ? 0.f : o[j][2 * i + 1] * f;
-            wild[i] |= !(fabsf(y[j]) <= 3.4e38f) || !(fabsf(y[8 + j]) <= 3.4e38f);
-          }
-          wild[i] &= l[i] == l[i];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (kE4m3) store_pair(p, at, 16 * t + 2 * j, y[2 * j], y[2 * j + 1]);
-            else store_pair(p, at, 8 * j + 2 * t, y[j], y[8 + j]);
-          }
-          if (p.lse != nullptr && t == 0) p.lse[at] = log_sum(m[i], l[i]);
-        }
         uint32_t which = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t b = __ballot_sync(0xffffffffu, wild[i]);
-          for (int r = 0; b != 0 && r < 8; ++r)
-            if ((b >> (4 * r)) & 15u) which |= 1u << (r + 8 * i);
+        for (int r = 0; r < kR; ++r) {
+          const int row = g + 8 * r;
+          bool wild = false;
+          if (row < mh) {
+            const float f = out_factor<kE4m3>(m[r], M[r], l[r]);
+            const int64_t at = (s_row0[cons.s] + static_cast<int64_t>(row / p.group)) * p.heads + cons.h * p.group + row % p.group;
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              y[j] = l[r] == 0.f ? 0.f : o[j][2 * r] * f;
+              y[8 + j] = l[r] == 0.f ? 0.f : o[j][2 * r + 1] * f;
+              wild |= !(fabsf(y[j]) <= 3.4e38f) || !(fabsf(y[8 + j]) <= 3.4e38f);
+            }
+            wild &= l[r] == l[r];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (kE4m3) store_pair(p, at, 16 * t + 2 * j, y[2 * j], y[2 * j + 1]);
+              else store_pair(p, at, 8 * j + 2 * t, y[j], y[8 + j]);
+            }
+            if (p.lse != nullptr && t == 0) p.lse[at] = log_sum(m[r], l[r]);
+          }
+          const uint32_t b = __ballot_sync(0xffffffffu, wild);
+          for (int i = 0; b != 0 && i < 8; ++i)
+            if ((b >> (4 * i)) & 15u) which |= 1u << (i + 8 * r);
         }
         if (which != 0) {
           __syncwarp();
           redo_rows<kE4m3>(a, p, which, s0 + cons.s, s_row0[cons.s], n, len, cons.h);
         }
       } else {
-        float* slot = started_before ? head_slot : tail_slot;
+        float* slot = slot_of(warp, started_before);
         if (!started_before) __syncwarp();   // (the ring's last reads are done)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = g + 8 * i;
+        for (int r = 0; r < kR; ++r) {
+          const int row = g + 8 * r;
           float* to = slot + row * kSlotStride;
+          if (kE4m3) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (kE4m3) {
-              to[16 * t + j] = o[j][2 * i];
-              to[16 * t + 8 + j] = o[j][2 * i + 1];
-            } else {
-              *reinterpret_cast<float2*>(to + 8 * j + 2 * t) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-            }
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(to + 16 * t + 4 * j) =
+                  j < 2 ? make_float4(o[4 * j][2 * r], o[4 * j + 1][2 * r], o[4 * j + 2][2 * r], o[4 * j + 3][2 * r])
+                        : make_float4(o[4 * j - 8][2 * r + 1], o[4 * j - 7][2 * r + 1], o[4 * j - 6][2 * r + 1], o[4 * j - 5][2 * r + 1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) *reinterpret_cast<float2*>(to + 8 * j + 2 * t) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
           }
           if (t == 0) {
-            slot[kM * kSlotStride + row] = m[i];
-            slot[kM * kSlotStride + kM + row] = M[i];
-            slot[kM * kSlotStride + 2 * kM + row] = l[i];
+            slot[kStats + row] = m[r];
+            slot[kStats + kM + row] = M[r];
+            slot[kStats + 2 * kM + row] = l[r];
           }
         }
       }
@@ -611,18 +653,22 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (done < hi) advance(cons);
   }
   if (!ok) {   // wait (a little) for the loads in flight before the CTA can leave
-    for (int64_t u = done; u < issued; ++u) mbar_wait_bounded(bar(static_cast<int>((u - lo) % kS)), static_cast<uint32_t>((u - lo) / kS) & 1u, 1000000ull);
+    for (int64_t u = done; u < issued; ++u) {
+      mbar_wait_bounded(bar(stage), phase, 1000000ull);
+      if (++stage == kS) stage = 0, phase ^= 1u;
+    }
   }
   ok = __syncthreads_and(ok);
 
   // ---------------------------------------------------------------- items over several warps of this CTA
   // `cons` is the last item of the warp's units; its first one it finds again.  The warps that have some of an item
-  // share its row heads.
+  // share its row heads, two of them at a time: half a warp each, first its lanes the parts, then four elements of O.
   float* ws_part = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
   if (ok && lo < hi) {
     At first{};
     locate(lo, first);
     const bool same = first.s == cons.s && first.h == cons.h;
+    const int half = lane >> 4, sub = lane & 15;
 #pragma unroll 1
     for (int what = 0; what < (same ? 1 : 2); ++what) {
       const At& at = what == 0 ? first : cons;
@@ -636,45 +682,54 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const bool w0_head = edge_of(w0) > ib;      // (the later ones have it in their head slots)
       const int n = s_count[at.s], mh = n * p.group;
       float* out_slot = ws_part + (ib < cta_lo ? 0 : kSlotFloats);
-      const float* mine = slot_of(w0 + min(lane, parts - 1), min(lane, parts - 1) > 0 || w0_head) + kM * kSlotStride;
+      const float* mine = slot_of(w0 + min(sub, parts - 1), min(sub, parts - 1) > 0 || w0_head);
       uint32_t which = 0;
-      for (int row = warp - w0; row < mh; row += parts) {
-        const float pm = lane < parts ? mine[row] : -INFINITY, pM = lane < parts ? mine[kM + row] : -INFINITY;
+      for (int r0 = 2 * (warp - w0); r0 < mh; r0 += 2 * parts) {
+        const int row = min(r0 + half, mh - 1);
+        const bool in = r0 + half < mh;
+        const float pm = sub < parts ? mine[kStats + row] : -INFINITY, pM = sub < parts ? mine[kStats + kM + row] : -INFINITY;
+        const float pl = sub < parts ? mine[kStats + 2 * kM + row] : 0.f;
         float jm = pm, jM = pM;
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) {
+        for (int d = 4; d > 0; d >>= 1) {   // (at most 8 parts)
           jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, d));
           jM = fmaxf(jM, __shfl_xor_sync(0xffffffffu, jM, d));
         }
-        jm = __shfl_sync(0xffffffffu, jm, 0), jM = __shfl_sync(0xffffffffu, jM, 0);
+        jm = __shfl_sync(0xffffffffu, jm, 0, 16), jM = __shfl_sync(0xffffffffu, jM, 0, 16);
         const float f = rescale(pM, jM);
-        float jl = lane < parts ? mine[2 * kM + row] * rescale(pm, jm) : 0.f;
+        float jl = pl * rescale(pm, jm);
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, d);
-        jl = __shfl_sync(0xffffffffu, jl, 0);
-        float2 jo = make_float2(0.f, 0.f);
+        for (int d = 4; d > 0; d >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, d);
+        jl = __shfl_sync(0xffffffffu, jl, 0, 16);
+        float4 jo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int w = 0; w < parts; ++w) {
-          const float2 part =
-              *reinterpret_cast<const float2*>(slot_of(w0 + w, w > 0 || w0_head) + row * kSlotStride + 2 * lane);
-          const float fw = __shfl_sync(0xffffffffu, f, w);
-          jo.x = fmaf(fw, part.x, jo.x), jo.y = fmaf(fw, part.y, jo.y);
+          const float4 y = *reinterpret_cast<const float4*>(slot_of(w0 + w, w > 0 || w0_head) + row * kSlotStride + 4 * sub);
+          const float fw = __shfl_sync(0xffffffffu, f, w, 16);
+          jo.x = fmaf(fw, y.x, jo.x), jo.y = fmaf(fw, y.y, jo.y), jo.z = fmaf(fw, y.z, jo.z), jo.w = fmaf(fw, y.w, jo.w);
         }
+        bool wild = false;
         if (complete) {
           const int64_t o_at = (s_row0[at.s] + static_cast<int64_t>(row / p.group)) * p.heads + at.h * p.group + row % p.group;
           const float of = out_factor<kE4m3>(jm, jM, jl);
-          const float y0 = jl == 0.f ? 0.f : jo.x * of, y1 = jl == 0.f ? 0.f : jo.y * of;
-          store_pair(p, o_at, 2 * lane, y0, y1);
-          if (p.lse != nullptr && lane == 0) p.lse[o_at] = log_sum(jm, jl);
-          if (__any_sync(0xffffffffu, (!(fabsf(y0) <= 3.4e38f) || !(fabsf(y1) <= 3.4e38f)) && jl == jl)) which |= 1u << row;
-        } else {
-          *reinterpret_cast<float2*>(out_slot + row * kSlotStride + 2 * lane) = jo;
-          if (lane == 0) {
+          jo.x *= of, jo.y *= of, jo.z *= of, jo.w *= of;
+          wild = (!(fabsf(jo.x) <= 3.4e38f) || !(fabsf(jo.y) <= 3.4e38f) || !(fabsf(jo.z) <= 3.4e38f) || !(fabsf(jo.w) <= 3.4e38f)) &&
+                 jl == jl && jl != 0.f;
+          if (in) {
+            *reinterpret_cast<uint2*>(p.out + o_at * kHeadDim + 4 * sub) =
+                jl == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(jo.x, jo.y), pack_bf16x2(jo.z, jo.w));
+            if (p.lse != nullptr && sub == 0) p.lse[o_at] = log_sum(jm, jl);
+          }
+        } else if (in) {
+          *reinterpret_cast<float4*>(out_slot + row * kSlotStride + 4 * sub) = jo;
+          if (sub == 0) {
             out_slot[kM * kSlotStride + row] = jm;
             out_slot[kM * kSlotStride + kM + row] = jM;
             out_slot[kM * kSlotStride + 2 * kM + row] = jl;
           }
         }
+        const uint32_t b = __ballot_sync(0xffffffffu, wild);
+        which |= ((b & 0xffffu) ? 1u << r0 : 0u) | ((b >> 16) && r0 + 1 < mh ? 2u << r0 : 0u);
       }
       if (which != 0) {
         __syncwarp();
@@ -690,8 +745,9 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       locate(cta_hi - 1, at);
       const int64_t ib = cta_hi - 1 - at.blk, ie = ib + at.units;
       if (ib >= cta_lo && ie > cta_hi) {
-        const int64_t last_warp = (ie * nw - 1) / U;   // of the last unit, ie - 1
-        j.parts = static_cast<int32_t>(last_warp / kW) - static_cast<int32_t>(blockIdx.x) + 1;
+        const int64_t x = ie - 1;   // its last unit, and the warp that has it
+        const int64_t w = x < more * (each + 1) ? quotient(x, each + 1) : more + quotient(x - more * (each + 1), each);
+        j.parts = static_cast<int32_t>(w / kW) - static_cast<int32_t>(blockIdx.x) + 1;
         j.s = s0 + at.s;
         j.h = at.h;
         j.n = s_count[at.s];
@@ -784,14 +840,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   if (wild != 0 && tid < 32) redo_rows<kE4m3>(a, p, wild, j.s, j.row0, j.n, j.len, j.h);
 }
 
-template <bool kE4m3>
+template <bool kE4m3, bool kTwo>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns, int grid,
                    float* ws, cudaStream_t stream) {
-  using C = Cfg<kE4m3>;
+  using C = Cfg<kE4m3, kTwo>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3>, C::kRequest, done);
+  const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3, kTwo>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  paged_step_kernel<kE4m3><<<grid, C::kWarps * 32, C::kRequest, stream>>>(tm_k, tm_v, a, p, s0, ns, ws);
+  paged_step_kernel<kE4m3, kTwo><<<grid, C::kWarps * 32, C::kRequest, stream>>>(tm_k, tm_v, a, p, s0, ns, ws);
   return cudaGetLastError();
 }
 
@@ -799,14 +855,20 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArg
 
 static_assert(kStepWsFloats * 4 >= 2 * kSlotFloats * 4 + sizeof(StepJoin), "workspace of a CTA");
 
-int paged_step_grid(int64_t most_units, bool e4m3, int num_sms) {
-  const int64_t w = e4m3 ? Cfg<true>::kWarps : Cfg<false>::kWarps;
+int paged_step_unit(bool e4m3) { return e4m3 ? Cfg<true, false>::kUnit : Cfg<false, false>::kUnit; }
+
+int paged_step_grid(int64_t most_units, int num_sms) {
+  constexpr int64_t w = Cfg<false, false>::kWarps;
   return static_cast<int>(std::min<int64_t>(std::min(num_sms, kStepMaxGrid), (most_units + w - 1) / w));
 }
 
+// At most 8 row heads where the call says so (max_rows): the products' second half, and its exponentials, are left out.
+// One token of 61 sequences over e4m3 pages, 16 heads: see above; the same by the kernel for 16 row heads: 1.2 times that.
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
                               int grid, bool e4m3, float* ws, cudaStream_t stream) {
-  return e4m3 ? launch<true>(tm_k, tm_v, a, p, s0, ns, grid, ws, stream) : launch<false>(tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
+  const bool two = a.max_rows * p.group > 8;
+  return e4m3 ? (two ? launch<true, true> : launch<true, false>)(tm_k, tm_v, a, p, s0, ns, grid, ws, stream)
+              : (two ? launch<false, true> : launch<false, false>)(tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
 }
 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {

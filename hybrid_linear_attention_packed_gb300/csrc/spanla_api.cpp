@@ -2182,8 +2182,9 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   span_la_status st = SPAN_LA_OK;
   CUtensorMap tm_q, tm_k, tm_v;
   const bool step = p.group <= kStepHeads, chunk = a.max_rows * p.group > kStepHeads;
-  const int64_t units = std::max<int64_t>(1, (a.capacity + kStepUnit - 1) / kStepUnit);   // of a sequence and head, at most
-  const int step_grid = step ? paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), e4m3, num_sms) : 0;
+  const int unit = paged_step_unit(e4m3);
+  const int64_t units = std::max<int64_t>(1, (a.capacity + unit - 1) / unit);   // of a sequence and head, at most
+  const int step_grid = step ? paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), num_sms) : 0;
   const int chunk_grid = chunk ? std::min(num_sms, kStepMaxGrid) : 0;
   const size_t step_ws = align256(static_cast<size_t>(step_grid > 1 ? step_grid : 0) * kStepWsFloats * sizeof(float));
   const size_t bytes = step_ws + static_cast<size_t>(chunk_grid > 1 ? chunk_grid : 0) * kChunkWsFloats * sizeof(float);
@@ -2198,8 +2199,8 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     for (int s0 = 0; s0 < a.seqs && e == cudaSuccess; s0 += kStepSeqs) e = launch(s0, std::min(kStepSeqs, a.seqs - s0));
   };
   if (step) {
-    st = encode_pages(&tm_k, a.k, a, e4m3, kStepUnit);
-    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, kStepUnit);
+    st = encode_pages(&tm_k, a.k, a, e4m3, unit);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, unit);
     if (st == SPAN_LA_OK)
       each([&](int s0, int ns) {
         cudaError_t x = counted_launch(kKernelPagedStep, stream,
