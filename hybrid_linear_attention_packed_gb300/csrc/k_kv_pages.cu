@@ -32,7 +32,6 @@ struct Places {            // of a CTA's rows: element offset of head 0 in the p
 __device__ __forceinline__ int find_seq(const KvArgs& a, int64_t t0) {
   const int lane = threadIdx.x & 31;
   const int64_t t = t0 + lane;
-  if (a.row_cu == nullptr) return t < a.seqs ? static_cast<int>(t) : -1;
   int lo = 0, n = a.seqs + 1;
   while (n > 1) {
     const int step = (n + 31) / 32, at = lo + lane * step;
@@ -49,14 +48,34 @@ __device__ __forceinline__ int find_seq(const KvArgs& a, int64_t t0) {
   return seq_of_row(a, t);
 }
 
+// The sequence of a warp's row t0 + lane, or -1, and its part of the call.  Up to 31 sequences by one read of all
+// offsets and lengths, each lane's own; more of them by a search.
+__device__ __forceinline__ int find_rows(const KvArgs& a, int64_t t0, SeqRows* r) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = t0 + lane;
+  bool bad = false;
+  if (a.row_cu == nullptr || a.seqs > 31) {
+    const int s = a.row_cu == nullptr ? (t < a.seqs ? static_cast<int>(t) : -1) : find_seq(a, t0);
+    if (s >= 0 && t < a.rows) *r = seq_rows(a, s, &bad);
+    return s >= 0 && t < a.rows ? s : -1;
+  }
+  const int32_t cu = a.row_cu[min(lane, a.seqs)], len = a.seq_len[min(lane, a.seqs - 1)];
+  int s = -1;
+  for (int i = 0; i < a.seqs; ++i)
+    if (__shfl_sync(0xffffffffu, cu, i) <= t) s = i;
+  const int64_t b = __shfl_sync(0xffffffffu, cu, max(s, 0)), e = __shfl_sync(0xffffffffu, cu, max(s, 0) + 1);
+  const int32_t n = __shfl_sync(0xffffffffu, len, max(s, 0));
+  *r = rows_between(a, b, e, n, &bad);
+  return t < a.rows ? s : -1;
+}
+
 __device__ __forceinline__ void find_places(const KvArgs& a, Places& pl) {
   if (threadIdx.x < kRows) {
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows, t = t0 + threadIdx.x;
     int64_t at = -1, scale_at = 0;
-    const int s = find_seq(a, t0);
-    if (s >= 0 && t < a.rows) {
-      bool bad = false;
-      const SeqRows r = seq_rows(a, s, &bad);
+    SeqRows r{};
+    const int s = find_rows(a, t0, &r);
+    if (s >= 0) {
       const int64_t pos = r.len - (r.n - (t - r.row0));   // (negative: the sequence is shorter than its packed rows)
       if (t >= r.row0 && t - r.row0 < r.n && pos >= 0) {
         const int32_t page = page_of(a, s, static_cast<int32_t>(pos));
@@ -117,27 +136,39 @@ __device__ __forceinline__ void convert(const Eight<T>& x, Eight<T>& y) {
   y = x;
 }
 
+// max(a, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // Units u: K of head u / 2 (u even) or V; a CTA's warps take every so manieth one.
 template <typename T, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows in) {
   __shared__ Places pl;
-  find_places(a, pl);
   const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  for (int unit = blockIdx.y * kWarps + (threadIdx.x >> 5); unit < 2 * a.heads; unit += gridDim.y * kWarps) {
-    const int head = unit >> 1;
-    const bool is_v = unit & 1;
-    const T* src = static_cast<const T*>(is_v ? in.v : in.k) + head * kHeadDim + sub * 8;
-    const int64_t stride = is_v ? in.v_row_stride : in.k_row_stride;
-    Eight<T> x[kSteps];
+  Eight<T> x[kSteps];
+  auto load = [&](int unit) {   // (rows of no sequence too: their places are not known yet)
+    const T* src = static_cast<const T*>((unit & 1) ? in.v : in.k) + (unit >> 1) * kHeadDim + sub * 8;
+    const int64_t stride = (unit & 1) ? in.v_row_stride : in.k_row_stride;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int r = 4 * i + (lane >> 3);
+      const int64_t t = t0 + 4 * i + (lane >> 3);
       x[i] = Eight<T>{};
-      if (pl.at[r] >= 0) x[i].load(src + (t0 + r) * stride);
+      if (t < a.rows) x[i].load(src + t * stride);
     }
+  };
+  const int first = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  if (first < 2 * a.heads) load(first);
+  find_places(a, pl);
+  for (int unit = first; unit < 2 * a.heads; unit += gridDim.y * kWarps) {
+    const int head = unit >> 1;
+    const bool is_v = unit & 1;
+    if (unit != first) load(unit);
     uint32_t code = 0;   // row `lane`'s power of two
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -146,10 +177,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
       if (kE4m3) {
         float f[8];
         x[i].get(f);
-        uint32_t top = 0;   // magnitudes as bits order like numbers
+        // The largest magnitude, NaN if there is one; where it is not finite, that of the finite ones (and NaN for the
+        // others).
+        float big = max3_abs(0.f, f[0], f[1]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (finite(f[c])) top = max(top, __float_as_uint(f[c]) & 0x7fffffffu);
+        for (int c = 2; c < 8; c += 2) big = max3_abs(big, f[c], f[c + 1]);
+        uint32_t top = __float_as_uint(big);
+        if (__any_sync(0xffffffffu, !finite(big))) {
+          top = 0;   // (magnitudes as bits order like numbers)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (finite(f[c])) top = max(top, __float_as_uint(f[c]) & 0x7fffffffu);
+            else f[c] = NAN;
+          }
+        }
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         // top = m 2^E, 1 <= m < 2: at most 448 2^e = 1.75 2^(8 + e) from e = E - 8 on, or E - 7 where m > 1.75.
@@ -161,8 +202,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
           uint32_t w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float y0 = finite(f[2 * c]) ? f[2 * c] * inv : NAN;
-            const float y1 = finite(f[2 * c + 1]) ? f[2 * c + 1] * inv : NAN;
+            float y0, y1;
+            f32x2_split(mul_f32x2(f32x2(f[2 * c], f[2 * c + 1]), f32x2(inv, inv)), y0, y1);
             w[c] = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
           }
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v : a.k) + at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
@@ -238,7 +279,8 @@ cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t
   // A CTA takes all heads of its rows where there are CTAs enough: finding the rows' places takes four reads one behind
   // the other, as long as copying a few heads.
   const int64_t blocks = (a.rows + kRows - 1) / kRows;
-  const int64_t split = std::min<int64_t>((2 * a.heads + kWarps - 1) / kWarps, std::max<int64_t>(1, (kBlocks + blocks - 1) / blocks));
+  const int64_t eights = (2 * a.heads + kWarps - 1) / kWarps;
+  const int64_t turns = std::max<int64_t>(1, eights * blocks / kBlocks), split = (eights + turns - 1) / turns;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
   kernel<<<grid, kWarps * 32, 0, stream>>>(a, x);
   return cudaGetLastError();

@@ -686,73 +686,91 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   griddep_wait();
 }
 
-// CTA (c, y): 16 row heads (y & 7) of tile y >> 3 of the item that begins in CTA c of the chunk kernel and goes on, from
-// the parts of it and the next CTAs.  A group of 16 lanes has a row head: first its lanes the parts' maxima and sums,
-// then four elements of O each.
-constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16;
+// CTA (c, y): 32 row heads (y & 3) of tile y >> 2 of the item that begins in CTA c of the chunk kernel and goes on, from
+// the parts of it and the next CTAs.  A group of 16 lanes has two row heads: its lanes the parts' maxima and sums, then
+// four elements of O each.  What an item of two parts needs is asked for before the record is there that says how many
+// there are.
+constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16, kJoinBoth = 2;
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
                                                                   const float* __restrict__ ws) {
-  __shared__ float factor[16][kStepMaxGrid];
+  __shared__ float factor[16][kJoinBoth][kStepMaxGrid];
   griddep_wait();
   const float* mine = ws + blockIdx.x * kChunkWsFloats;
-  const ChunkJoin j = *reinterpret_cast<const ChunkJoin*>(mine + 4 * kPartFloats);
-  const int x = blockIdx.y >> 3, grp = threadIdx.x >> 4, sub = threadIdx.x & 15, row = (blockIdx.y & 7) * 16 + grp;
-  const int32_t tile_rows = kTileRows / p.group, in = j.first + x * tile_rows + row / p.group;
-  const bool live = j.parts > 0 && row / p.group < tile_rows && in < j.n;
-  if (!__syncthreads_or(live)) return;
+  const int x = blockIdx.y >> 2, grp = threadIdx.x >> 4, sub = threadIdx.x & 15, row0 = (blockIdx.y & 3) * 32 + grp;
+  const int last = static_cast<int>(gridDim.x - 1 - blockIdx.x);
   auto part_of = [&](int i) { return mine + i * kChunkWsFloats + (2 * (i == 0 ? 1 : 0) + x) * kPartFloats; };
-  float pm[kJoinEach], pl[kJoinEach], m = -INFINITY, l = 0.f;
+  const ChunkJoin j = *reinterpret_cast<const ChunkJoin*>(mine + 4 * kPartFloats);
+  float pm0[kJoinBoth], pl0[kJoinBoth];
+  float4 ahead[kJoinBoth][2];
 #pragma unroll
-  for (int k = 0; k < kJoinEach; ++k) {
-    if (16 * k >= j.parts) break;
-    const int i = sub + 16 * k;
-    const bool has = live && i < j.parts;
-    const float* st = part_of(has ? i : 0) + kTileRows * kHeadDim + row;
-    pm[k] = has ? st[0] : -INFINITY, pl[k] = has ? st[kTileRows] : 0.f;
+  for (int b = 0; b < kJoinBoth; ++b) {
+    const float* st = part_of(min(sub, last)) + kTileRows * kHeadDim + row0 + 16 * b;
+    pm0[b] = st[0], pl0[b] = st[kTileRows];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ahead[b][i] = *reinterpret_cast<const float4*>(part_of(min(i, last)) + (row0 + 16 * b) * kHeadDim + 4 * sub);
   }
+  if (j.parts == 0) return;
+  const int32_t tile_rows = kTileRows / p.group;
+  uint32_t which[kJoinBoth];
 #pragma unroll
-  for (int k = 0; k < kJoinEach; ++k) {
-    if (16 * k >= j.parts) break;
-    m = fmaxf(m, pm[k]);
-  }
+  for (int b = 0; b < kJoinBoth; ++b) {
+    const int row = row0 + 16 * b;
+    const int32_t in = j.first + x * tile_rows + row / p.group;
+    const bool live = row / p.group < tile_rows && in < j.n;
+    float pm[kJoinEach], pl[kJoinEach], m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll
-  for (int k = 0; k < kJoinEach; ++k) {
-    if (16 * k >= j.parts) break;
-    const float f = pm[k] == m ? 1.f : pm[k] == -INFINITY ? 0.f : ex2(pm[k] - m);
-    l += pl[k] * f;
-    if (sub + 16 * k < j.parts) factor[grp][sub + 16 * k] = f;
-  }
-#pragma unroll
-  for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  __syncwarp();
-  bool wild = false;
-  const int head = j.h * p.group + row % p.group;
-  if (live) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < j.parts; ++i) {
-      const float4 y = *reinterpret_cast<const float4*>(part_of(i) + row * kHeadDim + 4 * sub);
-      const float f = factor[grp][i];
-      o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+    for (int k = 0; k < kJoinEach; ++k) {
+      if (16 * k >= j.parts) break;
+      const int i = sub + 16 * k;
+      pm[k] = -INFINITY, pl[k] = 0.f;
+      if (live && i < j.parts) {
+        const float* st = part_of(i) + kTileRows * kHeadDim + row;
+        pm[k] = k == 0 ? pm0[b] : st[0], pl[k] = k == 0 ? pl0[b] : st[kTileRows];
+      }
+      m = fmaxf(m, pm[k]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = (j.row0 + static_cast<int64_t>(in)) * p.heads + head;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    wild = !(fabsf(o.x) <= 3.4e38f) || !(fabsf(o.y) <= 3.4e38f) || !(fabsf(o.z) <= 3.4e38f) || !(fabsf(o.w) <= 3.4e38f);
-    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * sub) =
-        l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-    if (p.lse != nullptr && sub == 0) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) {
+      if (16 * k >= j.parts) break;
+      const float f = pm[k] == m ? 1.f : pm[k] == -INFINITY ? 0.f : ex2(pm[k] - m);
+      l += pl[k] * f;
+      factor[grp][b][sub + 16 * k] = f;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    __syncwarp();
+    bool wild = false;
+    if (live) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](const float4& y, float f) {
+        o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+      };
+      add(ahead[b][0], factor[grp][b][0]);
+      add(ahead[b][1], factor[grp][b][1]);   // (there are two parts at least)
+#pragma unroll 4
+      for (int i = 2; i < j.parts; ++i)
+        add(*reinterpret_cast<const float4*>(part_of(i) + row * kHeadDim + 4 * sub), factor[grp][b][i]);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t at = (j.row0 + static_cast<int64_t>(in)) * p.heads + j.h * p.group + row % p.group;
+      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+      wild = !(fabsf(o.x) <= 3.4e38f) || !(fabsf(o.y) <= 3.4e38f) || !(fabsf(o.z) <= 3.4e38f) || !(fabsf(o.w) <= 3.4e38f);
+      *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * sub) =
+          l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      if (p.lse != nullptr && sub == 0) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+    }
+    which[b] = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
   }
-  const uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
   __syncwarp();
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {   // the warp's two row heads
-    if (((which >> (16 * half)) & 0xffffu) == 0) continue;
-    const int rr = __shfl_sync(0xffffffffu, row, 16 * half), at = j.first + x * tile_rows + rr / p.group;
+  for (int k = 0; k < 2 * kJoinBoth; ++k) {   // the warp's row heads
+    const int b = k >> 1, half = k & 1;
+    if ((((b == 0 ? which[0] : which[1]) >> (16 * half)) & 0xffffu) == 0) continue;
+    const int rr = __shfl_sync(0xffffffffu, row0, 16 * half) + 16 * b, at = j.first + x * tile_rows + rr / p.group;
     attend_row<kE4m3>(a, p, j.s, j.row0 + static_cast<int64_t>(at), j.h * p.group + rr % p.group, max(0, j.len - j.n + at + 1));
   }
 }
@@ -795,7 +813,7 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
 
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, 16);
+  cfg.gridDim = dim3(grid, 8);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -41,9 +41,11 @@ constexpr int kSlotFloats = kM * kSlotStride + 3 * kM;
 template <bool kE4m3, bool kTwo>
 struct Cfg {
   static constexpr int kUnit = kE4m3 ? 64 : 32;                // cached rows
-  static constexpr int kWarps = 8;
-  // Three units of bf16 in flight a warp where there is room: with few units a warp, their latencies are the call.
-  static constexpr int kStages = kE4m3 || kTwo ? 2 : 3;
+  // e4m3 pages keep a warp busier for its bytes (conversions): as many warps as fit beside their rings.  (61 tokens:
+  // 8 warps 126 us, 10 132, 11 119.  bf16 pages, 128 tokens: 8 warps 231 us, 10 239, 11 242; three units in flight a warp
+  // instead of two: 245.)
+  static constexpr int kWarps = kE4m3 && !kTwo ? 11 : 8;
+  static constexpr int kStages = 2;
   static constexpr int kRows = kTwo ? 16 : 8;                  // row heads of a part in shared memory
   static constexpr int kSlot = kRows * kSlotStride + 3 * kM;   // its floats
   static constexpr uint32_t kRow = kE4m3 ? 64 : 128;           // bytes
@@ -691,7 +693,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const float pl = sub < parts ? mine[kStats + 2 * kM + row] : 0.f;
         float jm = pm, jM = pM;
 #pragma unroll
-        for (int d = 4; d > 0; d >>= 1) {   // (at most 8 parts)
+        for (int d = 8; d > 0; d >>= 1) {
           jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, d));
           jM = fmaxf(jM, __shfl_xor_sync(0xffffffffu, jM, d));
         }
@@ -699,7 +701,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const float f = rescale(pM, jM);
         float jl = pl * rescale(pm, jm);
 #pragma unroll
-        for (int d = 4; d > 0; d >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, d);
+        for (int d = 8; d > 0; d >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, d);
         jl = __shfl_sync(0xffffffffu, jl, 0, 16);
         float4 jo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -759,35 +761,50 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   }
 }
 
-// One CTA for each CTA of the step kernel: the item that begins in it and goes on, from the parts of this and the next
-// CTAs.  16 groups of 16 lanes: first a group has a row head, its lanes the parts' maxima and sums; then a group has a
-// row head and every so manieth part, its lanes four elements of O each.
-constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16;
+// CTA (c, y): row heads 4 y .. 4 y + 3 of the item that begins in CTA c of the step kernel and goes on, from the parts of
+// it and the next CTAs.  16 groups of 16 lanes: group (row, slice) has every fourth part of a row head, a lane four
+// elements of O; the row heads' maxima and sums are one group's, a lane a part.  What most items need is asked for before
+// the record is there that says what they need (the workspace holds all of it, whether or not it is of this item): the
+// kernel is three reads one behind the other else, and little more.
+constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16, kJoinRows = 4, kJoinSlices = 4, kJoinAhead = 2;
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
                                                                   const float* __restrict__ ws) {
   __shared__ float4 so[16][16];
-  __shared__ float factor[kM][kStepMaxGrid];
-  __shared__ float total[kM][3];
+  __shared__ float factor[kJoinRows][kStepMaxGrid];
+  __shared__ float total[kJoinRows][3];
   __shared__ uint32_t wild;
   griddep_launch_dependents();
   griddep_wait();
   const float* mine = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
-  const StepJoin j = *reinterpret_cast<const StepJoin*>(mine + 2 * kSlotFloats);
-  if (j.parts == 0) return;
-  const int tid = threadIdx.x, grp = tid >> 4, sub = tid & 15;
-  const int mh = j.n * p.group;
+  const int tid = threadIdx.x, grp = tid >> 4, sub = tid & 15, last = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+  const int row4 = grp & (kJoinRows - 1), row = kJoinRows * blockIdx.y + row4, slice = grp / kJoinRows;
   auto part_of = [&](int i) { return mine + static_cast<int64_t>(i) * kStepWsFloats + (i == 0 ? kSlotFloats : 0); };
-  if (tid == 0) wild = 0;
+  const StepJoin j = *reinterpret_cast<const StepJoin*>(mine + 2 * kSlotFloats);
+  float pm[kJoinEach], pM[kJoinEach], pl[kJoinEach];
   {
-    float pm[kJoinEach], pM[kJoinEach], pl[kJoinEach], m = -INFINITY, M = -INFINITY, l = 0.f;
+    const float* st = part_of(min(sub, last)) + kM * kSlotStride + row;
+    pm[0] = st[0], pM[0] = st[kM], pl[0] = st[2 * kM];
+  }
+  float4 ahead[kJoinAhead];
+#pragma unroll
+  for (int k = 0; k < kJoinAhead; ++k)
+    ahead[k] = *reinterpret_cast<const float4*>(part_of(min(slice + kJoinSlices * k, last)) + row * kSlotStride + 4 * sub);
+  const int mh = j.n * p.group;
+  if (j.parts == 0 || kJoinRows * static_cast<int>(blockIdx.y) >= mh) return;
+  if (tid == 0) wild = 0;
+  if (slice == 0) {
+    float m = -INFINITY, M = -INFINITY, l = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinEach; ++k) {
       const int i = sub + 16 * k;
-      const bool in = i < j.parts && grp < mh;
-      const float* st = part_of(in ? i : 0) + kM * kSlotStride + (in ? grp : 0);
-      pm[k] = in ? st[0] : -INFINITY, pM[k] = in ? st[kM] : -INFINITY, pl[k] = in ? st[2 * kM] : 0.f;
+      if (i >= j.parts) {
+        pm[k] = pM[k] = -INFINITY, pl[k] = 0.f;
+      } else if (k > 0) {
+        const float* st = part_of(i) + kM * kSlotStride + row;
+        pm[k] = st[0], pM[k] = st[kM], pl[k] = st[2 * kM];
+      }
     }
 #pragma unroll
     for (int k = 0; k < kJoinEach; ++k) m = fmaxf(m, pm[k]), M = fmaxf(M, pM[k]);
@@ -798,42 +815,41 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
 #pragma unroll
     for (int k = 0; k < kJoinEach; ++k) {
+      if (16 * k >= j.parts) break;
       l += pl[k] * rescale(pm[k], m);
-      if (sub + 16 * k < j.parts) factor[grp][sub + 16 * k] = rescale(pM[k], M);
+      factor[row4][sub + 16 * k] = rescale(pM[k], M);
     }
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (sub == 0) total[grp][0] = m, total[grp][1] = M, total[grp][2] = l;
+    if (sub == 0) total[row4][0] = m, total[row4][1] = M, total[row4][2] = l;
   }
   __syncthreads();
-  int rows = 1;
-  while (rows < mh) rows <<= 1;
-  const int row = grp & (rows - 1), slices = 16 / rows;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& x, float f) {
+    o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
+  };
   if (row < mh) {
+#pragma unroll
+    for (int k = 0; k < kJoinAhead; ++k)
+      if (slice + kJoinSlices * k < j.parts) add(ahead[k], factor[row4][slice + kJoinSlices * k]);
 #pragma unroll 8
-    for (int i = grp / rows; i < j.parts; i += slices) {
-      const float4 x = *reinterpret_cast<const float4*>(part_of(i) + row * kSlotStride + 4 * sub);
-      const float f = factor[row][i];
-      o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
-    }
+    for (int i = slice + kJoinSlices * kJoinAhead; i < j.parts; i += kJoinSlices)
+      add(*reinterpret_cast<const float4*>(part_of(i) + row * kSlotStride + 4 * sub), factor[row4][i]);
   }
   so[grp][sub] = o;
   __syncthreads();
-  if (grp < rows && row < mh) {
-    for (int i = 1; i < slices; ++i) {
-      const float4 x = so[grp + i * rows][sub];
-      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-    }
-    const float m = total[row][0], M = total[row][1], l = total[row][2], f = out_factor<kE4m3>(m, M, l);
+  if (slice == 0 && row < mh) {
+#pragma unroll
+    for (int i = 1; i < kJoinSlices; ++i) add(so[grp + i * kJoinRows][sub], 1.f);
+    const float m = total[row4][0], M = total[row4][1], l = total[row4][2], f = out_factor<kE4m3>(m, M, l);
     const int64_t at = (j.row0 + static_cast<int64_t>(row / p.group)) * p.heads + j.h * p.group + row % p.group;
     const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
     bool w = false;
 #pragma unroll
     for (int c = 0; c < 4; ++c) w |= !(fabsf(y[c]) <= 3.4e38f);
     if (w && l == l && l != 0.f) atomicOr(&wild, 1u << row);
-    store_pair(p, at, 4 * sub, l == 0.f ? 0.f : y[0], l == 0.f ? 0.f : y[1]);
-    store_pair(p, at, 4 * sub + 2, l == 0.f ? 0.f : y[2], l == 0.f ? 0.f : y[3]);
+    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * sub) =
+        l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     if (p.lse != nullptr && sub == 0) p.lse[at] = log_sum(m, l);
   }
   __syncthreads();
@@ -858,7 +874,7 @@ static_assert(kStepWsFloats * 4 >= 2 * kSlotFloats * 4 + sizeof(StepJoin), "work
 int paged_step_unit(bool e4m3) { return e4m3 ? Cfg<true, false>::kUnit : Cfg<false, false>::kUnit; }
 
 int paged_step_grid(int64_t most_units, int num_sms) {
-  constexpr int64_t w = Cfg<false, false>::kWarps;
+  constexpr int64_t w = Cfg<false, false>::kWarps;   // (the least that a CTA has)
   return static_cast<int>(std::min<int64_t>(std::min(num_sms, kStepMaxGrid), (most_units + w - 1) / w));
 }
 
@@ -873,7 +889,8 @@ cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  const int64_t most = std::min<int64_t>(kM, a.max_rows * p.group);   // row heads
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

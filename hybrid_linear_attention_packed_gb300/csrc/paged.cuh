@@ -24,13 +24,14 @@ struct SeqRows {
   int32_t n, len;
 };
 
-__device__ __forceinline__ SeqRows seq_rows(const KvArgs& a, int s, bool* bad) {
-  const int64_t b = a.row_cu != nullptr ? a.row_cu[s] : s;
-  const int64_t e = a.row_cu != nullptr ? a.row_cu[s + 1] : s + 1;
-  const int32_t len = a.seq_len[s];
+__device__ __forceinline__ SeqRows rows_between(const KvArgs& a, int64_t b, int64_t e, int32_t len, bool* bad) {
   const bool wrong = b < 0 || e < b || e > a.rows || e - b > a.max_rows || len < 0 || len > a.capacity;
   if (wrong) *bad = true;
   return {b, wrong ? 0 : static_cast<int32_t>(e - b), wrong ? 0 : len};
+}
+
+__device__ __forceinline__ SeqRows seq_rows(const KvArgs& a, int s, bool* bad) {
+  return rows_between(a, a.row_cu != nullptr ? a.row_cu[s] : s, a.row_cu != nullptr ? a.row_cu[s + 1] : s + 1, a.seq_len[s], bad);
 }
 
 // The sequence whose rows hold packed row t, or -1.

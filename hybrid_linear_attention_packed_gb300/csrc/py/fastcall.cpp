@@ -36,6 +36,7 @@ decltype(&span_la_qk_norm_rope) g_rope = nullptr;
 decltype(&span_la_kv_write) g_write = nullptr;
 decltype(&span_la_kv_read) g_read = nullptr;
 decltype(&span_la_softmax_paged) g_paged = nullptr;
+decltype(&span_la_softmax_paged_workspace) g_paged_bytes = nullptr;
 
 // (without the dispatcher: about 1 us less for a call that returns two tensors;
 // see usual_mode)
@@ -464,24 +465,29 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return none();
       lse = static_cast<float*>(t->data_ptr());
     }
+    // (on another stream than the current one, whose allocator this is, the library takes its own)
+    at::Tensor ws;
+    const int64_t bytes =
+        a[12] == Py_None ? g_paged_bytes(q->size(0), static_cast<int32_t>(q->size(1)), &c.c, static_cast<int32_t>(max_rows)) : 0;
+    if (bytes > 0) ws = new_tensor({bytes}, at::kByte, c.dev);
     span_la_status st;
     Py_BEGIN_ALLOW_THREADS
     st = g_paged(q->data_ptr(), qs, q->size(0), static_cast<int32_t>(q->size(1)), &c.c, static_cast<int32_t>(max_rows),
-                 static_cast<float>(PyFloat_AS_DOUBLE(a[9])), out.data_ptr(), lse, stream);
+                 static_cast<float>(PyFloat_AS_DOUBLE(a[9])), out.data_ptr(), lse, bytes > 0 ? ws.data_ptr() : nullptr, stream);
     Py_END_ALLOW_THREADS
     return st != SPAN_LA_OK ? PyLong_FromLong(st) : wrap(out);
   });
 }
 
 // bind(addresses of span_la_decay_pass, .._branches_from_state, .._step, span_la_qk_norm_rope, span_la_kv_write, .._read,
-// span_la_softmax_paged)
+// span_la_softmax_paged, .._workspace)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "bind takes eight addresses");
     return nullptr;
   }
-  void* p[7];
-  for (int i = 0; i < 7; ++i) {
+  void* p[8];
+  for (int i = 0; i < 8; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is NULL");
@@ -495,6 +501,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_write = reinterpret_cast<decltype(g_write)>(p[4]);
   g_read = reinterpret_cast<decltype(g_read)>(p[5]);
   g_paged = reinterpret_cast<decltype(g_paged)>(p[6]);
+  g_paged_bytes = reinterpret_cast<decltype(g_paged_bytes)>(p[7]);
   Py_RETURN_NONE;
 }
 

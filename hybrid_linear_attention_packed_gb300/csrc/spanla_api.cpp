@@ -2012,7 +2012,7 @@ Bytes bytes_at(const void* p, int64_t n, const char* name) {
 
 // Some of them (a call has at most a dozen).
 struct Ranges {
-  Bytes at[12];
+  Bytes at[16];
   int n = 0;
   void add(const Bytes& b) { at[n++] = b; }
 };
@@ -2178,19 +2178,31 @@ span_la_status encode_tile(CUtensorMap* map, const KvArgs& a, const PagedAttn& p
 
 // The launches of span_la_softmax_paged: sequences of few row heads and those of many each go to their kernel (they
 // tell them apart by the row offsets, which are in device memory).
-span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num_sms, cudaStream_t stream) {
+struct PagedGrids {
+  int unit, step, chunk;      // CTAs of each kernel; 0: not launched
+  size_t step_ws, bytes;      // workspace: of the step kernel, of both
+};
+PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int group, bool e4m3, int num_sms) {
+  PagedGrids g{};
+  g.unit = paged_step_unit(e4m3);
+  const int64_t units = std::max<int64_t>(1, (capacity + g.unit - 1) / g.unit);   // of a sequence and head, at most
+  g.step = group <= kStepHeads ? paged_step_grid(units * heads * std::min<int64_t>(seqs, kStepSeqs), num_sms) : 0;
+  g.chunk = max_rows * group > kStepHeads ? std::min(num_sms, kStepMaxGrid) : 0;
+  g.step_ws = align256(static_cast<size_t>(g.step > 1 ? g.step : 0) * kStepWsFloats * sizeof(float));
+  g.bytes = g.step_ws + static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float);
+  return g;
+}
+
+span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num_sms, void* workspace, cudaStream_t stream) {
   span_la_status st = SPAN_LA_OK;
   CUtensorMap tm_q, tm_k, tm_v;
-  const bool step = p.group <= kStepHeads, chunk = a.max_rows * p.group > kStepHeads;
-  const int unit = paged_step_unit(e4m3);
-  const int64_t units = std::max<int64_t>(1, (a.capacity + unit - 1) / unit);   // of a sequence and head, at most
-  const int step_grid = step ? paged_step_grid(units * a.heads * std::min(a.seqs, kStepSeqs), num_sms) : 0;
-  const int chunk_grid = chunk ? std::min(num_sms, kStepMaxGrid) : 0;
-  const size_t step_ws = align256(static_cast<size_t>(step_grid > 1 ? step_grid : 0) * kStepWsFloats * sizeof(float));
-  const size_t bytes = step_ws + static_cast<size_t>(chunk_grid > 1 ? chunk_grid : 0) * kChunkWsFloats * sizeof(float);
-  float* ws = nullptr;
+  const PagedGrids grids = paged_grids(a.capacity, a.heads, a.seqs, a.max_rows, p.group, e4m3, num_sms);
+  const int unit = grids.unit, step_grid = grids.step, chunk_grid = grids.chunk;
+  const bool step = step_grid > 0, chunk = chunk_grid > 0;
+  const size_t step_ws = grids.step_ws, bytes = grids.bytes;
+  float* ws = static_cast<float*>(workspace);
   cudaError_t e = cudaSuccess;
-  if (bytes > 0) {
+  if (bytes > 0 && workspace == nullptr) {
     if (injected_alloc_failure()) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): injected failure", bytes);
     e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, stream);
     if (e != cudaSuccess) return fail(SPAN_LA_ERR_NOMEM, "cudaMallocAsync(%zu): %s", bytes, cudaGetErrorString(e));
@@ -2226,7 +2238,7 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
         return x;
       });
   }
-  const cudaError_t ef = ws != nullptr ? cudaFreeAsync(ws, stream) : cudaSuccess;
+  const cudaError_t ef = ws != nullptr && workspace == nullptr ? cudaFreeAsync(ws, stream) : cudaSuccess;
   if (e == cudaSuccess) e = ef;
   if (st != SPAN_LA_OK) return st;
   return e == cudaSuccess ? SPAN_LA_OK : cuda_fail(e, "paged attention launch");
@@ -2970,7 +2982,7 @@ span_la_status span_la_kv_read(const span_la_kv_cache* cache, int64_t rows, int3
 
 span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_t rows, int32_t num_q_heads,
                                      const span_la_kv_cache* cache, int32_t max_rows, float scale, void* out,
-                                     float* lse_out, cudaStream_t stream) {
+                                     float* lse_out, void* workspace, cudaStream_t stream) {
   return guarded([&]() -> span_la_status {
     if (max_rows < 0) return fail(SPAN_LA_ERR_INVALID, "max_rows %d < 0", max_rows);
     if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(SPAN_LA_ERR_INVALID, "scale must be finite and >= 0");
@@ -2991,7 +3003,14 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     metadata.add(bytes_at(q, rows_bytes(q_row_stride, rows, num_q_heads, 2), "q"));
     if ((st = check_apart(out_lse, metadata)) != SPAN_LA_OK) return st;
     metadata.add(out_lse);
-    if ((st = check_apart(bytes_at(out, rows * width * 2, "out"), metadata)) != SPAN_LA_OK) return st;
+    const Bytes out_o = bytes_at(out, rows * width * 2, "out");
+    if ((st = check_apart(out_o, metadata)) != SPAN_LA_OK) return st;
+    if (workspace != nullptr) {
+      if (!aligned16(workspace)) return fail(SPAN_LA_ERR_INVALID, "workspace must be 16-byte aligned");
+      const int64_t bytes = span_la_softmax_paged_workspace(rows, num_q_heads, cache, max_rows);
+      metadata.add(out_o);
+      if ((st = check_apart(bytes_at(workspace, bytes, "workspace"), metadata)) != SPAN_LA_OK) return st;
+    }
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != SPAN_LA_OK) return st;
     a.err = dev->err;
@@ -3003,8 +3022,17 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     p.heads = num_q_heads;
     p.group = num_q_heads / a.heads;
     p.scale = scale == 0.f ? 0.125f : scale;
-    return run_paged(a, p, cache->dtype == SPAN_LA_E4M3, dev->num_sms, stream);
+    return run_paged(a, p, cache->dtype == SPAN_LA_E4M3, dev->num_sms, workspace, stream);
   });
+}
+
+int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const span_la_kv_cache* cache, int32_t max_rows) {
+  if (cache == nullptr || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 || rows < 1 ||
+      cache->num_seqs < 1 || max_rows < 0)
+    return 0;
+  return static_cast<int64_t>(paged_grids(static_cast<int64_t>(cache->table_width) * cache->page_rows, cache->num_heads, cache->num_seqs,
+                                          max_rows == 0 ? rows : max_rows, num_q_heads / cache->num_heads,
+                                          cache->dtype == SPAN_LA_E4M3, kStepMaxGrid).bytes);
 }
 
 }  // extern "C"

@@ -38,7 +38,7 @@ EXPORTED = ("span_la_pass", "span_la_branches_from_state", "span_la_check",
             "span_la_selftest_wait_timeout_noalloc", "span_la_pass_variant",
             "span_la_plan_prepare", "span_la_decay_pass", "span_la_decay_branches_from_state",
             "span_la_decay_step", "span_la_qk_norm_rope", "span_la_cache_decay_branches",
-            "span_la_kv_write", "span_la_kv_read", "span_la_softmax_paged")
+            "span_la_kv_write", "span_la_kv_read", "span_la_softmax_paged", "span_la_softmax_paged_workspace")
 NUM_KERNELS = 19
 
 
@@ -158,8 +158,10 @@ def load_library(path: Optional[str] = None):
         lib.span_la_kv_read.argtypes = [cachep, ctypes.c_int64, ctypes.c_int32, vp, vp, vp]
         lib.span_la_kv_read.restype = ctypes.c_int
         lib.span_la_softmax_paged.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, cachep, ctypes.c_int32,
-                                              ctypes.c_float, vp, vp, vp]
+                                              ctypes.c_float, vp, vp, vp, vp]
         lib.span_la_softmax_paged.restype = ctypes.c_int
+        lib.span_la_softmax_paged_workspace.argtypes = [ctypes.c_int64, ctypes.c_int32, cachep, ctypes.c_int32]
+        lib.span_la_softmax_paged_workspace.restype = ctypes.c_int64
         lib.span_la_cache_create.argtypes = [ctypes.c_int32, ctypes.c_int32,
                                              ctypes.POINTER(ctypes.c_void_p)]
         lib.span_la_cache_create.restype = ctypes.c_int
@@ -192,7 +194,8 @@ def _bind_fast(lib) -> None:
         return
     _fastcall.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                      for f in (lib.span_la_decay_pass, lib.span_la_decay_branches_from_state, lib.span_la_decay_step,
-                               lib.span_la_qk_norm_rope, lib.span_la_kv_write, lib.span_la_kv_read, lib.span_la_softmax_paged)])
+                               lib.span_la_qk_norm_rope, lib.span_la_kv_write, lib.span_la_kv_read, lib.span_la_softmax_paged,
+                               lib.span_la_softmax_paged_workspace)])
     _fast = _fastcall
 
 
@@ -873,9 +876,12 @@ def span_la_softmax_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
         max_rows = 1 if row_cu is None else 0
     elif max_rows < 1:
         raise ValueError("max_rows must be at least 1")
+    # The workspace from torch's allocator on the current stream (on another one: the library's own).
+    bytes_ = lib.span_la_softmax_paged_workspace(T, H, c, int(max_rows)) if stream is None else 0
+    ws = torch.empty(bytes_, dtype=torch.uint8, device=q.device) if bytes_ else None
     _raise(lib, lib.span_la_softmax_paged(q.data_ptr(), qs, T, H, c, int(max_rows), float(scale), out.data_ptr(),
-                                          lse.data_ptr() if lse is not None else None, _stream_handle(stream)),
-           "span_la_softmax_paged")
+                                          lse.data_ptr() if lse is not None else None, ws.data_ptr() if bytes_ else None,
+                                          _stream_handle(stream)), "span_la_softmax_paged")
     return out
 
 

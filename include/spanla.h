@@ -667,13 +667,21 @@ span_la_status span_la_kv_read(const span_la_kv_cache *cache, int64_t rows, int3
  *   scale            > 0, or 0 for 1/sqrt(64)
  *   out              device bf16 [rows][num_q_heads][64], 16-byte aligned
  *   lse_out          device fp32 [rows][num_q_heads] or NULL
+ *   workspace        device memory of span_la_softmax_paged_workspace() bytes,
+ *                    16-byte aligned, for this call alone until the stream has
+ *                    passed it; or NULL: allocated and freed on the stream (2 us
+ *                    of it)
  * A row that sees nothing (or nothing but scores of -infinity) gets o = 0 and
  * lse = -infinity.  What a row does not see does not reach it, whatever it holds.
  * Scores, sums and o are fp32; out is rounded to bf16.  Deterministic.
  */
 span_la_status span_la_softmax_paged(const void *q, int64_t q_row_stride, int64_t rows, int32_t num_q_heads,
                                      const span_la_kv_cache *cache, int32_t max_rows, float scale,
-                                     void *out, float *lse_out, cudaStream_t stream);
+                                     void *out, float *lse_out, void *workspace, cudaStream_t stream);
+
+/* Bytes of workspace of a span_la_softmax_paged call with these arguments, on any GPU (host only; 0 on arguments that
+ * the call refuses). */
+int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const span_la_kv_cache *cache, int32_t max_rows);
 
 /*
  * View-state cache ("Serving 0.88M TPS from Two RTXs and Mac Minis", section

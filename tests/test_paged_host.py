@@ -70,7 +70,7 @@ CACHE = [
 def test_every_call_refuses_the_cache(lib, kw, status, what):
     c = _cache(**kw)
     for st in (lib.span_la_kv_write(Q, OUT, 128, 128, 3, 0, c, None), lib.span_la_kv_read(c, 3, 0, Q, OUT, None),
-               lib.span_la_softmax_paged(Q, 256, 3, 4, c, 0, 0.0, OUT, LSE, None)):
+               lib.span_la_softmax_paged(Q, 256, 3, 4, c, 0, 0.0, OUT, LSE, None, None)):
         assert st == status and what in _detail(lib)
 
 
@@ -133,11 +133,14 @@ def test_read_refuses(lib, kw, status, what):
     (dict(lse=OUT + 4), INVALID, "out overlaps lse_out"),
     (dict(lse=LSE + 2), INVALID, "lse_out"),
     (dict(lse=LEN), INVALID, "lse_out overlaps seq_len"),
+    (dict(ws=FAKE * 4096 + 8), INVALID, "workspace must be"),
+    (dict(ws=OUT, max_rows=100), INVALID, "workspace overlaps"),
 ])
 def test_attention_refuses(lib, kw, status, what):
-    a = dict(q=Q, stride=256, heads=4, max_rows=0, scale=0.0, out=OUT, lse=LSE)
+    a = dict(q=Q, stride=256, heads=4, max_rows=0, scale=0.0, out=OUT, lse=LSE, ws=None)
     a.update(kw)
-    st = lib.span_la_softmax_paged(a["q"], a["stride"], 3, a["heads"], _cache(), a["max_rows"], a["scale"], a["out"], a["lse"], None)
+    st = lib.span_la_softmax_paged(a["q"], a["stride"], 3, a["heads"], _cache(), a["max_rows"], a["scale"], a["out"], a["lse"], a["ws"],
+                                   None)
     assert st == status and what in _detail(lib)
 
 
@@ -145,9 +148,18 @@ def test_nothing_to_do_needs_no_device(lib):
     c = _cache(num_seqs=0, page_table=None, seq_len=None, row_cu=None)
     assert lib.span_la_kv_write(None, None, 0, 0, 0, 0, c, None) == 0
     assert lib.span_la_kv_read(c, 0, 1, None, None, None) == 0
-    assert lib.span_la_softmax_paged(None, 0, 0, 4, c, 0, 0.0, None, None, None) == 0
+    assert lib.span_la_softmax_paged(None, 0, 0, 4, c, 0, 0.0, None, None, None, None) == 0
     c = _cache(num_seqs=0, row_cu=CU)             # rows of no sequence
-    assert lib.span_la_softmax_paged(Q, 256, 3, 4, c, 0, 0.0, OUT, None, None) == 0
+    assert lib.span_la_softmax_paged(Q, 256, 3, 4, c, 0, 0.0, OUT, None, None, None) == 0
+
+
+def test_workspace(lib):
+    """Enough for any GPU, nothing where a call has nothing to do or is refused."""
+    f = lib.span_la_softmax_paged_workspace
+    big = _cache(table_width=4000, table_stride=4000)
+    assert f(3, 4, big, 1) > 0 and f(3, 4, big, 100) > f(3, 4, big, 8)
+    assert f(3, 4, big, 0) == f(3, 4, big, 3) and f(3, 4, _cache(), 1) == 0      # (one CTA needs none)
+    assert f(0, 4, _cache(), 1) == 0 and f(3, 5, _cache(), 1) == 0 and f(3, 4, None, 1) == 0 and f(3, 4, _cache(num_seqs=0), 1) == 0
 
 
 def test_layouts_that_interleave_are_taken(lib):
