@@ -39,7 +39,7 @@ constexpr uint32_t kStageBytes = 2 * kTileBytes;      // K, V
 constexpr uint32_t kRawBytes = 2 * kTileRows * 64;    // of e4m3
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColP = 128, kColO = 192, kTileCols = 256;
-constexpr int kPartFloats = kChunkPartFloats;         // of a tile: O [128][64], then m and l of 128 row heads
+constexpr int kPartFloats = kChunkPartFloats;         // of a tile: O [16][128][4], then m and l of 128 row heads
 
 template <bool kE4m3>
 struct Cfg {
@@ -48,7 +48,7 @@ struct Cfg {
   static constexpr int kRaw = kE4m3 ? 2 : 0;
   // Registers of a thread, by warps of four: they add up to what the block is launched with.
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
-  static constexpr int kRegsFew = kE4m3 ? 72 : 88, kRegsConvert = 88, kRegsSoftmax = kE4m3 ? 176 : 208;
+  static constexpr int kRegsFew = 56, kRegsConvert = 88, kRegsSoftmax = kE4m3 ? 184 : 224;
   static_assert((kRegsFew + 2 * kRegsSoftmax + (kE4m3 ? kRegsConvert : 0)) * 128 <= kRegsLaunch * kThreads, "registers");
   static constexpr uint32_t kQ = 0;                                   // [2 buffers][2 tiles]
   static constexpr uint32_t kStage0 = 4 * kTileBytes;
@@ -117,17 +117,18 @@ __device__ __forceinline__ int32_t blocks_of(int32_t len, int32_t n, int32_t b, 
   return max(1, (len - n + min(n, (b + 1) * rows) + kTileRows - 1) >> 7);
 }
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's steps).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's steps), in 32 bits where they are enough.
+template <typename T>
+__device__ __forceinline__ int64_t floor_sum(T n, T m, T a, T b) {
   int64_t sum = 0;
   while (n > 0) {
-    if (a >= m) sum += n * (n - 1) / 2 * (a / m), a %= m;
-    if (b >= m) sum += n * (b / m), b %= m;
-    const int64_t last = a * n + b;
+    if (a >= m) sum += static_cast<int64_t>(n) * (n - 1) / 2 * (a / m), a %= m;
+    if (b >= m) sum += static_cast<int64_t>(n) * (b / m), b %= m;
+    const T last = a * n + b;
     if (last < m) break;
     n = last / m;
     b = last % m;
-    const int64_t x = m;
+    const T x = m;
     m = a, a = x;
   }
   return sum;
@@ -137,15 +138,28 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 __device__ __forceinline__ int64_t blocks_before(int32_t len, int32_t n, int32_t b, int32_t rows) {
   const int32_t items = (n + rows - 1) / rows, full = min(b, items - 1), first = len - n;   // full: items of `rows` rows
   const int32_t one = min(full, max(0, kTileRows - first) / rows);                          // those of one block
-  int64_t sum = one + floor_sum(full - one, kTileRows, rows, static_cast<int64_t>(first) + static_cast<int64_t>(one + 1) * rows + kTileRows - 1);
+  const int64_t start = static_cast<int64_t>(first) + static_cast<int64_t>(one + 1) * rows + kTileRows - 1;
+  const uint32_t more = static_cast<uint32_t>(full - one);
+  int64_t sum = one;
+  if (more > 0) {
+    if (more < (1u << 20) && start < (int64_t(1) << 31))
+      sum += floor_sum<uint32_t>(more, kTileRows, rows, static_cast<uint32_t>(start));
+    else
+      sum += floor_sum<uint64_t>(more, kTileRows, rows, static_cast<uint64_t>(start));
+  }
   if (b == items) sum += blocks_of(len, n, items - 1, rows);
   return sum;
 }
 
-// A run of blocks [j0, j1) of one item.
+// An item counts as so many blocks more than it has: what its start and end cost a CTA that goes from one item to the
+// next (512 rows behind 7,400, 16 heads: the CTAs with two items took 5 us longer than the others, of 26).
+constexpr int32_t kItemBlocks = 3;
+
+// A run of blocks [j0, j1) of one item, and the units it counts for.
 struct Run {
   int s, h;
   int32_t b, j0, j1, blocks;
+  int64_t units;
 };
 
 template <bool kE4m3>
@@ -206,7 +220,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       s_row0[s] = static_cast<int32_t>(r.row0);
       s_n[s] = here ? r.n : 0;
       sum[s] = mine;
-      mine += here ? blocks_before(r.len, r.n, (r.n + item_rows - 1) / item_rows, item_rows) * a.heads : 0;
+      const int32_t items = (r.n + item_rows - 1) / item_rows;
+      mine += here ? (blocks_before(r.len, r.n, items, item_rows) + static_cast<int64_t>(items) * kItemBlocks) * a.heads : 0;
     }
     if (bad) atomicOr(a.err, kErrSequence);
     int64_t upto = mine;
@@ -227,10 +242,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   }
   const uint32_t tmem = *tmem_slot;
   const int64_t U = sum[ns];
-  const int64_t nw = min(static_cast<int64_t>(gridDim.x), U);       // CTAs at work: each has a block at least
-  const int64_t lo = blockIdx.x < nw ? U * blockIdx.x / nw : U, hi = blockIdx.x + 1 < nw ? U * (blockIdx.x + 1) / nw : U;
+  // nw CTAs are at work, each has a unit at least: the first `more` have each + 1 of them, the others `each`.
+  const int64_t nw = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), U));
+  const int64_t each = quotient(U, nw), more = U - each * nw;
+  auto edge_of = [&](int64_t c) { return each * min(c, nw) + min(min(c, nw), more); };
+  const int64_t lo = edge_of(blockIdx.x), hi = edge_of(blockIdx.x + 1);
   // The run of blocks that unit `lo` begins (every warp finds it for itself).
   Run first{};
+  int64_t left = hi - lo;
+  // The run from unit `off` of the item on: its blocks are the units behind the first kItemBlocks.
+  auto take = [&](Run& r, int64_t off) {
+    r.blocks = blocks_of(s_len[r.s], s_n[r.s], r.b, item_rows);
+    r.units = min(static_cast<int64_t>(r.blocks) + kItemBlocks - off, left);
+    r.j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), off - kItemBlocks));
+    r.j1 = static_cast<int32_t>(max(static_cast<int64_t>(r.j0), off + r.units - kItemBlocks));
+    if (r.j1 == r.j0) left = 0;   // (the CTA's units end before the item's blocks begin)
+  };
   if (lo < hi) {
     int l = 0, r = ns;   // the last sequence that starts at lo or before
     while (r - l > 1) {
@@ -240,24 +267,25 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     first.s = l;
     const int32_t len = s_len[l], n = s_n[l], items = (n + item_rows - 1) / item_rows;
-    const int64_t a_head = (sum[l + 1] - sum[l]) / a.heads, in = lo - sum[l];
-    first.h = static_cast<int>(in / a_head);
+    const int64_t a_head = quotient(sum[l + 1] - sum[l], a.heads), in = lo - sum[l];
+    first.h = static_cast<int>(quotient(in, a_head));
     const int64_t rest = in - first.h * a_head;
     int32_t at = 0, count = items;   // the last item that starts at `rest` or before, 32 at a time
+    int64_t begin = 0;
     while (count > 1) {
       const int32_t step = (count + 31) / 32, mine = at + lane * step;
-      const int upto = __popc(__ballot_sync(0xffffffffu, mine < at + count && blocks_before(len, n, mine, item_rows) <= rest));
-      const int32_t from = max(upto - 1, 0) * step;
+      const int64_t b = mine < at + count ? blocks_before(len, n, mine, item_rows) + static_cast<int64_t>(mine) * kItemBlocks : INT64_MAX;
+      const int upto = max(__popc(__ballot_sync(0xffffffffu, b <= rest)) - 1, 0);
+      begin = __shfl_sync(0xffffffffu, b, upto);
+      const int32_t from = upto * step;
       count = min(step, count - from);
       at += from;
     }
     first.b = at;
-    first.blocks = blocks_of(len, n, at, item_rows);
-    first.j0 = static_cast<int32_t>(rest - blocks_before(len, n, at, item_rows));
-    first.j1 = static_cast<int32_t>(min(static_cast<int64_t>(first.blocks), first.j0 + (hi - lo)));
+    take(first, rest - begin);
   }
   auto next_run = [&](Run& r, int64_t& left) {
-    left -= r.j1 - r.j0;
+    left -= r.units;
     if (left <= 0) return;
     if ((r.b + 1) * static_cast<int64_t>(item_rows) < s_n[r.s]) {
       ++r.b;
@@ -269,15 +297,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         while (sum[r.s + 1] == sum[r.s]);
       }
     }
-    r.blocks = blocks_of(s_len[r.s], s_n[r.s], r.b, item_rows);
-    r.j0 = 0;
-    r.j1 = static_cast<int32_t>(min(static_cast<int64_t>(r.blocks), left));
+    take(r, 0);
   };
   // Rows of tile x of a run's item.
   auto rows_of = [&](const Run& r, int x) { return max(0, min(tile_rows, s_n[r.s] - r.b * item_rows - x * tile_rows)); };
 
   Run r = first;
-  int64_t left = hi - lo;
   if (warp < 4) {
     regs_dec<C::kRegsFew>();
     if (warp == 0) {
@@ -377,8 +402,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           }
         }
         if (r.j0 == 0 && r.j1 < r.blocks) {
-          const int64_t end = hi + (r.blocks - r.j1);   // of the item's units
-          join.parts = static_cast<int32_t>((end * nw - 1) / U) - static_cast<int32_t>(blockIdx.x) + 1;
+          const int64_t u = hi + (r.blocks - r.j1) - 1;   // the item's last unit, and the CTA that has it
+          const int64_t c = u < more * (each + 1) ? quotient(u, each + 1) : more + quotient(u - more * (each + 1), each);
+          join.parts = static_cast<int32_t>(c) - static_cast<int32_t>(blockIdx.x) + 1;
           join.s = s0 + r.s;
           join.h = r.h;
           join.first = r.b * item_rows;
@@ -594,10 +620,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m2, 0.6931471805599453f, logf(l));
       } else if (live) {
-        float4* dst = reinterpret_cast<float4*>(part + row * kHeadDim);
+        float4* dst = reinterpret_cast<float4*>(part) + row;   // four elements of all row heads, then the next four
 #pragma unroll
         for (int c = 0; c < 16; ++c)
-          dst[c] = make_float4(__uint_as_float(o[c >> 3][4 * (c & 7)]), __uint_as_float(o[c >> 3][4 * (c & 7) + 1]),
+          dst[c * kTileRows] = make_float4(__uint_as_float(o[c >> 3][4 * (c & 7)]), __uint_as_float(o[c >> 3][4 * (c & 7) + 1]),
                                __uint_as_float(o[c >> 3][4 * (c & 7) + 2]), __uint_as_float(o[c >> 3][4 * (c & 7) + 3]));
         part[kTileRows * kHeadDim + row] = m2;
         part[kTileRows * kHeadDim + kTileRows + row] = l;
@@ -687,90 +713,84 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // CTA (c, y): 32 row heads (y & 3) of tile y >> 2 of the item that begins in CTA c of the chunk kernel and goes on, from
-// the parts of it and the next CTAs.  A group of 16 lanes has two row heads: its lanes the parts' maxima and sums, then
-// four elements of O each.  What an item of two parts needs is asked for before the record is there that says how many
-// there are.
-constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16, kJoinBoth = 2;
+// the parts of it and the next CTAs.  A lane has a row head, warp w eight elements of O, and the maxima and sums of every
+// eighth part.  What an item of two parts needs is asked for before the record is there that says how many there are.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinAhead = 2;
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
                                                                   const float* __restrict__ ws) {
-  __shared__ float factor[16][kJoinBoth][kStepMaxGrid];
+  __shared__ float factor[kStepMaxGrid][32];
+  __shared__ float best[kJoinWarps][32], sums[kJoinWarps][32];
+  __shared__ uint32_t wild;
   griddep_wait();
   const float* mine = ws + blockIdx.x * kChunkWsFloats;
-  const int x = blockIdx.y >> 2, grp = threadIdx.x >> 4, sub = threadIdx.x & 15, row0 = (blockIdx.y & 3) * 32 + grp;
+  const int x = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (blockIdx.y & 3) * 32 + lane;
   const int last = static_cast<int>(gridDim.x - 1 - blockIdx.x);
   auto part_of = [&](int i) { return mine + i * kChunkWsFloats + (2 * (i == 0 ? 1 : 0) + x) * kPartFloats; };
+  auto four = [&](int i, int c) { return reinterpret_cast<const float4*>(part_of(i))[(2 * warp + c) * kTileRows + row]; };
   const ChunkJoin j = *reinterpret_cast<const ChunkJoin*>(mine + 4 * kPartFloats);
-  float pm0[kJoinBoth], pl0[kJoinBoth];
-  float4 ahead[kJoinBoth][2];
-#pragma unroll
-  for (int b = 0; b < kJoinBoth; ++b) {
-    const float* st = part_of(min(sub, last)) + kTileRows * kHeadDim + row0 + 16 * b;
-    pm0[b] = st[0], pl0[b] = st[kTileRows];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      ahead[b][i] = *reinterpret_cast<const float4*>(part_of(min(i, last)) + (row0 + 16 * b) * kHeadDim + 4 * sub);
+  float m0, l0;
+  {
+    const float* st = part_of(min(warp, last)) + kTileRows * kHeadDim + row;
+    m0 = st[0], l0 = st[kTileRows];
   }
-  if (j.parts == 0) return;
-  const int32_t tile_rows = kTileRows / p.group;
-  uint32_t which[kJoinBoth];
+  float4 ahead[kJoinAhead][2];
 #pragma unroll
-  for (int b = 0; b < kJoinBoth; ++b) {
-    const int row = row0 + 16 * b;
-    const int32_t in = j.first + x * tile_rows + row / p.group;
-    const bool live = row / p.group < tile_rows && in < j.n;
-    float pm[kJoinEach], pl[kJoinEach], m = -INFINITY, l = 0.f;
+  for (int i = 0; i < kJoinAhead; ++i) ahead[i][0] = four(min(i, last), 0), ahead[i][1] = four(min(i, last), 1);
+  const int32_t tile_rows = kTileRows / p.group, in = j.first + x * tile_rows + row / p.group;
+  const bool live = j.parts > 0 && row / p.group < tile_rows && in < j.n;
+  if (threadIdx.x == 0) wild = 0;
+  if (!__syncthreads_or(live)) return;
+  float m = warp < j.parts ? m0 : -INFINITY, l = 0.f;
+  for (int i = warp + kJoinWarps; i < j.parts; i += kJoinWarps) m = fmaxf(m, part_of(i)[kTileRows * kHeadDim + row]);
+  best[warp][lane] = m;
+  __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kJoinEach; ++k) {
-      if (16 * k >= j.parts) break;
-      const int i = sub + 16 * k;
-      pm[k] = -INFINITY, pl[k] = 0.f;
-      if (live && i < j.parts) {
-        const float* st = part_of(i) + kTileRows * kHeadDim + row;
-        pm[k] = k == 0 ? pm0[b] : st[0], pl[k] = k == 0 ? pl0[b] : st[kTileRows];
-      }
-      m = fmaxf(m, pm[k]);
-    }
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, best[w][lane]);
+  for (int i = warp; i < j.parts; i += kJoinWarps) {
+    const float* st = part_of(i) + kTileRows * kHeadDim + row;
+    const float pm = i == warp ? m0 : st[0], pl = i == warp ? l0 : st[kTileRows];
+    const float f = pm == m ? 1.f : pm == -INFINITY ? 0.f : ex2(pm - m);
+    factor[i][lane] = f;
+    l += pl * f;
+  }
+  sums[warp][lane] = l;
+  __syncthreads();
+  l = 0.f;
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  for (int w = 0; w < kJoinWarps; ++w) l += sums[w][lane];
+  if (live) {
+    float o[8] = {};
+    auto add = [&](const float4& y, int c, float f) {
+      o[4 * c] = fmaf(f, y.x, o[4 * c]), o[4 * c + 1] = fmaf(f, y.y, o[4 * c + 1]);
+      o[4 * c + 2] = fmaf(f, y.z, o[4 * c + 2]), o[4 * c + 3] = fmaf(f, y.w, o[4 * c + 3]);
+    };
 #pragma unroll
-    for (int k = 0; k < kJoinEach; ++k) {
-      if (16 * k >= j.parts) break;
-      const float f = pm[k] == m ? 1.f : pm[k] == -INFINITY ? 0.f : ex2(pm[k] - m);
-      l += pl[k] * f;
-      factor[grp][b][sub + 16 * k] = f;
-    }
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    __syncwarp();
-    bool wild = false;
-    if (live) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](const float4& y, float f) {
-        o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
-      };
-      add(ahead[b][0], factor[grp][b][0]);
-      add(ahead[b][1], factor[grp][b][1]);   // (there are two parts at least)
+    for (int i = 0; i < kJoinAhead; ++i) add(ahead[i][0], 0, factor[i][lane]), add(ahead[i][1], 1, factor[i][lane]);   // (two at least)
 #pragma unroll 4
-      for (int i = 2; i < j.parts; ++i)
-        add(*reinterpret_cast<const float4*>(part_of(i) + row * kHeadDim + 4 * sub), factor[grp][b][i]);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t at = (j.row0 + static_cast<int64_t>(in)) * p.heads + j.h * p.group + row % p.group;
-      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-      wild = !(fabsf(o.x) <= 3.4e38f) || !(fabsf(o.y) <= 3.4e38f) || !(fabsf(o.z) <= 3.4e38f) || !(fabsf(o.w) <= 3.4e38f);
-      *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * sub) =
-          l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-      if (p.lse != nullptr && sub == 0) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+    for (int i = kJoinAhead; i < j.parts; ++i) add(four(i, 0), 0, factor[i][lane]), add(four(i, 1), 1, factor[i][lane]);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = (j.row0 + static_cast<int64_t>(in)) * p.heads + j.h * p.group + row % p.group;
+    bool w = false;
+    uint32_t pk[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float y0 = o[2 * c] * inv, y1 = o[2 * c + 1] * inv;
+      w |= !(fabsf(y0) <= 3.4e38f) || !(fabsf(y1) <= 3.4e38f);
+      pk[c] = l == 0.f ? 0u : pack_bf16x2(y0, y1);
     }
-    which[b] = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
+    *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 8 * warp) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    if (p.lse != nullptr && warp == 0) p.lse[at] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+    if (w && l == l && l != 0.f) atomicOr(&wild, 1u << lane);
   }
-  __syncwarp();
-#pragma unroll 1
-  for (int k = 0; k < 2 * kJoinBoth; ++k) {   // the warp's row heads
-    const int b = k >> 1, half = k & 1;
-    if ((((b == 0 ? which[0] : which[1]) >> (16 * half)) & 0xffffu) == 0) continue;
-    const int rr = __shfl_sync(0xffffffffu, row0, 16 * half) + 16 * b, at = j.first + x * tile_rows + rr / p.group;
+  __syncthreads();
+  uint32_t which = wild;
+  for (int k = 0; which != 0; ++k) {   // the row heads that are done over, a warp each
+    const int i = __ffs(which) - 1;
+    which &= which - 1;
+    if (k % kJoinWarps != warp) continue;
+    const int rr = (blockIdx.y & 3) * 32 + i, at = j.first + x * tile_rows + rr / p.group;
     attend_row<kE4m3>(a, p, j.s, j.row0 + static_cast<int64_t>(at), j.h * p.group + rr % p.group, max(0, j.len - j.n + at + 1));
   }
 }

@@ -112,11 +112,6 @@ struct At {
   int32_t blk, units;  // unit of the item, units of the item
 };
 
-// a / b, quickly where both fit 32 bits.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-}
-
 // Output of a row head: elements d, d + 1.
 __device__ __forceinline__ void store_pair(const PagedAttn& p, int64_t at, int d, float x, float y) {
   *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + d) = pack_bf16x2(x, y);

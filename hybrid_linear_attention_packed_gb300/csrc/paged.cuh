@@ -59,6 +59,11 @@ __device__ __forceinline__ void check_sequences(const KvArgs& a) {
   if (bad) atomicOr(a.err, kErrSequence);
 }
 
+// a / b, quickly where both fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // 2^(code - 127); 255 is NaN.
 __device__ __forceinline__ float scale_of(uint32_t code) {
   return __uint_as_float(code == 0 ? 0x00400000u : code == 255 ? 0x7fffffffu : code << 23);
