@@ -9,10 +9,13 @@
 // that, as the next value of the grid is not an fp32 number.  Infinite and NaN
 // elements are held as NaN.
 //
-// A CTA of 8 warps takes 32 packed rows; each warp one head of K or V of them at
-// a time, 8 lanes a row (16 bytes of bf16 a lane), 4 rows at once, all 32 in
-// flight.  Consecutive rows of one head are neighbours in a page, and the 32
-// powers of two go out as one store.
+// A CTA of 8 warps takes 32 packed rows; each warp one head of K or V of 16 of them
+// at a time, 8 lanes a row (16 bytes of bf16 a lane), 4 rows at once, all 16 in
+// flight.  Consecutive rows of one head are neighbours in a page, and their powers
+// of two go out as one store.  (All 32 rows at once: twice the registers and half
+// the warps, 45 us for four prompts of fp32 rows instead of 40.)  Few rows are bound
+// by the reads that find their places, one behind the other: lengths, then the
+// page; the rows themselves are on their way meanwhile.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -20,8 +23,8 @@
 namespace spanla {
 namespace {
 
-constexpr int kRows = 32, kWarps = 8, kSteps = kRows / 4;
-constexpr int64_t kBlocks = 608;   // four for each of 152 SMs
+constexpr int kRows = 32, kWarps = 8, kSteps = 4;
+constexpr int64_t kBlocks = 4864;   // 32 for each of 152 SMs
 
 struct Places {            // of a CTA's rows: element offset of head 0 in the pages (-1: none), byte offset in the scales
   int64_t at[kRows], scale_at[kRows];
@@ -145,34 +148,36 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// Units u: K of head u / 2 (u even) or V; a CTA's warps take every so manieth one.
+// Units u: 16 of the rows (u & 1: the second 16), K or V (u & 2), head u / 4; a CTA's warps take every so manieth one.
 template <typename T, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows in) {
   __shared__ Places pl;
+  griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
   Eight<T> x[kSteps];
   auto load = [&](int unit) {   // (rows of no sequence too: their places are not known yet)
-    const T* src = static_cast<const T*>((unit & 1) ? in.v : in.k) + (unit >> 1) * kHeadDim + sub * 8;
-    const int64_t stride = (unit & 1) ? in.v_row_stride : in.k_row_stride;
+    const T* src = static_cast<const T*>((unit & 2) ? in.v : in.k) + (unit >> 2) * kHeadDim + sub * 8;
+    const int64_t stride = (unit & 2) ? in.v_row_stride : in.k_row_stride;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int64_t t = t0 + 4 * i + (lane >> 3);
+      const int64_t t = t0 + 16 * (unit & 1) + 4 * i + (lane >> 3);
       x[i] = Eight<T>{};
       if (t < a.rows) x[i].load(src + t * stride);
     }
   };
   const int first = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (first < 2 * a.heads) load(first);
+  if (first < 4 * a.heads) load(first);
   find_places(a, pl);
-  for (int unit = first; unit < 2 * a.heads; unit += gridDim.y * kWarps) {
-    const int head = unit >> 1;
-    const bool is_v = unit & 1;
+  for (int unit = first; unit < 4 * a.heads; unit += gridDim.y * kWarps) {
+    const int head = unit >> 2, half = 16 * (unit & 1);
+    const bool is_v = unit & 2;
     if (unit != first) load(unit);
-    uint32_t code = 0;   // row `lane`'s power of two
+    uint32_t code = 0;   // row `half + lane`'s power of two, lanes 0 .. 15
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int r = 4 * i + (lane >> 3);
+      const int r = half + 4 * i + (lane >> 3);
       const int64_t at = pl.at[r] + head * a.head_stride + sub * 8;
       if (kE4m3) {
         float f[8];
@@ -214,37 +219,39 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
         y.store(static_cast<__nv_bfloat16*>(is_v ? a.v : a.k) + at);
       }
     }
-    if (kE4m3 && pl.at[lane] >= 0)
-      (is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride] = static_cast<uint8_t>(code);
+    if (kE4m3 && lane < 16 && pl.at[half + lane] >= 0)
+      (is_v ? a.v_scale : a.k_scale)[pl.scale_at[half + lane] + head * a.scale_head_stride] = static_cast<uint8_t>(code);
   }
 }
 
 template <typename T, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvRows to) {
   __shared__ Places pl;
+  griddep_wait();
+  griddep_launch_dependents();
   find_places(a, pl);
   const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  for (int unit = blockIdx.y * kWarps + (threadIdx.x >> 5); unit < 2 * a.heads; unit += gridDim.y * kWarps) {
-    const int head = unit >> 1;
-    const bool is_v = unit & 1;
+  for (int unit = blockIdx.y * kWarps + (threadIdx.x >> 5); unit < 4 * a.heads; unit += gridDim.y * kWarps) {
+    const int head = unit >> 2, half = 16 * (unit & 1);
+    const bool is_v = unit & 2;
     T* dst = static_cast<T*>(is_v ? to.v : to.k) + head * kHeadDim + sub * 8;
     const int64_t stride = is_v ? to.v_row_stride : to.k_row_stride;
     if (kE4m3) {
       uint2 raw[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int r = 4 * i + (lane >> 3);
+        const int r = half + 4 * i + (lane >> 3);
         raw[i] = make_uint2(0u, 0u);
         if (pl.at[r] >= 0)
           raw[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8));
       }
       const float scale =
-          pl.at[lane] >= 0 ? scale_of((is_v ? a.v_scale : a.k_scale)[pl.scale_at[lane] + head * a.scale_head_stride]) : 0.f;
+          pl.at[half + (lane & 15)] >= 0 ? scale_of((is_v ? a.v_scale : a.k_scale)[pl.scale_at[half + (lane & 15)] + head * a.scale_head_stride]) : 0.f;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const float e = __shfl_sync(0xffffffffu, scale, r);
+        const int r = half + 4 * i + (lane >> 3);
+        const float e = __shfl_sync(0xffffffffu, scale, r - half);
         const uint32_t w[2] = {raw[i].x, raw[i].y};
         float f[8];
 #pragma unroll
@@ -260,12 +267,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
       Eight<__nv_bfloat16> x[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int r = 4 * i + (lane >> 3);
+        const int r = half + 4 * i + (lane >> 3);
         if (pl.at[r] >= 0) x[i].load(static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8);
       }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int r = 4 * i + (lane >> 3);
+        const int r = half + 4 * i + (lane >> 3);
         Eight<T> y;
         convert(x[i], y);
         if (pl.at[r] >= 0) y.store(dst + (t0 + r) * stride);
@@ -276,14 +283,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
 
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t stream) {
-  // A CTA takes all heads of its rows where there are CTAs enough: finding the rows' places takes four reads one behind
-  // the other, as long as copying a few heads.
+  // A CTA takes several heads of its rows where there are CTAs enough: finding the rows' places takes as long as copying a
+  // few heads.  (Sixteen views read from e4m3 pages: all heads 94 us, with 32 CTAs an SM 91, one head a warp 98; four
+  // prompts written: 49, 40, 39.)
   const int64_t blocks = (a.rows + kRows - 1) / kRows;
-  const int64_t eights = (2 * a.heads + kWarps - 1) / kWarps;
+  const int64_t eights = (4 * a.heads + kWarps - 1) / kWarps;
   const int64_t turns = std::max<int64_t>(1, eights * blocks / kBlocks), split = (eights + turns - 1) / turns;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
-  kernel<<<grid, kWarps * 32, 0, stream>>>(a, x);
-  return cudaGetLastError();
+  return launch_behind(kernel, grid, kWarps * 32, 0, stream, a, x);
 }
 
 }  // namespace

@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   __shared__ float factor[kStepMaxGrid][32];
   __shared__ float best[kJoinWarps][32], sums[kJoinWarps][32];
   __shared__ uint32_t wild;
+  griddep_launch_dependents();
   griddep_wait();
   const float* mine = ws + blockIdx.x * kChunkWsFloats;
   const int x = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (blockIdx.y & 3) * 32 + lane;
@@ -810,17 +811,10 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
   const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kRequest;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<kE4m3>, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
+  if (behind)   // (see the kernel's end)
+    return launch_behind(paged_chunk_kernel<kE4m3>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
+  paged_chunk_kernel<kE4m3><<<grid, C::kThreads, C::kRequest, stream>>>(tm_q, tm_k, tm_v, a, p, s0, ns, ws);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -832,16 +826,7 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
 }
 
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, 8);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return e4m3 ? cudaLaunchKernelEx(&cfg, chunk_join_kernel<true>, a, p, ws) : cudaLaunchKernelEx(&cfg, chunk_join_kernel<false>, a, p, ws);
+  return launch_behind(e4m3 ? chunk_join_kernel<true> : chunk_join_kernel<false>, dim3(grid, 8), kJoinThreads, 0, stream, a, p, ws);
 }
 
 }  // namespace spanla

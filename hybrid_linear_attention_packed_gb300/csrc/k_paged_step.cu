@@ -166,6 +166,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       tma_prefetch_desc(&tm_v);
     }
   }
+  griddep_wait();                // (what comes before the call)
   griddep_launch_dependents();   // (the next kernels of the call wait for this grid's end, or need not)
   // ---------------------------------------------------------------- the sequences' running sums of units
   {
@@ -858,8 +859,7 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArg
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3, kTwo>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  paged_step_kernel<kE4m3, kTwo><<<grid, C::kWarps * 32, C::kRequest, stream>>>(tm_k, tm_v, a, p, s0, ns, ws);
-  return cudaGetLastError();
+  return launch_behind(paged_step_kernel<kE4m3, kTwo>, dim3(grid), C::kWarps * 32, C::kRequest, stream, tm_k, tm_v, a, p, s0, ns, ws);
 }
 
 }  // namespace
@@ -883,17 +883,9 @@ cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
 }
 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
   const int64_t most = std::min<int64_t>(kM, a.max_rows * p.group);   // row heads
-  cfg.gridDim = dim3(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return e4m3 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<true>, a, p, ws) : cudaLaunchKernelEx(&cfg, paged_join_kernel<false>, a, p, ws);
+  const dim3 ctas(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
+  return launch_behind(e4m3 ? paged_join_kernel<true> : paged_join_kernel<false>, ctas, kJoinThreads, 0, stream, a, p, ws);
 }
 
 }  // namespace spanla

@@ -7,6 +7,8 @@
 // touched, and either sets a bit of the device error word (span_la_check).
 #pragma once
 
+#include <utility>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -57,6 +59,23 @@ __device__ __forceinline__ void check_sequences(const KvArgs& a) {
   bool bad = false;
   for (int s = threadIdx.x; s < a.seqs; s += blockDim.x) seq_rows(a, s, &bad);
   if (bad) atomicOr(a.err, kErrSequence);
+}
+
+// A launch whose CTAs may come up while the kernel before it in the stream still runs; they wait for its end
+// (griddep_wait) before they touch memory.  Calls one behind the other then do not wait for each other's launch.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // a / b, quickly where both fit 32 bits.
