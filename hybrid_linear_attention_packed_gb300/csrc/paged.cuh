@@ -115,34 +115,53 @@ __device__ __forceinline__ float2 cached_pair(const KvArgs& a, const void* base,
 
 // Softmax attention of one packed row t and query head by one warp, in fp32
 // throughout: the row of sequence s that sees its first `seen` rows.  The other
-// kernels send a row here whose products came out infinite or NaN: they multiply
-// rows that the row does not see by 0, this does not touch them.
+// kernels send a row here whose products came out infinite or NaN though its sum of
+// weights is finite: they multiply rows that the row does not see by 0, this does
+// not touch them.  (0.15 us a cached row, four of them at a time: a step of nothing
+// but NaN takes some hundred times as long as another.)
 template <bool kE4m3>
 __device__ __noinline__ void attend_row(const KvArgs& a, const PagedAttn& p, int s, int64_t t, int head, int32_t seen) {
+  constexpr int kAtOnce = 4;
   const int lane = threadIdx.x & 31, kvh = head / p.group;
   const float2 q = __bfloat1622float2(
       *reinterpret_cast<const __nv_bfloat162*>(p.q + t * p.q_row_stride + head * kHeadDim + 2 * lane));
   float m = -INFINITY, l = 0.f;
   float2 o = make_float2(0.f, 0.f);
   bool bad = false;
-  for (int32_t j = 0; j < seen; ++j) {
-    const int32_t page = page_of(a, s, j);
+  for (int32_t j0 = 0; j0 < seen; j0 += kAtOnce) {   // (a page holds a multiple of kAtOnce rows)
+    const int32_t page = page_of(a, s, j0);
     if (page < 0) {
       bad = true;
       continue;
     }
-    const float2 k = cached_pair<kE4m3>(a, a.k, a.k_scale, page, j, kvh, lane);
-    float x = q.x * k.x + q.y * k.y;
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= p.scale;
-    if (x == -INFINITY) continue;   // weight 0
-    const float2 v = cached_pair<kE4m3>(a, a.v, a.v_scale, page, j, kvh, lane);
-    const float m_new = x > m || x != x ? x : m;
-    const float old = m == m_new ? 1.f : m == -INFINITY ? 0.f : expf(m - m_new), w = expf(x - m_new);
-    l = l * old + w;
-    o.x = (old == 0.f ? 0.f : o.x * old) + w * v.x;
-    o.y = (old == 0.f ? 0.f : o.y * old) + w * v.y;
-    m = m_new;
+    const int n = min(kAtOnce, seen - j0);
+    float2 v[kAtOnce];
+    float x[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      v[i] = make_float2(0.f, 0.f), x[i] = 0.f;
+      if (i >= n) continue;
+      const float2 k = cached_pair<kE4m3>(a, a.k, a.k_scale, page, j0 + i, kvh, lane);
+      v[i] = cached_pair<kE4m3>(a, a.v, a.v_scale, page, j0 + i, kvh, lane);
+      x[i] = q.x * k.x + q.y * k.y;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i >= n) break;
+      const float y = x[i] * p.scale;
+      if (y == -INFINITY) continue;   // weight 0
+      const float m_new = y > m || y != y ? y : m;
+      const float old = m == m_new ? 1.f : m == -INFINITY ? 0.f : expf(m - m_new), w = expf(y - m_new);
+      l = l * old + w;
+      o.x = (old == 0.f ? 0.f : o.x * old) + w * v[i].x;
+      o.y = (old == 0.f ? 0.f : o.y * old) + w * v[i].y;
+      m = m_new;
+    }
   }
   if (bad && lane == 0) atomicOr(a.err, kErrPage);
   const bool none = l == 0.f;

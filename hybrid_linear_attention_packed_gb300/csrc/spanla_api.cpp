@@ -2147,6 +2147,11 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
   return SPAN_LA_OK;
 }
 
+// The most packed rows of a sequence that a call may have.
+int64_t most_rows(const span_la_kv_cache* c, int64_t rows, int32_t max_rows) {
+  return max_rows != 0 ? max_rows : c != nullptr && c->row_cu == nullptr ? 1 : rows;
+}
+
 // Boxes of `rows` rows of one page and head, out of pages [pages][heads][page_rows][64].
 span_la_status encode_pages(CUtensorMap* map, const void* base, const KvArgs& a, bool e4m3, int rows) {
   const cuuint64_t esz = e4m3 ? 1 : 2;
@@ -2988,7 +2993,7 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(SPAN_LA_ERR_INVALID, "scale must be finite and >= 0");
     KvArgs a{};
     Ranges pages, metadata;
-    span_la_status st = check_kv_cache(cache, rows, max_rows == 0 ? rows : max_rows, false, &a, &pages, &metadata);
+    span_la_status st = check_kv_cache(cache, rows, most_rows(cache, rows, max_rows), false, &a, &pages, &metadata);
     if (st != SPAN_LA_OK) return st;
     if (num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % a.heads != 0 || num_q_heads / a.heads > 128)
       return fail(SPAN_LA_ERR_INVALID, "num_q_heads %d is not a multiple of %d heads, at most 128 times it", num_q_heads, a.heads);
@@ -3031,7 +3036,7 @@ int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const
       cache->num_seqs < 1 || max_rows < 0)
     return 0;
   return static_cast<int64_t>(paged_grids(static_cast<int64_t>(cache->table_width) * cache->page_rows, cache->num_heads, cache->num_seqs,
-                                          max_rows == 0 ? rows : max_rows, num_q_heads / cache->num_heads,
+                                          most_rows(cache, rows, max_rows), num_q_heads / cache->num_heads,
                                           cache->dtype == SPAN_LA_E4M3, kStepMaxGrid).bytes);
 }
 

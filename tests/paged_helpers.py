@@ -59,8 +59,8 @@ def values(pages, scale):
 def check_attention(q, got, lse, cache, table, lens, cu, scale, weight_error, max_rows=None):
     """Every row against the float64 form.  Bounds: a score is off by at most 66 roundings of its products' sizes
     (64 products and sums, the scale) and 2^-23 of itself where it is multiplied for a power of two; a weight by twice
-    that (its own and the sum's), 2^-21 of exponentials and `weight_error` for what the weights are rounded to; the sum
-    of weights by a rounding for each of its terms.  Then o's own rounding."""
+    that (its own and the sum's), 2^-21 of exponentials and what the weights are rounded to (`weight_error` of a
+    sequence's packed rows); the sum of weights by a rounding for each of its terms.  Then o's own rounding."""
     k, v, ks, vs = cache
     K, V = values(k, ks), values(v, vs)
     qn, o, z = f64(q), f64(got), None if lse is None else f64(lse)
@@ -72,7 +72,7 @@ def check_attention(q, got, lse, cache, table, lens, cu, scale, weight_error, ma
         top = np.where(np.isfinite(rl), np.abs(rl), 0) + size
         ds = 66 * U32 * size + 2.0 ** -23 * top
         dw = 2 * ds + 2.0 ** -21 + L * U32
-        tol = 1.01 * U16 * np.abs(ref) + (weight_error + dw + (L + 64) * U32)[..., None] * mass + 1e-37
+        tol = 1.01 * U16 * np.abs(ref) + (weight_error(e - b) + dw + (L + 64) * U32)[..., None] * mass + 1e-37
         bad = ~(np.abs(o[b:e] - ref) <= tol)
         assert not bad.any(), (s, L, e - b, np.argwhere(bad)[:3], np.max(np.abs(o[b:e] - ref) / np.maximum(tol, 1e-300)))
         if z is not None:

@@ -12,8 +12,10 @@ from paged_helpers import BF16, E4M3, U16, check_attention, f64, i32, make_pages
 
 pytestmark = pytest.mark.gpu
 
-# What the weights are rounded to: to bf16, half a step (where they are held more exactly, so much the better).
-WEIGHTS = U16
+def weights(G, cache):
+    """What the weights of n packed rows are rounded to, at most: more than 16 row heads to bf16; fewer to a sum of two
+    bf16 numbers, or, over e4m3 pages, to fp16."""
+    return lambda n: U16 if n * G > 16 else 2.0 ** -16 if cache == BF16 else 2.0 ** -11
 
 
 def _setup(lens, rows, G, H, R, cache, dev, seed=0, layout="plain", v_size=1.0, q_size=1.0, width=None):
@@ -70,7 +72,7 @@ def test_attention(cuda_device, case, cache):
     lens, rows, G, H, R = CASES[case]
     q, c, table, cu = _setup(lens, rows, G, H, R, cache, cuda_device, seed=case)
     out, lse = _run(q, c, table, lens, cu, cuda_device)
-    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(G, cache))
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3])
@@ -84,7 +86,7 @@ def test_other_layouts_and_strided_queries(cuda_device, layout, cache, rows):
     big = torch.full((2, 40), 1 << 30, dtype=torch.int32, device=cuda_device)         # a part of a wider table
     big[:, 5:5 + table.shape[1]] = i32(table, cuda_device)
     out, lse = _run(q, c, table, lens, cu, cuda_device)
-    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(2, cache))
     again = span_la_softmax_paged(strided, c[0], c[1], big[:, 5:5 + table.shape[1]], i32(lens, cuda_device), i32(cu, cuda_device),
                                   c[2], c[3])
     span_la_check()
@@ -99,7 +101,7 @@ def test_scales(cuda_device, rows, scale, q_size, cache):
     lens = [500, 70]
     q, c, table, cu = _setup(lens, [rows, rows], 2, 2, 64, cache, cuda_device, seed=7, q_size=q_size)
     out, lse = _run(q, c, table, lens, cu, cuda_device, scale=scale)
-    check_attention(q, out, lse, c, table, lens, cu, scale, WEIGHTS)
+    check_attention(q, out, lse, c, table, lens, cu, scale, weights(2, cache))
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3])
@@ -120,7 +122,7 @@ def test_values_of_far_sizes(cuda_device, rows, big, small, cache):
     all_cu = np.concatenate([[0], np.cumsum(lens)])
     span_la_kv_write(k, v, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), i32(all_cu, cuda_device), c[2], c[3])
     out, lse = _run(q, c, table, lens, cu, cuda_device, scale=1.0)
-    check_attention(q, out, lse, c, table, lens, cu, 1.0, WEIGHTS)
+    check_attention(q, out, lse, c, table, lens, cu, 1.0, weights(2, cache))
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3])
@@ -130,7 +132,7 @@ def test_rows_that_see_nothing(cuda_device, rows, G, cache):
     lens, n = [0, rows // 2, 40, 1, rows - 1, 300], [rows, rows, 0, rows, rows, rows]
     q, c, table, cu = _setup(lens, n, G, 2, 16, cache, cuda_device, seed=9)
     out, lse = _run(q, c, table, lens, cu, cuda_device)
-    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(G, cache))
     assert (out[:rows] == 0).all() and torch.isneginf(lse[:rows]).all()
 
 
@@ -153,7 +155,7 @@ def test_what_a_row_does_not_see_does_not_reach_it(cuda_device, rows, G, cache, 
         if x == 0:                                       # keys that are not seen change no bit
             assert torch.equal(out[keep], clean[keep])
         ref_cu = np.concatenate([[0], np.cumsum([rows - 1] * 3)])
-        check_attention(q[keep], out[keep], lse[keep], c, table, before, ref_cu, 0.125, WEIGHTS)
+        check_attention(q[keep], out[keep], lse[keep], c, table, before, ref_cu, 0.125, lambda n: weights(G, cache)(n + 1))
         seen = f64(out[cu[1] + rows - 1])
         if x == 1 and not (cache == E4M3 and np.isfinite(what)):
             finite = np.ones(64, dtype=bool)
@@ -170,13 +172,13 @@ def test_other_rows_of_the_call_are_left(cuda_device):
     q = torch.cat([q, q])
     cu = [2, 12, 14, 16]
     out, _ = _run(q, c, table, lens, cu, cuda_device)
-    check_attention(q, out, None, c, table, lens, cu, 0.125, WEIGHTS)
+    check_attention(q, out, None, c, table, lens, cu, 0.125, weights(1, BF16))
     assert torch.isnan(out[:2]).all() and torch.isnan(out[16:]).all()
     out.fill_(float("nan"))
     span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), i32(cu, cuda_device), max_rows=4, out=out)
     with pytest.raises(SpanLAError, match="out of range"):
         span_la_check()
-    check_attention(q, out, None, c, table, lens, cu, 0.125, WEIGHTS, max_rows=4)
+    check_attention(q, out, None, c, table, lens, cu, 0.125, weights(1, BF16), max_rows=4)
     assert torch.isnan(out[2:12]).all()
 
 
@@ -191,7 +193,7 @@ def test_pages_out_of_range_are_not_seen_and_reported(cuda_device, rows):
     span_la_softmax_paged(q, c[0], c[1], i32(bad, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), out=out)
     with pytest.raises(SpanLAError, match="a page out of range"):
         span_la_check()
-    check_attention(q[:rows], out[:rows], None, c, table, lens[:1], cu[:2], 0.125, WEIGHTS)
+    check_attention(q[:rows], out[:rows], None, c, table, lens[:1], cu[:2], 0.125, weights(2, BF16))
     assert torch.isfinite(out.float()).all()
     lens_bad[1] = -5
     out.fill_(float("nan"))
@@ -200,7 +202,7 @@ def test_pages_out_of_range_are_not_seen_and_reported(cuda_device, rows):
         span_la_check()
     assert torch.isnan(out[rows:2 * rows]).all()
     keep = np.concatenate([np.arange(rows), np.arange(2 * rows, 3 * rows)])
-    check_attention(q[keep], out[keep], None, c, table[[0, 2]], [100, 300], [0, rows, 2 * rows], 0.125, WEIGHTS)
+    check_attention(q[keep], out[keep], None, c, table[[0, 2]], [100, 300], [0, rows, 2 * rows], 0.125, weights(2, BF16))
 
 
 @pytest.mark.parametrize("rows", [1, 4, 100])
@@ -228,10 +230,79 @@ def test_more_sequences_than_one_launch_takes(cuda_device):
     lens = rng.integers(1, 40, S)
     q, c, table, cu = _setup(list(lens), [1] * S, 1, 1, 16, BF16, cuda_device, seed=6)
     out, lse = _run(q, c, table, lens, cu, cuda_device, max_rows=1)
-    check_attention(q, out, lse, c, table, lens, cu, 0.125, WEIGHTS)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(1, BF16))
     single = span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device))
     span_la_check()
     assert torch.equal(single, out)
+
+
+def test_chunks_of_more_sequences_than_one_launch_takes(cuda_device):
+    """Among single tokens, empty sequences and short ones."""
+    S = 1100
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 60, S)
+    rows = np.minimum(rng.choice([0, 1, 3, 20, 35], S), lens)
+    q, c, table, cu = _setup(list(lens), list(rows), 2, 1, 16, E4M3, cuda_device, seed=6)
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(2, E4M3))
+
+
+@pytest.mark.parametrize("rows", [2, 60])
+def test_nothing_but_nan_and_infinities(cuda_device, rows):
+    """Values that are all infinite, NaN, or of both signs of infinity: what the formula gives, row by row."""
+    lens = [90, 70, 50, 40]
+    q, c, table, cu = _setup(lens, [min(rows, n) for n in lens], 2, 2, 16, BF16, cuda_device, seed=12)
+    c[1][torch.from_numpy(table[0, :6]).long()] = float("inf")
+    c[1][torch.from_numpy(table[1, :5]).long()] = float("nan")
+    c[1][int(table[2, 0]), :, 3] = float("inf")
+    c[1][int(table[2, 0]), 0, 5, :7] = float("-inf")
+    c[0][int(table[3, 0]), :, 2, 9] = float("nan")
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    o = f64(out)
+    assert np.all(o[cu[0]:cu[1]] == np.inf) and np.isnan(o[cu[1]:cu[2]]).all()
+    for i, y in enumerate(o[cu[2]:cu[3]]):               # row 3 is +inf, row 5 of key head 0 -inf in seven elements
+        seen = lens[2] - (cu[3] - cu[2]) + i + 1
+        both, one = y[:2, :7], np.concatenate([y[:2, 7:].ravel(), y[2:].ravel()])
+        assert np.isnan(both).all() if seen > 5 else np.all(both == np.inf) if seen > 3 else np.isfinite(both).all()
+        assert np.all(one == np.inf) if seen > 3 else np.isfinite(one).all()
+    for i, (y, z) in enumerate(zip(o[cu[3]:cu[4]], f64(lse)[cu[3]:cu[4]])):   # row 2's key is NaN
+        hit = lens[3] - (cu[4] - cu[3]) + i + 1 > 2
+        assert np.isnan(y).all() == hit and np.isnan(z).all() == hit and np.isfinite(y).all() != hit
+    assert np.isfinite(f64(lse)[:cu[3]]).all()
+
+
+def test_captured_behind_another_stream(cuda_device):
+    """Recorded where the rows come from a second stream, next to work on a third, and replayed; twice, so that two graphs
+    are in flight."""
+    dev, lens = cuda_device, [200, 33, 64]
+    q, c, table, cu = _setup(lens, [3, 30, 1], 1, 2, 16, BF16, dev, seed=13)
+    args = [c[0], c[1], i32(table, dev), i32(lens, dev), i32(cu, dev)]
+    ref = span_la_softmax_paged(q, *args)
+    src = q.clone()
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        main, side = torch.cuda.Stream(dev), torch.cuda.Stream(dev)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                x = src * 1.0
+                k, v = span_la_kv_read(*args[:4], args[4], len(q))
+            main.wait_stream(side)
+            span_la_kv_write(k, v, *args)                       # (what is there already)
+            o = span_la_softmax_paged(x, *args)
+            o2 = o * 2
+        graphs.append((g, main))
+        outs.append((o, o2))
+    for _ in range(3):
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    span_la_check()
+    for o, o2 in outs:
+        assert torch.equal(o, ref) and torch.equal(o2, ref * 2)
 
 
 def test_generation_step_by_step_in_a_graph(cuda_device):
@@ -279,7 +350,7 @@ def test_generation_step_by_step_in_a_graph(cuda_device):
     span_la_check()
     for s in range(S):
         ref, _, mass, _ = po.attend(f64(q[s * L:(s + 1) * L]), f64(k[s * L:(s + 1) * L]), f64(v[s * L:(s + 1) * L]), 0.125)
-        tol = 1.01 * U16 * np.abs(ref) + (WEIGHTS + 2.0 ** -12) * mass       # as check_attention, its small terms in one
+        tol = 1.01 * U16 * np.abs(ref) + (U16 + 2.0 ** -12) * mass       # as check_attention, its small terms in one
         assert np.all(np.abs(f64(got[s]) - ref) <= tol)
         assert np.all(np.abs(f64(got[s]) - f64(whole[s * L:(s + 1) * L])) <= 2 * tol)
 
@@ -305,7 +376,7 @@ def test_branches_over_a_view_read_back(cuda_device, cache):
         rows = slice(int(bcu[b]), int(bcu[b + 1]))
         K, V = np.concatenate([f64(vk), f64(bk[rows])]), np.concatenate([f64(vv), f64(bv[rows])])
         ref, _, mass, _ = po.attend(f64(q[rows]), K, V, 0.125)
-        assert np.all(np.abs(f64(out[rows]) - ref) <= 1.01 * U16 * np.abs(ref) + (WEIGHTS + 2.0 ** -12) * mass)
+        assert np.all(np.abs(f64(out[rows]) - ref) <= 1.01 * U16 * np.abs(ref) + (U16 + 2.0 ** -12) * mass)
     # The same branches with their own rows in the cache, in pages of their own behind a copy of the view's last one.
     n = -(-(view + max(blens)) // 64)
     kp, vp, ks, vs = kv_pages(4 * n, H, 64, cache, dev)
@@ -315,7 +386,7 @@ def test_branches_over_a_view_read_back(cuda_device, cache):
     span_la_kv_write(full[0], full[1], kp, vp, tb, lens, i32(np.concatenate([[0], np.cumsum([view + b for b in blens])]), dev), ks, vs)
     paged = span_la_softmax_paged(q, kp, vp, tb, lens, i32(bcu, dev), ks, vs)
     span_la_check()
-    check_attention(q, paged, None, (kp, vp, ks, vs), tb.cpu().numpy(), [view + b for b in blens], bcu, 0.125, WEIGHTS)
+    check_attention(q, paged, None, (kp, vp, ks, vs), tb.cpu().numpy(), [view + b for b in blens], bcu, 0.125, weights(1, cache))
 
 
 def test_pages_past_two_to_the_32(cuda_device):
@@ -330,6 +401,6 @@ def test_pages_past_two_to_the_32(cuda_device):
     for rows in (1, 40):
         q = torch.randn(rows, H, 64, device=cuda_device).to(BF16)
         out, lse = _run(q, (kp, vp, ks, vs), table, lens, [0, rows], cuda_device)
-        check_attention(q, out, lse, small, np.arange(3)[None], lens, [0, rows], 0.125, WEIGHTS)
+        check_attention(q, out, lse, small, np.arange(3)[None], lens, [0, rows], 0.125, weights(1, E4M3))
     del kp, vp, ks, vs
     torch.cuda.empty_cache()
