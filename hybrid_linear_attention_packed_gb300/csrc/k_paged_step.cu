@@ -143,7 +143,7 @@ __device__ __forceinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, u
 template <bool kE4m3, bool kTwo>
 __global__ void __launch_bounds__(Cfg<kE4m3, kTwo>::kWarps * 32, 1)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvArgs a,
-                  const __grid_constant__ PagedAttn p, int s0, int ns, float* __restrict__ ws) {
+                  const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, float* __restrict__ ws) {
   using C = Cfg<kE4m3, kTwo>;
   constexpr int kW = C::kWarps, kS = C::kStages, kUnit = C::kUnit, kN = kUnit / 8, kR = kTwo ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -202,10 +202,6 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   // nw warps are at work, each has a unit at least: the first `more` have each + 1 of them, the others `each`.
   const int64_t nw = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * kW, U));
   const int64_t each = quotient(U, nw), more = U - each * nw;
-  const int64_t edge_w = min(nw, static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));
-  const int64_t edge = each * edge_w + min(edge_w, more);         // lane w: the first unit of the CTA's warp w
-  auto edge_of = [&](int w) { return __shfl_sync(0xffffffffu, edge, w); };
-  const int64_t lo = edge_of(warp), hi = edge_of(warp + 1), cta_lo = edge_of(0), cta_hi = edge_of(kW);
   auto locate = [&](int64_t x, At& at) {
     int l = 0, r = ns;   // the last sequence that starts at x or before
     while (r - l > 1) {
@@ -219,6 +215,22 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     at.h = static_cast<int>(quotient(in, at.units));
     at.blk = static_cast<int32_t>(in - static_cast<int64_t>(at.h) * at.units);
   };
+  const int64_t edge_w = min(nw, static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));
+  int64_t edge = each * edge_w + min(edge_w, more);               // lane w: the first unit of the CTA's warp w
+  auto edge_of = [&](int w) { return __shfl_sync(0xffffffffu, edge, w); };
+  if (whole_items) {
+    // Items of a few units each: a CTA takes those that begin in its share, whole, and shares them out to its warps
+    // (the first ones, where there are fewer units than warps).
+    At at{};
+    if (edge < U) {
+      locate(edge, at);
+      edge -= at.blk;
+    }
+    const int64_t b = edge_of(0), n = edge_of(kW) - b, w = max(static_cast<int64_t>(1), min(static_cast<int64_t>(kW), n));
+    const int64_t per = quotient(n, w), rest = n - per * w, i = min(static_cast<int64_t>(lane), w);
+    edge = b + per * i + min(i, rest);
+  }
+  const int64_t lo = edge_of(warp), hi = edge_of(warp + 1), cta_lo = edge_of(0), cta_hi = edge_of(kW);
   auto advance = [&](At& at) {
     if (++at.blk < at.units) return;
     at.blk = 0;
@@ -736,7 +748,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
   }
   // What the join kernel finds of this CTA: the item that begins here and goes on, if there is one.
-  if (tid == 0 && gridDim.x > 1) {
+  if (tid == 0 && gridDim.x > 1 && !whole_items) {
     StepJoin j{};
     if (ok && cta_lo < cta_hi) {
       At at{};
@@ -854,12 +866,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 
 template <bool kE4m3, bool kTwo>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns, int grid,
-                   float* ws, cudaStream_t stream) {
+                   bool whole_items, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3, kTwo>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3, kTwo>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  return launch_behind(paged_step_kernel<kE4m3, kTwo>, dim3(grid), C::kWarps * 32, C::kRequest, stream, tm_k, tm_v, a, p, s0, ns, ws);
+  return launch_behind(paged_step_kernel<kE4m3, kTwo>, dim3(grid), C::kWarps * 32, C::kRequest, stream, tm_k, tm_v, a, p, s0, ns,
+                       whole_items, ws);
 }
 
 }  // namespace
@@ -876,10 +889,10 @@ int paged_step_grid(int64_t most_units, int num_sms) {
 // At most 8 row heads where the call says so (max_rows): the products' second half, and its exponentials, are left out.
 // One token of 61 sequences over e4m3 pages, 16 heads: see above; the same by the kernel for 16 row heads: 1.2 times that.
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
-                              int grid, bool e4m3, float* ws, cudaStream_t stream) {
+                              int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream) {
   const bool two = a.max_rows * p.group > 8;
-  return e4m3 ? (two ? launch<true, true> : launch<true, false>)(tm_k, tm_v, a, p, s0, ns, grid, ws, stream)
-              : (two ? launch<false, true> : launch<false, false>)(tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
+  return e4m3 ? (two ? launch<true, true> : launch<true, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream)
+              : (two ? launch<false, true> : launch<false, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream);
 }
 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {

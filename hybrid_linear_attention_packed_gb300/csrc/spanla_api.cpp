@@ -2185,6 +2185,7 @@ span_la_status encode_tile(CUtensorMap* map, const KvArgs& a, const PagedAttn& p
 // tell them apart by the row offsets, which are in device memory).
 struct PagedGrids {
   int unit, step, chunk;      // CTAs of each kernel; 0: not launched
+  bool whole;                 // step kernel: no item goes over several CTAs
   size_t step_ws, bytes;      // workspace: of the step kernel, of both
 };
 PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int group, bool e4m3, int num_sms) {
@@ -2192,8 +2193,11 @@ PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t ma
   g.unit = paged_step_unit(e4m3);
   const int64_t units = std::max<int64_t>(1, (capacity + g.unit - 1) / g.unit);   // of a sequence and head, at most
   g.step = group <= kStepHeads ? paged_step_grid(units * heads * std::min<int64_t>(seqs, kStepSeqs), num_sms) : 0;
+  // Tables of a few units (256 rows of bf16 pages, 512 of e4m3): a CTA's eight warps are enough for a sequence and head, and
+  // there is nothing to join.
+  g.whole = units <= 8;
   g.chunk = max_rows * group > kStepHeads ? std::min(num_sms, kStepMaxGrid) : 0;
-  g.step_ws = align256(static_cast<size_t>(g.step > 1 ? g.step : 0) * kStepWsFloats * sizeof(float));
+  g.step_ws = align256(static_cast<size_t>(g.step > 1 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
   g.bytes = g.step_ws + static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float);
   return g;
 }
@@ -2221,8 +2225,8 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     if (st == SPAN_LA_OK)
       each([&](int s0, int ns) {
         cudaError_t x = counted_launch(kKernelPagedStep, stream,
-                                       [&] { return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, ws, stream); });
-        if (x == cudaSuccess && step_grid > 1)
+                                       [&] { return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, grids.whole, ws, stream); });
+        if (x == cudaSuccess && step_grid > 1 && !grids.whole)
           x = counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, step_grid, e4m3, ws, stream); });
         return x;
       });
@@ -2232,7 +2236,7 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     if (st == SPAN_LA_OK) st = encode_pages(&tm_k, a.k, a, e4m3, kTileRows);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, kTileRows);
     float* cws = bytes > 0 ? ws + step_ws / sizeof(float) : nullptr;
-    const bool behind = step && step_grid > 1;   // (the join kernel lets it start early)
+    const bool behind = step;   // (which it need not wait for)
     if (st == SPAN_LA_OK)
       each([&](int s0, int ns) {
         cudaError_t x = counted_launch(kKernelPagedChunk, stream, [&] {

@@ -446,7 +446,7 @@ struct PagedAttn {
 };
 // Sequences of at most kStepHeads packed row heads (rows * group) of a key head (k_paged_step.cu), at most kStepSeqs in
 // a launch: [s0, s0 + ns).  `ws`: kStepWsFloats for each of the `grid` CTAs; the join kernel, with the same grid, follows
-// where there is more than one.
+// where there is more than one, unless the CTAs take whole items.
 constexpr int kStepHeads = 16, kStepSeqs = 512;
 constexpr int kStepWsFloats = 2432, kStepMaxGrid = 160;
 struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begins in the CTA and goes on in the next ones
@@ -457,7 +457,7 @@ struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begin
 int paged_step_unit(bool e4m3);   // cached rows of a unit of work
 int paged_step_grid(int64_t most_units, int num_sms);
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
-                              int grid, bool e4m3, float* ws, cudaStream_t stream);
+                              int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream);
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
 // Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles).
