@@ -281,6 +281,53 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
   }
 }
 
+// A warp: 16 rows of one page and head, of K or V.  Bound by memory (65 bytes in, 128 out, a row and head).
+__global__ void __launch_bounds__(kWarps * 32) kv_expand_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvArgs to,
+                                                                int group) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, sub = lane & 7, per_page = a.page_rows / 16;
+  // (sequence, page, head, K or V, 16 rows): the last varies fastest
+  int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int r0 = 16 * static_cast<int>(u % per_page);
+  u /= per_page;
+  const bool is_v = u & 1;
+  u >>= 1;
+  const int head = static_cast<int>(u % a.heads);
+  u /= a.heads;
+  const int32_t i = static_cast<int32_t>(u % to.copied);
+  const int s = static_cast<int>(u / to.copied);
+  if (s >= a.seqs) return;
+  bool bad = false;
+  const SeqRows r = seq_rows(a, s, &bad);
+  if (static_cast<int64_t>(r.n) * group <= kStepHeads || static_cast<int64_t>(i) * a.page_rows + r0 >= r.len) return;
+  const int32_t page = page_at(a, s, i);
+  if (page < 0) return;   // (the chunk kernel says so)
+  const int64_t from = page * a.page_stride + head * a.head_stride + sub * 8;
+  uint2 raw[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k)
+    raw[k] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + from + (r0 + 4 * k + (lane >> 3)) * a.row_stride));
+  const float scale = scale_of((is_v ? a.v_scale : a.k_scale)[page * a.scale_page_stride + head * a.scale_head_stride + r0 + (lane & 15)]);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + (static_cast<int64_t>(s) * to.copied + i) * to.page_stride +
+                       head * to.head_stride + sub * 8;
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int row = 4 * k + (lane >> 3);
+    const float e = __shfl_sync(0xffffffffu, scale, row);
+    const uint32_t w[2] = {raw[k].x, raw[k].y};
+    float f[8];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 y = from_e4m3x2((w[c >> 1] >> (16 * (c & 1))) & 0xffffu);
+      f[2 * c] = y.x * e, f[2 * c + 1] = y.y * e;
+    }
+    Eight<__nv_bfloat16> y;
+    y.set(f);
+    y.store(dst + (r0 + row) * to.row_stride);
+  }
+}
+
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t stream) {
   // A CTA takes several heads of its rows where there are CTAs enough: finding the rows' places takes as long as copying a
@@ -298,6 +345,11 @@ cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t
 cudaError_t launch_kv_write(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream) {
   if (f32) return launch(e4m3 ? kv_write_kernel<float, true> : kv_write_kernel<float, false>, a, x, stream);
   return launch(e4m3 ? kv_write_kernel<__nv_bfloat16, true> : kv_write_kernel<__nv_bfloat16, false>, a, x, stream);
+}
+
+cudaError_t launch_kv_expand(const KvArgs& a, const KvArgs& to, int group, cudaStream_t stream) {
+  const int64_t warps = static_cast<int64_t>(a.seqs) * to.copied * a.heads * 2 * (a.page_rows / 16);
+  return launch_behind(kv_expand_kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), kWarps * 32, 0, stream, a, to, group);
 }
 
 cudaError_t launch_kv_read(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream) {

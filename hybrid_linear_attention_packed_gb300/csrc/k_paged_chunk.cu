@@ -336,11 +336,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const int32_t page0 = (j * kTileRows) >> a.page_shift;
           if (page0 < win0 || page0 + copies > win0 + 32) {
             win0 = page0;
-            win = page0 + lane < n_pages ? a.table[(s0 + r.s) * a.table_stride + page0 + lane] : 0;
-            if (win < 0 || win >= a.pages) {
-              atomicOr(a.err, kErrPage);
-              win = -1;
-            }
+            win = page0 + lane < n_pages ? page_at(a, s0 + r.s, page0 + lane) : 0;
+            if (win < 0) atomicOr(a.err, kErrPage);
           }
           const int32_t page = __shfl_sync(0xffffffffu, win, (page0 - win0 + lane) & 31);
           const bool mine = lane < copies && page0 + lane < n_pages && page >= 0;
@@ -544,7 +541,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             break;
           }
           tc_fence_after_sync();
-          const float m_new = fmaxf(m_ref, mx);
+          const float m_new = mx > m_ref + raise_margin ? mx : m_ref;   // (by the row alone, not by its neighbours)
           const float f = m_new == m_ref ? 1.f : ex2((m_ref - m_new) * c2);   // 0 where m_ref = -inf
 #pragma unroll
           for (int h = 0; h < 4; ++h) {

@@ -266,11 +266,8 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (at.s != win_s || first < win0 || first + copies > win0 + 32) {
       win_s = at.s;
       win0 = first;
-      win = first + lane < n_pages ? a.table[(s0 + at.s) * a.table_stride + first + lane] : 0;
-      if (win < 0 || win >= a.pages) {
-        atomicOr(a.err, kErrPage);
-        win = -1;
-      }
+      win = first + lane < n_pages ? page_at(a, s0 + at.s, first + lane) : 0;
+      if (win < 0) atomicOr(a.err, kErrPage);
     }
     const int32_t page = __shfl_sync(0xffffffffu, win, (first - win0 + lane) & 31);
     const bool mine = lane < copies && first + lane < n_pages && page >= 0;

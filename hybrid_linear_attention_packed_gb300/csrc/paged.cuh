@@ -48,11 +48,14 @@ __device__ __forceinline__ int seq_of_row(const KvArgs& a, int64_t t) {
   return lo >= 1 && lo <= a.seqs ? lo - 1 : -1;
 }
 
-// The page of row `pos` (0 <= pos < len) of sequence s, or -1 (out of range).
-__device__ __forceinline__ int32_t page_of(const KvArgs& a, int s, int32_t pos) {
-  const int32_t p = a.table[s * a.table_stride + (pos >> a.page_shift)];
-  return p >= 0 && p < a.pages ? p : -1;
+// Entry i of sequence s in the table as a page of the arrays, or -1 (out of range).
+__device__ __forceinline__ int32_t page_at(const KvArgs& a, int s, int32_t i) {
+  const int32_t p = a.table[s * a.table_stride + i];
+  return p < 0 || p >= a.pages ? -1 : a.copied > 0 ? s * a.copied + i : p;
 }
+
+// The page of row `pos` (0 <= pos < len) of sequence s, or -1.
+__device__ __forceinline__ int32_t page_of(const KvArgs& a, int s, int32_t pos) { return page_at(a, s, pos >> a.page_shift); }
 
 // Every sequence's offsets and length, by the threads of one CTA.
 __device__ __forceinline__ void check_sequences(const KvArgs& a) {

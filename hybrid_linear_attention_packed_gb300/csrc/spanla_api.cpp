@@ -141,13 +141,13 @@ constexpr int kKernelSplit = 0, kKernelChunk = 1, kKernelScan = 2, kKernelTile =
               kKernelSpanState = 4, kKernelSpanOutput = 5, kKernelSoftmax = 6, kKernelRecurState = 7,
               kKernelRecurScan = 8, kKernelRecurOutput = 9, kKernelDecayStep = 10, kKernelNormRope = 11,
               kKernelSpanDecay = 12, kKernelKvWrite = 13, kKernelKvRead = 14, kKernelPagedStep = 15, kKernelPagedJoin = 16,
-              kKernelPagedChunk = 17, kKernelChunkJoin = 18;
+              kKernelPagedChunk = 17, kKernelChunkJoin = 18, kKernelKvExpand = 19;
 const char* const kKernelNames[SPAN_LA_NUM_KERNELS] = {"split_f32", "chunk_state", "segmented_scan",
                                                        "tile_output", "span_state", "span_output",
                                                        "softmax_attn", "recur_state", "recur_scan",
                                                        "recur_output", "decay_step", "qk_norm_rope",
                                                        "span_decay", "kv_write", "kv_read", "paged_step",
-                                                       "paged_join", "paged_chunk", "chunk_join"};
+                                                       "paged_join", "paged_chunk", "chunk_join", "kv_expand"};
 
 std::atomic<int64_t> g_launches[SPAN_LA_NUM_KERNELS];
 std::atomic<bool> g_profiling{false};
@@ -2156,7 +2156,7 @@ int64_t most_rows(const span_la_kv_cache* c, int64_t rows, int32_t max_rows) {
 span_la_status encode_pages(CUtensorMap* map, const void* base, const KvArgs& a, bool e4m3, int rows) {
   const cuuint64_t esz = e4m3 ? 1 : 2;
   const cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(a.page_rows), static_cast<cuuint64_t>(a.heads),
-                              static_cast<cuuint64_t>(a.pages)};
+                              a.copied > 0 ? static_cast<cuuint64_t>(a.copied) * a.seqs : static_cast<cuuint64_t>(a.pages)};
   const cuuint64_t strides[3] = {a.row_stride * esz, a.head_stride * esz, a.page_stride * esz};
   const cuuint32_t box[4] = {kHeadDim, static_cast<cuuint32_t>(std::min(rows, a.page_rows)), 1, 1};
   const cuuint32_t estride[4] = {1, 1, 1, 1};
@@ -2186,8 +2186,17 @@ span_la_status encode_tile(CUtensorMap* map, const KvArgs& a, const PagedAttn& p
 struct PagedGrids {
   int unit, step, chunk;      // CTAs of each kernel; 0: not launched
   bool whole;                 // step kernel: no item goes over several CTAs
-  size_t step_ws, bytes;      // workspace: of the step kernel, of both
+  bool expand;                // chunk kernel: over bf16 copies of the e4m3 pages
+  size_t step_ws, chunk_ws, copies, bytes;   // workspace: of each kernel, of K's (and of V's) copies, of all
 };
+
+// From this many row heads of a sequence and key head on, and up to this many bytes of copies, e4m3 pages are expanded to
+// bf16 ahead of the chunk kernel: it converts a block for every 256 row heads that see it, next to a softmax that needs
+// the issue slots.  (20,000 rows, four key heads, expanded and not: 8,192 row heads 179 us and 207, 2,048 66 and 69,
+// 1,024 47.4 and 46.3.)
+constexpr int64_t kExpandRowHeads = 2048;
+constexpr size_t kExpandBytes = size_t(128) << 20;
+
 PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int group, bool e4m3, int num_sms) {
   PagedGrids g{};
   g.unit = paged_step_unit(e4m3);
@@ -2198,7 +2207,11 @@ PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t ma
   g.whole = units <= 8;
   g.chunk = max_rows * group > kStepHeads ? std::min(num_sms, kStepMaxGrid) : 0;
   g.step_ws = align256(static_cast<size_t>(g.step > 1 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
-  g.bytes = g.step_ws + static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float);
+  g.chunk_ws = align256(static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
+  const double copy = static_cast<double>(seqs) * capacity * heads * kHeadDim * 2;
+  g.expand = e4m3 && g.chunk > 0 && max_rows * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
+  g.copies = g.expand ? align256(static_cast<size_t>(seqs * capacity * heads * kHeadDim * 2)) : 0;
+  g.bytes = g.step_ws + g.chunk_ws + 2 * g.copies;
   return g;
 }
 
@@ -2208,7 +2221,7 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   const PagedGrids grids = paged_grids(a.capacity, a.heads, a.seqs, a.max_rows, p.group, e4m3, num_sms);
   const int unit = grids.unit, step_grid = grids.step, chunk_grid = grids.chunk;
   const bool step = step_grid > 0, chunk = chunk_grid > 0;
-  const size_t step_ws = grids.step_ws, bytes = grids.bytes;
+  const size_t bytes = grids.bytes;
   float* ws = static_cast<float*>(workspace);
   cudaError_t e = cudaSuccess;
   if (bytes > 0 && workspace == nullptr) {
@@ -2219,7 +2232,20 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   auto each = [&](auto&& launch) {   // at most kStepSeqs sequences a launch
     for (int s0 = 0; s0 < a.seqs && e == cudaSuccess; s0 += kStepSeqs) e = launch(s0, std::min(kStepSeqs, a.seqs - s0));
   };
-  if (step) {
+  float* cws = bytes > 0 ? ws + grids.step_ws / sizeof(float) : nullptr;
+  KvArgs c = a;   // what the chunk kernel reads
+  if (grids.expand) {
+    // (Before the step kernel: the chunk kernel starts behind that, which has waited for this.)
+    c.k = reinterpret_cast<uint8_t*>(cws) + grids.chunk_ws;
+    c.v = static_cast<uint8_t*>(c.k) + grids.copies;
+    c.row_stride = kHeadDim;
+    c.head_stride = static_cast<int64_t>(a.page_rows) * kHeadDim;
+    c.page_stride = c.head_stride * a.heads;
+    c.copied = static_cast<int32_t>(a.capacity / a.page_rows);
+    e = counted_launch(kKernelKvExpand, stream, [&] { return launch_kv_expand(a, c, p.group, stream); });
+  }
+  const bool chunk_e4m3 = e4m3 && !grids.expand;
+  if (step && e == cudaSuccess) {
     st = encode_pages(&tm_k, a.k, a, e4m3, unit);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, unit);
     if (st == SPAN_LA_OK)
@@ -2233,17 +2259,16 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   }
   if (chunk && st == SPAN_LA_OK && e == cudaSuccess) {
     st = encode_tile(&tm_q, a, p);
-    if (st == SPAN_LA_OK) st = encode_pages(&tm_k, a.k, a, e4m3, kTileRows);
-    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, kTileRows);
-    float* cws = bytes > 0 ? ws + step_ws / sizeof(float) : nullptr;
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_k, c.k, c, chunk_e4m3, kTileRows);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, c.v, c, chunk_e4m3, kTileRows);
     const bool behind = step;   // (which it need not wait for)
     if (st == SPAN_LA_OK)
       each([&](int s0, int ns) {
         cudaError_t x = counted_launch(kKernelPagedChunk, stream, [&] {
-          return launch_paged_chunk(tm_q, tm_k, tm_v, a, p, s0, ns, chunk_grid, e4m3, cws, behind && s0 == 0, stream);
+          return launch_paged_chunk(tm_q, tm_k, tm_v, c, p, s0, ns, chunk_grid, chunk_e4m3, cws, behind && s0 == 0, stream);
         });
         if (x == cudaSuccess && chunk_grid > 1)
-          x = counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(a, p, chunk_grid, e4m3, cws, stream); });
+          x = counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(c, p, chunk_grid, chunk_e4m3, cws, stream); });
         return x;
       });
   }

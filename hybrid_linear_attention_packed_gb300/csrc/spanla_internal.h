@@ -422,6 +422,8 @@ struct KvArgs {
   int64_t rows;               // packed rows of the call
   int64_t max_rows;           // most rows of a sequence
   int32_t pages, page_rows, page_shift, heads, seqs;
+  int32_t copied;             // > 0: k and v are copies, of which page i of sequence s is page s * copied + i (the table
+                              // says which are there)
   unsigned* err;
 };
 
@@ -433,6 +435,10 @@ struct KvRows {
 };
 cudaError_t launch_kv_write(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvArgs& a, const KvRows& x, bool e4m3, bool f32, cudaStream_t stream);
+
+// The e4m3 pages of the sequences that the chunk kernel takes, as bf16 pages of their own: page i of sequence s is page
+// s * copied + i of `to` (`group`: query heads of a key head; k_kv_pages.cu).
+cudaError_t launch_kv_expand(const KvArgs& a, const KvArgs& to, int group, cudaStream_t stream);
 
 // Softmax attention of packed rows over the cache.
 struct PagedAttn {

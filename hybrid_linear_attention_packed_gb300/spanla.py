@@ -39,7 +39,7 @@ EXPORTED = ("span_la_pass", "span_la_branches_from_state", "span_la_check",
             "span_la_plan_prepare", "span_la_decay_pass", "span_la_decay_branches_from_state",
             "span_la_decay_step", "span_la_qk_norm_rope", "span_la_cache_decay_branches",
             "span_la_kv_write", "span_la_kv_read", "span_la_softmax_paged", "span_la_softmax_paged_workspace")
-NUM_KERNELS = 19
+NUM_KERNELS = 20
 
 
 class SpanLAError(RuntimeError):

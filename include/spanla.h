@@ -377,14 +377,15 @@ span_la_status span_la_plan_stats(const int32_t *view_cu_seqlens, int32_t num_vi
  *   6 softmax_attn (span_la_softmax_pass), 7 recur_state, 8 recur_scan,
  *   9 recur_output (decayed passes, fp32), 12 span_decay (bf16),
  *   10 decay_step, 11 qk_norm_rope, 13 kv_write, 14 kv_read, 15 paged_step,
- *   16 paged_join, 17 paged_chunk, 18 chunk_join (paged cache).
+ *   16 paged_join, 17 paged_chunk, 18 chunk_join, 19 kv_expand (paged
+ *   cache).
  * Launches of every kernel are always counted.  While profiling is enabled,
  * every launch is also bracketed by two CUDA events recorded on the call's
  * stream (one device only); span_la_profile_read() waits for the pending
  * events and adds their elapsed times up.  Enabling adds two event records per
  * launch and nothing else to the work on the stream.
  */
-#define SPAN_LA_NUM_KERNELS 19
+#define SPAN_LA_NUM_KERNELS 20
 
 /* Turn event timing on (non-zero) or off. */
 span_la_status span_la_profile_enable(int32_t enable);

@@ -8,7 +8,7 @@ from hybrid_linear_attention_packed_gb300 import (SpanLAError, kv_pages, packed_
                                                   span_la_softmax_branches_from_kv, span_la_softmax_paged,
                                                   span_la_softmax_pass)
 from oracle import paged_oracle as po
-from paged_helpers import BF16, E4M3, U16, check_attention, f64, i32, make_pages, make_table
+from paged_helpers import BF16, E4M3, U16, check_attention, f64, i32, make_pages, make_table, values
 
 pytestmark = pytest.mark.gpu
 
@@ -63,6 +63,8 @@ CASES = [
     ([900, 20, 450, 64, 1], [300, 1, 2, 64, 1], 1, 4, 64),
     ([2000], [1], 1, 16, 16),
     ([5000], [600], 1, 2, 256),
+    ([700, 40, 520, 9], [260, 1, 270, 9], 8, 2, 16),     # (many row heads: e4m3 pages are expanded first)
+    ([300, 33], [300, 20], 12, 1, 64),
 ]
 
 
@@ -138,7 +140,7 @@ def test_rows_that_see_nothing(cuda_device, rows, G, cache):
 
 @pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan"), 3.3e38])
 @pytest.mark.parametrize("cache", [BF16, E4M3])
-@pytest.mark.parametrize("rows,G", [(2, 1), (4, 4), (40, 2), (300, 1)])
+@pytest.mark.parametrize("rows,G", [(2, 1), (4, 4), (40, 2), (300, 1), (260, 8)])
 def test_what_a_row_does_not_see_does_not_reach_it(cuda_device, rows, G, cache, what):
     """The last row of every sequence holds infinities or NaN: only the last packed row sees it."""
     lens = [rows + 5, 310, rows]
@@ -182,27 +184,36 @@ def test_other_rows_of_the_call_are_left(cuda_device):
     assert torch.isnan(out[2:12]).all()
 
 
-@pytest.mark.parametrize("rows", [1, 70])
-def test_pages_out_of_range_are_not_seen_and_reported(cuda_device, rows):
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows,G", [(1, 2), (70, 2), (90, 24)])
+def test_pages_out_of_range_are_not_seen_and_reported(cuda_device, rows, G, cache):
     lens = [100, 200, 300]
-    q, c, table, cu = _setup(lens, [rows] * 3, 2, 2, 16, BF16, cuda_device, seed=5)
+    q, c, table, cu = _setup(lens, [rows] * 3, G, 2, 16, cache, cuda_device, seed=5)
     bad = table.copy()
     bad[1, 2], bad[2, 0] = 1 << 30, -1
     lens_bad = np.array(lens)
     out = torch.full_like(q, float("nan"))
-    span_la_softmax_paged(q, c[0], c[1], i32(bad, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), out=out)
+    span_la_softmax_paged(q, c[0], c[1], i32(bad, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), c[2], c[3], out=out)
     with pytest.raises(SpanLAError, match="a page out of range"):
         span_la_check()
-    check_attention(q[:rows], out[:rows], None, c, table, lens[:1], cu[:2], 0.125, weights(2, BF16))
+    check_attention(q[:rows], out[:rows], None, c, table, lens[:1], cu[:2], 0.125, weights(G, cache))
     assert torch.isfinite(out.float()).all()
+    for s, gone in ((1, range(32, 48)), (2, range(16))):      # the others: as if those rows had scores of -infinity
+        kv = [po.rows_of(values(c[x], c[2 + x]), table[s], lens[s]) for x in range(2)]
+        keep = [j for j in range(lens[s]) if j not in gone]
+        first = lens[s] - rows
+        assert first > max(gone)
+        ref, _, mass, _ = po.attend(f64(q[cu[s]:cu[s + 1]]), kv[0][keep], kv[1][keep], 0.125)
+        tol = 1.01 * U16 * np.abs(ref) + (U16 + 2.0 ** -12) * mass
+        assert np.all(np.abs(f64(out[cu[s]:cu[s + 1]]) - ref) <= tol)
     lens_bad[1] = -5
     out.fill_(float("nan"))
-    span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), out=out)
+    span_la_softmax_paged(q, c[0], c[1], i32(table, cuda_device), i32(lens_bad, cuda_device), i32(cu, cuda_device), c[2], c[3], out=out)
     with pytest.raises(SpanLAError, match="offsets or length"):
         span_la_check()
     assert torch.isnan(out[rows:2 * rows]).all()
     keep = np.concatenate([np.arange(rows), np.arange(2 * rows, 3 * rows)])
-    check_attention(q[keep], out[keep], None, c, table[[0, 2]], [100, 300], [0, rows, 2 * rows], 0.125, weights(2, BF16))
+    check_attention(q[keep], out[keep], None, c, table[[0, 2]], [100, 300], [0, rows, 2 * rows], 0.125, weights(G, cache))
 
 
 @pytest.mark.parametrize("rows", [1, 4, 100])
