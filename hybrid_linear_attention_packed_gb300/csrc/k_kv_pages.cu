@@ -105,7 +105,7 @@ template <>
 struct Eight<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void store(float* p) const { reinterpret_cast<float4*>(p)[0] = a, reinterpret_cast<float4*>(p)[1] = b; }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -116,7 +116,7 @@ struct Eight<float> {
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
         const int r = half + 4 * i + (lane >> 3);
         raw[i] = make_uint2(0u, 0u);
         if (pl.at[r] >= 0)
-          raw[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8));
+          raw[i] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + pl.at[r] + head * a.head_stride + sub * 8);
       }
       const float scale =
           pl.at[half + (lane & 15)] >= 0 ? scale_of((is_v ? a.v_scale : a.k_scale)[pl.scale_at[half + (lane & 15)] + head * a.scale_head_stride]) : 0.f;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_expand_kernel(const __grid_con
   uint2 raw[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k)
-    raw[k] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + from + (r0 + 4 * k + (lane >> 3)) * a.row_stride));
+    raw[k] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + from + (r0 + 4 * k + (lane >> 3)) * a.row_stride);
   const float scale = scale_of((is_v ? a.v_scale : a.k_scale)[page * a.scale_page_stride + head * a.scale_head_stride + r0 + (lane & 15)]);
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? to.v : to.k) + (static_cast<int64_t>(s) * to.copied + i) * to.page_stride +
                        head * to.head_stride + sub * 8;

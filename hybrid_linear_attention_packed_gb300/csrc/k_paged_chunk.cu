@@ -165,7 +165,7 @@ struct Run {
 template <bool kE4m3>
 __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, float* __restrict__ ws) {
+                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, float* ws) {
   using C = Cfg<kE4m3>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -552,7 +552,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
             tmem_st_16cols(ts + kColO + 16 * h, o);
           }
-          l = m_ref == -INFINITY ? 0.f : l * f;
+          l = m_ref * c2 == -INFINITY ? 0.f : l * f;
           m_ref = m_new;
         }
         const float neg = -(m_ref == -INFINITY ? 0.f : m_ref) * c2;
@@ -592,6 +592,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
       tc_fence_after_sync();
       const float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c2;
+      if (fabsf(m2) == INFINITY) l = m2 > 0.f ? NAN : 0.f;   // (the scale took the greatest score out of fp32: what the score gives)
       const bool complete = r.j0 == 0 && r.j1 == r.blocks;
       const int64_t at = (s_row0[r.s] + static_cast<int64_t>(in_seq)) * p.heads + r.h * p.group + my_head;
       float* part = ws + blockIdx.x * kChunkWsFloats + (2 * (r.j0 > 0 ? 0 : 1) + x) * kPartFloats;
@@ -716,7 +717,7 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinAhead = 2
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
-                                                                  const float* __restrict__ ws) {
+                                                                  const float* ws) {
   __shared__ float factor[kStepMaxGrid][32];
   __shared__ float best[kJoinWarps][32], sums[kJoinWarps][32];
   __shared__ uint32_t wild;

@@ -143,7 +143,7 @@ __device__ __forceinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, u
 template <bool kE4m3, bool kTwo>
 __global__ void __launch_bounds__(Cfg<kE4m3, kTwo>::kWarps * 32, 1)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvArgs a,
-                  const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, float* __restrict__ ws) {
+                  const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, float* ws) {
   using C = Cfg<kE4m3, kTwo>;
   constexpr int kW = C::kWarps, kS = C::kStages, kUnit = C::kUnit, kN = kUnit / 8, kR = kTwo ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -775,7 +775,7 @@ constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16, kJoinRows = 4, 
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
-                                                                  const float* __restrict__ ws) {
+                                                                  const float* ws) {
   __shared__ float4 so[16][16];
   __shared__ float factor[kJoinRows][kStepMaxGrid];
   __shared__ float total[kJoinRows][3];

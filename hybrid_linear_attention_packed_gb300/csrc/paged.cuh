@@ -65,7 +65,9 @@ __device__ __forceinline__ void check_sequences(const KvArgs& a) {
 }
 
 // A launch whose CTAs may come up while the kernel before it in the stream still runs; they wait for its end
-// (griddep_wait) before they touch memory.  Calls one behind the other then do not wait for each other's launch.
+// (griddep_wait) before they touch memory.  Calls one behind the other then do not wait for each other's launch.  What
+// such a kernel reads may be written while it is up, so it reads nothing by __restrict__ const pointers or __ldg: the
+// compiler may take those reads past the wait.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg{};

@@ -2073,6 +2073,7 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
   const int64_t esz = e4m3 ? 1 : 2;
   if (c->k == nullptr || c->v == nullptr || !aligned16(c->k) || !aligned16(c->v))
     return fail(SPAN_LA_ERR_INVALID, "k and v pages must be non-NULL and 16-byte aligned");
+  constexpr int64_t kMostCached = int64_t(1) << 30;   // rows of a sequence (the kernels round up to blocks in 32 bits)
   constexpr int64_t kMost = int64_t(1) << 39;   // elements that an axis spans (the tensor maps' limit; no overflow below)
   auto behind = [](const void* x, const void* y) {
     return static_cast<int64_t>(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x));
@@ -2102,8 +2103,8 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
   // (pages of K and V may be interleaved: what meets is looked for row by row)
   if (written && rows_meet(axes, kHeadDim, behind(c->k, c->v) / esz))
     return fail(SPAN_LA_ERR_INVALID, "k pages overlap v pages");
-  if (c->table_width < 0 || static_cast<int64_t>(c->table_width) * c->page_rows > INT32_MAX)
-    return fail(SPAN_LA_ERR_INVALID, "table_width %d pages of %d rows are too many", c->table_width, c->page_rows);
+  if (c->table_width < 0 || static_cast<int64_t>(c->table_width) * c->page_rows > kMostCached)
+    return fail(SPAN_LA_ERR_INVALID, "table_width %d pages of %d rows are not in [0, 2^30] rows", c->table_width, c->page_rows);
   if (c->num_seqs > 0) {
     auto word = [](const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
     if (c->table_width > 0 && !word(c->page_table)) return fail(SPAN_LA_ERR_INVALID, "page_table must be non-NULL and 4-byte aligned");
@@ -2209,7 +2210,7 @@ PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t ma
   g.step_ws = align256(static_cast<size_t>(g.step > 1 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
   g.chunk_ws = align256(static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
   const double copy = static_cast<double>(seqs) * capacity * heads * kHeadDim * 2;
-  g.expand = e4m3 && g.chunk > 0 && max_rows * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
+  g.expand = e4m3 && capacity > 0 && g.chunk > 0 && max_rows * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
   g.copies = g.expand ? align256(static_cast<size_t>(seqs * capacity * heads * kHeadDim * 2)) : 0;
   g.bytes = g.step_ws + g.chunk_ws + 2 * g.copies;
   return g;

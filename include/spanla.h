@@ -618,7 +618,7 @@ typedef struct {
     int32_t num_heads;
     int32_t dtype;              /* SPAN_LA_BF16 or SPAN_LA_E4M3 */
     int32_t num_seqs;
-    int32_t table_width;        /* entries in a row of page_table */
+    int32_t table_width;        /* entries in a row of page_table; times page_rows at most 2^30 */
     int64_t table_stride;       /* from row to row of page_table, >= table_width */
     const int32_t *page_table;  /* device [num_seqs][table_width] */
     const int32_t *seq_len;     /* device [num_seqs] */

@@ -282,6 +282,36 @@ def test_nothing_but_nan_and_infinities(cuda_device, rows):
     assert np.isfinite(f64(lse)[:cu[3]]).all()
 
 
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_scores_past_fp32(cuda_device, rows, cache):
+    """q . k of 64, -64 and 0 at a scale of 1e38: infinite scores of either sign, and weights of nothing else."""
+    keys = [[1.0] * 90, [-1.0] * 300, [-1.0] * 128 + [0.0] * 200, [-1.0] * 150 + [1.0] * 60, [0.0] * 70]
+    lens = [len(x) for x in keys]
+    q, c, table, cu = _setup(lens, [rows] * 5, 1, 2, 16, cache, cuda_device, seed=14)
+    at = np.concatenate([[0], np.cumsum(lens)])
+    k = torch.tensor(np.concatenate(keys), device=cuda_device, dtype=torch.float32)[:, None, None].expand(-1, 2, 64).contiguous()
+    v = torch.full_like(k, 3.0)
+    span_la_kv_write(k, v, c[0], c[1], i32(table, cuda_device), i32(lens, cuda_device), i32(at, cuda_device), c[2], c[3])
+    out, lse = _run(torch.ones_like(q), c, table, lens, cu, cuda_device, scale=1e38)
+    o, z = f64(out), f64(lse)
+    for s in (0, 3):
+        assert np.isnan(o[cu[s]:cu[s + 1]]).all() and np.isnan(z[cu[s]:cu[s + 1]]).all()
+    assert not o[cu[1]:cu[2]].any() and np.all(z[cu[1]:cu[2]] == -np.inf)
+    for s, zero in ((2, 200), (4, 70)):
+        n = zero - rows + 1 + np.arange(rows)                  # rows of score 0 that each sees
+        assert np.all(o[cu[s]:cu[s + 1]] == 3.0)
+        assert np.abs(z[cu[s]:cu[s + 1]] - np.log(n)[:, None]).max() < 1e-5
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 30, 2100])
+def test_a_table_of_no_pages(cuda_device, rows, cache):
+    q, c, _, _ = _setup([5], [rows], 1, 1, 16, cache, cuda_device, seed=15)
+    out, lse = _run(q, c, np.zeros((1, 0), np.int32), [0], [0, rows], cuda_device)
+    assert not f64(out).any() and np.all(f64(lse) == -np.inf)
+
+
 def test_captured_behind_another_stream(cuda_device):
     """Recorded where the rows come from a second stream, next to work on a third, and replayed; twice, so that two graphs
     are in flight."""

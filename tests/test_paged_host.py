@@ -58,6 +58,7 @@ CACHE = [
     (dict(scale_page_stride=16), INVALID, "overlap"),
     (dict(table_width=-1), INVALID, "table_width"),
     (dict(table_width=1 << 28, table_stride=1 << 28), INVALID, "table_width"),
+    (dict(table_width=(1 << 26) + 1, table_stride=1 << 27), INVALID, "table_width"),
     (dict(table_stride=3), INVALID, "table_stride"),
     (dict(page_table=None), INVALID, "page_table"),
     (dict(seq_len=LEN + 2), INVALID, "seq_len"),
