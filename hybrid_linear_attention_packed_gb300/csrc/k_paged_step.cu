@@ -24,7 +24,17 @@
 // A warp's first and last items may go on in other warps.  Those parts (m, M, l,
 // O) meet in shared memory for the warps of a CTA and then, for the items that go
 // over several CTAs, in the join kernel, which starts behind this one.
+//
+// Measured (with the join, one call behind the other): 128 tokens of up to 18,000
+// rows over bf16 pages, 8 key heads of 4, 222 us, 6.8 TB/s, as fast as a copy; 61
+// over e4m3 pages, 16 heads, 118 us, 5.3 TB/s (issue slots: a warp takes 766
+// instructions for 64 rows of e4m3, and its chains of them leave half of the slots
+// empty).  One token of one sequence, 7,401 rows, 16 heads, 11.4 us, of which the
+// data are 4.5: the lengths are there after 1.0, the first unit's data after 2.9,
+// the last unit is done after 7.4, the warps' parts are one after 8.5, and the join
+// begins after 9.5 and takes 2.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -62,7 +72,8 @@ struct Cfg {
   static constexpr uint32_t kInfo = kCount + kStepSeqs;        // 8 bytes a stage: the rows that are there
   static constexpr uint32_t kScan = kInfo + kWarps * kStages * 8;
   static constexpr uint32_t kBar = kScan + kWarps * 8;
-  static constexpr uint32_t kBytes = kBar + kWarps * kStages * 8;
+  static constexpr uint32_t kOpen = kBar + kWarps * kStages * 8;   // Open of each warp, and one more
+  static constexpr uint32_t kBytes = kOpen + (kWarps + 1) * 24;
   static constexpr uint32_t kRequest = kBytes + 1024;
   static_assert(kRequest <= 227 * 1024 && kRing >= kSlot * 4 && kInfo % 8 == 0 && kSum % 16 == 0 && kHead % 16 == 0, "shared memory");
 };
@@ -110,6 +121,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 struct At {
   int s, h;            // sequence (of this launch), key head
   int32_t blk, units;  // unit of the item, units of the item
+};
+
+// An item of several parts, by the warp in which it begins (or the CTA's first one).
+struct Open {
+  int64_t begin;       // its first unit
+  int32_t units, s, h; // units 0: none
 };
 
 // Output of a row head: elements d, d + 1.
@@ -197,11 +214,17 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (tid == kW * 32 - 1) sum[ns] = before + mine;
     __syncthreads();
   }
-  const int64_t U = sum[ns];
   // ---------------------------------------------------------------- this warp's units
   // nw warps are at work, each has a unit at least: the first `more` have each + 1 of them, the others `each`.
-  const int64_t nw = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * kW, U));
-  const int64_t each = quotient(U, nw), more = U - each * nw;
+  struct Shares {
+    int64_t nw, each, more;
+  };
+  auto shares = [&]() -> Shares {   // (twice, and not in registers meanwhile)
+    const int64_t U = *const_cast<volatile int64_t*>(sum + ns), nw = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * kW, U));
+    const int64_t each = quotient(U, nw);
+    return {nw, each, U - each * nw};
+  };
+  const Shares sh = shares();
   auto locate = [&](int64_t x, At& at) {
     int l = 0, r = ns;   // the last sequence that starts at x or before
     while (r - l > 1) {
@@ -215,14 +238,14 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     at.h = static_cast<int>(quotient(in, at.units));
     at.blk = static_cast<int32_t>(in - static_cast<int64_t>(at.h) * at.units);
   };
-  const int64_t edge_w = min(nw, static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));
-  int64_t edge = each * edge_w + min(edge_w, more);               // lane w: the first unit of the CTA's warp w
+  const int64_t edge_w = min(sh.nw, static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));
+  int64_t edge = sh.each * edge_w + min(edge_w, sh.more);               // lane w: the first unit of the CTA's warp w
   auto edge_of = [&](int w) { return __shfl_sync(0xffffffffu, edge, w); };
   if (whole_items) {
     // Items of a few units each: a CTA takes those that begin in its share, whole, and shares them out to its warps
     // (the first ones, where there are fewer units than warps).
     At at{};
-    if (edge < U) {
+    if (edge < sum[ns]) {
       locate(edge, at);
       edge -= at.blk;
     }
@@ -230,7 +253,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int64_t per = quotient(n, w), rest = n - per * w, i = min(static_cast<int64_t>(lane), w);
     edge = b + per * i + min(i, rest);
   }
-  const int64_t lo = edge_of(warp), hi = edge_of(warp + 1), cta_lo = edge_of(0), cta_hi = edge_of(kW);
+  const int64_t lo = edge_of(warp), hi = edge_of(warp + 1);
   auto advance = [&](At& at) {
     if (++at.blk < at.units) return;
     at.blk = 0;
@@ -300,6 +323,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncwarp();
   };
 
+  Open* open = reinterpret_cast<Open*>(smem + C::kOpen);
+  if (lane == 0) {
+    open[warp].units = 0;
+    if (warp == 0) open[kW].units = 0;
+  }
   At prod{}, cons{};
   int64_t issued = lo;
   if (lo < hi) {
@@ -632,6 +660,9 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           redo_rows<kE4m3>(a, p, which, s0 + cons.s, s_row0[cons.s], n, len, cons.h);
         }
       } else {
+        // (what began before the CTA is warp 0's to tell of: open[kW] where it ends in warp 0, as another may begin there)
+        if (lane == 0 && (item_done ? warp == 0 : warp == 0 || !started_before))
+          open[item_done ? kW : warp] = {done - 1 - cons.blk, cons.units, cons.s, cons.h};
         float* slot = slot_of(warp, started_before);
         if (!started_before) __syncwarp();   // (the ring's last reads are done)
 #pragma unroll
@@ -667,116 +698,159 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   }
   ok = __syncthreads_and(ok);
 
-  // ---------------------------------------------------------------- items over several warps of this CTA
-  // `cons` is the last item of the warp's units; its first one it finds again.  The warps that have some of an item
-  // share its row heads, two of them at a time: half a warp each, first its lanes the parts, then four elements of O.
+  // ---------------------------------------------------------------- items of several parts
+  // All warps share the row heads of all of them, two at a time: half a warp each, first its lanes the parts, then four
+  // elements of O; two such pairs side by side where a warp has more than one, as each is a chain of shuffles.
+  // (By the warps that had some of the item, one by one: 24 x 4 tokens 32.4 us instead of 30.8, of which CTAs with many
+  // short sequences took 6 here; 131,072 rows 20.4 instead of 18.4.)
   float* ws_part = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
-  if (ok && lo < hi) {
-    At first{};
-    locate(lo, first);
-    const bool same = first.s == cons.s && first.h == cons.h;
+  StepJoin join{};   // what the join kernel finds of this CTA: the item that begins here and goes on, if there is one
+  if (ok) {
     const int half = lane >> 4, sub = lane & 15;
+    const int64_t cta_lo = edge_of(0), cta_hi = edge_of(kW);
+    const Open my_open = open[min(lane, kW)];   // lane k: the k-th one and its pairs
+    const int my_pairs = lane <= kW && my_open.units != 0 ? (s_count[my_open.s] * p.group + 1) >> 1 : 0;
+    int upto = my_pairs;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    const int each_warp = (__shfl_sync(0xffffffffu, upto, kW) + kW - 1) / kW, from = each_warp * warp, to = from + each_warp;
+    if (tid <= kW && my_open.units != 0) {
+      const int64_t ie = my_open.begin + my_open.units;
+      if (my_open.begin >= cta_lo && ie > cta_hi) {
+        const int64_t x = ie - 1;   // its last unit, and the warp that has it
+        const Shares sh = shares();
+        const int64_t wide = sh.more * (sh.each + 1);
+        const int64_t w = x < wide ? quotient(x, sh.each + 1) : sh.more + quotient(x - wide, sh.each);
+        join = {static_cast<int32_t>(w / kW) - static_cast<int32_t>(blockIdx.x) + 1, s0 + my_open.s, my_open.h, s_count[my_open.s],
+                s_len[my_open.s], s_row0[my_open.s], {}};
+      }
+    }
+    uint32_t items = __ballot_sync(0xffffffffu, my_pairs > 0 && upto > from && upto - my_pairs < to);
 #pragma unroll 1
-    for (int what = 0; what < (same ? 1 : 2); ++what) {
-      const At& at = what == 0 ? first : cons;
-      const int64_t ib = what == 0 ? lo - first.blk : hi - 1 - cons.blk, ie = ib + at.units;
-      if (ib >= lo && ie <= hi) continue;
-      int w0 = warp, w1 = warp;   // the first and the last warp of the CTA with some of it
-      while (w0 > 0 && edge_of(w0) > ib) --w0;
-      while (w1 < kW - 1 && edge_of(w1 + 1) < min(ie, cta_hi)) ++w1;
+    for (; items != 0; items &= items - 1) {
+      const int k = __ffs(items) - 1;
+      const Open it = open[k];
+      const int before = __shfl_sync(0xffffffffu, upto - my_pairs, k);
+      const int64_t ib = it.begin, ie = ib + it.units;
+      const int w0 = k == kW ? 0 : k;   // the first and the last warp of the CTA with some of it
+      const int w1 = max(w0, __popc(__ballot_sync(0xffffffffu, lane > 0 && lane < kW && edge < min(ie, cta_hi))));
       const int parts = w1 - w0 + 1;
       const bool complete = ib >= cta_lo && ie <= cta_hi;
       const bool w0_head = edge_of(w0) > ib;      // (the later ones have it in their head slots)
-      const int n = s_count[at.s], mh = n * p.group;
+      const int n = s_count[it.s], mh = n * p.group;
       float* out_slot = ws_part + (ib < cta_lo ? 0 : kSlotFloats);
       const float* mine = slot_of(w0 + min(sub, parts - 1), min(sub, parts - 1) > 0 || w0_head);
+      const int end = min(to - before, (mh + 1) >> 1);
       uint32_t which = 0;
-      for (int r0 = 2 * (warp - w0); r0 < mh; r0 += 2 * parts) {
-        const int row = min(r0 + half, mh - 1);
-        const bool in = r0 + half < mh;
-        const float pm = sub < parts ? mine[kStats + row] : -INFINITY, pM = sub < parts ? mine[kStats + kM + row] : -INFINITY;
-        const float pl = sub < parts ? mine[kStats + 2 * kM + row] : 0.f;
-        float jm = pm, jM = pM;
+      auto join_pairs = [&](auto at_once, int i) {   // from pair i on
+        constexpr int kAtOnce = decltype(at_once)::value;
+        int row[kAtOnce];
+        float jm[kAtOnce], jM[kAtOnce], jl[kAtOnce], f[kAtOnce];
+        float4 jo[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          row[u] = min(2 * (i + u) + half, mh - 1);
+          jm[u] = sub < parts ? mine[kStats + row[u]] : -INFINITY;
+          jM[u] = sub < parts ? mine[kStats + kM + row[u]] : -INFINITY;
+          jl[u] = sub < parts ? mine[kStats + 2 * kM + row[u]] : 0.f;
+          jo[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float pm[kAtOnce], pM[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) pm[u] = jm[u], pM[u] = jM[u];
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) {
-          jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, d));
-          jM = fmaxf(jM, __shfl_xor_sync(0xffffffffu, jM, d));
-        }
-        jm = __shfl_sync(0xffffffffu, jm, 0, 16), jM = __shfl_sync(0xffffffffu, jM, 0, 16);
-        const float f = rescale(pM, jM);
-        float jl = pl * rescale(pm, jm);
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, d);
-        jl = __shfl_sync(0xffffffffu, jl, 0, 16);
-        float4 jo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+          for (int u = 0; u < kAtOnce; ++u) {
+            jm[u] = fmaxf(jm[u], __shfl_xor_sync(0xffffffffu, jm[u], d));
+            if (kE4m3) jM[u] = fmaxf(jM[u], __shfl_xor_sync(0xffffffffu, jM[u], d));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          if (!kE4m3) jM[u] = jm[u];   // (the same, over bf16 pages)
+          f[u] = rescale(pM[u], jM[u]);
+          jl[u] *= rescale(pm[u], jm[u]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) {
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) jl[u] += __shfl_xor_sync(0xffffffffu, jl[u], d);
+        }
+#pragma unroll 2
         for (int w = 0; w < parts; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(slot_of(w0 + w, w > 0 || w0_head) + row * kSlotStride + 4 * sub);
-          const float fw = __shfl_sync(0xffffffffu, f, w, 16);
-          jo.x = fmaf(fw, y.x, jo.x), jo.y = fmaf(fw, y.y, jo.y), jo.z = fmaf(fw, y.z, jo.z), jo.w = fmaf(fw, y.w, jo.w);
-        }
-        bool wild = false;
-        if (complete) {
-          const int64_t o_at = (s_row0[at.s] + static_cast<int64_t>(row / p.group)) * p.heads + at.h * p.group + row % p.group;
-          const float of = out_factor<kE4m3>(jm, jM, jl);
-          jo.x *= of, jo.y *= of, jo.z *= of, jo.w *= of;
-          wild = (!(fabsf(jo.x) <= 3.4e38f) || !(fabsf(jo.y) <= 3.4e38f) || !(fabsf(jo.z) <= 3.4e38f) || !(fabsf(jo.w) <= 3.4e38f)) &&
-                 jl == jl && jl != 0.f;
-          if (in) {
-            *reinterpret_cast<uint2*>(p.out + o_at * kHeadDim + 4 * sub) =
-                jl == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(jo.x, jo.y), pack_bf16x2(jo.z, jo.w));
-            if (p.lse != nullptr && sub == 0) p.lse[o_at] = log_sum(jm, jl);
-          }
-        } else if (in) {
-          *reinterpret_cast<float4*>(out_slot + row * kSlotStride + 4 * sub) = jo;
-          if (sub == 0) {
-            out_slot[kM * kSlotStride + row] = jm;
-            out_slot[kM * kSlotStride + kM + row] = jM;
-            out_slot[kM * kSlotStride + 2 * kM + row] = jl;
+          const float* slot = slot_of(w0 + w, w > 0 || w0_head) + 4 * sub;
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) {
+            const float4 y = *reinterpret_cast<const float4*>(slot + row[u] * kSlotStride);
+            const float fw = __shfl_sync(0xffffffffu, f[u], w, 16);
+            jo[u].x = fmaf(fw, y.x, jo[u].x), jo[u].y = fmaf(fw, y.y, jo[u].y);
+            jo[u].z = fmaf(fw, y.z, jo[u].z), jo[u].w = fmaf(fw, y.w, jo[u].w);
           }
         }
-        const uint32_t b = __ballot_sync(0xffffffffu, wild);
-        which |= ((b & 0xffffu) ? 1u << r0 : 0u) | ((b >> 16) && r0 + 1 < mh ? 2u << r0 : 0u);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const bool in = i + u < end && 2 * (i + u) + half < mh;
+          bool wild = false;
+          if (complete) {
+            const int r = row[u] / p.group;
+            const int64_t o_at = (s_row0[it.s] + static_cast<int64_t>(r)) * p.heads + it.h * p.group + row[u] - r * p.group;
+            const float of = out_factor<kE4m3>(jm[u], jM[u], jl[u]);
+            const float y[4] = {jo[u].x * of, jo[u].y * of, jo[u].z * of, jo[u].w * of};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wild |= !(fabsf(y[c]) <= 3.4e38f);
+            wild &= in && jl[u] == jl[u] && jl[u] != 0.f;
+            if (in) {
+              *reinterpret_cast<uint2*>(p.out + o_at * kHeadDim + 4 * sub) =
+                  jl[u] == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+              if (p.lse != nullptr && sub == 0) p.lse[o_at] = log_sum(jm[u], jl[u]);
+            }
+          } else if (in) {
+            *reinterpret_cast<float4*>(out_slot + row[u] * kSlotStride + 4 * sub) = jo[u];
+            if (sub == 0) {
+              out_slot[kM * kSlotStride + row[u]] = jm[u];
+              out_slot[kM * kSlotStride + kM + row[u]] = jM[u];
+              out_slot[kM * kSlotStride + 2 * kM + row[u]] = jl[u];
+            }
+          }
+          const uint32_t bits = __ballot_sync(0xffffffffu, wild);
+          which |= ((bits & 0xffffu) ? 1u : 0u) << (2 * (i + u)) | ((bits >> 16) ? 2u : 0u) << (2 * (i + u));
+        }
+      };
+      int i = max(from - before, 0);
+      if (end - i == 1) {
+        join_pairs(std::integral_constant<int, 1>(), i);
+      } else {
+#pragma unroll 1
+        for (; i < end; i += 2) join_pairs(std::integral_constant<int, 2>(), i);
       }
       if (which != 0) {
         __syncwarp();
-        redo_rows<kE4m3>(a, p, which, s0 + at.s, s_row0[at.s], n, s_len[at.s], at.h);
+        redo_rows<kE4m3>(a, p, which, s0 + it.s, s_row0[it.s], n, s_len[it.s], it.h);
       }
     }
   }
-  // What the join kernel finds of this CTA: the item that begins here and goes on, if there is one.
-  if (tid == 0 && gridDim.x > 1 && !whole_items) {
-    StepJoin j{};
-    if (ok && cta_lo < cta_hi) {
-      At at{};
-      locate(cta_hi - 1, at);
-      const int64_t ib = cta_hi - 1 - at.blk, ie = ib + at.units;
-      if (ib >= cta_lo && ie > cta_hi) {
-        const int64_t x = ie - 1;   // its last unit, and the warp that has it
-        const int64_t w = x < more * (each + 1) ? quotient(x, each + 1) : more + quotient(x - more * (each + 1), each);
-        j.parts = static_cast<int32_t>(w / kW) - static_cast<int32_t>(blockIdx.x) + 1;
-        j.s = s0 + at.s;
-        j.h = at.h;
-        j.n = s_count[at.s];
-        j.len = s_len[at.s];
-        j.row0 = s_row0[at.s];
-      }
-    }
-    *reinterpret_cast<StepJoin*>(ws_part + 2 * kSlotFloats) = j;
+  // (warp 0's lanes have the records: the one that has the item writes, or lane 0)
+  if (warp == 0 && gridDim.x > 1 && !whole_items) {
+    const uint32_t goes_on = __ballot_sync(0xffffffffu, join.parts > 0);
+    if (goes_on != 0 ? join.parts > 0 : lane == 0) *reinterpret_cast<StepJoin*>(ws_part + 2 * kSlotFloats) = join;
   }
 }
 
 // CTA (c, y): row heads 4 y .. 4 y + 3 of the item that begins in CTA c of the step kernel and goes on, from the parts of
-// it and the next CTAs.  16 groups of 16 lanes: group (row, slice) has every fourth part of a row head, a lane four
+// it and the next CTAs.  Groups of 16 lanes: group (row, slice) has every kJoinSlices-th part of a row head, a lane four
 // elements of O; the row heads' maxima and sums are one group's, a lane a part.  What most items need is asked for before
 // the record is there that says what they need (the workspace holds all of it, whether or not it is of this item): the
 // kernel is three reads one behind the other else, and little more.
-constexpr int kJoinThreads = 256, kJoinEach = kStepMaxGrid / 16, kJoinRows = 4, kJoinSlices = 4, kJoinAhead = 2;
+constexpr int kJoinEach = kStepMaxGrid / 16, kJoinRows = 4, kJoinAhead = 2;
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
+template <bool kE4m3, int kJoinSlices>
+__global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16) paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
                                                                   const float* ws) {
-  __shared__ float4 so[16][16];
+  __shared__ float4 so[kJoinRows * kJoinSlices][16];
   __shared__ float factor[kJoinRows][kStepMaxGrid];
   __shared__ float total[kJoinRows][3];
   __shared__ uint32_t wild;
@@ -884,7 +958,8 @@ int paged_step_grid(int64_t most_units, int num_sms) {
 }
 
 // At most 8 row heads where the call says so (max_rows): the products' second half, and its exponentials, are left out.
-// One token of 61 sequences over e4m3 pages, 16 heads: see above; the same by the kernel for 16 row heads: 1.2 times that.
+// (61 tokens over e4m3 pages, 16 heads: 117.5 us, by the kernel for 16 row heads 133; 128 tokens over bf16 pages, four heads
+// a key head: 221 and 223.)
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
                               int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream) {
   const bool two = a.max_rows * p.group > 8;
@@ -895,7 +970,13 @@ cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
   const int64_t most = std::min<int64_t>(kM, a.max_rows * p.group);   // row heads
   const dim3 ctas(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
-  return launch_behind(e4m3 ? paged_join_kernel<true> : paged_join_kernel<false>, ctas, kJoinThreads, 0, stream, a, p, ws);
+  // Items over four CTAs and more: twice the threads, as a thread then has several parts; but where the call has long
+  // chunks too (and its step kernel perhaps nothing), the bigger launch costs more.  (131,072 rows, up to 90 parts: 18.4 us,
+  // by twice the threads 17.7; 24 x 4 tokens, up to 6 parts: 30.5 and 31.9; a chunk of 512: 34.9 and 35.8.)
+  const bool many = static_cast<int64_t>(a.seqs) * a.heads * 4 <= grid && a.max_rows * p.group <= kM;
+  auto* kernel = many ? (e4m3 ? paged_join_kernel<true, 8> : paged_join_kernel<false, 8>)
+                      : (e4m3 ? paged_join_kernel<true, 4> : paged_join_kernel<false, 4>);
+  return launch_behind(kernel, ctas, many ? 512 : 256, 0, stream, a, p, ws);
 }
 
 }  // namespace spanla

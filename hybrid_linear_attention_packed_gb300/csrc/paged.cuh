@@ -122,8 +122,8 @@ __device__ __forceinline__ float2 cached_pair(const KvArgs& a, const void* base,
 // throughout: the row of sequence s that sees its first `seen` rows.  The other
 // kernels send a row here whose products came out infinite or NaN though its sum of
 // weights is finite: they multiply rows that the row does not see by 0, this does
-// not touch them.  (0.15 us a cached row, four of them at a time: a step of nothing
-// but NaN takes some hundred times as long as another.)
+// not touch them.  (0.38 us a cached row, four of them at a time, latency: a token over
+// 7,401 rows whose V is infinite somewhere 2.8 ms instead of 12 us.)
 template <bool kE4m3>
 __device__ __noinline__ void attend_row(const KvArgs& a, const PagedAttn& p, int s, int64_t t, int head, int32_t seen) {
   constexpr int kAtOnce = 4;
