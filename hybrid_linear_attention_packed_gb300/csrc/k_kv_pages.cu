@@ -15,7 +15,9 @@
 // of two go out as one store.  (All 32 rows at once: twice the registers and half
 // the warps, 45 us for four prompts of fp32 rows instead of 40.)  Few rows are bound
 // by the reads that find their places, one behind the other: lengths, then the
-// page; the rows themselves are on their way meanwhile.
+// page; the rows themselves are on their way meanwhile.  Measured: four prompts of
+// fp32 rows (20,576 rows, 16 heads) into e4m3 pages 36.6 us, 5.8 TB/s; sixteen views
+// (87,648 rows) out of bf16 pages 109.5 us, 6.6 TB/s; eight tokens written 2.7 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -281,7 +283,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
   }
 }
 
-// A warp: 16 rows of one page and head, of K or V.  Bound by memory (65 bytes in, 128 out, a row and head).
+// A warp: 16 rows of one page and head, of K or V.  Bound by memory (65 bytes in, 128 out, a row and head) and, as small
+// as it is, by its launch: 20,048 rows of 4 key heads 10 us from cold caches.
 __global__ void __launch_bounds__(kWarps * 32) kv_expand_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ KvArgs to,
                                                                 int group) {
   griddep_wait();

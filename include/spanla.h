@@ -668,10 +668,11 @@ span_la_status span_la_kv_read(const span_la_kv_cache *cache, int64_t rows, int3
  *   scale            > 0, or 0 for 1/sqrt(64)
  *   out              device bf16 [rows][num_q_heads][64], 16-byte aligned
  *   lse_out          device fp32 [rows][num_q_heads] or NULL
- *   workspace        device memory of span_la_softmax_paged_workspace() bytes,
- *                    16-byte aligned, for this call alone until the stream has
- *                    passed it; or NULL: allocated and freed on the stream (2 us
- *                    of it)
+ *   workspace        device memory of span_la_softmax_paged_workspace() bytes
+ *                    (up to 24 MB; 158 where 2,048 row heads and more may share
+ *                    E4M3 pages, which are then expanded into it), 16-byte
+ *                    aligned, for this call alone until the stream has passed it;
+ *                    or NULL: allocated and freed on the stream (2 us of it)
  * A row that sees nothing (or nothing but scores of -infinity) gets o = 0 and
  * lse = -infinity.  What a row does not see does not reach it, whatever it holds.
  * Scores, sums and o are fp32; out is rounded to bf16.  Deterministic.
