@@ -213,7 +213,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  griddep_launch_dependents();   // (the join kernel's CTAs wait for this grid's end)
+  griddep_wait();                // (what comes before the call)
+  griddep_launch_dependents();   // (the step kernel reads nothing of this one; what comes behind it waits for both)
   // ---------------------------------------------------------------- the sequences' running sums of blocks
   {
     const int per = (ns + C::kThreads - 1) / C::kThreads, b = min(ns, tid * per), e = min(ns, b + per);
@@ -711,9 +712,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
-  // The launches before it in the call work on other sequences, so it need not have waited for them; but what comes
-  // behind the call waits for it alone.
-  griddep_wait();
 }
 
 // CTA (c, y): 32 row heads (y & 3) of tile y >> 2 of the item that begins in CTA c of the chunk kernel and goes on, from
@@ -802,7 +800,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
 
 template <bool kE4m3>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0,
-                   int ns, int grid, float* ws, bool behind, cudaStream_t stream) {
+                   int ns, int grid, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3>;
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> regs{0};
@@ -815,18 +813,15 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
   const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  if (behind)   // (see the kernel's end)
-    return launch_behind(paged_chunk_kernel<kE4m3>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
-  paged_chunk_kernel<kE4m3><<<grid, C::kThreads, C::kRequest, stream>>>(tm_q, tm_k, tm_v, a, p, s0, ns, ws);
-  return cudaGetLastError();
+  return launch_behind(paged_chunk_kernel<kE4m3>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
-                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, bool behind, cudaStream_t stream) {
-  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, behind, stream)
-              : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, behind, stream);
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream) {
+  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream)
+              : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
 }
 
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {

@@ -160,7 +160,7 @@ __device__ __forceinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, u
 template <bool kE4m3, bool kTwo>
 __global__ void __launch_bounds__(Cfg<kE4m3, kTwo>::kWarps * 32, 1)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvArgs a,
-                  const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, float* ws) {
+                  const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, bool behind, float* ws) {
   using C = Cfg<kE4m3, kTwo>;
   constexpr int kW = C::kWarps, kS = C::kStages, kUnit = C::kUnit, kN = kUnit / 8, kR = kTwo ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -183,8 +183,10 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       tma_prefetch_desc(&tm_v);
     }
   }
-  griddep_wait();                // (what comes before the call)
-  griddep_launch_dependents();   // (the next kernels of the call wait for this grid's end, or need not)
+  // Behind the call's chunk kernel, which has waited for what comes before the call, and works on other sequences: no wait
+  // but one CTA's at the end, as what comes behind waits for this grid alone.
+  if (!behind) griddep_wait();
+  griddep_launch_dependents();
   // ---------------------------------------------------------------- the sequences' running sums of units
   {
     const int per = (ns + kW * 32 - 1) / (kW * 32), b = min(ns, tid * per), e = min(ns, b + per);
@@ -838,6 +840,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t goes_on = __ballot_sync(0xffffffffu, join.parts > 0);
     if (goes_on != 0 ? join.parts > 0 : lane == 0) *reinterpret_cast<StepJoin*>(ws_part + 2 * kSlotFloats) = join;
   }
+  if (behind && blockIdx.x == 0) griddep_wait();
 }
 
 // CTA (c, y): row heads 4 y .. 4 y + 3 of the item that begins in CTA c of the step kernel and goes on, from the parts of
@@ -937,13 +940,13 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16) paged_join_kerne
 
 template <bool kE4m3, bool kTwo>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns, int grid,
-                   bool whole_items, float* ws, cudaStream_t stream) {
+                   bool whole_items, bool behind, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3, kTwo>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3, kTwo>, C::kRequest, done);
   if (e != cudaSuccess) return e;
   return launch_behind(paged_step_kernel<kE4m3, kTwo>, dim3(grid), C::kWarps * 32, C::kRequest, stream, tm_k, tm_v, a, p, s0, ns,
-                       whole_items, ws);
+                       whole_items, behind, ws);
 }
 
 }  // namespace
@@ -961,10 +964,10 @@ int paged_step_grid(int64_t most_units, int num_sms) {
 // (61 tokens over e4m3 pages, 16 heads: 117.5 us, by the kernel for 16 row heads 133; 128 tokens over bf16 pages, four heads
 // a key head: 221 and 223.)
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
-                              int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream) {
+                              int grid, bool e4m3, bool whole_items, bool behind, float* ws, cudaStream_t stream) {
   const bool two = a.max_rows * p.group > 8;
-  return e4m3 ? (two ? launch<true, true> : launch<true, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream)
-              : (two ? launch<false, true> : launch<false, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream);
+  return e4m3 ? (two ? launch<true, true> : launch<true, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, behind, ws, stream)
+              : (two ? launch<false, true> : launch<false, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, behind, ws, stream);
 }
 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {

@@ -2236,7 +2236,6 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   float* cws = bytes > 0 ? ws + grids.step_ws / sizeof(float) : nullptr;
   KvArgs c = a;   // what the chunk kernel reads
   if (grids.expand) {
-    // (Before the step kernel: the chunk kernel starts behind that, which has waited for this.)
     c.k = reinterpret_cast<uint8_t*>(cws) + grids.chunk_ws;
     c.v = static_cast<uint8_t*>(c.k) + grids.copies;
     c.row_stride = kHeadDim;
@@ -2246,32 +2245,51 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     e = counted_launch(kKernelKvExpand, stream, [&] { return launch_kv_expand(a, c, p.group, stream); });
   }
   const bool chunk_e4m3 = e4m3 && !grids.expand;
-  if (step && e == cudaSuccess) {
+  CUtensorMap tm_ck, tm_cv;
+  if (chunk) {
+    st = encode_tile(&tm_q, a, p);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_ck, c.k, c, chunk_e4m3, kTileRows);
+    if (st == SPAN_LA_OK) st = encode_pages(&tm_cv, c.v, c, chunk_e4m3, kTileRows);
+  }
+  if (step && st == SPAN_LA_OK) {
     st = encode_pages(&tm_k, a.k, a, e4m3, unit);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, unit);
-    if (st == SPAN_LA_OK)
-      each([&](int s0, int ns) {
-        cudaError_t x = counted_launch(kKernelPagedStep, stream,
-                                       [&] { return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, grids.whole, ws, stream); });
-        if (x == cudaSuccess && step_grid > 1 && !grids.whole)
-          x = counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, step_grid, e4m3, ws, stream); });
-        return x;
-      });
   }
-  if (chunk && st == SPAN_LA_OK && e == cudaSuccess) {
-    st = encode_tile(&tm_q, a, p);
-    if (st == SPAN_LA_OK) st = encode_pages(&tm_k, c.k, c, chunk_e4m3, kTileRows);
-    if (st == SPAN_LA_OK) st = encode_pages(&tm_v, c.v, c, chunk_e4m3, kTileRows);
-    const bool behind = step;   // (which it need not wait for)
-    if (st == SPAN_LA_OK)
-      each([&](int s0, int ns) {
-        cudaError_t x = counted_launch(kKernelPagedChunk, stream, [&] {
-          return launch_paged_chunk(tm_q, tm_k, tm_v, c, p, s0, ns, chunk_grid, chunk_e4m3, cws, behind && s0 == 0, stream);
+  const bool step_join = step_grid > 1 && !grids.whole, chunk_join = chunk_grid > 1;
+  auto run_step = [&](int s0, int ns, bool behind) {
+    return counted_launch(kKernelPagedStep, stream, [&] {
+      return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, grids.whole, behind, ws, stream);
+    });
+  };
+  auto run_step_join = [&] { return counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, step_grid, e4m3, ws, stream); }); };
+  auto run_chunk = [&](int s0, int ns) {
+    return counted_launch(kKernelPagedChunk, stream, [&] {
+      return launch_paged_chunk(tm_q, tm_ck, tm_cv, c, p, s0, ns, chunk_grid, chunk_e4m3, cws, stream);
+    });
+  };
+  auto run_chunk_join = [&] {
+    return counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(c, p, chunk_grid, chunk_e4m3, cws, stream); });
+  };
+  if (st == SPAN_LA_OK && e == cudaSuccess) {
+    if (step && chunk && a.seqs <= kStepSeqs) {
+      // The chunk kernel first: where there are only chunks, the step kernel's CTAs come and go beside its last ones.  (A
+      // chunk of 512: XXX us, the step kernel first 34.5; 2,048 rows XXX and 176.9, the mixed step XXX and XXX.)
+      e = run_chunk(0, a.seqs);
+      if (e == cudaSuccess) e = run_step(0, a.seqs, true);
+      if (e == cudaSuccess && chunk_join) e = run_chunk_join();
+      if (e == cudaSuccess && step_join) e = run_step_join();
+    } else {
+      if (chunk)
+        each([&](int s0, int ns) {
+          const cudaError_t x = run_chunk(s0, ns);
+          return x == cudaSuccess && chunk_join ? run_chunk_join() : x;
         });
-        if (x == cudaSuccess && chunk_grid > 1)
-          x = counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(c, p, chunk_grid, chunk_e4m3, cws, stream); });
-        return x;
-      });
+      if (step)
+        each([&](int s0, int ns) {
+          const cudaError_t x = run_step(s0, ns, false);
+          return x == cudaSuccess && step_join ? run_step_join() : x;
+        });
+    }
   }
   const cudaError_t ef = ws != nullptr && workspace == nullptr ? cudaFreeAsync(ws, stream) : cudaSuccess;
   if (e == cudaSuccess) e = ef;

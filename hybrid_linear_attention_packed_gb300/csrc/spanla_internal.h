@@ -452,7 +452,8 @@ struct PagedAttn {
 };
 // Sequences of at most kStepHeads packed row heads (rows * group) of a key head (k_paged_step.cu), at most kStepSeqs in
 // a launch: [s0, s0 + ns).  `ws`: kStepWsFloats for each of the `grid` CTAs; the join kernel, with the same grid, follows
-// where there is more than one, unless the CTAs take whole items.
+// where there is more than one, unless the CTAs take whole items.  `behind`: behind the chunk kernel of the same call, whose
+// end it need not wait for.
 constexpr int kStepHeads = 16, kStepSeqs = 512;
 constexpr int kStepWsFloats = 2432, kStepMaxGrid = 160;
 struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begins in the CTA and goes on in the next ones
@@ -463,11 +464,10 @@ struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begin
 int paged_step_unit(bool e4m3);   // cached rows of a unit of work
 int paged_step_grid(int64_t most_units, int num_sms);
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
-                              int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream);
+                              int grid, bool e4m3, bool whole_items, bool behind, float* ws, cudaStream_t stream);
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
 // Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles).
-// `behind`: behind the step kernels of the same call, whose end it need not wait for.
 constexpr int kChunkPartFloats = kTileRows * kHeadDim + 2 * kTileRows;
 constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8;
 struct alignas(16) ChunkJoin {
@@ -476,7 +476,7 @@ struct alignas(16) ChunkJoin {
   int32_t pad;
 };
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
-                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, bool behind, cudaStream_t stream);
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream);
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
