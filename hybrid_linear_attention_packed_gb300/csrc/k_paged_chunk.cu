@@ -35,7 +35,7 @@
 //   12-15  e4m3 pages: K and V as they were loaded into bf16 tiles, a thread a row, times its power of two (exact)
 #include <algorithm>
 
-#include "paged.cuh"
+#include "paged_join.cuh"
 
 namespace spanla {
 namespace {
@@ -93,11 +93,6 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -717,16 +712,23 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // CTA (c, y): 32 row heads (y & 3) of tile y >> 2 of the item that begins in CTA c of the chunk kernel and goes on, from
 // the parts of it and the next CTAs.  A lane has a row head, warp w eight elements of O, and the maxima and sums of every
 // eighth part.  What an item of two parts needs is asked for before the record is there that says how many there are.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinAhead = 2;
+constexpr int kChunkJoinThreads = 256, kJoinWarps = kChunkJoinThreads / 32;
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
-                                                                  const float* ws) {
+// CTAs (c, 8 ..), where there are any: the step kernel's parts (of `step_grid` CTAs), which it has of the same call.
+template <bool kE4m3, bool kStepE4m3>
+__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
+                                                                       const float* ws, const __grid_constant__ KvArgs step, const float* step_ws,
+                                                                       int step_grid) {
   __shared__ float factor[kStepMaxGrid][32];
   __shared__ float best[kJoinWarps][32], sums[kJoinWarps][32];
   __shared__ uint32_t wild;
   griddep_launch_dependents();
   griddep_wait();
+  if (blockIdx.y >= 8) {
+    if (static_cast<int>(blockIdx.x) < step_grid)
+      join_step_parts<kStepE4m3, kChunkJoinThreads / 16 / kJoinRows>(step, p, step_ws, step_grid, static_cast<int>(blockIdx.y) - 8);
+    return;
+  }
   const float* mine = ws + blockIdx.x * kChunkWsFloats;
   const int x = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (blockIdx.y & 3) * 32 + lane;
   const int last = static_cast<int>(gridDim.x - 1 - blockIdx.x);
@@ -824,8 +826,11 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
               : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
 }
 
-cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
-  return launch_behind(e4m3 ? chunk_join_kernel<true> : chunk_join_kernel<false>, dim3(grid, 8), kJoinThreads, 0, stream, a, p, ws);
+cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, const KvArgs& step, int step_grid,
+                              bool step_e4m3, const float* step_ws, cudaStream_t stream) {
+  auto* kernel = e4m3 ? chunk_join_kernel<true, true> : step_e4m3 ? chunk_join_kernel<false, true> : chunk_join_kernel<false, false>;
+  return launch_behind(kernel, dim3(grid, step_grid > 0 ? 8 + kM / kJoinRows : 8), kChunkJoinThreads, 0, stream, a, p, ws, step, step_ws,
+                       step_grid);
 }
 
 }  // namespace spanla

@@ -36,16 +36,10 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "paged.cuh"
+#include "paged_join.cuh"
 
 namespace spanla {
 namespace {
-
-constexpr int kM = kStepHeads;            // row heads of an item, at most
-constexpr int kSlotStride = 72;           // floats from row head to row head of a part (72: no bank conflicts)
-
-// A part of an item: [kM][72] floats of O, then m, M, l of kM row heads.
-constexpr int kSlotFloats = kM * kSlotStride + 3 * kM;
 
 // kTwo: up to 16 row heads, as 8 and 8 (else up to 8, and the products' second half is empty).
 template <bool kE4m3, bool kTwo>
@@ -77,12 +71,6 @@ struct Cfg {
   static constexpr uint32_t kRequest = kBytes + 1024;
   static_assert(kRequest <= 227 * 1024 && kRing >= kSlot * 4 && kInfo % 8 == 0 && kSum % 16 == 0 && kHead % 16 == 0, "shared memory");
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -132,29 +120,6 @@ struct Open {
 // Output of a row head: elements d, d + 1.
 __device__ __forceinline__ void store_pair(const PagedAttn& p, int64_t at, int d, float x, float y) {
   *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + d) = pack_bf16x2(x, y);
-}
-
-// The weights of a row head are relative to 2^m, its O to 2^(M - 15) (bf16 pages: 2^m): o = O 2^(M - 15 - m) / l.
-template <bool kE4m3>
-__device__ __forceinline__ float out_factor(float m, float M, float l) {
-  return l == 0.f ? 0.f : (kE4m3 ? ex2(M - m - 15.f) : 1.f) / l;
-}
-__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l)); }
-
-// 2^(from - to), 0 where nothing is relative to `from`.
-__device__ __forceinline__ float rescale(float from, float to) { return from == to ? 1.f : from == -INFINITY ? 0.f : ex2(from - to); }
-
-// Row heads of an item whose O came out infinite or NaN though the sum of weights is finite: once more from the
-// cache, without the rows that they do not see (and without O's parts, whose infinities may cancel).
-template <bool kE4m3>
-__device__ __forceinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, uint32_t which, int s, int64_t row0, int n, int32_t len,
-                                          int h) {
-  while (which != 0) {
-    const int m = __ffs(which) - 1;
-    which &= which - 1;
-    const int r = m / p.group;
-    attend_row<kE4m3>(a, p, s, row0 + r, h * p.group + m % p.group, max(0, len - n + r + 1));
-  }
 }
 
 template <bool kE4m3, bool kTwo>
@@ -843,99 +808,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (behind && blockIdx.x == 0) griddep_wait();
 }
 
-// CTA (c, y): row heads 4 y .. 4 y + 3 of the item that begins in CTA c of the step kernel and goes on, from the parts of
-// it and the next CTAs.  Groups of 16 lanes: group (row, slice) has every kJoinSlices-th part of a row head, a lane four
-// elements of O; the row heads' maxima and sums are one group's, a lane a part.  What most items need is asked for before
-// the record is there that says what they need (the workspace holds all of it, whether or not it is of this item): the
-// kernel is three reads one behind the other else, and little more.
-constexpr int kJoinEach = kStepMaxGrid / 16, kJoinRows = 4, kJoinAhead = 2;
-
 template <bool kE4m3, int kJoinSlices>
-__global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16) paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
-                                                                  const float* ws) {
-  __shared__ float4 so[kJoinRows * kJoinSlices][16];
-  __shared__ float factor[kJoinRows][kStepMaxGrid];
-  __shared__ float total[kJoinRows][3];
-  __shared__ uint32_t wild;
+__global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16) paged_join_kernel(const __grid_constant__ KvArgs a,
+                                                                                  const __grid_constant__ PagedAttn p, const float* ws) {
   griddep_launch_dependents();
   griddep_wait();
-  const float* mine = ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats;
-  const int tid = threadIdx.x, grp = tid >> 4, sub = tid & 15, last = static_cast<int>(gridDim.x - 1 - blockIdx.x);
-  const int row4 = grp & (kJoinRows - 1), row = kJoinRows * blockIdx.y + row4, slice = grp / kJoinRows;
-  auto part_of = [&](int i) { return mine + static_cast<int64_t>(i) * kStepWsFloats + (i == 0 ? kSlotFloats : 0); };
-  const StepJoin j = *reinterpret_cast<const StepJoin*>(mine + 2 * kSlotFloats);
-  float pm[kJoinEach], pM[kJoinEach], pl[kJoinEach];
-  {
-    const float* st = part_of(min(sub, last)) + kM * kSlotStride + row;
-    pm[0] = st[0], pM[0] = st[kM], pl[0] = st[2 * kM];
-  }
-  float4 ahead[kJoinAhead];
-#pragma unroll
-  for (int k = 0; k < kJoinAhead; ++k)
-    ahead[k] = *reinterpret_cast<const float4*>(part_of(min(slice + kJoinSlices * k, last)) + row * kSlotStride + 4 * sub);
-  const int mh = j.n * p.group;
-  if (j.parts == 0 || kJoinRows * static_cast<int>(blockIdx.y) >= mh) return;
-  if (tid == 0) wild = 0;
-  if (slice == 0) {
-    float m = -INFINITY, M = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinEach; ++k) {
-      const int i = sub + 16 * k;
-      if (i >= j.parts) {
-        pm[k] = pM[k] = -INFINITY, pl[k] = 0.f;
-      } else if (k > 0) {
-        const float* st = part_of(i) + kM * kSlotStride + row;
-        pm[k] = st[0], pM[k] = st[kM], pl[k] = st[2 * kM];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kJoinEach; ++k) m = fmaxf(m, pm[k]), M = fmaxf(M, pM[k]);
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    }
-#pragma unroll
-    for (int k = 0; k < kJoinEach; ++k) {
-      if (16 * k >= j.parts) break;
-      l += pl[k] * rescale(pm[k], m);
-      factor[row4][sub + 16 * k] = rescale(pM[k], M);
-    }
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (sub == 0) total[row4][0] = m, total[row4][1] = M, total[row4][2] = l;
-  }
-  __syncthreads();
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float4& x, float f) {
-    o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
-  };
-  if (row < mh) {
-#pragma unroll
-    for (int k = 0; k < kJoinAhead; ++k)
-      if (slice + kJoinSlices * k < j.parts) add(ahead[k], factor[row4][slice + kJoinSlices * k]);
-#pragma unroll 8
-    for (int i = slice + kJoinSlices * kJoinAhead; i < j.parts; i += kJoinSlices)
-      add(*reinterpret_cast<const float4*>(part_of(i) + row * kSlotStride + 4 * sub), factor[row4][i]);
-  }
-  so[grp][sub] = o;
-  __syncthreads();
-  if (slice == 0 && row < mh) {
-#pragma unroll
-    for (int i = 1; i < kJoinSlices; ++i) add(so[grp + i * kJoinRows][sub], 1.f);
-    const float m = total[row4][0], M = total[row4][1], l = total[row4][2], f = out_factor<kE4m3>(m, M, l);
-    const int64_t at = (j.row0 + static_cast<int64_t>(row / p.group)) * p.heads + j.h * p.group + row % p.group;
-    const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
-    bool w = false;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) w |= !(fabsf(y[c]) <= 3.4e38f);
-    if (w && l == l && l != 0.f) atomicOr(&wild, 1u << row);
-    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * sub) =
-        l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-    if (p.lse != nullptr && sub == 0) p.lse[at] = log_sum(m, l);
-  }
-  __syncthreads();
-  if (wild != 0 && tid < 32) redo_rows<kE4m3>(a, p, wild, j.s, j.row0, j.n, j.len, j.h);
+  join_step_parts<kE4m3, kJoinSlices>(a, p, ws, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.y));
 }
 
 template <bool kE4m3, bool kTwo>

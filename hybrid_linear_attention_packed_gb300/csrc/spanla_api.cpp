@@ -2267,22 +2267,25 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
       return launch_paged_chunk(tm_q, tm_ck, tm_cv, c, p, s0, ns, chunk_grid, chunk_e4m3, cws, stream);
     });
   };
-  auto run_chunk_join = [&] {
-    return counted_launch(kKernelChunkJoin, stream, [&] { return launch_chunk_join(c, p, chunk_grid, chunk_e4m3, cws, stream); });
+  auto run_chunk_join = [&](bool with_step) {
+    return counted_launch(kKernelChunkJoin, stream, [&] {
+      return launch_chunk_join(c, p, chunk_grid, chunk_e4m3, cws, a, with_step ? step_grid : 0, e4m3, ws, stream);
+    });
   };
   if (st == SPAN_LA_OK && e == cudaSuccess) {
     if (step && chunk && a.seqs <= kStepSeqs) {
-      // The chunk kernel first: where there are only chunks, the step kernel's CTAs come and go beside its last ones.  (A
-      // chunk of 512: XXX us, the step kernel first 34.5; 2,048 rows XXX and 176.9, the mixed step XXX and XXX.)
+      // The chunk kernel first: where there are only chunks, the step kernel's CTAs come and go beside its last ones; and one
+      // kernel for both joins.  (A chunk of 512: the step kernel first 34.4 us, second 33.8, one join 33.1; 2,048 rows 176.3,
+      // 175.0, 174.5; the mixed step 110.7, 110.6, 108.4.)
       e = run_chunk(0, a.seqs);
       if (e == cudaSuccess) e = run_step(0, a.seqs, true);
-      if (e == cudaSuccess && chunk_join) e = run_chunk_join();
-      if (e == cudaSuccess && step_join) e = run_step_join();
+      if (e == cudaSuccess && chunk_join) e = run_chunk_join(step_join);
+      else if (e == cudaSuccess && step_join) e = run_step_join();
     } else {
       if (chunk)
         each([&](int s0, int ns) {
           const cudaError_t x = run_chunk(s0, ns);
-          return x == cudaSuccess && chunk_join ? run_chunk_join() : x;
+          return x == cudaSuccess && chunk_join ? run_chunk_join(false) : x;
         });
       if (step)
         each([&](int s0, int ns) {

@@ -477,7 +477,9 @@ struct alignas(16) ChunkJoin {
 };
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
                                const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream);
-cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
+// step, step_grid (0: none), ...: joins the step kernel's parts of the same call too.
+cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, const KvArgs& step, int step_grid,
+                              bool step_e4m3, const float* step_ws, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_probe(unsigned limit_us, unsigned* err, cudaStream_t stream);
 
