@@ -27,8 +27,8 @@
 //
 // Measured (with the join, one call behind the other): 128 tokens of up to 18,000
 // rows over bf16 pages, 8 key heads of 4, 222 us, 6.8 TB/s, as fast as a copy; 61
-// over e4m3 pages, 16 heads, 118 us, 5.3 TB/s (issue slots: a warp takes 766
-// instructions for 64 rows of e4m3, and its chains of them leave half of the slots
+// over e4m3 pages, 16 heads, 115.5 us, 5.4 TB/s (a warp takes 790 instructions for
+// 64 rows of e4m3, and the chains of eleven warps leave half of the SM's issue slots
 // empty).  One token of one sequence, 7,401 rows, 16 heads, 11.4 us, of which the
 // data are 4.5: the lengths are there after 1.0, the first unit's data after 2.9,
 // the last unit is done after 7.4, the warps' parts are one after 8.5, and the join
@@ -80,6 +80,14 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+
+// Two sums at once, two products.  (One by one 118.4 us instead of 115.5 for 61 tokens over e4m3 pages.)
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2(x, y)), "l"(f32x2(a, b)));
+  f32x2_split(d, x, y);
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) { f32x2_split(mul_f32x2(f32x2(x, y), f32x2(a, b)), x, y); }
 
 template <bool kHalfFloat>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -234,7 +242,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   const uint32_t ring = base + warp * C::kRing;
   uint8_t* ring_p = smem + warp * C::kRing;
   uint64_t* info = reinterpret_cast<uint64_t*>(smem + C::kInfo) + warp * kS;
-  float2* factors = reinterpret_cast<float2*>(smem + C::kFactors) + warp * kUnit;
+  float* factors = reinterpret_cast<float*>(smem + C::kFactors) + warp * kUnit * 2;
   uint8_t* scales = smem + C::kScales + warp * kS * 2 * kUnit;
   // A part that began in an earlier warp stands in the head slot, one that goes on in later ones in the ring, which is
   // done by then.
@@ -404,12 +412,16 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       fence_proxy_async_smem();   // (the next load of this stage comes behind it)
     }
     if (kE4m3) {
-      // (what a row's powers of two do: the score's factor, the weight's logarithm)
+      // (what a row's powers of two do: the score's factor, the weight's logarithm; of the two rows that a lane has of a
+      // block of 8, side by side: rows 0 3, 1 2, 4 7, 5 6)
 #pragma unroll
       for (int k = 0; k < kUnit / 32; ++k) {
         const uint8_t* sc = scales + stage * 2 * kUnit + lane + 32 * k;
         const uint32_t v = sc[kUnit];
-        factors[lane + 32 * k] = make_float2(scale_of(sc[0]), v == 255 ? NAN : static_cast<float>(static_cast<int>(v) - 127));
+        const int in4 = lane & 3, second = in4 >> 1;
+        float* to = factors + ((lane + 32 * k) >> 3) * 16 + (((lane >> 2) & 1) * 2 + (second ? 3 - in4 : in4)) * 4 + second;
+        to[0] = scale_of(sc[0]);
+        to[2] = v == 255 ? NAN : static_cast<float>(static_cast<int>(v) - 127);
       }
     }
     __syncwarp();
@@ -463,14 +475,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (r == 1 && !two) break;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          x[i][2 * r + c] *= qc[r];
-          if (kE4m3) {
-            const float2 sc = factors[i * 8 + (c ? f1 : f0)];
-            x[i][2 * r + c] *= sc.x;
-            z[i][2 * r + c] = x[i][2 * r + c] + sc.y;
-          }
+        mul2(x[i][2 * r], x[i][2 * r + 1], qc[r], qc[r]);
+        if (kE4m3) {
+          const float4 sc = *reinterpret_cast<const float4*>(factors + i * 16 + t * 4);
+          mul2(x[i][2 * r], x[i][2 * r + 1], sc.x, sc.y);
+          z[i][2 * r] = x[i][2 * r], z[i][2 * r + 1] = x[i][2 * r + 1];
+          add2(z[i][2 * r], z[i][2 * r + 1], sc.z, sc.w);
         }
       }
     }
@@ -522,11 +532,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
     }
     // Weights and O, 16 cached rows at a time.
-    float bm[kR], bM[kR];
+    float bm[kR], bM[kR], sum0[kR], sum1[kR];   // (less m, less M and 15 more)
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      bm[r] = m[r] == -INFINITY ? 0.f : m[r];
-      bM[r] = (M[r] == -INFINITY ? 0.f : M[r]) - 15.f;
+      bm[r] = m[r] == -INFINITY ? 0.f : -m[r];
+      bM[r] = 15.f - (M[r] == -INFINITY ? 0.f : M[r]);
+      sum0[r] = sum1[r] = 0.f;
     }
 #pragma unroll
     for (int ks = 0; ks < kN / 2; ++ks) {
@@ -537,10 +548,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int i = 2 * ks + half;
-          const float p0 = ex2(x[i][2 * r] - bm[r]), p1 = ex2(x[i][2 * r + 1] - bm[r]);
-          l[r] += p0 + p1;
+          add2(x[i][2 * r], x[i][2 * r + 1], bm[r], bm[r]);
+          const float p0 = ex2(x[i][2 * r]), p1 = ex2(x[i][2 * r + 1]);
+          add2(sum0[r], sum1[r], p0, p1);
           if (kE4m3) {
-            hi_p[2 * half + r] = half2_of(ex2(z[i][2 * r] - bM[r]), ex2(z[i][2 * r + 1] - bM[r]));
+            add2(z[i][2 * r], z[i][2 * r + 1], bM[r], bM[r]);
+            hi_p[2 * half + r] = half2_of(ex2(z[i][2 * r]), ex2(z[i][2 * r + 1]));
           } else {
             const uint32_t h = pack_bf16x2(p0, p1);
             hi_p[2 * half + r] = h;
@@ -577,6 +590,8 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int j = 0; j < 8; ++j) mma16816<false>(o[j], lo_p, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
       }
     }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) l[r] += sum0[r] + sum1[r];
     __syncwarp();
     ++done;
     if (issued < hi) {
@@ -839,7 +854,7 @@ int paged_step_grid(int64_t most_units, int num_sms) {
 }
 
 // At most 8 row heads where the call says so (max_rows): the products' second half, and its exponentials, are left out.
-// (61 tokens over e4m3 pages, 16 heads: 117.5 us, by the kernel for 16 row heads 133; 128 tokens over bf16 pages, four heads
+// (61 tokens over e4m3 pages, 16 heads: 117.5 us then, by the kernel for 16 row heads 133; 128 tokens over bf16 pages, four heads
 // a key head: 221 and 223.)
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
                               int grid, bool e4m3, bool whole_items, bool behind, float* ws, cudaStream_t stream) {
