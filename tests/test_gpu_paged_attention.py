@@ -7,6 +7,7 @@ from hybrid_linear_attention_packed_gb300 import (SpanLAError, kv_pages, packed_
                                                   span_la_kv_read, span_la_kv_write, span_la_qk_norm_rope,
                                                   span_la_softmax_branches_from_kv, span_la_softmax_paged,
                                                   span_la_softmax_pass)
+from hybrid_linear_attention_packed_gb300 import spanla
 from oracle import paged_oracle as po
 from paged_helpers import BF16, E4M3, U16, check_attention, f64, i32, make_pages, make_table, values
 
@@ -310,6 +311,62 @@ def test_a_table_of_no_pages(cuda_device, rows, cache):
     q, c, _, _ = _setup([5], [rows], 1, 1, 16, cache, cuda_device, seed=15)
     out, lse = _run(q, c, np.zeros((1, 0), np.int32), [0], [0, rows], cuda_device)
     assert not f64(out).any() and np.all(f64(lse) == -np.inf)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_sequences_that_share_pages(cuda_device, rows, cache):
+    """Three sequences behind the same 96 rows, and one that is another's whole table."""
+    q, c, table, cu = _setup([150, 300], [rows, rows], 2, 2, 32, cache, cuda_device, seed=16)
+    shared = np.full((4, 10), -7, np.int32)
+    shared[0, :5], shared[1, :10] = table[0, :5], table[1, :10]
+    shared[2, :3], shared[2, 3:8] = table[0, :3], table[1, 3:8]        # 96 rows of one, then the other's
+    shared[3, :10] = table[1, :10]
+    lens, cu = [150, 300, 256, 290], np.arange(5) * rows
+    q = torch.cat([q, q + 1])
+    out, lse = _run(q, c, shared, lens, cu, cuda_device)
+    check_attention(q, out, lse, c, shared, lens, cu, 0.125, weights(2, cache))
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("lens,rows,G,max_rows", [([3000, 200], [1, 2], 4, 2), ([900], [300], 2, 0), ([800, 500], [700, 1], 4, 0)])
+def test_the_workspace_is_enough_and_any(cuda_device, cache, lens, rows, G, max_rows):
+    """Calls without the extension module; with a workspace of just the bytes asked for, full of NaN, and what is behind it
+    left as it was; and with the library's own."""
+    dev = cuda_device
+    q, c, table, cu = _setup(lens, rows, G, 2, 32, cache, dev, seed=17)
+    ref, _ = _run(q, c, table, lens, cu, dev, max_rows=max_rows or None)
+    t, n, r = i32(table, dev), i32(lens, dev), i32(cu, dev)
+    cc, _ = spanla._kv_cache(c[0], c[1], t, n, r, c[2], c[3])
+    lib = spanla._lib
+    size = lib.span_la_softmax_paged_workspace(len(q), 2 * G, cc, max_rows)
+    ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device=dev)
+    for w in (ws.data_ptr(), None):
+        out = torch.full_like(q, float("nan"))
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        assert lib.span_la_softmax_paged(q.data_ptr(), q.stride(0), len(q), 2 * G, cc, max_rows, 0.0, out.data_ptr(), None, w, stream) == 0
+        span_la_check()
+        assert torch.equal(out, ref)
+    assert (ws[size:] == 0xFF).all()
+
+
+def test_the_same_without_the_extension_module(cuda_device, monkeypatch):
+    dev, lens, rows = cuda_device, [100, 40], [30, 1]
+    q, c, table, cu = _setup(lens, rows, 2, 2, 16, E4M3, dev, seed=18)
+    args = (c[0], c[1], i32(table, dev), i32(lens, dev), i32(cu, dev))
+    k, v = (torch.randn(31, 2, 64, device=dev) for _ in range(2))
+
+    def step():
+        span_la_kv_write(k, v, *args, c[2], c[3])
+        back = span_la_kv_read(*args, 31, c[2], c[3])
+        out = span_la_softmax_paged(q, *args, c[2], c[3])
+        span_la_check()
+        return (*back, out)
+
+    ref = step()
+    monkeypatch.setattr(spanla, "_fast", None)
+    k, v = k.clone(), v.clone()
+    assert all(torch.equal(a, b) for a, b in zip(step(), ref))
 
 
 def test_captured_behind_another_stream(cuda_device):
