@@ -616,13 +616,13 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const int row = g + 8 * r;
           bool wild = false;
           if (row < mh) {
-            const float f = out_factor<kE4m3>(m[r], M[r], l[r]);
+            const OutFactor f = out_factor<kE4m3>(m[r], M[r], l[r]);
             const int64_t at = (s_row0[cons.s] + static_cast<int64_t>(row / p.group)) * p.heads + cons.h * p.group + row % p.group;
             float y[16];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              y[j] = l[r] == 0.f ? 0.f : o[j][2 * r] * f;
-              y[8 + j] = l[r] == 0.f ? 0.f : o[j][2 * r + 1] * f;
+              y[j] = l[r] == 0.f ? 0.f : f(o[j][2 * r]);
+              y[8 + j] = l[r] == 0.f ? 0.f : f(o[j][2 * r + 1]);
               wild |= !(fabsf(y[j]) <= 3.4e38f) || !(fabsf(y[8 + j]) <= 3.4e38f);
             }
             wild &= l[r] == l[r];
@@ -780,8 +780,8 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (complete) {
             const int r = row[u] / p.group;
             const int64_t o_at = (s_row0[it.s] + static_cast<int64_t>(r)) * p.heads + it.h * p.group + row[u] - r * p.group;
-            const float of = out_factor<kE4m3>(jm[u], jM[u], jl[u]);
-            const float y[4] = {jo[u].x * of, jo[u].y * of, jo[u].z * of, jo[u].w * of};
+            const OutFactor of = out_factor<kE4m3>(jm[u], jM[u], jl[u]);
+            const float y[4] = {of(jo[u].x), of(jo[u].y), of(jo[u].z), of(jo[u].w)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) wild |= !(fabsf(y[c]) <= 3.4e38f);
             wild &= in && jl[u] == jl[u] && jl[u] != 0.f;

@@ -19,9 +19,15 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The weights of a row head are relative to 2^m, its O to 2^(M - 15) (bf16 pages: 2^m): o = O 2^(M - 15 - m) / l.
+// In two factors, 2^-15 / l and 2^(M - m), as their product need not be an fp32 number where V is small.
+struct OutFactor {
+  float a, b;
+  __device__ __forceinline__ float operator()(float o) const { return o * a * b; }
+};
 template <bool kE4m3>
-__device__ __forceinline__ float out_factor(float m, float M, float l) {
-  return l == 0.f ? 0.f : (kE4m3 ? ex2(M - m - 15.f) : 1.f) / l;
+__device__ __forceinline__ OutFactor out_factor(float m, float M, float l) {
+  if (l == 0.f) return {0.f, 0.f};
+  return {(kE4m3 ? 0x1p-15f : 1.f) / l, kE4m3 ? exp2f(M - m) : 1.f};
 }
 __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l)); }
 
@@ -118,9 +124,10 @@ __device__ __forceinline__ void join_step_parts(const KvArgs& a, const PagedAttn
   if (slice == 0 && row < mh) {
 #pragma unroll
     for (int i = 1; i < kJoinSlices; ++i) add(so[grp + i * kJoinRows][sub], 1.f);
-    const float m = total[row4][0], M = total[row4][1], l = total[row4][2], f = out_factor<kE4m3>(m, M, l);
+    const float m = total[row4][0], M = total[row4][1], l = total[row4][2];
+    const OutFactor f = out_factor<kE4m3>(m, M, l);
     const int64_t at = (j.row0 + static_cast<int64_t>(row / p.group)) * p.heads + j.h * p.group + row % p.group;
-    const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+    const float y[4] = {f(o.x), f(o.y), f(o.z), f(o.w)};
     bool w = false;
 #pragma unroll
     for (int c = 0; c < 4; ++c) w |= !(fabsf(y[c]) <= 3.4e38f);

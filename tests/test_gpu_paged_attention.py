@@ -79,6 +79,19 @@ def test_attention(cuda_device, case, cache):
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 2, 40])
+@pytest.mark.parametrize("size", [1e-34, 1e-32, 1e-30, 1e35])
+def test_small_and_large_values(cuda_device, size, rows, cache):
+    """Values near the ends of the exponent's range: within one CTA, over several, and in chunks."""
+    lens = [60, 9000]
+    q, c, table, cu = _setup(lens, [rows, rows], 4, 1, 64, cache, cuda_device, seed=21, v_size=size)
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    o = f64(out)
+    assert np.abs(o).max() < 20 * size and np.abs(o[cu[0]:cu[1]]).max() > size / 100
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(4, cache))
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
 @pytest.mark.parametrize("layout", ["interleaved", "rows"])
 @pytest.mark.parametrize("rows", [[1, 1], [3, 90]])
 def test_other_layouts_and_strided_queries(cuda_device, layout, cache, rows):
