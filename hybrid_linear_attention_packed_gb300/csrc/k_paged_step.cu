@@ -475,9 +475,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (r == 1 && !two) break;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        mul2(x[i][2 * r], x[i][2 * r + 1], qc[r], qc[r]);
-        if (kE4m3) {
-          const float4 sc = *reinterpret_cast<const float4*>(factors + i * 16 + t * 4);
+        if (!kE4m3) {
+          mul2(x[i][2 * r], x[i][2 * r + 1], qc[r], qc[r]);
+        } else {
+          float4 sc = *reinterpret_cast<const float4*>(factors + i * 16 + t * 4);
+          mul2(sc.x, sc.y, qc[r], qc[r]);   // (first, as a score may be an fp32 number that it is not without K's power)
           mul2(x[i][2 * r], x[i][2 * r + 1], sc.x, sc.y);
           z[i][2 * r] = x[i][2 * r], z[i][2 * r + 1] = x[i][2 * r + 1];
           add2(z[i][2 * r], z[i][2 * r + 1], sc.z, sc.w);

@@ -19,14 +19,14 @@ def weights(G, cache):
     return lambda n: U16 if n * G > 16 else 2.0 ** -16 if cache == BF16 else 2.0 ** -11
 
 
-def _setup(lens, rows, G, H, R, cache, dev, seed=0, layout="plain", v_size=1.0, q_size=1.0, width=None):
+def _setup(lens, rows, G, H, R, cache, dev, seed=0, layout="plain", v_size=1.0, q_size=1.0, width=None, k_size=1.0):
     """A cache whose rows of sequences hold numbers and all others NaN, and the queries."""
     g = torch.Generator(device=dev).manual_seed(seed)
     table, P = make_table(lens, R, 2, seed, width)
     c = make_pages(P, H, R, cache, dev, layout, fill=0xFF)
     cu = np.concatenate([[0], np.cumsum(lens)])
     T = int(cu[-1])
-    k = torch.randn(T, H, 64, generator=g, device=dev)
+    k = torch.randn(T, H, 64, generator=g, device=dev) * k_size
     v = torch.randn(T, H, 64, generator=g, device=dev) * v_size
     v = v * torch.exp2(torch.randint(-4, 5, (T, H, 1), generator=g, device=dev).float())    # rows of different sizes
     if T:
@@ -76,6 +76,16 @@ def test_attention(cuda_device, case, cache):
     q, c, table, cu = _setup(lens, rows, G, H, R, cache, cuda_device, seed=case)
     out, lse = _run(q, c, table, lens, cu, cuda_device)
     check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(G, cache))
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 4, 70])
+@pytest.mark.parametrize("q_size,k_size", [(1e37, 1e-34), (1e35, 1e-35), (1e-35, 1e35)])
+def test_queries_and_keys_of_far_sizes(cuda_device, q_size, k_size, rows, cache):
+    lens = [400, 70]
+    q, c, table, cu = _setup(lens, [rows, rows], 2, 2, 64, cache, cuda_device, seed=22, q_size=q_size, k_size=k_size)
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(2, cache))
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3])
