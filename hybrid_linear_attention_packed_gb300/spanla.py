@@ -874,8 +874,8 @@ def span_la_softmax_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
         _on_device(dev, "lse", lse)
     if max_rows is None:
         max_rows = 1 if row_cu is None else 0
-    elif max_rows < 1:
-        raise ValueError("max_rows must be at least 1")
+    elif not 1 <= max_rows < 1 << 31:
+        raise ValueError("max_rows must be at least 1, and below 2^31")
     # The workspace from torch's allocator on the current stream (on another one: the library's own).
     bytes_ = lib.span_la_softmax_paged_workspace(T, H, c, int(max_rows)) if stream is None else 0
     ws = torch.empty(bytes_, dtype=torch.uint8, device=q.device) if bytes_ else None

@@ -373,6 +373,58 @@ def test_the_workspace_is_enough_and_any(cuda_device, cache, lens, rows, G, max_
     assert (ws[size:] == 0xFF).all()
 
 
+REFUSED = [
+    ("attend", dict(page_table=lambda t: t.long()), "page_table"),
+    ("attend", dict(page_table=lambda t: t.t()), "page_table|seq_len"),
+    ("attend", dict(page_table=lambda t: t.cpu()), "page_table"),
+    ("attend", dict(seq_len=lambda t: t[:1]), "seq_len"),
+    ("attend", dict(row_cu=lambda t: t[:2]), "row_cu"),
+    ("attend", dict(row_cu=lambda t: t.float()), "row_cu"),
+    ("attend", dict(v_pages=lambda t: t[1:]), "share shape"),
+    ("attend", dict(v_pages=lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)), "strides"),
+    ("attend", dict(k_pages=lambda t: t.float()), "share shape|dtype"),
+    ("attend", dict(k_scale=lambda t: None), "k_scale"),
+    ("attend", dict(v_scale=lambda t: t.float()), "v_scale"),
+    ("attend", dict(q=lambda t: t.float()), "bf16"),
+    ("attend", dict(q=lambda t: t[:, :3], out=lambda t: None, lse=lambda t: None), "multiple"),
+    ("attend", dict(q=lambda t: t.cpu()), "q must"),
+    ("attend", dict(out=lambda t: t[:1]), "out"),
+    ("attend", dict(lse=lambda t: t.double()), "lse"),
+    ("attend", dict(max_rows=lambda t: 0), "max_rows"),
+    ("attend", dict(max_rows=lambda t: 1 << 32), "max_rows"),
+    ("attend", dict(scale=lambda t: -1.0), "scale"),
+    ("attend", dict(scale=lambda t: float("nan")), "scale"),
+    ("write", dict(k=lambda t: t.half()), "dtype"),
+    ("write", dict(v=lambda t: t.float()), "share"),
+    ("write", dict(k=lambda t: t[:, :1], v=lambda t: t[:, :1]), r"\[T, 2, 64\]"),
+    ("write", dict(row_cu=lambda t: None), "as many sequences"),
+    ("read", dict(total_rows=lambda t: None), "total_rows"),
+    ("read", dict(dtype=lambda t: torch.float16), "dtype"),
+    ("read", dict(k_out=lambda t: t[:3]), "k_out"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(REFUSED)))
+def test_the_binding_names_what_is_wrong(cuda_device, case):
+    op, change, what = REFUSED[case]
+    lens, rows = [40, 20], [3, 2]
+    q, c, table, cu = _setup(lens, rows, 2, 2, 16, E4M3, cuda_device, seed=19)
+    cache = dict(k_pages=c[0], v_pages=c[1], page_table=i32(table, cuda_device), seq_len=i32(lens, cuda_device), row_cu=i32(cu, cuda_device),
+                 k_scale=c[2], v_scale=c[3])
+    k = torch.zeros(5, 2, 64, dtype=BF16, device=cuda_device)
+    own = dict(attend=dict(q=q, max_rows=None, scale=0.0, out=torch.empty_like(q), lse=torch.empty(5, 4, device=cuda_device)),
+               write=dict(k=k, v=k.clone()), read=dict(total_rows=5, dtype=BF16, k_out=None))[op]
+    if "k_out" in change:
+        own["k_out"] = k
+    args = {**own, **cache}
+    for name, f in change.items():
+        args[name] = f(args[name])
+    call = dict(attend=span_la_softmax_paged, write=span_la_kv_write, read=span_la_kv_read)[op]
+    with pytest.raises((ValueError, SpanLAError), match=what):
+        call(**args)
+    span_la_check()
+
+
 def test_the_same_without_the_extension_module(cuda_device, monkeypatch):
     dev, lens, rows = cuda_device, [100, 40], [30, 1]
     q, c, table, cu = _setup(lens, rows, 2, 2, 16, E4M3, dev, seed=18)
