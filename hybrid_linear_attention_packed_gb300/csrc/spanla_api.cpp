@@ -2203,9 +2203,11 @@ PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t ma
   g.unit = paged_step_unit(e4m3);
   const int64_t units = std::max<int64_t>(1, (capacity + g.unit - 1) / g.unit);   // of a sequence and head, at most
   g.step = group <= kStepHeads ? paged_step_grid(units * heads * std::min<int64_t>(seqs, kStepSeqs), num_sms) : 0;
-  // Tables of a few units (256 rows of bf16 pages, 512 of e4m3): a CTA's eight warps are enough for a sequence and head, and
-  // there is nothing to join.
-  g.whole = units <= 8;
+  // Tables of a few units (512 rows of bf16 pages, 1,024 of e4m3): a CTA's eight warps are enough for a sequence and head, and
+  // there is nothing to join, nor a second launch.  (One token over 500 rows of bf16, 16 heads: 6.9 us, with joins 7.6; 61
+  // tokens 19.8 and 21.0; over 1,000 rows 9.4 and 8.0, 61 tokens 34.9 and 35.0; two key heads of 8, 2,000 rows of e4m3 12.6
+  // and 9.9.)
+  g.whole = units <= 16;
   g.chunk = max_rows * group > kStepHeads ? std::min(num_sms, kStepMaxGrid) : 0;
   g.step_ws = align256(static_cast<size_t>(g.step > 1 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
   g.chunk_ws = align256(static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
