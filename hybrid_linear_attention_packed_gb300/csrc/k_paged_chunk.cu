@@ -166,7 +166,7 @@ struct Run {
 template <bool kE4m3>
 __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, float* ws) {
+                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, float* ws) {
   using C = Cfg<kE4m3>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -255,7 +255,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   // The run from unit `off` of the item on: its blocks are the units behind the first kItemBlocks.
   auto take = [&](Run& r, int64_t off) {
     r.blocks = blocks_of(s_len[r.s], s_n[r.s], r.b, item_rows);
-    r.units = min(static_cast<int64_t>(r.blocks) + kItemBlocks - off, left);
+    r.units = static_cast<int64_t>(r.blocks) + kItemBlocks - off;
+    if (!whole_items) r.units = min(r.units, left);
     r.j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), off - kItemBlocks));
     r.j1 = static_cast<int32_t>(max(static_cast<int64_t>(r.j0), off + r.units - kItemBlocks));
     if (r.j1 == r.j0) left = 0;   // (the CTA's units end before the item's blocks begin)
@@ -303,6 +304,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   };
   // Rows of tile x of a run's item.
   auto rows_of = [&](const Run& r, int x) { return max(0, min(tile_rows, s_n[r.s] - r.b * item_rows - x * tile_rows)); };
+
+  // Whole items: a CTA takes those that begin in its units.
+  if (whole_items && left > 0 && first.units < first.blocks + kItemBlocks) next_run(first, left);
 
   Run r = first;
   if (warp < 4) {
@@ -412,7 +416,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           join.row0 = s_row0[r.s];
         }
       }
-      if (lane == 0 && gridDim.x > 1) {
+      if (lane == 0 && gridDim.x > 1 && !whole_items) {
         if (!ok) join.parts = 0;
         *reinterpret_cast<ChunkJoin*>(ws + blockIdx.x * kChunkWsFloats + 4 * kPartFloats) = join;
       }
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const __g
 
 template <bool kE4m3>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0,
-                   int ns, int grid, float* ws, cudaStream_t stream) {
+                   int ns, int grid, bool whole_items, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3>;
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> regs{0};
@@ -815,15 +819,16 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
   const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  return launch_behind(paged_chunk_kernel<kE4m3>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
+  return launch_behind(paged_chunk_kernel<kE4m3>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns,
+                       whole_items, ws);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
-                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream) {
-  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream)
-              : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream) {
+  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream)
+              : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream);
 }
 
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, const KvArgs& step, int step_grid,

@@ -2186,7 +2186,7 @@ span_la_status encode_tile(CUtensorMap* map, const KvArgs& a, const PagedAttn& p
 // tell them apart by the row offsets, which are in device memory).
 struct PagedGrids {
   int unit, step, chunk;      // CTAs of each kernel; 0: not launched
-  bool whole;                 // step kernel: no item goes over several CTAs
+  bool whole, chunk_whole;    // step kernel, chunk kernel: no item goes over several CTAs
   bool expand;                // chunk kernel: over bf16 copies of the e4m3 pages
   size_t step_ws, chunk_ws, copies, bytes;   // workspace: of each kernel, of K's (and of V's) copies, of all
 };
@@ -2197,8 +2197,9 @@ struct PagedGrids {
 // 1,024 47.4 and 46.3.)
 constexpr int64_t kExpandRowHeads = 2048;
 constexpr size_t kExpandBytes = size_t(128) << 20;
+constexpr int64_t kWholeBlocks = 4, kWholeItems = 128;
 
-PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int group, bool e4m3, int num_sms) {
+PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int group, bool e4m3, int num_sms) {
   PagedGrids g{};
   g.unit = paged_step_unit(e4m3);
   const int64_t units = std::max<int64_t>(1, (capacity + g.unit - 1) / g.unit);   // of a sequence and head, at most
@@ -2209,8 +2210,13 @@ PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t ma
   // and 9.9.)
   g.whole = units <= 16;
   g.chunk = max_rows * group > kStepHeads ? std::min(num_sms, kStepMaxGrid) : 0;
+  // The same for chunks over tables of up to 512 rows, where there are no more items than CTAs (on a smaller GPU too: the
+  // workspace is asked for without one).  (4 key heads of 2, bf16, eight sequences with 60 new rows of 100: 9.5 us, cut
+  // and joined 13.1; of 500: 12.6 and 14.9; one with 200 of 500: 15.4 and 14.9, from the host 15.7 and 15.8.)
+  const int64_t item_rows = 2 * (kTileRows / group);
+  g.chunk_whole = capacity <= kWholeBlocks * kTileRows && heads * (rows / item_rows + std::min<int64_t>(seqs, rows)) <= kWholeItems;
   g.step_ws = align256(static_cast<size_t>(g.step > 1 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
-  g.chunk_ws = align256(static_cast<size_t>(g.chunk > 1 ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
+  g.chunk_ws = align256(static_cast<size_t>(g.chunk > 1 && !g.chunk_whole ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
   const double copy = static_cast<double>(seqs) * capacity * heads * kHeadDim * 2;
   g.expand = e4m3 && capacity > 0 && g.chunk > 0 && max_rows * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
   g.copies = g.expand ? align256(static_cast<size_t>(seqs * capacity * heads * kHeadDim * 2)) : 0;
@@ -2221,7 +2227,7 @@ PagedGrids paged_grids(int64_t capacity, int64_t heads, int64_t seqs, int64_t ma
 span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num_sms, void* workspace, cudaStream_t stream) {
   span_la_status st = SPAN_LA_OK;
   CUtensorMap tm_q, tm_k, tm_v;
-  const PagedGrids grids = paged_grids(a.capacity, a.heads, a.seqs, a.max_rows, p.group, e4m3, num_sms);
+  const PagedGrids grids = paged_grids(a.rows, a.capacity, a.heads, a.seqs, a.max_rows, p.group, e4m3, num_sms);
   const int unit = grids.unit, step_grid = grids.step, chunk_grid = grids.chunk;
   const bool step = step_grid > 0, chunk = chunk_grid > 0;
   const size_t bytes = grids.bytes;
@@ -2257,7 +2263,7 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     st = encode_pages(&tm_k, a.k, a, e4m3, unit);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, unit);
   }
-  const bool step_join = step_grid > 1 && !grids.whole, chunk_join = chunk_grid > 1;
+  const bool step_join = step_grid > 1 && !grids.whole, chunk_join = chunk_grid > 1 && !grids.chunk_whole;
   auto run_step = [&](int s0, int ns, bool behind) {
     return counted_launch(kKernelPagedStep, stream, [&] {
       return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, grids.whole, behind, ws, stream);
@@ -2266,7 +2272,7 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
   auto run_step_join = [&] { return counted_launch(kKernelPagedJoin, stream, [&] { return launch_paged_join(a, p, step_grid, e4m3, ws, stream); }); };
   auto run_chunk = [&](int s0, int ns) {
     return counted_launch(kKernelPagedChunk, stream, [&] {
-      return launch_paged_chunk(tm_q, tm_ck, tm_cv, c, p, s0, ns, chunk_grid, chunk_e4m3, cws, stream);
+      return launch_paged_chunk(tm_q, tm_ck, tm_cv, c, p, s0, ns, chunk_grid, chunk_e4m3, grids.chunk_whole, cws, stream);
     });
   };
   auto run_chunk_join = [&](bool with_step) {
@@ -3085,10 +3091,10 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
 }
 
 int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const span_la_kv_cache* cache, int32_t max_rows) {
-  if (cache == nullptr || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 || rows < 1 ||
-      cache->num_seqs < 1 || max_rows < 0)
+  if (cache == nullptr || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 || num_q_heads / cache->num_heads > 128 ||
+      rows < 1 || cache->num_seqs < 1 || max_rows < 0)
     return 0;
-  return static_cast<int64_t>(paged_grids(static_cast<int64_t>(cache->table_width) * cache->page_rows, cache->num_heads, cache->num_seqs,
+  return static_cast<int64_t>(paged_grids(rows, static_cast<int64_t>(cache->table_width) * cache->page_rows, cache->num_heads, cache->num_seqs,
                                           most_rows(cache, rows, max_rows), num_q_heads / cache->num_heads,
                                           cache->dtype == SPAN_LA_E4M3, kStepMaxGrid).bytes);
 }

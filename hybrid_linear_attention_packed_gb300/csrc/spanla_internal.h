@@ -467,7 +467,8 @@ cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
                               int grid, bool e4m3, bool whole_items, bool behind, float* ws, cudaStream_t stream);
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream);
 
-// Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles).
+// Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles);
+// whole_items: no item over several CTAs, no workspace and no join.
 constexpr int kChunkPartFloats = kTileRows * kHeadDim + 2 * kTileRows;
 constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8;
 struct alignas(16) ChunkJoin {
@@ -476,7 +477,7 @@ struct alignas(16) ChunkJoin {
   int32_t pad;
 };
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
-                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, float* ws, cudaStream_t stream);
+                               const PagedAttn& p, int s0, int ns, int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream);
 // step, step_grid (0: none), ...: joins the step kernel's parts of the same call too.
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, const KvArgs& step, int step_grid,
                               bool step_e4m3, const float* step_ws, cudaStream_t stream);

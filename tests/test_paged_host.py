@@ -135,12 +135,12 @@ def test_read_refuses(lib, kw, status, what):
     (dict(lse=LSE + 2), INVALID, "lse_out"),
     (dict(lse=LEN), INVALID, "lse_out overlaps seq_len"),
     (dict(ws=FAKE * 4096 + 8), INVALID, "workspace must be"),
-    (dict(ws=OUT, max_rows=100), INVALID, "workspace overlaps"),
+    (dict(ws=OUT, max_rows=100, cache=dict(table_width=40, table_stride=40)), INVALID, "workspace overlaps"),
 ])
 def test_attention_refuses(lib, kw, status, what):
-    a = dict(q=Q, stride=256, heads=4, max_rows=0, scale=0.0, out=OUT, lse=LSE, ws=None)
+    a = dict(q=Q, stride=256, heads=4, max_rows=0, scale=0.0, out=OUT, lse=LSE, ws=None, cache={})
     a.update(kw)
-    st = lib.span_la_softmax_paged(a["q"], a["stride"], 3, a["heads"], _cache(), a["max_rows"], a["scale"], a["out"], a["lse"], a["ws"],
+    st = lib.span_la_softmax_paged(a["q"], a["stride"], 3, a["heads"], _cache(**a["cache"]), a["max_rows"], a["scale"], a["out"], a["lse"], a["ws"],
                                    None)
     assert st == status and what in _detail(lib)
 
@@ -160,6 +160,7 @@ def test_workspace(lib):
     big = _cache(table_width=4000, table_stride=4000)
     assert f(3, 4, big, 1) > 0 and f(3, 4, big, 100) > f(3, 4, big, 8)
     assert f(3, 4, big, 0) == f(3, 4, big, 3) and f(3, 4, _cache(), 1) == 0      # (one CTA needs none)
+    assert f(3, 4, _cache(), 100) == 0 and f(3, 258, _cache(), 100) == 0          # (whole items; refused)
     assert f(0, 4, _cache(), 1) == 0 and f(3, 5, _cache(), 1) == 0 and f(3, 4, None, 1) == 0 and f(3, 4, _cache(num_seqs=0), 1) == 0
 
 
