@@ -22,7 +22,7 @@
 // workspace for the join kernel, which starts behind this one.
 //
 // Measured: 2,048 rows behind 18,000 of 4 key heads of 4, bf16 pages, 167 us, 0.50
-// of cuBLAS's rate; 512 rows behind 7,400 of 16 heads 35 us with the launches beside
+// of cuBLAS's rate; 512 rows behind 7,400 of 16 heads 33 us with the launches beside
 // it.  A block of two tiles takes 2,450 cycles, of which the products are 1,790: the
 // rest is softmax (without exponentials and maxima 131 us) and hand-offs between
 // the warps, of which each waits for the one before (without products 161 us).
