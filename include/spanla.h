@@ -681,8 +681,8 @@ span_la_status span_la_softmax_paged(const void *q, int64_t q_row_stride, int64_
                                      const span_la_kv_cache *cache, int32_t max_rows, float scale,
                                      void *out, float *lse_out, void *workspace, cudaStream_t stream);
 
-/* Bytes of workspace of a span_la_softmax_paged call with these arguments, on any GPU (host only; 0 on arguments that
- * the call refuses). */
+/* Bytes of workspace of a span_la_softmax_paged call with these arguments, on any GPU (host only; 0 where it needs none,
+ * or refuses the arguments). */
 int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const span_la_kv_cache *cache, int32_t max_rows);
 
 /*
