@@ -558,10 +558,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
             tmem_st_16cols(ts + kColO + 16 * h, o);
           }
-          l = m_ref * c2 == -INFINITY ? 0.f : l * f;
+          l *= f;
           m_ref = m_new;
         }
-        const float neg = -(m_ref == -INFINITY ? 0.f : m_ref) * c2;
+        // (a reference that the scale takes to -infinity is none: its scores' weights are then 0, a NaN's NaN)
+        const float neg = m_ref * c2 == -INFINITY ? 0.f : -m_ref * c2;
         const uint64_t cc = f32x2(c2, c2), nn = f32x2(neg, neg);
         uint64_t acc[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         uint32_t pk[2][32];
@@ -598,7 +599,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
       tc_fence_after_sync();
       const float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c2;
-      if (fabsf(m2) == INFINITY) l = m2 > 0.f ? NAN : 0.f;   // (the scale took the greatest score out of fp32: what the score gives)
+      if (m2 == INFINITY) l = NAN;   // (the greatest score is infinite, or the scale took it there)
       const bool complete = r.j0 == 0 && r.j1 == r.blocks;
       const int64_t at = (s_row0[r.s] + static_cast<int64_t>(in_seq)) * p.heads + r.h * p.group + my_head;
       float* part = ws + blockIdx.x * kChunkWsFloats + (2 * (r.j0 > 0 ? 0 : 1) + x) * kPartFloats;
