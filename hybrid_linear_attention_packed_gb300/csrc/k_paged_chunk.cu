@@ -636,6 +636,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       // Rows whose O came out infinite or NaN though the sum of weights is finite: once more from the cache, without
       // the rows that they do not see.
       uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
+      if (which != 0) __syncwarp();   // (a row's first result is one thread's store, its second all lanes'; a vote orders no memory)
       while (which != 0) {
         const int i = __ffs(which) - 1;
         which &= which - 1;
