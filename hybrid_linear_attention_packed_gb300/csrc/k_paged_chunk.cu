@@ -635,14 +635,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
       // Rows whose O came out infinite or NaN though the sum of weights is finite: once more from the cache, without
       // the rows that they do not see.
-      uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
-      if (which != 0) __syncwarp();   // (a row's first result is one thread's store, its second all lanes'; a vote orders no memory)
-      while (which != 0) {
-        const int i = __ffs(which) - 1;
-        which &= which - 1;
-        const int rr = quarter * 32 + i, in = r.b * item_rows + x * tile_rows + rr / p.group;
-        attend_row<kE4m3>(a, p, s0 + r.s, s_row0[r.s] + static_cast<int64_t>(in), r.h * p.group + rr % p.group, max(0, len - n + in + 1));
-      }
+      const uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
+      if (which != 0)
+        redo_rows<kE4m3>(a, p, which, s0 + r.s, r.h, s_row0[r.s] + static_cast<int64_t>(in_seq - my_row), quarter * 32,
+                            len - n + in_seq - my_row + 1);
     }
   } else {
     // -------------------------------------------------------------- e4m3 rows into bf16 tiles
@@ -722,9 +718,9 @@ constexpr int kChunkJoinThreads = 256, kJoinWarps = kChunkJoinThreads / 32;
 
 // CTAs (c, 8 ..), where there are any: the step kernel's parts (of `step_grid` CTAs), which it has of the same call.
 template <bool kE4m3, bool kStepE4m3>
-__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p,
-                                                                       const float* ws, const __grid_constant__ KvArgs step, const float* step_ws,
-                                                                       int step_grid) {
+__global__ void __launch_bounds__(kChunkJoinThreads, 4)
+chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, const float* ws, const __grid_constant__ KvArgs step,
+                  const float* step_ws, int step_grid) {
   __shared__ float factor[kStepMaxGrid][32];
   __shared__ float best[kJoinWarps][32], sums[kJoinWarps][32];
   __shared__ uint32_t wild;
@@ -796,14 +792,10 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const __g
     if (w && l == l && l != 0.f) atomicOr(&wild, 1u << lane);
   }
   __syncthreads();
-  uint32_t which = wild;
-  for (int k = 0; which != 0; ++k) {   // the row heads that are done over, a warp each
-    const int i = __ffs(which) - 1;
-    which &= which - 1;
-    if (k % kJoinWarps != warp) continue;
-    const int rr = (blockIdx.y & 3) * 32 + i, at = j.first + x * tile_rows + rr / p.group;
-    attend_row<kE4m3>(a, p, j.s, j.row0 + static_cast<int64_t>(at), j.h * p.group + rr % p.group, max(0, j.len - j.n + at + 1));
-  }
+  const uint32_t which = wild & (0xfu << (4 * warp));   // the row heads that are done over, four a warp
+  const int32_t first = j.first + x * tile_rows;
+  if (which != 0)
+    redo_rows<kE4m3>(a, p, which, j.s, j.h, j.row0 + static_cast<int64_t>(first), (blockIdx.y & 3) * 32, j.len - j.n + first + 1);
 }
 
 template <bool kE4m3>

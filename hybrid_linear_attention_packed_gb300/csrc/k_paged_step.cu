@@ -639,10 +639,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           for (int i = 0; b != 0 && i < 8; ++i)
             if ((b >> (4 * i)) & 15u) which |= 1u << (i + 8 * r);
         }
-        if (which != 0) {
-          __syncwarp();
-          redo_rows<kE4m3>(a, p, which, s0 + cons.s, s_row0[cons.s], n, len, cons.h);
-        }
+        if (which != 0) redo_rows<kE4m3>(a, p, which, s0 + cons.s, cons.h, s_row0[cons.s], 0, len - n + 1);
       } else {
         // (what began before the CTA is warp 0's to tell of: open[kW] where it ends in warp 0, as another may begin there)
         if (lane == 0 && (item_done ? warp == 0 : warp == 0 || !started_before))
@@ -811,10 +808,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll 1
         for (; i < end; i += 2) join_pairs(std::integral_constant<int, 2>(), i);
       }
-      if (which != 0) {
-        __syncwarp();
-        redo_rows<kE4m3>(a, p, which, s0 + it.s, s_row0[it.s], n, s_len[it.s], it.h);
-      }
+      if (which != 0) redo_rows<kE4m3>(a, p, which, s0 + it.s, it.h, s_row0[it.s], 0, s_len[it.s] - n + 1);
     }
   }
   // (warp 0's lanes have the records: the one that has the item writes, or lane 0)
@@ -826,8 +820,8 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 template <bool kE4m3, int kJoinSlices>
-__global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16) paged_join_kernel(const __grid_constant__ KvArgs a,
-                                                                                  const __grid_constant__ PagedAttn p, const float* ws) {
+__global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16, 1024 / (kJoinRows * kJoinSlices * 16))
+paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, const float* ws) {
   griddep_launch_dependents();
   griddep_wait();
   join_step_parts<kE4m3, kJoinSlices>(a, p, ws, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.y));

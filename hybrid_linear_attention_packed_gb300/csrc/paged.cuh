@@ -104,75 +104,202 @@ __device__ __forceinline__ void half2_of_e4m3(uint32_t four, uint32_t& lo, uint3
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(four));
 }
-// Row elements 2 * lane, 2 * lane + 1 of row `pos` of the cache, given its page.
+
+// Eight elements of a cached row, as they lie and as fp32.
 template <bool kE4m3>
-__device__ __forceinline__ float2 cached_pair(const KvArgs& a, const void* base, const uint8_t* scale, int32_t page, int32_t pos,
-                                              int head, int lane) {
-  const int32_t r = pos & (a.page_rows - 1);
-  const int64_t at = page * a.page_stride + head * a.head_stride + r * a.row_stride + 2 * lane;
-  if (kE4m3) {
-    const float2 x = from_e4m3x2(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(base) + at));
-    const float e = scale_of(scale[page * a.scale_page_stride + head * a.scale_head_stride + r]);
-    return make_float2(x.x * e, x.y * e);
+struct EightOf;
+template <>
+struct EightOf<false> {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
   }
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(static_cast<const __nv_bfloat16*>(base) + at));
+  __device__ __forceinline__ void get(float, float (&x)[8]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[2 * c] = __uint_as_float(v[c] << 16), x[2 * c + 1] = __uint_as_float(v[c] & 0xffff0000u);
+  }
+  __device__ __forceinline__ bool finite() const {   // (0x0080 carried into a half's sign bit: its exponent was all ones)
+    auto carry = [](uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; };
+    return ((carry(w.x) | carry(w.y) | carry(w.z) | carry(w.w)) & 0x80008000u) == 0;
+  }
+};
+template <>
+struct EightOf<true> {
+  uint2 w;
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + at);
+  }
+  __device__ __forceinline__ void get(float scale, float (&x)[8]) const {
+    const uint32_t v[2] = {w.x, w.y};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 y = from_e4m3x2((v[c >> 1] >> (16 * (c & 1))) & 0xffffu);
+      x[2 * c] = y.x * scale, x[2 * c + 1] = y.y * scale;
+    }
+  }
+  __device__ __forceinline__ bool finite() const {   // (0x7f is NaN)
+    return ((((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) == 0;
+  }
+};
+
+__device__ __forceinline__ bool bf16_finite(uint32_t bits) { return (bits & 0x7f80u) != 0x7f80u; }
+
+// q . k of a row head, whose eight lanes have eight elements each.
+template <bool kE4m3>
+__device__ __forceinline__ float dot64(const EightOf<false>& q, const EightOf<kE4m3>& k, float k_scale) {
+  float x[8], y[8], sum = 0.f;
+  q.get(1.f, x);
+  k.get(k_scale, y);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) sum = fmaf(x[c], y[c], sum);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
 }
 
-// Softmax attention of one packed row t and query head by one warp, in fp32
-// throughout: the row of sequence s that sees its first `seen` rows.  The other
-// kernels send a row here whose products came out infinite or NaN though its sum of
-// weights is finite: they multiply rows that the row does not see by 0, this does
-// not touch them.  (0.38 us a cached row, four of them at a time, latency: a token over
-// 7,401 rows whose V is infinite somewhere 2.8 ms instead of 12 us.)
+// Elements of o that came out infinite or NaN, once more, by one warp.  The kernels multiply rows that a row does not see
+// by weights of 0, and 0 times an infinity or a NaN is NaN; weights that are no fp32 number any more, or sums past one, end
+// there too.  This touches only what a row sees.  `which` names row heads base + i (i a bit) of the rows from packed row
+// row0 on, of which row r sees the first seen0 + r rows of sequence s; their o has been stored, by any lanes of the warp (or
+// before a barrier), and only what is not finite in it is stored again.  Four row heads at a time, eight lanes each, eight
+// elements a lane.
+//
+// First, what is not finite in the rows of V that they see, and has a score above -infinity: the sum of that is the answer,
+// however small its weight.  (Looked for 16 rows at a time; most calls end here.)  Where there is none, the rest:
+//
+//   l' = l e^(m - m') + sum w,   o' = o l e^(m - m') / l' + sum w / l' v,   w = e^(x - m')
+//
+// in fp32: a mean at every step, which passes fp32 no more than V does.
 template <bool kE4m3>
-__device__ __noinline__ void attend_row(const KvArgs& a, const PagedAttn& p, int s, int64_t t, int head, int32_t seen) {
-  constexpr int kAtOnce = 4;
-  const int lane = threadIdx.x & 31, kvh = head / p.group;
-  const float2 q = __bfloat1622float2(
-      *reinterpret_cast<const __nv_bfloat162*>(p.q + t * p.q_row_stride + head * kHeadDim + 2 * lane));
-  float m = -INFINITY, l = 0.f;
-  float2 o = make_float2(0.f, 0.f);
-  bool bad = false;
-  for (int32_t j0 = 0; j0 < seen; j0 += kAtOnce) {   // (a page holds a multiple of kAtOnce rows)
-    const int32_t page = page_of(a, s, j0);
-    if (page < 0) {
-      bad = true;
-      continue;
+__device__ __noinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, uint32_t which, int s, int kvh, int64_t row0, int base,
+                                       int32_t seen0) {
+  constexpr int kAtOnce = 4, kScan = 16;   // (a page holds a multiple of both)
+  const int lane = threadIdx.x & 31, part = lane & 7;
+  auto scale_at = [&](const uint8_t* scales, int32_t page, int32_t in) {
+    return kE4m3 ? scale_of(scales[page * a.scale_page_stride + kvh * a.scale_head_stride + in]) : 1.f;
+  };
+  while (which != 0) {
+    int mine = -1;   // lanes 8 g .. 8 g + 7 have the g-th of them
+    for (int g = 0; g < 4 && which != 0; ++g) {
+      if (g == lane >> 3) mine = __ffs(which) - 1;
+      which &= which - 1;
     }
-    const int n = min(kAtOnce, seen - j0);
-    float2 v[kAtOnce];
-    float x[kAtOnce];
+    const int rr = base + max(mine, 0), r = rr / p.group, head = kvh * p.group + rr % p.group;
+    const int32_t seen = mine < 0 ? 0 : max(0, seen0 + r);
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((row0 + r) * p.heads + head) * kHeadDim + 8 * part);
+    uint32_t wanted = 0;   // elements to be found
+    __syncwarp();          // (what lanes of this warp have stored)
+    if (mine >= 0) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      v[i] = make_float2(0.f, 0.f), x[i] = 0.f;
-      if (i >= n) continue;
-      const float2 k = cached_pair<kE4m3>(a, a.k, a.k_scale, page, j0 + i, kvh, lane);
-      v[i] = cached_pair<kE4m3>(a, a.v, a.v_scale, page, j0 + i, kvh, lane);
-      x[i] = q.x * k.x + q.y * k.y;
+      for (int c = 0; c < 4; ++c)
+        wanted |= (bf16_finite(out[c]) ? 0u : 1u << (2 * c)) | (bf16_finite(out[c] >> 16) ? 0u : 2u << (2 * c));
     }
+    int32_t most = seen;   // rows to look at
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
+    for (int d = 8; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+    EightOf<false> q;
+    q.load(p.q, (row0 + r) * p.q_row_stride + head * kHeadDim + 8 * part);
+    float o[8];
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+    for (int c = 0; c < 8; ++c) o[c] = 0.f;
+    // ------------------------------------------------------------ what is not finite
+    uint32_t met = 0;
+    int32_t page = -1;
+    for (int32_t j0 = 0; j0 < most; j0 += kScan) {
+      if ((j0 & (a.page_rows - 1)) == 0) {
+        page = page_of(a, s, j0);
+        if (page < 0) atomicOr(a.err, kErrPage);
+        bool open = false;   // some element is not NaN yet
+#pragma unroll
+        for (int c = 0; c < 8; ++c) open |= ((wanted >> c) & 1u) && o[c] == o[c];
+        if (!__any_sync(0xffffffffu, open)) break;
+      }
+      if (page < 0) continue;
+      const int64_t at = page * a.page_stride + kvh * a.head_stride + 8 * part;
+      const int32_t in0 = (j0 & (a.page_rows - 1)) + (lane >> 3);
+      EightOf<kE4m3> v[kScan / 4];
+#pragma unroll
+      for (int i = 0; i < kScan / 4; ++i) v[i].load(a.v, at + (in0 + 4 * i) * a.row_stride);
+      uint32_t rows = 0;   // of 16
+#pragma unroll
+      for (int i = 0; i < kScan / 4; ++i) {
+        const bool here = j0 + (lane >> 3) + 4 * i < most;
+        const uint32_t b = __ballot_sync(0xffffffffu, here && (!v[i].finite() || (kE4m3 && !(scale_at(a.v_scale, page, in0 + 4 * i) < INFINITY))));
+#pragma unroll
+        for (int g = 0; g < 4; ++g) rows |= (b >> (8 * g)) & 0xffu ? 1u << (4 * i + g) : 0u;
+      }
+      for (; rows != 0; rows &= rows - 1) {
+        const int32_t j = j0 + __ffs(rows) - 1, in = j & (a.page_rows - 1);
+        EightOf<kE4m3> kk, vv;
+        kk.load(a.k, at + in * a.row_stride);
+        vv.load(a.v, at + in * a.row_stride);
+        const float x = dot64<kE4m3>(q, kk, scale_at(a.k_scale, page, in)) * p.scale;
+        if (j >= seen || x == -INFINITY) continue;
+        float y[8];
+        vv.get(scale_at(a.v_scale, page, in), y);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (!(fabsf(y[c]) < INFINITY)) o[c] += y[c], met |= 1u << c;
+      }
     }
+    __syncwarp();
+    auto store = [&](uint32_t which_ones) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (i >= n) break;
-      const float y = x[i] * p.scale;
-      if (y == -INFINITY) continue;   // weight 0
-      const float m_new = y > m || y != y ? y : m;
-      const float old = m == m_new ? 1.f : m == -INFINITY ? 0.f : expf(m - m_new), w = expf(y - m_new);
-      l = l * old + w;
-      o.x = (old == 0.f ? 0.f : o.x * old) + w * v[i].x;
-      o.y = (old == 0.f ? 0.f : o.y * old) + w * v[i].y;
-      m = m_new;
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t take = (which_ones >> (2 * c)) & 3u, two = pack_bf16x2(o[2 * c], o[2 * c + 1]);
+        if (take != 0) out[c] = take == 3u ? two : take == 1u ? (out[c] & 0xffff0000u) | (two & 0xffffu) : (out[c] & 0xffffu) | (two & 0xffff0000u);
+      }
+    };
+    store(wanted & met);
+    wanted &= ~met;
+    if (!__any_sync(0xffffffffu, wanted != 0)) continue;
+    // ------------------------------------------------------------ what is
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = 0.f;
+    for (int32_t j = 0; j < most; j += kAtOnce) {
+      if ((j & (a.page_rows - 1)) == 0) {
+        page = page_of(a, s, j);
+        if (__all_sync(0xffffffffu, wanted == 0 || l != l)) break;   // (NaN scores)
+      }
+      if (page < 0) continue;
+      EightOf<kE4m3> kk[kAtOnce], vv[kAtOnce];
+      const int64_t at = page * a.page_stride + kvh * a.head_stride + 8 * part;
+      auto in_page = [&](int i) { return (j + i < most ? j + i : j) & (a.page_rows - 1); };   // (no row that nobody sees)
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) kk[i].load(a.k, at + in_page(i) * a.row_stride), vv[i].load(a.v, at + in_page(i) * a.row_stride);
+      float w[kAtOnce], top = m;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        w[i] = dot64<kE4m3>(q, kk[i], scale_at(a.k_scale, page, in_page(i))) * p.scale;
+        if (j + i >= seen) w[i] = -INFINITY;
+        top = fmaxf(top, w[i]);
+      }
+      const float old = m == top ? l : m == -INFINITY ? 0.f : l * expf(m - top);
+      float sum = old;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        w[i] = w[i] == -INFINITY ? 0.f : expf(w[i] - top);
+        sum += w[i];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum, keep = old * inv;
+      m = top, l = sum;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] *= keep;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const float f = w[i] * inv;
+        float v[8];
+        vv[i].get(scale_at(a.v_scale, page, in_page(i)), v);
+        if (f != 0.f) {   // (what has no weight may hold anything)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) o[c] = fmaf(f, v[c], o[c]);
+        }
+      }
     }
+    store(wanted);
   }
-  if (bad && lane == 0) atomicOr(a.err, kErrPage);
-  const bool none = l == 0.f;
-  const int64_t at = t * p.heads + head;
-  *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + 2 * lane) = none ? 0u : pack_bf16x2(o.x / l, o.y / l);
-  if (p.lse != nullptr && lane == 0) p.lse[at] = none ? -INFINITY : m + logf(l);
 }
 
 }  // namespace spanla

@@ -34,19 +34,6 @@ __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -
 // 2^(from - to), 0 where nothing is relative to `from`.
 __device__ __forceinline__ float rescale(float from, float to) { return from == to ? 1.f : from == -INFINITY ? 0.f : ex2(from - to); }
 
-// Row heads of an item whose O came out infinite or NaN though the sum of weights is finite: once more from the
-// cache, without the rows that they do not see (and without O's parts, whose infinities may cancel).
-template <bool kE4m3>
-__device__ __forceinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, uint32_t which, int s, int64_t row0, int n, int32_t len,
-                                          int h) {
-  while (which != 0) {
-    const int m = __ffs(which) - 1;
-    which &= which - 1;
-    const int r = m / p.group;
-    attend_row<kE4m3>(a, p, s, row0 + r, h * p.group + m % p.group, max(0, len - n + r + 1));
-  }
-}
-
 // CTA (c, y): row heads 4 y .. 4 y + 3 of the item that begins in CTA c of the step kernel and goes on, from the parts of
 // it and the next CTAs.  Groups of 16 lanes: group (row, slice) has every kJoinSlices-th part of a row head, a lane four
 // elements of O; the row heads' maxima and sums are one group's, a lane a part.  What most items need is asked for before
@@ -137,7 +124,7 @@ __device__ __forceinline__ void join_step_parts(const KvArgs& a, const PagedAttn
     if (p.lse != nullptr && sub == 0) p.lse[at] = log_sum(m, l);
   }
   __syncthreads();
-  if (wild != 0 && tid < 32) redo_rows<kE4m3>(a, p, wild, j.s, j.row0, j.n, j.len, j.h);
+  if (wild != 0 && tid < 32) redo_rows<kE4m3>(a, p, wild, j.s, j.h, j.row0, 0, j.len - j.n + 1);
 }
 
 }  // namespace spanla

@@ -3,8 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import BF16, E4M3, f64
-from test_gpu_paged_attention import _run, _setup
+from paged_helpers import BF16, E4M3, check_attention, f64
+from test_gpu_paged_attention import _run, _setup, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,137 @@ def test_nothing_but_scores_of_minus_infinity(cuda_device, rows, cache, width):
         c[2].fill_(127)
     out, lse = _run(torch.ones_like(q), c, table, lens, cu, cuda_device, scale=1e38)
     assert not f64(out).any() and np.all(f64(lse) == -np.inf)
+
+
+def _values_at(c, table, s, row, head, dims, what):
+    """Write `what` into elements of one cached row of V."""
+    R = c[1].shape[2]
+    c[1][int(table[s, row // R]), head, row % R, dims] = what
+
+
+@pytest.mark.parametrize("width", [None, 200])
+def test_whole_items_behind_those_that_are_done_over(cuda_device, width):
+    """Several hundred short chunks, so that a CTA has many items one behind the other; every fifth sequence has infinities
+    and NaN in V, in rows that all of its packed rows see, some, or one.  They change the elements that see them, and no
+    bit beside."""
+    S, G, H = 700, 2, 2
+    rng = np.random.default_rng(34)
+    lens = [int(x) for x in rng.integers(40, 70, S)]
+    rows = [int(x) for x in rng.integers(9, 36, S)]
+    q, c, table, cu = _setup(lens, rows, G, H, 16, BF16, cuda_device, seed=34, width=width)
+    clean, clean_lse = _run(q, c, table, lens, cu, cuda_device)
+    size = torch.nan_to_num(c[1].float(), nan=0.0).abs().max().item()
+    want = {}
+    for s in range(0, S, 5):
+        for h in range(H):
+            at = [0, int(lens[s] - rows[s] + 3 + h), lens[s] - 1]           # seen by all rows, from the fourth on, by the last
+            for row, dim, what in zip(at, (1, 17, 63), (float("inf"), float("nan"), float("-inf"))):
+                _values_at(c, table, s, row, h, dim, what)
+                want[s, h, dim] = row, what
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    o, ref = f64(out), f64(clean)
+    assert torch.equal(lse, clean_lse)
+    for s in range(S):
+        b, e = int(cu[s]), int(cu[s + 1])
+        if s % 5:
+            assert torch.equal(out[b:e], clean[b:e])
+            continue
+        first = lens[s] - rows[s]
+        same = np.ones((e - b, G * H, 64), dtype=bool)
+        for (t, h, dim), (row, what) in want.items():
+            if t == s:
+                sees = np.arange(e - b) + first >= row
+                got = o[b:e, h * G:(h + 1) * G, dim][sees]
+                assert np.isnan(got).all() if np.isnan(what) else np.all(got == what)
+                same[:, h * G:(h + 1) * G, dim] = False
+                # (who does not see it: the same weights, rounded to bf16 or not, and o's own rounding, twice)
+                got, old = (x[b:e, h * G:(h + 1) * G, dim][~sees] for x in (o, ref))
+                assert np.all(np.abs(got - old) <= 2 * 2.0 ** -8 * (size + np.abs(old)))
+        assert np.array_equal(o[b:e][same], ref[b:e][same])
+
+
+@pytest.mark.parametrize("width", [None, 200])
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows,G", [(1, 1), (5, 3), (40, 2), (300, 1)])
+def test_small_weights_of_infinities_and_nan(cuda_device, rows, G, cache, width):
+    """Values whose weight is no fp32 number: positive all the same, so that an infinity stays one and a NaN one; and what
+    a score of -infinity hides (a NaN in V too) is not seen."""
+    lens, H = [rows + 310], 2
+    q, c, table, cu = _setup(lens, [rows], G, H, 16, cache, cuda_device, seed=35, width=width)
+    q = torch.ones_like(q)
+    low, hidden, hi = [3, 150, 305], 200, 290              # before and behind the row with the greatest score
+    R, flat = 16, (lambda x: x.view(torch.uint8)) if cache == E4M3 else (lambda x: x)
+    one = (lambda x: {-50.0: 0xE4, 40.0: 0x62}[x]) if cache == E4M3 else float      # (e4m3: -48 and 40)
+    at = lambda row: (int(table[0, row // R]), slice(None), row % R)  # noqa: E731
+    for row in low:
+        flat(c[0])[at(row)] = one(-50.0)
+    flat(c[0])[at(hi)] = one(40.0)
+    if cache == E4M3:
+        for x in (c[2], c[3]):
+            x[torch.from_numpy(table[0, :-(-lens[0] // R)]).long()] = 127
+    clean, clean_lse = _run(q, c, table, lens, cu, cuda_device)
+    assert np.isfinite(f64(clean)).all()
+    nan, inf = (0x7F, 0x7F) if cache == E4M3 else (float("nan"), float("inf"))
+    for dim, row, what in ((0, low[0], inf), (9, low[1], inf), (18, low[2], inf), (27, low[0], nan), (36, low[2], nan)):
+        flat(c[1])[at(row)][..., dim] = what
+    if cache == BF16:
+        c[1][at(low[1])][..., 18] = float("-inf")          # with the other sign in row low[2]: NaN
+        c[0][at(hidden)] = float("-inf")
+        c[1][at(hidden)] = float("nan")
+        c[1][at(hidden)] = 0
+        _, clean_lse = _run(q, c, table, lens, cu, cuda_device)
+        c[1][at(hidden)] = float("nan")
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    o = f64(out)
+    special = [0, 9, 18, 27, 36]
+    if cache == BF16:
+        assert np.all(o[..., [0, 9]] == np.inf) and np.isnan(o[..., [18, 27, 36]]).all()
+    else:
+        assert np.isnan(o[..., special]).all()
+    rest = np.delete(o, special, -1)
+    assert np.isfinite(rest).all() and np.isfinite(f64(lse)).all()
+    assert torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("width", [None, 700])
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows,G", [(1, 1), (4, 4), (40, 2), (300, 1)])
+def test_values_whose_sums_pass_fp32(cuda_device, rows, G, cache, width):
+    """Values of up to 3e38, of one sign and of both: the means are numbers, the sums of some hundred of them are not."""
+    lens = [rows + 400, rows + 5]
+    q, c, table, cu = _setup(lens, [rows, rows], G, 2, 16, cache, cuda_device, seed=36, width=width)
+    flat = (lambda x: x.view(torch.uint8)) if cache == E4M3 else (lambda x: x)
+    for s, L in enumerate(lens):
+        pages = torch.from_numpy(table[s, :-(-L // 16)]).long()
+        if cache == E4M3:
+            c[3][pages] = 246
+            flat(c[1])[pages] = 0x7E
+            flat(c[1])[pages, :, ::3, 1::2] = 0xFE
+        else:
+            c[1][pages] = 3e38
+            c[1][pages, :, ::3, 1::2] = -3e38
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    assert np.isfinite(f64(out)).all()
+    check_attention(q, out, lse, c, table, lens, cu, 0.125, weights(G, cache))
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+def test_what_an_infinity_in_v_costs(cuda_device, cache):
+    """Every row of a large chunk sees one (82,000 row heads, 20,000 rows): far from 0.38 us for each of them and cached row,
+    one behind the other in a warp."""
+    lens, rows, H = [21280], [1280], 64
+    q, c, table, cu = _setup(lens, rows, 1, H, 256, cache, cuda_device, seed=37)
+    clean, _ = _run(q, c, table, lens, cu, cuda_device)
+    c[1].view(torch.uint8 if cache == E4M3 else BF16)[int(table[0, 77]), :, 200, 5] = 0x7F if cache == E4M3 else float("inf")
+    ms = []
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        out, _ = _run(q, c, table, lens, cu, cuda_device)
+        b.record()
+        torch.cuda.synchronize()
+        ms.append(a.elapsed_time(b))
+    same = torch.ones(64, dtype=torch.bool, device=cuda_device)
+    same[5] = False
+    assert torch.equal(out[..., same], clean[..., same]) and not torch.isfinite(out[..., 5].float()).any()
+    assert min(ms) < 60, ms
