@@ -73,7 +73,8 @@ struct Cfg {
   static constexpr uint32_t kInfo = kBar + 8 * kNumBars;              // pages of a block that are there: bit i, rows 16 i ..
   static constexpr uint32_t kMissing = kInfo + 4 * (kStages + kRaw);
   static constexpr uint32_t kTmemSlot = kMissing + 4;
-  static constexpr uint32_t kBytes = kTmemSlot + 16;
+  static constexpr uint32_t kRedo = (kTmemSlot + 16 + 7) & ~7u;        // Redo of each softmax warp
+  static constexpr uint32_t kBytes = kRedo + 8 * 48;
   static constexpr uint32_t kRequest = kBytes + 1024;
   static_assert(kRequest <= 227 * 1024, "shared memory budget");
 };
@@ -162,6 +163,15 @@ struct Run {
   int32_t b, j0, j1, blocks;
   int64_t units;
 };
+
+// What a softmax warp keeps for the rows that it does over: where it began, and whether there are any.
+struct Redo {
+  Run first;
+  int64_t left;
+  int some;
+};
+static_assert(sizeof(Redo) == 48, "shared memory");
+constexpr uint32_t kRedoMark = 0x7f81u;   // what such elements hold till then (a NaN that no rounding gives)
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
@@ -491,6 +501,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const float c2 = p.scale * 1.4426950408889634f;
     const float raise_margin = fminf(8.f / c2, 1e37f);
     const int my_row = row / p.group, my_head = row % p.group;
+    Redo* redo = reinterpret_cast<Redo*>(smem + C::kRedo) + (warp - 4);
+    if (lane == 0) *redo = {r, left, 0};
+    __syncwarp();
     bool ok = true;
     int g = 0, gx = 0;
     for (; left > 0 && ok; next_run(r, left)) {
@@ -633,12 +646,35 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         part[kTileRows * kHeadDim + row] = m2;
         part[kTileRows * kHeadDim + kTileRows + row] = l;
       }
-      // Rows whose O came out infinite or NaN though the sum of weights is finite: once more from the cache, without
-      // the rows that they do not see.
-      const uint32_t which = __ballot_sync(0xffffffffu, wild && l == l && l != 0.f);
-      if (which != 0)
-        redo_rows<kE4m3>(a, p, which, s0 + r.s, r.h, s_row0[r.s] + static_cast<int64_t>(in_seq - my_row), quarter * 32,
-                            len - n + in_seq - my_row + 1);
+      if (wild && l == l && l != 0.f) {
+        redo->some = 1;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * kHeadDim);
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim / 2; ++c)
+          dst[c] = (bf16_finite(dst[c]) ? dst[c] & 0xffffu : kRedoMark) | (bf16_finite(dst[c] >> 16) ? dst[c] & 0xffff0000u : kRedoMark << 16);
+      }
+    }
+    // Rows of whole items whose O came out infinite or NaN though the sum of weights is finite: once more from the cache,
+    // without the rows that they do not see.  Behind the CTA's last item, when no other warp waits for this one but at the
+    // end: over a long cache it may take longer than a wait's limit.
+    __syncwarp();
+    if (ok && redo->some) {
+      r = redo->first;
+      left = redo->left;
+      for (; left > 0; next_run(r, left)) {
+        const int32_t rows = rows_of(r, x), first_row = r.b * item_rows + x * tile_rows;
+        bool wild = false;
+        if (r.j0 == 0 && r.j1 == r.blocks && my_row < rows) {
+          const int64_t at = (s_row0[r.s] + static_cast<int64_t>(first_row + my_row)) * p.heads + r.h * p.group + my_head;
+          const uint32_t* o = reinterpret_cast<const uint32_t*>(p.out + at * kHeadDim);
+#pragma unroll 8
+          for (int c = 0; c < kHeadDim / 2; ++c) wild |= (o[c] & 0xffffu) == kRedoMark || o[c] >> 16 == kRedoMark;
+        }
+        const uint32_t which = __ballot_sync(0xffffffffu, wild);
+        if (which != 0)
+          redo_rows<kE4m3>(a, p, which, s0 + r.s, r.h, s_row0[r.s] + static_cast<int64_t>(first_row), quarter * 32,
+                           s_len[r.s] - s_n[r.s] + first_row + 1);
+      }
     }
   } else {
     // -------------------------------------------------------------- e4m3 rows into bf16 tiles

@@ -119,6 +119,26 @@ def test_whole_items_behind_those_that_are_done_over(cuda_device, width):
 
 
 @pytest.mark.parametrize("width", [None, 200])
+def test_nan_scores_beside_values_that_are_not_finite(cuda_device, width):
+    """Row heads whose scores are NaN are NaN in every element, next to others, of the same and of other items of a CTA, that
+    see an infinity in one."""
+    S, G, H = 500, 2, 2
+    lens, rows = [60] * S, [30] * S
+    q, c, table, cu = _setup(lens, rows, G, H, 16, BF16, cuda_device, seed=38, width=width)
+    q = q.clone()
+    q.view(S, 30, G * H, 64)[:, 7, 1, 2] = float("nan")
+    c[1][torch.from_numpy(table[::3, 0].copy()).long(), :, 4, 40] = float("inf")
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    o, z = f64(out).reshape(S, 30, G * H, 64), f64(lse).reshape(S, 30, G * H)
+    nan = np.zeros((S, 30, G * H), dtype=bool)
+    nan[:, 7, 1] = True
+    assert np.isnan(o[nan]).all() and np.array_equal(np.isnan(z), nan) and np.isfinite(z[~nan]).all()
+    assert np.all(o[::3, ..., 40][~nan[::3]] == np.inf)
+    o[::3, ..., 40] = 0
+    assert np.isfinite(o[~nan]).all()
+
+
+@pytest.mark.parametrize("width", [None, 200])
 @pytest.mark.parametrize("cache", [BF16, E4M3])
 @pytest.mark.parametrize("rows,G", [(1, 1), (5, 3), (40, 2), (300, 1)])
 def test_small_weights_of_infinities_and_nan(cuda_device, rows, G, cache, width):
