@@ -73,8 +73,8 @@ struct Cfg {
   static constexpr uint32_t kInfo = kBar + 8 * kNumBars;              // pages of a block that are there: bit i, rows 16 i ..
   static constexpr uint32_t kMissing = kInfo + 4 * (kStages + kRaw);
   static constexpr uint32_t kTmemSlot = kMissing + 4;
-  static constexpr uint32_t kRedo = (kTmemSlot + 16 + 7) & ~7u;        // Redo of each softmax warp
-  static constexpr uint32_t kBytes = kRedo + 8 * 48;
+  static constexpr uint32_t kRedo = (kTmemSlot + 16 + 15) & ~15u;      // ChunkRedo of each softmax warp
+  static constexpr uint32_t kBytes = kRedo + kChunkSoftmaxWarps * sizeof(ChunkRedo);
   static constexpr uint32_t kRequest = kBytes + 1024;
   static_assert(kRequest <= 227 * 1024, "shared memory budget");
 };
@@ -164,19 +164,11 @@ struct Run {
   int64_t units;
 };
 
-// What a softmax warp keeps for the rows that it does over: where it began, and whether there are any.
-struct Redo {
-  Run first;
-  int64_t left;
-  int some;
-};
-static_assert(sizeof(Redo) == 48, "shared memory");
-constexpr uint32_t kRedoMark = 0x7f81u;   // what such elements hold till then (a NaN that no rounding gives)
-
-template <bool kE4m3>
+// kWhole: no item goes over several CTAs, there is no workspace, and no join kernel behind.
+template <bool kE4m3, bool kWhole>
 __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, float* ws) {
+                   const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, int s0, int ns, float* ws) {
   using C = Cfg<kE4m3>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -266,7 +258,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   auto take = [&](Run& r, int64_t off) {
     r.blocks = blocks_of(s_len[r.s], s_n[r.s], r.b, item_rows);
     r.units = static_cast<int64_t>(r.blocks) + kItemBlocks - off;
-    if (!whole_items) r.units = min(r.units, left);
+    if (!kWhole) r.units = min(r.units, left);
     r.j0 = static_cast<int32_t>(max(static_cast<int64_t>(0), off - kItemBlocks));
     r.j1 = static_cast<int32_t>(max(static_cast<int64_t>(r.j0), off + r.units - kItemBlocks));
     if (r.j1 == r.j0) left = 0;   // (the CTA's units end before the item's blocks begin)
@@ -316,7 +308,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   auto rows_of = [&](const Run& r, int x) { return max(0, min(tile_rows, s_n[r.s] - r.b * item_rows - x * tile_rows)); };
 
   // Whole items: a CTA takes those that begin in its units.
-  if (whole_items && left > 0 && first.units < first.blocks + kItemBlocks) next_run(first, left);
+  if (kWhole && left > 0 && first.units < first.blocks + kItemBlocks) next_run(first, left);
 
   Run r = first;
   if (warp < 4) {
@@ -426,7 +418,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           join.row0 = s_row0[r.s];
         }
       }
-      if (lane == 0 && gridDim.x > 1 && !whole_items) {
+      if (lane == 0 && !kWhole) {
         if (!ok) join.parts = 0;
         *reinterpret_cast<ChunkJoin*>(ws + blockIdx.x * kChunkWsFloats + 4 * kPartFloats) = join;
       }
@@ -501,8 +493,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const float c2 = p.scale * 1.4426950408889634f;
     const float raise_margin = fminf(8.f / c2, 1e37f);
     const int my_row = row / p.group, my_head = row % p.group;
-    Redo* redo = reinterpret_cast<Redo*>(smem + C::kRedo) + (warp - 4);
-    if (lane == 0) *redo = {r, left, 0};
+    ChunkRedo* redo = reinterpret_cast<ChunkRedo*>(smem + C::kRedo) + (warp - 4);
+    if (!kWhole && lane == 0) redo->some = 0;
     __syncwarp();
     bool ok = true;
     int g = 0, gx = 0;
@@ -646,34 +638,31 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         part[kTileRows * kHeadDim + row] = m2;
         part[kTileRows * kHeadDim + kTileRows + row] = l;
       }
-      if (wild && l == l && l != 0.f) {
+      // Rows whose O came out infinite or NaN though the sum of weights is finite are looked at once more, without the rows
+      // that they do not see: by the join kernel, which finds them by their marks.  (Here it would cost the loop over the
+      // blocks registers, 2,048 rows 183 us instead of 175; and, over a long cache, take longer than the CTA's other warps
+      // wait for this one.)  By this warp where there is no join, over at most 512 rows.
+      wild &= l == l && l != 0.f;
+      if (!kWhole && wild) {
+        if (redo->some == 0) redo->s = s0 + r.s, redo->h = r.h, redo->b = r.b;
+        redo->last_s = s0 + r.s, redo->last_h = r.h, redo->last_b = r.b;
         redo->some = 1;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * kHeadDim);
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim / 2; ++c)
-          dst[c] = (bf16_finite(dst[c]) ? dst[c] & 0xffffu : kRedoMark) | (bf16_finite(dst[c] >> 16) ? dst[c] & 0xffff0000u : kRedoMark << 16);
+        for (int c = 0; c < kHeadDim / 2; ++c) dst[c] = marked(dst[c]);
       }
-    }
-    // Rows of whole items whose O came out infinite or NaN though the sum of weights is finite: once more from the cache,
-    // without the rows that they do not see.  Behind the CTA's last item, when no other warp waits for this one but at the
-    // end: over a long cache it may take longer than a wait's limit.
-    __syncwarp();
-    if (ok && redo->some) {
-      r = redo->first;
-      left = redo->left;
-      for (; left > 0; next_run(r, left)) {
-        const int32_t rows = rows_of(r, x), first_row = r.b * item_rows + x * tile_rows;
-        bool wild = false;
-        if (r.j0 == 0 && r.j1 == r.blocks && my_row < rows) {
-          const int64_t at = (s_row0[r.s] + static_cast<int64_t>(first_row + my_row)) * p.heads + r.h * p.group + my_head;
-          const uint32_t* o = reinterpret_cast<const uint32_t*>(p.out + at * kHeadDim);
-#pragma unroll 8
-          for (int c = 0; c < kHeadDim / 2; ++c) wild |= (o[c] & 0xffffu) == kRedoMark || o[c] >> 16 == kRedoMark;
-        }
+      if (kWhole) {
         const uint32_t which = __ballot_sync(0xffffffffu, wild);
         if (which != 0)
-          redo_rows<kE4m3>(a, p, which, s0 + r.s, r.h, s_row0[r.s] + static_cast<int64_t>(first_row), quarter * 32,
-                           s_len[r.s] - s_n[r.s] + first_row + 1);
+          redo_rows<kE4m3>(a, p, which, s0 + r.s, r.h, s_row0[r.s] + static_cast<int64_t>(in_seq - my_row), quarter * 32,
+                           len - n + in_seq - my_row + 1);
+      }
+    }
+    if (!kWhole) {
+      __syncwarp();
+      if (lane == 0) {
+        if (!ok) redo->some = 0;   // (a wait ran out: there are items without any result)
+        reinterpret_cast<ChunkRedo*>(ws + blockIdx.x * kChunkWsFloats + 4 * kPartFloats + 8)[warp - 4] = *redo;
       }
     }
   } else {
@@ -752,7 +741,39 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // eighth part.  What an item of two parts needs is asked for before the record is there that says how many there are.
 constexpr int kChunkJoinThreads = 256, kJoinWarps = kChunkJoinThreads / 32;
 
-// CTAs (c, 8 ..), where there are any: the step kernel's parts (of `step_grid` CTAs), which it has of the same call.
+// A CTA: the rows that a softmax warp (x, quarter) has marked, in items from the first to the last that it names.
+template <bool kE4m3>
+__device__ __forceinline__ void redo_chunk_items(const KvArgs& a, const PagedAttn& p, const ChunkRedo& redo, int x, int quarter) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = quarter * 32 + 4 * warp + (lane >> 3);
+  const int32_t tile_rows = kTileRows / p.group;
+  int32_t h = redo.h, b = redo.b;
+  for (int32_t s = redo.s; s <= redo.last_s; ++s, h = b = 0) {
+    bool bad = false;
+    const SeqRows r = seq_rows(a, s, &bad);
+    if (static_cast<int64_t>(r.n) * p.group <= kStepHeads) continue;
+    const int32_t items = (r.n + 2 * tile_rows - 1) / (2 * tile_rows);
+    const int32_t last_h = s == redo.last_s ? redo.last_h : a.heads - 1;
+    for (; h <= last_h; ++h, b = 0) {
+      const int32_t last_b = s == redo.last_s && h == last_h ? redo.last_b : items - 1;
+      for (; b <= last_b; ++b) {
+        const int32_t first = (2 * b + x) * tile_rows, in = first + row / p.group;
+        bool mark = false;
+        if (row / p.group < tile_rows && in < r.n) {
+          const uint4 o = *reinterpret_cast<const uint4*>(p.out + ((r.row0 + in) * p.heads + h * p.group + row % p.group) * kHeadDim + 8 * (lane & 7));
+          mark = has_mark(o.x) || has_mark(o.y) || has_mark(o.z) || has_mark(o.w);
+        }
+        const uint32_t lanes = __ballot_sync(0xffffffffu, mark);
+        uint32_t which = 0;
+        for (int g = 0; g < 4; ++g)
+          if ((lanes >> (8 * g)) & 0xffu) which |= 1u << (4 * warp + g);
+        if (which != 0) redo_rows<kE4m3>(a, p, which, s, h, r.row0 + first, quarter * 32, r.len - r.n + first + 1);
+      }
+    }
+  }
+}
+
+// CTAs (c, 8 ..): the step kernel's parts (of `step_grid` CTAs), where it has some of the same call, and the row heads that it
+// has marked; the last ones: those that the chunk kernel has marked.
 template <bool kE4m3, bool kStepE4m3>
 __global__ void __launch_bounds__(kChunkJoinThreads, 4)
 chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, const float* ws, const __grid_constant__ KvArgs step,
@@ -762,12 +783,22 @@ chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ Page
   __shared__ uint32_t wild;
   griddep_launch_dependents();
   griddep_wait();
+  const float* mine = ws + blockIdx.x * kChunkWsFloats;
   if (blockIdx.y >= 8) {
-    if (static_cast<int>(blockIdx.x) < step_grid)
-      join_step_parts<kStepE4m3, kChunkJoinThreads / 16 / kJoinRows>(step, p, step_ws, step_grid, static_cast<int>(blockIdx.y) - 8);
+    const int y = static_cast<int>(blockIdx.y) - 8, steps = kM / kJoinRows;
+    if (blockIdx.y == gridDim.y - 1) {
+      const ChunkRedo* redo = reinterpret_cast<const ChunkRedo*>(mine + 4 * kPartFloats + 8);
+      uint32_t some = __ballot_sync(0xffffffffu, redo[threadIdx.x & (kChunkSoftmaxWarps - 1)].some != 0) & ((1u << kChunkSoftmaxWarps) - 1u);
+      for (; some != 0; some &= some - 1) {
+        const int w = __ffs(some) - 1;
+        redo_chunk_items<kE4m3>(a, p, redo[w], w >> 2, w & 3);
+      }
+    } else if (static_cast<int>(blockIdx.x) < step_grid) {
+      if (y < steps) join_step_parts<kStepE4m3, kChunkJoinThreads / 16 / kJoinRows>(step, p, step_ws, step_grid, y);
+      else redo_step_items<kStepE4m3>(step, p, step_ws);
+    }
     return;
   }
-  const float* mine = ws + blockIdx.x * kChunkWsFloats;
   const int x = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (blockIdx.y & 3) * 32 + lane;
   const int last = static_cast<int>(gridDim.x - 1 - blockIdx.x);
   auto part_of = [&](int i) { return mine + i * kChunkWsFloats + (2 * (i == 0 ? 1 : 0) + x) * kPartFloats; };
@@ -834,37 +865,36 @@ chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ Page
     redo_rows<kE4m3>(a, p, which, j.s, j.h, j.row0 + static_cast<int64_t>(first), (blockIdx.y & 3) * 32, j.len - j.n + first + 1);
 }
 
-template <bool kE4m3>
+template <bool kE4m3, bool kWhole>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0,
-                   int ns, int grid, bool whole_items, float* ws, cudaStream_t stream) {
+                   int ns, int grid, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3>;
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_relaxed) == 0) {   // the warps' shares of registers have to be those of the launch
     cudaFuncAttributes attr;
-    const cudaError_t e = cudaFuncGetAttributes(&attr, paged_chunk_kernel<kE4m3>);
+    const cudaError_t e = cudaFuncGetAttributes(&attr, paged_chunk_kernel<kE4m3, kWhole>);
     if (e != cudaSuccess) return e;
     regs.store(attr.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3>, C::kRequest, done);
+  const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3, kWhole>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  return launch_behind(paged_chunk_kernel<kE4m3>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns,
-                       whole_items, ws);
+  return launch_behind(paged_chunk_kernel<kE4m3, kWhole>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
                                const PagedAttn& p, int s0, int ns, int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream) {
-  return e4m3 ? launch<true>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream)
-              : launch<false>(tm_q, tm_k, tm_v, a, p, s0, ns, grid, whole_items, ws, stream);
+  if (whole_items) return (e4m3 ? launch<true, true> : launch<false, true>)(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
+  return (e4m3 ? launch<true, false> : launch<false, false>)(tm_q, tm_k, tm_v, a, p, s0, ns, grid, ws, stream);
 }
 
 cudaError_t launch_chunk_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, const KvArgs& step, int step_grid,
                               bool step_e4m3, const float* step_ws, cudaStream_t stream) {
   auto* kernel = e4m3 ? chunk_join_kernel<true, true> : step_e4m3 ? chunk_join_kernel<false, true> : chunk_join_kernel<false, false>;
-  return launch_behind(kernel, dim3(grid, step_grid > 0 ? 8 + kM / kJoinRows : 8), kChunkJoinThreads, 0, stream, a, p, ws, step, step_ws,
+  return launch_behind(kernel, dim3(grid, step_grid > 0 ? 8 + kM / kJoinRows + 2 : 8 + 1), kChunkJoinThreads, 0, stream, a, p, ws, step, step_ws,
                        step_grid);
 }
 

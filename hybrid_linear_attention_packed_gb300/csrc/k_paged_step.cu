@@ -67,7 +67,8 @@ struct Cfg {
   static constexpr uint32_t kScan = kInfo + kWarps * kStages * 8;
   static constexpr uint32_t kBar = kScan + kWarps * 8;
   static constexpr uint32_t kOpen = kBar + kWarps * kStages * 8;   // Open of each warp, and one more
-  static constexpr uint32_t kBytes = kOpen + (kWarps + 1) * 24;
+  static constexpr uint32_t kRedo = (kOpen + (kWarps + 1) * 24 + 15) & ~15u;   // StepRedo of each warp
+  static constexpr uint32_t kBytes = kRedo + kWarps * 16;
   static constexpr uint32_t kRequest = kBytes + 1024;
   static_assert(kRequest <= 227 * 1024 && kRing >= kSlot * 4 && kInfo % 8 == 0 && kSum % 16 == 0 && kHead % 16 == 0, "shared memory");
 };
@@ -130,10 +131,11 @@ __device__ __forceinline__ void store_pair(const PagedAttn& p, int64_t at, int d
   *reinterpret_cast<uint32_t*>(p.out + at * kHeadDim + d) = pack_bf16x2(x, y);
 }
 
-template <bool kE4m3, bool kTwo>
+// kWhole: the CTAs take whole items, there is no workspace, and no join kernel behind.
+template <bool kE4m3, bool kTwo, bool kWhole>
 __global__ void __launch_bounds__(Cfg<kE4m3, kTwo>::kWarps * 32, 1)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvArgs a,
-                  const __grid_constant__ PagedAttn p, int s0, int ns, bool whole_items, bool behind, float* ws) {
+                  const __grid_constant__ PagedAttn p, int s0, int ns, bool behind, float* ws) {
   using C = Cfg<kE4m3, kTwo>;
   constexpr int kW = C::kWarps, kS = C::kStages, kUnit = C::kUnit, kN = kUnit / 8, kR = kTwo ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -216,7 +218,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   const int64_t edge_w = min(sh.nw, static_cast<int64_t>(blockIdx.x) * kW + min(lane, kW));
   int64_t edge = sh.each * edge_w + min(edge_w, sh.more);               // lane w: the first unit of the CTA's warp w
   auto edge_of = [&](int w) { return __shfl_sync(0xffffffffu, edge, w); };
-  if (whole_items) {
+  if (kWhole) {
     // Items of a few units each: a CTA takes those that begin in its share, whole, and shares them out to its warps
     // (the first ones, where there are fewer units than warps).
     At at{};
@@ -299,7 +301,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   };
 
   Open* open = reinterpret_cast<Open*>(smem + C::kOpen);
+  // Row heads of whole items whose O came out infinite or NaN though the sum of weights is finite are looked at once more,
+  // without the rows that they do not see: by the join kernel, which finds them by their marks, or, where there is none, by
+  // this warp.  (A call here costs the loop over the units registers: 61 tokens over e4m3 pages 119.7 us instead of 117.7.)
+  StepRedo* redo = reinterpret_cast<StepRedo*>(smem + C::kRedo) + warp;
   if (lane == 0) {
+    if (!kWhole) *redo = {INT64_MAX, -1};
     open[warp].units = 0;
     if (warp == 0) open[kW].units = 0;
   }
@@ -634,12 +641,24 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               else store_pair(p, at, 8 * j + 2 * t, y[j], y[8 + j]);
             }
             if (p.lse != nullptr && t == 0) p.lse[at] = log_sum(m[r], l[r]);
+            if (!kWhole && wild) {   // (the lanes' elements that they have just stored)
+              uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * kHeadDim);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                uint32_t* two = dst + (kE4m3 ? 8 * t + j : 4 * j + t);
+                *two = marked(*two);
+              }
+              const int64_t it = static_cast<int64_t>(s0 + cons.s) * a.heads + cons.h;
+              *redo = {min(redo->first, it), it};
+            }
           }
-          const uint32_t b = __ballot_sync(0xffffffffu, wild);
-          for (int i = 0; b != 0 && i < 8; ++i)
-            if ((b >> (4 * i)) & 15u) which |= 1u << (i + 8 * r);
+          if (kWhole) {
+            const uint32_t b = __ballot_sync(0xffffffffu, wild);
+            for (int i = 0; b != 0 && i < 8; ++i)
+              if ((b >> (4 * i)) & 15u) which |= 1u << (i + 8 * r);
+          }
         }
-        if (which != 0) redo_rows<kE4m3>(a, p, which, s0 + cons.s, cons.h, s_row0[cons.s], 0, len - n + 1);
+        if (kWhole && which != 0) redo_rows<kE4m3>(a, p, which, s0 + cons.s, cons.h, s_row0[cons.s], 0, len - n + 1);
       } else {
         // (what began before the CTA is warp 0's to tell of: open[kW] where it ends in warp 0, as another may begin there)
         if (lane == 0 && (item_done ? warp == 0 : warp == 0 || !started_before))
@@ -788,6 +807,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               *reinterpret_cast<uint2*>(p.out + o_at * kHeadDim + 4 * sub) =
                   jl[u] == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
               if (p.lse != nullptr && sub == 0) p.lse[o_at] = log_sum(jm[u], jl[u]);
+              if (!kWhole && wild) {
+                uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + o_at * kHeadDim + 4 * sub);
+                dst[0] = marked(dst[0]), dst[1] = marked(dst[1]);
+                const int64_t ri = static_cast<int64_t>(s0 + it.s) * a.heads + it.h;
+                *redo = {min(redo->first, ri), max(redo->last, ri)};
+              }
             }
           } else if (in) {
             *reinterpret_cast<float4*>(out_slot + row[u] * kSlotStride + 4 * sub) = jo[u];
@@ -797,7 +822,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               out_slot[kM * kSlotStride + 2 * kM + row[u]] = jl[u];
             }
           }
-          const uint32_t bits = __ballot_sync(0xffffffffu, wild);
+          const uint32_t bits = kWhole ? __ballot_sync(0xffffffffu, wild) : 0u;
           which |= ((bits & 0xffffu) ? 1u : 0u) << (2 * (i + u)) | ((bits >> 16) ? 2u : 0u) << (2 * (i + u));
         }
       };
@@ -808,13 +833,21 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll 1
         for (; i < end; i += 2) join_pairs(std::integral_constant<int, 2>(), i);
       }
-      if (which != 0) redo_rows<kE4m3>(a, p, which, s0 + it.s, it.h, s_row0[it.s], 0, s_len[it.s] - n + 1);
+      if (kWhole && which != 0) redo_rows<kE4m3>(a, p, which, s0 + it.s, it.h, s_row0[it.s], 0, s_len[it.s] - n + 1);
     }
   }
   // (warp 0's lanes have the records: the one that has the item writes, or lane 0)
-  if (warp == 0 && gridDim.x > 1 && !whole_items) {
+  if (warp == 0 && !kWhole) {
     const uint32_t goes_on = __ballot_sync(0xffffffffu, join.parts > 0);
     if (goes_on != 0 ? join.parts > 0 : lane == 0) *reinterpret_cast<StepJoin*>(ws_part + 2 * kSlotFloats) = join;
+  }
+  if (!kWhole) {
+    StepRedo* to = reinterpret_cast<StepRedo*>(ws_part + 2 * kSlotFloats + sizeof(StepJoin) / 4);
+    __syncwarp();
+    if (lane == 0) {
+      to[warp] = ok ? *redo : StepRedo{INT64_MAX, -1};   // (not ok: a wait ran out, and there are items without any result)
+      if (warp + kW < kStepMostWarps) to[warp + kW] = {INT64_MAX, -1};
+    }
   }
   if (behind && blockIdx.x == 0) griddep_wait();
 }
@@ -824,23 +857,26 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices * 16, 1024 / (kJoinRow
 paged_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ PagedAttn p, const float* ws) {
   griddep_launch_dependents();
   griddep_wait();
-  join_step_parts<kE4m3, kJoinSlices>(a, p, ws, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.y));
+  if (blockIdx.y == gridDim.y - 1) redo_step_items<kE4m3>(a, p, ws);
+  else join_step_parts<kE4m3, kJoinSlices>(a, p, ws, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.y));
 }
 
-template <bool kE4m3, bool kTwo>
+template <bool kE4m3, bool kTwo, bool kWhole>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns, int grid,
-                   bool whole_items, bool behind, float* ws, cudaStream_t stream) {
+                   bool behind, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3, kTwo>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3, kTwo>, C::kRequest, done);
+  const cudaError_t e = set_smem_limit_once(paged_step_kernel<kE4m3, kTwo, kWhole>, C::kRequest, done);
   if (e != cudaSuccess) return e;
-  return launch_behind(paged_step_kernel<kE4m3, kTwo>, dim3(grid), C::kWarps * 32, C::kRequest, stream, tm_k, tm_v, a, p, s0, ns,
-                       whole_items, behind, ws);
+  return launch_behind(paged_step_kernel<kE4m3, kTwo, kWhole>, dim3(grid), C::kWarps * 32, C::kRequest, stream, tm_k, tm_v, a, p, s0, ns,
+                       behind, ws);
 }
 
 }  // namespace
 
-static_assert(kStepWsFloats * 4 >= 2 * kSlotFloats * 4 + sizeof(StepJoin), "workspace of a CTA");
+static_assert(kStepWsFloats * 4 >= 2 * kSlotFloats * 4 + sizeof(StepJoin) + kStepMostWarps * sizeof(StepRedo) &&
+                  Cfg<true, false>::kWarps <= kStepMostWarps && 2 * Cfg<false, false>::kWarps >= kStepMostWarps,
+              "workspace of a CTA");
 
 int paged_step_unit(bool e4m3) { return e4m3 ? Cfg<true, false>::kUnit : Cfg<false, false>::kUnit; }
 
@@ -855,13 +891,16 @@ int paged_step_grid(int64_t most_units, int num_sms) {
 cudaError_t launch_paged_step(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a, const PagedAttn& p, int s0, int ns,
                               int grid, bool e4m3, bool whole_items, bool behind, float* ws, cudaStream_t stream) {
   const bool two = a.max_rows * p.group > 8;
-  return e4m3 ? (two ? launch<true, true> : launch<true, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, behind, ws, stream)
-              : (two ? launch<false, true> : launch<false, false>)(tm_k, tm_v, a, p, s0, ns, grid, whole_items, behind, ws, stream);
+  auto* run = whole_items ? (e4m3 ? (two ? launch<true, true, true> : launch<true, false, true>)
+                                  : (two ? launch<false, true, true> : launch<false, false, true>))
+                          : (e4m3 ? (two ? launch<true, true, false> : launch<true, false, false>)
+                                  : (two ? launch<false, true, false> : launch<false, false, false>));
+  return run(tm_k, tm_v, a, p, s0, ns, grid, behind, ws, stream);
 }
 
 cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, bool e4m3, const float* ws, cudaStream_t stream) {
   const int64_t most = std::min<int64_t>(kM, a.max_rows * p.group);   // row heads
-  const dim3 ctas(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
+  const dim3 ctas(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows + 1));
   // Items over four CTAs and more: twice the threads, as a thread then has several parts; but where the call has long
   // chunks too (and its step kernel perhaps nothing), the bigger launch costs more.  (131,072 rows, up to 90 parts: 18.4 us,
   // by twice the threads 17.7; 24 x 4 tokens, up to 6 parts: 30.5 and 31.9; a chunk of 512: 34.9 and 35.8.)

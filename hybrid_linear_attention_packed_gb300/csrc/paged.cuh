@@ -145,6 +145,14 @@ struct EightOf<true> {
 
 __device__ __forceinline__ bool bf16_finite(uint32_t bits) { return (bits & 0x7f80u) != 0x7f80u; }
 
+// What elements to be found again by the join kernel hold till then: a NaN that no rounding gives.  (A row whose scores are
+// NaN is NaN, and stays so.)
+constexpr uint32_t kRedoMark = 0x7f81u;
+__device__ __forceinline__ bool has_mark(uint32_t two) { return (two & 0xffffu) == kRedoMark || two >> 16 == kRedoMark; }
+__device__ __forceinline__ uint32_t marked(uint32_t two) {
+  return (bf16_finite(two) ? two & 0xffffu : kRedoMark) | (bf16_finite(two >> 16) ? two & 0xffff0000u : kRedoMark << 16);
+}
+
 // q . k of a row head, whose eight lanes have eight elements each.
 template <bool kE4m3>
 __device__ __forceinline__ float dot64(const EightOf<false>& q, const EightOf<kE4m3>& k, float k_scale) {

@@ -34,6 +34,43 @@ __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -
 // 2^(from - to), 0 where nothing is relative to `from`.
 __device__ __forceinline__ float rescale(float from, float to) { return from == to ? 1.f : from == -INFINITY ? 0.f : ex2(from - to); }
 
+// A CTA: the row heads that a CTA of the step kernel has marked, in items of its own.  (On CTAs of their own, and not
+// beside a join, whose latency counts: one token 12.6 us then, instead of 11.4.)
+template <bool kE4m3>
+__device__ __forceinline__ void redo_step_items(const KvArgs& a, const PagedAttn& p, const float* ws) {
+  const StepRedo* marks = reinterpret_cast<const StepRedo*>(ws + static_cast<int64_t>(blockIdx.x) * kStepWsFloats + 2 * kSlotFloats +
+                                                            sizeof(StepJoin) / 4);
+  StepRedo x = marks[threadIdx.x & (kStepMostWarps - 1)];
+#pragma unroll
+  for (int d = kStepMostWarps / 2; d > 0; d >>= 1) {
+    x.first = min(x.first, static_cast<int64_t>(__shfl_xor_sync(0xffffffffu, x.first, d)));
+    x.last = max(x.last, static_cast<int64_t>(__shfl_xor_sync(0xffffffffu, x.last, d)));
+  }
+  const int lane = threadIdx.x & 31;
+  if (x.last < 0) return;   // (first is no item then)
+  for (int64_t it = x.first + (threadIdx.x >> 5); it <= x.last; it += blockDim.x >> 5) {
+    const int s = static_cast<int>(it / a.heads), h = static_cast<int>(it % a.heads);
+    bool bad = false;
+    const SeqRows r = seq_rows(a, s, &bad);
+    const int64_t mh = static_cast<int64_t>(r.n) * p.group;
+    if (mh > kM) continue;
+    uint32_t which = 0;
+    for (int i = 0; i < kM; i += 4) {
+      const int row = i + (lane >> 3);
+      bool mark = false;
+      if (row < mh) {
+        const uint4 o = *reinterpret_cast<const uint4*>(p.out + ((r.row0 + row / p.group) * p.heads + h * p.group + row % p.group) * kHeadDim +
+                                                        8 * (lane & 7));
+        mark = has_mark(o.x) || has_mark(o.y) || has_mark(o.z) || has_mark(o.w);
+      }
+      const uint32_t lanes = __ballot_sync(0xffffffffu, mark);
+      for (int g = 0; g < 4; ++g)
+        if ((lanes >> (8 * g)) & 0xffu) which |= 1u << (i + g);
+    }
+    if (which != 0) redo_rows<kE4m3>(a, p, which, s, h, r.row0, 0, r.len - r.n + 1);
+  }
+}
+
 // CTA (c, y): row heads 4 y .. 4 y + 3 of the item that begins in CTA c of the step kernel and goes on, from the parts of
 // it and the next CTAs.  Groups of 16 lanes: group (row, slice) has every kJoinSlices-th part of a row head, a lane four
 // elements of O; the row heads' maxima and sums are one group's, a lane a part.  What most items need is asked for before

@@ -2215,8 +2215,8 @@ PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t se
   // and joined 13.1; of 500: 12.6 and 14.9; one with 200 of 500: 15.4 and 14.9, from the host 15.7 and 15.8.)
   const int64_t item_rows = 2 * (kTileRows / group);
   g.chunk_whole = capacity <= kWholeBlocks * kTileRows && heads * (rows / item_rows + std::min<int64_t>(seqs, rows)) <= kWholeItems;
-  g.step_ws = align256(static_cast<size_t>(g.step > 1 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
-  g.chunk_ws = align256(static_cast<size_t>(g.chunk > 1 && !g.chunk_whole ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
+  g.step_ws = align256(static_cast<size_t>(g.step > 0 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
+  g.chunk_ws = align256(static_cast<size_t>(g.chunk > 0 && !g.chunk_whole ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
   const double copy = static_cast<double>(seqs) * capacity * heads * kHeadDim * 2;
   g.expand = e4m3 && capacity > 0 && g.chunk > 0 && max_rows * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
   g.copies = g.expand ? align256(static_cast<size_t>(seqs * capacity * heads * kHeadDim * 2)) : 0;
@@ -2263,7 +2263,7 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num
     st = encode_pages(&tm_k, a.k, a, e4m3, unit);
     if (st == SPAN_LA_OK) st = encode_pages(&tm_v, a.v, a, e4m3, unit);
   }
-  const bool step_join = step_grid > 1 && !grids.whole, chunk_join = chunk_grid > 1 && !grids.chunk_whole;
+  const bool step_join = step && !grids.whole, chunk_join = chunk && !grids.chunk_whole;
   auto run_step = [&](int s0, int ns, bool behind) {
     return counted_launch(kKernelPagedStep, stream, [&] {
       return launch_paged_step(tm_k, tm_v, a, p, s0, ns, step_grid, e4m3, grids.whole, behind, ws, stream);

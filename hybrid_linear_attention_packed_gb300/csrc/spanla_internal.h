@@ -452,14 +452,17 @@ struct PagedAttn {
 };
 // Sequences of at most kStepHeads packed row heads (rows * group) of a key head (k_paged_step.cu), at most kStepSeqs in
 // a launch: [s0, s0 + ns).  `ws`: kStepWsFloats for each of the `grid` CTAs; the join kernel, with the same grid, follows
-// where there is more than one, unless the CTAs take whole items.  `behind`: behind the chunk kernel of the same call, whose
+// unless the CTAs take whole items.  `behind`: behind the chunk kernel of the same call, whose
 // end it need not wait for.
 constexpr int kStepHeads = 16, kStepSeqs = 512;
-constexpr int kStepWsFloats = 2432, kStepMaxGrid = 160;
+constexpr int kStepWsFloats = 2496, kStepMaxGrid = 160, kStepMostWarps = 16;
 struct alignas(16) StepJoin {   // behind a CTA's two parts: the item that begins in the CTA and goes on in the next ones
   int32_t parts;                // CTAs with some of it, or 0
   int32_t s, h, n, len, row0;
   int32_t pad[2];
+};
+struct alignas(16) StepRedo {   // of each warp, behind that: whole items in which it has marked rows
+  int64_t first, last;          // s * heads + h of the first and the last of them; last < 0: none
 };
 int paged_step_unit(bool e4m3);   // cached rows of a unit of work
 int paged_step_grid(int64_t most_units, int num_sms);
@@ -470,12 +473,19 @@ cudaError_t launch_paged_join(const KvArgs& a, const PagedAttn& p, int grid, boo
 // Sequences of more row heads (k_paged_chunk.cu): as the step kernel's, with kChunkWsFloats a CTA (two parts of two tiles);
 // whole_items: no item over several CTAs, no workspace and no join.
 constexpr int kChunkPartFloats = kTileRows * kHeadDim + 2 * kTileRows;
-constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8;
 struct alignas(16) ChunkJoin {
   int32_t parts;
   int32_t s, h, first, n, len, row0;   // first: the item's first row in the sequence's packed rows
   int32_t pad;
 };
+struct alignas(16) ChunkRedo {   // of each softmax warp, behind the join's record: whole items in which it has marked rows
+  int32_t some;                  // 0: none
+  int32_t s, h, b;               // the first of them (b: its number in the sequence and head)
+  int32_t last_s, last_h, last_b;
+  int32_t pad;
+};
+constexpr int kChunkSoftmaxWarps = 8;
+constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8 + 8 * kChunkSoftmaxWarps;
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
                                const PagedAttn& p, int s0, int ns, int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream);
 // step, step_grid (0: none), ...: joins the step kernel's parts of the same call too.

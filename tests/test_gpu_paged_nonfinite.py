@@ -119,6 +119,45 @@ def test_whole_items_behind_those_that_are_done_over(cuda_device, width):
 
 
 @pytest.mark.parametrize("width", [None, 200])
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("S", [40, 300, 700])
+def test_tokens_and_chunks_that_see_nan(cuda_device, S, cache, width):
+    """Single tokens, drafted ones, chunks and empty sequences side by side, some of which see a NaN in one element of V, and
+    some of whose rows do not see one in their last row."""
+    G, H = 2, 2
+    rng = np.random.default_rng(39)
+    lens = [int(x) for x in rng.integers(40, 400, S)]
+    rows = [int(x) for x in rng.choice([0, 1, 4, 8, 20, 35], S)]
+    q, c, table, cu = _setup(lens, rows, G, H, 16, cache, cuda_device, seed=39, width=width)
+    clean, clean_lse = _run(q, c, table, lens, cu, cuda_device)
+    bits = c[1].view(torch.uint8) if cache == E4M3 else c[1]
+    nan = 0x7F if cache == E4M3 else float("nan")
+    for s in range(0, S, 3):
+        bits[int(table[s, 1]), 1, 5, 33] = nan
+        last = lens[s] - 1
+        bits[int(table[s, last // 16]), 0, last % 16, 50] = nan
+    out, lse = _run(q, c, table, lens, cu, cuda_device)
+    assert torch.equal(lse, clean_lse)
+    for s in range(S):
+        b, e = int(cu[s]), int(cu[s + 1])
+        x, y = out[b:e], clean[b:e]
+        if s % 3 == 0 and e > b:
+            sees = max(0, 21 - (lens[s] - rows[s]))             # packed rows from this one on see row 21
+            assert torch.isnan(x[sees:, G:, 33]).all() and torch.isnan(x[-1, :G, 50]).all()
+            assert torch.isfinite(x[:sees, G:, 33].float()).all()
+            same = torch.ones(x.shape, dtype=torch.bool, device=cuda_device)
+            same[:, G:, 33] = same[:, :G, 50] = False
+            x, y = x[same], y[same]
+            assert torch.isfinite(out[b:e - 1, :G, 50].float()).all()
+        assert torch.equal(x, y)
+    keep = np.concatenate([np.arange(cu[s], cu[s + 1] - 1) for s in range(S) if rows[s] > 0])     # no row's last, key head 0
+    ref_cu = np.concatenate([[0], np.cumsum([max(r - 1, 0) for r in rows])])
+    one = tuple(None if x is None else x[:, :1] for x in c)
+    check_attention(q[keep][:, :G], out[keep][:, :G], None, one, table, [n - (r > 0) for n, r in zip(lens, rows)], ref_cu, 0.125,
+                    lambda n: weights(G, cache)(n + 1))
+
+
+@pytest.mark.parametrize("width", [None, 200])
 def test_nan_scores_beside_values_that_are_not_finite(cuda_device, width):
     """Row heads whose scores are NaN are NaN in every element, next to others, of the same and of other items of a CTA, that
     see an infinity in one."""
