@@ -2153,6 +2153,11 @@ int64_t most_rows(const span_la_kv_cache* c, int64_t rows, int32_t max_rows) {
   return max_rows != 0 ? max_rows : c != nullptr && c->row_cu == nullptr ? 1 : rows;
 }
 
+// And that its longest sequence has, as far as the host can tell: what the caller says, or as many as there are on average.
+int64_t sure_rows(const span_la_kv_cache* c, int64_t rows, int32_t max_rows) {
+  return max_rows != 0 ? max_rows : c->num_seqs > 0 ? (rows + c->num_seqs - 1) / c->num_seqs : 0;
+}
+
 // Boxes of `rows` rows of one page and head, out of pages [pages][heads][page_rows][64].
 span_la_status encode_pages(CUtensorMap* map, const void* base, const KvArgs& a, bool e4m3, int rows) {
   const cuuint64_t esz = e4m3 ? 1 : 2;
@@ -2193,13 +2198,13 @@ struct PagedGrids {
 
 // From this many row heads of a sequence and key head on, and up to this many bytes of copies, e4m3 pages are expanded to
 // bf16 ahead of the chunk kernel: it converts a block for every 256 row heads that see it, next to a softmax that needs
-// the issue slots.  (20,000 rows, four key heads, expanded and not: 8,192 row heads 179 us and 207, 2,048 66 and 69,
-// 1,024 47.4 and 46.3.)
+// the issue slots.  (20,000 rows, four key heads, one sequence, expanded and not: 8,192 row heads 179 us and 207, 2,048 66
+// and 69, 1,024 47.4 and 46.3.)
 constexpr int64_t kExpandRowHeads = 2048;
 constexpr size_t kExpandBytes = size_t(128) << 20;
 constexpr int64_t kWholeBlocks = 4, kWholeItems = 128;
 
-PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int group, bool e4m3, int num_sms) {
+PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t seqs, int64_t max_rows, int64_t sure, int group, bool e4m3, int num_sms) {
   PagedGrids g{};
   g.unit = paged_step_unit(e4m3);
   const int64_t units = std::max<int64_t>(1, (capacity + g.unit - 1) / g.unit);   // of a sequence and head, at most
@@ -2218,16 +2223,17 @@ PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t se
   g.step_ws = align256(static_cast<size_t>(g.step > 0 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));
   g.chunk_ws = align256(static_cast<size_t>(g.chunk > 0 && !g.chunk_whole ? g.chunk : 0) * kChunkWsFloats * sizeof(float));
   const double copy = static_cast<double>(seqs) * capacity * heads * kHeadDim * 2;
-  g.expand = e4m3 && capacity > 0 && g.chunk > 0 && max_rows * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
+  g.expand = e4m3 && capacity > 0 && g.chunk > 0 && sure * group >= kExpandRowHeads && copy <= kExpandBytes / 2;
   g.copies = g.expand ? align256(static_cast<size_t>(seqs * capacity * heads * kHeadDim * 2)) : 0;
   g.bytes = g.step_ws + g.chunk_ws + 2 * g.copies;
   return g;
 }
 
-span_la_status run_paged(const KvArgs& a, const PagedAttn& p, bool e4m3, int num_sms, void* workspace, cudaStream_t stream) {
+span_la_status run_paged(const KvArgs& a, const PagedAttn& p, int64_t sure, bool e4m3, int num_sms, void* workspace,
+                         cudaStream_t stream) {
   span_la_status st = SPAN_LA_OK;
   CUtensorMap tm_q, tm_k, tm_v;
-  const PagedGrids grids = paged_grids(a.rows, a.capacity, a.heads, a.seqs, a.max_rows, p.group, e4m3, num_sms);
+  const PagedGrids grids = paged_grids(a.rows, a.capacity, a.heads, a.seqs, a.max_rows, sure, p.group, e4m3, num_sms);
   const int unit = grids.unit, step_grid = grids.step, chunk_grid = grids.chunk;
   const bool step = step_grid > 0, chunk = chunk_grid > 0;
   const size_t bytes = grids.bytes;
@@ -3086,7 +3092,7 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     p.heads = num_q_heads;
     p.group = num_q_heads / a.heads;
     p.scale = scale == 0.f ? 0.125f : scale;
-    return run_paged(a, p, cache->dtype == SPAN_LA_E4M3, dev->num_sms, workspace, stream);
+    return run_paged(a, p, sure_rows(cache, rows, max_rows), cache->dtype == SPAN_LA_E4M3, dev->num_sms, workspace, stream);
   });
 }
 
@@ -3095,7 +3101,7 @@ int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const
       rows < 1 || cache->num_seqs < 1 || max_rows < 0)
     return 0;
   return static_cast<int64_t>(paged_grids(rows, static_cast<int64_t>(cache->table_width) * cache->page_rows, cache->num_heads, cache->num_seqs,
-                                          most_rows(cache, rows, max_rows), num_q_heads / cache->num_heads,
+                                          most_rows(cache, rows, max_rows), sure_rows(cache, rows, max_rows), num_q_heads / cache->num_heads,
                                           cache->dtype == SPAN_LA_E4M3, kStepMaxGrid).bytes);
 }
 

@@ -164,6 +164,20 @@ def test_workspace(lib):
     assert f(0, 4, _cache(), 1) == 0 and f(3, 5, _cache(), 1) == 0 and f(3, 4, None, 1) == 0 and f(3, 4, _cache(num_seqs=0), 1) == 0
 
 
+def test_workspace_for_expanded_pages(lib):
+    """Copies of e4m3 pages where some sequence has 2,048 row heads: the caller says so, or there are as many on average."""
+    f = lib.span_la_softmax_paged_workspace
+    wide = dict(num_seqs=256, table_width=64, table_stride=64)                    # 1,024 rows of 2 heads: 2 x 64 MiB of copies
+    copies = 2 * 256 * 64 * 16 * 2 * 64 * 2
+    single = _cache(**wide)                                                       # 256 single tokens of 8 heads a key head
+    assert f(256, 16, single, 0) == f(256, 16, single, 255) < copies
+    assert f(256, 16, single, 256) == f(256, 16, single, 255) + copies            # one sequence may have them all
+    assert f(256 * 255, 16, single, 0) == f(256 * 255, 16, single, 255) < copies
+    assert f(256 * 255 + 1, 16, single, 0) == f(256 * 255, 16, single, 256) > copies
+    one = _cache(table_width=1000, table_stride=1000, num_seqs=1)
+    assert f(1024, 4, one, 0) == f(1024, 4, one, 1024) > f(1023, 4, one, 0) + 2 * 16000 * 2 * 64 * 2 - 1
+
+
 def test_layouts_that_interleave_are_taken(lib):
     """K and V of a page side by side, heads inside of rows: as far as the (missing) device, past every check."""
     if torch.cuda.is_available():
