@@ -118,6 +118,12 @@ bool stream_of(PyObject* o, int dev, cudaStream_t* s) {
   return true;
 }
 
+// True where `s`, given as `o`, is another stream than the current one: new
+// outputs are then made for it by spanla.py.
+bool other_stream(PyObject* o, cudaStream_t s, int dev) {
+  return o != Py_None && s != c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+}
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
 // Output tensor: the given one when it is like q, or a new one.
@@ -181,7 +187,8 @@ PyObject* py_pass(PyObject*, PyObject* const* a, Py_ssize_t n) {
     cudaStream_t stream;
     at::Tensor out, state;
     if (n != 10 || !c.take(a[0], a[1], a[2], a[3], true) || !vcu.take(a[4], 4, "i") || !bcu.take(a[5], 4, "i") ||
-        !par.take(a[6], 4, "i") || par.n != segments(bcu) || !stream_of(a[9], c.dev, &stream))
+        !par.take(a[6], 4, "i") || par.n != segments(bcu) || !stream_of(a[9], c.dev, &stream) ||
+        ((a[7] == Py_None || a[8] == Py_None) && other_stream(a[9], stream, c.dev)))
       return none();
     const int64_t V = segments(vcu);
     if (a[8] != Py_None) {
@@ -212,7 +219,7 @@ PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* kept = n == 9 ? tensor(a[0]) : nullptr;
     if (kept == nullptr || !c.take(a[1], a[2], a[3], a[4], true) || !states_of(*kept, c.dev, c.dims.num_heads) ||
         !bcu.take(a[5], 4, "i") || !par.take(a[6], 4, "i") || par.n != segments(bcu) || !stream_of(a[8], c.dev, &stream) ||
-        !output(a[7], *c.q, c.dev, &out))
+        (a[7] == Py_None && other_stream(a[8], stream, c.dev)) || !output(a[7], *c.q, c.dev, &out))
       return none();
     span_la_status st;
     Py_BEGIN_ALLOW_THREADS
@@ -235,7 +242,7 @@ PyObject* py_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* states = tensor(a[3]);
     if (states == nullptr || !states_of(*states, c.dev, c.dims.num_heads) || !index.take(a[5], 4, "i") ||
         (a[5] != Py_None && (index.n != c.dims.total_rows || index.n == 0)) || !stream_of(a[7], c.dev, &stream) ||
-        !output(a[6], *c.q, c.dev, &out))
+        (a[6] == Py_None && other_stream(a[7], stream, c.dev)) || !output(a[6], *c.q, c.dev, &out))
       return none();
     span_la_status st;
     Py_BEGIN_ALLOW_THREADS
@@ -306,6 +313,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor outs[2];
     if (pos->dim() != 1 || pos->size(0) != T || !contiguous_on(*pos, dev, at::kInt) || !freq.take(a[3], 8, "d") ||
         !PyFloat_Check(a[6]) || !PyBool_Check(a[7]) || !stream_of(a[10], dev, &stream) ||
+        ((a[8] == Py_None || a[9] == Py_None) && other_stream(a[10], stream, dev)) ||
         !side_of(a[0], a[4], a[8], dev, T, dt, &wdt, &sides[0], &outs[0]) ||
         !side_of(a[1], a[5], a[9], dev, T, dt, &wdt, &sides[1], &outs[1]) || freq.n > 32)
       return none();
@@ -413,7 +421,7 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Cache c;
     cudaStream_t stream;
     if (n != 10 || !PyLong_CheckExact(a[5]) || !PyBool_Check(a[8]) || !c.take(a[0], a[1], a[2], a[3], a[4], a[6], a[7]) ||
-        !stream_of(a[9], c.dev, &stream))
+        !stream_of(a[9], c.dev, &stream) || other_stream(a[9], stream, c.dev))
       return none();
     const int64_t T = PyLong_AsLongLong(a[5]);
     if (T < 1 || T > INT32_MAX) {
@@ -452,6 +460,7 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     at::Tensor out;
     if (a[10] == Py_None) {
+      if (other_stream(a[12], stream, c.dev)) return none();
       out = new_tensor(q->sizes(), at::kBFloat16, c.dev);
     } else {
       const at::Tensor* t = tensor(a[10]);

@@ -6,6 +6,10 @@ int32 arrays and passes raw pointers and the current CUDA stream through the C
 ABI declared in ``include/spanla.h``.  PyTorch is used for device memory and
 streams only.  There is no fallback: if the library is missing or cannot be
 loaded, every call raises.
+
+Outputs that a call with ``stream`` makes are that stream's memory, as tensors
+made under ``torch.cuda.stream(stream)`` are; whoever uses them on another
+stream waits for it first, as for any of its results.
 """
 from __future__ import annotations
 
@@ -240,6 +244,22 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _new(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A new output of a call on ``stream``.  On another stream than the current one it is that stream's memory, which no
+    work still pending elsewhere has held, and is not handed out again before the current stream, too, has passed the
+    tensor's last use."""
+    if stream is not None:
+        here = torch.cuda.current_stream(device)
+        if int(stream.cuda_stream) != int(here.cuda_stream):
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+            with torch.cuda.stream(stream):
+                x = torch.empty(shape, dtype=dtype, device=device)
+            x.record_stream(here)
+            return x
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dims_of(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> Dims:
     # The usual case in one expression; anything else goes through the
     # checks below, which name the problem.
@@ -291,9 +311,9 @@ def span_la_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     B = max(len(bcu) - 1, 0)
     H = q.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if view_state_out is None:
-        view_state_out = torch.empty((V, H, 64, 64), dtype=torch.float32, device=q.device)
+        view_state_out = _new((V, H, 64, 64), torch.float32, q.device, stream)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
     if (view_state_out.dtype != torch.float32 or not view_state_out.is_contiguous()
@@ -355,7 +375,7 @@ def span_la_branches_from_state(cached_state: torch.Tensor, q: torch.Tensor, k: 
             or tuple(cached_state.shape[1:]) != (q.shape[1], 64, 64)):
         raise ValueError("cached_state must be contiguous fp32 CUDA [P, H, 64, 64]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
     st = lib.span_la_branches_from_state(cached_state.data_ptr(), cached_state.shape[0],
@@ -380,7 +400,7 @@ def span_la_softmax_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     V = max(len(vcu) - 1, 0)
     B = max(len(bcu) - 1, 0)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda
@@ -415,7 +435,7 @@ def span_la_softmax_branches_from_kv(view_k: torch.Tensor, view_v: torch.Tensor,
     V = max(len(vcu) - 1, 0)
     B = max(len(bcu) - 1, 0)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda
@@ -439,7 +459,7 @@ def _on_device(dev: int, name: str, t: torch.Tensor) -> None:
         raise ValueError("%s must be on the current CUDA device (%d), got %s" % (name, dev, t.device))
 
 
-def _decay_args(q, k, v, log_decay, out) -> Tuple[Dims, torch.Tensor, int]:
+def _decay_args(q, k, v, log_decay, out, stream) -> Tuple[Dims, torch.Tensor, int]:
     """What the decayed calls check alike: q, k, v (as _dims_of), log_decay (may be None here) and out (allocated when
     None).  Returns the dims, out and the current device.  The usual case costs one look at each attribute."""
     dims = _dims_of(q, k, v)
@@ -454,7 +474,7 @@ def _decay_args(q, k, v, log_decay, out) -> Tuple[Dims, torch.Tensor, int]:
             raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
         _on_device(dev, "log_decay", log_decay)
     if out is None:
-        return dims, torch.empty_like(q), dev
+        return dims, _new(q.shape, q.dtype, q.device, stream), dev
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
     _on_device(dev, "out", out)
@@ -492,7 +512,7 @@ def span_la_decay_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     lib = _lib or load_library()
     if log_decay is None:
         raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
-    dims, out, dev = _decay_args(q, k, v, log_decay, out)
+    dims, out, dev = _decay_args(q, k, v, log_decay, out, stream)
     vcu, bcu, par = _i32(view_cu_seqlens), _i32(branch_cu_seqlens), _i32(branch_parent)
     V = max(len(vcu) - 1, 0)
     B = max(len(bcu) - 1, 0)
@@ -500,7 +520,7 @@ def span_la_decay_pass(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
         raise ValueError("one parent per branch")
     H = dims.num_heads
     if view_state_out is None:
-        view_state_out = torch.empty((V, H, 64, 64), dtype=torch.float32, device=q.device)
+        view_state_out = _new((V, H, 64, 64), torch.float32, q.device, stream)
     elif _check_states("view_state_out", view_state_out, H, dev) < V:
         raise ValueError("view_state_out must hold %d states" % V)
     st = lib.span_la_decay_pass(q.data_ptr(), k.data_ptr(), v.data_ptr(), dims, log_decay.data_ptr(), _iptr(vcu), V,
@@ -525,7 +545,7 @@ def span_la_decay_branches_from_state(cached_state: torch.Tensor, q: torch.Tenso
     lib = _lib or load_library()
     if log_decay is None:
         raise ValueError("log_decay must be contiguous fp32 CUDA [H]")
-    dims, out, dev = _decay_args(q, k, v, log_decay, out)
+    dims, out, dev = _decay_args(q, k, v, log_decay, out, stream)
     n = _check_states("cached_state", cached_state, dims.num_heads, dev)
     bcu, par = _i32(branch_cu_seqlens), _i32(branch_parent)
     B = max(len(bcu) - 1, 0)
@@ -554,7 +574,7 @@ def span_la_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, states
                 _raise(_lib, r, "span_la_decay_step")
             return r
     lib = _lib or load_library()
-    dims, out, dev = _decay_args(q, k, v, log_decay, out)
+    dims, out, dev = _decay_args(q, k, v, log_decay, out, stream)
     n = _check_states("states", states, dims.num_heads, dev)
     index = None
     if state_index is not None:
@@ -605,7 +625,7 @@ def _row_stride(name: str, x: torch.Tensor, T: int, H: int) -> int:
 
 
 def _qk_side(name: str, x: torch.Tensor, T: int, weight: Optional[torch.Tensor], out: Optional[torch.Tensor],
-             dev: int) -> Tuple[QkSide, torch.Tensor]:
+             dev: int, stream) -> Tuple[QkSide, torch.Tensor]:
     """The C struct of one side of span_la_qk_norm_rope, and its output."""
     sh = x.shape
     if len(sh) != 3 or sh[2] != 64 or not x.is_cuda:
@@ -613,10 +633,7 @@ def _qk_side(name: str, x: torch.Tensor, T: int, weight: Optional[torch.Tensor],
     _on_device(dev, name, x)
     H = sh[1]
     if out is None:
-        if x.is_contiguous():
-            out = torch.empty_like(x)
-        else:
-            out = torch.empty((T, H, 64), dtype=x.dtype, device=x.device)
+        out = _new((T, H, 64), x.dtype, x.device, stream)
         out_stride = H * 64
     else:
         if out.shape != sh or out.dtype != x.dtype or not out.is_cuda:
@@ -676,8 +693,8 @@ def span_la_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tens
             raise ValueError("q_weight and k_weight must share dtype")
         wdt = _DTYPES[wt]
     dev = _current_device()
-    qs, q_out = _qk_side("q", q, T, q_weight, q_out, dev)
-    ks, k_out = _qk_side("k", k, T, k_weight, k_out, dev)
+    qs, q_out = _qk_side("q", q, T, q_weight, q_out, dev, stream)
+    ks, k_out = _qk_side("k", k, T, k_weight, k_out, dev, stream)
     psh = positions.shape
     if (positions.dtype != torch.int32 or not positions.is_contiguous() or len(psh) != 1 or psh[0] != T
             or not positions.is_cuda):
@@ -824,7 +841,7 @@ def span_la_kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: to
     outs = []
     for name, x in (("k_out", k_out), ("v_out", v_out)):
         if x is None:
-            x = torch.empty((int(total_rows), c.num_heads, 64), dtype=dtype, device=k_pages.device)
+            x = _new((int(total_rows), c.num_heads, 64), dtype, k_pages.device, stream)
         elif (tuple(x.shape) != (int(total_rows), c.num_heads, 64) or x.dtype != dtype or not x.is_cuda or not x.is_contiguous()):
             raise ValueError("%s must be a contiguous CUDA tensor [%d, %d, 64] of %s" % (name, total_rows, c.num_heads, dtype))
         else:
@@ -863,7 +880,7 @@ def span_la_softmax_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
         raise ValueError("q must be bf16, got %s" % q.dtype)
     T, H = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty((T, H, 64), dtype=q.dtype, device=q.device)
+        out = _new((T, H, 64), q.dtype, q.device, stream)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous CUDA tensor like q")
     else:
@@ -962,14 +979,14 @@ class ViewStateCache:
         if ks.size != B:
             raise ValueError("one parent key per branch")
         if log_decay is not None:
-            dims, out, _ = _decay_args(q, k, v, log_decay, out)
+            dims, out, _ = _decay_args(q, k, v, log_decay, out, stream)
             _raise(self._lib, self._lib.span_la_cache_decay_branches(
                 self._live(), ks.ctypes.data if ks.size else None, q.data_ptr(), k.data_ptr(), v.data_ptr(), dims,
                 log_decay.data_ptr(), _iptr(bcu), B, out.data_ptr(), _stream_handle(stream)),
                 "span_la_cache_decay_branches")
             return out
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(q.shape, q.dtype, q.device, stream)
         if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
             raise ValueError("out must be a contiguous CUDA tensor like q")
         _raise(self._lib, self._lib.span_la_cache_branches(
