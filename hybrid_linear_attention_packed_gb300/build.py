@@ -14,6 +14,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -28,6 +29,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspanla.so")
 EXT_SRC = os.path.join(CSRC, "py", "fastcall.cpp")
 EXT = os.path.join(PKG, "_fastcall.so")
+
+# Registers of a thread that a kernel has to be compiled to (its warps share out what a block is launched with).
+REGISTERS = {"k_paged_chunk.cu": {"paged_chunk_kernelILb0E": 168, "paged_chunk_kernelILb1E": 128}}
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -47,6 +51,16 @@ def _sources():
 def _headers():
     return (glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _check_registers(src: str, report: str) -> None:
+    """Refuses an object whose kernels (by a part of their mangled names) have other registers than they need."""
+    want = REGISTERS.get(os.path.basename(src), {})
+    found = re.findall(r"Compiling entry function '(\S+)'.*?Used (\d+) registers", report, re.DOTALL)
+    for part, n in want.items():
+        used = [int(u) for name, u in found if part in name]
+        if not used or any(u != n for u in used):
+            raise RuntimeError("%s: %s has to have %d registers a thread, the compiler gave %s" % (src, part, n, used or "no report"))
 
 
 def _newer(product: str, sources) -> bool:
@@ -118,14 +132,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if not stale and not ext_stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
     def compile_one(src: str):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+        extra = ["-Xptxas", "-v"] if ptxas_verbose or os.path.basename(src) in REGISTERS else []
         cmd = [_nvcc()] + ARCH + COMMON + extra + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
+        _check_registers(src, r.stdout + r.stderr)
         if verbose or ptxas_verbose:
             sys.stderr.write(r.stdout + r.stderr)
         return obj

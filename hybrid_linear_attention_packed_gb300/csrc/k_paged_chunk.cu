@@ -52,7 +52,9 @@ struct Cfg {
   static constexpr int kThreads = kE4m3 ? 512 : 384;
   static constexpr int kStages = kE4m3 ? 3 : 4;
   static constexpr int kRaw = kE4m3 ? 2 : 0;
-  // Registers of a thread, by warps of four: they add up to what the block is launched with.
+  // Registers of a thread, by warps of four: they add up to what the block is launched with, for which the compiler has to
+  // give a thread kRegsLaunch (paged_chunk_registers, and the build, see that it did: with fewer, a warp would wait for its
+  // share for ever).
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
   static constexpr int kRegsFew = 56, kRegsConvert = 88, kRegsSoftmax = kE4m3 ? 184 : 224;
   static_assert((kRegsFew + 2 * kRegsSoftmax + (kE4m3 ? kRegsConvert : 0)) * 128 <= kRegsLaunch * kThreads, "registers");
@@ -870,20 +872,31 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
                    int ns, int grid, float* ws, cudaStream_t stream) {
   using C = Cfg<kE4m3>;
   static std::atomic<uint64_t> done{0};
-  static std::atomic<int> regs{0};
-  if (regs.load(std::memory_order_relaxed) == 0) {   // the warps' shares of registers have to be those of the launch
-    cudaFuncAttributes attr;
-    const cudaError_t e = cudaFuncGetAttributes(&attr, paged_chunk_kernel<kE4m3, kWhole>);
-    if (e != cudaSuccess) return e;
-    regs.store(attr.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
   const cudaError_t e = set_smem_limit_once(paged_chunk_kernel<kE4m3, kWhole>, C::kRequest, done);
   if (e != cudaSuccess) return e;
   return launch_behind(paged_chunk_kernel<kE4m3, kWhole>, dim3(grid), C::kThreads, C::kRequest, stream, tm_q, tm_k, tm_v, a, p, s0, ns, ws);
 }
 
 }  // namespace
+
+cudaError_t paged_chunk_registers(int* built, int* needed) {
+  static std::atomic<int> found{0};   // built, less what is needed, plus 1024 (0: not asked yet); the scarcest kernel's
+  int least = found.load(std::memory_order_relaxed);
+  if (least == 0) {
+    cudaFuncAttributes attr[4];
+    cudaError_t e = cudaFuncGetAttributes(&attr[0], paged_chunk_kernel<false, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr[1], paged_chunk_kernel<false, true>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr[2], paged_chunk_kernel<true, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr[3], paged_chunk_kernel<true, true>);
+    if (e != cudaSuccess) return e;
+    least = 1024 + std::min(std::min(attr[0].numRegs, attr[1].numRegs) - Cfg<false>::kRegsLaunch,
+                            std::min(attr[2].numRegs, attr[3].numRegs) - Cfg<true>::kRegsLaunch);
+    found.store(least, std::memory_order_relaxed);
+  }
+  *needed = Cfg<false>::kRegsLaunch;
+  *built = *needed + least - 1024;
+  return cudaSuccess;
+}
 
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
                                const PagedAttn& p, int s0, int ns, int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream) {

@@ -2236,6 +2236,14 @@ span_la_status run_paged(const KvArgs& a, const PagedAttn& p, int64_t sure, bool
   const PagedGrids grids = paged_grids(a.rows, a.capacity, a.heads, a.seqs, a.max_rows, sure, p.group, e4m3, num_sms);
   const int unit = grids.unit, step_grid = grids.step, chunk_grid = grids.chunk;
   const bool step = step_grid > 0, chunk = chunk_grid > 0;
+  if (chunk) {
+    int built = 0, needed = 0;
+    const cudaError_t er = paged_chunk_registers(&built, &needed);
+    if (er != cudaSuccess) return cuda_fail(er, "cudaFuncGetAttributes");
+    if (built < needed)
+      return fail(SPAN_LA_ERR_UNSUPPORTED, "the library was built with %d registers for a thread of the chunk kernel, which needs %d", built,
+                  needed);
+  }
   const size_t bytes = grids.bytes;
   float* ws = static_cast<float*>(workspace);
   cudaError_t e = cudaSuccess;

@@ -486,6 +486,8 @@ struct alignas(16) ChunkRedo {   // of each softmax warp, behind the join's reco
 };
 constexpr int kChunkSoftmaxWarps = 8;
 constexpr int64_t kChunkWsFloats = 4 * kChunkPartFloats + 8 + 8 * kChunkSoftmaxWarps;
+// What the compiler gave a thread of the chunk kernel, and what its warps' shares need; calls are refused where it is less.
+cudaError_t paged_chunk_registers(int* built, int* needed);
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const KvArgs& a,
                                const PagedAttn& p, int s0, int ns, int grid, bool e4m3, bool whole_items, float* ws, cudaStream_t stream);
 // step, step_grid (0: none), ...: joins the step kernel's parts of the same call too.

@@ -92,3 +92,21 @@ def test_extension_is_used_with_the_torch_it_was_built_for_only():
     """
     assert _child(load % "") == "True"
     assert _child(load % "torch.__version__ = '0.0.1+other'") == "False"
+
+
+REPORT = """ptxas info    : Compiling entry function '_ZN6spanla18paged_chunk_kernelILb0ELb%dEEEv' for 'sm_103a'
+ptxas info    : Function properties for _ZN6spanla18paged_chunk_kernelILb0ELb%dEEEv
+    48 bytes stack frame, 388 bytes spill stores, 540 bytes spill loads
+ptxas info    : Used %d registers, used 1 barriers
+"""
+
+
+def test_registers_of_the_chunk_kernel_are_checked_by_the_build():
+    """Its warps share out the block's registers: with fewer than they ask for one would wait for ever."""
+    other = REPORT.replace("ILb0E", "ILb1E")
+    good = REPORT % (0, 0, 168) + REPORT % (1, 1, 168) + other % (0, 0, 128) + other % (1, 1, 128)
+    spanla_build._check_registers("csrc/k_paged_chunk.cu", good)
+    spanla_build._check_registers("csrc/k_scan.cu", "")
+    for bad in (good.replace("Used 128", "Used 120"), good.replace("Used 168 registers", "Used 160 registers", 1), REPORT % (0, 0, 168), ""):
+        with pytest.raises(RuntimeError, match="registers a thread"):
+            spanla_build._check_registers("csrc/k_paged_chunk.cu", bad)
