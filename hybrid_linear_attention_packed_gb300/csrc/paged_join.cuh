@@ -101,6 +101,7 @@ __device__ __forceinline__ void join_step_parts(const KvArgs& a, const PagedAttn
   const int mh = j.n * p.group;
   if (j.parts == 0 || kJoinRows * y >= mh) return;
   if (tid == 0) wild = 0;
+  static_assert(kJoinRows * 16 % 32 == 0, "whole warps have slice 0, as the shuffles below need");
   if (slice == 0) {
     float m = -INFINITY, M = -INFINITY, l = 0.f;
 #pragma unroll
