@@ -2055,9 +2055,9 @@ bool rows_meet(const Axis (&axes)[3], int64_t width, int64_t d, int level = 2) {
   return false;
 }
 
-// What every call on a paged cache checks of it, and its kernels' arguments; `written`: its pages are.
-span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t max_rows, bool written, KvArgs* a,
-                              Ranges* pages, Ranges* metadata) {
+// Types and sizes of a paged cache.
+span_la_status check_kv_sizes(const span_la_kv_cache* c, int64_t rows) {
+  constexpr int64_t kMostCached = int64_t(1) << 30;   // rows of a sequence (the kernels round up to blocks in 32 bits)
   if (c == nullptr) return fail(SPAN_LA_ERR_INVALID, "cache is NULL");
   if (c->dtype != SPAN_LA_BF16 && c->dtype != SPAN_LA_E4M3)
     return fail(SPAN_LA_ERR_UNSUPPORTED, "cache dtype %d not supported", c->dtype);
@@ -2069,11 +2069,27 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
   if (c->num_seqs < 0) return fail(SPAN_LA_ERR_INVALID, "num_seqs %d < 0", c->num_seqs);
   if (c->row_cu == nullptr && rows != c->num_seqs)
     return fail(SPAN_LA_ERR_INVALID, "%lld rows without row_cu need as many sequences, got %d", (long long)rows, c->num_seqs);
+  if (c->table_width < 0 || static_cast<int64_t>(c->table_width) * c->page_rows > kMostCached)
+    return fail(SPAN_LA_ERR_INVALID, "table_width %d pages of %d rows are not in [0, 2^30] rows", c->table_width, c->page_rows);
+  return SPAN_LA_OK;
+}
+
+// The query heads of a call over it.
+span_la_status check_q_heads(const span_la_kv_cache* c, int32_t num_q_heads) {
+  if (num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % c->num_heads != 0 || num_q_heads / c->num_heads > 128)
+    return fail(SPAN_LA_ERR_INVALID, "num_q_heads %d is not a multiple of %d heads, at most 128 times it", num_q_heads, c->num_heads);
+  return SPAN_LA_OK;
+}
+
+// What every call on a paged cache checks of it, and its kernels' arguments; `written`: its pages are.
+span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t max_rows, bool written, KvArgs* a,
+                              Ranges* pages, Ranges* metadata) {
+  const span_la_status sizes = check_kv_sizes(c, rows);
+  if (sizes != SPAN_LA_OK) return sizes;
   const bool e4m3 = c->dtype == SPAN_LA_E4M3;
   const int64_t esz = e4m3 ? 1 : 2;
   if (c->k == nullptr || c->v == nullptr || !aligned16(c->k) || !aligned16(c->v))
     return fail(SPAN_LA_ERR_INVALID, "k and v pages must be non-NULL and 16-byte aligned");
-  constexpr int64_t kMostCached = int64_t(1) << 30;   // rows of a sequence (the kernels round up to blocks in 32 bits)
   constexpr int64_t kMost = int64_t(1) << 39;   // elements that an axis spans (the tensor maps' limit; no overflow below)
   auto behind = [](const void* x, const void* y) {
     return static_cast<int64_t>(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x));
@@ -2103,8 +2119,6 @@ span_la_status check_kv_cache(const span_la_kv_cache* c, int64_t rows, int64_t m
   // (pages of K and V may be interleaved: what meets is looked for row by row)
   if (written && rows_meet(axes, kHeadDim, behind(c->k, c->v) / esz))
     return fail(SPAN_LA_ERR_INVALID, "k pages overlap v pages");
-  if (c->table_width < 0 || static_cast<int64_t>(c->table_width) * c->page_rows > kMostCached)
-    return fail(SPAN_LA_ERR_INVALID, "table_width %d pages of %d rows are not in [0, 2^30] rows", c->table_width, c->page_rows);
   if (c->num_seqs > 0) {
     auto word = [](const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
     if (c->table_width > 0 && !word(c->page_table)) return fail(SPAN_LA_ERR_INVALID, "page_table must be non-NULL and 4-byte aligned");
@@ -3068,8 +3082,7 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     Ranges pages, metadata;
     span_la_status st = check_kv_cache(cache, rows, most_rows(cache, rows, max_rows), false, &a, &pages, &metadata);
     if (st != SPAN_LA_OK) return st;
-    if (num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % a.heads != 0 || num_q_heads / a.heads > 128)
-      return fail(SPAN_LA_ERR_INVALID, "num_q_heads %d is not a multiple of %d heads, at most 128 times it", num_q_heads, a.heads);
+    if ((st = check_q_heads(cache, num_q_heads)) != SPAN_LA_OK) return st;
     if (rows == 0 || a.seqs == 0) return SPAN_LA_OK;
     const int64_t width = static_cast<int64_t>(num_q_heads) * kHeadDim;
     if ((st = check_rows("q", q, q_row_stride, rows, num_q_heads, 2)) != SPAN_LA_OK) return st;
@@ -3105,8 +3118,8 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
 }
 
 int64_t span_la_softmax_paged_workspace(int64_t rows, int32_t num_q_heads, const span_la_kv_cache* cache, int32_t max_rows) {
-  if (cache == nullptr || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 || num_q_heads / cache->num_heads > 128 ||
-      rows < 1 || cache->num_seqs < 1 || max_rows < 0)
+  if (max_rows < 0 || check_kv_sizes(cache, rows) != SPAN_LA_OK || check_q_heads(cache, num_q_heads) != SPAN_LA_OK || rows == 0 ||
+      cache->num_seqs == 0)
     return 0;
   return static_cast<int64_t>(paged_grids(rows, static_cast<int64_t>(cache->table_width) * cache->page_rows, cache->num_heads, cache->num_seqs,
                                           most_rows(cache, rows, max_rows), sure_rows(cache, rows, max_rows), num_q_heads / cache->num_heads,

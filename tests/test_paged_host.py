@@ -164,6 +164,18 @@ def test_workspace(lib):
     assert f(0, 4, _cache(), 1) == 0 and f(3, 5, _cache(), 1) == 0 and f(3, 4, None, 1) == 0 and f(3, 4, _cache(num_seqs=0), 1) == 0
 
 
+@pytest.mark.parametrize("kw,rows,heads,max_rows", [
+    (dict(page_rows=48), 3, 4, 100), (dict(page_rows=0), 3, 4, 100), (dict(page_rows=1 << 20, table_width=1 << 20), 3, 4, 100),
+    (dict(dtype=7), 3, 4, 100), (dict(dtype=1), 3, 4, 1), (dict(table_width=-1), 3, 4, 100), (dict(table_width=1 << 30), 3, 4, 100),
+    (dict(num_pages=0), 3, 4, 100), (dict(num_heads=70000), 3, 70000, 100), (dict(num_seqs=-3), 3, 4, 100), (dict(row_cu=None), 4, 4, 0),
+    (dict(num_heads=40000), 3, 80000, 100), (dict(), 1 << 31, 4, 0), (dict(), -1, 4, 0), (dict(), 3, 4, -1), (dict(), 3, 5, 100),
+])
+def test_workspace_of_what_a_call_refuses_is_nothing(lib, kw, rows, heads, max_rows):
+    c = _cache(**{"table_width": 4000, "table_stride": 1 << 30, **kw})
+    assert lib.span_la_softmax_paged(Q, heads * 64, rows, heads, c, max_rows, 0.0, OUT, None, None, None) in (INVALID, UNSUPPORTED)
+    assert lib.span_la_softmax_paged_workspace(rows, heads, c, max_rows) == 0
+
+
 def test_workspace_for_expanded_pages(lib):
     """Copies of e4m3 pages where some sequence has 2,048 row heads: the caller says so, or there are as many on average."""
     f = lib.span_la_softmax_paged_workspace
