@@ -322,7 +322,6 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   }
 
   // ---------------------------------------------------------------- units
-  const float c2 = p.scale * 1.4426950408889634f;
   uint32_t qa[4][4];                  // Q fragments of the item
   float qc[kR];                       // what turns a score of row g, g + 8 into powers of two
   float o[8][4], m[kR], M[kR], l[kR];
@@ -379,9 +378,9 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             qa[c][i] = half2_of(x[0], x[1]);
             qa[c][2 + i] = half2_of(x[2], x[3]);
           }
-          qc[i] = c2 * (1.f / 16384.f) * __uint_as_float(static_cast<uint32_t>(e) << 23);
+          qc[i] = p.q_unit * __uint_as_float(static_cast<uint32_t>(e) << 23);   // (and p.k_unit goes to the keys' factors)
         } else {
-          qc[i] = c2;
+          qc[i] = p.scale * 1.4426950408889634f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             qa[c][i] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * c + 2 * t) : 0u;
@@ -427,7 +426,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const uint32_t v = sc[kUnit];
         const int in4 = lane & 3, second = in4 >> 1;
         float* to = factors + ((lane + 32 * k) >> 3) * 16 + (((lane >> 2) & 1) * 2 + (second ? 3 - in4 : in4)) * 4 + second;
-        to[0] = scale_of(sc[0]);
+        to[0] = scale_of(sc[0]) * p.k_unit;
         to[2] = v == 255 ? NAN : static_cast<float>(static_cast<int>(v) - 127);
       }
     }

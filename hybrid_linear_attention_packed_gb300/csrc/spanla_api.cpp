@@ -2243,6 +2243,16 @@ PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t se
   return g;
 }
 
+// q_unit and k_unit = 2^-s: rows' powers of two are 2^-126 to 2^127 for queries and 2^-126 to 2^119 for keys, and their
+// products with the units shall have all their bits.  Of the keys' so do those with s up to 23; with s = 17 (scale 0.125)
+// the queries' too.  Less where the scale is greater, as q_unit 2^127 is to stay a number.
+void paged_units(PagedAttn* p) {
+  const float c2 = p->scale * 1.4426950408889634f;
+  const int s = std::min(17, std::max(0, 14 - std::ilogb(c2)));
+  p->k_unit = std::ldexp(1.f, -s);
+  p->q_unit = std::ldexp(c2, s - 14);
+}
+
 span_la_status run_paged(const KvArgs& a, const PagedAttn& p, int64_t sure, bool e4m3, int num_sms, void* workspace,
                          cudaStream_t stream) {
   span_la_status st = SPAN_LA_OK;
@@ -3113,6 +3123,7 @@ span_la_status span_la_softmax_paged(const void* q, int64_t q_row_stride, int64_
     p.heads = num_q_heads;
     p.group = num_q_heads / a.heads;
     p.scale = scale == 0.f ? 0.125f : scale;
+    paged_units(&p);
     return run_paged(a, p, sure_rows(cache, rows, max_rows), cache->dtype == SPAN_LA_E4M3, dev->num_sms, workspace, stream);
   });
 }

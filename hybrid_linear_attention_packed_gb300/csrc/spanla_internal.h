@@ -449,6 +449,9 @@ struct PagedAttn {
   int32_t heads;              // query heads; head h reads key head h / group
   int32_t group;
   float scale;
+  // The step kernel over e4m3 pages: scale log2(e) 2^-14 = q_unit k_unit, of which a query's power of two is multiplied by
+  // the one and a cached row's by the other.
+  float q_unit, k_unit;
 };
 // Sequences of at most kStepHeads packed row heads (rows * group) of a key head (k_paged_step.cu), at most kStepSeqs in
 // a launch: [s0, s0 + ns).  `ws`: kStepWsFloats for each of the `grid` CTAs; the join kernel, with the same grid, follows

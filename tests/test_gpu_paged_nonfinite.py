@@ -1,4 +1,4 @@
-"""Attention over the paged cache with NaN and infinities in queries, keys and values."""
+"""Attention over the paged cache with NaN and infinities in queries, keys and values, and numbers next to them."""
 import numpy as np
 import pytest
 import torch
@@ -262,3 +262,15 @@ def test_what_an_infinity_in_v_costs(cuda_device, cache):
     same[5] = False
     assert torch.equal(out[..., same], clean[..., same]) and not torch.isfinite(out[..., 5].float()).any()
     assert min(ms) < 60, ms
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 4, 8, 70])
+@pytest.mark.parametrize("q_size,k_size,scale", [(1e-37, 1e37, 0.125), (2e-38, 4e37, 0.25), (1.0, 1e36, 1e-37), (1e-10, 3e37, 4e-28)])
+def test_small_queries_and_scales(cuda_device, q_size, k_size, scale, rows, cache):
+    """Queries, or a scale, next to the least fp32 numbers, and keys next to the greatest: scores of ordinary sizes."""
+    lens = [400, 70]
+    q, c, table, cu = _setup(lens, [rows, rows], 2, 2, 64, cache, cuda_device, seed=40, q_size=q_size, k_size=k_size)
+    out, lse = _run(q, c, table, lens, cu, cuda_device, scale=scale)
+    assert f64(lse).max() > 1 and f64(out).std() > 0.1
+    check_attention(q, out, lse, c, table, lens, cu, scale, weights(2, cache))
