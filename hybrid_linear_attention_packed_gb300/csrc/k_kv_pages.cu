@@ -13,10 +13,12 @@
 // at a time, 8 lanes a row (16 bytes of bf16 a lane), 4 rows at once, all 16 in
 // flight.  Consecutive rows of one head are neighbours in a page, and their powers
 // of two go out as one store.  (All 32 rows at once: twice the registers and half
-// the warps, 45 us for four prompts of fp32 rows instead of 40.)  Few rows are bound
+// the warps, 45 us for four prompts of fp32 rows where 16 took 40, before launches
+// overlapped.)  Few rows are bound
 // by the reads that find their places, one behind the other: lengths, then the
 // page; the rows themselves are on their way meanwhile.  Measured: four prompts of
-// fp32 rows (20,576 rows, 16 heads) into e4m3 pages 36.6 us, 5.8 TB/s; sixteen views
+// fp32 rows (20,576 rows, 16 heads) into e4m3 pages 36.6 us, 5.8 TB/s (35.3 one call
+// behind the other); sixteen views
 // (87,648 rows) out of bf16 pages 109.5 us, 6.6 TB/s; eight tokens written 2.7 us.
 #include <algorithm>
 
@@ -334,8 +336,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_expand_kernel(const __grid_con
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, const KvArgs& a, const KvRows& x, cudaStream_t stream) {
   // A CTA takes several heads of its rows where there are CTAs enough: finding the rows' places takes as long as copying a
-  // few heads.  (Sixteen views read from e4m3 pages: all heads 94 us, with 32 CTAs an SM 91, one head a warp 98; four
-  // prompts written: 49, 40, 39.)
+  // few heads.  (In a graph, all heads, with 32 CTAs an SM, one head a warp: sixteen views out of bf16 pages 111.6, 109.1
+  // and 110.5 us, out of e4m3 pages 88.4, 86.4 and 85.0; one view 8.8, 7.1, 7.1; four prompts written 44.0, 35.3, 35.2.)
   const int64_t blocks = (a.rows + kRows - 1) / kRows;
   const int64_t eights = (4 * a.heads + kWarps - 1) / kWarps;
   const int64_t turns = std::max<int64_t>(1, eights * blocks / kBlocks), split = (eights + turns - 1) / turns;

@@ -21,7 +21,7 @@
 // memory.  An item that goes over several CTAs leaves its parts (m, l, O) in the
 // workspace for the join kernel, which starts behind this one.
 //
-// Measured: 2,048 rows behind 18,000 of 4 key heads of 4, bf16 pages, 167 us, 0.50
+// Measured: 2,048 rows behind 18,000 of 4 key heads of 4, bf16 pages, 169 us, 0.49
 // of cuBLAS's rate; 512 rows behind 7,400 of 16 heads 33 us with the launches beside
 // it.  A block of two tiles takes 2,450 cycles, of which the products are 1,790: the
 // rest is softmax (without exponentials and maxima 131 us) and hand-offs between

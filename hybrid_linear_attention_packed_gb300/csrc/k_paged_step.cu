@@ -13,7 +13,7 @@
 //
 // A unit: S = Q K^T (m16n8k16, the row heads as M), running maximum m and sum l of
 // each row head in registers, O += P V.  bf16 pages: P enters as two bf16 parts
-// (hi + lo, 2^-17 of it), the M = 16 products being free beside the loads.  e4m3
+// (hi + lo, 2^-16 of it), the M = 16 products being free beside the loads.  e4m3
 // pages: q, K and V enter as fp16 (K and V exactly, q scaled by a power of two
 // for its row, then all but its least elements), the rows' powers of two go onto
 // the scores and the weights in fp32; the weights w_j = p_j 2^(e_j) have a running
@@ -27,7 +27,7 @@
 //
 // Measured (with the join, one call behind the other): 128 tokens of up to 18,000
 // rows over bf16 pages, 8 key heads of 4, 222 us, 6.8 TB/s, as fast as a copy; 61
-// over e4m3 pages, 16 heads, 115.5 us, 5.4 TB/s (a warp takes 790 instructions for
+// over e4m3 pages, 16 heads, 117 us, 5.4 TB/s (a warp takes 790 instructions for
 // 64 rows of e4m3, and the chains of eleven warps leave half of the SM's issue slots
 // empty).  One token of one sequence, 7,401 rows, 16 heads, 11.4 us, of which the
 // data are 4.5: the lengths are there after 1.0, the first unit's data after 2.9,

@@ -2213,7 +2213,8 @@ struct PagedGrids {
 // From this many row heads of a sequence and key head on, and up to this many bytes of copies, e4m3 pages are expanded to
 // bf16 ahead of the chunk kernel: it converts a block for every 256 row heads that see it, next to a softmax that needs
 // the issue slots.  (20,000 rows, four key heads, one sequence, expanded and not: 8,192 row heads 179 us and 207, 2,048 66
-// and 69, 1,024 47.4 and 46.3.)
+// and 69, 1,024 47.4 and 46.3.  Eight of 2,048 over 2,000 rows 59 and 65, over 6,000 128 and 142; two of 8,192 over 8,000 137
+// and 163; one of 2,048 over 4,000 beside 15 single tokens 44.0 and 40.4.)
 constexpr int64_t kExpandRowHeads = 2048;
 constexpr size_t kExpandBytes = size_t(128) << 20;
 constexpr int64_t kWholeBlocks = 4, kWholeItems = 128;
@@ -2226,12 +2227,13 @@ PagedGrids paged_grids(int64_t rows, int64_t capacity, int64_t heads, int64_t se
   // Tables of a few units (512 rows of bf16 pages, 1,024 of e4m3): a CTA's eight warps are enough for a sequence and head, and
   // there is nothing to join, nor a second launch.  (One token over 500 rows of bf16, 16 heads: 6.9 us, with joins 7.6; 61
   // tokens 19.8 and 21.0; over 1,000 rows 9.4 and 8.0, 61 tokens 34.9 and 35.0; two key heads of 8, 2,000 rows of e4m3 12.6
-  // and 9.9.)
+  // and 9.9.  e4m3, 1,000 rows: one token 9.9 and 10.3, 61 tokens 26.9 and 26.7, 24 x 4 of 4 key heads of 4 10.6 and 11.2.)
+  // By the table's width, as the lengths are not known here and the launches are chosen here.
   g.whole = units <= 16;
   g.chunk = max_rows * group > kStepHeads ? std::min(num_sms, kStepMaxGrid) : 0;
   // The same for chunks over tables of up to 512 rows, where there are no more items than CTAs (on a smaller GPU too: the
   // workspace is asked for without one).  (4 key heads of 2, bf16, eight sequences with 60 new rows of 100: 9.5 us, cut
-  // and joined 13.1; of 500: 12.6 and 14.9; one with 200 of 500: 15.4 and 14.9, from the host 15.7 and 15.8.)
+  // and joined 13.1; of 500: 12.1 and 14.6; one with 200 of 500: 14.7 and 15.3.)
   const int64_t item_rows = 2 * (kTileRows / group);
   g.chunk_whole = capacity <= kWholeBlocks * kTileRows && heads * (rows / item_rows + std::min<int64_t>(seqs, rows)) <= kWholeItems;
   g.step_ws = align256(static_cast<size_t>(g.step > 0 && !g.whole ? g.step : 0) * kStepWsFloats * sizeof(float));

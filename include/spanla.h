@@ -632,8 +632,9 @@ typedef struct {
  *                    SPAN_LA_F32), 16-byte aligned; rows k_row_stride and
  *                    v_row_stride elements apart (multiples of 16 bytes: parts
  *                    of a fused projection's rows)
- *   cache            a row of a page that two packed rows name gets either's
- *                    values; pages and scales overlap nothing else of the call
+ *   cache            a row of a page that two packed rows name holds some mixture
+ *                    of both (their values where they are the same); pages and
+ *                    scales overlap nothing else of the call
  * fp32 rows into bf16 pages are rounded to nearest even.
  */
 span_la_status span_la_kv_write(const void *k, const void *v, int64_t k_row_stride, int64_t v_row_stride,
@@ -664,18 +665,37 @@ span_la_status span_la_kv_read(const span_la_kv_cache *cache, int64_t rows, int3
  *                    q_row_stride elements apart (a multiple of 16 bytes)
  *   num_q_heads      a multiple of the cache's num_heads, at most 128 times it
  *   max_rows         the most packed rows of a sequence, or 0: not known (a small
- *                    one saves the launch for long chunks)
+ *                    one saves the launch for long chunks, a large one has E4M3
+ *                    pages expanded, see workspace)
  *   scale            > 0, or 0 for 1/sqrt(64)
  *   out              device bf16 [rows][num_q_heads][64], 16-byte aligned
  *   lse_out          device fp32 [rows][num_q_heads] or NULL
  *   workspace        device memory of span_la_softmax_paged_workspace() bytes
- *                    (up to 24 MB; 158 where 2,048 row heads and more may share
- *                    E4M3 pages, which are then expanded into it), 16-byte
+ *                    (up to 24 MB; up to 158 where E4M3 pages are expanded into it:
+ *                    where max_rows, or without it rows / num_seqs, says that some
+ *                    sequence has 2,048 row heads a key head and more), 16-byte
  *                    aligned, for this call alone until the stream has passed it;
  *                    or NULL: allocated and freed on the stream (2 us of it)
  * A row that sees nothing (or nothing but scores of -infinity) gets o = 0 and
- * lse = -infinity.  What a row does not see does not reach it, whatever it holds.
- * Scores, sums and o are fp32; out is rounded to bf16.  Deterministic.
+ * lse = -infinity; one with a score of NaN or +infinity is NaN.  What a row does
+ * not see does not reach it, whatever it holds.  An infinity or a NaN in V, with a
+ * score above -infinity, counts however small its weight; it makes a call longer,
+ * by up to some hundred times (1,280 rows and 64 heads over 21,280 rows, 0.45 ms:
+ * 25 ms where all rows see one infinity, 93 ms where one lies in the last row and
+ * its block's other rows are looked at once more).
+ *
+ * Scores, sums of weights and o are fp32; out is rounded to bf16.  The weights that
+ * multiply V are rounded: to bf16 (2^-8 of each) in sequences with more than 16 row
+ * heads (packed rows times query heads of a key head); with fewer to a sum of two
+ * bf16 numbers (2^-16) over bf16 pages, and over E4M3 pages to fp16, relative to the
+ * largest product of a weight and its row's power of two (2^-11 of each, or 2^-40 of
+ * that largest; elements of q then count to 2^-39 of their row's largest).  The same
+ * call gives the same bits; the last ones of a row may depend on the rest of the
+ * call (lengths, table_width and max_rows say how sums are cut).
+ *
+ * Where table_width * page_rows is at most 512 rows (E4M3 pages, single and drafted
+ * tokens: 1,024), a call needs one launch less, 0.5 to 3 us: a program with short
+ * sequences names just the columns of a wide table that they need (table_stride).
  */
 span_la_status span_la_softmax_paged(const void *q, int64_t q_row_stride, int64_t rows, int32_t num_q_heads,
                                      const span_la_kv_cache *cache, int32_t max_rows, float scale,
