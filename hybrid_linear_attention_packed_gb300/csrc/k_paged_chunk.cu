@@ -743,10 +743,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // eighth part.  What an item of two parts needs is asked for before the record is there that says how many there are.
 constexpr int kChunkJoinThreads = 256, kJoinWarps = kChunkJoinThreads / 32;
 
-// A CTA: the rows that a softmax warp (x, quarter) has marked, in items from the first to the last that it names.
+// A warp: the rows that a softmax warp (x, quarter) has marked, in items from the first to the last that it names.
 template <bool kE4m3>
 __device__ __forceinline__ void redo_chunk_items(const KvArgs& a, const PagedAttn& p, const ChunkRedo& redo, int x, int quarter) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = quarter * 32 + 4 * warp + (lane >> 3);
+  const int lane = threadIdx.x & 31;
   const int32_t tile_rows = kTileRows / p.group;
   int32_t h = redo.h, b = redo.b;
   for (int32_t s = redo.s; s <= redo.last_s; ++s, h = b = 0) {
@@ -758,16 +758,20 @@ __device__ __forceinline__ void redo_chunk_items(const KvArgs& a, const PagedAtt
     for (; h <= last_h; ++h, b = 0) {
       const int32_t last_b = s == redo.last_s && h == last_h ? redo.last_b : items - 1;
       for (; b <= last_b; ++b) {
-        const int32_t first = (2 * b + x) * tile_rows, in = first + row / p.group;
-        bool mark = false;
-        if (row / p.group < tile_rows && in < r.n) {
-          const uint4 o = *reinterpret_cast<const uint4*>(p.out + ((r.row0 + in) * p.heads + h * p.group + row % p.group) * kHeadDim + 8 * (lane & 7));
-          mark = has_mark(o.x) || has_mark(o.y) || has_mark(o.z) || has_mark(o.w);
-        }
-        const uint32_t lanes = __ballot_sync(0xffffffffu, mark);
+        const int32_t first = (2 * b + x) * tile_rows;
         uint32_t which = 0;
-        for (int g = 0; g < 4; ++g)
-          if ((lanes >> (8 * g)) & 0xffu) which |= 1u << (4 * warp + g);
+        for (int i = 0; i < 32; i += 4) {
+          const int row = quarter * 32 + i + (lane >> 3), in = first + row / p.group;
+          bool mark = false;
+          if (row / p.group < tile_rows && in < r.n) {
+            const uint4 o =
+                *reinterpret_cast<const uint4*>(p.out + ((r.row0 + in) * p.heads + h * p.group + row % p.group) * kHeadDim + 8 * (lane & 7));
+            mark = has_mark(o.x) || has_mark(o.y) || has_mark(o.z) || has_mark(o.w);
+          }
+          const uint32_t lanes = __ballot_sync(0xffffffffu, mark);
+          for (int g = 0; g < 4; ++g)
+            if ((lanes >> (8 * g)) & 0xffu) which |= 1u << (i + g);
+        }
         if (which != 0) redo_rows<kE4m3>(a, p, which, s, h, r.row0 + first, quarter * 32, r.len - r.n + first + 1);
       }
     }
@@ -789,12 +793,10 @@ chunk_join_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ Page
   if (blockIdx.y >= 8) {
     const int y = static_cast<int>(blockIdx.y) - 8, steps = kM / kJoinRows;
     if (blockIdx.y == gridDim.y - 1) {
-      const ChunkRedo* redo = reinterpret_cast<const ChunkRedo*>(mine + 4 * kPartFloats + 8);
-      uint32_t some = __ballot_sync(0xffffffffu, redo[threadIdx.x & (kChunkSoftmaxWarps - 1)].some != 0) & ((1u << kChunkSoftmaxWarps) - 1u);
-      for (; some != 0; some &= some - 1) {
-        const int w = __ffs(some) - 1;
-        redo_chunk_items<kE4m3>(a, p, redo[w], w >> 2, w & 3);
-      }
+      const int w = static_cast<int>(threadIdx.x) >> 5;   // a warp for each softmax warp
+      static_assert(kJoinWarps == kChunkSoftmaxWarps, "warps");
+      const ChunkRedo* redo = reinterpret_cast<const ChunkRedo*>(mine + 4 * kPartFloats + 8) + w;
+      if (redo->some != 0) redo_chunk_items<kE4m3>(a, p, *redo, w >> 2, w & 3);
     } else if (static_cast<int>(blockIdx.x) < step_grid) {
       if (y < steps) join_step_parts<kStepE4m3, kChunkJoinThreads / 16 / kJoinRows>(step, p, step_ws, step_grid, y);
       else redo_step_items<kStepE4m3>(step, p, step_ws);

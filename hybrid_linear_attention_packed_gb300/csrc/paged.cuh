@@ -174,7 +174,8 @@ __device__ __forceinline__ float dot64(const EightOf<false>& q, const EightOf<kE
 // elements a lane.
 //
 // First, what is not finite in the rows of V that they see, and has a score above -infinity: the sum of that is the answer,
-// however small its weight.  (Looked for 16 rows at a time; most calls end here.)  Where there is none, the rest:
+// however small its weight.  (The first 17 to 32 such rows are looked for once for all row heads, 16 rows at a time, more of
+// them by each four; most calls end here.)  Where there is none, the rest:
 //
 //   l' = l e^(m - m') + sum w,   o' = o l e^(m - m') / l' + sum w / l' v,   w = e^(x - m')
 //
@@ -187,6 +188,34 @@ __device__ __noinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, uint
   auto scale_at = [&](const uint8_t* scales, int32_t page, int32_t in) {
     return kE4m3 ? scale_of(scales[page * a.scale_page_stride + kvh * a.scale_head_stride + in]) : 1.f;
   };
+  // Of the 16 rows from j on, those below `end` with anything in V that is not finite (bits).
+  auto scan = [&](int32_t page, int32_t j, int32_t end) {
+    const int32_t in = (j & (a.page_rows - 1)) + (lane >> 3);
+    EightOf<kE4m3> v[kScan / 4];
+#pragma unroll
+    for (int i = 0; i < kScan / 4; ++i) v[i].load(a.v, page * a.page_stride + kvh * a.head_stride + 8 * part + (in + 4 * i) * a.row_stride);
+    uint32_t rows = 0;
+#pragma unroll
+    for (int i = 0; i < kScan / 4; ++i) {
+      const bool found = !v[i].finite() || (kE4m3 && !(scale_at(a.v_scale, page, in + 4 * i) < INFINITY));
+      const uint32_t b = __ballot_sync(0xffffffffu, found && j + (lane >> 3) + 4 * i < end);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) rows |= (b >> (8 * g)) & 0xffu ? 1u << (4 * i + g) : 0u;
+    }
+    return rows;
+  };
+  int listed = 0;              // lane i has the i-th such row
+  int32_t list = 0, next = 0;  // rows before `next` have been looked at
+  const int32_t last = which != 0 ? max(0, seen0 + (base + 31 - __clz(which)) / p.group) : 0;   // rows that any of them sees
+  for (int32_t page = -1; next < last && listed <= 32 - kScan; next += kScan) {
+    if ((next & (a.page_rows - 1)) == 0) {
+      page = page_of(a, s, next);
+      if (page < 0) atomicOr(a.err, kErrPage);
+    }
+    if (page < 0) continue;
+    for (uint32_t rows = scan(page, next, last); rows != 0; rows &= rows - 1, ++listed)
+      if (lane == listed) list = next + __ffs(rows) - 1;
+  }
   while (which != 0) {
     int mine = -1;   // lanes 8 g .. 8 g + 7 have the g-th of them
     for (int g = 0; g < 4 && which != 0; ++g) {
@@ -214,8 +243,26 @@ __device__ __noinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, uint
     // ------------------------------------------------------------ what is not finite
     uint32_t met = 0;
     int32_t page = -1;
-    for (int32_t j0 = 0; j0 < most; j0 += kScan) {
-      if ((j0 & (a.page_rows - 1)) == 0) {
+    auto look_at = [&](int32_t j, int32_t of_page) {
+      const int32_t in = j & (a.page_rows - 1);
+      const int64_t at = of_page * a.page_stride + kvh * a.head_stride + in * a.row_stride + 8 * part;
+      EightOf<kE4m3> kk, vv;
+      kk.load(a.k, at);
+      vv.load(a.v, at);
+      const float x = dot64<kE4m3>(q, kk, scale_at(a.k_scale, of_page, in)) * p.scale;
+      if (j >= seen || x == -INFINITY) return;
+      float y[8];
+      vv.get(scale_at(a.v_scale, of_page, in), y);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (!(fabsf(y[c]) < INFINITY)) o[c] += y[c], met |= 1u << c;
+    };
+    for (int i = 0; i < listed; ++i) {
+      const int32_t j = __shfl_sync(0xffffffffu, list, i);
+      look_at(j, page_of(a, s, j));
+    }
+    for (int32_t j0 = next; j0 < most; j0 += kScan) {
+      if (j0 == next || (j0 & (a.page_rows - 1)) == 0) {
         page = page_of(a, s, j0);
         if (page < 0) atomicOr(a.err, kErrPage);
         bool open = false;   // some element is not NaN yet
@@ -224,32 +271,7 @@ __device__ __noinline__ void redo_rows(const KvArgs& a, const PagedAttn& p, uint
         if (!__any_sync(0xffffffffu, open)) break;
       }
       if (page < 0) continue;
-      const int64_t at = page * a.page_stride + kvh * a.head_stride + 8 * part;
-      const int32_t in0 = (j0 & (a.page_rows - 1)) + (lane >> 3);
-      EightOf<kE4m3> v[kScan / 4];
-#pragma unroll
-      for (int i = 0; i < kScan / 4; ++i) v[i].load(a.v, at + (in0 + 4 * i) * a.row_stride);
-      uint32_t rows = 0;   // of 16
-#pragma unroll
-      for (int i = 0; i < kScan / 4; ++i) {
-        const bool here = j0 + (lane >> 3) + 4 * i < most;
-        const uint32_t b = __ballot_sync(0xffffffffu, here && (!v[i].finite() || (kE4m3 && !(scale_at(a.v_scale, page, in0 + 4 * i) < INFINITY))));
-#pragma unroll
-        for (int g = 0; g < 4; ++g) rows |= (b >> (8 * g)) & 0xffu ? 1u << (4 * i + g) : 0u;
-      }
-      for (; rows != 0; rows &= rows - 1) {
-        const int32_t j = j0 + __ffs(rows) - 1, in = j & (a.page_rows - 1);
-        EightOf<kE4m3> kk, vv;
-        kk.load(a.k, at + in * a.row_stride);
-        vv.load(a.v, at + in * a.row_stride);
-        const float x = dot64<kE4m3>(q, kk, scale_at(a.k_scale, page, in)) * p.scale;
-        if (j >= seen || x == -INFINITY) continue;
-        float y[8];
-        vv.get(scale_at(a.v_scale, page, in), y);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (!(fabsf(y[c]) < INFINITY)) o[c] += y[c], met |= 1u << c;
-      }
+      for (uint32_t rows = scan(page, j0, most); rows != 0; rows &= rows - 1) look_at(j0 + __ffs(rows) - 1, page);
     }
     __syncwarp();
     auto store = [&](uint32_t which_ones) {

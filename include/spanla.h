@@ -681,7 +681,7 @@ span_la_status span_la_kv_read(const span_la_kv_cache *cache, int64_t rows, int3
  * not see does not reach it, whatever it holds.  An infinity or a NaN in V, with a
  * score above -infinity, counts however small its weight; it makes a call longer,
  * by up to some hundred times (1,280 rows and 64 heads over 21,280 rows, 0.45 ms:
- * 25 ms where all rows see one infinity, 93 ms where one lies in the last row and
+ * 5 ms where all rows see one infinity, 80 ms where one lies in the last row and
  * its block's other rows are looked at once more).
  *
  * Scores, sums of weights and o are fp32; out is rounded to bf16.  The weights that
