@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import BF16, E4M3, check_attention, f64
+from oracle import paged_oracle as po
+from paged_helpers import BF16, E4M3, check_attention, f64, values
 from test_gpu_paged_attention import _run, _setup, weights
 
 pytestmark = pytest.mark.gpu
@@ -274,3 +275,70 @@ def test_small_queries_and_scales(cuda_device, q_size, k_size, scale, rows, cach
     out, lse = _run(q, c, table, lens, cu, cuda_device, scale=scale)
     assert f64(lse).max() > 1 and f64(out).std() > 0.1
     check_attention(q, out, lse, c, table, lens, cu, scale, weights(2, cache))
+
+
+def _by_definition(q, K, V, first, scale):
+    """(o, log of the sum, tolerance of o) of rows q [n, heads, 64] of which row i sees K, V[:first + i + 1] (float64): NaN
+    where a score is NaN or +infinity; elements of V that are not finite, with a score above -infinity, add up to o's."""
+    n, Hq = q.shape[:2]
+    o, z, tol = np.zeros((n, Hq, 64)), np.full((n, Hq), -np.inf), np.zeros((n, Hq, 64))
+    for i in range(n):
+        seen = first + i + 1
+        for h in range(Hq):
+            if seen <= 0:
+                continue
+            k, v = K[:seen, h // (Hq // K.shape[1])], V[:seen, h // (Hq // K.shape[1])]
+            x = (k @ q[i, h]) * scale
+            if np.isnan(x).any() or (x == np.inf).any():
+                o[i, h] = z[i, h] = np.nan
+                continue
+            live = x > -np.inf
+            if not live.any():
+                continue
+            x, v = x[live], v[live]
+            w = np.exp(x - x.max())
+            z[i, h] = x.max() + np.log(w.sum())
+            w /= w.sum()
+            fin = np.where(np.isfinite(v), v, 0.0)
+            o[i, h] = w @ fin
+            tol[i, h] = w @ np.abs(fin)
+            special = np.where(np.isfinite(v), 0.0, v).sum(0)
+            o[i, h] = np.where(special == 0, o[i, h], special)
+    return o, z, tol
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls_with_numbers_that_are_not_finite(cuda_device, seed):
+    dev, rng = cuda_device, np.random.default_rng(100 + seed)
+    cache, R, H, G = [BF16, E4M3][seed % 2], int(rng.choice([16, 32, 64, 128])), int(rng.integers(1, 4)), int(rng.choice([1, 2, 3, 5, 8]))
+    S = int(rng.integers(1, 9))
+    lens = [int(x) for x in rng.choice([0, 1, 17, 60, 130, 300, 700], S)]
+    rows = [int(x) for x in rng.choice([0, 1, 3, 7, 20, 70], S)]
+    if sum(rows) == 0:
+        rows[0] = 2
+    width = None if seed % 3 else -(-max(lens + [1]) // R) + 60
+    q, c, table, cu = _setup(lens, rows, G, H, R, cache, dev, seed=seed, width=width)
+    bits = [x.view(torch.uint8) if cache == E4M3 else x for x in c[:2]]
+    kinds = [0x7F] if cache == E4M3 else [float("nan"), float("inf"), float("-inf")]
+    for x, share in ((0, 0.3), (1, 3.0)):                      # (elements a sequence, on average)
+        for s in range(S):
+            for _ in range(rng.poisson(share) if lens[s] else 0):
+                row = int(rng.integers(lens[s]))
+                bits[x][int(table[s, row // R]), int(rng.integers(H)), row % R, int(rng.integers(64))] = kinds[int(rng.integers(len(kinds)))]
+    q = q.clone()
+    for _ in range(int(rng.poisson(0.7))):
+        q[int(rng.integers(len(q))), int(rng.integers(G * H)), int(rng.integers(64))] = float(rng.choice([np.nan, np.inf, -np.inf]))
+    max_rows = max(rows) if seed % 4 == 1 else None
+    out, lse = _run(q, c, table, lens, cu, dev, max_rows=max_rows)
+    o, z, qn = f64(out), f64(lse), f64(q)
+    with np.errstate(invalid="ignore", over="ignore"):
+        K, V = (values(c[i], c[2 + i]) for i in range(2))
+        for s in range(S):
+            b, e = int(cu[s]), int(cu[s + 1])
+            ref, rz, mass = _by_definition(qn[b:e], po.rows_of(K, table[s], lens[s]), po.rows_of(V, table[s], lens[s]), lens[s] - rows[s], 0.125)
+            got, fin = o[b:e], np.isfinite(ref)
+            assert np.array_equal(got[~fin], ref[~fin], equal_nan=True)
+            # o's rounding, and weights rounded to bf16 at the most, scores and sums in fp32
+            assert np.all(np.abs(got - ref)[fin] <= (1.01 * 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mass)[fin] + 1e-37)
+            fz = np.isfinite(rz)
+            assert np.array_equal(z[b:e][~fz], rz[~fz], equal_nan=True) and np.all(np.abs(z[b:e] - rz)[fz] < 1e-3)
